@@ -14,6 +14,11 @@ d mu / d A_ij = v_i v_j on the pattern), Significance (Jacobi preconditioning).
 
     A = CSRMatrix(row_ptr, col_idx, values)          # CUDA tensors
     x = solve(A, b, rtol=1e-8)                       # autograd: grads to values and b
+
+A network that predicts the values is built from layer_norm and gated_ffn (``dense.py``), whose
+gradients flow on from the solve's:
+
+    z = z + gated_ffn(layer_norm(z, w, b), w_in, w_out, b_in, b_out, activation="silu")
 """
 from __future__ import annotations
 
@@ -40,6 +45,8 @@ __all__ = [
     "SLA_BAD_CSR", "SLA_NONFINITE", "SLA_WORKSPACE_TOO_SMALL", "SLA_TIMEOUT", "SLA_CUDA_ERROR",
     "EigInfo", "sla_eig_workspace_bytes", "sla_eig_smallest", "sla_eig_grad_values", "EigSmallest",
     "eigsh_smallest", "sla_spmv_transpose", "sla_matvec_grad_values", "MatVec", "sla_set_spmv_variant", "sla_graph_cache_stats", "sla_test_set_barrier_wait", "SLA_SPMV_PLAIN", "SLA_SPMV_TMA",
+    "sla_layernorm", "sla_layernorm_backward_workspace_bytes", "sla_layernorm_backward", "LayerNorm", "layer_norm",
+    "sla_gated_ffn", "sla_gated_ffn_backward", "GatedFFN", "gated_ffn",
 ]
 from ._abi import SLA_SPMV_PLAIN, SLA_SPMV_TMA  # noqa: E402
 
@@ -724,3 +731,9 @@ def eigsh(A: CSRMatrix, k: int = 1, tol: Optional[float] = None, maxit: int = 20
     """Differentiable k smallest eigenvalues of SPD A ([k], ascending; gradient to A.values) and the
     eigenvectors ([k, n])."""
     return Eigsh.apply(A.row_ptr, A.col_idx, A.values, int(k), tol, maxit, precond)
+
+
+# --------------------------------------------------------------------------- dense operators
+
+from .dense import (GatedFFN, LayerNorm, gated_ffn, layer_norm, sla_gated_ffn, sla_gated_ffn_backward,  # noqa: E402
+                    sla_layernorm, sla_layernorm_backward, sla_layernorm_backward_workspace_bytes)

@@ -9,7 +9,8 @@ LIB_PATH = os.path.join(HERE, "libsla.so")
 
 SLA_OK, SLA_NOT_CONVERGED, SLA_BREAKDOWN, SLA_INVALID_ARG, SLA_BAD_CSR, SLA_NONFINITE = 0, 1, 2, 3, 4, 5
 SLA_WORKSPACE_TOO_SMALL, SLA_TIMEOUT, SLA_CUDA_ERROR = 6, 7, 8
-SLA_F32, SLA_F64 = 0, 1
+SLA_F32, SLA_F64, SLA_F16, SLA_BF16 = 0, 1, 2, 3
+SLA_ACT_SILU, SLA_ACT_GELU, SLA_ACT_GELU_TANH, SLA_ACT_RELU = 0, 1, 2, 3
 SLA_I32, SLA_I64 = 0, 1
 SLA_PRECOND_NONE, SLA_PRECOND_JACOBI = 0, 1
 SLA_LOOP_AUTO, SLA_LOOP_HOST, SLA_LOOP_GRAPH, SLA_LOOP_RESIDENT, SLA_LOOP_CLUSTER = 0, 1, 2, 3, 4
@@ -23,7 +24,9 @@ EXPORTS = [
     "sla_dist_cg_begin", "sla_dist_cg_start", "sla_dist_cg_spmv", "sla_dist_cg_update", "sla_dist_cg_direction",
     "sla_dist_pack", "sla_dist_cg_info", "sla_spmv_transpose", "sla_matvec_grad_values", "sla_dist_scatter_add",
     "sla_graph_cache_stats", "sla_eigsh_workspace_bytes", "sla_eigsh", "sla_bicgstab_workspace_bytes",
-    "sla_bicgstab_solve", "sla_bicgstab_adjoint",
+    "sla_bicgstab_solve", "sla_bicgstab_adjoint", "sla_layernorm", "sla_layernorm_backward_workspace_bytes",
+    "sla_layernorm_backward", "sla_gated_ffn_saved_bytes", "sla_gated_ffn_workspace_bytes",
+    "sla_gated_ffn_backward_workspace_bytes", "sla_gated_ffn", "sla_gated_ffn_backward",
 ]
 SLA_SPMV_PLAIN, SLA_SPMV_TMA = 0, 1
 
@@ -52,6 +55,11 @@ class sla_eig_opts(ctypes.Structure):
 class sla_eig_info(ctypes.Structure):
     _fields_ = [("iters", ctypes.c_int64), ("inner_iters", ctypes.c_int64), ("mu", ctypes.c_double),
                 ("residual", ctypes.c_double), ("status", ctypes.c_int32), ("pad", ctypes.c_int32)]
+
+
+class sla_ffn(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("width", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("out", ctypes.c_int64), ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
 
 
 def bind(lib):
@@ -99,6 +107,16 @@ def bind(lib):
     lib.sla_dist_cg_direction.argtypes = [i64, i32, P, i32, P, P, P, P, P]
     lib.sla_dist_pack.argtypes = [i64, i32, P, P, i64, P, P]
     lib.sla_dist_cg_info.argtypes = [P, I, ctypes.POINTER(i32), P]
+    f64, F = ctypes.c_double, ctypes.POINTER(sla_ffn)
+    lib.sla_layernorm.argtypes = [i64, i64, i32, i32, P, i64, P, P, f64, P, P, P, P]
+    lib.sla_layernorm_backward_workspace_bytes.argtypes = [i64, i64, i32]
+    lib.sla_layernorm_backward.argtypes = [i64, i64, i32, i32, P, i64, P, i64, P, P, P, P, P, P, P, sz, P]
+    for name in ["sla_gated_ffn_saved_bytes", "sla_gated_ffn_workspace_bytes", "sla_gated_ffn_backward_workspace_bytes"]:
+        getattr(lib, name).argtypes = [F]
+        getattr(lib, name).restype = sz
+    lib.sla_layernorm_backward_workspace_bytes.restype = sz
+    lib.sla_gated_ffn.argtypes = [F, P, i64, P, P, P, P, P, P, sz, P, sz, P]
+    lib.sla_gated_ffn_backward.argtypes = [F, P, i64, P, i64, P, P, P, sz, P, P, P, P, P, P, sz, P]
     lib.sla_set_spmv_variant.argtypes = [i32]
     lib.sla_graph_cache_stats.argtypes = [ctypes.POINTER(i64)] * 3
     lib.sla_test_set_barrier_wait.argtypes = [ctypes.c_uint32, i64]
@@ -106,7 +124,8 @@ def bind(lib):
                  "sla_dist_cg_direction", "sla_dist_pack", "sla_dist_cg_info",
                  "sla_set_spmv_variant", "sla_graph_cache_stats", "sla_test_set_barrier_wait", "sla_validate_csr", "sla_spmv", "sla_cg_solve", "sla_cg_adjoint", "sla_grad_values",
                  "sla_cg_solve_batched", "sla_cg_adjoint_batched", "sla_cg_solve_static", "sla_eig_smallest",
-                 "sla_eig_grad_values", "sla_eigsh", "sla_bicgstab_solve", "sla_bicgstab_adjoint"]:
+                 "sla_eig_grad_values", "sla_eigsh", "sla_bicgstab_solve", "sla_bicgstab_adjoint",
+                 "sla_layernorm", "sla_layernorm_backward", "sla_gated_ffn", "sla_gated_ffn_backward"]:
         getattr(lib, name).restype = i32
     return lib
 

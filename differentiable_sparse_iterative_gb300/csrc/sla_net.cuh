@@ -1,0 +1,80 @@
+// Element types and vector loads of the dense operators (layer norm, gated feed-forward block).
+//
+// Data is bfloat16, float16 or float32; everything is computed in float32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sla.h"
+
+namespace sla {
+
+using bf16 = __nv_bfloat16;
+using f16 = __half;
+
+template <typename T>
+struct NetType;
+template <>
+struct NetType<float> {
+  static constexpr int dtype = SLA_F32;
+};
+template <>
+struct NetType<f16> {
+  static constexpr int dtype = SLA_F16;
+};
+template <>
+struct NetType<bf16> {
+  static constexpr int dtype = SLA_BF16;
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(f16 v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
+
+// Rounded to nearest even; float16 overflows to infinity beyond 65504.
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ f16 from_f32<f16>(float v) {
+  return __float2half_rn(v);
+}
+template <>
+__device__ __forceinline__ bf16 from_f32<bf16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// N consecutive elements moved in the widest pieces their size allows (p aligned to them).
+template <typename T, int N>
+struct alignas(sizeof(T) * N >= 16 ? 16 : sizeof(T) * N) Pack {
+  T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void load_f32(const T *p, float (&out)[N]) {
+  const Pack<T, N> q = *reinterpret_cast<const Pack<T, N> *>(p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[i] = to_f32(q.v[i]);
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_f32(T *p, const float (&in)[N]) {
+  Pack<T, N> q;
+#pragma unroll
+  for (int i = 0; i < N; ++i) q.v[i] = from_f32<T>(in[i]);
+  *reinterpret_cast<Pack<T, N> *>(p) = q;
+}
+
+inline bool net_dtype(int32_t d) { return d == SLA_F32 || d == SLA_F16 || d == SLA_BF16; }
+inline size_t net_size(int32_t d) { return d == SLA_F32 ? 4 : 2; }
+
+// Streaming multiprocessors of the current device (152 on GB300), asked once per device.
+int sm_count();
+
+}  // namespace sla

@@ -1,0 +1,279 @@
+"""Dense operators of a coefficient network: layer norm and the gated feed-forward block.
+
+The values of a matrix often come from a network over the grid cells (one token a cell) that is
+trained through the solve; these are the two halves of its residual block z + gated_ffn(layer_norm(z)).
+As everywhere in this package the compute is libsla's (``csrc/sla_norm.cu``, ``csrc/sla_ffn.cu``, C ABI
+in ``include/sla.h``): this module marshals torch tensors, and a CPU tensor raises.
+
+Data is float32, float16 or bfloat16.  The sla_* functions are the C calls under their names (no
+autograd graph, leading dimensions allowed); layer_norm and gated_ffn are differentiable.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _abi
+
+ACTIVATIONS = {"silu": _abi.SLA_ACT_SILU, "gelu": _abi.SLA_ACT_GELU, "gelu_tanh": _abi.SLA_ACT_GELU_TANH,
+               "relu": _abi.SLA_ACT_RELU}
+_DT = {torch.float32: _abi.SLA_F32, torch.float16: _abi.SLA_F16, torch.bfloat16: _abi.SLA_BF16}
+
+
+def _base():
+    import differentiable_sparse_iterative_gb300 as base  # lib, _check, _stream: the package imports this module
+    return base
+
+
+def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> Tuple[int, int, int]:
+    """(address, rows, elements between rows) of a tensor read as rows of its last dimension."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libsla has no CPU path)")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have dtype {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must have a last dimension of at least one element")
+    width = t.shape[-1]
+    rows = t.numel() // width
+    if t.is_contiguous():
+        return t.data_ptr(), rows, width
+    if t.dim() == 2 and (width == 1 or t.stride(1) == 1) and (t.stride(0) >= width or rows <= 1):
+        return t.data_ptr(), rows, t.stride(0)
+    raise ValueError(f"{name} must be contiguous, or a matrix with contiguous rows that do not overlap")
+
+
+def _param(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> Optional[int]:
+    if t is None:
+        return None
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return _DT[t.dtype]
+
+
+def _scratch(need: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
+    if ws is not None and ws.numel() * ws.element_size() >= need:
+        return ws
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+
+
+# --------------------------------------------------------------------------- layer norm
+
+def _ln_params(x, weight, bias):
+    pt = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
+    if pt not in (x.dtype, torch.float32):
+        raise ValueError(f"weight and bias must have dtype {x.dtype} or torch.float32, got {pt}")
+    return pt
+
+
+def sla_layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, y: Optional[torch.Tensor] = None, stats: bool = False):
+    """Layer norm over the last dimension (asynchronous).  weight and bias ([width], of x's type or
+    float32) default to one and zero.  Returns y, or with stats=True (y, mean, rstd): the rows'
+    float32 statistics that sla_layernorm_backward takes."""
+    base = _base()
+    ptr, rows, ldx = _rows(x, "x")
+    dt, width, dev = _type(x, "x"), x.shape[-1], x.device
+    pt = _ln_params(x, weight, bias)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    mean = rstd = None
+    if stats:
+        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
+    base._check(base.lib().sla_layernorm(rows, width, dt, _DT[pt], ptr, ldx, _param(weight, "weight", (width,), pt, dev),
+                                         _param(bias, "bias", (width,), pt, dev), float(eps),
+                                         _param(y, "y", x.shape, x.dtype, dev), mean.data_ptr() if stats else None,
+                                         rstd.data_ptr() if stats else None, base._stream(dev)), "sla_layernorm")
+    return (y, mean, rstd) if stats else y
+
+
+def sla_layernorm_backward_workspace_bytes(rows: int, width: int, dtype: torch.dtype) -> int:
+    return _base().lib().sla_layernorm_backward_workspace_bytes(int(rows), int(width), _DT[dtype])
+
+
+def sla_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
+                           rstd: torch.Tensor, want_grad_x: bool = True, want_grad_weight: bool = True,
+                           want_grad_bias: bool = True, param_dtype: Optional[torch.dtype] = None,
+                           workspace: Optional[torch.Tensor] = None):
+    """Gradients of sla_layernorm (asynchronous): (dx, dweight, dbias), None where not wanted.
+    dweight and dbias have weight's type (param_dtype, default x's, when there is no weight)."""
+    base = _base()
+    ptr, rows, ldx = _rows(x, "x")
+    gptr, grows, lddy = _rows(dy, "dy", x)
+    if dy.shape != x.shape:
+        raise ValueError(f"dy must have x's shape {tuple(x.shape)}, got {tuple(dy.shape)}")
+    dt, width, dev = _type(x, "x"), x.shape[-1], x.device
+    pt = weight.dtype if weight is not None else param_dtype or x.dtype
+    if pt not in (x.dtype, torch.float32):
+        raise ValueError(f"weight must have dtype {x.dtype} or torch.float32, got {pt}")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if want_grad_x else None
+    dw = torch.empty(width, dtype=pt, device=dev) if want_grad_weight else None
+    db = torch.empty(width, dtype=pt, device=dev) if want_grad_bias else None
+    ws, nbytes = None, 0
+    if want_grad_weight or want_grad_bias:
+        ws = _scratch(sla_layernorm_backward_workspace_bytes(rows, width, x.dtype), dev, workspace)
+        nbytes = ws.numel() * ws.element_size()
+    base._check(base.lib().sla_layernorm_backward(
+        rows, width, dt, _DT[pt], gptr, lddy, ptr, ldx, _param(weight, "weight", (width,), pt, dev),
+        _param(mean, "mean", (rows,), torch.float32, dev), _param(rstd, "rstd", (rows,), torch.float32, dev),
+        dx.data_ptr() if want_grad_x else None, dw.data_ptr() if want_grad_weight else None,
+        db.data_ptr() if want_grad_bias else None, ws.data_ptr() if ws is not None else None, nbytes,
+        base._stream(dev)), "sla_layernorm_backward")
+    return dx, dw, db
+
+
+def _matrix_ready(t: torch.Tensor) -> torch.Tensor:
+    """t, or a contiguous copy where its rows cannot be read in place (expanded or transposed tensors)."""
+    if t.is_contiguous() or (t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+        return t
+    return t.contiguous()
+
+
+class LayerNorm(torch.autograd.Function):
+    """y = layer norm of x's last dimension.  Saved for backward: x, the weight and two floats a row."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        x = _matrix_ready(x)
+        y, mean, rstd = sla_layernorm(x, weight, bias, eps=eps, stats=True)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.param_dtype = _ln_params(x, weight, bias)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        dx, dw, db = sla_layernorm_backward(_matrix_ready(dy), x, weight, mean, rstd, need_x, need_w, need_b,
+                                            param_dtype=ctx.param_dtype)
+        return dx, dw, db, None
+
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5) -> torch.Tensor:
+    """Differentiable layer norm over the last dimension (gradients flow to x, weight and bias)."""
+    if _wants_grad(x, weight, bias):
+        return LayerNorm.apply(x, weight, bias, eps)
+    return sla_layernorm(_matrix_ready(x), weight, bias, eps=eps)
+
+
+# --------------------------------------------------------------------------- gated feed-forward block
+
+def _ffn(x, w_in, w_out, activation) -> Tuple[_abi.sla_ffn, int, int]:
+    """(descriptor, address of x, its leading dimension)"""
+    ptr, rows, ldx = _rows(x, "x")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r} (one of {', '.join(ACTIVATIONS)})")
+    if w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape[0] != 2 * w_out.shape[1]:
+        raise ValueError("w_in must be [2 * hidden, width] and w_out [out, hidden], got "
+                         f"{tuple(w_in.shape)} and {tuple(w_out.shape)}")
+    f = _abi.sla_ffn()
+    f.tokens, f.width, f.hidden, f.out = rows, x.shape[-1], w_out.shape[1], w_out.shape[0]
+    f.dtype, f.activation = _type(x, "x"), ACTIVATIONS[activation]
+    return f, ptr, ldx
+
+
+def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in: Optional[torch.Tensor] = None,
+                  b_out: Optional[torch.Tensor] = None, activation: str = "silu", y: Optional[torch.Tensor] = None,
+                  save: bool = False, workspace: Optional[torch.Tensor] = None):
+    """y = (act(x Wg^T + bg) * (x Wu^T + bu)) w_out^T + b_out (asynchronous).
+
+    w_in stacks Wg over Wu ([2 hidden, width]), b_in likewise; w_out is [out, hidden].  activation:
+    "silu", "gelu", "gelu_tanh" or "relu".  Returns y, or with save=True (y, saved): the byte buffer
+    of intermediates that sla_gated_ffn_backward takes."""
+    base = _base()
+    f, ptr, ldx = _ffn(x, w_in, w_out, activation)
+    lib, dt, dev, fp = base.lib(), x.dtype, x.device, ctypes.byref(f)
+    shape = x.shape[:-1] + (f.out,)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    saved = torch.empty(max(lib.sla_gated_ffn_saved_bytes(fp), 256), dtype=torch.uint8, device=dev) if save else None
+    ws = _scratch(lib.sla_gated_ffn_workspace_bytes(fp), dev, workspace)
+    base._check(lib.sla_gated_ffn(
+        fp, ptr, ldx, _param(w_in, "w_in", (2 * f.hidden, f.width), dt, dev),
+        _param(b_in, "b_in", (2 * f.hidden,), dt, dev), _param(w_out, "w_out", (f.out, f.hidden), dt, dev),
+        _param(b_out, "b_out", (f.out,), dt, dev), _param(y, "y", shape, dt, dev),
+        saved.data_ptr() if save else None, saved.numel() if save else 0, ws.data_ptr(),
+        ws.numel() * ws.element_size(), base._stream(dev)), "sla_gated_ffn")
+    return (y, saved) if save else y
+
+
+def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
+                           saved: torch.Tensor, activation: str = "silu", want_grad_x: bool = True,
+                           want_grad_weights: bool = True, want_grad_bias: bool = False,
+                           workspace: Optional[torch.Tensor] = None):
+    """Gradients of sla_gated_ffn (asynchronous): (dx, dw_in, dw_out, db_in, db_out), None where not
+    wanted.  x, the weights, the activation and `saved` are the forward call's."""
+    base = _base()
+    f, ptr, ldx = _ffn(x, w_in, w_out, activation)
+    gptr, grows, lddy = _rows(dy, "dy", x)
+    if dy.shape != x.shape[:-1] + (f.out,):
+        raise ValueError(f"dy must have shape {tuple(x.shape[:-1]) + (f.out,)}, got {tuple(dy.shape)}")
+    lib, dt, dev, fp = base.lib(), x.dtype, x.device, ctypes.byref(f)
+
+    def out(want, *shape):
+        return torch.empty(shape, dtype=dt, device=dev) if want else None
+
+    dx = out(want_grad_x, *x.shape)
+    grads = (out(want_grad_weights, 2 * f.hidden, f.width), out(want_grad_weights, f.out, f.hidden),
+             out(want_grad_bias, 2 * f.hidden), out(want_grad_bias, f.out))
+    ws = _scratch(lib.sla_gated_ffn_backward_workspace_bytes(fp), dev, workspace)
+    if saved.dtype != torch.uint8 or not saved.is_cuda or not saved.is_contiguous():
+        raise ValueError("saved must be the buffer that sla_gated_ffn(..., save=True) returned")
+    base._check(lib.sla_gated_ffn_backward(
+        fp, gptr, lddy, ptr, ldx, _param(w_in, "w_in", (2 * f.hidden, f.width), dt, dev),
+        _param(w_out, "w_out", (f.out, f.hidden), dt, dev), saved.data_ptr(), saved.numel(),
+        *(None if t is None else t.data_ptr() for t in (dx,) + grads), ws.data_ptr(),
+        ws.numel() * ws.element_size(), base._stream(dev)), "sla_gated_ffn_backward")
+    return (dx,) + grads
+
+
+class GatedFFN(torch.autograd.Function):
+    """y = (act(x Wg^T + bg) * (x Wu^T + bu)) w_out^T + b_out.  Saved for backward: x, the weights and
+    g, u and h (3 hidden values a token)."""
+
+    @staticmethod
+    def forward(ctx, x, w_in, w_out, b_in, b_out, activation):
+        x, w_in, w_out = _matrix_ready(x), w_in.contiguous(), w_out.contiguous()
+        y, saved = sla_gated_ffn(x, w_in, w_out, b_in, b_out, activation=activation, save=True)
+        ctx.save_for_backward(x, w_in, w_out, saved)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w_in, w_out, saved = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw_in, dw_out, db_in, db_out = sla_gated_ffn_backward(
+            _matrix_ready(dy), x, w_in, w_out, saved, activation=ctx.activation, want_grad_x=need[0],
+            want_grad_weights=need[1] or need[2], want_grad_bias=need[3] or need[4])
+        return (dx, dw_in if need[1] else None, dw_out if need[2] else None, db_in if need[3] else None,
+                db_out if need[4] else None, None)
+
+
+def gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in: Optional[torch.Tensor] = None,
+              b_out: Optional[torch.Tensor] = None, activation: str = "silu") -> torch.Tensor:
+    """Differentiable gated feed-forward block (gradients flow to x, the weights and the biases)."""
+    if _wants_grad(x, w_in, w_out, b_in, b_out):
+        return GatedFFN.apply(x, w_in, w_out, b_in, b_out, activation)
+    return sla_gated_ffn(_matrix_ready(x), w_in.contiguous(), w_out.contiguous(), b_in, b_out, activation=activation)

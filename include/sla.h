@@ -77,7 +77,9 @@ typedef enum sla_status {
   SLA_CUDA_ERROR = 8           /* a CUDA runtime call failed */
 } sla_status;
 
-typedef enum sla_dtype { SLA_F32 = 0, SLA_F64 = 1 } sla_dtype;
+/* The solvers take SLA_F32 and SLA_F64; the dense operators (sla_layernorm, sla_gated_ffn) SLA_F32,
+   SLA_F16 (IEEE half) and SLA_BF16 (bfloat16). */
+typedef enum sla_dtype { SLA_F32 = 0, SLA_F64 = 1, SLA_F16 = 2, SLA_BF16 = 3 } sla_dtype;
 typedef enum sla_itype { SLA_I32 = 0, SLA_I64 = 1 } sla_itype;
 typedef enum sla_precond { SLA_PRECOND_NONE = 0, SLA_PRECOND_JACOBI = 1 } sla_precond;
 
@@ -497,6 +499,93 @@ SLA_API sla_status sla_dist_cg_info(const void *state, sla_cg_info *info, int32_
  */
 SLA_API sla_status sla_cg_solve_static(const sla_csr *A, const void *b, const void *x0, const sla_cg_opts *opts,
                                        void *x, sla_cg_info *info, double *history, void *stream);
+
+/* ---------------------------------------------------------------- dense operators of a coefficient network */
+
+/*
+ * A matrix's values often come from a network over the grid cells (one row, or token, a cell),
+ * trained through the solve.  These two operators are its residual block  z + ffn(layernorm(z)).
+ * Both take SLA_F32, SLA_F16 or SLA_BF16 data and compute in float32.  Matrices are row-major with
+ * unit column stride; the leading dimensions ldx and lddy (elements between rows) may exceed the
+ * row length, weights and outputs are dense.  Rows of no alignment beyond their element type are
+ * taken.  All calls are asynchronous on the stream; results do not depend on the order in which
+ * blocks run (no atomics: the same call gives the same bits).
+ */
+
+/*
+ * y[r] = (x[r] - mean_r) * rstd_r * weight + bias,  rstd_r = 1 / sqrt(var_r + eps), over rows of
+ * `width` elements (1 <= width <= 2^24; var is the mean of squared deviations).
+ *   param_dtype    type of weight and bias: dtype or SLA_F32
+ *   weight, bias   device, [width] or NULL (1 and 0)
+ *   mean, rstd     device, [rows] float32 or NULL: the rows' statistics, for the backward call
+ * A NaN or an infinity in a row makes that row NaN and leaves the others alone.  rows = 0 writes nothing.
+ */
+SLA_API sla_status sla_layernorm(int64_t rows, int64_t width, int32_t dtype, int32_t param_dtype, const void *x,
+                                 int64_t ldx, const void *weight, const void *bias, double eps, void *y, float *mean,
+                                 float *rstd, void *stream);
+
+/* Scratch of sla_layernorm_backward (0 for invalid arguments). */
+SLA_API size_t sla_layernorm_backward_workspace_bytes(int64_t rows, int64_t width, int32_t dtype);
+
+/*
+ * Gradients of sla_layernorm for an upstream gradient dy: dx [rows][width] in dtype, dweight and
+ * dbias [width] in param_dtype (each NULL when not wanted; summed over the rows in float32).
+ * mean and rstd are those the forward call wrote.  The workspace is needed for dweight and dbias
+ * only (256-byte aligned).  rows = 0 sets dweight and dbias to zero.
+ */
+SLA_API sla_status sla_layernorm_backward(int64_t rows, int64_t width, int32_t dtype, int32_t param_dtype,
+                                          const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                          const void *weight, const float *mean, const float *rstd, void *dx,
+                                          void *dweight, void *dbias, void *workspace, size_t ws_bytes,
+                                          void *stream);
+
+typedef enum sla_act {
+  SLA_ACT_SILU = 0,       /* g / (1 + exp(-g)) */
+  SLA_ACT_GELU = 1,       /* g Phi(g), Phi the normal distribution function */
+  SLA_ACT_GELU_TANH = 2,  /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+  SLA_ACT_RELU = 3        /* max(g, 0), derivative 0 at 0 */
+} sla_act;
+
+/* A gated feed-forward block: width -> 2 x hidden -> out, over `tokens` rows. */
+typedef struct sla_ffn {
+  int64_t tokens;         /* rows of x, 0 <= tokens < 2^31 */
+  int64_t width;          /* columns of x, 1 .. 2^24, as hidden and out */
+  int64_t hidden;
+  int64_t out;            /* columns of y */
+  int32_t dtype;          /* SLA_F32, SLA_F16 or SLA_BF16, of every array */
+  int32_t activation;     /* sla_act */
+} sla_ffn;
+
+/* Bytes of the buffer that carries a forward call's intermediates to its backward call, and of the
+   scratch of the two calls (0 for invalid arguments). */
+SLA_API size_t sla_gated_ffn_saved_bytes(const sla_ffn *f);
+SLA_API size_t sla_gated_ffn_workspace_bytes(const sla_ffn *f);
+SLA_API size_t sla_gated_ffn_backward_workspace_bytes(const sla_ffn *f);
+
+/*
+ *   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) * u,  y = h w_out^T + b_out
+ *   w_in   device, [2 hidden][width]: Wg over Wu;  b_in [2 hidden] or NULL: bg then bu
+ *   w_out  device, [out][hidden];  b_out [out] or NULL
+ *   y      device, [tokens][out]
+ *   saved  device, sla_gated_ffn_saved_bytes, 256-byte aligned, or NULL: kept for the backward call
+ *   workspace  device, sla_gated_ffn_workspace_bytes, 256-byte aligned
+ * Sums run in float32.  With 16-bit data, g, u (where saved) and h are rounded to dtype; with
+ * float32 data they stay float32, as do the products.  A float16 block whose |h| passes 65504 gives
+ * infinities, as float16 data does everywhere.
+ */
+SLA_API sla_status sla_gated_ffn(const sla_ffn *f, const void *x, int64_t ldx, const void *w_in, const void *b_in,
+                                 const void *w_out, const void *b_out, void *y, void *saved, size_t saved_bytes,
+                                 void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients for an upstream gradient dy [tokens][out] (lddy): dx [tokens][width], dw_in, dw_out,
+ * db_in [2 hidden] and db_out [out], each NULL when not wanted.  x, the weights and `saved` are the
+ * forward call's.  tokens = 0 sets the weights' and biases' gradients to zero.
+ */
+SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                          const void *w_in, const void *w_out, const void *saved, size_t saved_bytes,
+                                          void *dx, void *dw_in, void *dw_out, void *db_in, void *db_out,
+                                          void *workspace, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------- tuning and testing */
 
