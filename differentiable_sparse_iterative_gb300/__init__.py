@@ -46,7 +46,7 @@ __all__ = [
     "EigInfo", "sla_eig_workspace_bytes", "sla_eig_smallest", "sla_eig_grad_values", "EigSmallest",
     "eigsh_smallest", "sla_spmv_transpose", "sla_matvec_grad_values", "MatVec", "sla_set_spmv_variant", "sla_graph_cache_stats", "sla_test_set_barrier_wait", "SLA_SPMV_PLAIN", "SLA_SPMV_TMA",
     "sla_layernorm", "sla_layernorm_backward_workspace_bytes", "sla_layernorm_backward", "LayerNorm", "layer_norm",
-    "sla_gated_ffn", "sla_gated_ffn_backward", "GatedFFN", "gated_ffn",
+    "sla_gated_ffn", "sla_gated_ffn_backward", "sla_gated_ffn_check", "GatedFFN", "gated_ffn",
 ]
 from ._abi import SLA_SPMV_PLAIN, SLA_SPMV_TMA  # noqa: E402
 
@@ -736,4 +736,4 @@ def eigsh(A: CSRMatrix, k: int = 1, tol: Optional[float] = None, maxit: int = 20
 # --------------------------------------------------------------------------- dense operators
 
 from .dense import (GatedFFN, LayerNorm, gated_ffn, layer_norm, sla_gated_ffn, sla_gated_ffn_backward,  # noqa: E402
-                    sla_layernorm, sla_layernorm_backward, sla_layernorm_backward_workspace_bytes)
+                    sla_gated_ffn_check, sla_layernorm, sla_layernorm_backward, sla_layernorm_backward_workspace_bytes)

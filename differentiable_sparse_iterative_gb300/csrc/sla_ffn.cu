@@ -4,140 +4,524 @@
 //   dh = dy w_out,  dg = dh u act'(g),  du = dh act(g)
 //   dx = [dg du] w_in,  dw_in = [dg du]^T x,  dw_out = dy^T h,  db_in = sum [dg du],  db_out = sum dy
 //
-// Six matrix products; the activation, the product with u and their derivatives are the epilogues
-// of the two products that make g, u and dh.
+// Six tensor-core products (sla_product.cuh); the activation, the product with u and their
+// derivatives are the epilogues of the two that make g, u and dh.  This file lays out the operands,
+// picks each product's tile shape and split, and adds what is split.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
-#include "sla_act.cuh"
 #include "sla_common.cuh"
 #include "sla_host.h"
 #include "sla_net.cuh"
+#include "sla_product.cuh"
 
 namespace sla {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
+__device__ uint32_t d_timeouts;  // blocks of products that gave up a wait, since the last sla_gated_ffn_check
 
-enum Epilogue { kStore, kGate, kGateBack };
-
-// One product C = A B^T of matrices given by their strides, with its epilogue.
-template <typename T>
-struct Product {
-  int64_t m, n, k;
-  const T *a;
-  int64_t a_row, a_col;  // A(i, k) = a[i * a_row + k * a_col]
-  const T *b;
-  int64_t b_row, b_col;
-  int64_t b_up;     // kGate: offset of the up projection's rows in b
-  const T *bias;    // kStore: [n]; kGate: [2 n]; NULL: none
-  T *c;             // kStore: C; kGate: h
-  int64_t ldc;
-  T *gu;            // kGate: [m][ldgu], g and u (NULL: not kept); kGateBack: read
-  int64_t ldgu;
-  T *dgu;           // kGateBack: [m][ldgu]
-  int act;
-};
-
-template <typename T, int EPI>
-__global__ void __launch_bounds__(256) product_tile(Product<T> p) {
-  constexpr int NB = EPI == kGate ? 2 : 1;
-  __shared__ float sa[kDepth][kTile + 1], sb[NB][kDepth][kTile + 1];
-  const int64_t m0 = blockIdx.y * (int64_t)kTile, n0 = blockIdx.x * (int64_t)kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[NB][4][4] = {};
-  for (int64_t k0 = 0; k0 < p.k; k0 += kDepth) {
-    for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-      const int r = i / kDepth, kk = i % kDepth;
-      const bool kin = k0 + kk < p.k;
-      sa[kk][r] = kin && m0 + r < p.m ? to_f32(p.a[(m0 + r) * p.a_row + (k0 + kk) * p.a_col]) : 0.f;
-#pragma unroll
-      for (int q = 0; q < NB; ++q)
-        sb[q][kk][r] =
-            kin && n0 + r < p.n ? to_f32(p.b[q * p.b_up + (n0 + r) * p.b_row + (k0 + kk) * p.b_col]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kDepth; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int q = 0; q < NB; ++q)
-            acc[q][i][j] = fmaf(sa[kk][ty + 16 * i], sb[q][kk][tx + 16 * j], acc[q][i][j]);
-    __syncthreads();
+uint32_t *timeouts_address() {
+  static thread_local int cached_dev = -1;
+  static thread_local uint32_t *cached = nullptr;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  if (dev != cached_dev) {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, d_timeouts) != cudaSuccess) return nullptr;
+    cached = (uint32_t *)p;
+    cached_dev = dev;
   }
-  constexpr bool fast = sizeof(T) == 2;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = m0 + ty + 16 * i, c = n0 + tx + 16 * j;
-      if (r >= p.m || c >= p.n) continue;
-      if (EPI == kStore) {
-        p.c[r * p.ldc + c] = from_f32<T>(acc[0][i][j] + (p.bias ? to_f32(p.bias[c]) : 0.f));
-      } else if (EPI == kGate) {
-        const float g = acc[0][i][j] + (p.bias ? to_f32(p.bias[c]) : 0.f);
-        const float u = acc[NB - 1][i][j] + (p.bias ? to_f32(p.bias[p.n + c]) : 0.f);
-        if (p.gu) {
-          p.gu[r * p.ldgu + c] = from_f32<T>(g);
-          p.gu[r * p.ldgu + p.n + c] = from_f32<T>(u);
-        }
-        p.c[r * p.ldc + c] = from_f32<T>(activate<fast>(p.act, g).a * u);
-      } else {
-        const float g = to_f32(p.gu[r * p.ldgu + c]), u = to_f32(p.gu[r * p.ldgu + p.n + c]);
-        const ActValue v = activate<fast>(p.act, g);
-        p.dgu[r * p.ldgu + c] = from_f32<T>(acc[0][i][j] * u * v.da);
-        p.dgu[r * p.ldgu + p.n + c] = from_f32<T>(acc[0][i][j] * v.a);
-      }
-    }
+  return cached;
 }
 
-// Column sums of a [rows][cols] matrix, one block for 32 columns.
+// ------------------------------------------------------------------ operands
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// A 16-bit matrix that TMA can read: [sheets][rows][cols], cols contiguous.
+struct Operand {
+  const void *p;
+  int64_t cols, rows, sheets, ld, sheet;
+};
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (EncodeFn)p;
+  }();
+  return fn;
+}
+
+// Map of boxes of 64 columns by box_rows rows, 128-byte swizzle, zeros outside.
+cudaError_t encode(CUtensorMap *map, const Operand &o, int box_rows, bool f16) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.sheets};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.sheet * 2};
+  const cuuint32_t box[3] = {kDepth, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<void *>(o.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// dst[sheet * S + .]: the matrix with rows padded to ld (zeros), float32 split into three sheets.  One thread
+// moves eight columns.  sheets of src (halves) lie `src_sheet` apart; sheet q of half i goes to q * halves + i.
 template <typename T>
-__global__ void __launch_bounds__(1024) column_sums(int64_t rows, int64_t cols, const T *__restrict__ a, int64_t lda,
-                                                    T *__restrict__ out) {
-  __shared__ float sm[32][33];
+__global__ void __launch_bounds__(256) pack_operand(int64_t rows, int64_t cols, int halves, const T *__restrict__ src,
+                                                    int64_t src_ld, int64_t src_half, int vec,
+                                                    uint16_t *__restrict__ dst, int64_t ld) {
+  const int64_t chunks = ld / 8, total = halves * rows * chunks, sheet = rows * ld;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t c = i % chunks * 8, hr = i / chunks;
+    const int64_t half = hr / rows, r = hr - half * rows;
+    float v[8];
+    const T *s = src + half * src_half + r * src_ld + c;
+    load_row<T, 8>(s, v, (int)(cols - c < 8 ? cols - c : 8), vec);
+    store_operand<T, 8>(dst + half * sheet + r * ld + c, halves * sheet, v, 8, true);
+  }
+}
+
+bool tma_ready(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+template <typename T>
+constexpr int sheets_of() {
+  return sizeof(T) == 4 ? 3 : 1;
+}
+
+size_t packed_bytes(int64_t rows, int64_t cols, int32_t dtype) {
+  return align256((size_t)rows * (size_t)round_up(cols, 8) * 2 * (dtype == SLA_F32 ? 3 : 1));
+}
+
+// Scratch handed out front to back.
+struct Arena {
+  char *base;
+  size_t used = 0;
+  void *take(size_t bytes) {
+    void *p = base ? base + used : nullptr;
+    used += align256(bytes);
+    return p;
+  }
+};
+
+struct Call {
+  cudaStream_t st;
+  cudaError_t err = cudaSuccess;
+  uint64_t launches = 0;
+  uint32_t *timeouts = nullptr;
+  void launched(cudaError_t e) {
+    ++launches;
+    if (err == cudaSuccess) err = e;
+  }
+};
+
+// The matrix as an operand: in place where TMA can read it, else packed into `to`.
+template <typename T>
+Operand as_operand(Call &c, const T *src, int64_t rows, int64_t cols, int64_t ld, int halves, void *to) {
+  const int64_t half = rows * ld;                          // between the halves of src
+  if (rows == 1 && halves == 1) ld = round_up(cols, 8);  // a single row has no distance to the next
+  if (sizeof(T) == 2 && tma_ready(src, ld) && (halves == 1 || half % 8 == 0))
+    return {src, cols, rows, halves, ld, rows * ld};
+  const int64_t pitch = round_up(cols, 8);
+  const int64_t work = halves * rows * (pitch / 8);
+  const int vec = aligned(src, 16) && ld * sizeof(T) % 16 == 0;
+  pack_operand<T><<<(unsigned)std::min<int64_t>((work + 255) / 256, 152 * 32), 256, 0, c.st>>>(
+      rows, cols, halves, src, ld, half, vec, (uint16_t *)to, pitch);
+  c.launched(cudaGetLastError());
+  return {to, cols, rows, (int64_t)sheets_of<T>() * halves, pitch, rows * pitch};
+}
+
+// ------------------------------------------------------------------ plans
+
+// Deepest sum of products that float32 data adds up in one accumulator, in blocks of kDepth: the tensor
+// core drops up to one unit of the running sum for every 16 products (2048 / 16 * 2^-24 * 2/3 = 5e-6 in all).
+constexpr int kFloatBlocks = 2048 / kDepth;
+
+struct ProductPlan {
+  int shape, splits;
+  size_t partial_bytes;
+};
+
+struct ProductSize {
+  int64_t m, n, k;           // of one half, of one segment
+  int m_halves, n_halves, k_halves;
+};
+
+// The tile shape and split with the least predicted time: rounds of tiles over the multiprocessors, each
+// its k blocks and a fixed cost (first loads, last epilogue), plus writing and reading a split's sums.
+ProductPlan plan_product(const ProductSize &s, int sheets, bool gate) {
+  const int kb = (int)((s.k + kDepth - 1) / kDepth);
+  const int pairs = sheets == 3 ? 6 : 1;
+  const int deepest = sheets == 3 ? std::max(1, kFloatBlocks / s.k_halves) : kb;
+  const int sms = sm_count();
+  const double block_us[kProductTileCount] = {0.29, 0.33, 0.18, 0.11};
+  ProductPlan best{0, 1, 0};
+  double best_us = 1e30;
+  for (int i = 1; i < kProductTileCount; ++i) {
+    const int bm = 128 * kProductTiles[i].cg, bn = kProductTiles[i].bn;
+    const int64_t workers = sms / kProductTiles[i].cg;
+    const int64_t mt = s.m_halves * ((s.m + bm - 1) / bm);
+    for (int splits = 1; splits <= kb && splits <= 512; splits = splits < 4 ? splits + 1 : splits + splits / 4) {
+      if ((kb + splits - 1) / splits > deepest && splits < kb) continue;
+      const int64_t cols = gate && splits == 1 ? bn / 2 : bn;  // a split gate's columns are summed as plain ones
+      const int halves = gate && splits > 1 ? 2 : s.n_halves;
+      const int64_t nt = halves * ((s.n + cols - 1) / cols);
+      const int64_t rounds = (mt * nt * splits + workers - 1) / workers;
+      double us = rounds * (((kb + splits - 1) / splits) * s.k_halves * pairs * block_us[i] + 2.0);
+      if (splits > 1) {
+        const double bytes = 4.0 * s.m * s.m_halves * (double)round_up(s.n, 16) * halves * splits;
+        us += 4.0 + 2.0 * bytes / 5e6;
+      }
+      if (us < best_us) {
+        best_us = us;
+        best = {i, splits, 0};
+      }
+    }
+  }
+  if (best.splits > 1) {
+    const int halves = gate ? 2 : s.n_halves;
+    best.partial_bytes = align256(4 * (size_t)(s.m * s.m_halves) * (size_t)(round_up(s.n, 16) * halves) * best.splits);
+  }
+  return best;
+}
+
+// ------------------------------------------------------------------ sums of splits
+
+// The epilogue of a product whose k was split: sums the parts in order, four columns a thread.
+template <typename T, int EPI>
+__global__ void __launch_bounds__(256) finish_splits(ProductArgs p, const float *__restrict__ parts, int64_t rows) {
+  const int64_t chunks = (p.n + 3) / 4, total = rows * chunks;
+  constexpr bool fast = sizeof(T) == 2;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t row = i / chunks;
+    const int col = (int)(i - row * chunks) * 4, count = p.n - col;
+    const float *src = parts + row * p.ldc + col;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.splits; ++s) {
+      float t[4];
+      load_f32<float, 4>(src + s * p.c_split, t);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += t[k];
+      if (EPI == kGate) {
+        load_f32<float, 4>(src + s * p.c_split + p.c_n_half, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] += t[k];
+      }
+    }
+    if (EPI == kStore) {
+      T *out = (T *)p.c + row * (int64_t)p.n + col;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < count) out[k] = from_f32<T>(v[k] + (p.bias ? to_f32(((const T *)p.bias)[col + k]) : 0.f));
+      continue;
+    }
+    const int64_t o = row * p.ldg + col;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= count) break;
+      if (EPI == kGate) {
+        float g = v[k], up = u[k];
+        if (p.bias) {
+          g += to_f32(((const T *)p.bias)[col + k]);
+          up += to_f32(((const T *)p.bias)[p.n + col + k]);
+        }
+        if (p.g) {
+          ((T *)p.g)[o + k] = from_f32<T>(g);
+          ((T *)p.u)[o + k] = from_f32<T>(up);
+        }
+        v[k] = activate<fast>(p.act, g).a * up;
+      } else {
+        const float g = to_f32(((const T *)p.g)[o + k]), up = to_f32(((const T *)p.u)[o + k]);
+        const ActValue a = activate<fast>(p.act, g);
+        u[k] = v[k] * a.a;
+        v[k] = v[k] * up * a.da;
+      }
+    }
+    if (EPI == kGate) {
+      store_operand<T, 4>(p.h + o, p.sheet, v, count, false);
+    } else {
+      store_operand<T, 4>(p.h + o, 2 * p.sheet, v, count, false);
+      store_operand<T, 4>(p.h + p.sheet + o, 2 * p.sheet, u, count, false);
+    }
+  }
+}
+
+// One product: A(m, k) and B(n, k) with their majors, and the epilogue's arrays in `p`.
+template <typename T>
+void run_product(Call &c, Epilogue epi, const ProductSize &s, const Operand &a, bool a_mn, const Operand &b, bool b_mn,
+                 ProductArgs p, float *parts) {
+  if (c.err != cudaSuccess) return;
+  constexpr int S = sheets_of<T>();
+  const ProductPlan plan = plan_product(s, S, epi == kGate);
+  const ProductTile tile = kProductTiles[plan.shape];
+  const bool split = plan.splits > 1;
+  const int bm = 128 * tile.cg, bn = tile.bn;
+  const bool gate = epi == kGate && !split;
+  p.m = (int)s.m, p.n = (int)s.n;
+  p.m_halves = s.m_halves, p.n_halves = epi == kGate && split ? 2 : s.n_halves;
+  const int cols = gate ? bn / 2 : bn;
+  p.m_tiles = (int)((s.m + bm - 1) / bm), p.n_tiles = (int)((s.n + cols - 1) / cols);
+  p.k_blocks = (int)((s.k + kDepth - 1) / kDepth);
+  p.splits = plan.splits;
+  p.a_mn = a_mn, p.b_mn = b_mn, p.f16 = sizeof(T) == 2 && NetType<T>::dtype == SLA_F16;
+  p.timeouts = c.timeouts;
+  // sheets: part q of the value, in pairs where A (B) has halves of rows, of columns or of k
+  const int a_pair = s.m_halves * s.k_halves, b_pair = (epi == kGate ? 2 : s.n_halves) * s.k_halves;
+  static const int8_t order[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
+  p.segments = 0;
+  for (int q = S == 3 ? 0 : 5; q < 6; ++q)
+    for (int h = 0; h < s.k_halves; ++h) {
+      p.a_sheet[p.segments] = (int8_t)(order[q][0] * a_pair + h);
+      p.b_sheet[p.segments++] = (int8_t)(order[q][1] * b_pair + h);
+    }
+  CUtensorMap ma, mb;
+  const bool f16 = p.f16;
+  cudaError_t e = encode(&ma, a, a_mn ? kDepth : 128, f16);
+  if (e == cudaSuccess) e = encode(&mb, b, b_mn ? kDepth : gate ? bn / 2 : bn / tile.cg, f16);
+  if (e != cudaSuccess) {
+    c.err = e;
+    return;
+  }
+  const int64_t items = (int64_t)p.m_halves * p.m_tiles * p.n_halves * p.n_tiles * p.splits;
+  const int blocks = (int)std::min<int64_t>(items, sm_count() / tile.cg) * tile.cg;
+  if (!split) {
+    c.launched(launch_product<T>(epi, plan.shape, blocks, ma, mb, p, c.st));
+    return;
+  }
+  ProductArgs q = p;
+  const int64_t ncols = round_up(s.n, 16) * p.n_halves, rows = s.m * s.m_halves;
+  q.c = parts, q.ldc = ncols, q.c_n_half = round_up(s.n, 16), q.c_m_half = s.m * ncols, q.c_split = rows * ncols;
+  q.vec = 1;
+  c.launched(launch_product<T>(kPartial, plan.shape, blocks, ma, mb, q, c.st));
+  p.ldc = ncols, p.c_n_half = q.c_n_half, p.c_split = q.c_split;
+  const unsigned grid = (unsigned)std::min<int64_t>((rows * ((s.n + 3) / 4) + 255) / 256, 152 * 16);
+  if (epi == kStore)
+    finish_splits<T, kStore><<<grid, 256, 0, c.st>>>(p, parts, rows);
+  else if (epi == kGate)
+    finish_splits<T, kGate><<<grid, 256, 0, c.st>>>(p, parts, rows);
+  else
+    finish_splits<T, kGateBack><<<grid, 256, 0, c.st>>>(p, parts, rows);
+  c.launched(cudaGetLastError());
+}
+
+// ------------------------------------------------------------------ column sums (bias gradients)
+
+constexpr int kSumRows = 512;    // rows of a part at least
+constexpr int kSumParts = 64;    // parts at most
+
+// parts[part][cols]: sums over a part of the rows; S sheets `sheet` apart are parts of one value.
+template <typename T, int S>
+__global__ void __launch_bounds__(256) column_parts(int64_t rows, int64_t cols, const T *__restrict__ a, int64_t lda,
+                                                    int64_t sheet, int64_t per, float *__restrict__ parts) {
+  __shared__ float sm[8][33];
   const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
   const int64_t c = blockIdx.x * 32ll + lane;
+  const int64_t r0 = blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
   float s = 0.f;
   if (c < cols)
-    for (int64_t r = wy; r < rows; r += 32) s += to_f32(a[r * lda + c]);
+    for (int64_t r = r0 + wy; r < r1; r += 8) {
+      float v = 0.f;
+#pragma unroll
+      for (int q = S - 1; q >= 0; --q) v += to_f32(a[q * sheet + r * lda + c]);
+      s += v;
+    }
   sm[wy][lane] = s;
   __syncthreads();
   if (wy == 0 && c < cols) {
     float t = 0.f;
-    for (int i = 0; i < 32; ++i) t += sm[i][lane];
-    out[c] = from_f32<T>(t);
+    for (int i = 0; i < 8; ++i) t += sm[i][lane];
+    parts[blockIdx.y * cols + c] = t;
   }
 }
 
-template <typename T, int EPI>
-void launch(const Product<T> &p, cudaStream_t st) {
-  const dim3 grid((unsigned)((p.n + kTile - 1) / kTile), (unsigned)((p.m + kTile - 1) / kTile));
-  product_tile<T, EPI><<<grid, 256, 0, st>>>(p);
+template <typename T>
+__global__ void __launch_bounds__(256) add_parts(int nparts, int64_t cols, const float *__restrict__ parts,
+                                                 T *__restrict__ out) {
+  const int64_t c = blockIdx.x * 256ll + threadIdx.x;
+  if (c >= cols) return;
+  float s = 0.f;
+  for (int p = 0; p < nparts; ++p) s += parts[p * cols + c];
+  out[c] = from_f32<T>(s);
 }
 
-int64_t pitch(int64_t n) { return (n + 7) / 8 * 8; }
+template <typename E, int S, typename T>
+void column_sums(Call &c, int64_t rows, int64_t cols, const E *a, int64_t lda, int64_t sheet, T *out, float *parts) {
+  const int64_t per = std::max<int64_t>(kSumRows, (rows + kSumParts - 1) / kSumParts);
+  const int n = (int)((rows + per - 1) / per);
+  column_parts<E, S><<<dim3((unsigned)((cols + 31) / 32), n), 256, 0, c.st>>>(rows, cols, a, lda, sheet, per, parts);
+  add_parts<T><<<(unsigned)((cols + 255) / 256), 256, 0, c.st>>>(n, cols, parts, out);
+  c.launched(cudaGetLastError());
+  c.launched(cudaSuccess);
+}
 
-struct FfnLayout {
-  size_t h, total;
+// ------------------------------------------------------------------ buffers
+
+int64_t hidden_pitch(const sla_ffn *f) { return round_up(f->hidden, 16); }
+
+// g, u (dtype) and h (operand sheets), rows hidden_pitch apart.
+struct SavedLayout {
+  size_t u, h, total;
 };
 
-FfnLayout saved_layout(const sla_ffn *f) {
-  FfnLayout L;
-  const size_t e = net_size(f->dtype);
-  L.h = align256(e * (size_t)f->tokens * (size_t)pitch(2 * f->hidden));
-  L.total = L.h + align256(e * (size_t)f->tokens * (size_t)pitch(f->hidden));
+SavedLayout saved_layout(const sla_ffn *f) {
+  const size_t n = (size_t)f->tokens * (size_t)hidden_pitch(f);
+  SavedLayout L;
+  L.u = align256(n * net_size(f->dtype));
+  L.h = 2 * L.u;
+  L.total = L.h + align256(n * 2 * (f->dtype == SLA_F32 ? 3 : 1));
   return L;
 }
+
+ProductSize gate_size(const sla_ffn *f) { return {f->tokens, f->hidden, f->width, 1, 1, 1}; }
+ProductSize out_size(const sla_ffn *f) { return {f->tokens, f->out, f->hidden, 1, 1, 1}; }
+ProductSize dh_size(const sla_ffn *f) { return {f->tokens, f->hidden, f->out, 1, 1, 1}; }
+ProductSize dx_size(const sla_ffn *f) { return {f->tokens, f->width, f->hidden, 1, 1, 2}; }
+ProductSize dw_in_size(const sla_ffn *f) { return {f->hidden, f->width, f->tokens, 2, 1, 1}; }
+ProductSize dw_out_size(const sla_ffn *f) { return {f->out, f->hidden, f->tokens, 1, 1, 1}; }
+
+struct ForwardScratch {
+  void *x, *w_in, *w_out, *h;
+  float *parts;
+  size_t total;
+};
+
+ForwardScratch forward_scratch(const sla_ffn *f, char *base) {
+  const int S = f->dtype == SLA_F32 ? 3 : 1;
+  Arena a{base};
+  ForwardScratch w;
+  w.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
+  w.w_in = a.take(packed_bytes(2 * f->hidden, f->width, f->dtype));
+  w.w_out = a.take(packed_bytes(f->out, f->hidden, f->dtype));
+  w.h = a.take(saved_layout(f).total - saved_layout(f).h);
+  w.parts = (float *)a.take(std::max(plan_product(gate_size(f), S, true).partial_bytes,
+                                     plan_product(out_size(f), S, false).partial_bytes));
+  w.total = a.used;
+  return w;
+}
+
+struct BackwardScratch {
+  void *dy, *x, *w_in, *w_out, *dgu;
+  float *parts;
+  size_t total;
+};
+
+BackwardScratch backward_scratch(const sla_ffn *f, char *base) {
+  const int S = f->dtype == SLA_F32 ? 3 : 1;
+  Arena a{base};
+  BackwardScratch w;
+  w.dy = a.take(packed_bytes(f->tokens, f->out, f->dtype));
+  w.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
+  w.w_in = a.take(packed_bytes(2 * f->hidden, f->width, f->dtype));
+  w.w_out = a.take(packed_bytes(f->out, f->hidden, f->dtype));
+  w.dgu = a.take((size_t)f->tokens * (size_t)hidden_pitch(f) * 2 * 2 * S);
+  size_t parts = kSumParts * sizeof(float) * (size_t)std::max(f->hidden, f->out);
+  for (const ProductSize &s : {dh_size(f), dx_size(f), dw_in_size(f), dw_out_size(f)})
+    parts = std::max(parts, plan_product(s, S, false).partial_bytes);
+  w.parts = (float *)a.take(parts);
+  w.total = a.used;
+  return w;
+}
+
+// ------------------------------------------------------------------ the two calls
+
+sla_status finish(const Call &c) {
+  count_launches(c.launches);
+  return c.err == cudaSuccess ? SLA_OK : fail(c.err);
+}
+
+template <typename T>
+bool vec_out(const T *p, int64_t ld) {
+  return aligned(p, 16) && ld * sizeof(T) % 16 == 0;
+}
+
+template <typename T>
+sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, const T *b_in, const T *w_out,
+                   const T *b_out, T *y, char *saved, char *ws, cudaStream_t st) {
+  Call c{st};
+  c.timeouts = timeouts_address();
+  if (!c.timeouts) return fail(cudaGetLastError());
+  const SavedLayout L = saved_layout(f);
+  const ForwardScratch w = forward_scratch(f, ws);
+  const int64_t ldg = hidden_pitch(f);
+  void *h = saved ? saved + L.h : w.h;
+  const Operand ox = as_operand(c, x, f->tokens, f->width, ldx, 1, w.x);
+  const Operand oi = as_operand(c, w_in, f->hidden, f->width, f->width, 2, w.w_in);
+  const Operand oo = as_operand(c, w_out, f->out, f->hidden, f->hidden, 1, w.w_out);
+  ProductArgs p{};
+  p.act = f->activation, p.bias = b_in, p.vec = 1;
+  p.g = saved, p.u = saved ? saved + L.u : nullptr;
+  p.h = (uint16_t *)h, p.ldg = ldg, p.sheet = f->tokens * ldg;
+  run_product<T>(c, kGate, gate_size(f), ox, false, oi, false, p, w.parts);
+  const Operand oh{h, f->hidden, f->tokens, sheets_of<T>(), ldg, f->tokens * ldg};
+  ProductArgs q{};
+  q.bias = b_out, q.c = y, q.ldc = f->out, q.vec = vec_out(y, f->out);
+  run_product<T>(c, kStore, out_size(f), oh, false, oo, false, q, w.parts);
+  return finish(c);
+}
+
+template <typename T>
+sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int64_t ldx, const T *w_in,
+                    const T *w_out, const char *saved, T *dx, T *dw_in, T *dw_out, T *db_in, T *db_out, char *ws,
+                    cudaStream_t st) {
+  using E = typename std::conditional<sizeof(T) == 4, bf16, T>::type;  // type of the operand sheets
+  constexpr int S = sheets_of<T>();
+  Call c{st};
+  c.timeouts = timeouts_address();
+  if (!c.timeouts) return fail(cudaGetLastError());
+  const SavedLayout L = saved_layout(f);
+  const BackwardScratch w = backward_scratch(f, ws);
+  const int64_t ldg = hidden_pitch(f), sheet = f->tokens * ldg;
+  const bool inner = dx || dw_in || db_in;
+  Operand ody{}, ox{}, oi{};
+  if (inner || dw_out) ody = as_operand(c, dy, f->tokens, f->out, lddy, 1, w.dy);
+  const Operand odgu{w.dgu, f->hidden, f->tokens, 2 * S, ldg, sheet};
+  const Operand oh{saved + L.h, f->hidden, f->tokens, S, ldg, sheet};
+  if (inner) {
+    const Operand oo = as_operand(c, w_out, f->out, f->hidden, f->hidden, 1, w.w_out);
+    ProductArgs p{};
+    p.act = f->activation, p.vec = 1;
+    p.g = (void *)saved, p.u = (void *)(saved + L.u);
+    p.h = (uint16_t *)w.dgu, p.ldg = ldg, p.sheet = sheet;
+    run_product<T>(c, kGateBack, dh_size(f), ody, false, oo, true, p, w.parts);
+  }
+  auto store = [&](const ProductSize &s, const Operand &a, bool a_mn, const Operand &b, T *out) {
+    ProductArgs p{};
+    p.c = out, p.ldc = s.n, p.c_m_half = s.m * s.n, p.vec = vec_out(out, s.n);
+    run_product<T>(c, kStore, s, a, a_mn, b, true, p, w.parts);
+  };
+  if (dx) {
+    oi = as_operand(c, w_in, f->hidden, f->width, f->width, 2, w.w_in);
+    store(dx_size(f), odgu, false, oi, dx);
+  }
+  if (dw_in) {
+    ox = as_operand(c, x, f->tokens, f->width, ldx, 1, w.x);
+    store(dw_in_size(f), odgu, true, ox, dw_in);
+  }
+  if (dw_out) store(dw_out_size(f), ody, true, oh, dw_out);
+  if (db_in)
+    for (int half = 0; half < 2; ++half)
+      column_sums<E, S>(c, f->tokens, f->hidden, (const E *)w.dgu + half * sheet, ldg, 2 * sheet,
+                        db_in + half * f->hidden, w.parts);
+  if (db_out) column_sums<T, 1>(c, f->tokens, f->out, dy, lddy, 0, db_out, w.parts);
+  return finish(c);
+}
+
+// ------------------------------------------------------------------ argument checks
 
 sla_status check_ffn(const sla_ffn *f) {
   if (!f) return SLA_INVALID_ARG;
   const int64_t most = (int64_t)1 << 24;
-  if (f->tokens < 0 || f->tokens > ((int64_t)1 << 31) - 1) return SLA_INVALID_ARG;
+  if (f->tokens < 0 || f->tokens > (int64_t)1 << 30) return SLA_INVALID_ARG;
   if (f->width < 1 || f->width > most || f->hidden < 1 || f->hidden > most || f->out < 1 || f->out > most)
     return SLA_INVALID_ARG;
   if (!net_dtype(f->dtype) || f->activation < SLA_ACT_SILU || f->activation > SLA_ACT_RELU) return SLA_INVALID_ARG;
@@ -156,73 +540,6 @@ sla_status check_scratch(const void *ws, size_t bytes, size_t need) {
   return bytes < need ? SLA_WORKSPACE_TOO_SMALL : SLA_OK;
 }
 
-template <typename T>
-sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, const T *b_in, const T *w_out,
-                   const T *b_out, T *y, char *saved, char *ws, cudaStream_t st) {
-  const FfnLayout L = saved_layout(f);
-  T *h = (T *)(saved ? saved + L.h : ws);
-  Product<T> p{};
-  p.m = f->tokens, p.n = f->hidden, p.k = f->width;
-  p.a = x, p.a_row = ldx, p.a_col = 1;
-  p.b = w_in, p.b_row = f->width, p.b_col = 1, p.b_up = f->hidden * f->width;
-  p.bias = b_in, p.c = h, p.ldc = pitch(f->hidden), p.gu = (T *)saved, p.ldgu = pitch(2 * f->hidden);
-  p.act = f->activation;
-  launch<T, kGate>(p, st);
-  Product<T> q{};
-  q.m = f->tokens, q.n = f->out, q.k = f->hidden;
-  q.a = h, q.a_row = pitch(f->hidden), q.a_col = 1;
-  q.b = w_out, q.b_row = f->hidden, q.b_col = 1;
-  q.bias = b_out, q.c = y, q.ldc = f->out;
-  launch<T, kStore>(q, st);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(e);
-  count_launches(2);
-  return SLA_OK;
-}
-
-template <typename T>
-sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int64_t ldx, const T *w_in,
-                    const T *w_out, const char *saved, T *dx, T *dw_in, T *dw_out, T *db_in, T *db_out, char *ws,
-                    cudaStream_t st) {
-  const FfnLayout L = saved_layout(f);
-  const T *h = (const T *)(saved + L.h);
-  T *dgu = (T *)ws;
-  const int64_t ldgu = pitch(2 * f->hidden);
-  uint64_t launches = 0;
-  if (dx || dw_in || db_in) {
-    Product<T> p{};
-    p.m = f->tokens, p.n = f->hidden, p.k = f->out;
-    p.a = dy, p.a_row = lddy, p.a_col = 1;
-    p.b = w_out, p.b_row = 1, p.b_col = f->hidden;
-    p.gu = (T *)saved, p.ldgu = ldgu, p.dgu = dgu, p.act = f->activation;
-    launch<T, kGateBack>(p, st);
-    ++launches;
-  }
-  auto product = [&](int64_t m, int64_t n, int64_t k, const T *a, int64_t ar, int64_t ac, const T *b, int64_t br,
-                     int64_t bc, T *c) {
-    Product<T> p{};
-    p.m = m, p.n = n, p.k = k, p.a = a, p.a_row = ar, p.a_col = ac, p.b = b, p.b_row = br, p.b_col = bc;
-    p.c = c, p.ldc = n;
-    launch<T, kStore>(p, st);
-    ++launches;
-  };
-  if (dx) product(f->tokens, f->width, 2 * f->hidden, dgu, ldgu, 1, w_in, 1, f->width, dx);
-  if (dw_in) product(2 * f->hidden, f->width, f->tokens, dgu, 1, ldgu, x, 1, ldx, dw_in);
-  if (dw_out) product(f->out, f->hidden, f->tokens, dy, 1, lddy, h, 1, pitch(f->hidden), dw_out);
-  if (db_in) {
-    column_sums<T><<<(unsigned)((2 * f->hidden + 31) / 32), 1024, 0, st>>>(f->tokens, 2 * f->hidden, dgu, ldgu, db_in);
-    ++launches;
-  }
-  if (db_out) {
-    column_sums<T><<<(unsigned)((f->out + 31) / 32), 1024, 0, st>>>(f->tokens, f->out, dy, lddy, db_out);
-    ++launches;
-  }
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(e);
-  count_launches(launches);
-  return SLA_OK;
-}
-
 }  // namespace
 }  // namespace sla
 
@@ -235,13 +552,11 @@ SLA_API size_t sla_gated_ffn_saved_bytes(const sla_ffn *f) {
 }
 
 SLA_API size_t sla_gated_ffn_workspace_bytes(const sla_ffn *f) {
-  if (check_ffn(f) != SLA_OK) return 0;
-  return saved_layout(f).total - saved_layout(f).h;
+  return check_ffn(f) == SLA_OK ? forward_scratch(f, nullptr).total : 0;
 }
 
 SLA_API size_t sla_gated_ffn_backward_workspace_bytes(const sla_ffn *f) {
-  if (check_ffn(f) != SLA_OK) return 0;
-  return saved_layout(f).h;
+  return check_ffn(f) == SLA_OK ? backward_scratch(f, nullptr).total : 0;
 }
 
 SLA_API sla_status sla_gated_ffn(const sla_ffn *f, const void *x, int64_t ldx, const void *w_in, const void *b_in,
@@ -297,6 +612,17 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
               (T *)dx, (T *)dw_in, (T *)dw_out, (T *)db_in, (T *)db_out, (char *)workspace, st)
   return f->dtype == SLA_F32 ? SLA_FFN_BWD(float) : f->dtype == SLA_F16 ? SLA_FFN_BWD(f16) : SLA_FFN_BWD(bf16);
 #undef SLA_FFN_BWD
+}
+
+SLA_API sla_status sla_gated_ffn_check(void *stream) {
+  uint32_t *p = timeouts_address();
+  if (!p) return fail(cudaGetLastError());
+  uint32_t n = 0;
+  cudaError_t e = cudaMemcpyAsync(&n, p, sizeof(n), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e == cudaSuccess && n) e = cudaMemsetAsync(p, 0, sizeof(n), (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(e);
+  return n ? SLA_TIMEOUT : SLA_OK;
 }
 
 }  // extern "C"

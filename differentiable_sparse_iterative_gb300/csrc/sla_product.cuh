@@ -1,0 +1,455 @@
+// Tensor-core matrix products of the gated feed-forward block, with the block's elementwise work as
+// their epilogues.
+//
+//   C[m][n] = sum over segments s, sum over k of A_s(m, k) B_s(n, k)
+//
+// Operands are 16-bit and read by TMA from three-dimensional tensors (contiguous dimension, rows,
+// sheets).  A segment names a sheet of A and one of B, which covers
+//   - float32 data, held as three bfloat16 sheets x = x0 + x1 + x2 of falling size (8 bits each, 24
+//     in all): the six products x_i y_j with i + j <= 2, smallest first, give float32's accuracy
+//     (what is dropped is below 2^-26 of a term);
+//   - the sum over both halves of [g u], which lie in two sheets.
+// Either operand may be k-major (k contiguous) or mn-major (rows or columns contiguous): the tensor
+// core reads both from the 128-byte swizzled tiles that TMA writes, so no operand is transposed.
+//
+// One block (or a pair of blocks on two multiprocessors, CG = 2, each with half of B and its own 128
+// rows) keeps a tile of 128 CG x BN in tensor memory, twice: while eight warps empty one through the
+// epilogue, one thread feeds the next tile's mma and another its TMA loads.  Blocks are persistent and
+// take tiles in bands of kBand tile rows, so that what the running blocks read stays in L2.
+#pragma once
+
+#include "sla_act.cuh"
+#include "sla_net.cuh"
+#include "sla_tc.cuh"
+
+namespace sla {
+
+enum Epilogue {
+  kStore,     // c = sum (+ bias)
+  kPartial,   // float32 sums of one split of k
+  kGate,      // columns of g and u side by side: h = act(g) u, g and u kept
+  kGateBack,  // sum = dh: dg = dh u act'(g), du = dh act(g)
+};
+
+constexpr int kDepth = 64;      // k of a stage: 128 bytes, the swizzle's width
+constexpr int kBand = 8;
+constexpr int kMaxSegments = 12;
+constexpr int kEpilogueWarps = 8;
+constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
+
+struct ProductArgs {
+  int m, n;                  // rows and columns of one half of C
+  int m_halves, n_halves;    // 2: A's (B's) sheets come in pairs, one for each half of C's rows (columns)
+  int m_tiles, n_tiles;      // of one half
+  int k_blocks;              // of a segment
+  int splits;                // k_blocks are dealt to this many blocks (kPartial)
+  int segments;
+  int8_t a_sheet[kMaxSegments], b_sheet[kMaxSegments];
+  int a_mn, b_mn;
+  int f16;                   // operands are float16 (else bfloat16)
+  int act;
+  int vec;                   // rows of c, g, u, h, dgu may be accessed 16 bytes at a time
+  void *c;                   // kStore: T, kPartial: float [splits][..]
+  int64_t ldc, c_m_half, c_n_half, c_split;
+  const void *bias;          // T, [n] (kStore) or [2 n] (kGate), or NULL
+  void *g, *u;               // T [m][ldg]: written by kGate (NULL: not kept), read by kGateBack
+  uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
+  int64_t ldg, sheet;        // elements between rows and between sheets of h
+  uint32_t *timeouts;
+};
+
+// Tile shapes: CG blocks of 128 rows, BN columns, stages that fill the shared memory of a multiprocessor.
+template <int CG, int BN>
+struct ProductShape {
+  static constexpr int a_bytes = 128 * kDepth * 2;
+  static constexpr int b_bytes = BN / CG * kDepth * 2;
+  static constexpr int stages = (208 * 1024) / (a_bytes + b_bytes) > 8 ? 8 : (208 * 1024) / (a_bytes + b_bytes);
+  static constexpr int smem = stages * (a_bytes + b_bytes) + 1024 /* alignment */ + 256 /* barriers */;
+};
+
+// Three bfloat16 values whose sum is v to 2^-24: each the rounded rest of the one before.  An
+// infinity stays in the first (its rest would be NaN).
+__device__ __forceinline__ void split3(float v, uint16_t (&s)[3]) {
+  const bf16 a = __float2bfloat16_rn(v);
+  const float fa = __bfloat162float(a);
+  const float r = isinf(fa) ? 0.f : v - fa;
+  const bf16 b = __float2bfloat16_rn(r);
+  const bf16 c = __float2bfloat16_rn(r - __bfloat162float(b));
+  s[0] = __bfloat16_as_ushort(a);
+  s[1] = __bfloat16_as_ushort(b);
+  s[2] = __bfloat16_as_ushort(c);
+}
+
+__device__ __forceinline__ uint16_t bits16(f16 v) { return __half_as_ushort(v); }
+__device__ __forceinline__ uint16_t bits16(bf16 v) { return __bfloat16_as_ushort(v); }
+
+// N values of a row as an operand of a later product: one sheet of T, or float32's three.
+template <typename T, int N>
+__device__ __forceinline__ void store_operand(uint16_t *p, int64_t sheet, const float (&v)[N], int count, bool vec) {
+  constexpr int S = sizeof(T) == 4 ? 3 : 1;
+  uint16_t w[S][N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (S == 3) {
+      uint16_t s[3];
+      split3(v[i], s);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) w[q][i] = s[q];
+    } else {
+      w[0][i] = bits16(from_f32<T>(v[i]));
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < S; ++q) {
+    uint16_t *d = p + q * sheet;
+    if (vec && count >= N) {
+#pragma unroll
+      for (int i = 0; i < N; i += 8) *reinterpret_cast<Pack<uint16_t, 8> *>(d + i) = *reinterpret_cast<Pack<uint16_t, 8> *>(&w[q][i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < count) d[i] = w[q][i];
+    }
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[N], int count, bool vec) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec && count >= N) {
+#pragma unroll
+    for (int i = 0; i < N; i += V) {
+      Pack<T, V> q;
+#pragma unroll
+      for (int k = 0; k < V; ++k) q.v[k] = from_f32<T>(v[i + k]);
+      *reinterpret_cast<Pack<T, V> *>(p + i) = q;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < count) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void load_row(const T *p, float (&v)[N], int count, bool vec) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec && count >= N) {
+#pragma unroll
+    for (int i = 0; i < N; i += V) {
+      const Pack<T, V> q = *reinterpret_cast<const Pack<T, V> *>(p + i);
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[i + k] = to_f32(q.v[k]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < count ? to_f32(p[i]) : 0.f;
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < count) v[i] += to_f32(bias[i]);
+}
+
+// The tile (of all halves) and split of a work item.
+struct Tile {
+  int m_half, m0, n_half, n0, split;
+};
+
+template <int EPI, int CG, int BN>
+__device__ __forceinline__ Tile tile_of(const ProductArgs &p, int item) {
+  const int mt = p.m_halves * p.m_tiles, nt = p.n_halves * p.n_tiles, per = mt * nt;
+  Tile t;
+  t.split = item / per;
+  int i = item - t.split * per;
+  const int band = i / (kBand * nt);
+  i -= band * kBand * nt;
+  const int rows = min(kBand, mt - band * kBand);
+  const int tn = i / rows, tm = band * kBand + i % rows;
+  t.m_half = tm / p.m_tiles;
+  t.m0 = (tm - t.m_half * p.m_tiles) * 128 * CG;
+  t.n_half = tn / p.n_tiles;
+  t.n0 = (tn - t.n_half * p.n_tiles) * (EPI == kGate ? BN / 2 : BN);
+  return t;
+}
+
+__device__ __forceinline__ void split_range(const ProductArgs &p, int split, int &k0, int &k1) {
+  k0 = (int)((int64_t)p.k_blocks * split / p.splits);
+  k1 = (int)((int64_t)p.k_blocks * (split + 1) / p.splits);
+}
+
+template <typename T, int EPI, int CG, int BN>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                   const __grid_constant__ ProductArgs p) {
+  using Shape = ProductShape<CG, BN>;
+  constexpr int S = Shape::stages;
+  extern __shared__ uint8_t raw[];
+  uint8_t *tiles = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *sa = tiles, *sb = tiles + S * Shape::a_bytes;
+  uint64_t *full = (uint64_t *)(tiles + S * (Shape::a_bytes + Shape::b_bytes));
+  uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 2, *drained = acc_empty + 2;
+  uint32_t *tmem_slot = (uint32_t *)(drained + 1);
+  volatile uint32_t *dead = tmem_slot + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
+  const int items = p.m_halves * p.m_tiles * p.n_halves * p.n_tiles * p.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, kEpilogueWarps * CG);
+    }
+    mbar_init(drained, 1);
+    *dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+    tma_prefetch_map(&ma);
+    tma_prefetch_map(&mb);
+  }
+  if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    // loads: one stage is kDepth of k of the tile's rows of A and columns of B
+    constexpr uint32_t bytes = CG * (Shape::a_bytes + Shape::b_bytes);
+    uint32_t n = 0;
+    for (int item = worker; item < items && !*dead; item += workers) {
+      const Tile t = tile_of<EPI, CG, BN>(p, item);
+      int k0, k1;
+      split_range(p, t.split, k0, k1);
+      const int am = t.m0 + (int)rank * 128;
+      for (int seg = 0; seg < p.segments && !*dead; ++seg) {
+        const int az = p.a_sheet[seg] + t.m_half, bz = p.b_sheet[seg] + t.n_half;
+        for (int kb = k0; kb < k1; ++kb, ++n) {
+          const int s = n % S;
+          if (n >= S && !mbar_wait_clocks(empty + s, ((n / S) - 1) & 1)) {
+            *dead = 1;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+          uint8_t *da = sa + s * Shape::a_bytes, *db = sb + s * Shape::b_bytes;
+          const int k = kb * kDepth;
+          if (p.a_mn) {
+            tma_load<CG>(da, &ma, am, k, az, full + s);
+            tma_load<CG>(da + Shape::a_bytes / 2, &ma, am + 64, k, az, full + s);
+          } else {
+            tma_load<CG>(da, &ma, k, am, az, full + s);
+          }
+          if (EPI == kGate) {
+            // half of the columns are g's, half u's; in a pair of blocks each loads one of them
+            if (CG == 2) {
+              tma_load<CG>(db, &mb, k, t.n0, bz + (int)rank, full + s);
+            } else {
+              tma_load<CG>(db, &mb, k, t.n0, bz, full + s);
+              tma_load<CG>(db + Shape::b_bytes / 2, &mb, k, t.n0, bz + 1, full + s);
+            }
+          } else if (p.b_mn) {
+#pragma unroll
+            for (int j = 0; j < BN / CG / 64; ++j)
+              tma_load<CG>(db + j * kDepth * 128, &mb, t.n0 + (int)rank * (BN / CG) + j * 64, k, bz, full + s);
+          } else {
+            tma_load<CG>(db, &mb, k, t.n0 + (int)rank * (BN / CG), bz, full + s);
+          }
+        }
+      }
+    }
+    // every copy has landed before the block may end (the mma thread waited for all but after a timeout)
+    if (rank == 0)
+      for (uint32_t i = n > S ? n - S : 0; i < n; ++i)
+        if (!mbar_wait_clocks(full + i % S, (i / S) & 1)) *dead = 1;
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    const uint32_t idesc = tc_idesc(p.f16, p.a_mn, p.b_mn, 128 * CG, BN);
+    const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
+    uint32_t n = 0, tile = 0;
+    for (int item = worker; item < items && !*dead; item += workers, ++tile) {
+      const Tile t = tile_of<EPI, CG, BN>(p, item);
+      int k0, k1;
+      split_range(p, t.split, k0, k1);
+      const uint32_t acc = tile & 1, use = tile >> 1;
+      if (use > 0 && !mbar_wait_clocks(acc_empty + acc, (use - 1) & 1)) {
+        *dead = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + acc * BN;
+      const int steps = p.segments * (k1 - k0);
+      for (int i = 0; i < steps; ++i, ++n) {
+        const int s = n % S;
+        if (!mbar_wait_clocks(full + s, (n / S) & 1)) {
+          *dead = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t a = tc_desc(sa + s * Shape::a_bytes, p.a_mn, Shape::a_bytes / 2);
+        const uint64_t b = tc_desc(sb + s * Shape::b_bytes, p.b_mn, kDepth * 128);
+#pragma unroll
+        for (int j = 0; j < kDepth / 16; ++j)
+          tc_mma<CG>(d, a + j * a_step, b + j * b_step, idesc, i > 0 || j > 0);
+        tc_commit<CG>(empty + s);
+      }
+      if (*dead) break;
+      tc_commit<CG>(acc_full + acc);
+    }
+    if (*dead) {  // the mma in flight still read shared memory
+      tc_commit<CG>(drained);
+      mbar_wait_clocks(drained, 0);
+    }
+  } else if (warp >= 2) {
+    const int quarter = warp & 3, side = (warp - 2) >> 2;
+    // columns at a time (g and u together, and float32's three sheets, need the registers of two)
+    constexpr int N = EPI == kGate && (BN == 64 || sizeof(T) == 4) ? 16 : 32;
+    constexpr bool fast = sizeof(T) == 2;
+    uint32_t tile = 0;
+    for (int item = worker; item < items; item += workers, ++tile) {
+      const Tile t = tile_of<EPI, CG, BN>(p, item);
+      const uint32_t acc = tile & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
+        *dead = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t base = tmem + acc * BN + ((uint32_t)quarter << 21);
+      const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
+      const bool live = row < p.m;
+      constexpr int width = EPI == kGate ? BN / 4 : BN / 2;  // columns of this warp
+#pragma unroll 1
+      for (int c = side * width; c < (side + 1) * width; c += N) {
+        const int col = t.n0 + c, count = p.n - col;
+        float v[N];
+        if constexpr (N == 32)
+          tmem_load32(base + c, v);
+        else
+          tmem_load16(base + c, v);
+        if constexpr (EPI == kGate) {
+          float u[N];
+          if constexpr (N == 32)
+            tmem_load32(base + BN / 2 + c, u);
+          else
+            tmem_load16(base + BN / 2 + c, u);
+          tmem_wait(v);
+          tmem_wait(u);
+          if (live && count > 0) {
+            if (p.bias) {
+              add_bias<T, N>(v, (const T *)p.bias + col, count);
+              add_bias<T, N>(u, (const T *)p.bias + p.n + col, count);
+            }
+            const int64_t o = row * p.ldg + col;
+            if (p.g) {
+              store_row<T, N>((T *)p.g + o, v, count, p.vec);
+              store_row<T, N>((T *)p.u + o, u, count, p.vec);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = activate<fast>(p.act, v[i]).a * u[i];
+            store_operand<T, N>(p.h + o, p.sheet, v, count, p.vec);
+          }
+        } else if constexpr (EPI == kGateBack) {
+          float g[N], u[N];
+          const int64_t o = row * p.ldg + col;
+          if (live && count > 0) {
+            load_row<T, N>((const T *)p.g + o, g, count, p.vec);
+            load_row<T, N>((const T *)p.u + o, u, count, p.vec);
+          }
+          tmem_wait(v);
+          if (live && count > 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const ActValue a = activate<fast>(p.act, g[i]);
+              g[i] = v[i] * u[i] * a.da;
+              u[i] = v[i] * a.a;
+            }
+            // sheets: dg and du of each part of the value
+            store_operand<T, N>(p.h + o, 2 * p.sheet, g, count, p.vec);
+            store_operand<T, N>(p.h + p.sheet + o, 2 * p.sheet, u, count, p.vec);
+          }
+        } else {
+          tmem_wait(v);
+          if (live && count > 0) {
+            const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
+            if constexpr (EPI == kPartial) {
+              store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, p.vec);
+            } else {
+              if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count);
+              store_row<T, N>((T *)p.c + o, v, count, p.vec);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          mbar_arrive_rank(acc_empty + acc, 0);
+        else
+          mbar_arrive(acc_empty + acc);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  if (CG == 2) cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_free<CG>(tmem, 2 * BN);
+  if (threadIdx.x == 0 && *dead) atomicAdd(p.timeouts, 1u);
+}
+
+// Tile shapes by index, widest first.
+struct ProductTile {
+  int cg, bn;
+};
+constexpr ProductTile kProductTiles[] = {{2, 256}, {1, 256}, {1, 128}, {1, 64}};
+constexpr int kProductTileCount = 4;
+
+// Launches `epi` with tile shape kProductTiles[shape] on `blocks` blocks.
+template <typename T>
+cudaError_t launch_product(int epi, int shape, int blocks, const CUtensorMap &a, const CUtensorMap &b,
+                           const ProductArgs &p, cudaStream_t st);
+
+template <typename T, int EPI, int CG, int BN>
+cudaError_t launch_product_as(int blocks, const CUtensorMap &a, const CUtensorMap &b, const ProductArgs &p,
+                              cudaStream_t st) {
+  constexpr int smem = ProductShape<CG, BN>::smem;
+  auto kernel = product_kernel<T, EPI, CG, BN>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG == 2 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a, b, p);
+}
+
+template <typename T, int EPI>
+cudaError_t launch_product_shape(int shape, int blocks, const CUtensorMap &a, const CUtensorMap &b,
+                                 const ProductArgs &p, cudaStream_t st) {
+  switch (shape) {
+    case 0: return launch_product_as<T, EPI, 2, 256>(blocks, a, b, p, st);
+    case 1: return launch_product_as<T, EPI, 1, 256>(blocks, a, b, p, st);
+    case 2: return launch_product_as<T, EPI, 1, 128>(blocks, a, b, p, st);
+    default: return launch_product_as<T, EPI, 1, 64>(blocks, a, b, p, st);
+  }
+}
+
+}  // namespace sla

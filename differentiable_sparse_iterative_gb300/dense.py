@@ -247,6 +247,13 @@ def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor
     return (dx,) + grads
 
 
+def sla_gated_ffn_check(device=None) -> None:
+    """Synchronises the current stream and raises SlaError(SLA_TIMEOUT) if a bounded wait inside a
+    gated_ffn kernel expired since the last check (never expected)."""
+    base = _base()
+    base._check(base.lib().sla_gated_ffn_check(base._stream(device)), "sla_gated_ffn_check")
+
+
 class GatedFFN(torch.autograd.Function):
     """y = (act(x Wg^T + bg) * (x Wu^T + bu)) w_out^T + b_out.  Saved for backward: x, the weights and
     g, u and h (3 hidden values a token)."""

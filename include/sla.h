@@ -548,7 +548,7 @@ typedef enum sla_act {
 
 /* A gated feed-forward block: width -> 2 x hidden -> out, over `tokens` rows. */
 typedef struct sla_ffn {
-  int64_t tokens;         /* rows of x, 0 <= tokens < 2^31 */
+  int64_t tokens;         /* rows of x, 0 <= tokens <= 2^30 */
   int64_t width;          /* columns of x, 1 .. 2^24, as hidden and out */
   int64_t hidden;
   int64_t out;            /* columns of y */
@@ -570,8 +570,9 @@ SLA_API size_t sla_gated_ffn_backward_workspace_bytes(const sla_ffn *f);
  *   saved  device, sla_gated_ffn_saved_bytes, 256-byte aligned, or NULL: kept for the backward call
  *   workspace  device, sla_gated_ffn_workspace_bytes, 256-byte aligned
  * Sums run in float32.  With 16-bit data, g, u (where saved) and h are rounded to dtype; with
- * float32 data they stay float32, as do the products.  A float16 block whose |h| passes 65504 gives
- * infinities, as float16 data does everywhere.
+ * float32 data they stay float32, and the products are float32's (each factor split into three
+ * bfloat16 parts, 24 bits in all; an infinity among the factors gives NaN).  A float16 block whose
+ * |h| passes 65504 gives infinities, as float16 data does everywhere.
  */
 SLA_API sla_status sla_gated_ffn(const sla_ffn *f, const void *x, int64_t ldx, const void *w_in, const void *b_in,
                                  const void *w_out, const void *b_out, void *y, void *saved, size_t saved_bytes,
@@ -586,6 +587,13 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
                                           const void *w_in, const void *w_out, const void *saved, size_t saved_bytes,
                                           void *dx, void *dw_in, void *dw_out, void *db_in, void *db_out,
                                           void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Every wait inside the products' kernels is bounded (about two seconds); one that expires, which no
+ * input can cause, leaves its tile unwritten.  Synchronises the stream and returns SLA_TIMEOUT if
+ * that happened on this device since the last check, else SLA_OK.
+ */
+SLA_API sla_status sla_gated_ffn_check(void *stream);
 
 /* ---------------------------------------------------------------- tuning and testing */
 
