@@ -167,7 +167,7 @@ ProductPlan plan_product(const ProductSize &s, int sheets, bool gate) {
   const double block_us[kProductTileCount] = {0.29, 0.33, 0.18, 0.11};
   ProductPlan best{0, 1, 0};
   double best_us = 1e30;
-  for (int i = 1; i < kProductTileCount; ++i) {
+  for (int i = 0; i < kProductTileCount; ++i) {
     const int bm = 128 * kProductTiles[i].cg, bn = kProductTiles[i].bn;
     const int64_t workers = sms / kProductTiles[i].cg;
     const int64_t mt = s.m_halves * ((s.m + bm - 1) / bm);
