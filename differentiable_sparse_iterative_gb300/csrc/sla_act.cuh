@@ -11,6 +11,8 @@
 
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "sla.h"
 
 namespace sla {
@@ -30,25 +32,35 @@ struct ActValue {
   float a, da;
 };
 
-template <bool Fast>
-__device__ __forceinline__ ActValue activate(int act, float g) {
-  if (act == SLA_ACT_SILU) {
+template <int Act, bool Fast>
+__device__ __forceinline__ ActValue activate(float g) {
+  if constexpr (Act == SLA_ACT_SILU) {
     const float s = sigmoid<Fast>(g);
     return {g * s, s * (1.f + g * (1.f - s))};
-  }
-  if (act == SLA_ACT_GELU) {
+  } else if constexpr (Act == SLA_ACT_GELU) {
     const float phi = 0.5f * (1.f + erff(g * 0.7071067811865476f));
     const float e = Fast ? __expf(-0.5f * g * g) : expf(-0.5f * g * g);
     return {g * phi, phi + g * e * 0.3989422804014327f};
-  }
-  if (act == SLA_ACT_GELU_TANH) {
+  } else if constexpr (Act == SLA_ACT_GELU_TANH) {
     const float z = 0.7978845608028654f * (g + 0.044715f * g * g * g);
     const float t = tanh_of<Fast>(z);
     return {0.5f * g * (1.f + t), 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * 0.7978845608028654f *
                                                           (1.f + 3.f * 0.044715f * g * g)};
+  } else {
+    // written so that a NaN stays one
+    return {g < 0.f ? 0.f : g, g > 0.f ? 1.f : 0.f};
   }
-  // written so that a NaN stays one
-  return {g < 0.f ? 0.f : g, g > 0.f ? 1.f : 0.f};
+}
+
+// Calls f with the activation as a constant: one branch for a whole loop, not one for each value.
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F &&f) {
+  switch (act) {
+    case SLA_ACT_SILU: f(std::integral_constant<int, SLA_ACT_SILU>{}); break;
+    case SLA_ACT_GELU: f(std::integral_constant<int, SLA_ACT_GELU>{}); break;
+    case SLA_ACT_GELU_TANH: f(std::integral_constant<int, SLA_ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, SLA_ACT_RELU>{});
+  }
 }
 
 }  // namespace sla

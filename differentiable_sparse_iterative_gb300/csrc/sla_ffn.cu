@@ -87,7 +87,13 @@ __global__ void __launch_bounds__(256) pack_operand(int64_t rows, int64_t cols, 
     const int64_t half = hr / rows, r = hr - half * rows;
     float v[8];
     const T *s = src + half * src_half + r * src_ld + c;
-    load_row<T, 8>(s, v, (int)(cols - c < 8 ? cols - c : 8), vec);
+    const int count = (int)(cols - c < 8 ? cols - c : 8);
+    if (vec && count == 8) {
+      load_f32<T, 8>(s, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = k < count ? to_f32(s[k]) : 0.f;
+    }
     store_operand<T, 8>(dst + half * sheet + r * ld + c, halves * sheet, v, 8, true);
   }
 }
@@ -239,12 +245,14 @@ __global__ void __launch_bounds__(256) finish_splits(ProductArgs p, const float 
           ((T *)p.g)[o + k] = from_f32<T>(g);
           ((T *)p.u)[o + k] = from_f32<T>(up);
         }
-        v[k] = activate<fast>(p.act, g).a * up;
+        with_activation(p.act, [&](auto act) { v[k] = activate<act.value, fast>(g).a * up; });
       } else {
         const float g = to_f32(((const T *)p.g)[o + k]), up = to_f32(((const T *)p.u)[o + k]);
-        const ActValue a = activate<fast>(p.act, g);
-        u[k] = v[k] * a.a;
-        v[k] = v[k] * up * a.da;
+        with_activation(p.act, [&](auto act) {
+          const ActValue a = activate<act.value, fast>(g);
+          u[k] = v[k] * a.a;
+          v[k] = v[k] * up * a.da;
+        });
       }
     }
     if (EPI == kGate) {
@@ -441,7 +449,7 @@ sla_status finish(const Call &c) {
 
 template <typename T>
 bool vec_out(const T *p, int64_t ld) {
-  return aligned(p, 16) && ld * sizeof(T) % 16 == 0;
+  return aligned(p, 32) && ld * sizeof(T) % 32 == 0;
 }
 
 template <typename T>

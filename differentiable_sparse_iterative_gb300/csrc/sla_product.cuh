@@ -48,7 +48,7 @@ struct ProductArgs {
   int a_mn, b_mn;
   int f16;                   // operands are float16 (else bfloat16)
   int act;
-  int vec;                   // rows of c, g, u, h, dgu may be accessed 16 bytes at a time
+  int vec;                   // rows of c are aligned to 32 bytes (those of g, u and h always are)
   void *c;                   // kStore: T, kPartial: float [splits][..]
   int64_t ldc, c_m_half, c_n_half, c_split;
   const void *bias;          // T, [n] (kStore) or [2 n] (kGate), or NULL
@@ -83,6 +83,42 @@ __device__ __forceinline__ void split3(float v, uint16_t (&s)[3]) {
 __device__ __forceinline__ uint16_t bits16(f16 v) { return __half_as_ushort(v); }
 __device__ __forceinline__ uint16_t bits16(bf16 v) { return __bfloat16_as_ushort(v); }
 
+// 32 bytes, a whole sector of L2, in one move (p aligned to them).
+struct alignas(32) Sector {
+  uint32_t w[8];
+};
+
+__device__ __forceinline__ void store_sector(void *p, const Sector &s) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(s.w[0]), "r"(s.w[1]),
+               "r"(s.w[2]), "r"(s.w[3]), "r"(s.w[4]), "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ Sector load_sector(const void *p) {
+  Sector s;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(s.w[0]), "=r"(s.w[1]), "=r"(s.w[2]), "=r"(s.w[3]), "=r"(s.w[4]), "=r"(s.w[5]), "=r"(s.w[6]),
+                 "=r"(s.w[7])
+               : "l"(p)
+               : "memory");
+  return s;
+}
+
+__device__ __forceinline__ uint32_t pair16(float a, float b, f16) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pair16(float a, float b, bf16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpair16(uint32_t w, f16) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ float2 unpair16(uint32_t w, bf16) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+}
+
 // N values of a row as an operand of a later product: one sheet of T, or float32's three.
 template <typename T, int N>
 __device__ __forceinline__ void store_operand(uint16_t *p, int64_t sheet, const float (&v)[N], int count, bool vec) {
@@ -103,8 +139,19 @@ __device__ __forceinline__ void store_operand(uint16_t *p, int64_t sheet, const 
   for (int q = 0; q < S; ++q) {
     uint16_t *d = p + q * sheet;
     if (vec && count >= N) {
+      if constexpr (N % 16 == 0) {
 #pragma unroll
-      for (int i = 0; i < N; i += 8) *reinterpret_cast<Pack<uint16_t, 8> *>(d + i) = *reinterpret_cast<Pack<uint16_t, 8> *>(&w[q][i]);
+        for (int i = 0; i < N; i += 16) {
+          Sector t;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) t.w[k] = w[q][i + 2 * k] | ((uint32_t)w[q][i + 2 * k + 1] << 16);
+          store_sector(d + i, t);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+          *reinterpret_cast<Pack<uint16_t, 8> *>(d + i) = *reinterpret_cast<Pack<uint16_t, 8> *>(&w[q][i]);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -113,16 +160,22 @@ __device__ __forceinline__ void store_operand(uint16_t *p, int64_t sheet, const 
   }
 }
 
+// N values of a row of T; vec: the row is aligned to 32 bytes.
 template <typename T, int N>
 __device__ __forceinline__ void store_row(T *p, const float (&v)[N], int count, bool vec) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 32 / sizeof(T);
   if (vec && count >= N) {
 #pragma unroll
     for (int i = 0; i < N; i += V) {
-      Pack<T, V> q;
+      Sector q;
 #pragma unroll
-      for (int k = 0; k < V; ++k) q.v[k] = from_f32<T>(v[i + k]);
-      *reinterpret_cast<Pack<T, V> *>(p + i) = q;
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (sizeof(T) == 4)
+          q.w[k] = __float_as_uint(v[i + k]);
+        else
+          q.w[k] = pair16(v[i + 2 * k], v[i + 2 * k + 1], T{});
+      }
+      store_sector(p + i, q);
     }
   } else {
 #pragma unroll
@@ -133,13 +186,21 @@ __device__ __forceinline__ void store_row(T *p, const float (&v)[N], int count, 
 
 template <typename T, int N>
 __device__ __forceinline__ void load_row(const T *p, float (&v)[N], int count, bool vec) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 32 / sizeof(T);
   if (vec && count >= N) {
 #pragma unroll
     for (int i = 0; i < N; i += V) {
-      const Pack<T, V> q = *reinterpret_cast<const Pack<T, V> *>(p + i);
+      const Sector q = load_sector(p + i);
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[i + k] = to_f32(q.v[k]);
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (sizeof(T) == 4) {
+          v[i + k] = __uint_as_float(q.w[k]);
+        } else {
+          const float2 f = unpair16(q.w[k], T{});
+          v[i + 2 * k] = f.x;
+          v[i + 2 * k + 1] = f.y;
+        }
+      }
     }
   } else {
 #pragma unroll
@@ -352,8 +413,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               store_row<T, N>((T *)p.g + o, v, count, p.vec);
               store_row<T, N>((T *)p.u + o, u, count, p.vec);
             }
+            with_activation(p.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = activate<fast>(p.act, v[i]).a * u[i];
+              for (int i = 0; i < N; ++i) v[i] = activate<act.value, fast>(v[i]).a * u[i];
+            });
             store_operand<T, N>(p.h + o, p.sheet, v, count, p.vec);
           }
         } else if constexpr (EPI == kGateBack) {
@@ -365,12 +428,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
           tmem_wait(v);
           if (live && count > 0) {
+            with_activation(p.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const ActValue a = activate<fast>(p.act, g[i]);
-              g[i] = v[i] * u[i] * a.da;
-              u[i] = v[i] * a.a;
-            }
+              for (int i = 0; i < N; ++i) {
+                const ActValue a = activate<act.value, fast>(g[i]);
+                g[i] = v[i] * u[i] * a.da;
+                u[i] = v[i] * a.a;
+              }
+            });
             // sheets: dg and du of each part of the value
             store_operand<T, N>(p.h + o, 2 * p.sheet, g, count, p.vec);
             store_operand<T, N>(p.h + p.sheet + o, 2 * p.sheet, u, count, p.vec);
