@@ -324,50 +324,81 @@ void run_product(Call &c, Epilogue epi, const ProductSize &s, const Operand &a, 
 
 // ------------------------------------------------------------------ column sums (bias gradients)
 
-constexpr int kSumRows = 512;    // rows of a part at least
-constexpr int kSumParts = 64;    // parts at most
+constexpr int kSumParts = 512;  // parts of the rows at most
 
-// parts[part][cols]: sums over a part of the rows; S sheets `sheet` apart are parts of one value.
-template <typename T, int S>
-__global__ void __launch_bounds__(256) column_parts(int64_t rows, int64_t cols, const T *__restrict__ a, int64_t lda,
-                                                    int64_t sheet, int64_t per, float *__restrict__ parts) {
-  __shared__ float sm[8][33];
-  const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
-  const int64_t c = blockIdx.x * 32ll + lane;
+// parts[part][cols]: sums over a part of the rows, VEC columns a thread; the block's threads cover
+// 256 / tpr rows at a time.  S sheets `sheet` apart are parts of one value.
+template <typename E, int S, int VEC>
+__global__ void __launch_bounds__(256) column_parts(int64_t rows, int64_t cols, const E *__restrict__ a, int64_t lda,
+                                                    int64_t sheet, int tpr, int64_t per, float *__restrict__ parts) {
+  __shared__ float sm[256 * VEC];
+  const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = 256 / tpr;
+  const int64_t c = (blockIdx.x * (int64_t)tpr + t) * VEC;
   const int64_t r0 = blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
-  float s = 0.f;
+  float s[VEC] = {};
   if (c < cols)
-    for (int64_t r = r0 + wy; r < r1; r += 8) {
-      float v = 0.f;
+#pragma unroll 4
+    for (int64_t r = r0 + group; r < r1; r += groups) {
 #pragma unroll
-      for (int q = S - 1; q >= 0; --q) v += to_f32(a[q * sheet + r * lda + c]);
-      s += v;
+      for (int q = S - 1; q >= 0; --q) {
+        float v[VEC];
+        load_f32<E, VEC>(a + q * sheet + r * lda + c, v);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) s[k] += v[k];
+      }
     }
-  sm[wy][lane] = s;
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) sm[threadIdx.x * VEC + k] = s[k];
   __syncthreads();
-  if (wy == 0 && c < cols) {
-    float t = 0.f;
-    for (int i = 0; i < 8; ++i) t += sm[i][lane];
-    parts[blockIdx.y * cols + c] = t;
+  for (int i = threadIdx.x; i < tpr * VEC; i += 256) {
+    const int64_t col = blockIdx.x * (int64_t)tpr * VEC + i;
+    float sum = 0.f;
+    for (int g = 0; g < groups; ++g) sum += sm[g * tpr * VEC + i];
+    if (col < cols) parts[blockIdx.y * cols + col] = sum;
   }
 }
 
+// Sums of the parts, in order; column c of half h of `pitch` columns goes to out[h * n + c].
 template <typename T>
-__global__ void __launch_bounds__(256) add_parts(int nparts, int64_t cols, const float *__restrict__ parts,
-                                                 T *__restrict__ out) {
-  const int64_t c = blockIdx.x * 256ll + threadIdx.x;
-  if (c >= cols) return;
+__global__ void __launch_bounds__(256) add_parts(int nparts, int64_t cols, int64_t pitch, int64_t n,
+                                                 const float *__restrict__ parts, T *__restrict__ out) {
+  __shared__ float sm[8][33];
+  const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
+  const int64_t c = blockIdx.x * 32ll + lane;
   float s = 0.f;
-  for (int p = 0; p < nparts; ++p) s += parts[p * cols + c];
-  out[c] = from_f32<T>(s);
+  if (c < cols)
+#pragma unroll 8
+    for (int p = wy; p < nparts; p += 8) s += parts[p * cols + c];
+  sm[wy][lane] = s;
+  __syncthreads();
+  const int64_t half = c / pitch, i = c - half * pitch;
+  if (wy == 0 && c < cols && i < n) {
+    float t = 0.f;
+    for (int k = 0; k < 8; ++k) t += sm[k][lane];
+    out[half * n + i] = from_f32<T>(t);
+  }
 }
 
+// out = column sums of [rows][cols] (in halves of `pitch` columns, the first n of each wanted).
 template <typename E, int S, typename T>
-void column_sums(Call &c, int64_t rows, int64_t cols, const E *a, int64_t lda, int64_t sheet, T *out, float *parts) {
-  const int64_t per = std::max<int64_t>(kSumRows, (rows + kSumParts - 1) / kSumParts);
-  const int n = (int)((rows + per - 1) / per);
-  column_parts<E, S><<<dim3((unsigned)((cols + 31) / 32), n), 256, 0, c.st>>>(rows, cols, a, lda, sheet, per, parts);
-  add_parts<T><<<(unsigned)((cols + 255) / 256), 256, 0, c.st>>>(n, cols, parts, out);
+void column_sums(Call &c, int64_t rows, int64_t cols, const E *a, int64_t lda, int64_t sheet, int64_t pitch, int64_t n,
+                 T *out, float *parts) {
+  constexpr int V = 16 / sizeof(E);
+  const bool vec = aligned(a, 16) && lda % V == 0 && cols % V == 0 && sheet % V == 0;
+  const int64_t chunks = vec ? cols / V : cols;
+  int tpr = 1;
+  while (tpr < 32 && tpr < chunks) tpr <<= 1;
+  const int64_t tiles = (chunks + tpr - 1) / tpr;
+  // enough blocks to fill the GPU, each with at least eight turns of its threads
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kSumParts, 152 * 8 / tiles));
+  const int64_t per = std::max<int64_t>(8 * (256 / tpr), (rows + most - 1) / most);
+  const int nparts = (int)((rows + per - 1) / per);
+  const dim3 grid((unsigned)tiles, nparts);
+  if (vec)
+    column_parts<E, S, V><<<grid, 256, 0, c.st>>>(rows, cols, a, lda, sheet, tpr, per, parts);
+  else
+    column_parts<E, S, 1><<<grid, 256, 0, c.st>>>(rows, cols, a, lda, sheet, tpr, per, parts);
+  add_parts<T><<<(unsigned)((cols + 31) / 32), 256, 0, c.st>>>(nparts, cols, pitch, n, parts, out);
   c.launched(cudaGetLastError());
   c.launched(cudaSuccess);
 }
@@ -419,7 +450,7 @@ ForwardScratch forward_scratch(const sla_ffn *f, char *base) {
 
 struct BackwardScratch {
   void *dy, *x, *w_in, *w_out, *dgu;
-  float *parts;
+  float *sums, *parts;
   size_t total;
 };
 
@@ -432,7 +463,8 @@ BackwardScratch backward_scratch(const sla_ffn *f, char *base) {
   w.w_in = a.take(packed_bytes(2 * f->hidden, f->width, f->dtype));
   w.w_out = a.take(packed_bytes(f->out, f->hidden, f->dtype));
   w.dgu = a.take((size_t)f->tokens * (size_t)hidden_pitch(f) * 2 * 2 * S);
-  size_t parts = kSumParts * sizeof(float) * (size_t)std::max(f->hidden, f->out);
+  w.sums = (float *)a.take((size_t)((f->tokens + 31) / 32) * 2 * (size_t)hidden_pitch(f) * sizeof(float));
+  size_t parts = kSumParts * sizeof(float) * (size_t)std::max(2 * hidden_pitch(f), f->out);
   for (const ProductSize &s : {dh_size(f), dx_size(f), dw_in_size(f), dw_out_size(f)})
     parts = std::max(parts, plan_product(s, S, false).partial_bytes);
   w.parts = (float *)a.take(parts);
@@ -466,13 +498,13 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
   const Operand oi = as_operand(c, w_in, f->hidden, f->width, f->width, 2, w.w_in);
   const Operand oo = as_operand(c, w_out, f->out, f->hidden, f->hidden, 1, w.w_out);
   ProductArgs p{};
-  p.act = f->activation, p.bias = b_in, p.vec = 1;
+  p.act = f->activation, p.bias = b_in, p.bias_vec = aligned(b_in, 32) && f->hidden % 16 == 0, p.vec = 1;
   p.g = saved, p.u = saved ? saved + L.u : nullptr;
   p.h = (uint16_t *)h, p.ldg = ldg, p.sheet = f->tokens * ldg;
   run_product<T>(c, kGate, gate_size(f), ox, false, oi, false, p, w.parts);
   const Operand oh{h, f->hidden, f->tokens, sheets_of<T>(), ldg, f->tokens * ldg};
   ProductArgs q{};
-  q.bias = b_out, q.c = y, q.ldc = f->out, q.vec = vec_out(y, f->out);
+  q.bias = b_out, q.bias_vec = aligned(b_out, 32), q.c = y, q.ldc = f->out, q.vec = vec_out(y, f->out);
   run_product<T>(c, kStore, out_size(f), oh, false, oo, false, q, w.parts);
   return finish(c);
 }
@@ -500,7 +532,15 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
     p.act = f->activation, p.vec = 1;
     p.g = (void *)saved, p.u = (void *)(saved + L.u);
     p.h = (uint16_t *)w.dgu, p.ldg = ldg, p.sheet = sheet;
+    // the epilogue sums dg and du over 32 rows on its way, unless the product is split
+    if (db_in && plan_product(dh_size(f), S, false).splits == 1) p.sums = w.sums;
     run_product<T>(c, kGateBack, dh_size(f), ody, false, oo, true, p, w.parts);
+    if (p.sums)
+      column_sums<float, 1>(c, (f->tokens + 31) / 32, 2 * ldg, p.sums, 2 * ldg, 0, ldg, f->hidden, db_in, w.parts);
+    else if (db_in)
+      for (int half = 0; half < 2; ++half)
+        column_sums<E, S>(c, f->tokens, f->hidden, (const E *)w.dgu + half * sheet, ldg, 2 * sheet, f->hidden,
+                          f->hidden, db_in + half * f->hidden, w.parts);
   }
   auto store = [&](const ProductSize &s, const Operand &a, bool a_mn, const Operand &b, T *out) {
     ProductArgs p{};
@@ -516,11 +556,7 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
     store(dw_in_size(f), odgu, true, ox, dw_in);
   }
   if (dw_out) store(dw_out_size(f), ody, true, oh, dw_out);
-  if (db_in)
-    for (int half = 0; half < 2; ++half)
-      column_sums<E, S>(c, f->tokens, f->hidden, (const E *)w.dgu + half * sheet, ldg, 2 * sheet,
-                        db_in + half * f->hidden, w.parts);
-  if (db_out) column_sums<T, 1>(c, f->tokens, f->out, dy, lddy, 0, db_out, w.parts);
+  if (db_out) column_sums<T, 1>(c, f->tokens, f->out, dy, lddy, 0, f->out, f->out, db_out, w.parts);
   return finish(c);
 }
 

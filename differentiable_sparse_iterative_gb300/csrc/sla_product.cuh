@@ -52,9 +52,11 @@ struct ProductArgs {
   void *c;                   // kStore: T, kPartial: float [splits][..]
   int64_t ldc, c_m_half, c_n_half, c_split;
   const void *bias;          // T, [n] (kStore) or [2 n] (kGate), or NULL
+  int bias_vec;              // its 16 values at any multiple of 16 columns are aligned to 32 bytes
   void *g, *u;               // T [m][ldg]: written by kGate (NULL: not kept), read by kGateBack
   uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
   int64_t ldg, sheet;        // elements between rows and between sheets of h
+  float *sums;               // kGateBack: [m / 32][2][ldg] sums of dg and du over 32 rows, or NULL
   uint32_t *timeouts;
 };
 
@@ -209,10 +211,30 @@ __device__ __forceinline__ void load_row(const T *p, float (&v)[N], int count, b
 }
 
 template <typename T, int N>
-__device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count) {
+__device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count, bool vec) {
+  float b[N];
+  load_row<T, N>(bias, b, count, vec);
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i < count) v[i] += to_f32(bias[i]);
+  for (int i = 0; i < N; ++i) v[i] += b[i];
+}
+
+// Column sums of a 32 x 32 tile, thread = row, v = its columns: lane c gets column c's sum.  Each step
+// trades half of the columns with the lane that has the other half: 31 shuffles in all.
+__device__ __forceinline__ float sum_columns(const float (&v)[32], int lane) {
+  float w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float give = lane & 16 ? v[i] : v[i + 16], keep = lane & 16 ? v[i + 16] : v[i];
+    w[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float give = lane & o ? w[i] : w[i + o], keep = lane & o ? w[i + o] : w[i];
+      w[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  return w[0];
 }
 
 // The tile (of all halves) and split of a work item.
@@ -405,8 +427,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           tmem_wait(u);
           if (live && count > 0) {
             if (p.bias) {
-              add_bias<T, N>(v, (const T *)p.bias + col, count);
-              add_bias<T, N>(u, (const T *)p.bias + p.n + col, count);
+              add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
+              add_bias<T, N>(u, (const T *)p.bias + p.n + col, count, p.bias_vec);
             }
             const int64_t o = row * p.ldg + col;
             if (p.g) {
@@ -425,6 +447,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (live && count > 0) {
             load_row<T, N>((const T *)p.g + o, g, count, p.vec);
             load_row<T, N>((const T *)p.u + o, u, count, p.vec);
+          } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] = u[i] = 0.f;
           }
           tmem_wait(v);
           if (live && count > 0) {
@@ -440,6 +465,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             store_operand<T, N>(p.h + o, 2 * p.sheet, g, count, p.vec);
             store_operand<T, N>(p.h + p.sheet + o, 2 * p.sheet, u, count, p.vec);
           }
+          if (p.sums && row - lane < p.m) {
+            const float sg = sum_columns(g, lane), su = sum_columns(u, lane);
+            if (lane < count) {
+              float *to = p.sums + (int64_t)(row >> 5) * 2 * p.ldg + col + lane;
+              to[0] = sg;
+              to[p.ldg] = su;
+            }
+          }
         } else {
           tmem_wait(v);
           if (live && count > 0) {
@@ -447,7 +480,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             if constexpr (EPI == kPartial) {
               store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, p.vec);
             } else {
-              if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count);
+              if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
               store_row<T, N>((T *)p.c + o, v, count, p.vec);
             }
           }
