@@ -34,8 +34,6 @@ enum Epilogue {
 constexpr int kDepth = 64;      // k of a stage: 128 bytes, the swizzle's width
 constexpr int kBand = 8;
 constexpr int kMaxSegments = 12;
-constexpr int kEpilogueWarps = 8;
-constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
 
 struct ProductArgs {
   int m, n;                  // rows and columns of one half of C
@@ -59,6 +57,11 @@ struct ProductArgs {
   float *sums;               // kGateBack: [m / 32][2][ldg] sums of dg and du over 32 rows, or NULL
   uint32_t *timeouts;
 };
+
+// Warps that empty the accumulators: each waits on tensor memory and on global memory in turn, so the
+// widest tiles, whose epilogue would else outlast their products, take sixteen.
+template <int BN>
+inline constexpr int kEpilogueWarps = BN == 256 ? 16 : 8;
 
 // Tile shapes: CG blocks of 128 rows, BN columns, stages that fill the shared memory of a multiprocessor.
 template <int CG, int BN>
@@ -218,24 +221,53 @@ __device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count
   for (int i = 0; i < N; ++i) v[i] += b[i];
 }
 
-// Column sums of a 32 x 32 tile, thread = row, v = its columns: lane c gets column c's sum.  Each step
-// trades half of the columns with the lane that has the other half: 31 shuffles in all.
-__device__ __forceinline__ float sum_columns(const float (&v)[32], int lane) {
-  float w[16];
+// Column sums of a tile of 32 rows (thread = row) and N = 16 or 32 columns: lane c gets column c's (N =
+// 16: column c % 16's) sum.  Each step trades half of the columns with the lane that has the other half.
+template <int N>
+__device__ __forceinline__ float sum_columns(const float (&v)[N], int lane) {
+  float w[N];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float give = lane & 16 ? v[i] : v[i + 16], keep = lane & 16 ? v[i + 16] : v[i];
-    w[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
-  }
+  for (int i = 0; i < N; ++i) w[i] = v[i];
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1)
+  for (int o = N / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const float give = lane & o ? w[i] : w[i + o], keep = lane & o ? w[i + o] : w[i];
       w[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
-  return w[0];
+  return N == 16 ? w[0] + __shfl_xor_sync(0xffffffffu, w[0], 16) : w[0];
 }
+
+// N values of a row as loaded, so that they can be asked for long before they are used.
+template <typename T, int N>
+struct RawRow {
+  static constexpr int n = N * sizeof(T) / 32;
+  Sector s[n];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) s[i] = load_sector(p + i * (32 / sizeof(T)));
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[i].w[k] = 0;
+  }
+  __device__ __forceinline__ void values(float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (sizeof(T) == 4) {
+          v[8 * i + k] = __uint_as_float(s[i].w[k]);
+        } else {
+          const float2 f = unpair16(s[i].w[k], T{});
+          v[16 * i + 2 * k] = f.x;
+          v[16 * i + 2 * k + 1] = f.y;
+        }
+      }
+  }
+};
 
 // The tile (of all halves) and split of a work item.
 struct Tile {
@@ -265,7 +297,7 @@ __device__ __forceinline__ void split_range(const ProductArgs &p, int split, int
 }
 
 template <typename T, int EPI, int CG, int BN>
-__global__ void __launch_bounds__(kProductThreads, 1)
+__global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
     product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                    const __grid_constant__ ProductArgs p) {
   using Shape = ProductShape<CG, BN>;
@@ -290,7 +322,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, kEpilogueWarps * CG);
+      mbar_init(acc_empty + i, kEpilogueWarps<BN> * CG);
     }
     mbar_init(drained, 1);
     *dead = 0;
@@ -393,22 +425,45 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
   } else if (warp >= 2) {
     const int quarter = warp & 3, side = (warp - 2) >> 2;
-    // columns at a time (g and u together, and float32's three sheets, need the registers of two)
-    constexpr int N = EPI == kGate && (BN == 64 || sizeof(T) == 4) ? 16 : 32;
+    // columns of this warp, N at a time (as many as the registers hold: 112 a thread with sixteen warps)
+    constexpr int width = (EPI == kGate ? BN / 2 : BN) / (kEpilogueWarps<BN> / 4);
+    constexpr int N = BN == 256 || width == 16 || (EPI == kGate && sizeof(T) == 4) ? 16 : 32;
     constexpr bool fast = sizeof(T) == 2;
     uint32_t tile = 0;
     for (int item = worker; item < items; item += workers, ++tile) {
       const Tile t = tile_of<EPI, CG, BN>(p, item);
       const uint32_t acc = tile & 1;
+      const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
+      const bool live = row < p.m;
+      // kGateBack: g and u of the next columns are on their way while these are worked on, and those of
+      // the first while the product runs (rows are padded to whole sectors of 16 columns)
+      RawRow<T, N> raw_g, raw_u;
+      auto ask = [&](int c) {
+        const int64_t o = row * p.ldg + t.n0 + c;
+        if (live && t.n0 + c + N <= p.ldg) {
+          raw_g.load((const T *)p.g + o);
+          raw_u.load((const T *)p.u + o);
+        } else {
+          raw_g.clear();
+          raw_u.clear();
+          if (N == 32 && live && t.n0 + c < p.ldg) {  // half of the columns are there
+            RawRow<T, 16> half;
+            half.load((const T *)p.g + o);
+#pragma unroll
+            for (int i = 0; i < half.n; ++i) raw_g.s[i] = half.s[i];
+            half.load((const T *)p.u + o);
+#pragma unroll
+            for (int i = 0; i < half.n; ++i) raw_u.s[i] = half.s[i];
+          }
+        }
+      };
+      if constexpr (EPI == kGateBack) ask(side * width);
       if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
         *dead = 1;
         break;
       }
       tc_fence_after();
       const uint32_t base = tmem + acc * BN + ((uint32_t)quarter << 21);
-      const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
-      const bool live = row < p.m;
-      constexpr int width = EPI == kGate ? BN / 4 : BN / 2;  // columns of this warp
 #pragma unroll 1
       for (int c = side * width; c < (side + 1) * width; c += N) {
         const int col = t.n0 + c, count = p.n - col;
@@ -444,13 +499,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         } else if constexpr (EPI == kGateBack) {
           float g[N], u[N];
           const int64_t o = row * p.ldg + col;
-          if (live && count > 0) {
-            load_row<T, N>((const T *)p.g + o, g, count, p.vec);
-            load_row<T, N>((const T *)p.u + o, u, count, p.vec);
-          } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) g[i] = u[i] = 0.f;
-          }
+          raw_g.values(g);
+          raw_u.values(u);
+          if (c + N < (side + 1) * width) ask(c + N);
           tmem_wait(v);
           if (live && count > 0) {
             with_activation(p.act, [&](auto act) {
@@ -467,7 +518,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
           if (p.sums && row - lane < p.m) {
             const float sg = sum_columns(g, lane), su = sum_columns(u, lane);
-            if (lane < count) {
+            if (lane < N && lane < count) {
               float *to = p.sums + (int64_t)(row >> 5) * 2 * p.ldg + col + lane;
               to[0] = sg;
               to[p.ldg] = su;
@@ -527,7 +578,7 @@ cudaError_t launch_product_as(int blocks, const CUtensorMap &a, const CUtensorMa
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kProductThreads);
+  cfg.blockDim = dim3(64 + 32 * kEpilogueWarps<BN>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
