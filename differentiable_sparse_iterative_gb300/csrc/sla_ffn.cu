@@ -498,7 +498,7 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
   const Operand oi = as_operand(c, w_in, f->hidden, f->width, f->width, 2, w.w_in);
   const Operand oo = as_operand(c, w_out, f->out, f->hidden, f->hidden, 1, w.w_out);
   ProductArgs p{};
-  p.act = f->activation, p.bias = b_in, p.bias_vec = aligned(b_in, 32) && f->hidden % 16 == 0, p.vec = 1;
+  p.act = f->activation, p.bias = b_in, p.bias_vec = b_in && aligned(b_in, 32) && f->hidden % 16 == 0, p.vec = 1;
   p.g = saved, p.u = saved ? saved + L.u : nullptr;
   p.h = (uint16_t *)h, p.ldg = ldg, p.sheet = f->tokens * ldg;
   run_product<T>(c, kGate, gate_size(f), ox, false, oi, false, p, w.parts);

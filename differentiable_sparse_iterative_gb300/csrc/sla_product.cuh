@@ -50,7 +50,7 @@ struct ProductArgs {
   void *c;                   // kStore: T, kPartial: float [splits][..]
   int64_t ldc, c_m_half, c_n_half, c_split;
   const void *bias;          // T, [n] (kStore) or [2 n] (kGate), or NULL
-  int bias_vec;              // its 16 values at any multiple of 16 columns are aligned to 32 bytes
+  int bias_vec;              // there is one, and its values from any multiple of 16 columns are aligned to 32 bytes
   void *g, *u;               // T [m][ldg]: written by kGate (NULL: not kept), read by kGateBack
   uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
   int64_t ldg, sheet;        // elements between rows and between sheets of h
@@ -435,10 +435,18 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
       const uint32_t acc = tile & 1;
       const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
       const bool live = row < p.m;
-      // kGateBack: g and u of the next columns are on their way while these are worked on, and those of
-      // the first while the product runs (rows are padded to whole sectors of 16 columns)
+      // What the next columns need from memory is on its way while these are worked on, and the first
+      // columns' while the product runs.  kGateBack: g and u (rows are padded to whole sectors of 16
+      // columns); kGate: the biases.
       RawRow<T, N> raw_g, raw_u;
       auto ask = [&](int c) {
+        if (EPI == kGate) {
+          if (p.bias_vec && t.n0 + c + N <= p.n) {
+            raw_g.load((const T *)p.bias + t.n0 + c);
+            raw_u.load((const T *)p.bias + p.n + t.n0 + c);
+          }
+          return;
+        }
         const int64_t o = row * p.ldg + t.n0 + c;
         if (live && t.n0 + c + N <= p.ldg) {
           raw_g.load((const T *)p.g + o);
@@ -457,13 +465,23 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
           }
         }
       };
-      if constexpr (EPI == kGateBack) ask(side * width);
+      if constexpr (EPI == kGateBack || EPI == kGate) ask(side * width);
       if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
         *dead = 1;
         break;
       }
       tc_fence_after();
       const uint32_t base = tmem + acc * BN + ((uint32_t)quarter << 21);
+      auto release = [&] {  // this warp has read its part of the accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            mbar_arrive_rank(acc_empty + acc, 0);
+          else
+            mbar_arrive(acc_empty + acc);
+        }
+      };
 #pragma unroll 1
       for (int c = side * width; c < (side + 1) * width; c += N) {
         const int col = t.n0 + c, count = p.n - col;
@@ -478,12 +496,20 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
             tmem_load32(base + BN / 2 + c, u);
           else
             tmem_load16(base + BN / 2 + c, u);
+          float bg[N], bu[N];
+          raw_g.values(bg);
+          raw_u.values(bu);
+          if (c + N < (side + 1) * width) ask(c + N);
           tmem_wait(v);
           tmem_wait(u);
+          if (c + N >= (side + 1) * width) release();
           if (live && count > 0) {
-            if (p.bias) {
-              add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
-              add_bias<T, N>(u, (const T *)p.bias + p.n + col, count, p.bias_vec);
+            if (p.bias_vec && count >= N) {
+#pragma unroll
+              for (int i = 0; i < N; ++i) v[i] += bg[i], u[i] += bu[i];
+            } else if (p.bias) {
+              add_bias<T, N>(v, (const T *)p.bias + col, count, false);
+              add_bias<T, N>(u, (const T *)p.bias + p.n + col, count, false);
             }
             const int64_t o = row * p.ldg + col;
             if (p.g) {
@@ -503,6 +529,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
           raw_u.values(u);
           if (c + N < (side + 1) * width) ask(c + N);
           tmem_wait(v);
+          if (c + N >= (side + 1) * width) release();
           if (live && count > 0) {
             with_activation(p.act, [&](auto act) {
 #pragma unroll
@@ -526,6 +553,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
           }
         } else {
           tmem_wait(v);
+          if (c + N >= (side + 1) * width) release();
           if (live && count > 0) {
             const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
             if constexpr (EPI == kPartial) {
@@ -536,14 +564,6 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
             }
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 2)
-          mbar_arrive_rank(acc_empty + acc, 0);
-        else
-          mbar_arrive(acc_empty + acc);
       }
     }
   }

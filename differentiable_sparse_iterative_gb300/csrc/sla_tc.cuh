@@ -25,12 +25,14 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Arrival on the barrier at the same place in the shared memory of block `rank` of the cluster.
+// Arrival on the barrier at the same place in the shared memory of block `rank` of the cluster.  Relaxed:
+// it publishes no memory (a release at cluster scope would wait for the thread's stores to global
+// memory); what it follows, loads from tensor memory, tcgen05.wait has completed.
 __device__ __forceinline__ void mbar_arrive_rank(uint64_t *bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 r;\n\t"
       "mapa.shared::cluster.u32 r, %0, %1;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar)),
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
 }
