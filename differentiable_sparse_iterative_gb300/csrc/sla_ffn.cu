@@ -170,7 +170,7 @@ ProductPlan plan_product(const ProductSize &s, int sheets, bool gate) {
   const int pairs = sheets == 3 ? 6 : 1;
   const int deepest = sheets == 3 ? std::max(1, kFloatBlocks / s.k_halves) : kb;
   const int sms = sm_count();
-  const double block_us[kProductTileCount] = {0.29, 0.33, 0.18, 0.11};
+  const double block_us[kProductTileCount] = {0.29, 0.16, 0.18, 0.11};
   ProductPlan best{0, 1, 0};
   double best_us = 1e30;
   for (int i = 0; i < kProductTileCount; ++i) {

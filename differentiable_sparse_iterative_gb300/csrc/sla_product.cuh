@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
 struct ProductTile {
   int cg, bn;
 };
-constexpr ProductTile kProductTiles[] = {{2, 256}, {1, 256}, {1, 128}, {1, 64}};
+constexpr ProductTile kProductTiles[] = {{2, 256}, {2, 128}, {1, 128}, {1, 64}};
 constexpr int kProductTileCount = 4;
 
 // Launches `epi` with tile shape kProductTiles[shape] on `blocks` blocks.
@@ -615,7 +615,7 @@ cudaError_t launch_product_shape(int shape, int blocks, const CUtensorMap &a, co
                                  const ProductArgs &p, cudaStream_t st) {
   switch (shape) {
     case 0: return launch_product_as<T, EPI, 2, 256>(blocks, a, b, p, st);
-    case 1: return launch_product_as<T, EPI, 1, 256>(blocks, a, b, p, st);
+    case 1: return launch_product_as<T, EPI, 2, 128>(blocks, a, b, p, st);
     case 2: return launch_product_as<T, EPI, 1, 128>(blocks, a, b, p, st);
     default: return launch_product_as<T, EPI, 1, 64>(blocks, a, b, p, st);
   }
