@@ -11,7 +11,7 @@
 // registers in a second sweep: the one-sweep form mean(x^2) - mu^2 cancels when a row sits far
 // from zero.  VEC is 16 bytes of elements; rows that cannot be read that way (width, stride or
 // address) take VEC = 1, still coalesced over the threads.  Rows wider than the registers of a
-// 1024-thread block hold (kMaxItems) are re-read from L2 by the *_wide kernels.
+// 512-thread block hold (16,384 16-bit elements) are re-read from L2 by the *_wide kernels.
 //
 // Backward: a thread sees the same columns in every row of its group, so dw and db accumulate in
 // its registers over the block's rows (persistent blocks, rows in strides of the grid), then
@@ -43,8 +43,9 @@ int sm_count() {
 
 namespace {
 
-constexpr int kLnBlock = 256;     // threads of a block while a row fits a warp
-constexpr int kMaxThreads = 1024; // threads of a block that shares one row
+constexpr int kLnBlock = 256;     // threads of a block while a row takes no more
+constexpr int kMaxThreads = 512;  // threads of a block that shares one row
+constexpr int kInFlight = 4;      // vectors of a thread on their way at a time: rows are taken in bundles
 constexpr int kColTile = 32;      // columns of a block of the column sums
 constexpr int kMaxParts = 1216;   // blocks that leave partial column sums (8 a multiprocessor)
 
@@ -62,61 +63,93 @@ __device__ __forceinline__ float group_sum(float v, int tpr, float *slot) {
   return s;
 }
 
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Pack<T, N> &q, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = to_f32(q.v[i]);
+}
+
+// Rows of a bundle: as many as keep kInFlight vectors of a thread in flight.
+template <int NI>
+inline constexpr int kBundle = NI >= kInFlight ? 1 : kInFlight / NI;
+
 template <typename T, typename P, int VEC, int NI>
 __global__ void __launch_bounds__(kMaxThreads) ln_forward(int64_t rows, int width, int tpr, const T *__restrict__ x,
                                                           int64_t ldx, const P *__restrict__ w,
                                                           const P *__restrict__ b, float eps, T *__restrict__ y,
                                                           float *__restrict__ mean, float *__restrict__ rstd) {
-  __shared__ float slots[2][32];
-  const int t = threadIdx.x & (tpr - 1);
-  const int64_t row = blockIdx.x * (int64_t)(blockDim.x / tpr) + threadIdx.x / tpr;
-  const bool live = row < rows;
-  float v[NI][VEC];
-  float s = 0.f;
+  constexpr int R = kBundle<NI>;
+  __shared__ float slots[2 * R][32];
+  const int t = threadIdx.x & (tpr - 1), groups = blockDim.x / tpr;
+  const int64_t row0 = blockIdx.x * (int64_t)groups * R + threadIdx.x / tpr;
+  Pack<T, VEC> raw[R][NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int c = (i * tpr + t) * VEC;
-    if (live && c < width) {
-      load_f32<T, VEC>(x + row * ldx + c, v[i]);
-    } else {
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = row0 + r * groups;
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) v[i][k] = 0.f;
+    for (int i = 0; i < NI; ++i) {
+      const int c = (i * tpr + t) * VEC;
+      if (row < rows && c < width) {
+        raw[r][i] = *reinterpret_cast<const Pack<T, VEC> *>(x + row * ldx + c);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) raw[r][i].v[k] = from_f32<T>(0.f);
+      }
     }
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) s += v[i][k];
   }
   const float inv = 1.f / (float)width;
-  const float mu = group_sum(s, tpr, slots[0]) * inv;
-  float q = 0.f;
+  float mu[R], rs[R];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const bool in = (i * tpr + t) * VEC < width;
+  for (int r = 0; r < R; ++r) {
+    float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const float d = v[i][k] - mu;
-      q += in ? d * d : 0.f;
+    for (int i = 0; i < NI; ++i) {
+      float v[VEC];
+      unpack(raw[r][i], v);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s += v[k];
     }
+    mu[r] = group_sum(s, tpr, slots[r]) * inv;
   }
-  const float rs = 1.f / sqrtf(group_sum(q, tpr, slots[1]) * inv + eps);
-  if (!live) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const bool in = (i * tpr + t) * VEC < width;
+      float v[VEC];
+      unpack(raw[r][i], v);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) q += in ? (v[k] - mu[r]) * (v[k] - mu[r]) : 0.f;
+    }
+    rs[r] = 1.f / sqrtf(group_sum(q, tpr, slots[R + r]) * inv + eps);
+  }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int c = (i * tpr + t) * VEC;
     if (c >= width) break;
-    float out[VEC], wv[VEC], bv[VEC];
+    float wv[VEC], bv[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) wv[k] = 1.f, bv[k] = 0.f;
     if (w) load_f32<P, VEC>(w + c, wv);
     if (b) load_f32<P, VEC>(b + c, bv);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const float xh = (v[i][k] - mu) * rs;
-      out[k] = (w ? xh * wv[k] : xh) + (b ? bv[k] : 0.f);
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = row0 + r * groups;
+      if (row >= rows) break;
+      float v[VEC];
+      unpack(raw[r][i], v);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) v[k] = (v[k] - mu[r]) * rs[r] * wv[k] + bv[k];
+      store_f32<T, VEC>(y + row * width + c, v);
     }
-    store_f32<T, VEC>(y + row * width + c, out);
   }
-  if (t == 0) {
-    if (mean) mean[row] = mu;
-    if (rstd) rstd[row] = rs;
-  }
+  if (t == 0 && mean)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = row0 + r * groups;
+      if (row < rows) mean[row] = mu[r], rstd[row] = rs[r];
+    }
 }
 
 // Rows of any width, one block a row, three sweeps (the second and third hit L2).
@@ -156,67 +189,89 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward(int64_t rows, int wid
                                                            const P *__restrict__ w, const float *__restrict__ mean,
                                                            const float *__restrict__ rstd, T *__restrict__ dx,
                                                            float *__restrict__ parts) {
-  extern __shared__ float cols[];  // tpr <= 32: [2][width]
-  __shared__ float slots[2][2][32];
+  constexpr int R = kBundle<2 * NI>;  // two vectors, of x and of dy, for each of the forward pass's
+  extern __shared__ float cols[];     // more than one group: [2][width]
+  __shared__ float slots[2][2 * R][32];
   const int t = threadIdx.x & (tpr - 1), groups = blockDim.x / tpr;
-  const int64_t step = (int64_t)gridDim.x * groups;
+  const int64_t step = (int64_t)gridDim.x * groups * R;
   const float inv = 1.f / (float)width;
   float aw[NI][VEC], ab[NI][VEC];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) aw[i][k] = ab[i][k] = 0.f;
-  int turn = 0;  // the slots alternate, so a row's sums never meet the previous row's reads
+  int turn = 0;  // the slots alternate, so a bundle's sums never meet the previous one's reads
   // every thread of a block makes the same number of turns (the sums need whole warps and blocks)
-  for (int64_t base = blockIdx.x * (int64_t)groups; base < rows; base += step, turn ^= 1) {
-    const int64_t row = base + threadIdx.x / tpr;
-    const bool live = row < rows;
-    const float mu = live ? mean[row] : 0.f, rs = live ? rstd[row] : 0.f;
-    float xh[NI][VEC], g[NI][VEC];
-    float s1 = 0.f, s2 = 0.f;
+  for (int64_t base = blockIdx.x * (int64_t)groups * R; base < rows; base += step, turn ^= 1) {
+    Pack<T, VEC> rx[R][NI], rg[R][NI];
+    float mu[R], rs[R], m1[R], m2[R];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int c = (i * tpr + t) * VEC;
-      if (live && c < width) {
-        load_f32<T, VEC>(x + row * ldx + c, xh[i]);
-        load_f32<T, VEC>(dy + row * lddy + c, g[i]);
-      } else {
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = base + r * groups + threadIdx.x / tpr;
+      const bool live = row < rows;
+      mu[r] = live ? mean[row] : 0.f;
+      rs[r] = live ? rstd[row] : 0.f;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) xh[i][k] = mu, g[i][k] = 0.f;
+      for (int i = 0; i < NI; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        if (live && c < width) {
+          rx[r][i] = *reinterpret_cast<const Pack<T, VEC> *>(x + row * ldx + c);
+          rg[r][i] = *reinterpret_cast<const Pack<T, VEC> *>(dy + row * lddy + c);
+        } else {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) rx[r][i].v[k] = rg[r][i].v[k] = from_f32<T>(0.f);
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int c = (i * tpr + t) * VEC;
-      float wv[VEC];
-      if (w && c < width) load_f32<P, VEC>(w + c, wv);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        xh[i][k] = (xh[i][k] - mu) * rs;
-        aw[i][k] += g[i][k] * xh[i][k];
-        ab[i][k] += g[i][k];
-        if (w && c < width) g[i][k] *= wv[k];
-        s1 += g[i][k];
-        s2 += g[i][k] * xh[i][k];
-      }
-    }
-    const float m1 = group_sum(s1, tpr, slots[turn][0]) * inv;
-    const float m2 = group_sum(s2, tpr, slots[turn][1]) * inv;
-    if (live && dx) {
+    for (int r = 0; r < R; ++r) {
+      float s1 = 0.f, s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int c = (i * tpr + t) * VEC;
         if (c >= width) break;
-        float out[VEC];
+        float wv[VEC], xv[VEC], g[VEC];
+        unpack(rx[r][i], xv);
+        unpack(rg[r][i], g);
+        if (w) load_f32<P, VEC>(w + c, wv);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) out[k] = rs * (g[i][k] - m1 - xh[i][k] * m2);
-        store_f32<T, VEC>(dx + row * width + c, out);
+        for (int k = 0; k < VEC; ++k) {
+          const float xh = (xv[k] - mu[r]) * rs[r];
+          aw[i][k] += g[k] * xh;
+          ab[i][k] += g[k];
+          if (w) g[k] *= wv[k];
+          s1 += g[k];
+          s2 += g[k] * xh;
+        }
+      }
+      m1[r] = group_sum(s1, tpr, slots[turn][2 * r]) * inv;
+      m2[r] = group_sum(s2, tpr, slots[turn][2 * r + 1]) * inv;
+    }
+    if (!dx) continue;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = base + r * groups + threadIdx.x / tpr;
+      if (row >= rows) break;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        if (c >= width) break;
+        float wv[VEC], xv[VEC], g[VEC];
+        unpack(rx[r][i], xv);
+        unpack(rg[r][i], g);
+        if (w) load_f32<P, VEC>(w + c, wv);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          const float xh = (xv[k] - mu[r]) * rs[r];
+          g[k] = rs[r] * ((w ? g[k] * wv[k] : g[k]) - m1[r] - xh * m2[r]);
+        }
+        store_f32<T, VEC>(dx + row * width + c, g);
       }
     }
   }
   if (!parts) return;
   float *pw = parts + (int64_t)blockIdx.x * 2 * width, *pb = pw + width;
-  if (tpr >= 32 && groups == 1) {
+  if (groups == 1) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int c = (i * tpr + t) * VEC;
@@ -226,7 +281,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward(int64_t rows, int wid
     }
     return;
   }
-  // the groups of a warp by shuffles, then the warps one after another
+  // the groups of a warp by shuffles, then the groups that are left one after another
   for (int o = tpr; o < 32; o <<= 1) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
@@ -236,9 +291,9 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward(int64_t rows, int wid
         ab[i][k] += __shfl_xor_sync(0xffffffffu, ab[i][k], o);
       }
   }
-  const int warps = blockDim.x >> 5;
-  for (int turn_of = 0; turn_of < warps; ++turn_of) {
-    if ((int)(threadIdx.x >> 5) == turn_of && (int)(threadIdx.x & 31) < tpr) {
+  const int apart = tpr < 32 ? 32 : tpr;
+  for (int turn_of = 0; turn_of < (int)blockDim.x / apart; ++turn_of) {
+    if ((int)threadIdx.x / apart == turn_of && (int)threadIdx.x % apart < tpr) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int c = (i * tpr + t) * VEC;
@@ -335,24 +390,25 @@ struct LnPlan {
   int vec, items, tpr, block;  // vec = 0: the wide kernels
 };
 
-// Widest vector, then the fewest threads a row that hold it in at most four vectors (eight single elements) each.
-LnPlan ln_plan(int64_t width, int vec) {
+// Widest vector, then the fewest threads a row that hold it in `few` vectors (8 single elements) each, or
+// in four (16) where even kMaxThreads threads cannot.
+LnPlan ln_plan(int64_t width, int vec, int few) {
   const int64_t nv = (width + vec - 1) / vec;
-  const int most = vec > 1 ? 4 : 8;
+  const int most = vec > 1 ? 4 : 16;
   if (nv > (int64_t)kMaxThreads * most) return {0, 0, kMaxThreads, kMaxThreads};
+  const int enough = vec > 1 ? few : 8;
   int tpr = 1;
-  while ((int64_t)tpr * most < nv || (tpr < 32 && tpr < nv)) tpr <<= 1;
+  while (tpr < kMaxThreads && ((int64_t)tpr * enough < nv || (tpr < 32 && tpr < nv))) tpr <<= 1;
   const int need = (int)((nv + tpr - 1) / tpr);
-  const int items = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : 8;
-  return {vec, items, tpr, std::max(tpr, kLnBlock)};
+  const int items = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 16;
+  return {vec, items, tpr, tpr > 32 ? tpr : kLnBlock};
 }
 
 template <typename T, typename P, int VEC, int NI>
 void launch_forward(const LnPlan &pl, int64_t rows, int64_t width, const void *x, int64_t ldx, const void *w,
                     const void *b, float eps, void *y, float *mean, float *rstd, cudaStream_t st) {
-  const int block = pl.tpr > 32 ? pl.tpr : pl.block;
-  const int64_t rpb = block / pl.tpr;
-  ln_forward<T, P, VEC, NI><<<(unsigned)((rows + rpb - 1) / rpb), block, 0, st>>>(
+  const int64_t rpb = pl.block / pl.tpr * kBundle<NI>;
+  ln_forward<T, P, VEC, NI><<<(unsigned)((rows + rpb - 1) / rpb), pl.block, 0, st>>>(
       rows, (int)width, pl.tpr, (const T *)x, ldx, (const P *)w, (const P *)b, eps, (T *)y, mean, rstd);
 }
 
@@ -360,7 +416,7 @@ template <typename T, typename P>
 cudaError_t forward(int64_t rows, int64_t width, bool vec_ok, const void *x, int64_t ldx, const void *w,
                     const void *b, float eps, void *y, float *mean, float *rstd, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const LnPlan pl = ln_plan(width, vec_ok ? V : 1);
+  const LnPlan pl = ln_plan(width, vec_ok ? V : 1, 4);
 #define SLA_LN_FWD(VEC, NI) launch_forward<T, P, VEC, NI>(pl, rows, width, x, ldx, w, b, eps, y, mean, rstd, st)
   if (pl.vec == 0)
     ln_forward_wide<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
@@ -368,26 +424,23 @@ cudaError_t forward(int64_t rows, int64_t width, bool vec_ok, const void *x, int
   else if (pl.vec > 1)
     pl.items == 1 ? SLA_LN_FWD(V, 1) : pl.items == 2 ? SLA_LN_FWD(V, 2) : SLA_LN_FWD(V, 4);
   else
-    pl.items <= 2 ? SLA_LN_FWD(1, 2) : pl.items == 4 ? SLA_LN_FWD(1, 4) : SLA_LN_FWD(1, 8);
+    pl.items <= 2 ? SLA_LN_FWD(1, 2) : pl.items <= 8 ? SLA_LN_FWD(1, 8) : SLA_LN_FWD(1, 16);
 #undef SLA_LN_FWD
   return cudaGetLastError();
-}
-
-// Blocks of the backward pass: enough to fill the GPU, no more than there are row groups.
-int backward_grid(int64_t rows, int64_t rpb, int block) {
-  const int per_sm = std::max(1, std::min(8, 1024 / block));
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(sm_count() * per_sm, kMaxParts), (rows + rpb - 1) / rpb));
 }
 
 template <typename T, typename P, int VEC, int NI>
 int launch_backward(const LnPlan &pl, int64_t rows, int64_t width, const void *dy, int64_t lddy, const void *x,
                     int64_t ldx, const void *w, const float *mean, const float *rstd, void *dx, float *parts,
                     cudaStream_t st) {
-  const int block = pl.tpr > 32 ? pl.tpr : pl.block;
-  const int grid = backward_grid(rows, block / pl.tpr, block);
-  const size_t smem = pl.tpr <= 32 && parts ? 2 * sizeof(float) * (size_t)width : 0;
-  ln_backward<T, P, VEC, NI><<<grid, block, smem, st>>>(rows, (int)width, pl.tpr, (const T *)dy, lddy, (const T *)x,
-                                                        ldx, (const P *)w, mean, rstd, (T *)dx, parts);
+  const int groups = pl.block / pl.tpr;
+  const int64_t rpb = groups * kBundle<2 * NI>;
+  // enough blocks to fill the GPU (1024 threads a multiprocessor), no more than there are bundles
+  const int per_sm = std::max(1, 1024 / pl.block);
+  const int grid = (int)std::min<int64_t>(std::min(sm_count() * per_sm, kMaxParts), (rows + rpb - 1) / rpb);
+  const size_t smem = groups > 1 && parts ? 2 * sizeof(float) * (size_t)width : 0;
+  ln_backward<T, P, VEC, NI><<<grid, pl.block, smem, st>>>(rows, (int)width, pl.tpr, (const T *)dy, lddy,
+                                                           (const T *)x, ldx, (const P *)w, mean, rstd, (T *)dx, parts);
   return grid;
 }
 
@@ -396,7 +449,7 @@ cudaError_t backward(int64_t rows, int64_t width, bool vec_ok, const void *dy, i
                      int64_t ldx, const void *w, const float *mean, const float *rstd, void *dx, void *dw, void *db,
                      float *parts, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const LnPlan pl = ln_plan(width, vec_ok ? V : 1);
+  const LnPlan pl = ln_plan(width, vec_ok ? V : 1, 16 / V);  // 16 elements and their two sums fit the registers
   int nparts = 0;
   const int ctiles = (int)((width + kColTile - 1) / kColTile);
 #define SLA_LN_BWD(VEC, NI) \
@@ -413,7 +466,7 @@ cudaError_t backward(int64_t rows, int64_t width, bool vec_ok, const void *dy, i
   } else if (pl.vec > 1) {
     nparts = pl.items == 1 ? SLA_LN_BWD(V, 1) : pl.items == 2 ? SLA_LN_BWD(V, 2) : SLA_LN_BWD(V, 4);
   } else {
-    nparts = pl.items <= 2 ? SLA_LN_BWD(1, 2) : pl.items == 4 ? SLA_LN_BWD(1, 4) : SLA_LN_BWD(1, 8);
+    nparts = pl.items <= 2 ? SLA_LN_BWD(1, 2) : pl.items <= 8 ? SLA_LN_BWD(1, 8) : SLA_LN_BWD(1, 16);
   }
 #undef SLA_LN_BWD
   if (parts) ln_reduce_parts<P><<<dim3(ctiles, 2), 1024, 0, st>>>(nparts, width, parts, (P *)dw, (P *)db);

@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // loads: one stage is kDepth of k of the tile's rows of A and columns of B
     constexpr uint32_t bytes = CG * (Shape::a_bytes + Shape::b_bytes);
     uint32_t n = 0;
@@ -351,76 +351,87 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
         const int az = p.a_sheet[seg] + t.m_half, bz = p.b_sheet[seg] + t.n_half;
         for (int kb = k0; kb < k1; ++kb, ++n) {
           const int s = n % S;
-          if (n >= S && !mbar_wait_clocks(empty + s, ((n / S) - 1) & 1)) {
+          if (n >= S && !__all_sync(0xffffffffu, mbar_wait_clocks(empty + s, ((n / S) - 1) & 1))) {
             *dead = 1;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
-          uint8_t *da = sa + s * Shape::a_bytes, *db = sb + s * Shape::b_bytes;
-          const int k = kb * kDepth;
-          if (p.a_mn) {
-            tma_load<CG>(da, &ma, am, k, az, full + s);
-            tma_load<CG>(da + Shape::a_bytes / 2, &ma, am + 64, k, az, full + s);
-          } else {
-            tma_load<CG>(da, &ma, k, am, az, full + s);
-          }
-          if (EPI == kGate) {
-            // half of the columns are g's, half u's; in a pair of blocks each loads one of them
-            if (CG == 2) {
-              tma_load<CG>(db, &mb, k, t.n0, bz + (int)rank, full + s);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+            uint8_t *da = sa + s * Shape::a_bytes, *db = sb + s * Shape::b_bytes;
+            const int k = kb * kDepth;
+            if (p.a_mn) {
+              tma_load<CG>(da, &ma, am, k, az, full + s);
+              tma_load<CG>(da + Shape::a_bytes / 2, &ma, am + 64, k, az, full + s);
             } else {
-              tma_load<CG>(db, &mb, k, t.n0, bz, full + s);
-              tma_load<CG>(db + Shape::b_bytes / 2, &mb, k, t.n0, bz + 1, full + s);
+              tma_load<CG>(da, &ma, k, am, az, full + s);
             }
-          } else if (p.b_mn) {
+            if (EPI == kGate) {
+              // half of the columns are g's, half u's; in a pair of blocks each loads one of them
+              if (CG == 2) {
+                tma_load<CG>(db, &mb, k, t.n0, bz + (int)rank, full + s);
+              } else {
+                tma_load<CG>(db, &mb, k, t.n0, bz, full + s);
+                tma_load<CG>(db + Shape::b_bytes / 2, &mb, k, t.n0, bz + 1, full + s);
+              }
+            } else if (p.b_mn) {
 #pragma unroll
-            for (int j = 0; j < BN / CG / 64; ++j)
-              tma_load<CG>(db + j * kDepth * 128, &mb, t.n0 + (int)rank * (BN / CG) + j * 64, k, bz, full + s);
-          } else {
-            tma_load<CG>(db, &mb, k, t.n0 + (int)rank * (BN / CG), bz, full + s);
+              for (int j = 0; j < BN / CG / 64; ++j)
+                tma_load<CG>(db + j * kDepth * 128, &mb, t.n0 + (int)rank * (BN / CG) + j * 64, k, bz, full + s);
+            } else {
+              tma_load<CG>(db, &mb, k, t.n0 + (int)rank * (BN / CG), bz, full + s);
+            }
           }
+          __syncwarp();
         }
       }
     }
-    // every copy has landed before the block may end (the mma thread waited for all but after a timeout)
+    // every copy has landed before the block may end (the mma warp waited for all but after a timeout)
     if (rank == 0)
       for (uint32_t i = n > S ? n - S : 0; i < n; ++i)
         if (!mbar_wait_clocks(full + i % S, (i / S) & 1)) *dead = 1;
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     const uint32_t idesc = tc_idesc(p.f16, p.a_mn, p.b_mn, 128 * CG, BN);
     const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
+    const uint64_t a0 = tc_desc(sa, p.a_mn, Shape::a_bytes / 2), b0 = tc_desc(sb, p.b_mn, kDepth * 128);
     uint32_t n = 0, tile = 0;
     for (int item = worker; item < items && !*dead; item += workers, ++tile) {
       const Tile t = tile_of<EPI, CG, BN>(p, item);
       int k0, k1;
       split_range(p, t.split, k0, k1);
       const uint32_t acc = tile & 1, use = tile >> 1;
-      if (use > 0 && !mbar_wait_clocks(acc_empty + acc, (use - 1) & 1)) {
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_clocks(acc_empty + acc, (use - 1) & 1))) {
         *dead = 1;
         break;
       }
       tc_fence_after();
       const uint32_t d = tmem + acc * BN;
       const int steps = p.segments * (k1 - k0);
+      bool lost = false;
       for (int i = 0; i < steps; ++i, ++n) {
         const int s = n % S;
-        if (!mbar_wait_clocks(full + s, (n / S) & 1)) {
-          *dead = 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_clocks(full + s, (n / S) & 1))) {
+          lost = true;
           break;
         }
         tc_fence_after();
-        const uint64_t a = tc_desc(sa + s * Shape::a_bytes, p.a_mn, Shape::a_bytes / 2);
-        const uint64_t b = tc_desc(sb + s * Shape::b_bytes, p.b_mn, kDepth * 128);
+        const uint64_t a = a0 + s * (Shape::a_bytes >> 4), b = b0 + s * (Shape::b_bytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < kDepth / 16; ++j)
-          tc_mma<CG>(d, a + j * a_step, b + j * b_step, idesc, i > 0 || j > 0);
-        tc_commit<CG>(empty + s);
+          for (int j = 0; j < kDepth / 16; ++j)
+            tc_mma<CG>(d, a + j * a_step, b + j * b_step, idesc, i > 0 || j > 0);
+          tc_commit<CG>(empty + s);
+          if (i == steps - 1) tc_commit<CG>(acc_full + acc);
+        }
+        __syncwarp();
       }
-      if (*dead) break;
-      tc_commit<CG>(acc_full + acc);
+      if (lost) {
+        *dead = 1;
+        break;
+      }
     }
     if (*dead) {  // the mma in flight still read shared memory
-      tc_commit<CG>(drained);
+      if (elect_one()) tc_commit<CG>(drained);
+      __syncwarp();
       mbar_wait_clocks(drained, 0);
     }
   } else if (warp >= 2) {

@@ -23,34 +23,52 @@ ACTIVATIONS = {"silu": _abi.SLA_ACT_SILU, "gelu": _abi.SLA_ACT_GELU, "gelu_tanh"
 _DT = {torch.float32: _abi.SLA_F32, torch.float16: _abi.SLA_F16, torch.bfloat16: _abi.SLA_BF16}
 
 
-def _base():
-    import differentiable_sparse_iterative_gb300 as base  # lib, _check, _stream: the package imports this module
-    return base
+_library = None
+
+
+def _lib():
+    global _library
+    if _library is None:
+        import differentiable_sparse_iterative_gb300 as base  # the package imports this module
+        _library = base.lib()
+    return _library
+
+
+def _check(status: int, where: str) -> None:
+    if status != _abi.SLA_OK:
+        from . import SlaError
+        raise SlaError(status, where)
+
+
+# a call is a few microseconds of GPU time for one token: the stream's handle without a Stream object
+_stream = torch._C._cuda_getCurrentRawStream
+_empty = torch.empty
 
 
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> Tuple[int, int, int]:
     """(address, rows, elements between rows) of a tensor read as rows of its last dimension."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libsla has no CPU path)")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.dtype != like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have dtype {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if t.dim() < 1 or t.shape[-1] < 1:
+    dim = t.dim()
+    width = t.size(dim - 1) if dim else 0
+    if width < 1:
         raise ValueError(f"{name} must have a last dimension of at least one element")
-    width = t.shape[-1]
-    rows = t.numel() // width
+    rows = t.size(0) if dim == 2 else t.numel() // width
     if t.is_contiguous():
         return t.data_ptr(), rows, width
-    if t.dim() == 2 and (width == 1 or t.stride(1) == 1) and (t.stride(0) >= width or rows <= 1):
+    if dim == 2 and (width == 1 or t.stride(1) == 1) and (t.stride(0) >= width or rows <= 1):
         return t.data_ptr(), rows, t.stride(0)
     raise ValueError(f"{name} must be contiguous, or a matrix with contiguous rows that do not overlap")
 
 
-def _param(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> Optional[int]:
+def _param(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> Optional[int]:
     if t is None:
         return None
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
@@ -60,22 +78,27 @@ def _param(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> Option
 
 
 def _type(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _DT:
+    dt = _DT.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return _DT[t.dtype]
+    return dt
 
 
-def _scratch(need: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
-    if ws is not None and ws.numel() * ws.element_size() >= need:
-        return ws
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+def _scratch(need: int, device, ws: Optional[torch.Tensor]) -> Tuple[torch.Tensor, int]:
+    """(buffer, bytes): the caller's workspace where it is large enough, else a new one."""
+    if ws is not None:
+        have = ws.numel() * ws.element_size()
+        if have >= need:
+            return ws, have
+    need = max(need, 256)
+    return _empty(need, dtype=torch.uint8, device=device), need
 
 
 # --------------------------------------------------------------------------- layer norm
 
 def _ln_params(x, weight, bias):
     pt = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
-    if pt not in (x.dtype, torch.float32):
+    if pt != x.dtype and pt != torch.float32:
         raise ValueError(f"weight and bias must have dtype {x.dtype} or torch.float32, got {pt}")
     return pt
 
@@ -85,24 +108,28 @@ def sla_layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     """Layer norm over the last dimension (asynchronous).  weight and bias ([width], of x's type or
     float32) default to one and zero.  Returns y, or with stats=True (y, mean, rstd): the rows'
     float32 statistics that sla_layernorm_backward takes."""
-    base = _base()
     ptr, rows, ldx = _rows(x, "x")
-    dt, width, dev = _type(x, "x"), x.shape[-1], x.device
+    xt, dev, index, shape = x.dtype, x.device, x.get_device(), x.shape
+    dt, width = _type(x, "x"), shape[-1]
     pt = _ln_params(x, weight, bias)
+    wp = _param(weight, "weight", (width,), pt, index)
+    bp = _param(bias, "bias", (width,), pt, index)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    mean = rstd = None
+        y = _empty(shape, dtype=xt, device=dev)
+        yp = y.data_ptr()
+    else:
+        yp = _param(y, "y", shape, xt, index)
+    mean = rstd = mp = rp = None
     if stats:
-        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
-    base._check(base.lib().sla_layernorm(rows, width, dt, _DT[pt], ptr, ldx, _param(weight, "weight", (width,), pt, dev),
-                                         _param(bias, "bias", (width,), pt, dev), float(eps),
-                                         _param(y, "y", x.shape, x.dtype, dev), mean.data_ptr() if stats else None,
-                                         rstd.data_ptr() if stats else None, base._stream(dev)), "sla_layernorm")
+        mean, rstd = _empty(rows, dtype=torch.float32, device=dev), _empty(rows, dtype=torch.float32, device=dev)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    _check(_lib().sla_layernorm(rows, width, dt, _DT[pt], ptr, ldx, wp, bp, eps, yp, mp, rp, _stream(index)),
+           "sla_layernorm")
     return (y, mean, rstd) if stats else y
 
 
 def sla_layernorm_backward_workspace_bytes(rows: int, width: int, dtype: torch.dtype) -> int:
-    return _base().lib().sla_layernorm_backward_workspace_bytes(int(rows), int(width), _DT[dtype])
+    return _lib().sla_layernorm_backward_workspace_bytes(int(rows), int(width), _DT[dtype])
 
 
 def sla_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
@@ -111,28 +138,35 @@ def sla_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[t
                            workspace: Optional[torch.Tensor] = None):
     """Gradients of sla_layernorm (asynchronous): (dx, dweight, dbias), None where not wanted.
     dweight and dbias have weight's type (param_dtype, default x's, when there is no weight)."""
-    base = _base()
     ptr, rows, ldx = _rows(x, "x")
-    gptr, grows, lddy = _rows(dy, "dy", x)
-    if dy.shape != x.shape:
-        raise ValueError(f"dy must have x's shape {tuple(x.shape)}, got {tuple(dy.shape)}")
-    dt, width, dev = _type(x, "x"), x.shape[-1], x.device
-    pt = weight.dtype if weight is not None else param_dtype or x.dtype
-    if pt not in (x.dtype, torch.float32):
-        raise ValueError(f"weight must have dtype {x.dtype} or torch.float32, got {pt}")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if want_grad_x else None
-    dw = torch.empty(width, dtype=pt, device=dev) if want_grad_weight else None
-    db = torch.empty(width, dtype=pt, device=dev) if want_grad_bias else None
-    ws, nbytes = None, 0
+    gptr, _, lddy = _rows(dy, "dy", x)
+    xt, dev, index, shape = x.dtype, x.device, x.get_device(), x.shape
+    if dy.shape != shape:
+        raise ValueError(f"dy must have x's shape {tuple(shape)}, got {tuple(dy.shape)}")
+    dt, width = _type(x, "x"), shape[-1]
+    pt = weight.dtype if weight is not None else param_dtype or xt
+    if pt != xt and pt != torch.float32:
+        raise ValueError(f"weight must have dtype {xt} or torch.float32, got {pt}")
+    wp = _param(weight, "weight", (width,), pt, index)
+    mp = _param(mean, "mean", (rows,), torch.float32, index)
+    rp = _param(rstd, "rstd", (rows,), torch.float32, index)
+    dx = dw = db = dxp = dwp = dbp = wsp = None
+    nbytes = 0
+    if want_grad_x:
+        dx = _empty(shape, dtype=xt, device=dev)
+        dxp = dx.data_ptr()
+    if want_grad_weight:
+        dw = _empty(width, dtype=pt, device=dev)
+        dwp = dw.data_ptr()
+    if want_grad_bias:
+        db = _empty(width, dtype=pt, device=dev)
+        dbp = db.data_ptr()
+    lib = _lib()
     if want_grad_weight or want_grad_bias:
-        ws = _scratch(sla_layernorm_backward_workspace_bytes(rows, width, x.dtype), dev, workspace)
-        nbytes = ws.numel() * ws.element_size()
-    base._check(base.lib().sla_layernorm_backward(
-        rows, width, dt, _DT[pt], gptr, lddy, ptr, ldx, _param(weight, "weight", (width,), pt, dev),
-        _param(mean, "mean", (rows,), torch.float32, dev), _param(rstd, "rstd", (rows,), torch.float32, dev),
-        dx.data_ptr() if want_grad_x else None, dw.data_ptr() if want_grad_weight else None,
-        db.data_ptr() if want_grad_bias else None, ws.data_ptr() if ws is not None else None, nbytes,
-        base._stream(dev)), "sla_layernorm_backward")
+        ws, nbytes = _scratch(lib.sla_layernorm_backward_workspace_bytes(rows, width, dt), dev, workspace)
+        wsp = ws.data_ptr()
+    _check(lib.sla_layernorm_backward(rows, width, dt, _DT[pt], gptr, lddy, ptr, ldx, wp, mp, rp, dxp, dwp, dbp, wsp,
+                                      nbytes, _stream(index)), "sla_layernorm_backward")
     return dx, dw, db
 
 
@@ -178,18 +212,20 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
 
 # --------------------------------------------------------------------------- gated feed-forward block
 
-def _ffn(x, w_in, w_out, activation) -> Tuple[_abi.sla_ffn, int, int]:
-    """(descriptor, address of x, its leading dimension)"""
+def _ffn(x, w_in, w_out, activation):
+    """(descriptor, address of x, its leading dimension, addresses of w_in and w_out)"""
     ptr, rows, ldx = _rows(x, "x")
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"unknown activation {activation!r} (one of {', '.join(ACTIVATIONS)})")
-    if w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape[0] != 2 * w_out.shape[1]:
+    if w_in.dim() != 2 or w_out.dim() != 2 or w_in.size(0) != 2 * w_out.size(1):
         raise ValueError("w_in must be [2 * hidden, width] and w_out [out, hidden], got "
                          f"{tuple(w_in.shape)} and {tuple(w_out.shape)}")
-    f = _abi.sla_ffn()
-    f.tokens, f.width, f.hidden, f.out = rows, x.shape[-1], w_out.shape[1], w_out.shape[0]
-    f.dtype, f.activation = _type(x, "x"), ACTIVATIONS[activation]
-    return f, ptr, ldx
+    out, hidden = w_out.shape
+    width, index = x.size(-1), x.get_device()
+    f = _abi.sla_ffn(rows, width, hidden, out, _type(x, "x"), act)
+    return (f, ptr, ldx, _param(w_in, "w_in", (2 * hidden, width), x.dtype, index),
+            _param(w_out, "w_out", (out, hidden), x.dtype, index))
 
 
 def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in: Optional[torch.Tensor] = None,
@@ -200,20 +236,23 @@ def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in
     w_in stacks Wg over Wu ([2 hidden, width]), b_in likewise; w_out is [out, hidden].  activation:
     "silu", "gelu", "gelu_tanh" or "relu".  Returns y, or with save=True (y, saved): the byte buffer
     of intermediates that sla_gated_ffn_backward takes."""
-    base = _base()
-    f, ptr, ldx = _ffn(x, w_in, w_out, activation)
-    lib, dt, dev, fp = base.lib(), x.dtype, x.device, ctypes.byref(f)
+    f, ptr, ldx, wip, wop = _ffn(x, w_in, w_out, activation)
+    lib, dt, dev, index, fp = _lib(), x.dtype, x.device, x.get_device(), ctypes.byref(f)
+    bip = _param(b_in, "b_in", (2 * f.hidden,), dt, index)
+    bop = _param(b_out, "b_out", (f.out,), dt, index)
     shape = x.shape[:-1] + (f.out,)
     if y is None:
-        y = torch.empty(shape, dtype=dt, device=dev)
-    saved = torch.empty(max(lib.sla_gated_ffn_saved_bytes(fp), 256), dtype=torch.uint8, device=dev) if save else None
-    ws = _scratch(lib.sla_gated_ffn_workspace_bytes(fp), dev, workspace)
-    base._check(lib.sla_gated_ffn(
-        fp, ptr, ldx, _param(w_in, "w_in", (2 * f.hidden, f.width), dt, dev),
-        _param(b_in, "b_in", (2 * f.hidden,), dt, dev), _param(w_out, "w_out", (f.out, f.hidden), dt, dev),
-        _param(b_out, "b_out", (f.out,), dt, dev), _param(y, "y", shape, dt, dev),
-        saved.data_ptr() if save else None, saved.numel() if save else 0, ws.data_ptr(),
-        ws.numel() * ws.element_size(), base._stream(dev)), "sla_gated_ffn")
+        y = _empty(shape, dtype=dt, device=dev)
+        yp = y.data_ptr()
+    else:
+        yp = _param(y, "y", shape, dt, index)
+    saved, sp, sn = None, None, 0
+    if save:
+        saved, sn = _scratch(lib.sla_gated_ffn_saved_bytes(fp), dev, None)
+        sp = saved.data_ptr()
+    ws, nbytes = _scratch(lib.sla_gated_ffn_workspace_bytes(fp), dev, workspace)
+    _check(lib.sla_gated_ffn(fp, ptr, ldx, wip, bip, wop, bop, yp, sp, sn, ws.data_ptr(), nbytes, _stream(index)),
+           "sla_gated_ffn")
     return (y, saved) if save else y
 
 
@@ -223,35 +262,33 @@ def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor
                            workspace: Optional[torch.Tensor] = None):
     """Gradients of sla_gated_ffn (asynchronous): (dx, dw_in, dw_out, db_in, db_out), None where not
     wanted.  x, the weights, the activation and `saved` are the forward call's."""
-    base = _base()
-    f, ptr, ldx = _ffn(x, w_in, w_out, activation)
-    gptr, grows, lddy = _rows(dy, "dy", x)
+    f, ptr, ldx, wip, wop = _ffn(x, w_in, w_out, activation)
+    gptr, _, lddy = _rows(dy, "dy", x)
     if dy.shape != x.shape[:-1] + (f.out,):
         raise ValueError(f"dy must have shape {tuple(x.shape[:-1]) + (f.out,)}, got {tuple(dy.shape)}")
-    lib, dt, dev, fp = base.lib(), x.dtype, x.device, ctypes.byref(f)
-
-    def out(want, *shape):
-        return torch.empty(shape, dtype=dt, device=dev) if want else None
-
-    dx = out(want_grad_x, *x.shape)
-    grads = (out(want_grad_weights, 2 * f.hidden, f.width), out(want_grad_weights, f.out, f.hidden),
-             out(want_grad_bias, 2 * f.hidden), out(want_grad_bias, f.out))
-    ws = _scratch(lib.sla_gated_ffn_backward_workspace_bytes(fp), dev, workspace)
-    if saved.dtype != torch.uint8 or not saved.is_cuda or not saved.is_contiguous():
+    if saved.dtype != torch.uint8 or saved.get_device() != x.get_device() or not saved.is_contiguous():
         raise ValueError("saved must be the buffer that sla_gated_ffn(..., save=True) returned")
-    base._check(lib.sla_gated_ffn_backward(
-        fp, gptr, lddy, ptr, ldx, _param(w_in, "w_in", (2 * f.hidden, f.width), dt, dev),
-        _param(w_out, "w_out", (f.out, f.hidden), dt, dev), saved.data_ptr(), saved.numel(),
-        *(None if t is None else t.data_ptr() for t in (dx,) + grads), ws.data_ptr(),
-        ws.numel() * ws.element_size(), base._stream(dev)), "sla_gated_ffn_backward")
-    return (dx,) + grads
+    lib, dt, dev, fp = _lib(), x.dtype, x.device, ctypes.byref(f)
+    dx = dw_in = dw_out = db_in = db_out = None
+    if want_grad_x:
+        dx = _empty(x.shape, dtype=dt, device=dev)
+    if want_grad_weights:
+        dw_in, dw_out = _empty(w_in.shape, dtype=dt, device=dev), _empty(w_out.shape, dtype=dt, device=dev)
+    if want_grad_bias:
+        db_in, db_out = _empty(2 * f.hidden, dtype=dt, device=dev), _empty(f.out, dtype=dt, device=dev)
+    grads = (dx, dw_in, dw_out, db_in, db_out)
+    ws, nbytes = _scratch(lib.sla_gated_ffn_backward_workspace_bytes(fp), dev, workspace)
+    _check(lib.sla_gated_ffn_backward(fp, gptr, lddy, ptr, ldx, wip, wop, saved.data_ptr(), saved.numel(),
+                                      *[None if t is None else t.data_ptr() for t in grads], ws.data_ptr(), nbytes,
+                                      _stream(x.get_device())), "sla_gated_ffn_backward")
+    return grads
 
 
-def sla_gated_ffn_check(device=None) -> None:
+def sla_gated_ffn_check(device: Optional[int] = None) -> None:
     """Synchronises the current stream and raises SlaError(SLA_TIMEOUT) if a bounded wait inside a
     gated_ffn kernel expired since the last check (never expected)."""
-    base = _base()
-    base._check(base.lib().sla_gated_ffn_check(base._stream(device)), "sla_gated_ffn_check")
+    _check(_lib().sla_gated_ffn_check(_stream(torch.cuda.current_device() if device is None else device)),
+           "sla_gated_ffn_check")
 
 
 class GatedFFN(torch.autograd.Function):
