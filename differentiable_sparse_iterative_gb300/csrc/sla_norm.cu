@@ -6,21 +6,26 @@
 //
 // Both directions are bound by memory (8 and 12 operations an element), so each is one pass: a
 // group of `tpr` threads (a power of two: part of a warp, a warp, or the block) keeps a row in
-// registers as NI vectors of VEC elements a thread, and reduces with shuffles (and shared memory
-// beyond a warp).  The variance is the mean of squared differences from the mean, taken from the
-// registers in a second sweep: the one-sweep form mean(x^2) - mu^2 cancels when a row sits far
-// from zero.  VEC is 16 bytes of elements; rows that cannot be read that way (width, stride or
-// address) take VEC = 1, still coalesced over the threads.  Rows wider than the registers of a
-// 512-thread block hold (16,384 16-bit elements) are re-read from L2 by the *_wide kernels.
+// registers as NI vectors of 16 bytes a thread, and reduces with shuffles (and shared memory beyond
+// a warp).  The variance is the mean of squared differences from the mean, taken from the registers
+// in a second sweep: the one-sweep form mean(x^2) - mu^2 cancels when a row sits far from zero.
 //
-// Backward: a thread sees the same columns in every row of its group, so dw and db accumulate in
-// its registers over the block's rows (persistent blocks, rows in strides of the grid), then
-// across the block in a fixed order, then over the blocks' partial sums in a second kernel.  No
-// atomics: the same call gives the same bits.
+// Blocks are persistent.  The next rows are loaded while the present ones are worked on, and a thread
+// sees the same columns in every row, so it reads the weights once, and dw and db accumulate in its
+// registers, then across the block in a fixed order, then over the blocks' partial sums in a second
+// kernel.  No atomics: the same call gives the same bits.
+//
+// Widths that no vector divides: row r starts (r * width) mod VEC elements behind a 16-byte boundary,
+// which repeats every `classes` = VEC / gcd(width, VEC) rows.  A block takes the rows of one class; its
+// vectors are the aligned ones, shifted by that many columns, and only the first and the last of a
+// row are moved element by element.  Arrays whose rows do not start at the same boundary (strided or
+// odd views) and rows wider than the registers of a 512-thread block hold take the *_any kernels,
+// which read element by element and re-read from L2.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "sla_common.cuh"
 #include "sla_host.h"
@@ -45,120 +50,239 @@ namespace {
 
 constexpr int kLnBlock = 256;     // threads of a block while a row takes no more
 constexpr int kMaxThreads = 512;  // threads of a block that shares one row
-constexpr int kInFlight = 4;      // vectors of a thread on their way at a time: rows are taken in bundles
 constexpr int kColTile = 32;      // columns of a block of the column sums
 constexpr int kMaxParts = 1216;   // blocks that leave partial column sums (8 a multiprocessor)
 
-// Sum over the tpr threads of a group, the same value in each of them.  For tpr > 32 the block is
-// one group; `slot` (32 floats) must not be in use by an earlier sum that a thread still reads.
-__device__ __forceinline__ float group_sum(float v, int tpr, float *slot) {
-  const int in_warp = tpr < 32 ? tpr : 32;
-  for (int o = in_warp >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (tpr <= 32) return v;
-  const int lane = threadIdx.x & 31, warps = tpr >> 5;
-  if (lane == 0) slot[threadIdx.x >> 5] = v;
+// Sums over the tpr threads of a group, the same values in each of them.  `slot` (16 K floats) must not be in
+// use by an earlier sum that a thread still reads; for tpr > 32 every thread of the block takes part.
+template <int K>
+__device__ __forceinline__ void group_sums(float (&v)[K], int tpr, float *slot) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (tpr > o) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+  if (tpr <= 32) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp & ~(warps - 1);
+  if (lane == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) slot[k * 16 + warp] = v[k];
   __syncthreads();
-  float s = lane < warps ? slot[lane] : 0.f;
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = lane < warps ? slot[k * 16 + first + lane] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
+}
+
+__device__ __forceinline__ float group_sum(float v, int tpr, float *slot) {
+  float a[1] = {v};
+  group_sums(a, tpr, slot);
+  return a[0];
+}
+
+// 16 bytes of a row, as pairs of float32.
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T), pairs = n / 2;
+  uint4 q;
+  // Elements [c, c + n) of a row of `width`, of which those outside are 0.
+  __device__ __forceinline__ void load(const T *row, int c, int width) {
+    if (c >= 0 && c + n <= width) {
+      q = *reinterpret_cast<const uint4 *>(row + c);
+      return;
+    }
+    Pack<T, n> e;
+#pragma unroll
+    for (int k = 0; k < n; ++k) e.v[k] = c + k >= 0 && c + k < width ? row[c + k] : from_f32<T>(0.f);
+    q = *reinterpret_cast<uint4 *>(&e);
+  }
+  __device__ __forceinline__ void values(float2 (&v)[pairs]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (sizeof(T) == 4) {
+      v[0] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      v[1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = unpair16(w[k], T{});
+    }
+  }
+  static __device__ __forceinline__ void store(T *row, int c, int width, const float2 (&v)[pairs]) {
+    if (c >= 0 && c + n <= width) {
+      uint4 q;
+      if constexpr (sizeof(T) == 4)
+        q = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                       __float_as_uint(v[1].y));
+      else
+        q = make_uint4(pair16(v[0].x, v[0].y, T{}), pair16(v[1].x, v[1].y, T{}), pair16(v[2].x, v[2].y, T{}),
+                       pair16(v[3].x, v[3].y, T{}));
+      *reinterpret_cast<uint4 *>(row + c) = q;
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < n; ++k)
+      if (c + k >= 0 && c + k < width) row[c + k] = from_f32<T>(k & 1 ? v[k / 2].y : v[k / 2].x);
+  }
+};
+
+// Columns [c, c + 2 PAIRS) of a parameter as pairs, `other` where there is none and 0 outside of the row.
+// vec: whole vectors may be read at once.
+template <typename P, int PAIRS>
+__device__ __forceinline__ void param_pairs(const P *p, int c, int width, float other, bool vec, float2 (&v)[PAIRS]) {
+  float e[2 * PAIRS];
+  if (vec && p && c < width) {
+    load_f32<P, 2 * PAIRS>(p + c, e);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2 * PAIRS; ++k)
+      e[k] = c + k >= 0 && c + k < width ? (p ? to_f32(p[c + k]) : other) : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < PAIRS; ++k) v[k] = f2(e[2 * k], e[2 * k + 1]);
+}
+
+// Which rows and columns a thread works on.
+struct Share {
+  int t, first;        // thread of the group; column of its first vector's first element
+  int64_t row, step;   // its first row; rows from turn to turn
+  int64_t next;        // rows between the rows of a bundle
+};
+
+template <int VEC, int R>
+__device__ __forceinline__ Share share_of(int tpr, int classes, int shift, int64_t shift_step) {
+  const int groups = blockDim.x / tpr, cls = blockIdx.x % classes;
+  Share s;
+  s.t = threadIdx.x & (tpr - 1);
+  s.first = -(int)((shift + cls * shift_step) % VEC) + s.t * VEC;
+  s.next = (int64_t)groups * classes;
+  s.row = ((int64_t)(blockIdx.x / classes) * R * groups + threadIdx.x / tpr) * classes + cls;
+  s.step = (int64_t)(gridDim.x / classes) * R * groups * classes;
   return s;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void unpack(const Pack<T, N> &q, float (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = to_f32(q.v[i]);
-}
+// Weights stay in registers while they are not more than 16 columns a thread.
+template <typename T, int NI>
+inline constexpr bool kKeepParams = NI * Vec<T>::n <= 16;
 
-// Rows of a bundle: as many as keep kInFlight vectors of a thread in flight.
-template <int NI>
-inline constexpr int kBundle = NI >= kInFlight ? 1 : kInFlight / NI;
-
-template <typename T, typename P, int VEC, int NI>
-__global__ void __launch_bounds__(kMaxThreads) ln_forward(int64_t rows, int width, int tpr, const T *__restrict__ x,
-                                                          int64_t ldx, const P *__restrict__ w,
-                                                          const P *__restrict__ b, float eps, T *__restrict__ y,
-                                                          float *__restrict__ mean, float *__restrict__ rstd) {
-  constexpr int R = kBundle<NI>;
-  __shared__ float slots[2 * R][32];
-  const int t = threadIdx.x & (tpr - 1), groups = blockDim.x / tpr;
-  const int64_t row0 = blockIdx.x * (int64_t)groups * R + threadIdx.x / tpr;
-  Pack<T, VEC> raw[R][NI];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t row = row0 + r * groups;
+// shift: elements between a 16-byte boundary and row 0, shift_step: added by each row (mod VEC).
+template <typename T, typename P, int NI, int R>
+__global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 : 1)
+    ln_forward(int64_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec, const T *__restrict__ x, int64_t ldx,
+                                                          const P *__restrict__ w, const P *__restrict__ b, float eps,
+                                                          T *__restrict__ y, float *__restrict__ mean,
+                                                          float *__restrict__ rstd) {
+  using V = Vec<T>;
+  constexpr int N = V::n, H = V::pairs;
+  constexpr bool keep = kKeepParams<T, NI>;
+  __shared__ float slots[2][2][R * 16];
+  const Share s = share_of<N, R>(tpr, classes, shift, shift_step);
+  const int apart = tpr * N;
+  const float inv = 1.f / (float)width;
+  float2 wk[keep ? NI : 1][H], bk[keep ? NI : 1][H];
+  if constexpr (keep)
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int c = (i * tpr + t) * VEC;
-      if (row < rows && c < width) {
-        raw[r][i] = *reinterpret_cast<const Pack<T, VEC> *>(x + row * ldx + c);
-      } else {
+      param_pairs<P, H>(w, s.first + i * apart, width, 1.f, pvec, wk[i]);
+      param_pairs<P, H>(b, s.first + i * apart, width, 0.f, pvec, bk[i]);
+    }
+  V raw[R][NI];
+  const T *px = x + s.row * ldx;  // the row that is asked for next
+  T *py = y + s.row * (int64_t)width;
+  const int64_t x_next = s.next * ldx, x_step = s.step * ldx, y_next = s.next * width, y_step = s.step * width;
+  auto ask = [&](int64_t row) {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) raw[r][i].v[k] = from_f32<T>(0.f);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int c = s.first + i * apart;
+        raw[r][i].q = make_uint4(0, 0, 0, 0);
+        if (row + r * s.next < rows && c < width) raw[r][i].load(px + r * x_next, c, width);
+      }
+    px += x_step;
+  };
+  ask(s.row);
+  int turn = 0;  // the slots alternate, so a turn's sums never meet the previous one's reads
+  // every thread of a block makes the same number of turns (the sums need whole warps and blocks)
+  const int64_t lead = s.row - (int64_t)(threadIdx.x / tpr) * classes;
+  for (int64_t ahead = lead, row = s.row; ahead < rows; ahead += s.step, row += s.step, py += y_step, turn ^= 1) {
+    float2 v[R][NI][H];
+    float sum[R], sq[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 a = f2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        raw[r][i].values(v[r][i]);
+#pragma unroll
+        for (int k = 0; k < H; ++k) a = add2(a, v[r][i][k]);
+      }
+      sum[r] = a.x + a.y;
+    }
+    if (ahead + s.step < rows) ask(row + s.step);
+    group_sums<R>(sum, tpr, slots[turn][0]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float mu = sum[r] * inv;
+      const float2 minus = f2(-mu, -mu);
+      float2 a = f2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int c = s.first + i * apart;
+        if (c >= 0 && c + N <= width) {
+#pragma unroll
+          for (int k = 0; k < H; ++k) v[r][i][k] = add2(v[r][i][k], minus);
+        } else {  // no differences where there is no row
+#pragma unroll
+          for (int k = 0; k < H; ++k) {
+            v[r][i][k].x = c + 2 * k >= 0 && c + 2 * k < width ? v[r][i][k].x - mu : 0.f;
+            v[r][i][k].y = c + 2 * k + 1 >= 0 && c + 2 * k + 1 < width ? v[r][i][k].y - mu : 0.f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < H; ++k) a = fma2(v[r][i][k], v[r][i][k], a);
+      }
+      sum[r] = mu;
+      sq[r] = a.x + a.y;
+    }
+    group_sums<R>(sq, tpr, slots[turn][1]);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int c = s.first + i * apart;
+      float2 wv[H], bv[H];
+      if constexpr (keep) {
+#pragma unroll
+        for (int k = 0; k < H; ++k) wv[k] = wk[i][k], bv[k] = bk[i][k];
+      } else {
+        param_pairs<P, H>(w, c, width, 1.f, pvec, wv);
+        param_pairs<P, H>(b, c, width, 0.f, pvec, bv);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float rs = rsqrtf(sq[r] * inv + eps);  // 2 units in the last place
+        const int64_t at = row + r * s.next;
+#pragma unroll
+        for (int k = 0; k < H; ++k) v[r][i][k] = fma2(mul2(v[r][i][k], f2(rs, rs)), wv[k], bv[k]);
+        if (at < rows && c < width) V::store(py + r * y_next, c, width, v[r][i]);
+        if (i == 0 && s.t == 0 && at < rows && mean) {
+          mean[at] = sum[r];
+          rstd[at] = rs;
+        }
       }
     }
   }
-  const float inv = 1.f / (float)width;
-  float mu[R], rs[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      float v[VEC];
-      unpack(raw[r][i], v);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) s += v[k];
-    }
-    mu[r] = group_sum(s, tpr, slots[r]) * inv;
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const bool in = (i * tpr + t) * VEC < width;
-      float v[VEC];
-      unpack(raw[r][i], v);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) q += in ? (v[k] - mu[r]) * (v[k] - mu[r]) : 0.f;
-    }
-    rs[r] = 1.f / sqrtf(group_sum(q, tpr, slots[R + r]) * inv + eps);
-  }
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int c = (i * tpr + t) * VEC;
-    if (c >= width) break;
-    float wv[VEC], bv[VEC];
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) wv[k] = 1.f, bv[k] = 0.f;
-    if (w) load_f32<P, VEC>(w + c, wv);
-    if (b) load_f32<P, VEC>(b + c, bv);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t row = row0 + r * groups;
-      if (row >= rows) break;
-      float v[VEC];
-      unpack(raw[r][i], v);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) v[k] = (v[k] - mu[r]) * rs[r] * wv[k] + bv[k];
-      store_f32<T, VEC>(y + row * width + c, v);
-    }
-  }
-  if (t == 0 && mean)
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t row = row0 + r * groups;
-      if (row < rows) mean[row] = mu[r], rstd[row] = rs[r];
-    }
 }
 
-// Rows of any width, one block a row, three sweeps (the second and third hit L2).
+// Rows of any width and alignment, one block a row, three sweeps (the second and third hit L2).
 template <typename T, typename P>
-__global__ void __launch_bounds__(kMaxThreads) ln_forward_wide(int64_t rows, int64_t width, const T *__restrict__ x,
-                                                               int64_t ldx, const P *__restrict__ w,
-                                                               const P *__restrict__ b, float eps, T *__restrict__ y,
-                                                               float *__restrict__ mean, float *__restrict__ rstd) {
-  __shared__ float slots[2][32];
+__global__ void __launch_bounds__(kMaxThreads) ln_forward_any(int64_t rows, int64_t width, const T *__restrict__ x,
+                                                              int64_t ldx, const P *__restrict__ w,
+                                                              const P *__restrict__ b, float eps, T *__restrict__ y,
+                                                              float *__restrict__ mean, float *__restrict__ rstd) {
+  __shared__ float slots[2][16];
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const T *xr = x + row * ldx;
     float s = 0.f;
@@ -174,136 +298,155 @@ __global__ void __launch_bounds__(kMaxThreads) ln_forward_wide(int64_t rows, int
       const float xh = (to_f32(xr[c]) - mu) * rs;
       y[row * width + c] = from_f32<T>((w ? xh * to_f32(w[c]) : xh) + (b ? to_f32(b[c]) : 0.f));
     }
-    if (threadIdx.x == 0) {
-      if (mean) mean[row] = mu;
-      if (rstd) rstd[row] = rs;
+    if (threadIdx.x == 0 && mean) {
+      mean[row] = mu;
+      rstd[row] = rs;
     }
-    __syncthreads();  // slots[0] is free again
+    __syncthreads();  // the slots are free again
   }
 }
 
 // parts: [gridDim.x][2][width] partial sums of dw and db (NULL: dx only).
-template <typename T, typename P, int VEC, int NI>
-__global__ void __launch_bounds__(kMaxThreads) ln_backward(int64_t rows, int width, int tpr, const T *__restrict__ dy,
-                                                           int64_t lddy, const T *__restrict__ x, int64_t ldx,
+template <typename T, typename P, int NI, int R>
+__global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 : 1)
+    ln_backward(int64_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec, const T *__restrict__ dy, int64_t lddy,
+                                                           const T *__restrict__ x, int64_t ldx,
                                                            const P *__restrict__ w, const float *__restrict__ mean,
                                                            const float *__restrict__ rstd, T *__restrict__ dx,
                                                            float *__restrict__ parts) {
-  constexpr int R = kBundle<2 * NI>;  // two vectors, of x and of dy, for each of the forward pass's
-  extern __shared__ float cols[];     // more than one group: [2][width]
-  __shared__ float slots[2][2 * R][32];
-  const int t = threadIdx.x & (tpr - 1), groups = blockDim.x / tpr;
-  const int64_t step = (int64_t)gridDim.x * groups * R;
+  using V = Vec<T>;
+  constexpr int N = V::n, H = V::pairs;
+  constexpr bool keep = kKeepParams<T, NI>;
+  extern __shared__ float cols[];  // more than one group: [2][width]
+  __shared__ float slots[2][2 * R * 16];
+  const Share s = share_of<N, R>(tpr, classes, shift, shift_step);
+  const int apart = tpr * N, groups = blockDim.x / tpr;
   const float inv = 1.f / (float)width;
-  float aw[NI][VEC], ab[NI][VEC];
+  float2 wk[keep ? NI : 1][H], aw[NI][H], ab[NI][H];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NI; ++i) {
+    if constexpr (keep) param_pairs<P, H>(w, s.first + i * apart, width, 1.f, pvec, wk[i]);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) aw[i][k] = ab[i][k] = 0.f;
-  int turn = 0;  // the slots alternate, so a bundle's sums never meet the previous one's reads
-  // every thread of a block makes the same number of turns (the sums need whole warps and blocks)
-  for (int64_t base = blockIdx.x * (int64_t)groups * R; base < rows; base += step, turn ^= 1) {
-    Pack<T, VEC> rx[R][NI], rg[R][NI];
-    float mu[R], rs[R], m1[R], m2[R];
+    for (int k = 0; k < H; ++k) aw[i][k] = ab[i][k] = f2(0.f, 0.f);
+  }
+  V rx[R][NI], rg[R][NI];
+  float rm[R], rr[R];
+  const T *px = x + s.row * ldx, *pg = dy + s.row * lddy;  // the rows that are asked for next
+  T *pd = dx + s.row * (int64_t)width;
+  const int64_t x_next = s.next * ldx, g_next = s.next * lddy, d_next = s.next * width;
+  auto ask = [&](int64_t row) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t row = base + r * groups + threadIdx.x / tpr;
+    for (int r = 0; r < R; ++r, row += s.next) {
       const bool live = row < rows;
-      mu[r] = live ? mean[row] : 0.f;
-      rs[r] = live ? rstd[row] : 0.f;
+      rm[r] = live ? mean[row] : 0.f;
+      rr[r] = live ? rstd[row] : 0.f;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int c = (i * tpr + t) * VEC;
+        const int c = s.first + i * apart;
+        rx[r][i].q = rg[r][i].q = make_uint4(0, 0, 0, 0);
         if (live && c < width) {
-          rx[r][i] = *reinterpret_cast<const Pack<T, VEC> *>(x + row * ldx + c);
-          rg[r][i] = *reinterpret_cast<const Pack<T, VEC> *>(dy + row * lddy + c);
-        } else {
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) rx[r][i].v[k] = rg[r][i].v[k] = from_f32<T>(0.f);
+          rx[r][i].load(px + r * x_next, c, width);
+          rg[r][i].load(pg + r * g_next, c, width);
         }
       }
     }
+    px += s.step * ldx;
+    pg += s.step * lddy;
+  };
+  ask(s.row);
+  int turn = 0;
+  const int64_t lead = s.row - (int64_t)(threadIdx.x / tpr) * classes;
+  for (int64_t ahead = lead, row = s.row; ahead < rows; ahead += s.step, row += s.step, turn ^= 1) {
+    float2 xh[R][NI][H], g[R][NI][H];
+    float sums[2 * R], rs[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float s1 = 0.f, s2 = 0.f;
+      rs[r] = rr[r];
+      const float2 scale = f2(rs[r], rs[r]);
+      float2 a1 = f2(0.f, 0.f), a2 = a1;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        if (c >= width) break;
-        float wv[VEC], xv[VEC], g[VEC];
-        unpack(rx[r][i], xv);
-        unpack(rg[r][i], g);
-        if (w) load_f32<P, VEC>(w + c, wv);
+        float2 wv[H];
+        if constexpr (keep) {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const float xh = (xv[k] - mu[r]) * rs[r];
-          aw[i][k] += g[k] * xh;
-          ab[i][k] += g[k];
-          if (w) g[k] *= wv[k];
-          s1 += g[k];
-          s2 += g[k] * xh;
+          for (int k = 0; k < H; ++k) wv[k] = wk[i][k];
+        } else {
+          param_pairs<P, H>(w, s.first + i * apart, width, 1.f, pvec, wv);
+        }
+        rx[r][i].values(xh[r][i]);
+        rg[r][i].values(g[r][i]);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+          // dy is 0 outside of the row: what xh is there does not count
+          xh[r][i][k] = mul2(add2(xh[r][i][k], f2(-rm[r], -rm[r])), scale);
+          aw[i][k] = fma2(g[r][i][k], xh[r][i][k], aw[i][k]);
+          ab[i][k] = add2(ab[i][k], g[r][i][k]);
+          g[r][i][k] = mul2(g[r][i][k], wv[k]);
+          a1 = add2(a1, g[r][i][k]);
+          a2 = fma2(g[r][i][k], xh[r][i][k], a2);
         }
       }
-      m1[r] = group_sum(s1, tpr, slots[turn][2 * r]) * inv;
-      m2[r] = group_sum(s2, tpr, slots[turn][2 * r + 1]) * inv;
+      sums[2 * r] = a1.x + a1.y;
+      sums[2 * r + 1] = a2.x + a2.y;
     }
+    if (ahead + s.step < rows) ask(row + s.step);
+    group_sums<2 * R>(sums, tpr, slots[turn]);
+    T *out = pd;
+    pd += s.step * width;
     if (!dx) continue;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t row = base + r * groups + threadIdx.x / tpr;
-      if (row >= rows) break;
+      const int64_t at = row + r * s.next;
+      const float m1 = -sums[2 * r] * inv, m2 = -sums[2 * r + 1] * inv;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        if (c >= width) break;
-        float wv[VEC], xv[VEC], g[VEC];
-        unpack(rx[r][i], xv);
-        unpack(rg[r][i], g);
-        if (w) load_f32<P, VEC>(w + c, wv);
+        const int c = s.first + i * apart;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const float xh = (xv[k] - mu[r]) * rs[r];
-          g[k] = rs[r] * ((w ? g[k] * wv[k] : g[k]) - m1[r] - xh * m2[r]);
-        }
-        store_f32<T, VEC>(dx + row * width + c, g);
+        for (int k = 0; k < H; ++k)
+          g[r][i][k] = mul2(fma2(xh[r][i][k], f2(m2, m2), add2(g[r][i][k], f2(m1, m1))), f2(rs[r], rs[r]));
+        if (at < rows && c < width) V::store(out + r * d_next, c, width, g[r][i]);
       }
     }
   }
   if (!parts) return;
   float *pw = parts + (int64_t)blockIdx.x * 2 * width, *pb = pw + width;
   if (groups == 1) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int c = (i * tpr + t) * VEC;
-      if (c >= width) break;
-      store_f32<float, VEC>(pw + c, aw[i]);
-      store_f32<float, VEC>(pb + c, ab[i]);
-    }
-    return;
-  }
-  // the groups of a warp by shuffles, then the groups that are left one after another
-  for (int o = tpr; o < 32; o <<= 1) {
+    // (columns of the shifted vectors that are not in the row do not exist)
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        aw[i][k] += __shfl_xor_sync(0xffffffffu, aw[i][k], o);
-        ab[i][k] += __shfl_xor_sync(0xffffffffu, ab[i][k], o);
+      for (int k = 0; k < N; ++k) {
+        const int c = s.first + i * apart + k;
+        if (c < 0 || c >= width) continue;
+        pw[c] = k & 1 ? aw[i][k / 2].y : aw[i][k / 2].x;
+        pb[c] = k & 1 ? ab[i][k / 2].y : ab[i][k / 2].x;
       }
+    return;
   }
-  const int apart = tpr < 32 ? 32 : tpr;
-  for (int turn_of = 0; turn_of < (int)blockDim.x / apart; ++turn_of) {
-    if ((int)threadIdx.x / apart == turn_of && (int)threadIdx.x % apart < tpr) {
+  // the groups of a warp by shuffles, then what is left one after another
+  for (int o = tpr; o < 32; o <<= 1)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        if (c >= width) break;
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          cols[c + k] = turn_of ? cols[c + k] + aw[i][k] : aw[i][k];
-          cols[width + c + k] = turn_of ? cols[width + c + k] + ab[i][k] : ab[i][k];
-        }
+      for (int k = 0; k < H; ++k) {
+        aw[i][k].x += __shfl_xor_sync(0xffffffffu, aw[i][k].x, o);
+        aw[i][k].y += __shfl_xor_sync(0xffffffffu, aw[i][k].y, o);
+        ab[i][k].x += __shfl_xor_sync(0xffffffffu, ab[i][k].x, o);
+        ab[i][k].y += __shfl_xor_sync(0xffffffffu, ab[i][k].y, o);
       }
+  const int size = tpr < 32 ? 32 : tpr;
+  for (int from = 0; from < (int)blockDim.x; from += size) {
+    if ((int)threadIdx.x >= from && (int)threadIdx.x < from + tpr) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int c = s.first + i * apart + k;
+          if (c < 0 || c >= width) continue;
+          const float a = k & 1 ? aw[i][k / 2].y : aw[i][k / 2].x, d = k & 1 ? ab[i][k / 2].y : ab[i][k / 2].x;
+          cols[c] = from ? cols[c] + a : a;
+          cols[width + c] = from ? cols[width + c] + d : d;
+        }
     }
     __syncthreads();
   }
@@ -311,13 +454,12 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward(int64_t rows, int wid
 }
 
 template <typename T, typename P>
-__global__ void __launch_bounds__(kMaxThreads) ln_backward_wide(int64_t rows, int64_t width,
-                                                                const T *__restrict__ dy, int64_t lddy,
-                                                                const T *__restrict__ x, int64_t ldx,
-                                                                const P *__restrict__ w,
-                                                                const float *__restrict__ mean,
-                                                                const float *__restrict__ rstd, T *__restrict__ dx) {
-  __shared__ float slots[2][32];
+__global__ void __launch_bounds__(kMaxThreads) ln_backward_any(int64_t rows, int64_t width, const T *__restrict__ dy,
+                                                               int64_t lddy, const T *__restrict__ x, int64_t ldx,
+                                                               const P *__restrict__ w,
+                                                               const float *__restrict__ mean,
+                                                               const float *__restrict__ rstd, T *__restrict__ dx) {
+  __shared__ float slots[2][16];
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const float mu = mean[row], rs = rstd[row];
     float s1 = 0.f, s2 = 0.f;
@@ -339,7 +481,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_backward_wide(int64_t rows, in
 
 // Partial column sums of dw and db for rows of any width: block (column tile, part), rows in strides.
 template <typename T>
-__global__ void __launch_bounds__(1024) ln_columns_wide(int64_t rows, int64_t width, const T *__restrict__ dy,
+__global__ void __launch_bounds__(1024) ln_columns_any(int64_t rows, int64_t width, const T *__restrict__ dy,
                                                         int64_t lddy, const T *__restrict__ x, int64_t ldx,
                                                         const float *__restrict__ mean,
                                                         const float *__restrict__ rstd, float *__restrict__ parts) {
@@ -375,6 +517,7 @@ __global__ void __launch_bounds__(1024) ln_reduce_parts(int nparts, int64_t widt
   if (!out) return;
   float s = 0.f;
   if (c < width)
+#pragma unroll 8
     for (int p = wy; p < nparts; p += 32) s += parts[((int64_t)p * 2 + which) * width + c];
   sm[wy][lane] = s;
   __syncthreads();
@@ -385,88 +528,104 @@ __global__ void __launch_bounds__(1024) ln_reduce_parts(int nparts, int64_t widt
   }
 }
 
-// How the rows of one call are laid over threads.
+// How the rows of one call are laid over threads; items = 0: the *_any kernels.
 struct LnPlan {
-  int vec, items, tpr, block;  // vec = 0: the wide kernels
+  int items, tpr, block, classes, shift;
+  int64_t shift_step;
+  // whole vectors of a parameter may be read at once
+  bool pvec(std::initializer_list<const void *> params) const {
+    for (const void *p : params)
+      if (!aligned(p, 16)) return false;
+    return !shift && !shift_step;
+  }
 };
 
-// Widest vector, then the fewest threads a row that hold it in `few` vectors (8 single elements) each, or
-// in four (16) where even kMaxThreads threads cannot.
-LnPlan ln_plan(int64_t width, int vec, int few) {
-  const int64_t nv = (width + vec - 1) / vec;
-  const int most = vec > 1 ? 4 : 16;
-  if (nv > (int64_t)kMaxThreads * most) return {0, 0, kMaxThreads, kMaxThreads};
-  const int enough = vec > 1 ? few : 8;
+struct Rows {
+  const void *p;
+  int64_t ld;
+};
+
+// The fewest threads a row that hold it in two vectors each, or in four where even kMaxThreads threads
+// cannot.  The arrays have to start every row at the same place behind a 16-byte boundary.
+LnPlan ln_plan(int64_t width, int32_t dtype, std::initializer_list<Rows> arrays) {
+  const int e = (int)net_size(dtype), vec = 16 / e;
+  LnPlan pl{0, kMaxThreads, kMaxThreads, 1, 0, 0};
+  pl.shift = (int)((uintptr_t)arrays.begin()->p % 16 / e);
+  pl.shift_step = arrays.begin()->ld % vec;
+  for (const Rows &a : arrays)
+    if (a.p && ((int)((uintptr_t)a.p % 16 / e) != pl.shift || a.ld % vec != pl.shift_step)) return pl;
+  while ((pl.classes * pl.shift_step) % vec) pl.classes *= 2;
+  // a shifted row may need one vector more
+  const int64_t nv = (width + vec - 1) / vec + (pl.shift || pl.shift_step ? 1 : 0);
+  if (nv > kMaxThreads * 4) return pl;
   int tpr = 1;
-  while (tpr < kMaxThreads && ((int64_t)tpr * enough < nv || (tpr < 32 && tpr < nv))) tpr <<= 1;
-  const int need = (int)((nv + tpr - 1) / tpr);
-  const int items = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 16;
-  return {vec, items, tpr, tpr > 32 ? tpr : kLnBlock};
+  while (tpr < kMaxThreads && (2 * tpr < nv || (tpr < 32 && tpr < nv))) tpr <<= 1;
+  const int64_t need = (nv + tpr - 1) / tpr;
+  pl.items = need <= 1 ? 1 : need <= 2 ? 2 : 4;
+  pl.tpr = tpr;
+  pl.block = std::max(tpr, kLnBlock);
+  return pl;
 }
 
-template <typename T, typename P, int VEC, int NI>
+// Blocks that fill the GPU with `threads` a multiprocessor, in whole sets of classes, no more than there are bundles.
+int ln_grid(const LnPlan &pl, int64_t rows, int64_t rows_a_turn, int threads) {
+  const int64_t most = std::min(sm_count() * std::max(1, threads / pl.block), kMaxParts);
+  const int64_t need = ((rows + pl.classes - 1) / pl.classes + rows_a_turn - 1) / rows_a_turn;
+  return (int)(std::max<int64_t>(1, std::min<int64_t>(most / pl.classes, need)) * pl.classes);
+}
+
+template <typename T, typename P, int NI, int R>
 void launch_forward(const LnPlan &pl, int64_t rows, int64_t width, const void *x, int64_t ldx, const void *w,
                     const void *b, float eps, void *y, float *mean, float *rstd, cudaStream_t st) {
-  const int64_t rpb = pl.block / pl.tpr * kBundle<NI>;
-  ln_forward<T, P, VEC, NI><<<(unsigned)((rows + rpb - 1) / rpb), pl.block, 0, st>>>(
-      rows, (int)width, pl.tpr, (const T *)x, ldx, (const P *)w, (const P *)b, eps, (T *)y, mean, rstd);
+  const int grid = ln_grid(pl, rows, pl.block / pl.tpr * R, 1024);
+  ln_forward<T, P, NI, R><<<grid, pl.block, 0, st>>>(rows, (int)width, pl.tpr, pl.classes, pl.shift, pl.shift_step,
+                                                     pl.pvec({w, b}) && width % Vec<T>::n == 0, (const T *)x, ldx, (const P *)w, (const P *)b, eps, (T *)y, mean,
+                                                     rstd);
 }
 
 template <typename T, typename P>
-cudaError_t forward(int64_t rows, int64_t width, bool vec_ok, const void *x, int64_t ldx, const void *w,
+cudaError_t forward(int64_t rows, int64_t width, const LnPlan &pl, const void *x, int64_t ldx, const void *w,
                     const void *b, float eps, void *y, float *mean, float *rstd, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  const LnPlan pl = ln_plan(width, vec_ok ? V : 1, 4);
-#define SLA_LN_FWD(VEC, NI) launch_forward<T, P, VEC, NI>(pl, rows, width, x, ldx, w, b, eps, y, mean, rstd, st)
-  if (pl.vec == 0)
-    ln_forward_wide<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
+#define SLA_LN_FWD(NI, R) launch_forward<T, P, NI, R>(pl, rows, width, x, ldx, w, b, eps, y, mean, rstd, st)
+  if (pl.items == 0)
+    ln_forward_any<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
         rows, width, (const T *)x, ldx, (const P *)w, (const P *)b, eps, (T *)y, mean, rstd);
-  else if (pl.vec > 1)
-    pl.items == 1 ? SLA_LN_FWD(V, 1) : pl.items == 2 ? SLA_LN_FWD(V, 2) : SLA_LN_FWD(V, 4);
   else
-    pl.items <= 2 ? SLA_LN_FWD(1, 2) : pl.items <= 8 ? SLA_LN_FWD(1, 8) : SLA_LN_FWD(1, 16);
+    pl.items == 1 ? SLA_LN_FWD(1, 2) : pl.items == 2 ? SLA_LN_FWD(2, 1) : SLA_LN_FWD(4, 1);
 #undef SLA_LN_FWD
   return cudaGetLastError();
 }
 
-template <typename T, typename P, int VEC, int NI>
+template <typename T, typename P, int NI, int R>
 int launch_backward(const LnPlan &pl, int64_t rows, int64_t width, const void *dy, int64_t lddy, const void *x,
                     int64_t ldx, const void *w, const float *mean, const float *rstd, void *dx, float *parts,
                     cudaStream_t st) {
-  const int groups = pl.block / pl.tpr;
-  const int64_t rpb = groups * kBundle<2 * NI>;
-  // enough blocks to fill the GPU (1024 threads a multiprocessor), no more than there are bundles
-  const int per_sm = std::max(1, 1024 / pl.block);
-  const int grid = (int)std::min<int64_t>(std::min(sm_count() * per_sm, kMaxParts), (rows + rpb - 1) / rpb);
+  const int groups = pl.block / pl.tpr, grid = ln_grid(pl, rows, groups * R, NI == 1 ? 768 : 512);
   const size_t smem = groups > 1 && parts ? 2 * sizeof(float) * (size_t)width : 0;
-  ln_backward<T, P, VEC, NI><<<grid, pl.block, smem, st>>>(rows, (int)width, pl.tpr, (const T *)dy, lddy,
-                                                           (const T *)x, ldx, (const P *)w, mean, rstd, (T *)dx, parts);
+  ln_backward<T, P, NI, R><<<grid, pl.block, smem, st>>>(rows, (int)width, pl.tpr, pl.classes, pl.shift,
+                                                         pl.shift_step, pl.pvec({w}) && width % Vec<T>::n == 0,
+                                                         (const T *)dy, lddy, (const T *)x, ldx, (const P *)w, mean, rstd, (T *)dx, parts);
   return grid;
 }
 
 template <typename T, typename P>
-cudaError_t backward(int64_t rows, int64_t width, bool vec_ok, const void *dy, int64_t lddy, const void *x,
+cudaError_t backward(int64_t rows, int64_t width, const LnPlan &pl, const void *dy, int64_t lddy, const void *x,
                      int64_t ldx, const void *w, const float *mean, const float *rstd, void *dx, void *dw, void *db,
                      float *parts, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  const LnPlan pl = ln_plan(width, vec_ok ? V : 1, 16 / V);  // 16 elements and their two sums fit the registers
   int nparts = 0;
   const int ctiles = (int)((width + kColTile - 1) / kColTile);
-#define SLA_LN_BWD(VEC, NI) \
-  launch_backward<T, P, VEC, NI>(pl, rows, width, dy, lddy, x, ldx, w, mean, rstd, dx, parts, st)
-  if (pl.vec == 0) {
+#define SLA_LN_BWD(NI, R) launch_backward<T, P, NI, R>(pl, rows, width, dy, lddy, x, ldx, w, mean, rstd, dx, parts, st)
+  if (pl.items == 0) {
     if (dx)
-      ln_backward_wide<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
+      ln_backward_any<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
           rows, width, (const T *)dy, lddy, (const T *)x, ldx, (const P *)w, mean, rstd, (T *)dx);
     if (parts) {
       nparts = (int)std::max<int64_t>(1, std::min<int64_t>(16, (rows + 127) / 128));
-      ln_columns_wide<T><<<dim3(ctiles, nparts), 1024, 0, st>>>(rows, width, (const T *)dy, lddy, (const T *)x, ldx,
-                                                                mean, rstd, parts);
+      ln_columns_any<T><<<dim3(ctiles, nparts), 1024, 0, st>>>(rows, width, (const T *)dy, lddy, (const T *)x, ldx,
+                                                               mean, rstd, parts);
     }
-  } else if (pl.vec > 1) {
-    nparts = pl.items == 1 ? SLA_LN_BWD(V, 1) : pl.items == 2 ? SLA_LN_BWD(V, 2) : SLA_LN_BWD(V, 4);
   } else {
-    nparts = pl.items <= 2 ? SLA_LN_BWD(1, 2) : pl.items <= 8 ? SLA_LN_BWD(1, 8) : SLA_LN_BWD(1, 16);
+    nparts = pl.items == 1 ? SLA_LN_BWD(1, 1) : pl.items == 2 ? SLA_LN_BWD(2, 1) : SLA_LN_BWD(4, 1);
   }
 #undef SLA_LN_BWD
   if (parts) ln_reduce_parts<P><<<dim3(ctiles, 2), 1024, 0, st>>>(nparts, width, parts, (P *)dw, (P *)db);
@@ -484,11 +643,6 @@ sla_status check_rows(const void *p, int64_t rows, int64_t width, int64_t ld, in
   if (rows == 0) return SLA_OK;
   if (!p || !aligned(p, net_size(dtype))) return SLA_INVALID_ARG;
   return ld >= width || rows == 1 ? SLA_OK : SLA_INVALID_ARG;
-}
-
-bool vec_rows(const void *p, int64_t width, int64_t ld, int32_t dtype) {
-  const size_t e = net_size(dtype);
-  return aligned(p, 16) && (width * e) % 16 == 0 && (ld * (int64_t)e) % 16 == 0;
 }
 
 // Calls f with the element and parameter types of a call.
@@ -515,11 +669,11 @@ SLA_API sla_status sla_layernorm(int64_t rows, int64_t width, int32_t dtype, int
   SLA_CHECK(check_rows(y, rows, width, width, dtype));
   const size_t ps = net_size(param_dtype);
   if (!aligned(weight, ps) || !aligned(bias, ps) || !aligned(mean, 4) || !aligned(rstd, 4)) return SLA_INVALID_ARG;
+  if (!mean != !rstd) return SLA_INVALID_ARG;
   if (rows == 0) return SLA_OK;
-  const bool vec = vec_rows(x, width, ldx, dtype) && vec_rows(y, width, width, dtype) && aligned(weight, 16) &&
-                   aligned(bias, 16);
+  const LnPlan pl = ln_plan(width, dtype, {{x, rows == 1 ? width : ldx}, {y, width}});
   const cudaError_t e = by_type(dtype, param_dtype, [&](auto t, auto p) {
-    return forward<decltype(t), decltype(p)>(rows, width, vec, x, ldx, weight, bias, (float)eps, y, mean, rstd,
+    return forward<decltype(t), decltype(p)>(rows, width, pl, x, ldx, weight, bias, (float)eps, y, mean, rstd,
                                              (cudaStream_t)stream);
   });
   if (e != cudaSuccess) return fail(e);
@@ -559,10 +713,10 @@ SLA_API sla_status sla_layernorm_backward(int64_t rows, int64_t width, int32_t d
     return e == cudaSuccess ? SLA_OK : fail(e);
   }
   if (!dx && !sums) return SLA_OK;
-  const bool vec = vec_rows(dy, width, lddy, dtype) && vec_rows(x, width, ldx, dtype) &&
-                   vec_rows(dx, width, width, dtype) && aligned(weight, 16);
+  const bool one = rows == 1;  // a single row has no distance to the next
+  const LnPlan pl = ln_plan(width, dtype, {{x, one ? width : ldx}, {dy, one ? width : lddy}, {dx, width}});
   const cudaError_t e = by_type(dtype, param_dtype, [&](auto t, auto p) {
-    return backward<decltype(t), decltype(p)>(rows, width, vec, dy, lddy, x, ldx, weight, mean, rstd, dx, dweight,
+    return backward<decltype(t), decltype(p)>(rows, width, pl, dy, lddy, x, ldx, weight, mean, rstd, dx, dweight,
                                               dbias, sums ? (float *)workspace : nullptr, st);
   });
   if (e != cudaSuccess) return fail(e);

@@ -109,21 +109,6 @@ __device__ __forceinline__ Sector load_sector(const void *p) {
   return s;
 }
 
-__device__ __forceinline__ uint32_t pair16(float a, float b, f16) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t pair16(float a, float b, bf16) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 unpair16(uint32_t w, f16) {
-  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-__device__ __forceinline__ float2 unpair16(uint32_t w, bf16) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
-}
-
 // N values of a row as an operand of a later product: one sheet of T, or float32's three.
 template <typename T, int N>
 __device__ __forceinline__ void store_operand(uint16_t *p, int64_t sheet, const float (&v)[N], int count, bool vec) {

@@ -517,7 +517,7 @@ SLA_API sla_status sla_cg_solve_static(const sla_csr *A, const void *b, const vo
  * `width` elements (1 <= width <= 2^24; var is the mean of squared deviations).
  *   param_dtype    type of weight and bias: dtype or SLA_F32
  *   weight, bias   device, [width] or NULL (1 and 0)
- *   mean, rstd     device, [rows] float32 or NULL: the rows' statistics, for the backward call
+ *   mean, rstd     device, [rows] float32, or both NULL: the rows' statistics, for the backward call
  * A NaN or an infinity in a row makes that row NaN and leaves the others alone.  rows = 0 writes nothing.
  */
 SLA_API sla_status sla_layernorm(int64_t rows, int64_t width, int32_t dtype, int32_t param_dtype, const void *x,
