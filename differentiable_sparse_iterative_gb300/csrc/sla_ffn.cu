@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "sla_common.cuh"
+#include "sla_few.cuh"
 #include "sla_host.h"
 #include "sla_net.cuh"
 #include "sla_product.cuh"
@@ -501,6 +502,20 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
   const ForwardScratch w = forward_scratch(f, ws);
   const int64_t ldg = hidden_pitch(f);
   void *h = saved ? saved + L.h : w.h;
+  if (f->tokens <= kFewTokens) {
+    FewArgs p{};
+    p.tokens = (int)f->tokens, p.n = (int)f->hidden, p.k = (int)f->width, p.act = f->activation;
+    p.x = x, p.ldx = ldx, p.w = w_in, p.bias = b_in;
+    p.x_vec = aligned(x, 16) && (f->tokens == 1 || ldx % 8 == 0), p.w_vec = aligned(w_in, 16) && f->width % 8 == 0;
+    p.g = saved, p.u = saved ? saved + L.u : nullptr, p.h = (uint16_t *)h, p.ldg = ldg, p.sheet = f->tokens * ldg;
+    c.launched(launch_few<T>(kGate, p, st));
+    FewArgs q{};
+    q.tokens = (int)f->tokens, q.n = (int)f->out, q.k = (int)f->hidden;
+    q.x = h, q.ldx = ldg, q.x_sheet = p.sheet, q.x_vec = 1, q.w = w_out, q.bias = b_out;
+    q.w_vec = aligned(w_out, 16) && f->hidden % 8 == 0, q.c = y;
+    c.launched(launch_few<T>(kStore, q, st));
+    return finish(c);
+  }
   const Operand ox = as_operand(c, x, f->tokens, f->width, ldx, 1, w.x);
   const Operand oi = as_operand(c, w_in, f->hidden, f->width, f->width, 2, w.w_in);
   const Operand oo = as_operand(c, w_out, f->out, f->hidden, f->hidden, 1, w.w_out);

@@ -18,6 +18,8 @@
 // take tiles in bands of kBand tile rows, so that what the running blocks read stays in L2.
 #pragma once
 
+#include <atomic>
+
 #include "sla_act.cuh"
 #include "sla_net.cuh"
 #include "sla_tc.cuh"
@@ -590,7 +592,14 @@ cudaError_t launch_product_as(int blocks, const CUtensorMap &a, const CUtensorMa
                               cudaStream_t st) {
   constexpr int smem = ProductShape<CG, BN>::smem;
   auto kernel = product_kernel<T, EPI, CG, BN>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // once per device: the attribute stays with the loaded kernel
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !(allowed.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) allowed.fetch_or(1ull << (dev & 63));
+  }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks);

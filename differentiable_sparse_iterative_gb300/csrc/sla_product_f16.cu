@@ -1,4 +1,5 @@
-// The tensor-core products of sla_product.cuh for f16 data.
+// The tensor-core products of sla_product.cuh and sla_few.cuh for f16 data.
+#include "sla_few.cuh"
 #include "sla_product.cuh"
 
 namespace sla {
@@ -12,6 +13,11 @@ cudaError_t launch_product<f16>(int epi, int shape, int blocks, const CUtensorMa
     case kGateBack: return launch_product_shape<f16, kGateBack>(shape, blocks, a, b, p, st);
     default: return launch_product_shape<float, kPartial>(shape, blocks, a, b, p, st);
   }
+}
+
+template <>
+cudaError_t launch_few<f16>(Epilogue epi, const FewArgs &p, cudaStream_t st) {
+  return epi == kGate ? launch_few_gate<f16, true>(p, st) : launch_few_gate<f16, false>(p, st);
 }
 
 }  // namespace sla
