@@ -5,50 +5,140 @@
 //   gelu_tanh  a = g (1 + t) / 2,  a' = (1 + t) / 2 + g (1 - t^2) z' / 2,  t = tanh z, z = sqrt(2/pi) (g + 0.044715 g^3)
 //   relu       a = max(g, 0),      a' = [g > 0]
 //
-// Fast: the hardware's approximate exponential and division, for data of 16 bits (their error of
-// a few 2^-22 disappears in the rounding to 2^-9 or 2^-12); float32 data takes expf, erff, tanhf.
+// float32 data takes expf, erff and tanhf, one value at a time (activate).  16-bit data takes pairs of
+// values (activate2): packed float32 arithmetic, the approximate exponential and reciprocal (their
+// errors of a few 2^-22 disappear in the rounding to 2^-9 or 2^-12), one reciprocal for both sigmoids of
+// a pair, and for gelu the normal distribution by Abramowitz and Stegun 7.1.26 (1.5e-7), whose
+// exponential is the density's too.  The special function unit gives 16 results a clock, so a
+// sigmoid's exponential and reciprocal are what the epilogues of narrow products wait for: one
+// reciprocal less for a pair is worth the multiplications.
 #pragma once
 
 #include <cuda_runtime.h>
 
 #include <type_traits>
 
-#include "sla.h"
+#include "sla_net.cuh"
 
 namespace sla {
-
-template <bool Fast>
-__device__ __forceinline__ float sigmoid(float g) {
-  return Fast ? __fdividef(1.f, 1.f + __expf(-g)) : 1.f / (1.f + expf(-g));
-}
-
-// 1 - 2 / (1 + e^2z): 1 and -1 at the ends, where e^2z is infinite or zero
-template <bool Fast>
-__device__ __forceinline__ float tanh_of(float z) {
-  return Fast ? 1.f - 2.f * sigmoid<true>(-2.f * z) : tanhf(z);
-}
 
 struct ActValue {
   float a, da;
 };
 
-template <int Act, bool Fast>
+template <int Act>
 __device__ __forceinline__ ActValue activate(float g) {
   if constexpr (Act == SLA_ACT_SILU) {
-    const float s = sigmoid<Fast>(g);
+    const float s = 1.f / (1.f + expf(-g));
     return {g * s, s * (1.f + g * (1.f - s))};
   } else if constexpr (Act == SLA_ACT_GELU) {
     const float phi = 0.5f * (1.f + erff(g * 0.7071067811865476f));
-    const float e = Fast ? __expf(-0.5f * g * g) : expf(-0.5f * g * g);
-    return {g * phi, phi + g * e * 0.3989422804014327f};
+    return {g * phi, phi + g * expf(-0.5f * g * g) * 0.3989422804014327f};
   } else if constexpr (Act == SLA_ACT_GELU_TANH) {
-    const float z = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-    const float t = tanh_of<Fast>(z);
+    const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
     return {0.5f * g * (1.f + t), 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * 0.7978845608028654f *
                                                           (1.f + 3.f * 0.044715f * g * g)};
   } else {
     // written so that a NaN stays one
     return {g < 0.f ? 0.f : g, g > 0.f ? 1.f : 0.f};
+  }
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / (1 + 2^m) of both, m held below 86 (2^-86 for less): each denominator stays finite, so a pair whose
+// product is infinite gives two zeros and never infinity times zero.  NaN goes in as 86: callers
+// multiply by the value it came from.
+__device__ __forceinline__ float2 sigmoid2(float2 m) {
+  const float2 d = add2(f2(ex2_approx(fminf(m.x, 86.f)), ex2_approx(fminf(m.y, 86.f))), f2(1.f, 1.f));
+  const float r = rcp_approx(d.x * d.y);
+  return mul2(f2(d.y, d.x), f2(r, r));
+}
+
+// The activation of a pair; da: also its derivative.
+template <int Act, bool Derivative>
+__device__ __forceinline__ void activate2(float2 g, float2 &a, float2 &da) {
+  const float2 one = f2(1.f, 1.f);
+  if constexpr (Act == SLA_ACT_SILU) {
+    const float2 s = sigmoid2(mul2(g, f2(-1.4426950408889634f, -1.4426950408889634f)));
+    a = mul2(g, s);
+    if (Derivative) da = fma2(a, fma2(s, f2(-1.f, -1.f), one), s);  // s + a (1 - s)
+  } else if constexpr (Act == SLA_ACT_GELU) {
+    const float2 x = f2(fabsf(g.x), fabsf(g.y));
+    const float2 den = fma2(x, f2(0.3275911f * 0.7071067811865476f, 0.3275911f * 0.7071067811865476f), one);
+    const float2 t = f2(rcp_approx(den.x), rcp_approx(den.y));
+    float2 q = fma2(t, f2(1.061405429f, 1.061405429f), f2(-1.453152027f, -1.453152027f));
+    q = fma2(q, t, f2(1.421413741f, 1.421413741f));
+    q = fma2(q, t, f2(-0.284496736f, -0.284496736f));
+    q = fma2(q, t, f2(0.254829592f, 0.254829592f));
+    const float2 m = mul2(mul2(g, g), f2(-0.7213475204444817f, -0.7213475204444817f));
+    const float2 e = f2(ex2_approx(m.x), ex2_approx(m.y));
+    q = mul2(mul2(q, t), mul2(e, f2(0.5f, 0.5f)));  // 1 - Phi(|g|)
+    const float2 phi = f2(g.x < 0.f ? q.x : 1.f - q.x, g.y < 0.f ? q.y : 1.f - q.y);
+    a = mul2(g, phi);
+    if (Derivative) da = fma2(mul2(g, e), f2(0.3989422804014327f, 0.3989422804014327f), phi);
+  } else if constexpr (Act == SLA_ACT_GELU_TANH) {
+    // (1 + tanh z) / 2 = 1 / (1 + e^-2z);  with s that: 1 - t^2 = 4 s (1 - s)
+    constexpr float c = 0.7978845608028654f, k = -2.f * 1.4426950408889634f * c;
+    const float2 gg = mul2(g, g);
+    const float2 s = sigmoid2(mul2(g, fma2(gg, f2(k * 0.044715f, k * 0.044715f), f2(k, k))));
+    a = mul2(g, s);
+    if (Derivative) {
+      const float2 dz = fma2(gg, f2(2.f * c * 3.f * 0.044715f, 2.f * c * 3.f * 0.044715f), f2(2.f * c, 2.f * c));
+      da = fma2(mul2(a, dz), fma2(s, f2(-1.f, -1.f), one), s);
+    }
+  } else {
+    a = f2(g.x < 0.f ? 0.f : g.x, g.y < 0.f ? 0.f : g.y);
+    da = f2(g.x > 0.f ? 1.f : 0.f, g.y > 0.f ? 1.f : 0.f);
+  }
+}
+
+// v = act(v) * u;  16-bit data (Fast) in pairs.
+template <int Act, bool Fast, int N>
+__device__ __forceinline__ void gate_values(float (&v)[N], const float (&u)[N]) {
+  if constexpr (Fast && N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float2 a, da;
+      activate2<Act, false>(f2(v[i], v[i + 1]), a, da);
+      a = mul2(a, f2(u[i], u[i + 1]));
+      v[i] = a.x, v[i + 1] = a.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = activate<Act>(v[i]).a * u[i];
+  }
+}
+
+// From v = dh:  g = dg = dh u act'(g),  u = du = dh act(g).
+template <int Act, bool Fast, int N>
+__device__ __forceinline__ void gate_gradients(const float (&v)[N], float (&g)[N], float (&u)[N]) {
+  if constexpr (Fast && N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float2 a, da;
+      const float2 dh = f2(v[i], v[i + 1]);
+      activate2<Act, true>(f2(g[i], g[i + 1]), a, da);
+      da = mul2(mul2(dh, f2(u[i], u[i + 1])), da);
+      a = mul2(dh, a);
+      g[i] = da.x, g[i + 1] = da.y, u[i] = a.x, u[i + 1] = a.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const ActValue a = activate<Act>(g[i]);
+      g[i] = v[i] * u[i] * a.da;
+      u[i] = v[i] * a.a;
+    }
   }
 }
 

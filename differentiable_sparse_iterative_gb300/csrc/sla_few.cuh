@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
         ((T *)p.g)[o] = from_f32<T>(v);
         ((T *)p.u)[o] = from_f32<T>(u);
       }
-      float a[1];
-      with_activation(p.act, [&](auto act) { a[0] = activate<act.value, sizeof(T) == 2>(v).a * u; });
+      float a[1] = {v}, b[1] = {u};
+      with_activation(p.act, [&](auto act) { gate_values<act.value, sizeof(T) == 2, 1>(a, b); });
       store_operand<T, 1>(p.h + o, p.sheet, a, 1, false);
     } else {
       ((T *)p.c)[token * (int64_t)p.n + r] = from_f32<T>(v);

@@ -240,33 +240,30 @@ __global__ void __launch_bounds__(256) finish_splits(ProductArgs p, const float 
       continue;
     }
     const int64_t o = row * p.ldg + col;
+    if (EPI == kGate) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k >= count) break;
-      if (EPI == kGate) {
-        float g = v[k], up = u[k];
+      for (int k = 0; k < 4; ++k) {
+        if (k >= count) break;
         if (p.bias) {
-          g += to_f32(((const T *)p.bias)[col + k]);
-          up += to_f32(((const T *)p.bias)[p.n + col + k]);
+          v[k] += to_f32(((const T *)p.bias)[col + k]);
+          u[k] += to_f32(((const T *)p.bias)[p.n + col + k]);
         }
         if (p.g) {
-          ((T *)p.g)[o + k] = from_f32<T>(g);
-          ((T *)p.u)[o + k] = from_f32<T>(up);
+          ((T *)p.g)[o + k] = from_f32<T>(v[k]);
+          ((T *)p.u)[o + k] = from_f32<T>(u[k]);
         }
-        with_activation(p.act, [&](auto act) { v[k] = activate<act.value, fast>(g).a * up; });
-      } else {
-        const float g = to_f32(((const T *)p.g)[o + k]), up = to_f32(((const T *)p.u)[o + k]);
-        with_activation(p.act, [&](auto act) {
-          const ActValue a = activate<act.value, fast>(g);
-          u[k] = v[k] * a.a;
-          v[k] = v[k] * up * a.da;
-        });
       }
-    }
-    if (EPI == kGate) {
+      with_activation(p.act, [&](auto act) { gate_values<act.value, fast, 4>(v, u); });
       store_operand<T, 4>(p.h + o, p.sheet, v, count, false);
     } else {
-      store_operand<T, 4>(p.h + o, 2 * p.sheet, v, count, false);
+      float g[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        g[k] = k < count ? to_f32(((const T *)p.g)[o + k]) : 0.f;
+        u[k] = k < count ? to_f32(((const T *)p.u)[o + k]) : 0.f;
+      }
+      with_activation(p.act, [&](auto act) { gate_gradients<act.value, fast, 4>(v, g, u); });
+      store_operand<T, 4>(p.h + o, 2 * p.sheet, g, count, false);
       store_operand<T, 4>(p.h + p.sheet + o, 2 * p.sheet, u, count, false);
     }
   }

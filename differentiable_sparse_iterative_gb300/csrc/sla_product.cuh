@@ -514,10 +514,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
               store_row<T, N>((T *)p.g + o, v, count, p.vec);
               store_row<T, N>((T *)p.u + o, u, count, p.vec);
             }
-            with_activation(p.act, [&](auto act) {
-#pragma unroll
-              for (int i = 0; i < N; ++i) v[i] = activate<act.value, fast>(v[i]).a * u[i];
-            });
+            with_activation(p.act, [&](auto act) { gate_values<act.value, fast, N>(v, u); });
             store_operand<T, N>(p.h + o, p.sheet, v, count, p.vec);
           }
         } else if constexpr (EPI == kGateBack) {
@@ -529,14 +526,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
           tmem_wait(v);
           if (c + N >= (side + 1) * width) release();
           if (live && count > 0) {
-            with_activation(p.act, [&](auto act) {
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const ActValue a = activate<act.value, fast>(g[i]);
-                g[i] = v[i] * u[i] * a.da;
-                u[i] = v[i] * a.a;
-              }
-            });
+            with_activation(p.act, [&](auto act) { gate_gradients<act.value, fast, N>(v, g, u); });
             // sheets: dg and du of each part of the value
             store_operand<T, N>(p.h + o, 2 * p.sheet, g, count, p.vec);
             store_operand<T, N>(p.h + p.sheet + o, 2 * p.sheet, u, count, p.vec);
