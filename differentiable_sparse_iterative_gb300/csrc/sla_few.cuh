@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
   int turn = rank * kFewWarps + warp;
   ask(turn);
   if (Gate)
-    asm volatile("griddepcontrol.launch_dependents;");
+    grid_dependency_launch();
   else
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_dependency_wait();
 
   float acc[M][NT][4] = {};
   for (; turn < turns; turn += kFewTurns * stride) {
@@ -242,27 +242,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
 template <typename T, bool Gate, int NT>
 cudaError_t launch_few_as(const FewArgs &p, int ranks, cudaStream_t st) {
   constexpr int per = (Gate ? 2 : 1) * 16 * 8 * NT;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((p.n + 15) / 16 * ranks);
-  cfg.blockDim = dim3(32 * kFewWarps);
-  cfg.dynamicSmemBytes = (kFewWarps + 1) * per * sizeof(float);
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  int n = 0;
-  if (ranks > 1) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = ranks;
-    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  if (!Gate) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  cfg.attrs = at;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, few_kernel<T, Gate, NT>, p, ranks);
+  LaunchConfig cfg(dim3((p.n + 15) / 16 * ranks), 32 * kFewWarps, (kFewWarps + 1) * per * sizeof(float), st, !Gate, ranks);
+  return cudaLaunchKernelEx(&cfg.c, few_kernel<T, Gate, NT>, p, ranks);
 }
 
 template <typename T, bool Gate>

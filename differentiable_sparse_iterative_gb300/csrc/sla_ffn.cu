@@ -76,26 +76,42 @@ cudaError_t encode(CUtensorMap *map, const Operand &o, int box_rows, bool f16) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// dst[sheet * S + .]: the matrix with rows padded to ld (zeros), float32 split into three sheets.  One thread
-// moves eight columns.  sheets of src (halves) lie `src_sheet` apart; sheet q of half i goes to q * halves + i.
+// Up to four matrices laid out for TMA in one launch: rows padded to ld (zeros), float32 split into three
+// sheets.  Halves of src lie src_half apart; part q of half i becomes sheet q * halves + i.
+struct PackJob {
+  const void *src;
+  uint16_t *dst;
+  int64_t rows, cols, src_ld, src_half, ld;
+  int halves, vec, first, blocks;  // its blocks of the grid
+};
+
+struct PackJobs {
+  PackJob job[4];
+  int count = 0, blocks = 0;
+};
+
+// A thread moves eight columns at a time.
 template <typename T>
-__global__ void __launch_bounds__(256) pack_operand(int64_t rows, int64_t cols, int halves, const T *__restrict__ src,
-                                                    int64_t src_ld, int64_t src_half, int vec,
-                                                    uint16_t *__restrict__ dst, int64_t ld) {
-  const int64_t chunks = ld / 8, total = halves * rows * chunks, sheet = rows * ld;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+__global__ void __launch_bounds__(256) pack_operands(const __grid_constant__ PackJobs jobs) {
+  grid_dependency_wait();
+  grid_dependency_launch();
+  int which = 0;
+  while (which + 1 < jobs.count && (int)blockIdx.x >= jobs.job[which + 1].first) ++which;
+  const PackJob &j = jobs.job[which];
+  const int64_t chunks = j.ld / 8, total = j.halves * j.rows * chunks, sheet = j.rows * j.ld;
+  for (int64_t i = (blockIdx.x - j.first) * 256ll + threadIdx.x; i < total; i += j.blocks * 256ll) {
     const int64_t c = i % chunks * 8, hr = i / chunks;
-    const int64_t half = hr / rows, r = hr - half * rows;
+    const int64_t half = hr / j.rows, r = hr - half * j.rows;
     float v[8];
-    const T *s = src + half * src_half + r * src_ld + c;
-    const int count = (int)(cols - c < 8 ? cols - c : 8);
-    if (vec && count == 8) {
+    const T *s = (const T *)j.src + half * j.src_half + r * j.src_ld + c;
+    const int count = (int)(j.cols - c < 8 ? j.cols - c : 8);
+    if (j.vec && count == 8) {
       load_f32<T, 8>(s, v);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = k < count ? to_f32(s[k]) : 0.f;
     }
-    store_operand<T, 8>(dst + half * sheet + r * ld + c, halves * sheet, v, 8, true);
+    store_operand<T, 8>(j.dst + half * sheet + r * j.ld + c, j.halves * sheet, v, 8, true);
   }
 }
 
@@ -126,26 +142,44 @@ struct Call {
   cudaError_t err = cudaSuccess;
   uint64_t launches = 0;
   uint32_t *timeouts = nullptr;
+  // the kernels after a call's first may be made ready while the one before them runs
+  bool early() const { return launches > 0; }
+  template <typename... P, typename... A>
+  void launch(void (*kernel)(P...), dim3 grid, int block, A &&...args) {
+    if (err != cudaSuccess) return;
+    LaunchConfig cfg(grid, block, 0, st, early());
+    launched(cudaLaunchKernelEx(&cfg.c, kernel, P(args)...));
+  }
   void launched(cudaError_t e) {
     ++launches;
     if (err == cudaSuccess) err = e;
   }
 };
 
-// The matrix as an operand: in place where TMA can read it, else packed into `to`.
+// The matrix as an operand: in place where TMA can read it, else a job to pack it into `to` (or, where an
+// earlier call did that, from there).
 template <typename T>
-Operand as_operand(Call &c, const T *src, int64_t rows, int64_t cols, int64_t ld, int halves, void *to) {
-  const int64_t half = rows * ld;                          // between the halves of src
+Operand as_operand(PackJobs &jobs, const T *src, int64_t rows, int64_t cols, int64_t ld, int halves, void *to,
+                   bool packed = false) {
+  const int64_t half = rows * ld;                        // between the halves of src
   if (rows == 1 && halves == 1) ld = round_up(cols, 8);  // a single row has no distance to the next
-  if (sizeof(T) == 2 && tma_ready(src, ld) && (halves == 1 || half % 8 == 0))
+  if (!packed && sizeof(T) == 2 && tma_ready(src, ld) && (halves == 1 || half % 8 == 0))
     return {src, cols, rows, halves, ld, rows * ld};
   const int64_t pitch = round_up(cols, 8);
-  const int64_t work = halves * rows * (pitch / 8);
-  const int vec = aligned(src, 16) && ld * sizeof(T) % 16 == 0;
-  pack_operand<T><<<(unsigned)std::min<int64_t>((work + 255) / 256, 152 * 32), 256, 0, c.st>>>(
-      rows, cols, halves, src, ld, half, vec, (uint16_t *)to, pitch);
-  c.launched(cudaGetLastError());
+  if (!packed) {
+    PackJob &j = jobs.job[jobs.count++];
+    j.src = src, j.dst = (uint16_t *)to, j.rows = rows, j.cols = cols, j.src_ld = ld, j.src_half = half, j.ld = pitch;
+    j.halves = halves, j.vec = aligned(src, 16) && ld * sizeof(T) % 16 == 0;
+    j.first = jobs.blocks;
+    j.blocks = (int)std::min<int64_t>((halves * rows * (pitch / 8) + 255) / 256, 152 * 16);
+    jobs.blocks += j.blocks;
+  }
   return {to, cols, rows, (int64_t)sheets_of<T>() * halves, pitch, rows * pitch};
+}
+
+template <typename T>
+void run_packs(Call &c, const PackJobs &jobs) {
+  if (jobs.count) c.launch(pack_operands<T>, dim3(jobs.blocks), 256, jobs);
 }
 
 // ------------------------------------------------------------------ plans
@@ -154,73 +188,105 @@ Operand as_operand(Call &c, const T *src, int64_t rows, int64_t cols, int64_t ld
 // core drops up to one unit of the running sum for every 16 products (2048 / 16 * 2^-24 * 2/3 = 5e-6 in all).
 constexpr int kFloatBlocks = 2048 / kDepth;
 
-struct ProductPlan {
-  int shape, splits;
-  size_t partial_bytes;
-};
-
 struct ProductSize {
   int64_t m, n, k;           // of one half, of one segment
   int m_halves, n_halves, k_halves;
 };
 
-// The tile shape and split with the least predicted time: rounds of tiles over the multiprocessors, each
-// its k blocks and a fixed cost (first loads, last epilogue), plus writing and reading a split's sums.
-// A k block (64 deep) measured 0.27 us with the 256 x 256 tile, where the tensor core is the limit, and
-// 0.22 to 0.26 us with the smaller ones, where it is the 64 bytes a clock that a multiprocessor takes in
-// from L2; pairs of blocks start 2 us later than single ones.
-ProductPlan plan_product(const ProductSize &s, int sheets, bool gate) {
-  const int64_t kb = (s.k + kDepth - 1) / kDepth;
-  const int64_t deepest = sheets == 3 ? std::max(1, kFloatBlocks / s.k_halves) : kb;
-  const int64_t least = (kb + deepest - 1) / deepest;
-  const int sms = sm_count();
+// Tile shape and splits of the products of one launch.
+struct ProductPlan {
+  int shape;
+  int splits[kGroup];
+  size_t partial[kGroup + 1];  // where each product's split sums start, and their end
+};
+
+// The tile shape and splits with the least predicted time.  Workers (multiprocessors, or pairs) take the
+// items in turn, each of which costs its k blocks or its epilogue, whichever is longer; splits cost writing
+// and reading their sums and a launch.  Measured: a k block (64 deep) 0.27 us with the 256 x 256 tile, where
+// the tensor core is the limit, and 0.22 to 0.26 us with the smaller ones, where it is the 64 bytes a clock
+// that a multiprocessor takes in from L2; pairs of blocks start 2 us later than single ones.
+ProductPlan plan_products(Epilogue epi, const ProductSize *s, int count, int sheets) {
   static const double block_us[kProductTileCount] = {0.27, 0.225, 0.255, 0.245};
   static const double start_us[kProductTileCount] = {5.0, 5.0, 3.0, 3.0};
-  const double per_block = s.k_halves * (sheets == 3 ? 6 : 1);
-  ProductPlan best{0, 1, 0};
+  static const double epilogue_us[3][kProductTileCount] = {
+      {2.1, 1.25, 1.25, 0.8}, {3.4, 1.8, 1.8, 1.15}, {11.0, 5.9, 5.9, 3.4}};  // kStore, kGate, kGateBack
+  const int sms = sm_count();
+  ProductPlan best{};
   double best_us = 1e30;
   for (int i = 0; i < kProductTileCount; ++i) {
     const int64_t bm = 128 * kProductTiles[i].cg, bn = kProductTiles[i].bn, workers = sms / kProductTiles[i].cg;
-    const int64_t mt = s.m_halves * ((s.m + bm - 1) / bm);
-    // whole; as many splits as fill the workers once, or twice
-    const int64_t plain = std::max<int64_t>(1, mt * (gate ? 2 : s.n_halves) * ((s.n + bn - 1) / bn));
-    for (int64_t want : {(int64_t)1, workers / plain, 2 * workers / plain}) {
-      const int64_t splits = std::min(std::max(want, least), kb);
-      // columns of a split gate product are summed as plain ones, g's and u's in halves
-      const int halves = gate && splits > 1 ? 2 : s.n_halves;
-      const int64_t cols = gate && splits == 1 ? bn / 2 : bn;
-      const int64_t items = mt * halves * ((s.n + cols - 1) / cols) * splits;
-      const int64_t rounds = (items + workers - 1) / workers;
-      double us = start_us[i] + rounds * (((kb + splits - 1) / splits) * per_block * block_us[i] + 1.5);
-      if (splits > 1) {
-        const double bytes = 4.0 * s.m * s.m_halves * (double)round_up(s.n, 16) * halves * splits;
-        us += 4.0 + 2.0 * bytes / 5e6;
+    int64_t tiles[kGroup], kb[kGroup], least[kGroup];
+    double per[kGroup], blocks = 0;
+    for (int j = 0; j < count; ++j) {
+      kb[j] = (s[j].k + kDepth - 1) / kDepth;
+      per[j] = s[j].k_halves * (sheets == 3 ? 6 : 1);
+      const int64_t deepest = sheets == 3 ? std::max(1, kFloatBlocks / s[j].k_halves) : kb[j];
+      least[j] = (kb[j] + deepest - 1) / deepest;
+      // columns of g and of u make separate tiles when their product is split
+      tiles[j] = s[j].m_halves * ((s[j].m + bm - 1) / bm) * (epi == kGate ? 2 : s[j].n_halves) * ((s[j].n + bn - 1) / bn);
+      blocks += tiles[j] * kb[j] * per[j];
+    }
+    for (int fill = 0; fill < 3; ++fill) {  // whole; as many items as workers; twice as many
+      ProductPlan plan{i, {}, {}};
+      double busy = 0, us = start_us[i], longest = 0;
+      bool split = false;
+      int64_t items = 0;
+      size_t partial = 0;
+      for (int j = 0; j < count; ++j) {
+        int64_t n = least[j], t = tiles[j];
+        if (fill) n = std::max(n, (int64_t)(kb[j] * per[j] * fill * workers / std::max(1.0, blocks)));
+        n = std::min(n, kb[j]);
+        if (epi == kGate && n == 1)
+          t = s[j].m_halves * ((s[j].m + bm - 1) / bm) * ((s[j].n + bn / 2 - 1) / (bn / 2));
+        const double main = (kb[j] + n - 1) / n * per[j] * block_us[i], end = epilogue_us[n > 1 ? kStore : epi][i];
+        plan.splits[j] = (int)n;
+        plan.partial[j] = partial;
+        if (n > 1) {
+          const int halves = epi == kGate ? 2 : s[j].n_halves;
+          partial += align256(4 * (size_t)(s[j].m * s[j].m_halves) * (size_t)(round_up(s[j].n, 16) * halves) * n);
+          split = true;
+        }
+        // rounds of this product's items, a partial round shared with the next product's
+        const double rounds = count > 1 ? (double)(t * n) / workers : (double)((t * n + workers - 1) / workers);
+        busy += rounds * std::max(main, end);
+        longest = std::max(longest, std::max(main, end));
+        us += j == 0 ? std::min(main, end) : 0;
+        items += t * n;
       }
+      plan.partial[count] = partial;
+      us += count > 1 ? std::max(longest, busy + (items > workers ? 0.5 * longest : 0)) : busy;
+      if (split) us += 4.0 + 2.0 * partial / 5e6;
       if (us < best_us) {
         best_us = us;
-        best = {i, (int)splits, 0};
+        best = plan;
       }
     }
-  }
-  if (best.splits > 1) {
-    const int halves = gate ? 2 : s.n_halves;
-    best.partial_bytes = align256(4 * (size_t)(s.m * s.m_halves) * (size_t)(round_up(s.n, 16) * halves) * best.splits);
   }
   return best;
 }
 
 // ------------------------------------------------------------------ sums of splits
 
-// The epilogue of a product whose k was split: sums the parts in order, four columns a thread.
+struct SplitSums {
+  ProductArgs p[kGroup];  // c: the result; ldc, c_n_half, c_split: of the sums
+  const float *parts[kGroup];
+  int64_t rows[kGroup];
+};
+
+// The epilogue of products whose k was split (blockIdx.y: which): adds the parts in order, four columns a thread.
 template <typename T, int EPI>
-__global__ void __launch_bounds__(256) finish_splits(ProductArgs p, const float *__restrict__ parts, int64_t rows) {
-  const int64_t chunks = (p.n + 3) / 4, total = rows * chunks;
+__global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ SplitSums f) {
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const ProductArgs &p = f.p[blockIdx.y];
+  const int64_t chunks = (p.n + 3) / 4, total = f.rows[blockIdx.y] * chunks;
   constexpr bool fast = sizeof(T) == 2;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int64_t row = i / chunks;
     const int col = (int)(i - row * chunks) * 4, count = p.n - col;
-    const float *src = parts + row * p.ldc + col;
+    const float *src = f.parts[blockIdx.y] + row * p.ldc + col;
     float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
       float t[4];
       load_f32<float, 4>(src + s * p.c_split, t);
@@ -236,7 +302,14 @@ __global__ void __launch_bounds__(256) finish_splits(ProductArgs p, const float 
       T *out = (T *)p.c + row * (int64_t)p.n + col;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (k < count) out[k] = from_f32<T>(v[k] + (p.bias ? to_f32(((const T *)p.bias)[col + k]) : 0.f));
+        if (p.bias && k < count) v[k] += to_f32(((const T *)p.bias)[col + k]);
+      if (p.vec && count >= 4) {
+        store_f32<T, 4>(out, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < count) out[k] = from_f32<T>(v[k]);
+      }
       continue;
     }
     const int64_t o = row * p.ldg + col;
@@ -270,61 +343,99 @@ __global__ void __launch_bounds__(256) finish_splits(ProductArgs p, const float 
 }
 
 // One product: A(m, k) and B(n, k) with their majors, and the epilogue's arrays in `p`.
+struct ProductJob {
+  ProductSize s;
+  Operand a;
+  bool a_mn;
+  Operand b;
+  bool b_mn;
+  ProductArgs p;
+  bool wanted;
+};
+
+// Runs the wanted ones of up to kGroup products with the plan made for all of them (whose split sums `parts` holds).
 template <typename T>
-void run_product(Call &c, Epilogue epi, const ProductSize &s, const Operand &a, bool a_mn, const Operand &b, bool b_mn,
-                 ProductArgs p, float *parts) {
+void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, float *parts) {
   if (c.err != cudaSuccess) return;
   constexpr int S = sheets_of<T>();
-  const ProductPlan plan = plan_product(s, S, epi == kGate);
+  ProductSize sizes[kGroup];
+  for (int j = 0; j < count; ++j) sizes[j] = jobs[j].s;
+  const ProductPlan plan = plan_products(epi, sizes, count, S);
   const ProductTile tile = kProductTiles[plan.shape];
-  const bool split = plan.splits > 1;
   const int bm = 128 * tile.cg, bn = tile.bn;
-  const bool gate = epi == kGate && !split;
-  p.m = (int)s.m, p.n = (int)s.n;
-  p.m_halves = s.m_halves, p.n_halves = epi == kGate && split ? 2 : s.n_halves;
-  const int cols = gate ? bn / 2 : bn;
-  p.m_tiles = (int)((s.m + bm - 1) / bm), p.n_tiles = (int)((s.n + cols - 1) / cols);
-  p.k_blocks = (int)((s.k + kDepth - 1) / kDepth);
-  p.splits = plan.splits;
-  p.a_mn = a_mn, p.b_mn = b_mn, p.f16 = sizeof(T) == 2 && NetType<T>::dtype == SLA_F16;
-  p.timeouts = c.timeouts;
-  // sheets: part q of the value, in pairs where A (B) has halves of rows, of columns or of k
-  const int a_pair = s.m_halves * s.k_halves, b_pair = (epi == kGate ? 2 : s.n_halves) * s.k_halves;
-  static const int8_t order[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
-  p.segments = 0;
-  for (int q = S == 3 ? 0 : 5; q < 6; ++q)
-    for (int h = 0; h < s.k_halves; ++h) {
-      p.a_sheet[p.segments] = (int8_t)(order[q][0] * a_pair + h);
-      p.b_sheet[p.segments++] = (int8_t)(order[q][1] * b_pair + h);
+  // items with the most k blocks first, so that the last round is one of short ones
+  int order[kGroup] = {0, 1, 2};
+  auto depth = [&](int j) {
+    return (double)jobs[j].s.k * jobs[j].s.k_halves / plan.splits[j];
+  };
+  std::stable_sort(order, order + count, [&](int x, int y) { return depth(x) > depth(y); });
+  ProductLaunch l;
+  l.count = 0;
+  l.first[0] = 0;
+  l.timeouts = c.timeouts;
+  SplitSums f;
+  int nsplit = 0;
+  int64_t items = 0, finish = 0;
+  for (int oi = 0; oi < count; ++oi) {
+    const int j = order[oi];
+    if (!jobs[j].wanted) continue;
+    const ProductSize &s = jobs[j].s;
+    const Operand &a = jobs[j].a, &b = jobs[j].b;
+    const bool split = plan.splits[j] > 1, gate = epi == kGate && !split;
+    ProductArgs &p = l.p[l.count];
+    p = jobs[j].p;
+    p.m = (int)s.m, p.n = (int)s.n;
+    p.m_halves = s.m_halves, p.n_halves = epi == kGate && split ? 2 : s.n_halves;
+    const int cols = gate ? bn / 2 : bn;
+    p.m_tiles = (int)((s.m + bm - 1) / bm), p.n_tiles = (int)((s.n + cols - 1) / cols);
+    p.k_blocks = (int)((s.k + kDepth - 1) / kDepth);
+    p.splits = plan.splits[j];
+    p.a_mn = jobs[j].a_mn, p.b_mn = jobs[j].b_mn, p.f16 = sizeof(T) == 2 && NetType<T>::dtype == SLA_F16;
+    // sheets: part q of the value, in pairs where A (B) has halves of rows, of columns or of k
+    const int a_pair = s.m_halves * s.k_halves, b_pair = (epi == kGate ? 2 : s.n_halves) * s.k_halves;
+    static const int8_t pairs[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
+    p.segments = 0;
+    for (int q = S == 3 ? 0 : 5; q < 6; ++q)
+      for (int h = 0; h < s.k_halves; ++h) {
+        p.a_sheet[p.segments] = (int8_t)(pairs[q][0] * a_pair + h);
+        p.b_sheet[p.segments++] = (int8_t)(pairs[q][1] * b_pair + h);
+      }
+    cudaError_t e = encode(&l.a[l.count], a, p.a_mn ? kDepth : 128, p.f16);
+    if (e == cudaSuccess) e = encode(&l.b[l.count], b, p.b_mn ? kDepth : gate ? bn / 2 : bn / tile.cg, p.f16);
+    if (e != cudaSuccess) {
+      c.err = e;
+      return;
     }
-  CUtensorMap ma, mb;
-  const bool f16 = p.f16;
-  cudaError_t e = encode(&ma, a, a_mn ? kDepth : 128, f16);
-  if (e == cudaSuccess) e = encode(&mb, b, b_mn ? kDepth : gate ? bn / 2 : bn / tile.cg, f16);
-  if (e != cudaSuccess) {
-    c.err = e;
-    return;
+    if (split) {
+      const int64_t ncols = round_up(s.n, 16) * p.n_halves, rows = s.m * s.m_halves;
+      float *to = parts + plan.partial[j] / sizeof(float);
+      ProductArgs &q = f.p[nsplit];
+      q = p;
+      q.ldc = p.ldc = ncols;
+      q.c_n_half = p.c_n_half = round_up(s.n, 16);
+      q.c_split = p.c_split = rows * ncols;
+      p.c_m_half = s.m * ncols;
+      p.c = to;
+      f.parts[nsplit] = to;
+      f.rows[nsplit++] = rows;
+      finish = std::max(finish, rows * ((s.n + 3) / 4));
+    }
+    items += (int64_t)p.m_halves * p.m_tiles * p.n_halves * p.n_tiles * p.splits;
+    l.first[++l.count] = (int)items;
   }
-  const int64_t items = (int64_t)p.m_halves * p.m_tiles * p.n_halves * p.n_tiles * p.splits;
+  if (!l.count) return;
+  // a split gate or gate-back product leaves plain sums
+  const int as = nsplit ? kStore : epi;
   const int blocks = (int)std::min<int64_t>(items, sm_count() / tile.cg) * tile.cg;
-  if (!split) {
-    c.launched(launch_product<T>(epi, plan.shape, blocks, ma, mb, p, c.st));
-    return;
-  }
-  ProductArgs q = p;
-  const int64_t ncols = round_up(s.n, 16) * p.n_halves, rows = s.m * s.m_halves;
-  q.c = parts, q.ldc = ncols, q.c_n_half = round_up(s.n, 16), q.c_m_half = s.m * ncols, q.c_split = rows * ncols;
-  q.vec = 1;
-  c.launched(launch_product<T>(kPartial, plan.shape, blocks, ma, mb, q, c.st));
-  p.ldc = ncols, p.c_n_half = q.c_n_half, p.c_split = q.c_split;
-  const unsigned grid = (unsigned)std::min<int64_t>((rows * ((s.n + 3) / 4) + 255) / 256, 152 * 16);
+  c.launched(launch_product<T>(as, plan.shape, blocks, l, c.early(), c.st));
+  if (!nsplit) return;
+  const dim3 grid((unsigned)std::min<int64_t>((finish + 255) / 256, 152 * 16), nsplit);
   if (epi == kStore)
-    finish_splits<T, kStore><<<grid, 256, 0, c.st>>>(p, parts, rows);
+    c.launch(finish_splits<T, kStore>, grid, 256, f);
   else if (epi == kGate)
-    finish_splits<T, kGate><<<grid, 256, 0, c.st>>>(p, parts, rows);
+    c.launch(finish_splits<T, kGate>, grid, 256, f);
   else
-    finish_splits<T, kGateBack><<<grid, 256, 0, c.st>>>(p, parts, rows);
-  c.launched(cudaGetLastError());
+    c.launch(finish_splits<T, kGateBack>, grid, 256, f);
 }
 
 // ------------------------------------------------------------------ column sums (bias gradients)
@@ -337,6 +448,8 @@ template <typename E, int S, int VEC>
 __global__ void __launch_bounds__(256) column_parts(int64_t rows, int64_t cols, const E *__restrict__ a, int64_t lda,
                                                     int64_t sheet, int tpr, int64_t per, float *__restrict__ parts) {
   __shared__ float sm[256 * VEC];
+  grid_dependency_wait();
+  grid_dependency_launch();
   const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = 256 / tpr;
   const int64_t c = (blockIdx.x * (int64_t)tpr + t) * VEC;
   const int64_t r0 = blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
@@ -368,6 +481,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) add_parts(int nparts, int64_t cols, int64_t pitch, int64_t n,
                                                  const float *__restrict__ parts, T *__restrict__ out) {
   __shared__ float sm[8][33];
+  grid_dependency_wait();
+  grid_dependency_launch();
   const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
   const int64_t c = blockIdx.x * 32ll + lane;
   float s = 0.f;
@@ -399,22 +514,23 @@ void column_sums(Call &c, int64_t rows, int64_t cols, const E *a, int64_t lda, i
   const int64_t per = std::max<int64_t>(8 * (256 / tpr), (rows + most - 1) / most);
   const int nparts = (int)((rows + per - 1) / per);
   const dim3 grid((unsigned)tiles, nparts);
-  if (vec)
-    column_parts<E, S, V><<<grid, 256, 0, c.st>>>(rows, cols, a, lda, sheet, tpr, per, parts);
-  else
-    column_parts<E, S, 1><<<grid, 256, 0, c.st>>>(rows, cols, a, lda, sheet, tpr, per, parts);
-  add_parts<T><<<(unsigned)((cols + 31) / 32), 256, 0, c.st>>>(nparts, cols, pitch, n, parts, out);
-  c.launched(cudaGetLastError());
-  c.launched(cudaSuccess);
+  c.launch(vec ? column_parts<E, S, V> : column_parts<E, S, 1>, grid, 256, rows, cols, a, lda, sheet, tpr, per, parts);
+  c.launch(add_parts<T>, dim3((unsigned)((cols + 31) / 32)), 256, nparts, cols, pitch, n, parts, out);
 }
 
 // ------------------------------------------------------------------ buffers
 
 int64_t hidden_pitch(const sla_ffn *f) { return round_up(f->hidden, 16); }
 
-// g, u (dtype) and h (operand sheets), rows hidden_pitch apart.
+// Whether a forward call leaves its packed copy of a matrix with this many columns to the backward call:
+// where TMA can never read the original.  (One that is only misaligned is packed by each call.)
+bool keeps_packed(const sla_ffn *f, int64_t cols) {
+  return f->tokens > kFewTokens && (f->dtype == SLA_F32 || cols % 8 != 0);
+}
+
+// g, u (dtype) and h (operand sheets), rows hidden_pitch apart, then packed copies of x, w_in and w_out.
 struct SavedLayout {
-  size_t u, h, total;
+  size_t u, h, x, w_in, w_out, total;
 };
 
 SavedLayout saved_layout(const sla_ffn *f) {
@@ -422,7 +538,10 @@ SavedLayout saved_layout(const sla_ffn *f) {
   SavedLayout L;
   L.u = align256(n * net_size(f->dtype));
   L.h = 2 * L.u;
-  L.total = L.h + align256(n * 2 * (f->dtype == SLA_F32 ? 3 : 1));
+  L.x = L.h + align256(n * 2 * (f->dtype == SLA_F32 ? 3 : 1));
+  L.w_in = L.x + (keeps_packed(f, f->width) ? packed_bytes(f->tokens, f->width, f->dtype) : 0);
+  L.w_out = L.w_in + (keeps_packed(f, f->width) ? packed_bytes(2 * f->hidden, f->width, f->dtype) : 0);
+  L.total = L.w_out + (keeps_packed(f, f->hidden) ? packed_bytes(f->out, f->hidden, f->dtype) : 0);
   return L;
 }
 
@@ -446,9 +565,10 @@ ForwardScratch forward_scratch(const sla_ffn *f, char *base) {
   w.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
   w.w_in = a.take(packed_bytes(2 * f->hidden, f->width, f->dtype));
   w.w_out = a.take(packed_bytes(f->out, f->hidden, f->dtype));
-  w.h = a.take(saved_layout(f).total - saved_layout(f).h);
-  w.parts = (float *)a.take(std::max(plan_product(gate_size(f), S, true).partial_bytes,
-                                     plan_product(out_size(f), S, false).partial_bytes));
+  w.h = a.take(saved_layout(f).x - saved_layout(f).h);
+  const ProductSize gate = gate_size(f), out = out_size(f);
+  w.parts = (float *)a.take(
+      std::max(plan_products(kGate, &gate, 1, S).partial[1], plan_products(kStore, &out, 1, S).partial[1]));
   w.total = a.used;
   return w;
 }
@@ -470,8 +590,9 @@ BackwardScratch backward_scratch(const sla_ffn *f, char *base) {
   w.dgu = a.take((size_t)f->tokens * (size_t)hidden_pitch(f) * 2 * 2 * S);
   w.sums = (float *)a.take((size_t)((f->tokens + 31) / 32) * 2 * (size_t)hidden_pitch(f) * sizeof(float));
   size_t parts = kSumParts * sizeof(float) * (size_t)std::max(2 * hidden_pitch(f), f->out);
-  for (const ProductSize &s : {dh_size(f), dx_size(f), dw_in_size(f), dw_out_size(f)})
-    parts = std::max(parts, plan_product(s, S, false).partial_bytes);
+  const ProductSize dh = dh_size(f), rest[kGroup] = {dx_size(f), dw_in_size(f), dw_out_size(f)};
+  parts = std::max(parts, plan_products(kGateBack, &dh, 1, S).partial[1]);
+  parts = std::max(parts, plan_products(kStore, rest, kGroup, S).partial[kGroup]);
   w.parts = (float *)a.take(parts);
   w.total = a.used;
   return w;
@@ -513,18 +634,23 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
     c.launched(launch_few<T>(kStore, q, st));
     return finish(c);
   }
-  const Operand ox = as_operand(c, x, f->tokens, f->width, ldx, 1, w.x);
-  const Operand oi = as_operand(c, w_in, f->hidden, f->width, f->width, 2, w.w_in);
-  const Operand oo = as_operand(c, w_out, f->out, f->hidden, f->hidden, 1, w.w_out);
-  ProductArgs p{};
-  p.act = f->activation, p.bias = b_in, p.bias_vec = b_in && aligned(b_in, 32) && f->hidden % 16 == 0, p.vec = 1;
-  p.g = saved, p.u = saved ? saved + L.u : nullptr;
-  p.h = (uint16_t *)h, p.ldg = ldg, p.sheet = f->tokens * ldg;
-  run_product<T>(c, kGate, gate_size(f), ox, false, oi, false, p, w.parts);
+  PackJobs packs;
+  const bool keep_x = saved && keeps_packed(f, f->width), keep_o = saved && keeps_packed(f, f->hidden);
+  const Operand ox = as_operand(packs, x, f->tokens, f->width, ldx, 1, keep_x ? saved + L.x : w.x);
+  const Operand oi = as_operand(packs, w_in, f->hidden, f->width, f->width, 2, keep_x ? saved + L.w_in : w.w_in);
+  const Operand oo = as_operand(packs, w_out, f->out, f->hidden, f->hidden, 1, keep_o ? saved + L.w_out : w.w_out);
+  run_packs<T>(c, packs);
   const Operand oh{h, f->hidden, f->tokens, sheets_of<T>(), ldg, f->tokens * ldg};
-  ProductArgs q{};
-  q.bias = b_out, q.bias_vec = aligned(b_out, 32), q.c = y, q.ldc = f->out, q.vec = vec_out(y, f->out);
-  run_product<T>(c, kStore, out_size(f), oh, false, oo, false, q, w.parts);
+  ProductJob gate{gate_size(f), ox, false, oi, false, {}, true};
+  gate.p.act = f->activation, gate.p.vec = 1;
+  gate.p.bias = b_in, gate.p.bias_vec = b_in && aligned(b_in, 32) && f->hidden % 16 == 0;
+  gate.p.g = saved, gate.p.u = saved ? saved + L.u : nullptr;
+  gate.p.h = (uint16_t *)h, gate.p.ldg = ldg, gate.p.sheet = f->tokens * ldg;
+  run_products<T>(c, kGate, &gate, 1, w.parts);
+  ProductJob out{out_size(f), oh, false, oo, false, {}, true};
+  out.p.bias = b_out, out.p.bias_vec = aligned(b_out, 32);
+  out.p.c = y, out.p.ldc = f->out, out.p.vec = vec_out(y, f->out);
+  run_products<T>(c, kStore, &out, 1, w.parts);
   return finish(c);
 }
 
@@ -541,40 +667,40 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
   const BackwardScratch w = backward_scratch(f, ws);
   const int64_t ldg = hidden_pitch(f), sheet = f->tokens * ldg;
   const bool inner = dx || dw_in || db_in;
-  Operand ody{}, ox{}, oi{};
-  if (inner || dw_out) ody = as_operand(c, dy, f->tokens, f->out, lddy, 1, w.dy);
+  const bool kept_x = keeps_packed(f, f->width), kept_o = keeps_packed(f, f->hidden);
+  char *sv = const_cast<char *>(saved);
+  PackJobs packs;
+  Operand ody{}, ox{}, oi{}, oo{};
+  if (inner || dw_out) ody = as_operand(packs, dy, f->tokens, f->out, lddy, 1, w.dy);
+  if (dw_in) ox = as_operand(packs, x, f->tokens, f->width, ldx, 1, kept_x ? sv + L.x : w.x, kept_x);
+  if (dx) oi = as_operand(packs, w_in, f->hidden, f->width, f->width, 2, kept_x ? sv + L.w_in : w.w_in, kept_x);
+  if (inner) oo = as_operand(packs, w_out, f->out, f->hidden, f->hidden, 1, kept_o ? sv + L.w_out : w.w_out, kept_o);
+  run_packs<T>(c, packs);
   const Operand odgu{w.dgu, f->hidden, f->tokens, 2 * S, ldg, sheet};
   const Operand oh{saved + L.h, f->hidden, f->tokens, S, ldg, sheet};
   if (inner) {
-    const Operand oo = as_operand(c, w_out, f->out, f->hidden, f->hidden, 1, w.w_out);
-    ProductArgs p{};
-    p.act = f->activation, p.vec = 1;
-    p.g = (void *)saved, p.u = (void *)(saved + L.u);
-    p.h = (uint16_t *)w.dgu, p.ldg = ldg, p.sheet = sheet;
+    ProductJob dh{dh_size(f), ody, false, oo, true, {}, true};
+    dh.p.act = f->activation, dh.p.vec = 1;
+    dh.p.g = sv, dh.p.u = sv + L.u;
+    dh.p.h = (uint16_t *)w.dgu, dh.p.ldg = ldg, dh.p.sheet = sheet;
     // the epilogue sums dg and du over 32 rows on its way, unless the product is split
-    if (db_in && plan_product(dh_size(f), S, false).splits == 1) p.sums = w.sums;
-    run_product<T>(c, kGateBack, dh_size(f), ody, false, oo, true, p, w.parts);
-    if (p.sums)
-      column_sums<float, 1>(c, (f->tokens + 31) / 32, 2 * ldg, p.sums, 2 * ldg, 0, ldg, f->hidden, db_in, w.parts);
+    if (db_in && plan_products(kGateBack, &dh.s, 1, S).splits[0] == 1) dh.p.sums = w.sums;
+    run_products<T>(c, kGateBack, &dh, 1, w.parts);
+    if (dh.p.sums)
+      column_sums<float, 1>(c, (f->tokens + 31) / 32, 2 * ldg, w.sums, 2 * ldg, 0, ldg, f->hidden, db_in, w.parts);
     else if (db_in)
       for (int half = 0; half < 2; ++half)
         column_sums<E, S>(c, f->tokens, f->hidden, (const E *)w.dgu + half * sheet, ldg, 2 * sheet, f->hidden,
                           f->hidden, db_in + half * f->hidden, w.parts);
   }
-  auto store = [&](const ProductSize &s, const Operand &a, bool a_mn, const Operand &b, T *out) {
-    ProductArgs p{};
-    p.c = out, p.ldc = s.n, p.c_m_half = s.m * s.n, p.vec = vec_out(out, s.n);
-    run_product<T>(c, kStore, s, a, a_mn, b, true, p, w.parts);
+  auto job = [&](const ProductSize &s, const Operand &a, bool a_mn, const Operand &b, T *out) {
+    ProductJob j{s, a, a_mn, b, true, {}, out != nullptr};
+    j.p.c = out, j.p.ldc = s.n, j.p.c_m_half = s.m * s.n, j.p.vec = vec_out(out, s.n);
+    return j;
   };
-  if (dx) {
-    oi = as_operand(c, w_in, f->hidden, f->width, f->width, 2, w.w_in);
-    store(dx_size(f), odgu, false, oi, dx);
-  }
-  if (dw_in) {
-    ox = as_operand(c, x, f->tokens, f->width, ldx, 1, w.x);
-    store(dw_in_size(f), odgu, true, ox, dw_in);
-  }
-  if (dw_out) store(dw_out_size(f), ody, true, oh, dw_out);
+  const ProductJob rest[kGroup] = {job(dx_size(f), odgu, false, oi, dx), job(dw_in_size(f), odgu, true, ox, dw_in),
+                                   job(dw_out_size(f), ody, true, oh, dw_out)};
+  run_products<T>(c, kStore, rest, kGroup, w.parts);
   if (db_out) column_sums<T, 1>(c, f->tokens, f->out, dy, lddy, 0, f->out, f->out, db_out, w.parts);
   return finish(c);
 }

@@ -114,6 +114,36 @@ __device__ __forceinline__ float2 unpair16(uint32_t w, bf16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// Programmatic dependent launch: a kernel of a chain may start while the one before it still runs; it
+// waits here before it touches memory that others write, and lets the next one start in turn.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+// A launch's attributes.  early: it may start before its predecessor in the stream has ended (which then
+// has to be a kernel of the same call: others' results are waited for in the ordinary way).
+struct LaunchConfig {
+  cudaLaunchConfig_t c{};
+  cudaLaunchAttribute at[2];
+  LaunchConfig(dim3 grid, int block, size_t smem, cudaStream_t st, bool early, int cluster = 1) {
+    c.gridDim = grid;
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = at;
+    if (cluster > 1) {
+      at[c.numAttrs].id = cudaLaunchAttributeClusterDimension;
+      at[c.numAttrs].val.clusterDim.x = cluster;
+      at[c.numAttrs].val.clusterDim.y = at[c.numAttrs].val.clusterDim.z = 1;
+      ++c.numAttrs;
+    }
+    if (early) {
+      at[c.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[c.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+      ++c.numAttrs;
+    }
+  }
+};
+
 inline bool net_dtype(int32_t d) { return d == SLA_F32 || d == SLA_F16 || d == SLA_BF16; }
 inline size_t net_size(int32_t d) { return d == SLA_F32 ? 4 : 2; }
 

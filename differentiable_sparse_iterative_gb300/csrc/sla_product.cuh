@@ -27,8 +27,7 @@
 namespace sla {
 
 enum Epilogue {
-  kStore,     // c = sum (+ bias)
-  kPartial,   // float32 sums of one split of k
+  kStore,     // c = sum (+ bias), or the float32 sums of one split of k
   kGate,      // columns of g and u side by side: h = act(g) u, g and u kept
   kGateBack,  // sum = dh: dg = dh u act'(g), du = dh act(g)
 };
@@ -36,20 +35,21 @@ enum Epilogue {
 constexpr int kDepth = 64;      // k of a stage: 128 bytes, the swizzle's width
 constexpr int kBand = 8;
 constexpr int kMaxSegments = 12;
+constexpr int kGroup = 3;       // products of one launch
 
 struct ProductArgs {
   int m, n;                  // rows and columns of one half of C
   int m_halves, n_halves;    // 2: A's (B's) sheets come in pairs, one for each half of C's rows (columns)
   int m_tiles, n_tiles;      // of one half
   int k_blocks;              // of a segment
-  int splits;                // k_blocks are dealt to this many blocks (kPartial)
+  int splits;                // k_blocks are dealt to this many work items, whose sums are added later
   int segments;
   int8_t a_sheet[kMaxSegments], b_sheet[kMaxSegments];
   int a_mn, b_mn;
   int f16;                   // operands are float16 (else bfloat16)
   int act;
   int vec;                   // rows of c are aligned to 32 bytes (those of g, u and h always are)
-  void *c;                   // kStore: T, kPartial: float [splits][..]
+  void *c;                   // kStore: T, or with splits float [splits][..]
   int64_t ldc, c_m_half, c_n_half, c_split;
   const void *bias;          // T, [n] (kStore) or [2 n] (kGate), or NULL
   int bias_vec;              // there is one, and its values from any multiple of 16 columns are aligned to 32 bytes
@@ -57,6 +57,14 @@ struct ProductArgs {
   uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
   int64_t ldg, sheet;        // elements between rows and between sheets of h
   float *sums;               // kGateBack: [m / 32][2][ldg] sums of dg and du over 32 rows, or NULL
+};
+
+// Up to three products that do not depend on one another, with one tile shape (kStore; one product else).
+struct ProductLaunch {
+  CUtensorMap a[kGroup], b[kGroup];
+  ProductArgs p[kGroup];
+  int first[kGroup + 1];     // work items before each product's
+  int count;
   uint32_t *timeouts;
 };
 
@@ -278,6 +286,14 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs &p, int item) {
   return t;
 }
 
+// The product of a work item, which becomes the item's number among that product's.
+__device__ __forceinline__ int product_of(const ProductLaunch &l, int &item) {
+  int i = 0;
+  while (i + 1 < l.count && item >= l.first[i + 1]) ++i;
+  item -= l.first[i];
+  return i;
+}
+
 __device__ __forceinline__ void split_range(const ProductArgs &p, int split, int &k0, int &k1) {
   k0 = (int)((int64_t)p.k_blocks * split / p.splits);
   k1 = (int)((int64_t)p.k_blocks * (split + 1) / p.splits);
@@ -285,8 +301,7 @@ __device__ __forceinline__ void split_range(const ProductArgs &p, int split, int
 
 template <typename T, int EPI, int CG, int BN>
 __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
-    product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                   const __grid_constant__ ProductArgs p) {
+    product_kernel(const __grid_constant__ ProductLaunch l) {
   using Shape = ProductShape<CG, BN>;
   constexpr int S = Shape::stages;
   extern __shared__ uint8_t raw[];
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
-  const int items = p.m_halves * p.m_tiles * p.n_halves * p.n_tiles * p.splits;
+  const int items = l.first[l.count];
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -315,8 +330,8 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
     *dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
-    tma_prefetch_map(&ma);
-    tma_prefetch_map(&mb);
+    tma_prefetch_map(&l.a[0]);
+    tma_prefetch_map(&l.b[0]);
   }
   if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
   tc_fence_before();
@@ -324,12 +339,19 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // what came before in the stream has written its results; what comes next may be made ready meanwhile
+  grid_dependency_wait();
+  grid_dependency_launch();
 
   if (warp == 0) {
     // loads: one stage is kDepth of k of the tile's rows of A and columns of B
     constexpr uint32_t bytes = CG * (Shape::a_bytes + Shape::b_bytes);
     uint32_t n = 0;
-    for (int item = worker; item < items && !*dead; item += workers) {
+    for (int next = worker; next < items && !*dead; next += workers) {
+      int item = next;
+      const int which = EPI == kStore ? product_of(l, item) : 0;
+      const ProductArgs &p = l.p[which];
+      const CUtensorMap &ma = l.a[which], &mb = l.b[which];
       const Tile t = tile_of<EPI, CG, BN>(p, item);
       int k0, k1;
       split_range(p, t.split, k0, k1);
@@ -377,11 +399,14 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
       for (uint32_t i = n > S ? n - S : 0; i < n; ++i)
         if (!mbar_wait_clocks(full + i % S, (i / S) & 1)) *dead = 1;
   } else if (warp == 1 && rank == 0) {
-    const uint32_t idesc = tc_idesc(p.f16, p.a_mn, p.b_mn, 128 * CG, BN);
-    const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
-    const uint64_t a0 = tc_desc(sa, p.a_mn, Shape::a_bytes / 2), b0 = tc_desc(sb, p.b_mn, kDepth * 128);
     uint32_t n = 0, tile = 0;
-    for (int item = worker; item < items && !*dead; item += workers, ++tile) {
+    for (int next = worker; next < items && !*dead; next += workers, ++tile) {
+      int item = next;
+      const int which = EPI == kStore ? product_of(l, item) : 0;
+      const ProductArgs &p = l.p[which];
+      const uint32_t idesc = tc_idesc(p.f16, p.a_mn, p.b_mn, 128 * CG, BN);
+      const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
+      const uint64_t a0 = tc_desc(sa, p.a_mn, Shape::a_bytes / 2), b0 = tc_desc(sb, p.b_mn, kDepth * 128);
       const Tile t = tile_of<EPI, CG, BN>(p, item);
       int k0, k1;
       split_range(p, t.split, k0, k1);
@@ -428,7 +453,10 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
     constexpr int N = BN == 256 || width == 16 || (EPI == kGate && sizeof(T) == 4) ? 16 : 32;
     constexpr bool fast = sizeof(T) == 2;
     uint32_t tile = 0;
-    for (int item = worker; item < items; item += workers, ++tile) {
+    for (int next = worker; next < items; next += workers, ++tile) {
+      int item = next;
+      const int which = EPI == kStore ? product_of(l, item) : 0;
+      const ProductArgs &p = l.p[which];
       const Tile t = tile_of<EPI, CG, BN>(p, item);
       const uint32_t acc = tile & 1;
       const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
@@ -544,8 +572,8 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
           if (c + N >= (side + 1) * width) release();
           if (live && count > 0) {
             const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
-            if constexpr (EPI == kPartial) {
-              store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, p.vec);
+            if (p.splits > 1) {
+              store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
             } else {
               if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
               store_row<T, N>((T *)p.c + o, v, count, p.vec);
@@ -562,7 +590,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_free<CG>(tmem, 2 * BN);
-  if (threadIdx.x == 0 && *dead) atomicAdd(p.timeouts, 1u);
+  if (threadIdx.x == 0 && *dead) atomicAdd(l.timeouts, 1u);
 }
 
 // Tile shapes by index, widest first.
@@ -572,14 +600,13 @@ struct ProductTile {
 constexpr ProductTile kProductTiles[] = {{2, 256}, {2, 128}, {1, 128}, {1, 64}};
 constexpr int kProductTileCount = 4;
 
-// Launches `epi` with tile shape kProductTiles[shape] on `blocks` blocks.
+// Launches `epi` with tile shape kProductTiles[shape] on `blocks` blocks.  early: the launch may be made
+// ready while the kernel before it in the stream, one of this call's own, still runs.
 template <typename T>
-cudaError_t launch_product(int epi, int shape, int blocks, const CUtensorMap &a, const CUtensorMap &b,
-                           const ProductArgs &p, cudaStream_t st);
+cudaError_t launch_product(int epi, int shape, int blocks, const ProductLaunch &l, bool early, cudaStream_t st);
 
 template <typename T, int EPI, int CG, int BN>
-cudaError_t launch_product_as(int blocks, const CUtensorMap &a, const CUtensorMap &b, const ProductArgs &p,
-                              cudaStream_t st) {
+cudaError_t launch_product_as(int blocks, const ProductLaunch &l, bool early, cudaStream_t st) {
   constexpr int smem = ProductShape<CG, BN>::smem;
   auto kernel = product_kernel<T, EPI, CG, BN>;
   // once per device: the attribute stays with the loaded kernel
@@ -591,28 +618,17 @@ cudaError_t launch_product_as(int blocks, const CUtensorMap &a, const CUtensorMa
     if (e == cudaSuccess) allowed.fetch_or(1ull << (dev & 63));
   }
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(64 + 32 * kEpilogueWarps<BN>);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a, b, p);
+  LaunchConfig cfg(dim3(blocks), 64 + 32 * kEpilogueWarps<BN>, smem, st, early, CG);
+  return cudaLaunchKernelEx(&cfg.c, kernel, l);
 }
 
 template <typename T, int EPI>
-cudaError_t launch_product_shape(int shape, int blocks, const CUtensorMap &a, const CUtensorMap &b,
-                                 const ProductArgs &p, cudaStream_t st) {
+cudaError_t launch_product_shape(int shape, int blocks, const ProductLaunch &l, bool early, cudaStream_t st) {
   switch (shape) {
-    case 0: return launch_product_as<T, EPI, 2, 256>(blocks, a, b, p, st);
-    case 1: return launch_product_as<T, EPI, 2, 128>(blocks, a, b, p, st);
-    case 2: return launch_product_as<T, EPI, 1, 128>(blocks, a, b, p, st);
-    default: return launch_product_as<T, EPI, 1, 64>(blocks, a, b, p, st);
+    case 0: return launch_product_as<T, EPI, 2, 256>(blocks, l, early, st);
+    case 1: return launch_product_as<T, EPI, 2, 128>(blocks, l, early, st);
+    case 2: return launch_product_as<T, EPI, 1, 128>(blocks, l, early, st);
+    default: return launch_product_as<T, EPI, 1, 64>(blocks, l, early, st);
   }
 }
 
