@@ -62,16 +62,20 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Map of boxes of 64 columns by box_rows rows, 128-byte swizzle, zeros outside.
-cudaError_t encode(CUtensorMap *map, const Operand &o, int box_rows, bool f16) {
+// Map of boxes of box_cols columns (64, 32 or 16: a swizzle of as many bytes as a row of the box has) by
+// box_rows rows, zeros outside.
+cudaError_t encode(CUtensorMap *map, const Operand &o, int box_cols, int box_rows, bool f16) {
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.sheets};
   const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.sheet * 2};
-  const cuuint32_t box[3] = {kDepth, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
   const CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                         const_cast<void *>(o.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                        : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                         : CU_TENSOR_MAP_SWIZZLE_32B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -400,8 +404,20 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, floa
         p.a_sheet[p.segments] = (int8_t)(pairs[q][0] * a_pair + h);
         p.b_sheet[p.segments++] = (int8_t)(pairs[q][1] * b_pair + h);
       }
-    cudaError_t e = encode(&l.a[l.count], a, p.a_mn ? kDepth : 128, p.f16);
-    if (e == cudaSuccess) e = encode(&l.b[l.count], b, p.b_mn ? kDepth : gate ? bn / 2 : bn / tile.cg, p.f16);
+    cudaError_t e = encode(&l.a[l.count], a, kDepth, p.a_mn ? kDepth : 128, p.f16);
+    if (e == cudaSuccess) e = encode(&l.b[l.count], b, kDepth, p.b_mn ? kDepth : gate ? bn / 2 : bn / tile.cg, p.f16);
+    if (sizeof(T) == 2 && epi != kStore && !split) {
+      // the epilogue's own arrays (see tma_epilogue); a warp's columns of the 64-wide gate tile are 16
+      const int box = gate && bn == 64 ? 16 : 32;
+      const Operand h{p.h, s.n, s.m, epi == kGate ? 1 : 2, p.ldg, p.sheet};
+      Operand g = h, u = h;
+      g.p = p.g, u.p = p.u;
+      if (epi == kGate && p.g) {
+        if (e == cudaSuccess) e = encode(&l.out[0], g, box, 32, p.f16);
+        if (e == cudaSuccess) e = encode(&l.out[1], u, box, 32, p.f16);
+      }
+      if (e == cudaSuccess) e = encode(&l.out[epi == kGate ? 2 : 0], h, box, 32, p.f16);
+    }
     if (e != cudaSuccess) {
       c.err = e;
       return;
@@ -424,9 +440,18 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, floa
     l.first[++l.count] = (int)items;
   }
   if (!l.count) return;
+  // The items before the last product's are the longer ones; the workers that get one of them less make up
+  // for it with short ones.
+  const int64_t workers = std::min<int64_t>(items, sm_count() / tile.cg);
+  l.lead = l.first[l.count - 1], l.extra = 0;
+  if (l.count > 1 && l.lead % workers) {
+    auto blocks_of = [](const ProductArgs &p) { return (double)p.k_blocks / p.splits * p.segments; };
+    const int64_t shorter = workers - l.lead % workers, shorts = l.first[l.count] - l.lead;
+    l.extra = (int)std::min<int64_t>((int64_t)(blocks_of(l.p[l.count - 2]) / blocks_of(l.p[l.count - 1])), shorts / shorter);
+  }
   // a split gate or gate-back product leaves plain sums
   const int as = nsplit ? kStore : epi;
-  const int blocks = (int)std::min<int64_t>(items, sm_count() / tile.cg) * tile.cg;
+  const int blocks = (int)workers * tile.cg;
   c.launched(launch_product<T>(as, plan.shape, blocks, l, c.early(), c.st));
   if (!nsplit) return;
   const dim3 grid((unsigned)std::min<int64_t>((finish + 255) / 256, 152 * 16), nsplit);

@@ -62,9 +62,11 @@ struct ProductArgs {
 // Up to three products that do not depend on one another, with one tile shape (kStore; one product else).
 struct ProductLaunch {
   CUtensorMap a[kGroup], b[kGroup];
+  CUtensorMap out[3];        // kTmaStores: g, u, h, or dg and du (one map, two sheets)
   ProductArgs p[kGroup];
   int first[kGroup + 1];     // work items before each product's
   int count;
+  int lead, extra;           // see item_of
   uint32_t *timeouts;
 };
 
@@ -73,13 +75,30 @@ struct ProductLaunch {
 template <int BN>
 inline constexpr int kEpilogueWarps = BN == 256 ? 16 : 8;
 
-// Tile shapes: CG blocks of 128 rows, BN columns, stages that fill the shared memory of a multiprocessor.
-template <int CG, int BN>
+// The epilogues that write arrays of this library's own (g, u, h, dg, du) in 16 bits put them together in
+// shared memory and store them by TMA: a warp that stores 32 bytes of 32 rows at a time keeps the
+// load-store unit busy for 32 cycles (it was at 78 % of its rate with g, u and h stored so).
+template <typename T, int EPI>
+inline constexpr bool kTmaStores = sizeof(T) == 2 && (EPI == kGate || EPI == kGateBack);
+
+// Columns that one warp of the epilogue takes, and those of one store.
+template <int EPI, int BN>
+inline constexpr int kWarpColumns = (EPI == kGate ? BN / 2 : BN) / (kEpilogueWarps<BN> / 4);
+template <int EPI, int BN>
+inline constexpr int kStoreColumns = kWarpColumns<EPI, BN> < 32 ? kWarpColumns<EPI, BN> : 32;
+
+// Tile shapes: CG blocks of 128 rows, BN columns, stages that fill what the stores leave of a multiprocessor's
+// shared memory (two boxes of 32 rows a warp).
+template <typename T, int EPI, int CG, int BN>
 struct ProductShape {
   static constexpr int a_bytes = 128 * kDepth * 2;
   static constexpr int b_bytes = BN / CG * kDepth * 2;
-  static constexpr int stages = (208 * 1024) / (a_bytes + b_bytes) > 8 ? 8 : (208 * 1024) / (a_bytes + b_bytes);
-  static constexpr int smem = stages * (a_bytes + b_bytes) + 1024 /* alignment */ + 256 /* barriers */;
+  static constexpr int box = 32 * kStoreColumns<EPI, BN> * 2;
+  static constexpr int boxes = kTmaStores<T, EPI> ? kEpilogueWarps<BN> * 2 * box : 0;
+  static constexpr int room = (225 * 1024 - boxes) / (a_bytes + b_bytes);
+  static constexpr int stages = room > 8 ? 8 : room;
+  static constexpr int smem = stages * (a_bytes + b_bytes) + boxes + 1024 /* alignment */ + 256 /* barriers */;
+  static_assert(stages >= 4 && smem <= 227 * 1024, "shared memory");
 };
 
 // Three bfloat16 values whose sum is v to 2^-24: each the rounded rest of the one before.  An
@@ -286,6 +305,24 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs &p, int item) {
   return t;
 }
 
+// A worker's i-th work item, or -1.  Workers take the items in turn.  Where the items of the last product are
+// shorter than those before it (`lead` of them), the workers that got one less of those first take
+// `extra` of the short ones, about as long together.
+__device__ __forceinline__ int item_of(const ProductLaunch &l, int worker, int workers, int i) {
+  int item = worker + i * workers;
+  if (l.extra) {
+    const int mine = worker < l.lead ? (l.lead - worker - 1) / workers + 1 : 0, over = l.lead % workers;
+    if (i < mine) return item;
+    i -= mine;
+    if (worker >= over) {
+      if (i < l.extra) return l.lead + (worker - over) * l.extra + i;
+      i -= l.extra;
+    }
+    item = l.lead + l.extra * (workers - over) + worker + i * workers;
+  }
+  return item < l.first[l.count] ? item : -1;
+}
+
 // The product of a work item, which becomes the item's number among that product's.
 __device__ __forceinline__ int product_of(const ProductLaunch &l, int &item) {
   int i = 0;
@@ -299,15 +336,328 @@ __device__ __forceinline__ void split_range(const ProductArgs &p, int split, int
   k1 = (int)((int64_t)p.k_blocks * (split + 1) / p.splits);
 }
 
+// A warp has read its part of an accumulator.
+template <int CG>
+__device__ __forceinline__ void release_accumulator(uint64_t *acc_empty, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    if (CG == 2)
+      mbar_arrive_rank(acc_empty, 0);
+    else
+      mbar_arrive(acc_empty);
+  }
+}
+
+// A box of 32 rows and W 16-bit columns in shared memory, thread = row, in TMA's swizzle for rows of W * 2
+// bytes: units of 16 bytes (8 columns) change places within their row, so that writing them meets no bank
+// conflicts.
+template <typename T, int W>
+struct StoreBox {
+  static constexpr int units = W / 8;
+  uint4 *sm;
+  int lane;
+  __device__ __forceinline__ void put(int part, const uint32_t (&w)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int unit = 2 * part + i;
+      sm[lane * units + (unit ^ ((lane / (8 / units)) & (units - 1)))] =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
+  // 16 columns of the thread's row from column 16 * part
+  __device__ __forceinline__ void put(int part, const float (&v)[16]) const {
+    uint32_t w[8];
+    pack(v, w);
+    put(part, w);
+  }
+  static __device__ __forceinline__ void pack(const float (&v)[16], uint32_t (&w)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pair16(v[2 * k], v[2 * k + 1], T{});
+  }
+};
+
+// kGate and kGateBack in 16 bits: 16 columns at a time, stored in boxes of W.
+template <typename T, int EPI, int CG, int BN>
+__device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tmem, uint8_t *boxes, uint64_t *acc_full,
+                                             uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
+                                             uint32_t rank) {
+  const ProductArgs &p = l.p[0];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, side = (warp - 2) >> 2;
+  constexpr int width = kWarpColumns<EPI, BN>, W = kStoreColumns<EPI, BN>, box = ProductShape<T, EPI, CG, BN>::box;
+  uint8_t *mine = boxes + (warp - 2) * 2 * box;
+  const StoreBox<T, W> box0{(uint4 *)mine, lane}, box1{(uint4 *)(mine + box), lane};
+  // boxes 0 and 1 hold what the warp's lanes have put there: to columns x.. of rows y.. of two maps or sheets
+  auto store2 = [&](const CUtensorMap *m0, const CUtensorMap *m1, int x, int y, int z1) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store(m0, x, y, 0, box0.sm);
+      tma_store_commit();
+      tma_store(m1, x, y, z1, box1.sm);
+      tma_store_commit();
+    }
+  };
+  for (int tile = 0;; ++tile) {
+    int item = item_of(l, worker, workers, tile);
+    if (item < 0) break;
+    const Tile t = tile_of<EPI, CG, BN>(p, item);
+    const uint32_t acc = tile & 1;
+    const int row0 = t.m0 + (int)rank * 128 + quarter * 32, row = row0 + lane;
+    const bool live = row < p.m;
+    const int first = side * width;
+    // What the next columns need from memory is on its way while these are worked on, and the first
+    // columns' while the product runs.  kGateBack: g and u (rows are padded to whole sectors of 16
+    // columns); kGate: the biases.
+    RawRow<T, 16> raw_g, raw_u;
+    auto ask = [&](int c) {
+      if constexpr (EPI == kGate) {
+        if (p.bias_vec && t.n0 + c + 16 <= p.n) {
+          raw_g.load((const T *)p.bias + t.n0 + c);
+          raw_u.load((const T *)p.bias + p.n + t.n0 + c);
+        }
+      } else if (live && t.n0 + c + 16 <= p.ldg) {
+        const int64_t o = row * p.ldg + t.n0 + c;
+        raw_g.load((const T *)p.g + o);
+        raw_u.load((const T *)p.u + o);
+      } else {
+        raw_g.clear();
+        raw_u.clear();
+      }
+    };
+    ask(first);
+    if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
+      *dead = 1;
+      break;
+    }
+    tc_fence_after();
+    const uint32_t base = tmem + acc * BN + ((uint32_t)quarter << 21);
+#pragma unroll 1
+    for (int c = first; c < first + width; c += W) {
+      const bool some = row0 < p.m && t.n0 + c < p.n, last = c + W >= first + width;
+      uint32_t ph[W / 16][8];
+      if (lane == 0) tma_store_read<0>();  // the boxes are free
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < W; j += 16) {
+        const int count = p.n - t.n0 - c - j;
+        float v[16];
+        tmem_load16(base + c + j, v);
+        if constexpr (EPI == kGate) {
+          float u[16], bg[16], bu[16];
+          tmem_load16(base + BN / 2 + c + j, u);
+          raw_g.values(bg);
+          raw_u.values(bu);
+          if (c + j + 16 < first + width) ask(c + j + 16);
+          tmem_wait(v);
+          tmem_wait(u);
+          if (p.bias_vec && count >= 16) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += bg[i], u[i] += bu[i];
+          } else if (p.bias) {
+            add_bias<T, 16>(v, (const T *)p.bias + t.n0 + c + j, count, false);
+            add_bias<T, 16>(u, (const T *)p.bias + p.n + t.n0 + c + j, count, false);
+          }
+          if (p.g) {
+            box0.put(j / 16, v);
+            box1.put(j / 16, u);
+          }
+          with_activation(p.act, [&](auto act) { gate_values<act.value, true, 16>(v, u); });
+          box0.pack(v, ph[j / 16]);
+        } else {
+          float g[16], u[16];
+          raw_g.values(g);
+          raw_u.values(u);
+          if (c + j + 16 < first + width) ask(c + j + 16);
+          tmem_wait(v);
+          with_activation(p.act, [&](auto act) { gate_gradients<act.value, true, 16>(v, g, u); });
+          box0.put(j / 16, g);
+          box1.put(j / 16, u);
+          if (p.sums && row0 < p.m) {
+            if (!live) {  // not a row: its product is no zero if a weight is infinite
+#pragma unroll
+              for (int i = 0; i < 16; ++i) g[i] = u[i] = 0.f;
+            }
+            const float sg = sum_columns(g, lane), su = sum_columns(u, lane);
+            if (lane < 16 && lane < count) {
+              float *to = p.sums + (int64_t)(row0 >> 5) * 2 * p.ldg + t.n0 + c + j + lane;
+              to[0] = sg;
+              to[p.ldg] = su;
+            }
+          }
+        }
+      }
+      if (last) release_accumulator<CG>(acc_empty + acc, lane);
+      if (!some) continue;
+      if constexpr (EPI == kGate) {
+        if (p.g) {
+          store2(&l.out[0], &l.out[1], t.n0 + c, row0, 0);
+          if (lane == 0) tma_store_read<1>();  // g's box is free again
+          __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < W / 16; ++j) box0.put(j, ph[j]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store(&l.out[2], t.n0 + c, row0, 0, box0.sm);
+          tma_store_commit();
+        }
+      } else {
+        store2(&l.out[0], &l.out[0], t.n0 + c, row0, 1);
+      }
+    }
+  }
+  if (lane == 0) tma_store_done();
+  __syncwarp();
+}
+
+// Straight from the registers: results in the caller's arrays (kStore), which TMA may not be able to write,
+// and float32's.
+template <typename T, int EPI, int CG, int BN>
+__device__ __forceinline__ void direct_epilogue(const ProductLaunch &l, uint32_t tmem, uint64_t *acc_full,
+                                                uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
+                                                uint32_t rank) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, side = (warp - 2) >> 2;
+  // columns of this warp, N at a time (as many as the registers hold: 112 a thread with sixteen warps)
+  constexpr int width = kWarpColumns<EPI, BN>;
+  constexpr int N = BN == 256 || width == 16 || EPI != kStore ? 16 : 32;
+  constexpr bool fast = sizeof(T) == 2;
+  uint32_t tile = 0;
+  for (;; ++tile) {
+    int item = item_of(l, worker, workers, tile);
+    if (item < 0) break;
+    const int which = EPI == kStore ? product_of(l, item) : 0;
+    const ProductArgs &p = l.p[which];
+    const Tile t = tile_of<EPI, CG, BN>(p, item);
+    const uint32_t acc = tile & 1;
+    const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
+    const bool live = row < p.m;
+    // What the next columns need from memory is on its way while these are worked on, and the first
+    // columns' while the product runs.  kGateBack: g and u (rows are padded to whole sectors of 16
+    // columns); kGate: the biases.
+    RawRow<T, N> raw_g, raw_u;
+    auto ask = [&](int c) {
+      if (EPI == kGate) {
+        if (p.bias_vec && t.n0 + c + N <= p.n) {
+          raw_g.load((const T *)p.bias + t.n0 + c);
+          raw_u.load((const T *)p.bias + p.n + t.n0 + c);
+        }
+        return;
+      }
+      const int64_t o = row * p.ldg + t.n0 + c;
+      if (live && t.n0 + c + N <= p.ldg) {
+        raw_g.load((const T *)p.g + o);
+        raw_u.load((const T *)p.u + o);
+      } else {
+        raw_g.clear();
+        raw_u.clear();
+        if (N == 32 && live && t.n0 + c < p.ldg) {  // half of the columns are there
+          RawRow<T, 16> half;
+          half.load((const T *)p.g + o);
+#pragma unroll
+          for (int i = 0; i < half.n; ++i) raw_g.s[i] = half.s[i];
+          half.load((const T *)p.u + o);
+#pragma unroll
+          for (int i = 0; i < half.n; ++i) raw_u.s[i] = half.s[i];
+        }
+      }
+    };
+    if constexpr (EPI == kGateBack || EPI == kGate) ask(side * width);
+    if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
+      *dead = 1;
+      break;
+    }
+    tc_fence_after();
+    const uint32_t base = tmem + acc * BN + ((uint32_t)quarter << 21);
+#pragma unroll 1
+    for (int c = side * width; c < (side + 1) * width; c += N) {
+      const int col = t.n0 + c, count = p.n - col;
+      float v[N];
+      if constexpr (N == 32)
+        tmem_load32(base + c, v);
+      else
+        tmem_load16(base + c, v);
+      if constexpr (EPI == kGate) {
+        float u[N];
+        if constexpr (N == 32)
+          tmem_load32(base + BN / 2 + c, u);
+        else
+          tmem_load16(base + BN / 2 + c, u);
+        float bg[N], bu[N];
+        raw_g.values(bg);
+        raw_u.values(bu);
+        if (c + N < (side + 1) * width) ask(c + N);
+        tmem_wait(v);
+        tmem_wait(u);
+        if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
+        if (live && count > 0) {
+          if (p.bias_vec && count >= N) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += bg[i], u[i] += bu[i];
+          } else if (p.bias) {
+            add_bias<T, N>(v, (const T *)p.bias + col, count, false);
+            add_bias<T, N>(u, (const T *)p.bias + p.n + col, count, false);
+          }
+          const int64_t o = row * p.ldg + col;
+          if (p.g) {
+            store_row<T, N>((T *)p.g + o, v, count, p.vec);
+            store_row<T, N>((T *)p.u + o, u, count, p.vec);
+          }
+          with_activation(p.act, [&](auto act) { gate_values<act.value, fast, N>(v, u); });
+          store_operand<T, N>(p.h + o, p.sheet, v, count, p.vec);
+        }
+      } else if constexpr (EPI == kGateBack) {
+        float g[N], u[N];
+        const int64_t o = row * p.ldg + col;
+        raw_g.values(g);
+        raw_u.values(u);
+        if (c + N < (side + 1) * width) ask(c + N);
+        tmem_wait(v);
+        if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
+        if (live && count > 0) {
+          with_activation(p.act, [&](auto act) { gate_gradients<act.value, fast, N>(v, g, u); });
+          // sheets: dg and du of each part of the value
+          store_operand<T, N>(p.h + o, 2 * p.sheet, g, count, p.vec);
+          store_operand<T, N>(p.h + p.sheet + o, 2 * p.sheet, u, count, p.vec);
+        }
+        if (p.sums && row - lane < p.m) {
+          const float sg = sum_columns(g, lane), su = sum_columns(u, lane);
+          if (lane < N && lane < count) {
+            float *to = p.sums + (int64_t)(row >> 5) * 2 * p.ldg + col + lane;
+            to[0] = sg;
+            to[p.ldg] = su;
+          }
+        }
+      } else {
+        tmem_wait(v);
+        if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
+        if (live && count > 0) {
+          const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
+          if (p.splits > 1) {
+            store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
+          } else {
+            if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
+            store_row<T, N>((T *)p.c + o, v, count, p.vec);
+          }
+        }
+      }
+    }
+  }
+}
+
 template <typename T, int EPI, int CG, int BN>
 __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
     product_kernel(const __grid_constant__ ProductLaunch l) {
-  using Shape = ProductShape<CG, BN>;
+  using Shape = ProductShape<T, EPI, CG, BN>;
   constexpr int S = Shape::stages;
   extern __shared__ uint8_t raw[];
   uint8_t *tiles = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sa = tiles, *sb = tiles + S * Shape::a_bytes;
-  uint64_t *full = (uint64_t *)(tiles + S * (Shape::a_bytes + Shape::b_bytes));
+  uint8_t *boxes = tiles + S * (Shape::a_bytes + Shape::b_bytes);
+  uint64_t *full = (uint64_t *)(boxes + Shape::boxes);
   uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 2, *drained = acc_empty + 2;
   uint32_t *tmem_slot = (uint32_t *)(drained + 1);
   volatile uint32_t *dead = tmem_slot + 1;
@@ -315,7 +665,6 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
-  const int items = l.first[l.count];
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -347,8 +696,9 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
     // loads: one stage is kDepth of k of the tile's rows of A and columns of B
     constexpr uint32_t bytes = CG * (Shape::a_bytes + Shape::b_bytes);
     uint32_t n = 0;
-    for (int next = worker; next < items && !*dead; next += workers) {
-      int item = next;
+    for (int i = 0; !*dead; ++i) {
+      int item = item_of(l, worker, workers, i);
+      if (item < 0) break;
       const int which = EPI == kStore ? product_of(l, item) : 0;
       const ProductArgs &p = l.p[which];
       const CUtensorMap &ma = l.a[which], &mb = l.b[which];
@@ -400,8 +750,9 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
         if (!mbar_wait_clocks(full + i % S, (i / S) & 1)) *dead = 1;
   } else if (warp == 1 && rank == 0) {
     uint32_t n = 0, tile = 0;
-    for (int next = worker; next < items && !*dead; next += workers, ++tile) {
-      int item = next;
+    for (; !*dead; ++tile) {
+      int item = item_of(l, worker, workers, tile);
+      if (item < 0) break;
       const int which = EPI == kStore ? product_of(l, item) : 0;
       const ProductArgs &p = l.p[which];
       const uint32_t idesc = tc_idesc(p.f16, p.a_mn, p.b_mn, 128 * CG, BN);
@@ -447,141 +798,10 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
       mbar_wait_clocks(drained, 0);
     }
   } else if (warp >= 2) {
-    const int quarter = warp & 3, side = (warp - 2) >> 2;
-    // columns of this warp, N at a time (as many as the registers hold: 112 a thread with sixteen warps)
-    constexpr int width = (EPI == kGate ? BN / 2 : BN) / (kEpilogueWarps<BN> / 4);
-    constexpr int N = BN == 256 || width == 16 || (EPI == kGate && sizeof(T) == 4) ? 16 : 32;
-    constexpr bool fast = sizeof(T) == 2;
-    uint32_t tile = 0;
-    for (int next = worker; next < items; next += workers, ++tile) {
-      int item = next;
-      const int which = EPI == kStore ? product_of(l, item) : 0;
-      const ProductArgs &p = l.p[which];
-      const Tile t = tile_of<EPI, CG, BN>(p, item);
-      const uint32_t acc = tile & 1;
-      const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
-      const bool live = row < p.m;
-      // What the next columns need from memory is on its way while these are worked on, and the first
-      // columns' while the product runs.  kGateBack: g and u (rows are padded to whole sectors of 16
-      // columns); kGate: the biases.
-      RawRow<T, N> raw_g, raw_u;
-      auto ask = [&](int c) {
-        if (EPI == kGate) {
-          if (p.bias_vec && t.n0 + c + N <= p.n) {
-            raw_g.load((const T *)p.bias + t.n0 + c);
-            raw_u.load((const T *)p.bias + p.n + t.n0 + c);
-          }
-          return;
-        }
-        const int64_t o = row * p.ldg + t.n0 + c;
-        if (live && t.n0 + c + N <= p.ldg) {
-          raw_g.load((const T *)p.g + o);
-          raw_u.load((const T *)p.u + o);
-        } else {
-          raw_g.clear();
-          raw_u.clear();
-          if (N == 32 && live && t.n0 + c < p.ldg) {  // half of the columns are there
-            RawRow<T, 16> half;
-            half.load((const T *)p.g + o);
-#pragma unroll
-            for (int i = 0; i < half.n; ++i) raw_g.s[i] = half.s[i];
-            half.load((const T *)p.u + o);
-#pragma unroll
-            for (int i = 0; i < half.n; ++i) raw_u.s[i] = half.s[i];
-          }
-        }
-      };
-      if constexpr (EPI == kGateBack || EPI == kGate) ask(side * width);
-      if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
-        *dead = 1;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t base = tmem + acc * BN + ((uint32_t)quarter << 21);
-      auto release = [&] {  // this warp has read its part of the accumulator
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2)
-            mbar_arrive_rank(acc_empty + acc, 0);
-          else
-            mbar_arrive(acc_empty + acc);
-        }
-      };
-#pragma unroll 1
-      for (int c = side * width; c < (side + 1) * width; c += N) {
-        const int col = t.n0 + c, count = p.n - col;
-        float v[N];
-        if constexpr (N == 32)
-          tmem_load32(base + c, v);
-        else
-          tmem_load16(base + c, v);
-        if constexpr (EPI == kGate) {
-          float u[N];
-          if constexpr (N == 32)
-            tmem_load32(base + BN / 2 + c, u);
-          else
-            tmem_load16(base + BN / 2 + c, u);
-          float bg[N], bu[N];
-          raw_g.values(bg);
-          raw_u.values(bu);
-          if (c + N < (side + 1) * width) ask(c + N);
-          tmem_wait(v);
-          tmem_wait(u);
-          if (c + N >= (side + 1) * width) release();
-          if (live && count > 0) {
-            if (p.bias_vec && count >= N) {
-#pragma unroll
-              for (int i = 0; i < N; ++i) v[i] += bg[i], u[i] += bu[i];
-            } else if (p.bias) {
-              add_bias<T, N>(v, (const T *)p.bias + col, count, false);
-              add_bias<T, N>(u, (const T *)p.bias + p.n + col, count, false);
-            }
-            const int64_t o = row * p.ldg + col;
-            if (p.g) {
-              store_row<T, N>((T *)p.g + o, v, count, p.vec);
-              store_row<T, N>((T *)p.u + o, u, count, p.vec);
-            }
-            with_activation(p.act, [&](auto act) { gate_values<act.value, fast, N>(v, u); });
-            store_operand<T, N>(p.h + o, p.sheet, v, count, p.vec);
-          }
-        } else if constexpr (EPI == kGateBack) {
-          float g[N], u[N];
-          const int64_t o = row * p.ldg + col;
-          raw_g.values(g);
-          raw_u.values(u);
-          if (c + N < (side + 1) * width) ask(c + N);
-          tmem_wait(v);
-          if (c + N >= (side + 1) * width) release();
-          if (live && count > 0) {
-            with_activation(p.act, [&](auto act) { gate_gradients<act.value, fast, N>(v, g, u); });
-            // sheets: dg and du of each part of the value
-            store_operand<T, N>(p.h + o, 2 * p.sheet, g, count, p.vec);
-            store_operand<T, N>(p.h + p.sheet + o, 2 * p.sheet, u, count, p.vec);
-          }
-          if (p.sums && row - lane < p.m) {
-            const float sg = sum_columns(g, lane), su = sum_columns(u, lane);
-            if (lane < N && lane < count) {
-              float *to = p.sums + (int64_t)(row >> 5) * 2 * p.ldg + col + lane;
-              to[0] = sg;
-              to[p.ldg] = su;
-            }
-          }
-        } else {
-          tmem_wait(v);
-          if (c + N >= (side + 1) * width) release();
-          if (live && count > 0) {
-            const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
-            if (p.splits > 1) {
-              store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
-            } else {
-              if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
-              store_row<T, N>((T *)p.c + o, v, count, p.vec);
-            }
-          }
-        }
-      }
-    }
+    if constexpr (kTmaStores<T, EPI>)
+      tma_epilogue<T, EPI, CG, BN>(l, tmem, boxes, acc_full, acc_empty, dead, worker, workers, rank);
+    else
+      direct_epilogue<T, EPI, CG, BN>(l, tmem, acc_full, acc_empty, dead, worker, workers, rank);
   }
   __syncwarp();
   tc_fence_before();
@@ -607,7 +827,7 @@ cudaError_t launch_product(int epi, int shape, int blocks, const ProductLaunch &
 
 template <typename T, int EPI, int CG, int BN>
 cudaError_t launch_product_as(int blocks, const ProductLaunch &l, bool early, cudaStream_t st) {
-  constexpr int smem = ProductShape<CG, BN>::smem;
+  constexpr int smem = ProductShape<T, EPI, CG, BN>::smem;
   auto kernel = product_kernel<T, EPI, CG, BN>;
   // once per device: the attribute stays with the loaded kernel
   static std::atomic<uint64_t> allowed{0};

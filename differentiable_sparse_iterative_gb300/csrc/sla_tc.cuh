@@ -75,6 +75,21 @@ __device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int 
         : "memory");
 }
 
+// Box from shared memory to a tensor (what lies outside of it is not written).  The thread that issues
+// stores commits them and waits for them.
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, int x, int y, int z, const void *src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the last N groups of this thread's stores have read their shared memory.
+template <int N>
+__device__ __forceinline__ void tma_store_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
