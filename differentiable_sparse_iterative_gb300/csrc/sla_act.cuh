@@ -55,13 +55,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// 1 / (1 + 2^m) of both, m held below 86 (2^-86 for less): each denominator stays finite, so a pair whose
-// product is infinite gives two zeros and never infinity times zero.  NaN goes in as 86: callers
-// multiply by the value it came from.
+// 1 / (1 + 2^m) of both.  (One reciprocal for the product of both denominators needs m held below 86, and
+// the two of them in the other order: 7 % slower than two reciprocals.)
 __device__ __forceinline__ float2 sigmoid2(float2 m) {
-  const float2 d = add2(f2(ex2_approx(fminf(m.x, 86.f)), ex2_approx(fminf(m.y, 86.f))), f2(1.f, 1.f));
-  const float r = rcp_approx(d.x * d.y);
-  return mul2(f2(d.y, d.x), f2(r, r));
+  const float2 d = add2(f2(ex2_approx(m.x), ex2_approx(m.y)), f2(1.f, 1.f));
+  return f2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
 // The activation of a pair; da: also its derivative.

@@ -75,6 +75,13 @@ struct ProductLaunch {
 template <int BN>
 inline constexpr int kEpilogueWarps = BN == 256 ? 16 : 8;
 
+// Teams of epilogue warps, which take the tiles in turn: while one waits (for the accumulator, for its
+// stores) the other computes.  The smaller tiles, of which a block often has one, get all warps together.
+template <int BN>
+inline constexpr int kTeams = BN == 256 ? 2 : 1;
+template <int BN>
+inline constexpr int kTeamWarps = kEpilogueWarps<BN> / kTeams<BN>;
+
 // The epilogues that write arrays of this library's own (g, u, h, dg, du) in 16 bits put them together in
 // shared memory and store them by TMA: a warp that stores 32 bytes of 32 rows at a time keeps the
 // load-store unit busy for 32 cycles (it was at 78 % of its rate with g, u and h stored so).
@@ -83,7 +90,7 @@ inline constexpr bool kTmaStores = sizeof(T) == 2 && (EPI == kGate || EPI == kGa
 
 // Columns that one warp of the epilogue takes, and those of one store.
 template <int EPI, int BN>
-inline constexpr int kWarpColumns = (EPI == kGate ? BN / 2 : BN) / (kEpilogueWarps<BN> / 4);
+inline constexpr int kWarpColumns = (EPI == kGate ? BN / 2 : BN) / (kTeamWarps<BN> / 4);
 template <int EPI, int BN>
 inline constexpr int kStoreColumns = kWarpColumns<EPI, BN> < 32 ? kWarpColumns<EPI, BN> : 32;
 
@@ -384,7 +391,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
                                              uint32_t rank) {
   const ProductArgs &p = l.p[0];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, side = (warp - 2) >> 2;
+  const int quarter = warp & 3, team = (warp - 2) / kTeamWarps<BN>, side = (warp - 2) % kTeamWarps<BN> / 4;
   constexpr int width = kWarpColumns<EPI, BN>, W = kStoreColumns<EPI, BN>, box = ProductShape<T, EPI, CG, BN>::box;
   uint8_t *mine = boxes + (warp - 2) * 2 * box;
   const StoreBox<T, W> box0{(uint4 *)mine, lane}, box1{(uint4 *)(mine + box), lane};
@@ -399,7 +406,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
       tma_store_commit();
     }
   };
-  for (int tile = 0;; ++tile) {
+  for (int tile = team;; tile += kTeams<BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
     const Tile t = tile_of<EPI, CG, BN>(p, item);
@@ -445,16 +452,22 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
         float v[16];
         tmem_load16(base + c + j, v);
         if constexpr (EPI == kGate) {
-          float u[16], bg[16], bu[16];
+          float u[16];
           tmem_load16(base + BN / 2 + c + j, u);
-          raw_g.values(bg);
-          raw_u.values(bu);
+          const RawRow<T, 16> bias_g = raw_g, bias_u = raw_u;
           if (c + j + 16 < first + width) ask(c + j + 16);
           tmem_wait(v);
           tmem_wait(u);
           if (p.bias_vec && count >= 16) {
+            float bg[16], bu[16];
+            bias_g.values(bg);
+            bias_u.values(bu);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += bg[i], u[i] += bu[i];
+            for (int i = 0; i < 16; i += 2) {
+              const float2 a = add2(f2(v[i], v[i + 1]), f2(bg[i], bg[i + 1]));
+              const float2 b = add2(f2(u[i], u[i + 1]), f2(bu[i], bu[i + 1]));
+              v[i] = a.x, v[i + 1] = a.y, u[i] = b.x, u[i + 1] = b.y;
+            }
           } else if (p.bias) {
             add_bias<T, 16>(v, (const T *)p.bias + t.n0 + c + j, count, false);
             add_bias<T, 16>(u, (const T *)p.bias + p.n + t.n0 + c + j, count, false);
@@ -520,13 +533,12 @@ __device__ __forceinline__ void direct_epilogue(const ProductLaunch &l, uint32_t
                                                 uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
                                                 uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, side = (warp - 2) >> 2;
+  const int quarter = warp & 3, team = (warp - 2) / kTeamWarps<BN>, side = (warp - 2) % kTeamWarps<BN> / 4;
   // columns of this warp, N at a time (as many as the registers hold: 112 a thread with sixteen warps)
   constexpr int width = kWarpColumns<EPI, BN>;
   constexpr int N = BN == 256 || width == 16 || EPI != kStore ? 16 : 32;
   constexpr bool fast = sizeof(T) == 2;
-  uint32_t tile = 0;
-  for (;; ++tile) {
+  for (int tile = team;; tile += kTeams<BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
     const int which = EPI == kStore ? product_of(l, item) : 0;
@@ -662,7 +674,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
   uint32_t *tmem_slot = (uint32_t *)(drained + 1);
   volatile uint32_t *dead = tmem_slot + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
 
@@ -673,7 +685,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, kEpilogueWarps<BN> * CG);
+      mbar_init(acc_empty + i, kTeamWarps<BN> * CG);
     }
     mbar_init(drained, 1);
     *dead = 0;

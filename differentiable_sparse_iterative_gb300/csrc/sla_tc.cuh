@@ -13,10 +13,24 @@ namespace sla {
 // A wait that has not ended after this many clocks (about 2 s) never will.
 constexpr long long kWaitClocks = 4000000000ll;
 
+// One try of a wait, during which the warp may sleep up to 100 us: warps that wait for a tile or a stage
+// must not take issue slots from those that compute.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ bool mbar_wait_clocks(uint64_t *bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait_long(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
+  while (!mbar_try_wait_long(bar, parity))
     if (clock64() - t0 > kWaitClocks) return false;
   return true;
 }
