@@ -100,43 +100,45 @@ __device__ __forceinline__ void activate2(float2 g, float2 &a, float2 &da) {
   }
 }
 
-// v = act(v) * u;  16-bit data (Fast) in pairs.
-template <int Act, bool Fast, int N>
-__device__ __forceinline__ void gate_values(float (&v)[N], const float (&u)[N]) {
+// h = act(g) u from g and u, 16-bit data (Fast) in pairs.  Keep: g and u become the factors of the backward
+// pass, dg = dh (u act'(g)) and du = dh act(g).  They are what a forward call leaves behind, in the place
+// of g and u: as many bytes, one rounding each, and the backward epilogue is two products.
+template <int Act, bool Fast, bool Keep, int N>
+__device__ __forceinline__ void gate(float (&g)[N], float (&u)[N], float (&h)[N]) {
   if constexpr (Fast && N % 2 == 0) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       float2 a, da;
-      activate2<Act, false>(f2(v[i], v[i + 1]), a, da);
-      a = mul2(a, f2(u[i], u[i + 1]));
-      v[i] = a.x, v[i + 1] = a.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = activate<Act>(v[i]).a * u[i];
-  }
-}
-
-// From v = dh:  g = dg = dh u act'(g),  u = du = dh act(g).
-template <int Act, bool Fast, int N>
-__device__ __forceinline__ void gate_gradients(const float (&v)[N], float (&g)[N], float (&u)[N]) {
-  if constexpr (Fast && N % 2 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      float2 a, da;
-      const float2 dh = f2(v[i], v[i + 1]);
-      activate2<Act, true>(f2(g[i], g[i + 1]), a, da);
-      da = mul2(mul2(dh, f2(u[i], u[i + 1])), da);
-      a = mul2(dh, a);
-      g[i] = da.x, g[i + 1] = da.y, u[i] = a.x, u[i + 1] = a.y;
+      const float2 up = f2(u[i], u[i + 1]);
+      activate2<Act, Keep>(f2(g[i], g[i + 1]), a, da);
+      const float2 v = mul2(a, up);
+      h[i] = v.x, h[i + 1] = v.y;
+      if (Keep) {
+        da = mul2(da, up);
+        g[i] = da.x, g[i + 1] = da.y, u[i] = a.x, u[i + 1] = a.y;
+      }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const ActValue a = activate<Act>(g[i]);
-      g[i] = v[i] * u[i] * a.da;
-      u[i] = v[i] * a.a;
+      h[i] = a.a * u[i];
+      if (Keep) {
+        g[i] = u[i] * a.da;
+        u[i] = a.a;
+      }
     }
+  }
+}
+
+// From v = dh and the factors:  g = dg, u = du.
+template <int N>
+__device__ __forceinline__ void gate_gradients(const float (&v)[N], float (&g)[N], float (&u)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 dh = f2(v[i], v[i + 1]);
+    const float2 a = mul2(dh, f2(g[i], g[i + 1])), b = mul2(dh, f2(u[i], u[i + 1]));
+    g[i] = a.x, g[i + 1] = a.y, u[i] = b.x, u[i + 1] = b.y;
   }
 }
 

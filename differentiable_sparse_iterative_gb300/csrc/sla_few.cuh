@@ -34,7 +34,7 @@ struct FewArgs {
   int x_vec, w_vec;        // 16-byte loads of 8 values can be used
   int act;
   void *c;                 // T [tokens][n] (out)
-  void *g, *u;             // T [tokens][ldg] or NULL (gate)
+  void *g, *u;             // T [tokens][ldg]: u act'(g) and act(g), or NULL (gate)
   uint16_t *h;             // operand sheets (gate)
   int64_t ldg, sheet;
 };
@@ -225,13 +225,13 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
     }
     if (Gate) {
       const int64_t o = token * p.ldg + r;
+      float a[1] = {v}, b[1] = {u}, h[1];
+      with_activation(p.act, [&](auto act) { gate<act.value, sizeof(T) == 2, true, 1>(a, b, h); });
       if (p.g) {
-        ((T *)p.g)[o] = from_f32<T>(v);
-        ((T *)p.u)[o] = from_f32<T>(u);
+        ((T *)p.g)[o] = from_f32<T>(a[0]);
+        ((T *)p.u)[o] = from_f32<T>(b[0]);
       }
-      float a[1] = {v}, b[1] = {u};
-      with_activation(p.act, [&](auto act) { gate_values<act.value, sizeof(T) == 2, 1>(a, b); });
-      store_operand<T, 1>(p.h + o, p.sheet, a, 1, false);
+      store_operand<T, 1>(p.h + o, p.sheet, h, 1, false);
     } else {
       ((T *)p.c)[token * (int64_t)p.n + r] = from_f32<T>(v);
     }

@@ -325,13 +325,17 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
           v[k] += to_f32(((const T *)p.bias)[col + k]);
           u[k] += to_f32(((const T *)p.bias)[p.n + col + k]);
         }
-        if (p.g) {
-          ((T *)p.g)[o + k] = from_f32<T>(v[k]);
-          ((T *)p.u)[o + k] = from_f32<T>(u[k]);
-        }
       }
-      with_activation(p.act, [&](auto act) { gate_values<act.value, fast, 4>(v, u); });
-      store_operand<T, 4>(p.h + o, p.sheet, v, count, false);
+      float h[4];
+      with_activation(p.act, [&](auto act) { gate<act.value, fast, true, 4>(v, u, h); });
+      if (p.g)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < count) {
+            ((T *)p.g)[o + k] = from_f32<T>(v[k]);
+            ((T *)p.u)[o + k] = from_f32<T>(u[k]);
+          }
+      store_operand<T, 4>(p.h + o, p.sheet, h, count, false);
     } else {
       float g[4];
 #pragma unroll
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
         g[k] = k < count ? to_f32(((const T *)p.g)[o + k]) : 0.f;
         u[k] = k < count ? to_f32(((const T *)p.u)[o + k]) : 0.f;
       }
-      with_activation(p.act, [&](auto act) { gate_gradients<act.value, fast, 4>(v, g, u); });
+      gate_gradients(v, g, u);
       store_operand<T, 4>(p.h + o, 2 * p.sheet, g, count, false);
       store_operand<T, 4>(p.h + p.sheet + o, 2 * p.sheet, u, count, false);
     }
@@ -553,7 +557,7 @@ bool keeps_packed(const sla_ffn *f, int64_t cols) {
   return f->tokens > kFewTokens && (f->dtype == SLA_F32 || cols % 8 != 0);
 }
 
-// g, u (dtype) and h (operand sheets), rows hidden_pitch apart, then packed copies of x, w_in and w_out.
+// u act'(g), act(g) (dtype) and h (operand sheets), rows hidden_pitch apart, then packed copies of x, w_in and w_out.
 struct SavedLayout {
   size_t u, h, x, w_in, w_out, total;
 };

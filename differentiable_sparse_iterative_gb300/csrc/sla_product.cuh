@@ -28,8 +28,8 @@ namespace sla {
 
 enum Epilogue {
   kStore,     // c = sum (+ bias), or the float32 sums of one split of k
-  kGate,      // columns of g and u side by side: h = act(g) u, g and u kept
-  kGateBack,  // sum = dh: dg = dh u act'(g), du = dh act(g)
+  kGate,      // columns of g and u side by side: h = act(g) u; u act'(g) and act(g) kept for kGateBack
+  kGateBack,  // sum = dh: dg = dh (u act'(g)), du = dh act(g)
 };
 
 constexpr int kDepth = 64;      // k of a stage: 128 bytes, the swizzle's width
@@ -53,7 +53,7 @@ struct ProductArgs {
   int64_t ldc, c_m_half, c_n_half, c_split;
   const void *bias;          // T, [n] (kStore) or [2 n] (kGate), or NULL
   int bias_vec;              // there is one, and its values from any multiple of 16 columns are aligned to 32 bytes
-  void *g, *u;               // T [m][ldg]: written by kGate (NULL: not kept), read by kGateBack
+  void *g, *u;               // T [m][ldg]: u act'(g) and act(g), written by kGate (NULL: not kept), read by kGateBack
   uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
   int64_t ldg, sheet;        // elements between rows and between sheets of h
   float *sums;               // kGateBack: [m / 32][2][ldg] sums of dg and du over 32 rows, or NULL
@@ -62,7 +62,7 @@ struct ProductArgs {
 // Up to three products that do not depend on one another, with one tile shape (kStore; one product else).
 struct ProductLaunch {
   CUtensorMap a[kGroup], b[kGroup];
-  CUtensorMap out[3];        // kTmaStores: g, u, h, or dg and du (one map, two sheets)
+  CUtensorMap out[3];        // kTmaStores: the arrays at g, u and h, or dg and du (one map, two sheets)
   ProductArgs p[kGroup];
   int first[kGroup + 1];     // work items before each product's
   int count;
@@ -82,9 +82,9 @@ inline constexpr int kTeams = BN == 256 ? 2 : 1;
 template <int BN>
 inline constexpr int kTeamWarps = kEpilogueWarps<BN> / kTeams<BN>;
 
-// The epilogues that write arrays of this library's own (g, u, h, dg, du) in 16 bits put them together in
+// The epilogues that write arrays of this library's own (h, the factors, dg, du) in 16 bits put them together in
 // shared memory and store them by TMA: a warp that stores 32 bytes of 32 rows at a time keeps the
-// load-store unit busy for 32 cycles (it was at 78 % of its rate with g, u and h stored so).
+// load-store unit busy for 32 cycles (it was at 78 % of its rate with three arrays stored so).
 template <typename T, int EPI>
 inline constexpr bool kTmaStores = sizeof(T) == 2 && (EPI == kGate || EPI == kGateBack);
 
@@ -415,7 +415,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
     const bool live = row < p.m;
     const int first = side * width;
     // What the next columns need from memory is on its way while these are worked on, and the first
-    // columns' while the product runs.  kGateBack: g and u (rows are padded to whole sectors of 16
+    // columns' while the product runs.  kGateBack: the factors (rows are padded to whole sectors of 16
     // columns); kGate: the biases.
     RawRow<T, 16> raw_g, raw_u;
     auto ask = [&](int c) {
@@ -472,19 +472,22 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
             add_bias<T, 16>(v, (const T *)p.bias + t.n0 + c + j, count, false);
             add_bias<T, 16>(u, (const T *)p.bias + p.n + t.n0 + c + j, count, false);
           }
+          float h[16];
           if (p.g) {
+            with_activation(p.act, [&](auto act) { gate<act.value, true, true, 16>(v, u, h); });
             box0.put(j / 16, v);
             box1.put(j / 16, u);
+          } else {
+            with_activation(p.act, [&](auto act) { gate<act.value, true, false, 16>(v, u, h); });
           }
-          with_activation(p.act, [&](auto act) { gate_values<act.value, true, 16>(v, u); });
-          box0.pack(v, ph[j / 16]);
+          box0.pack(h, ph[j / 16]);
         } else {
           float g[16], u[16];
           raw_g.values(g);
           raw_u.values(u);
           if (c + j + 16 < first + width) ask(c + j + 16);
           tmem_wait(v);
-          with_activation(p.act, [&](auto act) { gate_gradients<act.value, true, 16>(v, g, u); });
+          gate_gradients(v, g, u);
           box0.put(j / 16, g);
           box1.put(j / 16, u);
           if (p.sums && row0 < p.m) {
@@ -548,7 +551,7 @@ __device__ __forceinline__ void direct_epilogue(const ProductLaunch &l, uint32_t
     const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
     const bool live = row < p.m;
     // What the next columns need from memory is on its way while these are worked on, and the first
-    // columns' while the product runs.  kGateBack: g and u (rows are padded to whole sectors of 16
+    // columns' while the product runs.  kGateBack: the factors (rows are padded to whole sectors of 16
     // columns); kGate: the biases.
     RawRow<T, N> raw_g, raw_u;
     auto ask = [&](int c) {
@@ -614,12 +617,15 @@ __device__ __forceinline__ void direct_epilogue(const ProductLaunch &l, uint32_t
             add_bias<T, N>(u, (const T *)p.bias + p.n + col, count, false);
           }
           const int64_t o = row * p.ldg + col;
+          float h[N];
           if (p.g) {
+            with_activation(p.act, [&](auto act) { gate<act.value, fast, true, N>(v, u, h); });
             store_row<T, N>((T *)p.g + o, v, count, p.vec);
             store_row<T, N>((T *)p.u + o, u, count, p.vec);
+          } else {
+            with_activation(p.act, [&](auto act) { gate<act.value, fast, false, N>(v, u, h); });
           }
-          with_activation(p.act, [&](auto act) { gate_values<act.value, fast, N>(v, u); });
-          store_operand<T, N>(p.h + o, p.sheet, v, count, p.vec);
+          store_operand<T, N>(p.h + o, p.sheet, h, count, p.vec);
         }
       } else if constexpr (EPI == kGateBack) {
         float g[N], u[N];
@@ -630,7 +636,7 @@ __device__ __forceinline__ void direct_epilogue(const ProductLaunch &l, uint32_t
         tmem_wait(v);
         if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
         if (live && count > 0) {
-          with_activation(p.act, [&](auto act) { gate_gradients<act.value, fast, N>(v, g, u); });
+          gate_gradients(v, g, u);
           // sheets: dg and du of each part of the value
           store_operand<T, N>(p.h + o, 2 * p.sheet, g, count, p.vec);
           store_operand<T, N>(p.h + p.sheet + o, 2 * p.sheet, u, count, p.vec);
