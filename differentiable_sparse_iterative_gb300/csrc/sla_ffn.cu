@@ -62,21 +62,24 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Map of boxes of box_cols columns (64, 32 or 16: a swizzle of as many bytes as a row of the box has) by
-// box_rows rows, zeros outside.
-cudaError_t encode(CUtensorMap *map, const Operand &o, int box_cols, int box_rows, bool f16) {
+// Map of boxes of box_cols columns by box_rows rows, zeros outside; the swizzle is as many bytes as a row
+// of the box has (128, 64 or 32).
+cudaError_t encode(CUtensorMap *map, const Operand &o, int box_cols, int box_rows, int32_t dtype) {
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
+  const size_t e = net_size(dtype);
   const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.sheets};
-  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)o.sheet * 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * e, (cuuint64_t)o.sheet * e};
   const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
-  const CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                        const_cast<void *>(o.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                        : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                         : CU_TENSOR_MAP_SWIZZLE_32B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUtensorMapDataType type = dtype == SLA_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == SLA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const size_t row = box_cols * e;
+  const CUtensorMapSwizzle swizzle = row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                 : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUresult r = fn(map, type, 3, const_cast<void *>(o.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -366,6 +369,7 @@ template <typename T>
 void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, float *parts) {
   if (c.err != cudaSuccess) return;
   constexpr int S = sheets_of<T>();
+  constexpr int32_t part = S == 3 ? SLA_BF16 : NetType<T>::dtype;  // type of the operands
   ProductSize sizes[kGroup];
   for (int j = 0; j < count; ++j) sizes[j] = jobs[j].s;
   const ProductPlan plan = plan_products(epi, sizes, count, S);
@@ -408,19 +412,20 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, floa
         p.a_sheet[p.segments] = (int8_t)(pairs[q][0] * a_pair + h);
         p.b_sheet[p.segments++] = (int8_t)(pairs[q][1] * b_pair + h);
       }
-    cudaError_t e = encode(&l.a[l.count], a, kDepth, p.a_mn ? kDepth : 128, p.f16);
-    if (e == cudaSuccess) e = encode(&l.b[l.count], b, kDepth, p.b_mn ? kDepth : gate ? bn / 2 : bn / tile.cg, p.f16);
-    if (sizeof(T) == 2 && epi != kStore && !split) {
+    cudaError_t e = encode(&l.a[l.count], a, kDepth, p.a_mn ? kDepth : 128, part);
+    if (e == cudaSuccess) e = encode(&l.b[l.count], b, kDepth, p.b_mn ? kDepth : gate ? bn / 2 : bn / tile.cg, part);
+    if (epi != kStore && !split) {
       // the epilogue's own arrays (see tma_epilogue); a warp's columns of the 64-wide gate tile are 16
-      const int box = gate && bn == 64 ? 16 : 32;
-      const Operand h{p.h, s.n, s.m, epi == kGate ? 1 : 2, p.ldg, p.sheet};
+      const int box = S == 3 || (gate && bn == 64) ? 16 : 32;
+      const Operand h{p.h, s.n, s.m, S * (epi == kGate ? 1 : 2), p.ldg, p.sheet};
       Operand g = h, u = h;
+      g.sheets = u.sheets = 1;
       g.p = p.g, u.p = p.u;
       if (epi == kGate && p.g) {
-        if (e == cudaSuccess) e = encode(&l.out[0], g, box, 32, p.f16);
-        if (e == cudaSuccess) e = encode(&l.out[1], u, box, 32, p.f16);
+        if (e == cudaSuccess) e = encode(&l.out[0], g, box, 32, NetType<T>::dtype);
+        if (e == cudaSuccess) e = encode(&l.out[1], u, box, 32, NetType<T>::dtype);
       }
-      if (e == cudaSuccess) e = encode(&l.out[epi == kGate ? 2 : 0], h, box, 32, p.f16);
+      if (e == cudaSuccess) e = encode(&l.out[epi == kGate ? 2 : 0], h, box, 32, part);
     }
     if (e != cudaSuccess) {
       c.err = e;
@@ -469,7 +474,8 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, floa
 
 // ------------------------------------------------------------------ column sums (bias gradients)
 
-constexpr int kSumParts = 512;  // parts of the rows at most
+constexpr int kSumParts = 512;    // parts of the rows at most
+constexpr int kDirectRows = 1024; // rows that are added up without parts
 
 // parts[part][cols]: sums over a part of the rows, VEC columns a thread; the block's threads cover
 // 256 / tpr rows at a time.  S sheets `sheet` apart are parts of one value.
@@ -505,47 +511,80 @@ __global__ void __launch_bounds__(256) column_parts(int64_t rows, int64_t cols, 
   }
 }
 
-// Sums of the parts, in order; column c of half h of `pitch` columns goes to out[h * n + c].
+// Rows of float32 to be added up, in order; column c of half h of `pitch` columns goes to out[h * n + c].
+struct AddJob {
+  const float *rows;
+  void *out;
+  int64_t cols, pitch, n;
+  int count, first;  // rows; its first block
+};
+
+struct AddJobs {
+  AddJob job[3];
+  int jobs = 0, blocks = 0;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) add_parts(int nparts, int64_t cols, int64_t pitch, int64_t n,
-                                                 const float *__restrict__ parts, T *__restrict__ out) {
-  __shared__ float sm[8][33];
+__global__ void __launch_bounds__(1024) add_rows(const __grid_constant__ AddJobs jobs) {
+  __shared__ float sm[32][33];
   grid_dependency_wait();
   grid_dependency_launch();
+  int which = 0;
+  while (which + 1 < jobs.jobs && (int)blockIdx.x >= jobs.job[which + 1].first) ++which;
+  const AddJob &j = jobs.job[which];
   const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
-  const int64_t c = blockIdx.x * 32ll + lane;
+  const int64_t c = (blockIdx.x - j.first) * 32ll + lane;
   float s = 0.f;
-  if (c < cols)
+  if (c < j.cols)
 #pragma unroll 8
-    for (int p = wy; p < nparts; p += 8) s += parts[p * cols + c];
+    for (int p = wy; p < j.count; p += 32) s += j.rows[p * j.cols + c];
   sm[wy][lane] = s;
   __syncthreads();
-  const int64_t half = c / pitch, i = c - half * pitch;
-  if (wy == 0 && c < cols && i < n) {
+  const int64_t half = c / j.pitch, i = c - half * j.pitch;
+  if (wy == 0 && c < j.cols && i < j.n) {
     float t = 0.f;
-    for (int k = 0; k < 8; ++k) t += sm[k][lane];
-    out[half * n + i] = from_f32<T>(t);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) t += sm[k][lane];
+    ((T *)j.out)[half * j.n + i] = from_f32<T>(t);
   }
 }
 
-// out = column sums of [rows][cols] (in halves of `pitch` columns, the first n of each wanted).
-template <typename E, int S, typename T>
-void column_sums(Call &c, int64_t rows, int64_t cols, const E *a, int64_t lda, int64_t sheet, int64_t pitch, int64_t n,
-                 T *out, float *parts) {
-  constexpr int V = 16 / sizeof(E);
-  const bool vec = aligned(a, 16) && lda % V == 0 && cols % V == 0 && sheet % V == 0;
-  const int64_t chunks = vec ? cols / V : cols;
-  int tpr = 1;
-  while (tpr < 32 && tpr < chunks) tpr <<= 1;
-  const int64_t tiles = (chunks + tpr - 1) / tpr;
-  // enough blocks to fill the GPU, each with at least eight turns of its threads
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kSumParts, 152 * 8 / tiles));
-  const int64_t per = std::max<int64_t>(8 * (256 / tpr), (rows + most - 1) / most);
-  const int nparts = (int)((rows + per - 1) / per);
-  const dim3 grid((unsigned)tiles, nparts);
-  c.launch(vec ? column_parts<E, S, V> : column_parts<E, S, 1>, grid, 256, rows, cols, a, lda, sheet, tpr, per, parts);
-  c.launch(add_parts<T>, dim3((unsigned)((cols + 31) / 32)), 256, nparts, cols, pitch, n, parts, out);
-}
+// Column sums of up to three matrices: each in two steps, of which the second is one launch for all.
+struct ColumnSums {
+  Call &c;
+  float *parts;  // scratch for kSumParts rows of every matrix
+  AddJobs jobs;
+  void add(const float *rows, int count, int64_t cols, int64_t pitch, int64_t n, void *out) {
+    jobs.job[jobs.jobs++] = {rows, out, cols, pitch, n, count, jobs.blocks};
+    jobs.blocks += (int)((cols + 31) / 32);
+  }
+  // out = column sums of [rows][cols] (in halves of `pitch` columns, the first n of each wanted)
+  template <typename E, int S>
+  void of(int64_t rows, int64_t cols, const E *a, int64_t lda, int64_t sheet, int64_t pitch, int64_t n, void *out) {
+    if (sizeof(E) == 4 && S == 1 && lda == cols && rows <= kDirectRows) {
+      add((const float *)a, (int)rows, cols, pitch, n, out);
+      return;
+    }
+    constexpr int V = 16 / sizeof(E);
+    const bool vec = aligned(a, 16) && lda % V == 0 && cols % V == 0 && sheet % V == 0;
+    const int64_t chunks = vec ? cols / V : cols;
+    int tpr = 1;
+    while (tpr < 32 && tpr < chunks) tpr <<= 1;
+    const int64_t tiles = (chunks + tpr - 1) / tpr;
+    // enough blocks to fill the GPU, each with at least eight turns of its threads
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kSumParts, 152 * 8 / tiles));
+    const int64_t per = std::max<int64_t>(8 * (256 / tpr), (rows + most - 1) / most);
+    const int nparts = (int)((rows + per - 1) / per);
+    c.launch(vec ? column_parts<E, S, V> : column_parts<E, S, 1>, dim3((unsigned)tiles, nparts), 256, rows, cols, a, lda,
+             sheet, tpr, per, parts);
+    add(parts, nparts, cols, pitch, n, out);
+    parts += kSumParts * cols;
+  }
+  template <typename T>
+  void finish() {
+    if (jobs.jobs) c.launch(add_rows<T>, dim3(jobs.blocks), 1024, jobs);
+  }
+};
 
 // ------------------------------------------------------------------ buffers
 
@@ -604,7 +643,7 @@ ForwardScratch forward_scratch(const sla_ffn *f, char *base) {
 
 struct BackwardScratch {
   void *dy, *x, *w_in, *w_out, *dgu;
-  float *sums, *parts;
+  float *sums, *columns, *parts;
   size_t total;
 };
 
@@ -618,7 +657,8 @@ BackwardScratch backward_scratch(const sla_ffn *f, char *base) {
   w.w_out = a.take(packed_bytes(f->out, f->hidden, f->dtype));
   w.dgu = a.take((size_t)f->tokens * (size_t)hidden_pitch(f) * 2 * 2 * S);
   w.sums = (float *)a.take((size_t)((f->tokens + 31) / 32) * 2 * (size_t)hidden_pitch(f) * sizeof(float));
-  size_t parts = kSumParts * sizeof(float) * (size_t)std::max(2 * hidden_pitch(f), f->out);
+  w.columns = (float *)a.take(kSumParts * sizeof(float) * (size_t)(2 * hidden_pitch(f) + f->out));
+  size_t parts = 0;
   const ProductSize dh = dh_size(f), rest[kGroup] = {dx_size(f), dw_in_size(f), dw_out_size(f)};
   parts = std::max(parts, plan_products(kGateBack, &dh, 1, S).partial[1]);
   parts = std::max(parts, plan_products(kStore, rest, kGroup, S).partial[kGroup]);
@@ -707,6 +747,7 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
   run_packs<T>(c, packs);
   const Operand odgu{w.dgu, f->hidden, f->tokens, 2 * S, ldg, sheet};
   const Operand oh{saved + L.h, f->hidden, f->tokens, S, ldg, sheet};
+  ColumnSums columns{c, w.columns, {}};
   if (inner) {
     ProductJob dh{dh_size(f), ody, false, oo, true, {}, true};
     dh.p.act = f->activation, dh.p.vec = 1;
@@ -716,12 +757,14 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
     if (db_in && plan_products(kGateBack, &dh.s, 1, S).splits[0] == 1) dh.p.sums = w.sums;
     run_products<T>(c, kGateBack, &dh, 1, w.parts);
     if (dh.p.sums)
-      column_sums<float, 1>(c, (f->tokens + 31) / 32, 2 * ldg, w.sums, 2 * ldg, 0, ldg, f->hidden, db_in, w.parts);
+      columns.of<float, 1>((f->tokens + 31) / 32, 2 * ldg, w.sums, 2 * ldg, 0, ldg, f->hidden, db_in);
     else if (db_in)
       for (int half = 0; half < 2; ++half)
-        column_sums<E, S>(c, f->tokens, f->hidden, (const E *)w.dgu + half * sheet, ldg, 2 * sheet, f->hidden,
-                          f->hidden, db_in + half * f->hidden, w.parts);
+        columns.of<E, S>(f->tokens, f->hidden, (const E *)w.dgu + half * sheet, ldg, 2 * sheet, f->hidden, f->hidden,
+                         db_in + half * f->hidden);
   }
+  if (db_out) columns.of<T, 1>(f->tokens, f->out, dy, lddy, 0, f->out, f->out, db_out);
+  columns.finish<T>();
   auto job = [&](const ProductSize &s, const Operand &a, bool a_mn, const Operand &b, T *out) {
     ProductJob j{s, a, a_mn, b, true, {}, out != nullptr};
     j.p.c = out, j.p.ldc = s.n, j.p.c_m_half = s.m * s.n, j.p.vec = vec_out(out, s.n);
@@ -730,7 +773,6 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
   const ProductJob rest[kGroup] = {job(dx_size(f), odgu, false, oi, dx), job(dw_in_size(f), odgu, true, ox, dw_in),
                                    job(dw_out_size(f), ody, true, oh, dw_out)};
   run_products<T>(c, kStore, rest, kGroup, w.parts);
-  if (db_out) column_sums<T, 1>(c, f->tokens, f->out, dy, lddy, 0, f->out, f->out, db_out, w.parts);
   return finish(c);
 }
 

@@ -48,7 +48,7 @@ struct ProductArgs {
   int a_mn, b_mn;
   int f16;                   // operands are float16 (else bfloat16)
   int act;
-  int vec;                   // rows of c are aligned to 32 bytes (those of g, u and h always are)
+  int vec;                   // rows of c are aligned to 32 bytes
   void *c;                   // kStore: T, or with splits float [splits][..]
   int64_t ldc, c_m_half, c_n_half, c_split;
   const void *bias;          // T, [n] (kStore) or [2 n] (kGate), or NULL
@@ -70,38 +70,43 @@ struct ProductLaunch {
   uint32_t *timeouts;
 };
 
-// Warps that empty the accumulators: each waits on tensor memory and on global memory in turn, so the
-// widest tiles, whose epilogue would else outlast their products, take sixteen.
-template <int BN>
-inline constexpr int kEpilogueWarps = BN == 256 ? 16 : 8;
+// Warps that empty the accumulators: each waits on tensor memory, on global memory and on the special
+// function unit in turn, so the widest 16-bit tiles, whose epilogue would else outlast their products, take
+// sixteen.  (float32's need the registers of eight, and their products take six times as long.)
+template <typename T, int BN>
+inline constexpr int kEpilogueWarps = BN == 256 && sizeof(T) == 2 ? 16 : 8;
 
 // Teams of epilogue warps, which take the tiles in turn: while one waits (for the accumulator, for its
-// stores) the other computes.  The smaller tiles, of which a block often has one, get all warps together.
-template <int BN>
-inline constexpr int kTeams = BN == 256 ? 2 : 1;
-template <int BN>
-inline constexpr int kTeamWarps = kEpilogueWarps<BN> / kTeams<BN>;
+// stores) the other computes.  Elsewhere all warps share a tile: a block often has but one.
+template <typename T, int BN>
+inline constexpr int kTeams = kEpilogueWarps<T, BN> / 8;
 
-// The epilogues that write arrays of this library's own (h, the factors, dg, du) in 16 bits put them together in
-// shared memory and store them by TMA: a warp that stores 32 bytes of 32 rows at a time keeps the
-// load-store unit busy for 32 cycles (it was at 78 % of its rate with three arrays stored so).
-template <typename T, int EPI>
-inline constexpr bool kTmaStores = sizeof(T) == 2 && (EPI == kGate || EPI == kGateBack);
+// Columns that one warp of the epilogue takes.
+template <typename T, int EPI, int BN>
+inline constexpr int kWarpColumns = (EPI == kGate ? BN / 2 : BN) / 2;
 
-// Columns that one warp of the epilogue takes, and those of one store.
-template <int EPI, int BN>
-inline constexpr int kWarpColumns = (EPI == kGate ? BN / 2 : BN) / (kTeamWarps<BN> / 4);
-template <int EPI, int BN>
-inline constexpr int kStoreColumns = kWarpColumns<EPI, BN> < 32 ? kWarpColumns<EPI, BN> : 32;
+// The epilogues that write arrays of this library's own (h, the factors, dg, du) put them together in
+// shared memory, in boxes of 32 rows, and store them by TMA: a warp that stores 32 bytes of 32 rows at a
+// time keeps the load-store unit busy for 32 cycles (it was at 78 % of its rate with three arrays
+// stored so).
+template <int EPI>
+inline constexpr bool kTmaStores = EPI == kGate || EPI == kGateBack;
+
+// Columns of one store: 64 bytes a row, or 16 columns of float32 (64 bytes) and of its sheets (32 bytes).
+template <typename T, int EPI, int BN>
+inline constexpr int kStoreColumns = sizeof(T) == 4 || kWarpColumns<T, EPI, BN> < 32 ? 16 : 32;
 
 // Tile shapes: CG blocks of 128 rows, BN columns, stages that fill what the stores leave of a multiprocessor's
-// shared memory (two boxes of 32 rows a warp).
+// shared memory.
 template <typename T, int EPI, int CG, int BN>
 struct ProductShape {
   static constexpr int a_bytes = 128 * kDepth * 2;
   static constexpr int b_bytes = BN / CG * kDepth * 2;
-  static constexpr int box = 32 * kStoreColumns<EPI, BN> * 2;
-  static constexpr int boxes = kTmaStores<T, EPI> ? kEpilogueWarps<BN> * 2 * box : 0;
+  // a warp's boxes: 16-bit data two, which it uses again and again; float32 two of factors and three of h, or
+  // three each of dg and du
+  static constexpr int box = 32 * kStoreColumns<T, EPI, BN> * 2;
+  static constexpr int warp_boxes = !kTmaStores<EPI> ? 0 : sizeof(T) == 2 ? 2 * box : EPI == kGate ? 7 * box : 6 * box;
+  static constexpr int boxes = kEpilogueWarps<T, BN> * warp_boxes;
   static constexpr int room = (225 * 1024 - boxes) / (a_bytes + b_bytes);
   static constexpr int stages = room > 8 ? 8 : room;
   static constexpr int smem = stages * (a_bytes + b_bytes) + boxes + 1024 /* alignment */ + 256 /* barriers */;
@@ -356,45 +361,63 @@ __device__ __forceinline__ void release_accumulator(uint64_t *acc_empty, int lan
   }
 }
 
-// A box of 32 rows and W 16-bit columns in shared memory, thread = row, in TMA's swizzle for rows of W * 2
-// bytes: units of 16 bytes (8 columns) change places within their row, so that writing them meets no bank
-// conflicts.
-template <typename T, int W>
+// A box of 32 rows in shared memory, thread = row, in TMA's swizzle for rows of `Bytes` bytes: units of 16
+// bytes change places within their row, so that writing them meets no bank conflicts.
+template <int Bytes>
 struct StoreBox {
-  static constexpr int units = W / 8;
-  uint4 *sm;
+  static constexpr int units = Bytes / 16;
+  uint8_t *sm;
   int lane;
+  __device__ __forceinline__ void put(int unit, uint4 q) const {
+    reinterpret_cast<uint4 *>(sm)[lane * units + (unit ^ ((lane / (8 / units)) & (units - 1)))] = q;
+  }
+  // 16 columns of the thread's row: 16 bits from column 16 * part, or float32
   __device__ __forceinline__ void put(int part, const uint32_t (&w)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int unit = 2 * part + i;
-      sm[lane * units + (unit ^ ((lane / (8 / units)) & (units - 1)))] =
-          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
+    for (int i = 0; i < 2; ++i) put(2 * part + i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
   }
-  // 16 columns of the thread's row from column 16 * part
-  __device__ __forceinline__ void put(int part, const float (&v)[16]) const {
-    uint32_t w[8];
-    pack(v, w);
-    put(part, w);
-  }
-  static __device__ __forceinline__ void pack(const float (&v)[16], uint32_t (&w)[8]) {
+  __device__ __forceinline__ void put(const float (&v)[16]) const {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = pair16(v[2 * k], v[2 * k + 1], T{});
+    for (int i = 0; i < 4; ++i)
+      put(i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                        __float_as_uint(v[4 * i + 3])));
   }
 };
 
-// kGate and kGateBack in 16 bits: 16 columns at a time, stored in boxes of W.
+template <typename T>
+__device__ __forceinline__ void pack16(const float (&v)[16], uint32_t (&w)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = pair16(v[2 * k], v[2 * k + 1], T{});
+}
+
+// float32's three sheets of 16 columns into boxes `apart` bytes apart.
+__device__ __forceinline__ void put_sheets(uint8_t *box, int apart, int lane, const float (&v)[16]) {
+  uint32_t w[3][8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint16_t a[3], b[3];
+    split3(v[2 * k], a);
+    split3(v[2 * k + 1], b);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) w[q][k] = a[q] | ((uint32_t)b[q] << 16);
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) StoreBox<32>{box + q * apart, lane}.put(0, w[q]);
+}
+
+// kGate and kGateBack: 16 columns at a time, stored in boxes of W.
 template <typename T, int EPI, int CG, int BN>
 __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tmem, uint8_t *boxes, uint64_t *acc_full,
                                              uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
                                              uint32_t rank) {
   const ProductArgs &p = l.p[0];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, team = (warp - 2) / kTeamWarps<BN>, side = (warp - 2) % kTeamWarps<BN> / 4;
-  constexpr int width = kWarpColumns<EPI, BN>, W = kStoreColumns<EPI, BN>, box = ProductShape<T, EPI, CG, BN>::box;
-  uint8_t *mine = boxes + (warp - 2) * 2 * box;
-  const StoreBox<T, W> box0{(uint4 *)mine, lane}, box1{(uint4 *)(mine + box), lane};
+  const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
+  constexpr int width = kWarpColumns<T, EPI, BN>, W = kStoreColumns<T, EPI, BN>, box = ProductShape<T, EPI, CG, BN>::box;
+  constexpr bool f32 = sizeof(T) == 4;
+  uint8_t *mine = boxes + (warp - 2) * ProductShape<T, EPI, CG, BN>::warp_boxes;
+  const StoreBox<f32 ? 64 : 2 * W> box0{mine, lane}, box1{mine + (f32 ? 2 * box : box), lane};
+  uint8_t *sheets = mine + (EPI == kGate ? 4 * box : 0);  // float32: of h, or of dg and then of du
   // boxes 0 and 1 hold what the warp's lanes have put there: to columns x.. of rows y.. of two maps or sheets
   auto store2 = [&](const CUtensorMap *m0, const CUtensorMap *m1, int x, int y, int z1) {
     fence_proxy_async_smem();
@@ -406,7 +429,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
       tma_store_commit();
     }
   };
-  for (int tile = team;; tile += kTeams<BN>) {
+  for (int tile = team;; tile += kTeams<T, BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
     const Tile t = tile_of<EPI, CG, BN>(p, item);
@@ -474,13 +497,24 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
           }
           float h[16];
           if (p.g) {
-            with_activation(p.act, [&](auto act) { gate<act.value, true, true, 16>(v, u, h); });
-            box0.put(j / 16, v);
-            box1.put(j / 16, u);
+            with_activation(p.act, [&](auto act) { gate<act.value, !f32, true, 16>(v, u, h); });
+            if constexpr (f32) {
+              box0.put(v);
+              box1.put(u);
+            } else {
+              uint32_t w[8];
+              pack16<T>(v, w);
+              box0.put(j / 16, w);
+              pack16<T>(u, w);
+              box1.put(j / 16, w);
+            }
           } else {
-            with_activation(p.act, [&](auto act) { gate<act.value, true, false, 16>(v, u, h); });
+            with_activation(p.act, [&](auto act) { gate<act.value, !f32, false, 16>(v, u, h); });
           }
-          box0.pack(h, ph[j / 16]);
+          if constexpr (f32)
+            put_sheets(sheets, box, lane, h);
+          else
+            pack16<T>(h, ph[j / 16]);
         } else {
           float g[16], u[16];
           raw_g.values(g);
@@ -488,8 +522,16 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
           if (c + j + 16 < first + width) ask(c + j + 16);
           tmem_wait(v);
           gate_gradients(v, g, u);
-          box0.put(j / 16, g);
-          box1.put(j / 16, u);
+          if constexpr (f32) {
+            put_sheets(sheets, box, lane, g);
+            put_sheets(sheets + 3 * box, box, lane, u);
+          } else {
+            uint32_t w[8];
+            pack16<T>(g, w);
+            box0.put(j / 16, w);
+            pack16<T>(u, w);
+            box1.put(j / 16, w);
+          }
           if (p.sums && row0 < p.m) {
             if (!live) {  // not a row: its product is no zero if a weight is infinite
 #pragma unroll
@@ -506,10 +548,26 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
       }
       if (last) release_accumulator<CG>(acc_empty + acc, lane);
       if (!some) continue;
-      if constexpr (EPI == kGate) {
+      if constexpr (f32) {
+        if (EPI == kGate && p.g) store2(&l.out[0], &l.out[1], t.n0 + c, row0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            if (EPI == kGate) {
+              tma_store(&l.out[2], t.n0 + c, row0, q, sheets + q * box);
+            } else {  // the sheets of dgu come in pairs: dg and du of each part of the value
+              tma_store(&l.out[0], t.n0 + c, row0, 2 * q, sheets + q * box);
+              tma_store(&l.out[0], t.n0 + c, row0, 2 * q + 1, sheets + (3 + q) * box);
+            }
+          }
+          tma_store_commit();
+        }
+      } else if constexpr (EPI == kGate) {
         if (p.g) {
           store2(&l.out[0], &l.out[1], t.n0 + c, row0, 0);
-          if (lane == 0) tma_store_read<1>();  // g's box is free again
+          if (lane == 0) tma_store_read<1>();  // box 0 is free again
           __syncwarp();
         }
 #pragma unroll
@@ -529,58 +587,24 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
   __syncwarp();
 }
 
-// Straight from the registers: results in the caller's arrays (kStore), which TMA may not be able to write,
-// and float32's.
-template <typename T, int EPI, int CG, int BN>
-__device__ __forceinline__ void direct_epilogue(const ProductLaunch &l, uint32_t tmem, uint64_t *acc_full,
-                                                uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
-                                                uint32_t rank) {
+// kStore: straight from the registers, since TMA may not be able to write the caller's arrays.
+template <typename T, int CG, int BN>
+__device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t tmem, uint64_t *acc_full,
+                                               uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
+                                               uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, team = (warp - 2) / kTeamWarps<BN>, side = (warp - 2) % kTeamWarps<BN> / 4;
-  // columns of this warp, N at a time (as many as the registers hold: 112 a thread with sixteen warps)
-  constexpr int width = kWarpColumns<EPI, BN>;
-  constexpr int N = BN == 256 || width == 16 || EPI != kStore ? 16 : 32;
-  constexpr bool fast = sizeof(T) == 2;
-  for (int tile = team;; tile += kTeams<BN>) {
+  const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
+  // columns of this warp, N at a time (as many as the registers hold: 96 a thread with sixteen warps)
+  constexpr int width = kWarpColumns<T, kStore, BN>;
+  constexpr int N = kEpilogueWarps<T, BN> == 16 ? 16 : 32;
+  for (int tile = team;; tile += kTeams<T, BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
-    const int which = EPI == kStore ? product_of(l, item) : 0;
-    const ProductArgs &p = l.p[which];
-    const Tile t = tile_of<EPI, CG, BN>(p, item);
+    const ProductArgs &p = l.p[product_of(l, item)];
+    const Tile t = tile_of<kStore, CG, BN>(p, item);
     const uint32_t acc = tile & 1;
     const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
     const bool live = row < p.m;
-    // What the next columns need from memory is on its way while these are worked on, and the first
-    // columns' while the product runs.  kGateBack: the factors (rows are padded to whole sectors of 16
-    // columns); kGate: the biases.
-    RawRow<T, N> raw_g, raw_u;
-    auto ask = [&](int c) {
-      if (EPI == kGate) {
-        if (p.bias_vec && t.n0 + c + N <= p.n) {
-          raw_g.load((const T *)p.bias + t.n0 + c);
-          raw_u.load((const T *)p.bias + p.n + t.n0 + c);
-        }
-        return;
-      }
-      const int64_t o = row * p.ldg + t.n0 + c;
-      if (live && t.n0 + c + N <= p.ldg) {
-        raw_g.load((const T *)p.g + o);
-        raw_u.load((const T *)p.u + o);
-      } else {
-        raw_g.clear();
-        raw_u.clear();
-        if (N == 32 && live && t.n0 + c < p.ldg) {  // half of the columns are there
-          RawRow<T, 16> half;
-          half.load((const T *)p.g + o);
-#pragma unroll
-          for (int i = 0; i < half.n; ++i) raw_g.s[i] = half.s[i];
-          half.load((const T *)p.u + o);
-#pragma unroll
-          for (int i = 0; i < half.n; ++i) raw_u.s[i] = half.s[i];
-        }
-      }
-    };
-    if constexpr (EPI == kGateBack || EPI == kGate) ask(side * width);
     if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
       *dead = 1;
       break;
@@ -595,71 +619,15 @@ __device__ __forceinline__ void direct_epilogue(const ProductLaunch &l, uint32_t
         tmem_load32(base + c, v);
       else
         tmem_load16(base + c, v);
-      if constexpr (EPI == kGate) {
-        float u[N];
-        if constexpr (N == 32)
-          tmem_load32(base + BN / 2 + c, u);
-        else
-          tmem_load16(base + BN / 2 + c, u);
-        float bg[N], bu[N];
-        raw_g.values(bg);
-        raw_u.values(bu);
-        if (c + N < (side + 1) * width) ask(c + N);
-        tmem_wait(v);
-        tmem_wait(u);
-        if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
-        if (live && count > 0) {
-          if (p.bias_vec && count >= N) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += bg[i], u[i] += bu[i];
-          } else if (p.bias) {
-            add_bias<T, N>(v, (const T *)p.bias + col, count, false);
-            add_bias<T, N>(u, (const T *)p.bias + p.n + col, count, false);
-          }
-          const int64_t o = row * p.ldg + col;
-          float h[N];
-          if (p.g) {
-            with_activation(p.act, [&](auto act) { gate<act.value, fast, true, N>(v, u, h); });
-            store_row<T, N>((T *)p.g + o, v, count, p.vec);
-            store_row<T, N>((T *)p.u + o, u, count, p.vec);
-          } else {
-            with_activation(p.act, [&](auto act) { gate<act.value, fast, false, N>(v, u, h); });
-          }
-          store_operand<T, N>(p.h + o, p.sheet, h, count, p.vec);
-        }
-      } else if constexpr (EPI == kGateBack) {
-        float g[N], u[N];
-        const int64_t o = row * p.ldg + col;
-        raw_g.values(g);
-        raw_u.values(u);
-        if (c + N < (side + 1) * width) ask(c + N);
-        tmem_wait(v);
-        if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
-        if (live && count > 0) {
-          gate_gradients(v, g, u);
-          // sheets: dg and du of each part of the value
-          store_operand<T, N>(p.h + o, 2 * p.sheet, g, count, p.vec);
-          store_operand<T, N>(p.h + p.sheet + o, 2 * p.sheet, u, count, p.vec);
-        }
-        if (p.sums && row - lane < p.m) {
-          const float sg = sum_columns(g, lane), su = sum_columns(u, lane);
-          if (lane < N && lane < count) {
-            float *to = p.sums + (int64_t)(row >> 5) * 2 * p.ldg + col + lane;
-            to[0] = sg;
-            to[p.ldg] = su;
-          }
-        }
-      } else {
-        tmem_wait(v);
-        if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
-        if (live && count > 0) {
-          const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
-          if (p.splits > 1) {
-            store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
-          } else {
-            if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
-            store_row<T, N>((T *)p.c + o, v, count, p.vec);
-          }
+      tmem_wait(v);
+      if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
+      if (live && count > 0) {
+        const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
+        if (p.splits > 1) {
+          store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
+        } else {
+          if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
+          store_row<T, N>((T *)p.c + o, v, count, p.vec);
         }
       }
     }
@@ -667,7 +635,7 @@ __device__ __forceinline__ void direct_epilogue(const ProductLaunch &l, uint32_t
 }
 
 template <typename T, int EPI, int CG, int BN>
-__global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
+__global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
     product_kernel(const __grid_constant__ ProductLaunch l) {
   using Shape = ProductShape<T, EPI, CG, BN>;
   constexpr int S = Shape::stages;
@@ -691,7 +659,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, kTeamWarps<BN> * CG);
+      mbar_init(acc_empty + i, 8 * CG);
     }
     mbar_init(drained, 1);
     *dead = 0;
@@ -816,10 +784,10 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<BN>, 1)
       mbar_wait_clocks(drained, 0);
     }
   } else if (warp >= 2) {
-    if constexpr (kTmaStores<T, EPI>)
+    if constexpr (kTmaStores<EPI>)
       tma_epilogue<T, EPI, CG, BN>(l, tmem, boxes, acc_full, acc_empty, dead, worker, workers, rank);
     else
-      direct_epilogue<T, EPI, CG, BN>(l, tmem, acc_full, acc_empty, dead, worker, workers, rank);
+      store_epilogue<T, CG, BN>(l, tmem, acc_full, acc_empty, dead, worker, workers, rank);
   }
   __syncwarp();
   tc_fence_before();
@@ -856,7 +824,7 @@ cudaError_t launch_product_as(int blocks, const ProductLaunch &l, bool early, cu
     if (e == cudaSuccess) allowed.fetch_or(1ull << (dev & 63));
   }
   if (e != cudaSuccess) return e;
-  LaunchConfig cfg(dim3(blocks), 64 + 32 * kEpilogueWarps<BN>, smem, st, early, CG);
+  LaunchConfig cfg(dim3(blocks), 64 + 32 * kEpilogueWarps<T, BN>, smem, st, early, CG);
   return cudaLaunchKernelEx(&cfg.c, kernel, l);
 }
 
