@@ -215,8 +215,10 @@ struct ProductPlan {
 ProductPlan plan_products(Epilogue epi, const ProductSize *s, int count, int sheets) {
   static const double block_us[kProductTileCount] = {0.27, 0.225, 0.255, 0.245};
   static const double start_us[kProductTileCount] = {5.0, 5.0, 3.0, 3.0};
-  static const double epilogue_us[3][kProductTileCount] = {
-      {2.1, 1.25, 1.25, 0.8}, {3.4, 1.8, 1.8, 1.15}, {11.0, 5.9, 5.9, 3.4}};  // kStore, kGate, kGateBack
+  static const double epilogues_us[2][3][kProductTileCount] = {
+      {{2.1, 1.25, 1.25, 0.8}, {3.0, 1.8, 1.8, 1.15}, {10.0, 5.5, 5.5, 3.0}},   // kStore, kGate, kGateBack
+      {{3.0, 1.6, 1.6, 0.9}, {9.0, 4.5, 4.5, 2.3}, {11.0, 6.0, 6.0, 3.0}}};     // float32
+  const auto &epilogue_us = epilogues_us[sheets == 3];
   const int sms = sm_count();
   ProductPlan best{};
   double best_us = 1e30;

@@ -62,7 +62,7 @@ struct ProductArgs {
 // Up to three products that do not depend on one another, with one tile shape (kStore; one product else).
 struct ProductLaunch {
   CUtensorMap a[kGroup], b[kGroup];
-  CUtensorMap out[3];        // kTmaStores: the arrays at g, u and h, or dg and du (one map, two sheets)
+  CUtensorMap out[3];        // kGate, kGateBack: the arrays at g, u and h, or dg and du (one map, two sheets)
   ProductArgs p[kGroup];
   int first[kGroup + 1];     // work items before each product's
   int count;
@@ -89,12 +89,17 @@ inline constexpr int kWarpColumns = (EPI == kGate ? BN / 2 : BN) / 2;
 // shared memory, in boxes of 32 rows, and store them by TMA: a warp that stores 32 bytes of 32 rows at a
 // time keeps the load-store unit busy for 32 cycles (it was at 78 % of its rate with three arrays
 // stored so).
-template <int EPI>
-inline constexpr bool kTmaStores = EPI == kGate || EPI == kGateBack;
-
+//
 // Columns of one store: 64 bytes a row, or 16 columns of float32 (64 bytes) and of its sheets (32 bytes).
 template <typename T, int EPI, int BN>
 inline constexpr int kStoreColumns = sizeof(T) == 4 || kWarpColumns<T, EPI, BN> < 32 ? 16 : 32;
+
+// kStore: columns of a turn (as many as the registers hold: 96 a thread with sixteen warps), and the bytes from
+// row to row of the transposing buffer: an odd number of words, so that neither rows nor columns meet bank conflicts.
+template <typename T, int BN>
+inline constexpr int kTurnColumns = kEpilogueWarps<T, BN> == 16 ? 16 : 32;
+template <typename T, int BN>
+inline constexpr int kRowBytes = kTurnColumns<T, BN> * sizeof(T) + 4;
 
 // Tile shapes: CG blocks of 128 rows, BN columns, stages that fill what the stores leave of a multiprocessor's
 // shared memory.
@@ -105,8 +110,11 @@ struct ProductShape {
   // a warp's boxes: 16-bit data two, which it uses again and again; float32 two of factors and three of h, or
   // three each of dg and du
   static constexpr int box = 32 * kStoreColumns<T, EPI, BN> * 2;
-  static constexpr int warp_boxes = !kTmaStores<EPI> ? 0 : sizeof(T) == 2 ? 2 * box : EPI == kGate ? 7 * box : 6 * box;
-  static constexpr int boxes = kEpilogueWarps<T, BN> * warp_boxes;
+  static constexpr int warp_boxes = EPI == kStore      ? 32 * kRowBytes<T, BN>
+                                    : sizeof(T) == 2   ? 2 * box
+                                    : EPI == kGate     ? 7 * box
+                                                       : 6 * box;
+  static constexpr int boxes = (kEpilogueWarps<T, BN> * warp_boxes + 1023) / 1024 * 1024;
   static constexpr int room = (225 * 1024 - boxes) / (a_bytes + b_bytes);
   static constexpr int stages = room > 8 ? 8 : room;
   static constexpr int smem = stages * (a_bytes + b_bytes) + boxes + 1024 /* alignment */ + 256 /* barriers */;
@@ -587,16 +595,17 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
   __syncwarp();
 }
 
-// kStore: straight from the registers, since TMA may not be able to write the caller's arrays.
+// kStore: straight from the registers, since TMA may not be able to write the caller's arrays.  Rows that are
+// not aligned to whole sectors would take a store an element, each to 32 lines: they go through shared
+// memory, so that a warp's stores run along the rows (2049 x 131 outputs: 16 -> 10 us).
 template <typename T, int CG, int BN>
-__device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t tmem, uint64_t *acc_full,
-                                               uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
+__device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t tmem, uint8_t *boxes,
+                                               uint64_t *acc_full, uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
                                                uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
-  // columns of this warp, N at a time (as many as the registers hold: 96 a thread with sixteen warps)
-  constexpr int width = kWarpColumns<T, kStore, BN>;
-  constexpr int N = kEpilogueWarps<T, BN> == 16 ? 16 : 32;
+  constexpr int width = kWarpColumns<T, kStore, BN>, N = kTurnColumns<T, BN>, pitch = kRowBytes<T, BN>;
+  uint8_t *mine = boxes + (warp - 2) * 32 * pitch;
   for (int tile = team;; tile += kTeams<T, BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
@@ -627,8 +636,28 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
           store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
         } else {
           if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
-          store_row<T, N>((T *)p.c + o, v, count, p.vec);
+          if (p.vec && count >= N) store_row<T, N>((T *)p.c + o, v, count, true);
         }
+      }
+      if (p.splits == 1 && !(p.vec && count >= N) && count > 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4 / sizeof(T)) {
+          uint32_t w;
+          if constexpr (sizeof(T) == 4)
+            w = __float_as_uint(v[i]);
+          else
+            w = pair16(v[i], v[i + 1], T{});
+          *reinterpret_cast<uint32_t *>(mine + lane * pitch + i * sizeof(T)) = w;
+        }
+        __syncwarp();
+        const int rows = p.m - (row - lane);
+        T *out = (T *)p.c + t.m_half * p.c_m_half + t.n_half * p.c_n_half + (row - lane) * p.ldc + col;
+#pragma unroll 8
+        for (int i = 0; i < N; ++i) {
+          const int r = (i * 32 + lane) / N, k = (i * 32 + lane) % N;
+          if (r < rows && k < count) out[r * p.ldc + k] = *reinterpret_cast<const T *>(mine + r * pitch + k * sizeof(T));
+        }
+        __syncwarp();
       }
     }
   }
@@ -784,10 +813,10 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
       mbar_wait_clocks(drained, 0);
     }
   } else if (warp >= 2) {
-    if constexpr (kTmaStores<EPI>)
+    if constexpr (EPI != kStore)
       tma_epilogue<T, EPI, CG, BN>(l, tmem, boxes, acc_full, acc_empty, dead, worker, workers, rank);
     else
-      store_epilogue<T, CG, BN>(l, tmem, acc_full, acc_empty, dead, worker, workers, rank);
+      store_epilogue<T, CG, BN>(l, tmem, boxes, acc_full, acc_empty, dead, worker, workers, rank);
   }
   __syncwarp();
   tc_fence_before();
