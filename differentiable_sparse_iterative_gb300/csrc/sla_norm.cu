@@ -16,11 +16,11 @@
 // kernel.  No atomics: the same call gives the same bits.
 //
 // Widths that no vector divides: row r starts (r * width) mod VEC elements behind a 16-byte boundary,
-// which repeats every `classes` = VEC / gcd(width, VEC) rows.  A block takes the rows of one class; its
-// vectors are the aligned ones, shifted by that many columns, and only the first and the last of a
-// row are moved element by element.  Arrays whose rows do not start at the same boundary (strided or
-// odd views) and rows wider than the registers of a 512-thread block hold take the *_any kernels,
-// which read element by element and re-read from L2.
+// which repeats every `classes` = VEC / gcd(width, VEC) rows.  A block takes the rows of one class, so its
+// threads keep their columns: the aligned vectors inside of the row, and one element each of the at
+// most VEC - 1 before and after them (Edge).  Arrays whose rows do not start at the same boundary (strided
+// or odd views) and rows wider than the registers of a 512-thread block hold take the *_any
+// kernels, which read element by element and re-read from L2.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -90,17 +90,7 @@ template <typename T>
 struct Vec {
   static constexpr int n = 16 / sizeof(T), pairs = n / 2;
   uint4 q;
-  // Elements [c, c + n) of a row of `width`, of which those outside are 0.
-  __device__ __forceinline__ void load(const T *row, int c, int width) {
-    if (c >= 0 && c + n <= width) {
-      q = *reinterpret_cast<const uint4 *>(row + c);
-      return;
-    }
-    Pack<T, n> e;
-#pragma unroll
-    for (int k = 0; k < n; ++k) e.v[k] = c + k >= 0 && c + k < width ? row[c + k] : from_f32<T>(0.f);
-    q = *reinterpret_cast<uint4 *>(&e);
-  }
+  __device__ __forceinline__ void load(const T *p) { q = *reinterpret_cast<const uint4 *>(p); }
   __device__ __forceinline__ void values(float2 (&v)[pairs]) const {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
     if constexpr (sizeof(T) == 4) {
@@ -111,35 +101,26 @@ struct Vec {
       for (int k = 0; k < 4; ++k) v[k] = unpair16(w[k], T{});
     }
   }
-  static __device__ __forceinline__ void store(T *row, int c, int width, const float2 (&v)[pairs]) {
-    if (c >= 0 && c + n <= width) {
-      uint4 q;
-      if constexpr (sizeof(T) == 4)
-        q = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
-                       __float_as_uint(v[1].y));
-      else
-        q = make_uint4(pair16(v[0].x, v[0].y, T{}), pair16(v[1].x, v[1].y, T{}), pair16(v[2].x, v[2].y, T{}),
-                       pair16(v[3].x, v[3].y, T{}));
-      *reinterpret_cast<uint4 *>(row + c) = q;
-      return;
-    }
-#pragma unroll
-    for (int k = 0; k < n; ++k)
-      if (c + k >= 0 && c + k < width) row[c + k] = from_f32<T>(k & 1 ? v[k / 2].y : v[k / 2].x);
+  static __device__ __forceinline__ void store(T *p, const float2 (&v)[pairs]) {
+    uint4 q;
+    if constexpr (sizeof(T) == 4)
+      q = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+    else
+      q = make_uint4(pair16(v[0].x, v[0].y, T{}), pair16(v[1].x, v[1].y, T{}), pair16(v[2].x, v[2].y, T{}),
+                     pair16(v[3].x, v[3].y, T{}));
+    *reinterpret_cast<uint4 *>(p) = q;
   }
 };
 
-// Columns [c, c + 2 PAIRS) of a parameter as pairs, `other` where there is none and 0 outside of the row.
-// vec: whole vectors may be read at once.
+// Columns [c, c + 2 PAIRS) of a parameter as pairs, `other` where there is none.  vec: they may be read at once.
 template <typename P, int PAIRS>
-__device__ __forceinline__ void param_pairs(const P *p, int c, int width, float other, bool vec, float2 (&v)[PAIRS]) {
+__device__ __forceinline__ void param_pairs(const P *p, int c, bool in, float other, bool vec, float2 (&v)[PAIRS]) {
   float e[2 * PAIRS];
-  if (vec && p && c < width) {
+  if (vec && p && in) {
     load_f32<P, 2 * PAIRS>(p + c, e);
   } else {
 #pragma unroll
-    for (int k = 0; k < 2 * PAIRS; ++k)
-      e[k] = c + k >= 0 && c + k < width ? (p ? to_f32(p[c + k]) : other) : 0.f;
+    for (int k = 0; k < 2 * PAIRS; ++k) e[k] = in ? (p ? to_f32(p[c + k]) : other) : 0.f;
   }
 #pragma unroll
   for (int k = 0; k < PAIRS; ++k) v[k] = f2(e[2 * k], e[2 * k + 1]);
@@ -147,17 +128,23 @@ __device__ __forceinline__ void param_pairs(const P *p, int c, int width, float 
 
 // Which rows and columns a thread works on.
 struct Share {
-  int t, first;        // thread of the group; column of its first vector's first element
+  int t, first;        // thread of the group; column of its first vector
+  int end;             // the column that no vector reaches
+  int edge;            // column of its single element, or -1
   int64_t row, step;   // its first row; rows from turn to turn
   int64_t next;        // rows between the rows of a bundle
 };
 
 template <int VEC, int R>
-__device__ __forceinline__ Share share_of(int tpr, int classes, int shift, int64_t shift_step) {
+__device__ __forceinline__ Share share_of(int width, int tpr, int classes, int shift, int64_t shift_step) {
   const int groups = blockDim.x / tpr, cls = blockIdx.x % classes;
   Share s;
   s.t = threadIdx.x & (tpr - 1);
-  s.first = -(int)((shift + cls * shift_step) % VEC) + s.t * VEC;
+  const int head = min(width, (VEC - (int)((shift + cls * shift_step) % VEC)) % VEC), body = (width - head) / VEC * VEC;
+  s.first = head + s.t * VEC;
+  s.end = head + body;
+  const int e = s.t < head ? s.t : s.t + body;
+  s.edge = e < width ? e : -1;
   s.next = (int64_t)groups * classes;
   s.row = ((int64_t)(blockIdx.x / classes) * R * groups + threadIdx.x / tpr) * classes + cls;
   s.step = (int64_t)(gridDim.x / classes) * R * groups * classes;
@@ -169,39 +156,48 @@ template <typename T, int NI>
 inline constexpr bool kKeepParams = NI * Vec<T>::n <= 16;
 
 // shift: elements between a 16-byte boundary and row 0, shift_step: added by each row (mod VEC).
-template <typename T, typename P, int NI, int R>
+template <typename T, typename P, int NI, int R, bool Edge>
 __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 : 1)
-    ln_forward(int64_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec, const T *__restrict__ x, int64_t ldx,
-                                                          const P *__restrict__ w, const P *__restrict__ b, float eps,
-                                                          T *__restrict__ y, float *__restrict__ mean,
-                                                          float *__restrict__ rstd) {
+    ln_forward(int64_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec,
+               const T *__restrict__ x, int64_t ldx, const P *__restrict__ w, const P *__restrict__ b, float eps,
+               T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
   using V = Vec<T>;
   constexpr int N = V::n, H = V::pairs;
   constexpr bool keep = kKeepParams<T, NI>;
   __shared__ float slots[2][2][R * 16];
-  const Share s = share_of<N, R>(tpr, classes, shift, shift_step);
+  const Share s = share_of<N, R>(width, tpr, classes, shift, shift_step);
   const int apart = tpr * N;
   const float inv = 1.f / (float)width;
   float2 wk[keep ? NI : 1][H], bk[keep ? NI : 1][H];
   if constexpr (keep)
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      param_pairs<P, H>(w, s.first + i * apart, width, 1.f, pvec, wk[i]);
-      param_pairs<P, H>(b, s.first + i * apart, width, 0.f, pvec, bk[i]);
+      const int c = s.first + i * apart;
+      param_pairs<P, H>(w, c, c < s.end, 1.f, pvec, wk[i]);
+      param_pairs<P, H>(b, c, c < s.end, 0.f, pvec, bk[i]);
     }
+  const bool edge = Edge && s.edge >= 0;
+  float we = 1.f, be = 0.f;
+  if (edge && w) we = to_f32(w[s.edge]);
+  if (edge && b) be = to_f32(b[s.edge]);
   V raw[R][NI];
+  float raw_e[R];
   const T *px = x + s.row * ldx;  // the row that is asked for next
   T *py = y + s.row * (int64_t)width;
   const int64_t x_next = s.next * ldx, x_step = s.step * ldx, y_next = s.next * width, y_step = s.step * width;
   auto ask = [&](int64_t row) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      const bool live = row + r * s.next < rows;
+      raw_e[r] = 0.f;
+      if (edge && live) raw_e[r] = to_f32(px[r * x_next + s.edge]);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int c = s.first + i * apart;
         raw[r][i].q = make_uint4(0, 0, 0, 0);
-        if (row + r * s.next < rows && c < width) raw[r][i].load(px + r * x_next, c, width);
+        if (live && c < s.end) raw[r][i].load(px + r * x_next + c);
       }
+    }
     px += x_step;
   };
   ask(s.row);
@@ -210,7 +206,7 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 
   const int64_t lead = s.row - (int64_t)(threadIdx.x / tpr) * classes;
   for (int64_t ahead = lead, row = s.row; ahead < rows; ahead += s.step, row += s.step, py += y_step, turn ^= 1) {
     float2 v[R][NI][H];
-    float sum[R], sq[R];
+    float sum[R], sq[R], ve[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 a = f2(0.f, 0.f);
@@ -220,7 +216,8 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 
 #pragma unroll
         for (int k = 0; k < H; ++k) a = add2(a, v[r][i][k]);
       }
-      sum[r] = a.x + a.y;
+      ve[r] = raw_e[r];
+      sum[r] = a.x + a.y + (Edge ? ve[r] : 0.f);
     }
     if (ahead + s.step < rows) ask(row + s.step);
     group_sums<R>(sum, tpr, slots[turn][0]);
@@ -228,27 +225,26 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 
     for (int r = 0; r < R; ++r) {
       const float mu = sum[r] * inv;
       const float2 minus = f2(-mu, -mu);
-      float2 a = f2(0.f, 0.f);
+      sq[r] = 0.f;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int c = s.first + i * apart;
-        if (c >= 0 && c + N <= width) {
+        float2 a = f2(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < H; ++k) v[r][i][k] = add2(v[r][i][k], minus);
-        } else {  // no differences where there is no row
-#pragma unroll
-          for (int k = 0; k < H; ++k) {
-            v[r][i][k].x = c + 2 * k >= 0 && c + 2 * k < width ? v[r][i][k].x - mu : 0.f;
-            v[r][i][k].y = c + 2 * k + 1 >= 0 && c + 2 * k + 1 < width ? v[r][i][k].y - mu : 0.f;
-          }
+        for (int k = 0; k < H; ++k) {
+          v[r][i][k] = add2(v[r][i][k], minus);
+          a = fma2(v[r][i][k], v[r][i][k], a);
         }
-#pragma unroll
-        for (int k = 0; k < H; ++k) a = fma2(v[r][i][k], v[r][i][k], a);
+        sq[r] += s.first + i * apart < s.end ? a.x + a.y : 0.f;  // no differences where there is no row
+      }
+      if (edge) {
+        ve[r] -= mu;
+        sq[r] += ve[r] * ve[r];
       }
       sum[r] = mu;
-      sq[r] = a.x + a.y;
     }
     group_sums<R>(sq, tpr, slots[turn][1]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) sq[r] = rsqrtf(sq[r] * inv + eps);  // 2 units in the last place
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int c = s.first + i * apart;
@@ -257,20 +253,24 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 
 #pragma unroll
         for (int k = 0; k < H; ++k) wv[k] = wk[i][k], bv[k] = bk[i][k];
       } else {
-        param_pairs<P, H>(w, c, width, 1.f, pvec, wv);
-        param_pairs<P, H>(b, c, width, 0.f, pvec, bv);
+        param_pairs<P, H>(w, c, c < s.end, 1.f, pvec, wv);
+        param_pairs<P, H>(b, c, c < s.end, 0.f, pvec, bv);
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float rs = rsqrtf(sq[r] * inv + eps);  // 2 units in the last place
-        const int64_t at = row + r * s.next;
 #pragma unroll
-        for (int k = 0; k < H; ++k) v[r][i][k] = fma2(mul2(v[r][i][k], f2(rs, rs)), wv[k], bv[k]);
-        if (at < rows && c < width) V::store(py + r * y_next, c, width, v[r][i]);
-        if (i == 0 && s.t == 0 && at < rows && mean) {
-          mean[at] = sum[r];
-          rstd[at] = rs;
-        }
+        for (int k = 0; k < H; ++k) v[r][i][k] = fma2(mul2(v[r][i][k], f2(sq[r], sq[r])), wv[k], bv[k]);
+        if (row + r * s.next < rows && c < s.end) V::store(py + r * y_next + c, v[r][i]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t at = row + r * s.next;
+      if (at >= rows) continue;
+      if (edge) py[r * y_next + s.edge] = from_f32<T>(ve[r] * sq[r] * we + be);
+      if (s.t == 0 && mean) {
+        mean[at] = sum[r];
+        rstd[at] = sq[r];
       }
     }
   }
@@ -307,30 +307,33 @@ __global__ void __launch_bounds__(kMaxThreads) ln_forward_any(int64_t rows, int6
 }
 
 // parts: [gridDim.x][2][width] partial sums of dw and db (NULL: dx only).
-template <typename T, typename P, int NI, int R>
+template <typename T, typename P, int NI, int R, bool Edge>
 __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 : 1)
-    ln_backward(int64_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec, const T *__restrict__ dy, int64_t lddy,
-                                                           const T *__restrict__ x, int64_t ldx,
-                                                           const P *__restrict__ w, const float *__restrict__ mean,
-                                                           const float *__restrict__ rstd, T *__restrict__ dx,
-                                                           float *__restrict__ parts) {
+    ln_backward(int64_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec,
+                const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx, const P *__restrict__ w,
+                const float *__restrict__ mean, const float *__restrict__ rstd, T *__restrict__ dx,
+                float *__restrict__ parts) {
   using V = Vec<T>;
   constexpr int N = V::n, H = V::pairs;
   constexpr bool keep = kKeepParams<T, NI>;
   extern __shared__ float cols[];  // more than one group: [2][width]
   __shared__ float slots[2][2 * R * 16];
-  const Share s = share_of<N, R>(tpr, classes, shift, shift_step);
+  const Share s = share_of<N, R>(width, tpr, classes, shift, shift_step);
   const int apart = tpr * N, groups = blockDim.x / tpr;
   const float inv = 1.f / (float)width;
   float2 wk[keep ? NI : 1][H], aw[NI][H], ab[NI][H];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    if constexpr (keep) param_pairs<P, H>(w, s.first + i * apart, width, 1.f, pvec, wk[i]);
+    const int c = s.first + i * apart;
+    if constexpr (keep) param_pairs<P, H>(w, c, c < s.end, 1.f, pvec, wk[i]);
 #pragma unroll
     for (int k = 0; k < H; ++k) aw[i][k] = ab[i][k] = f2(0.f, 0.f);
   }
+  const bool edge = Edge && s.edge >= 0;
+  float we = 1.f, awe = 0.f, abe = 0.f;
+  if (edge && w) we = to_f32(w[s.edge]);
   V rx[R][NI], rg[R][NI];
-  float rm[R], rr[R];
+  float rm[R], rr[R], ex[R], eg[R];
   const T *px = x + s.row * ldx, *pg = dy + s.row * lddy;  // the rows that are asked for next
   T *pd = dx + s.row * (int64_t)width;
   const int64_t x_next = s.next * ldx, g_next = s.next * lddy, d_next = s.next * width;
@@ -340,13 +343,18 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
       const bool live = row < rows;
       rm[r] = live ? mean[row] : 0.f;
       rr[r] = live ? rstd[row] : 0.f;
+      ex[r] = eg[r] = 0.f;
+      if (edge && live) {
+        ex[r] = to_f32(px[r * x_next + s.edge]);
+        eg[r] = to_f32(pg[r * g_next + s.edge]);
+      }
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int c = s.first + i * apart;
         rx[r][i].q = rg[r][i].q = make_uint4(0, 0, 0, 0);
-        if (live && c < width) {
-          rx[r][i].load(px + r * x_next, c, width);
-          rg[r][i].load(pg + r * g_next, c, width);
+        if (live && c < s.end) {
+          rx[r][i].load(px + r * x_next + c);
+          rg[r][i].load(pg + r * g_next + c);
         }
       }
     }
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
   const int64_t lead = s.row - (int64_t)(threadIdx.x / tpr) * classes;
   for (int64_t ahead = lead, row = s.row; ahead < rows; ahead += s.step, row += s.step, turn ^= 1) {
     float2 xh[R][NI][H], g[R][NI][H];
-    float sums[2 * R], rs[R];
+    float sums[2 * R], rs[R], xe[R], ge[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       rs[r] = rr[r];
@@ -371,7 +379,8 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
 #pragma unroll
           for (int k = 0; k < H; ++k) wv[k] = wk[i][k];
         } else {
-          param_pairs<P, H>(w, s.first + i * apart, width, 1.f, pvec, wv);
+          const int c = s.first + i * apart;
+          param_pairs<P, H>(w, c, c < s.end, 1.f, pvec, wv);
         }
         rx[r][i].values(xh[r][i]);
         rg[r][i].values(g[r][i]);
@@ -388,6 +397,15 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
       }
       sums[2 * r] = a1.x + a1.y;
       sums[2 * r + 1] = a2.x + a2.y;
+      xe[r] = ge[r] = 0.f;
+      if (edge) {
+        xe[r] = (ex[r] - rm[r]) * rs[r];
+        awe += eg[r] * xe[r];
+        abe += eg[r];
+        ge[r] = eg[r] * we;
+        sums[2 * r] += ge[r];
+        sums[2 * r + 1] += ge[r] * xe[r];
+      }
     }
     if (ahead + s.step < rows) ask(row + s.step);
     group_sums<2 * R>(sums, tpr, slots[turn]);
@@ -396,35 +414,37 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
     if (!dx) continue;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t at = row + r * s.next;
       const float m1 = -sums[2 * r] * inv, m2 = -sums[2 * r + 1] * inv;
+      if (row + r * s.next >= rows) continue;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int c = s.first + i * apart;
 #pragma unroll
         for (int k = 0; k < H; ++k)
           g[r][i][k] = mul2(fma2(xh[r][i][k], f2(m2, m2), add2(g[r][i][k], f2(m1, m1))), f2(rs[r], rs[r]));
-        if (at < rows && c < width) V::store(out + r * d_next, c, width, g[r][i]);
+        if (c < s.end) V::store(out + r * d_next + c, g[r][i]);
       }
+      if (edge) out[r * d_next + s.edge] = from_f32<T>(rs[r] * (ge[r] + m1 + xe[r] * m2));
     }
   }
   if (!parts) return;
   float *pw = parts + (int64_t)blockIdx.x * 2 * width, *pb = pw + width;
   if (groups == 1) {
-    // (columns of the shifted vectors that are not in the row do not exist)
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NI; ++i) {
+      const int c = s.first + i * apart;
+      if (c >= s.end) break;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int c = s.first + i * apart + k;
-        if (c < 0 || c >= width) continue;
-        pw[c] = k & 1 ? aw[i][k / 2].y : aw[i][k / 2].x;
-        pb[c] = k & 1 ? ab[i][k / 2].y : ab[i][k / 2].x;
+      for (int k = 0; k < H; ++k) {
+        pw[c + 2 * k] = aw[i][k].x, pw[c + 2 * k + 1] = aw[i][k].y;
+        pb[c + 2 * k] = ab[i][k].x, pb[c + 2 * k + 1] = ab[i][k].y;
       }
+    }
+    if (edge) pw[s.edge] = awe, pb[s.edge] = abe;
     return;
   }
   // the groups of a warp by shuffles, then what is left one after another
-  for (int o = tpr; o < 32; o <<= 1)
+  for (int o = tpr; o < 32; o <<= 1) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -434,19 +454,29 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
         ab[i][k].x += __shfl_xor_sync(0xffffffffu, ab[i][k].x, o);
         ab[i][k].y += __shfl_xor_sync(0xffffffffu, ab[i][k].y, o);
       }
+    if (Edge) {
+      awe += __shfl_xor_sync(0xffffffffu, awe, o);
+      abe += __shfl_xor_sync(0xffffffffu, abe, o);
+    }
+  }
   const int size = tpr < 32 ? 32 : tpr;
   for (int from = 0; from < (int)blockDim.x; from += size) {
     if ((int)threadIdx.x >= from && (int)threadIdx.x < from + tpr) {
+      auto put = [&](int c, float a, float d) {
+        cols[c] = from ? cols[c] + a : a;
+        cols[width + c] = from ? cols[width + c] + d : d;
+      };
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+      for (int i = 0; i < NI; ++i) {
+        const int c = s.first + i * apart;
+        if (c >= s.end) break;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int c = s.first + i * apart + k;
-          if (c < 0 || c >= width) continue;
-          const float a = k & 1 ? aw[i][k / 2].y : aw[i][k / 2].x, d = k & 1 ? ab[i][k / 2].y : ab[i][k / 2].x;
-          cols[c] = from ? cols[c] + a : a;
-          cols[width + c] = from ? cols[width + c] + d : d;
+        for (int k = 0; k < H; ++k) {
+          put(c + 2 * k, aw[i][k].x, ab[i][k].x);
+          put(c + 2 * k + 1, aw[i][k].y, ab[i][k].y);
         }
+      }
+      if (edge) put(s.edge, awe, abe);
     }
     __syncthreads();
   }
@@ -532,11 +562,12 @@ __global__ void __launch_bounds__(1024) ln_reduce_parts(int nparts, int64_t widt
 struct LnPlan {
   int items, tpr, block, classes, shift;
   int64_t shift_step;
+  bool edge;  // rows have elements outside of their aligned vectors
   // whole vectors of a parameter may be read at once
   bool pvec(std::initializer_list<const void *> params) const {
     for (const void *p : params)
       if (!aligned(p, 16)) return false;
-    return !shift && !shift_step;
+    return !edge;
   }
 };
 
@@ -549,16 +580,16 @@ struct Rows {
 // cannot.  The arrays have to start every row at the same place behind a 16-byte boundary.
 LnPlan ln_plan(int64_t width, int32_t dtype, std::initializer_list<Rows> arrays) {
   const int e = (int)net_size(dtype), vec = 16 / e;
-  LnPlan pl{0, kMaxThreads, kMaxThreads, 1, 0, 0};
+  LnPlan pl{0, kMaxThreads, kMaxThreads, 1, 0, 0, false};
   pl.shift = (int)((uintptr_t)arrays.begin()->p % 16 / e);
   pl.shift_step = arrays.begin()->ld % vec;
   for (const Rows &a : arrays)
     if (a.p && ((int)((uintptr_t)a.p % 16 / e) != pl.shift || a.ld % vec != pl.shift_step)) return pl;
   while ((pl.classes * pl.shift_step) % vec) pl.classes *= 2;
-  // a shifted row may need one vector more
-  const int64_t nv = (width + vec - 1) / vec + (pl.shift || pl.shift_step ? 1 : 0);
+  pl.edge = pl.shift || pl.shift_step || width % vec;
+  const int64_t nv = width / vec;
   if (nv > kMaxThreads * 4) return pl;
-  int tpr = 1;
+  int tpr = pl.edge ? 2 * vec : 1;  // at most 2 (vec - 1) single elements
   while (tpr < kMaxThreads && (2 * tpr < nv || (tpr < 32 && tpr < nv))) tpr <<= 1;
   const int64_t need = (nv + tpr - 1) / tpr;
   pl.items = need <= 1 ? 1 : need <= 2 ? 2 : 4;
@@ -574,19 +605,21 @@ int ln_grid(const LnPlan &pl, int64_t rows, int64_t rows_a_turn, int threads) {
   return (int)(std::max<int64_t>(1, std::min<int64_t>(most / pl.classes, need)) * pl.classes);
 }
 
-template <typename T, typename P, int NI, int R>
+template <typename T, typename P, int NI, int R, bool Edge>
 void launch_forward(const LnPlan &pl, int64_t rows, int64_t width, const void *x, int64_t ldx, const void *w,
                     const void *b, float eps, void *y, float *mean, float *rstd, cudaStream_t st) {
   const int grid = ln_grid(pl, rows, pl.block / pl.tpr * R, 1024);
-  ln_forward<T, P, NI, R><<<grid, pl.block, 0, st>>>(rows, (int)width, pl.tpr, pl.classes, pl.shift, pl.shift_step,
-                                                     pl.pvec({w, b}) && width % Vec<T>::n == 0, (const T *)x, ldx, (const P *)w, (const P *)b, eps, (T *)y, mean,
+  ln_forward<T, P, NI, R, Edge><<<grid, pl.block, 0, st>>>(rows, (int)width, pl.tpr, pl.classes, pl.shift, pl.shift_step,
+                                                     pl.pvec({w, b}), (const T *)x, ldx, (const P *)w, (const P *)b, eps, (T *)y, mean,
                                                      rstd);
 }
 
 template <typename T, typename P>
 cudaError_t forward(int64_t rows, int64_t width, const LnPlan &pl, const void *x, int64_t ldx, const void *w,
                     const void *b, float eps, void *y, float *mean, float *rstd, cudaStream_t st) {
-#define SLA_LN_FWD(NI, R) launch_forward<T, P, NI, R>(pl, rows, width, x, ldx, w, b, eps, y, mean, rstd, st)
+#define SLA_LN_FWD(NI, R)                                                                                       \
+  (pl.edge ? launch_forward<T, P, NI, R, true>(pl, rows, width, x, ldx, w, b, eps, y, mean, rstd, st)           \
+           : launch_forward<T, P, NI, R, false>(pl, rows, width, x, ldx, w, b, eps, y, mean, rstd, st))
   if (pl.items == 0)
     ln_forward_any<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
         rows, width, (const T *)x, ldx, (const P *)w, (const P *)b, eps, (T *)y, mean, rstd);
@@ -596,14 +629,14 @@ cudaError_t forward(int64_t rows, int64_t width, const LnPlan &pl, const void *x
   return cudaGetLastError();
 }
 
-template <typename T, typename P, int NI, int R>
+template <typename T, typename P, int NI, int R, bool Edge>
 int launch_backward(const LnPlan &pl, int64_t rows, int64_t width, const void *dy, int64_t lddy, const void *x,
                     int64_t ldx, const void *w, const float *mean, const float *rstd, void *dx, float *parts,
                     cudaStream_t st) {
   const int groups = pl.block / pl.tpr, grid = ln_grid(pl, rows, groups * R, NI == 1 ? 768 : 512);
   const size_t smem = groups > 1 && parts ? 2 * sizeof(float) * (size_t)width : 0;
-  ln_backward<T, P, NI, R><<<grid, pl.block, smem, st>>>(rows, (int)width, pl.tpr, pl.classes, pl.shift,
-                                                         pl.shift_step, pl.pvec({w}) && width % Vec<T>::n == 0,
+  ln_backward<T, P, NI, R, Edge><<<grid, pl.block, smem, st>>>(rows, (int)width, pl.tpr, pl.classes, pl.shift,
+                                                         pl.shift_step, pl.pvec({w}),
                                                          (const T *)dy, lddy, (const T *)x, ldx, (const P *)w, mean, rstd, (T *)dx, parts);
   return grid;
 }
@@ -614,7 +647,9 @@ cudaError_t backward(int64_t rows, int64_t width, const LnPlan &pl, const void *
                      float *parts, cudaStream_t st) {
   int nparts = 0;
   const int ctiles = (int)((width + kColTile - 1) / kColTile);
-#define SLA_LN_BWD(NI, R) launch_backward<T, P, NI, R>(pl, rows, width, dy, lddy, x, ldx, w, mean, rstd, dx, parts, st)
+#define SLA_LN_BWD(NI, R)                                                                                           \
+  (pl.edge ? launch_backward<T, P, NI, R, true>(pl, rows, width, dy, lddy, x, ldx, w, mean, rstd, dx, parts, st)    \
+           : launch_backward<T, P, NI, R, false>(pl, rows, width, dy, lddy, x, ldx, w, mean, rstd, dx, parts, st))
   if (pl.items == 0) {
     if (dx)
       ln_backward_any<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
