@@ -5,13 +5,11 @@
 //   gelu_tanh  a = g (1 + t) / 2,  a' = (1 + t) / 2 + g (1 - t^2) z' / 2,  t = tanh z, z = sqrt(2/pi) (g + 0.044715 g^3)
 //   relu       a = max(g, 0),      a' = [g > 0]
 //
-// float32 data takes expf, erff and tanhf, one value at a time (activate).  16-bit data takes pairs of
-// values (activate2): packed float32 arithmetic, the approximate exponential and reciprocal (their
-// errors of a few 2^-22 disappear in the rounding to 2^-9 or 2^-12), one reciprocal for both sigmoids of
-// a pair, and for gelu the normal distribution by Abramowitz and Stegun 7.1.26 (1.5e-7), whose
-// exponential is the density's too.  The special function unit gives 16 results a clock, so a
-// sigmoid's exponential and reciprocal are what the epilogues of narrow products wait for: one
-// reciprocal less for a pair is worth the multiplications.
+// They are taken for pairs of values: packed float32 arithmetic, the approximate exponential and
+// reciprocal, and for gelu the normal distribution by Abramowitz and Stegun 7.1.26 (1.5e-7), whose
+// exponential is the density's too.  Errors are a few 2^-22, for float32 data below what its sums
+// lose, for 16-bit data far below the rounding to 2^-9 or 2^-12.  (expf, erff and division cost the
+// float32 epilogue three times the instructions.)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -21,28 +19,6 @@
 #include "sla_net.cuh"
 
 namespace sla {
-
-struct ActValue {
-  float a, da;
-};
-
-template <int Act>
-__device__ __forceinline__ ActValue activate(float g) {
-  if constexpr (Act == SLA_ACT_SILU) {
-    const float s = 1.f / (1.f + expf(-g));
-    return {g * s, s * (1.f + g * (1.f - s))};
-  } else if constexpr (Act == SLA_ACT_GELU) {
-    const float phi = 0.5f * (1.f + erff(g * 0.7071067811865476f));
-    return {g * phi, phi + g * expf(-0.5f * g * g) * 0.3989422804014327f};
-  } else if constexpr (Act == SLA_ACT_GELU_TANH) {
-    const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
-    return {0.5f * g * (1.f + t), 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * 0.7978845608028654f *
-                                                          (1.f + 3.f * 0.044715f * g * g)};
-  } else {
-    // written so that a NaN stays one
-    return {g < 0.f ? 0.f : g, g > 0.f ? 1.f : 0.f};
-  }
-}
 
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -100,33 +76,22 @@ __device__ __forceinline__ void activate2(float2 g, float2 &a, float2 &da) {
   }
 }
 
-// h = act(g) u from g and u, 16-bit data (Fast) in pairs.  Keep: g and u become the factors of the backward
-// pass, dg = dh (u act'(g)) and du = dh act(g).  They are what a forward call leaves behind, in the place
-// of g and u: as many bytes, one rounding each, and the backward epilogue is two products.
-template <int Act, bool Fast, bool Keep, int N>
+// h = act(g) u from g and u.  Keep: g and u become the factors of the backward pass, dg = dh (u act'(g)) and
+// du = dh act(g).  They are what a forward call leaves behind, in the place of g and u: as many bytes, one
+// rounding each, and the backward epilogue is two products.
+template <int Act, bool Keep, int N>
 __device__ __forceinline__ void gate(float (&g)[N], float (&u)[N], float (&h)[N]) {
-  if constexpr (Fast && N % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      float2 a, da;
-      const float2 up = f2(u[i], u[i + 1]);
-      activate2<Act, Keep>(f2(g[i], g[i + 1]), a, da);
-      const float2 v = mul2(a, up);
-      h[i] = v.x, h[i + 1] = v.y;
-      if (Keep) {
-        da = mul2(da, up);
-        g[i] = da.x, g[i + 1] = da.y, u[i] = a.x, u[i + 1] = a.y;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const ActValue a = activate<Act>(g[i]);
-      h[i] = a.a * u[i];
-      if (Keep) {
-        g[i] = u[i] * a.da;
-        u[i] = a.a;
-      }
+  for (int i = 0; i < N; i += 2) {
+    constexpr int next = N > 1;
+    float2 a, da;
+    const float2 up = f2(u[i], u[i + next]);
+    activate2<Act, Keep>(f2(g[i], g[i + next]), a, da);
+    const float2 v = mul2(a, up);
+    h[i + next] = v.y, h[i] = v.x;
+    if (Keep) {
+      da = mul2(da, up);
+      g[i + next] = da.y, g[i] = da.x, u[i + next] = a.y, u[i] = a.x;
     }
   }
 }

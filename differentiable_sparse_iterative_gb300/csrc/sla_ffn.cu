@@ -62,15 +62,15 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Map of boxes of box_cols columns by box_rows rows, zeros outside; the swizzle is as many bytes as a row
+// Map of boxes of box_cols columns by box_rows rows (and some sheets), zeros outside; the swizzle is as many bytes as a row
 // of the box has (128, 64 or 32).
-cudaError_t encode(CUtensorMap *map, const Operand &o, int box_cols, int box_rows, int32_t dtype) {
+cudaError_t encode(CUtensorMap *map, const Operand &o, int box_cols, int box_rows, int32_t dtype, int box_sheets = 1) {
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const size_t e = net_size(dtype);
   const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.sheets};
   const cuuint64_t strides[2] = {(cuuint64_t)o.ld * e, (cuuint64_t)o.sheet * e};
-  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, (cuuint32_t)box_sheets}, step[3] = {1, 1, 1};
   const CUtensorMapDataType type = dtype == SLA_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dtype == SLA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -84,7 +84,7 @@ cudaError_t encode(CUtensorMap *map, const Operand &o, int box_cols, int box_row
 }
 
 // Up to four matrices laid out for TMA in one launch: rows padded to ld (zeros), float32 split into three
-// sheets.  Halves of src lie src_half apart; part q of half i becomes sheet q * halves + i.
+// sheets.  Halves of src lie src_half apart; part q of half i becomes sheet 3 i + q.
 struct PackJob {
   const void *src;
   uint16_t *dst;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(256) pack_operands(const __grid_constant__ Pac
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = k < count ? to_f32(s[k]) : 0.f;
     }
-    store_operand<T, 8>(j.dst + half * sheet + r * j.ld + c, j.halves * sheet, v, 8, true);
+    store_operand<T, 8>(j.dst + half * kParts<T> * sheet + r * j.ld + c, sheet, v, 8, true);
   }
 }
 
@@ -191,9 +191,11 @@ void run_packs(Call &c, const PackJobs &jobs) {
 
 // ------------------------------------------------------------------ plans
 
-// Deepest sum of products that float32 data adds up in one accumulator, in blocks of kDepth: the tensor
-// core drops up to one unit of the running sum for every 16 products (2048 / 16 * 2^-24 * 2/3 = 5e-6 in all).
-constexpr int kFloatBlocks = 2048 / kDepth;
+constexpr int kPlanDepth = 64;  // k of the blocks that plans are made in
+
+// Deepest sum of products that float32 data adds up in one accumulator, in such blocks: the tensor core
+// drops up to one unit of the running sum for every 16 products (2048 / 16 * 2^-24 * 2/3 = 5e-6 in all).
+constexpr int kFloatBlocks = 2048 / kPlanDepth;
 
 struct ProductSize {
   int64_t m, n, k;           // of one half, of one segment
@@ -213,22 +215,23 @@ struct ProductPlan {
 // the tensor core is the limit, and 0.22 to 0.26 us with the smaller ones, where it is the 64 bytes a clock
 // that a multiprocessor takes in from L2; pairs of blocks start 2 us later than single ones.
 ProductPlan plan_products(Epilogue epi, const ProductSize *s, int count, int sheets) {
-  static const double block_us[kProductTileCount] = {0.27, 0.225, 0.255, 0.245};
+  static const double blocks_us[2][kProductTileCount] = {{0.27, 0.225, 0.255, 0.245}, {0, 0.81, 1.0, 0.84}};
+  const auto &block_us = blocks_us[sheets == 3];
   static const double start_us[kProductTileCount] = {5.0, 5.0, 3.0, 3.0};
   static const double epilogues_us[2][3][kProductTileCount] = {
       {{2.1, 1.25, 1.25, 0.8}, {3.0, 1.8, 1.8, 1.15}, {10.0, 5.5, 5.5, 3.0}},   // kStore, kGate, kGateBack
-      {{3.0, 1.6, 1.6, 0.9}, {9.0, 4.5, 4.5, 2.3}, {11.0, 6.0, 6.0, 3.0}}};     // float32
+      {{0, 1.6, 1.6, 0.9}, {0, 4.5, 4.5, 2.3}, {0, 6.0, 6.0, 3.0}}};            // float32
   const auto &epilogue_us = epilogues_us[sheets == 3];
   const int sms = sm_count();
   ProductPlan best{};
   double best_us = 1e30;
-  for (int i = 0; i < kProductTileCount; ++i) {
+  for (int i = sheets == 3 ? 1 : 0; i < kProductTileCount; ++i) {
     const int64_t bm = 128 * kProductTiles[i].cg, bn = kProductTiles[i].bn, workers = sms / kProductTiles[i].cg;
     int64_t tiles[kGroup], kb[kGroup], least[kGroup];
     double per[kGroup], blocks = 0;
     for (int j = 0; j < count; ++j) {
-      kb[j] = (s[j].k + kDepth - 1) / kDepth;
-      per[j] = s[j].k_halves * (sheets == 3 ? 6 : 1);
+      kb[j] = (s[j].k + kPlanDepth - 1) / kPlanDepth;
+      per[j] = s[j].k_halves;
       const int64_t deepest = sheets == 3 ? std::max(1, kFloatBlocks / s[j].k_halves) : kb[j];
       least[j] = (kb[j] + deepest - 1) / deepest;
       // columns of g and of u make separate tiles when their product is split
@@ -289,7 +292,6 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
   grid_dependency_launch();
   const ProductArgs &p = f.p[blockIdx.y];
   const int64_t chunks = (p.n + 3) / 4, total = f.rows[blockIdx.y] * chunks;
-  constexpr bool fast = sizeof(T) == 2;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int64_t row = i / chunks;
     const int col = (int)(i - row * chunks) * 4, count = p.n - col;
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
         }
       }
       float h[4];
-      with_activation(p.act, [&](auto act) { gate<act.value, fast, true, 4>(v, u, h); });
+      with_activation(p.act, [&](auto act) { gate<act.value, true, 4>(v, u, h); });
       if (p.g)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -349,8 +351,8 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
         u[k] = k < count ? to_f32(((const T *)p.u)[o + k]) : 0.f;
       }
       gate_gradients(v, g, u);
-      store_operand<T, 4>(p.h + o, 2 * p.sheet, g, count, false);
-      store_operand<T, 4>(p.h + p.sheet + o, 2 * p.sheet, u, count, false);
+      store_operand<T, 4>(p.h + o, p.sheet, g, count, false);
+      store_operand<T, 4>(p.h + kParts<T> * p.sheet + o, p.sheet, u, count, false);
     }
   }
 }
@@ -370,7 +372,7 @@ struct ProductJob {
 template <typename T>
 void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, float *parts) {
   if (c.err != cudaSuccess) return;
-  constexpr int S = sheets_of<T>();
+  constexpr int S = sheets_of<T>(), D = kDepth<T>;
   constexpr int32_t part = S == 3 ? SLA_BF16 : NetType<T>::dtype;  // type of the operands
   ProductSize sizes[kGroup];
   for (int j = 0; j < count; ++j) sizes[j] = jobs[j].s;
@@ -402,20 +404,13 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, floa
     p.m_halves = s.m_halves, p.n_halves = epi == kGate && split ? 2 : s.n_halves;
     const int cols = gate ? bn / 2 : bn;
     p.m_tiles = (int)((s.m + bm - 1) / bm), p.n_tiles = (int)((s.n + cols - 1) / cols);
-    p.k_blocks = (int)((s.k + kDepth - 1) / kDepth);
+    p.k_blocks = (int)((s.k + D - 1) / D);
     p.splits = plan.splits[j];
     p.a_mn = jobs[j].a_mn, p.b_mn = jobs[j].b_mn, p.f16 = sizeof(T) == 2 && NetType<T>::dtype == SLA_F16;
-    // sheets: part q of the value, in pairs where A (B) has halves of rows, of columns or of k
-    const int a_pair = s.m_halves * s.k_halves, b_pair = (epi == kGate ? 2 : s.n_halves) * s.k_halves;
-    static const int8_t pairs[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
-    p.segments = 0;
-    for (int q = S == 3 ? 0 : 5; q < 6; ++q)
-      for (int h = 0; h < s.k_halves; ++h) {
-        p.a_sheet[p.segments] = (int8_t)(pairs[q][0] * a_pair + h);
-        p.b_sheet[p.segments++] = (int8_t)(pairs[q][1] * b_pair + h);
-      }
-    cudaError_t e = encode(&l.a[l.count], a, kDepth, p.a_mn ? kDepth : 128, part);
-    if (e == cudaSuccess) e = encode(&l.b[l.count], b, kDepth, p.b_mn ? kDepth : gate ? bn / 2 : bn / tile.cg, part);
+    p.segments = s.k_halves;
+    for (int h = 0; h < s.k_halves; ++h) p.a_sheet[h] = p.b_sheet[h] = (int8_t)h;
+    cudaError_t e = encode(&l.a[l.count], a, p.a_mn ? 64 : D, p.a_mn ? D : 128, part);
+    if (e == cudaSuccess) e = encode(&l.b[l.count], b, p.b_mn ? 64 : D, p.b_mn ? D : gate ? bn / 2 : bn / tile.cg, part);
     if (epi != kStore && !split) {
       // the epilogue's own arrays (see tma_epilogue); a warp's columns of the 64-wide gate tile are 16
       const int box = S == 3 || (gate && bn == 64) ? 16 : 32;
@@ -427,7 +422,7 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, floa
         if (e == cudaSuccess) e = encode(&l.out[0], g, box, 32, NetType<T>::dtype);
         if (e == cudaSuccess) e = encode(&l.out[1], u, box, 32, NetType<T>::dtype);
       }
-      if (e == cudaSuccess) e = encode(&l.out[epi == kGate ? 2 : 0], h, box, 32, part);
+      if (e == cudaSuccess) e = encode(&l.out[epi == kGate ? 2 : 0], h, box, 32, part, S == 3 ? (int)h.sheets : 1);
     }
     if (e != cudaSuccess) {
       c.err = e;
@@ -762,7 +757,7 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
       columns.of<float, 1>((f->tokens + 31) / 32, 2 * ldg, w.sums, 2 * ldg, 0, ldg, f->hidden, db_in);
     else if (db_in)
       for (int half = 0; half < 2; ++half)
-        columns.of<E, S>(f->tokens, f->hidden, (const E *)w.dgu + half * sheet, ldg, 2 * sheet, f->hidden, f->hidden,
+        columns.of<E, S>(f->tokens, f->hidden, (const E *)w.dgu + half * S * sheet, ldg, sheet, f->hidden, f->hidden,
                          db_in + half * f->hidden);
   }
   if (db_out) columns.of<T, 1>(f->tokens, f->out, dy, lddy, 0, f->out, f->out, db_out);

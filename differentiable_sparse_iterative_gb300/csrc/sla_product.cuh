@@ -4,11 +4,14 @@
 //   C[m][n] = sum over segments s, sum over k of A_s(m, k) B_s(n, k)
 //
 // Operands are 16-bit and read by TMA from three-dimensional tensors (contiguous dimension, rows,
-// sheets).  A segment names a sheet of A and one of B, which covers
-//   - float32 data, held as three bfloat16 sheets x = x0 + x1 + x2 of falling size (8 bits each, 24
-//     in all): the six products x_i y_j with i + j <= 2, smallest first, give float32's accuracy
-//     (what is dropped is below 2^-26 of a term);
-//   - the sum over both halves of [g u], which lie in two sheets.
+// sheets).  A segment names a sheet of A and one of B: the sum over both halves of [g u], which lie in
+// two sheets, has two.  float32 data is held as three bfloat16 parts x = x0 + x1 + x2 of falling size (8
+// bits each, 24 in all), in sheets of their own; the six products x_i y_j with i + j <= 2 give float32's
+// accuracy (what is dropped is below 2^-26 of a term).  A stage then holds all parts of its k, so that
+// six products share six tiles (two tiles a product left the smaller tile shapes waiting for L2: 1.53 us
+// a block of 64 k instead of 1.0), and the five small products have an accumulator of their own: the
+// tensor core drops up to a unit of the running sum for every 16 k, which the small products
+// would feel five times as often in the large one's.
 // Either operand may be k-major (k contiguous) or mn-major (rows or columns contiguous): the tensor
 // core reads both from the 128-byte swizzled tiles that TMA writes, so no operand is transposed.
 //
@@ -32,16 +35,22 @@ enum Epilogue {
   kGateBack,  // sum = dh: dg = dh (u act'(g)), du = dh act(g)
 };
 
-constexpr int kDepth = 64;      // k of a stage: 128 bytes, the swizzle's width
 constexpr int kBand = 8;
-constexpr int kMaxSegments = 12;
+constexpr int kMaxSegments = 2;
+
+template <typename T>
+inline constexpr int kParts = sizeof(T) == 4 ? 3 : 1;  // sheets that make one value
+template <typename T>
+inline constexpr int kDepth = sizeof(T) == 4 ? 32 : 64;  // k of a stage
+template <typename T>
+inline constexpr int kSums = sizeof(T) == 4 ? 2 : 1;  // accumulators of a tile
 constexpr int kGroup = 3;       // products of one launch
 
 struct ProductArgs {
   int m, n;                  // rows and columns of one half of C
-  int m_halves, n_halves;    // 2: A's (B's) sheets come in pairs, one for each half of C's rows (columns)
+  int m_halves, n_halves;    // 2: A (B) has sheets for each half of C's rows (columns)
   int m_tiles, n_tiles;      // of one half
-  int k_blocks;              // of a segment
+  int k_blocks;              // of kDepth, of a segment
   int splits;                // k_blocks are dealt to this many work items, whose sums are added later
   int segments;
   int8_t a_sheet[kMaxSegments], b_sheet[kMaxSegments];
@@ -62,7 +71,7 @@ struct ProductArgs {
 // Up to three products that do not depend on one another, with one tile shape (kStore; one product else).
 struct ProductLaunch {
   CUtensorMap a[kGroup], b[kGroup];
-  CUtensorMap out[3];        // kGate, kGateBack: the arrays at g, u and h, or dg and du (one map, two sheets)
+  CUtensorMap out[3];        // kGate, kGateBack: the arrays at g, u and h, or dg and du (one map)
   ProductArgs p[kGroup];
   int first[kGroup + 1];     // work items before each product's
   int count;
@@ -105,8 +114,9 @@ inline constexpr int kRowBytes = kTurnColumns<T, BN> * sizeof(T) + 4;
 // shared memory.
 template <typename T, int EPI, int CG, int BN>
 struct ProductShape {
-  static constexpr int a_bytes = 128 * kDepth * 2;
-  static constexpr int b_bytes = BN / CG * kDepth * 2;
+  static constexpr int a_bytes = 128 * kDepth<T> * 2;
+  static constexpr int b_bytes = BN / CG * kDepth<T> * 2;
+  static constexpr int stage_bytes = kParts<T> * (a_bytes + b_bytes);
   // a warp's boxes: 16-bit data two, which it uses again and again; float32 two of factors and three of h, or
   // three each of dg and du
   static constexpr int box = 32 * kStoreColumns<T, EPI, BN> * 2;
@@ -115,10 +125,11 @@ struct ProductShape {
                                     : EPI == kGate     ? 7 * box
                                                        : 6 * box;
   static constexpr int boxes = (kEpilogueWarps<T, BN> * warp_boxes + 1023) / 1024 * 1024;
-  static constexpr int room = (225 * 1024 - boxes) / (a_bytes + b_bytes);
+  static constexpr int room = (225 * 1024 - boxes) / stage_bytes;
   static constexpr int stages = room > 8 ? 8 : room;
-  static constexpr int smem = stages * (a_bytes + b_bytes) + boxes + 1024 /* alignment */ + 256 /* barriers */;
-  static_assert(stages >= 4 && smem <= 227 * 1024, "shared memory");
+  static constexpr int smem = stages * stage_bytes + boxes + 1024 /* alignment */ + 256 /* barriers */;
+  static constexpr int columns = 2 * kSums<T> * BN;  // of tensor memory
+  static_assert(stages >= 3 && smem <= 227 * 1024 && columns <= 512, "shared and tensor memory");
 };
 
 // Three bfloat16 values whose sum is v to 2^-24: each the rounded rest of the one before.  An
@@ -356,6 +367,29 @@ __device__ __forceinline__ void split_range(const ProductArgs &p, int split, int
   k1 = (int)((int64_t)p.k_blocks * (split + 1) / p.splits);
 }
 
+// N columns of a tile's sums: loaded, and (after the wait) float32's two added.
+template <typename T, int BN, int N>
+struct Sums {
+  float v[N], small[kSums<T> == 2 ? N : 1];
+  __device__ __forceinline__ void load(uint32_t addr) {
+    if constexpr (N == 32) {
+      tmem_load32(addr, v);
+      if constexpr (kSums<T> == 2) tmem_load32(addr + BN, small);
+    } else {
+      tmem_load16(addr, v);
+      if constexpr (kSums<T> == 2) tmem_load16(addr + BN, small);
+    }
+  }
+  __device__ __forceinline__ void wait() {
+    tmem_wait(v);
+    if constexpr (kSums<T> == 2) {
+      tmem_wait(small);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += small[i];
+    }
+  }
+};
+
 // A warp has read its part of an accumulator.
 template <int CG>
 __device__ __forceinline__ void release_accumulator(uint64_t *acc_empty, int lane) {
@@ -470,7 +504,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
       break;
     }
     tc_fence_after();
-    const uint32_t base = tmem + acc * BN + ((uint32_t)quarter << 21);
+    const uint32_t base = tmem + acc * kSums<T> * BN + ((uint32_t)quarter << 21);
 #pragma unroll 1
     for (int c = first; c < first + width; c += W) {
       const bool some = row0 < p.m && t.n0 + c < p.n, last = c + W >= first + width;
@@ -480,15 +514,17 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
 #pragma unroll
       for (int j = 0; j < W; j += 16) {
         const int count = p.n - t.n0 - c - j;
-        float v[16];
-        tmem_load16(base + c + j, v);
+        Sums<T, BN, 16> sum;
+        float(&v)[16] = sum.v;
+        sum.load(base + c + j);
         if constexpr (EPI == kGate) {
-          float u[16];
-          tmem_load16(base + BN / 2 + c + j, u);
+          Sums<T, BN, 16> sum_u;
+          float(&u)[16] = sum_u.v;
+          sum_u.load(base + BN / 2 + c + j);
           const RawRow<T, 16> bias_g = raw_g, bias_u = raw_u;
           if (c + j + 16 < first + width) ask(c + j + 16);
-          tmem_wait(v);
-          tmem_wait(u);
+          sum.wait();
+          sum_u.wait();
           if (p.bias_vec && count >= 16) {
             float bg[16], bu[16];
             bias_g.values(bg);
@@ -505,7 +541,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
           }
           float h[16];
           if (p.g) {
-            with_activation(p.act, [&](auto act) { gate<act.value, !f32, true, 16>(v, u, h); });
+            with_activation(p.act, [&](auto act) { gate<act.value, true, 16>(v, u, h); });
             if constexpr (f32) {
               box0.put(v);
               box1.put(u);
@@ -517,7 +553,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
               box1.put(j / 16, w);
             }
           } else {
-            with_activation(p.act, [&](auto act) { gate<act.value, !f32, false, 16>(v, u, h); });
+            with_activation(p.act, [&](auto act) { gate<act.value, false, 16>(v, u, h); });
           }
           if constexpr (f32)
             put_sheets(sheets, box, lane, h);
@@ -528,7 +564,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
           raw_g.values(g);
           raw_u.values(u);
           if (c + j + 16 < first + width) ask(c + j + 16);
-          tmem_wait(v);
+          sum.wait();
           gate_gradients(v, g, u);
           if constexpr (f32) {
             put_sheets(sheets, box, lane, g);
@@ -560,16 +596,8 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
         if (EPI == kGate && p.g) store2(&l.out[0], &l.out[1], t.n0 + c, row0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            if (EPI == kGate) {
-              tma_store(&l.out[2], t.n0 + c, row0, q, sheets + q * box);
-            } else {  // the sheets of dgu come in pairs: dg and du of each part of the value
-              tma_store(&l.out[0], t.n0 + c, row0, 2 * q, sheets + q * box);
-              tma_store(&l.out[0], t.n0 + c, row0, 2 * q + 1, sheets + (3 + q) * box);
-            }
-          }
+        if (lane == 0) {  // all three or six sheets at once
+          tma_store(&l.out[EPI == kGate ? 2 : 0], t.n0 + c, row0, 0, sheets);
           tma_store_commit();
         }
       } else if constexpr (EPI == kGate) {
@@ -619,16 +647,14 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
       break;
     }
     tc_fence_after();
-    const uint32_t base = tmem + acc * BN + ((uint32_t)quarter << 21);
+    const uint32_t base = tmem + acc * kSums<T> * BN + ((uint32_t)quarter << 21);
 #pragma unroll 1
     for (int c = side * width; c < (side + 1) * width; c += N) {
       const int col = t.n0 + c, count = p.n - col;
-      float v[N];
-      if constexpr (N == 32)
-        tmem_load32(base + c, v);
-      else
-        tmem_load16(base + c, v);
-      tmem_wait(v);
+      Sums<T, BN, N> sum;
+      float(&v)[N] = sum.v;
+      sum.load(base + c);
+      sum.wait();
       if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
       if (live && count > 0) {
         const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
@@ -670,8 +696,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
   constexpr int S = Shape::stages;
   extern __shared__ uint8_t raw[];
   uint8_t *tiles = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sa = tiles, *sb = tiles + S * Shape::a_bytes;
-  uint8_t *boxes = tiles + S * (Shape::a_bytes + Shape::b_bytes);
+  uint8_t *boxes = tiles + S * Shape::stage_bytes;
   uint64_t *full = (uint64_t *)(boxes + Shape::boxes);
   uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 2, *drained = acc_empty + 2;
   uint32_t *tmem_slot = (uint32_t *)(drained + 1);
@@ -697,7 +722,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
     tma_prefetch_map(&l.a[0]);
     tma_prefetch_map(&l.b[0]);
   }
-  if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
+  if (warp == 1) tmem_alloc<CG>(tmem_slot, Shape::columns);
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync_all();
@@ -708,8 +733,8 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
   grid_dependency_launch();
 
   if (warp == 0) {
-    // loads: one stage is kDepth of k of the tile's rows of A and columns of B
-    constexpr uint32_t bytes = CG * (Shape::a_bytes + Shape::b_bytes);
+    // loads: one stage is kDepth of k of the tile's rows of A and columns of B, all parts
+    constexpr uint32_t bytes = CG * Shape::stage_bytes;
     uint32_t n = 0;
     for (int i = 0; !*dead; ++i) {
       int item = item_of(l, worker, workers, i);
@@ -722,7 +747,8 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
       split_range(p, t.split, k0, k1);
       const int am = t.m0 + (int)rank * 128;
       for (int seg = 0; seg < p.segments && !*dead; ++seg) {
-        const int az = p.a_sheet[seg] + t.m_half, bz = p.b_sheet[seg] + t.n_half;
+        // the parts of a value are neighbouring sheets
+        const int az = (p.a_sheet[seg] + t.m_half) * kParts<T>, bz = (p.b_sheet[seg] + t.n_half) * kParts<T>;
         for (int kb = k0; kb < k1; ++kb, ++n) {
           const int s = n % S;
           if (n >= S && !__all_sync(0xffffffffu, mbar_wait_clocks(empty + s, ((n / S) - 1) & 1))) {
@@ -731,28 +757,37 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
           }
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
-            uint8_t *da = sa + s * Shape::a_bytes, *db = sb + s * Shape::b_bytes;
-            const int k = kb * kDepth;
-            if (p.a_mn) {
-              tma_load<CG>(da, &ma, am, k, az, full + s);
-              tma_load<CG>(da + Shape::a_bytes / 2, &ma, am + 64, k, az, full + s);
-            } else {
-              tma_load<CG>(da, &ma, k, am, az, full + s);
-            }
-            if (EPI == kGate) {
-              // half of the columns are g's, half u's; in a pair of blocks each loads one of them
-              if (CG == 2) {
-                tma_load<CG>(db, &mb, k, t.n0, bz + (int)rank, full + s);
-              } else {
-                tma_load<CG>(db, &mb, k, t.n0, bz, full + s);
-                tma_load<CG>(db + Shape::b_bytes / 2, &mb, k, t.n0, bz + 1, full + s);
-              }
-            } else if (p.b_mn) {
+            const int k = kb * kDepth<T>;
 #pragma unroll
-              for (int j = 0; j < BN / CG / 64; ++j)
-                tma_load<CG>(db + j * kDepth * 128, &mb, t.n0 + (int)rank * (BN / CG) + j * 64, k, bz, full + s);
-            } else {
-              tma_load<CG>(db, &mb, k, t.n0 + (int)rank * (BN / CG), bz, full + s);
+            for (int q = 0; q < kParts<T>; ++q) {
+              uint8_t *da = tiles + s * Shape::stage_bytes + q * Shape::a_bytes;
+              const int z = az + q;
+              if (p.a_mn) {
+                tma_load<CG>(da, &ma, am, k, z, full + s);
+                tma_load<CG>(da + Shape::a_bytes / 2, &ma, am + 64, k, z, full + s);
+              } else {
+                tma_load<CG>(da, &ma, k, am, z, full + s);
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < kParts<T>; ++q) {
+              uint8_t *db = tiles + s * Shape::stage_bytes + kParts<T> * Shape::a_bytes + q * Shape::b_bytes;
+              const int z = bz + q;
+              if (EPI == kGate) {
+                // half of the columns are g's, half u's; in a pair of blocks each loads one of them
+                if (CG == 2) {
+                  tma_load<CG>(db, &mb, k, t.n0, z + (int)rank * kParts<T>, full + s);
+                } else {
+                  tma_load<CG>(db, &mb, k, t.n0, z, full + s);
+                  tma_load<CG>(db + Shape::b_bytes / 2, &mb, k, t.n0, z + kParts<T>, full + s);
+                }
+              } else if (p.b_mn) {
+#pragma unroll
+                for (int j = 0; j < BN / CG / 64; ++j)
+                  tma_load<CG>(db + j * kDepth<T> * 128, &mb, t.n0 + (int)rank * (BN / CG) + j * 64, k, z, full + s);
+              } else {
+                tma_load<CG>(db, &mb, k, t.n0 + (int)rank * (BN / CG), z, full + s);
+              }
             }
           }
           __syncwarp();
@@ -772,7 +807,8 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
       const ProductArgs &p = l.p[which];
       const uint32_t idesc = tc_idesc(p.f16, p.a_mn, p.b_mn, 128 * CG, BN);
       const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
-      const uint64_t a0 = tc_desc(sa, p.a_mn, Shape::a_bytes / 2), b0 = tc_desc(sb, p.b_mn, kDepth * 128);
+      const uint64_t a0 = tc_desc(tiles, p.a_mn, Shape::a_bytes / 2, kDepth<T>);
+      const uint64_t b0 = tc_desc(tiles + kParts<T> * Shape::a_bytes, p.b_mn, kDepth<T> * 128, kDepth<T>);
       const Tile t = tile_of<EPI, CG, BN>(p, item);
       int k0, k1;
       split_range(p, t.split, k0, k1);
@@ -782,7 +818,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t d = tmem + acc * BN;
+      const uint32_t d = tmem + acc * kSums<T> * BN;
       const int steps = p.segments * (k1 - k0);
       bool lost = false;
       for (int i = 0; i < steps; ++i, ++n) {
@@ -792,11 +828,21 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
           break;
         }
         tc_fence_after();
-        const uint64_t a = a0 + s * (Shape::a_bytes >> 4), b = b0 + s * (Shape::b_bytes >> 4);
+        const uint64_t a = a0 + s * (Shape::stage_bytes >> 4), b = b0 + s * (Shape::stage_bytes >> 4);
         if (elect_one()) {
+          if constexpr (kParts<T> == 3) {
+            constexpr int pairs[6][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {2, 0}};
 #pragma unroll
-          for (int j = 0; j < kDepth / 16; ++j)
-            tc_mma<CG>(d, a + j * a_step, b + j * b_step, idesc, i > 0 || j > 0);
+            for (int q = 0; q < 6; ++q)
+#pragma unroll
+              for (int j = 0; j < kDepth<T> / 16; ++j)
+                tc_mma<CG>(q ? d + BN : d, a + pairs[q][0] * (Shape::a_bytes >> 4) + j * a_step,
+                           b + pairs[q][1] * (Shape::b_bytes >> 4) + j * b_step, idesc, i > 0 || j > 0 || q > 1);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kDepth<T> / 16; ++j)
+              tc_mma<CG>(d, a + j * a_step, b + j * b_step, idesc, i > 0 || j > 0);
+          }
           tc_commit<CG>(empty + s);
           if (i == steps - 1) tc_commit<CG>(acc_full + acc);
         }
@@ -824,11 +870,11 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
   __syncwarp();
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_free<CG>(tmem, 2 * BN);
+  if (warp == 1) tmem_free<CG>(tmem, Shape::columns);
   if (threadIdx.x == 0 && *dead) atomicAdd(l.timeouts, 1u);
 }
 
-// Tile shapes by index, widest first.
+// Tile shapes by index, widest first.  float32's two accumulators, twice, leave no room for the widest.
 struct ProductTile {
   int cg, bn;
 };
@@ -859,8 +905,9 @@ cudaError_t launch_product_as(int blocks, const ProductLaunch &l, bool early, cu
 
 template <typename T, int EPI>
 cudaError_t launch_product_shape(int shape, int blocks, const ProductLaunch &l, bool early, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2)
+    if (shape == 0) return launch_product_as<T, EPI, 2, 256>(blocks, l, early, st);
   switch (shape) {
-    case 0: return launch_product_as<T, EPI, 2, 256>(blocks, l, early, st);
     case 1: return launch_product_as<T, EPI, 2, 128>(blocks, l, early, st);
     case 2: return launch_product_as<T, EPI, 1, 128>(blocks, l, early, st);
     default: return launch_product_as<T, EPI, 1, 64>(blocks, l, early, st);

@@ -201,14 +201,15 @@ __device__ __forceinline__ void tmem_wait(float (&v)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-// Shared-memory matrix descriptor (16-bit elements, 128-byte swizzle; fields in units of 16 bytes).
-//   k-major:  rows of 64 values of k (128 bytes), groups of 8 rows 1024 bytes apart
-//   mn-major: rows of 64 values of m or n, one row a value of k: groups of 8 k 1024 bytes apart
-//             (stride), chunks of 64 m or n `chunk` bytes apart (leading)
-__device__ __forceinline__ uint64_t tc_desc(const void *smem, bool mn, uint32_t chunk) {
+// Shared-memory matrix descriptor (16-bit elements; fields in units of 16 bytes).
+//   k-major:  rows of 64 (32) values of k in a swizzle of their 128 (64) bytes, groups of 8 rows one after another
+//   mn-major: rows of 64 values of m or n, one row a value of k, 128-byte swizzle: groups of 8 k 1024 bytes
+//             apart (stride), chunks of 64 m or n `chunk` bytes apart (leading)
+__device__ __forceinline__ uint64_t tc_desc(const void *smem, bool mn, uint32_t chunk, int depth) {
   const uint64_t addr = (smem_u32(smem) >> 4) & 0x3FFF;
-  const uint64_t lead = mn ? (chunk >> 4) : 1;
-  return addr | (lead << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+  const bool narrow = !mn && depth == 32;
+  const uint64_t lead = mn ? (chunk >> 4) : 1, stride = (narrow ? 512 : 1024) >> 4;
+  return addr | (lead << 16) | (stride << 32) | (1ull << 46) | ((narrow ? 4ull : 2ull) << 61);
 }
 
 // Instruction descriptor: float32 accumulator, A and B both float16 or both bfloat16.
