@@ -443,7 +443,11 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, floa
       finish = std::max(finish, rows * ((s.n + 3) / 4));
     }
     items += (int64_t)p.m_halves * p.m_tiles * p.n_halves * p.n_tiles * p.splits;
-    l.first[++l.count] = (int)items;
+    l.first[++l.count] = (int)std::min<int64_t>(items, INT32_MAX);
+  }
+  if (items > INT32_MAX) {  // more tiles than a launch counts
+    c.err = cudaErrorInvalidConfiguration;
+    return;
   }
   if (!l.count) return;
   // The items before the last product's are the longer ones; the workers that get one of them less make up

@@ -720,8 +720,8 @@ SLA_API sla_status sla_layernorm(int64_t rows, int64_t width, int32_t dtype, int
 
 SLA_API size_t sla_layernorm_backward_workspace_bytes(int64_t rows, int64_t width, int32_t dtype) {
   if (check_ln(rows, width, dtype, dtype) != SLA_OK) return 0;
-  // the most blocks that any layout of these rows leaves partial sums from
-  const int64_t parts = std::max<int64_t>(16, std::min<int64_t>(kMaxParts, rows));
+  // the most blocks that any layout of these rows leaves partial sums from (whole sets of up to 8 classes)
+  const int64_t parts = std::max<int64_t>(16, std::min<int64_t>(kMaxParts, rows + 7));
   return align256((size_t)parts * 2 * (size_t)width * sizeof(float));
 }
 

@@ -569,10 +569,11 @@ SLA_API size_t sla_gated_ffn_backward_workspace_bytes(const sla_ffn *f);
  *   y      device, [tokens][out]
  *   saved  device, sla_gated_ffn_saved_bytes, 256-byte aligned, or NULL: kept for the backward call
  *   workspace  device, sla_gated_ffn_workspace_bytes, 256-byte aligned
- * Sums run in float32.  With 16-bit data, g, u (where saved) and h are rounded to dtype; with
- * float32 data they stay float32, and the products are float32's (each factor split into three
- * bfloat16 parts, 24 bits in all; an infinity among the factors gives NaN).  A float16 block whose
- * |h| passes 65504 gives infinities, as float16 data does everywhere.
+ * Sums run in float32.  With 16-bit data, h and what is saved (act(g) and u act'(g)) are rounded to
+ * dtype; with float32 data they stay float32, and the products are float32's (each factor split into
+ * three bfloat16 parts, 24 bits in all; an infinity among the factors gives NaN).  A float16 block
+ * whose |h| passes 65504 gives infinities, as float16 data does everywhere.  The first call on a
+ * device looks up addresses and sets kernel attributes: make it before any stream capture.
  */
 SLA_API sla_status sla_gated_ffn(const sla_ffn *f, const void *x, int64_t ldx, const void *w_in, const void *b_in,
                                  const void *w_out, const void *b_out, void *y, void *saved, size_t saved_bytes,

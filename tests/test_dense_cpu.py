@@ -89,3 +89,12 @@ def test_cpu_tensors_are_refused():
                  lambda: sla.sla_layernorm_backward(x, x, None, x[:, 0], x[:, 0])):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_layernorm_workspace_covers_every_class_of_rows(lib):
+    # rows of odd widths are dealt to blocks in whole sets of up to 8 classes, so that a few rows can have more
+    # blocks than there are rows: the partial sums of all of them have to fit
+    for rows in (1, 9, 17, 20, 100, 1209, 1215, 5000):
+        for width, dtype, classes in ((8191, 3, 8), (8193, 2, 8), (4095, 0, 4), (4100, 3, 2)):
+            blocks = min(1216 // classes * classes, -(-rows // classes) * classes)
+            assert lib.sla_layernorm_backward_workspace_bytes(rows, width, dtype) >= blocks * 2 * width * 4
