@@ -14,6 +14,7 @@
 #include "sla_common.cuh"
 #include "sla_few.cuh"
 #include "sla_host.h"
+#include "sla_narrow.cuh"
 #include "sla_net.cuh"
 #include "sla_product.cuh"
 
@@ -668,16 +669,54 @@ BackwardScratch backward_scratch(const sla_ffn *f, char *base) {
   return w;
 }
 
+// ------------------------------------------------------------------ narrow blocks
+
+template <typename T>
+bool vec_out(const T *p, int64_t ld) {
+  return aligned(p, 32) && ld * sizeof(T) % 32 == 0;
+}
+
+// Tiles of x that the fused kernel of a narrow block keeps on their way (4 to 2), or 0 where its weights and
+// they do not fit a multiprocessor's shared memory.
+int narrow_stages(const sla_ffn *f) {
+  if (f->dtype == SLA_F32 || f->width > kNarrowMost || f->out > kNarrowMost || f->hidden > 64 * kNarrowChunk) return 0;
+  for (int s = 4; s >= 2; --s)
+    if (narrow_bytes((f->width + 63) / 64, (f->hidden + kNarrowChunk - 1) / kNarrowChunk, round_up(f->out, 16), s) <=
+        227 * 1024)
+      return s;
+  return 0;
+}
+
+template <typename T>
+void run_narrow(Call &c, const sla_ffn *f, int stages, const Operand &x, const Operand &w_in, const T *b_in,
+                const Operand &w_out, const T *b_out, T *y) {
+  if constexpr (sizeof(T) == 2) {
+    if (c.err != cudaSuccess) return;
+    NarrowArgs p;
+    p.tokens = (int)f->tokens, p.hidden = (int)f->hidden, p.out = (int)f->out;
+    p.k_blocks = (int)((f->width + 63) / 64), p.chunks = (int)((f->hidden + kNarrowChunk - 1) / kNarrowChunk);
+    p.out_pad = (int)round_up(f->out, 16), p.stages = stages;
+    p.f16 = f->dtype == SLA_F16, p.act = f->activation;
+    p.b_in = b_in, p.b_in_vec = aligned(b_in, 32) && f->hidden % 16 == 0;
+    p.b_out = b_out, p.b_out_vec = aligned(b_out, 32);
+    p.y = y, p.y_vec = vec_out(y, f->out), p.timeouts = c.timeouts;
+    cudaError_t e = encode(&p.x, x, 64, 128, f->dtype);
+    if (e == cudaSuccess) e = encode(&p.w_in, w_in, 64, 64, f->dtype);
+    if (e == cudaSuccess) e = encode(&p.w_out, w_out, 64, p.out_pad, f->dtype);
+    if (e == cudaSuccess) {
+      const int blocks = (int)std::min<int64_t>((f->tokens + 127) / 128, sm_count());
+      c.launched(launch_narrow<T>(p, blocks, c.early(), c.st));
+    } else {
+      c.err = e;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ the two calls
 
 sla_status finish(const Call &c) {
   count_launches(c.launches);
   return c.err == cudaSuccess ? SLA_OK : fail(c.err);
-}
-
-template <typename T>
-bool vec_out(const T *p, int64_t ld) {
-  return aligned(p, 32) && ld * sizeof(T) % 32 == 0;
 }
 
 template <typename T>
@@ -710,6 +749,10 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
   const Operand oi = as_operand(packs, w_in, f->hidden, f->width, f->width, 2, keep_x ? saved + L.w_in : w.w_in);
   const Operand oo = as_operand(packs, w_out, f->out, f->hidden, f->hidden, 1, keep_o ? saved + L.w_out : w.w_out);
   run_packs<T>(c, packs);
+  if (const int stages = saved ? 0 : narrow_stages(f)) {
+    run_narrow<T>(c, f, stages, ox, oi, b_in, oo, b_out, y);
+    return finish(c);
+  }
   const Operand oh{h, f->hidden, f->tokens, sheets_of<T>(), ldg, f->tokens * ldg};
   ProductJob gate{gate_size(f), ox, false, oi, false, {}, true};
   gate.p.act = f->activation, gate.p.vec = 1;

@@ -1,0 +1,280 @@
+// The whole gated feed-forward block of a narrow network in one kernel (16-bit data, forward, nothing kept).
+//
+// Between the two products of a narrow block h is the largest array by far: at 64 -> 256 -> 64 it is four
+// times x, and a million tokens write and read 1 GB of it for 0.25 GB of x and y.  Here it never leaves
+// the multiprocessor.  A block keeps both weight matrices in shared memory for its lifetime and takes
+// tiles of 128 tokens; of the hidden units it takes 64 at a time:
+//
+//   S = X [Wg; Wu]^T   128 x 128 in tensor memory, twice     (mma)
+//   H = act(g) u       128 x 64 in shared memory, twice      (sixteen warps, in two teams)
+//   Y += H Wo^T        128 x out in tensor memory, twice     (mma)
+//
+// The mma warp issues the first product of a chunk, then the second of the chunk before, so that one team
+// computes H while the tensor core works for the other.  H is written as TMA would have put it there: 128-byte
+// rows of 64 hidden units, 16-byte units swizzled by the row.
+#pragma once
+
+#include "sla_product.cuh"
+
+namespace sla {
+
+constexpr int kNarrowMost = 128;    // columns of x and of y at most
+constexpr int kNarrowChunk = 64;    // hidden units at a time
+constexpr int kNarrowTile = 16384;  // bytes of 128 rows of 64 values
+
+struct NarrowArgs {
+  CUtensorMap x, w_in, w_out;  // boxes of 64 columns by 128, 64 and out_pad rows
+  int tokens, hidden, out;
+  int k_blocks, chunks, out_pad, stages;
+  int f16, act;
+  const void *b_in, *b_out;    // T or NULL
+  int b_in_vec, b_out_vec, y_vec;
+  void *y;                     // T [tokens][out]
+  uint32_t *timeouts;
+};
+
+// Bytes of shared memory with `stages` tiles of x: weights, x, H and the barriers.
+inline int64_t narrow_bytes(int64_t k_blocks, int64_t chunks, int64_t out_pad, int stages) {
+  return chunks * (k_blocks * kNarrowTile + out_pad * 128) + stages * k_blocks * kNarrowTile + 2 * kNarrowTile + 1024 + 256;
+}
+
+template <typename T>
+cudaError_t launch_narrow(const NarrowArgs &p, int blocks, bool early, cudaStream_t st);
+
+template <typename T>
+__global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ NarrowArgs p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t *w_in = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *w_out = w_in + p.chunks * p.k_blocks * kNarrowTile;
+  uint8_t *xs = w_out + p.chunks * p.out_pad * 128;
+  uint8_t *hs = xs + p.stages * p.k_blocks * kNarrowTile;
+  uint64_t *w_full = (uint64_t *)(hs + 2 * kNarrowTile);
+  uint64_t *s_full = w_full + 1, *s_empty = s_full + 2, *h_full = s_empty + 2, *h_empty = h_full + 2,
+           *y_full = h_empty + 2, *y_empty = y_full + 2, *drained = y_empty + 2, *x_full = drained + 1,
+           *x_empty = x_full + 4;
+  uint32_t *tmem_slot = (uint32_t *)(x_empty + 4);
+  volatile uint32_t *dead = tmem_slot + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = (p.tokens + 127) / 128, mine = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+
+  if (threadIdx.x == 0) {
+    mbar_init(w_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, 8);
+      mbar_init(h_full + i, 8);
+      mbar_init(h_empty + i, 1);
+      mbar_init(y_full + i, 1);
+      mbar_init(y_empty + i, 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(x_full + i, 1);
+      mbar_init(x_empty + i, 1);
+    }
+    mbar_init(drained, 1);
+    *dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+    tma_prefetch_map(&p.x);
+    tma_prefetch_map(&p.w_in);
+    tma_prefetch_map(&p.w_out);
+  }
+  if (warp == 1) tmem_alloc<1>(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_dependency_launch();
+
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_arrive_expect_tx(w_full, p.chunks * (p.k_blocks * kNarrowTile + p.out_pad * 128));
+      for (int c = 0; c < p.chunks; ++c) {
+        for (int k = 0; k < p.k_blocks; ++k) {
+          uint8_t *to = w_in + (c * p.k_blocks + k) * kNarrowTile;  // 64 rows of Wg, then of Wu
+          tma_load<1>(to, &p.w_in, k * 64, c * kNarrowChunk, 0, w_full);
+          tma_load<1>(to + kNarrowTile / 2, &p.w_in, k * 64, c * kNarrowChunk, 1, w_full);
+        }
+        tma_load<1>(w_out + c * p.out_pad * 128, &p.w_out, c * kNarrowChunk, 0, 0, w_full);
+      }
+    }
+    __syncwarp();
+    int n = 0;
+    for (; n < mine && !*dead; ++n) {
+      const int s = n % p.stages;
+      if (n >= p.stages && !__all_sync(0xffffffffu, mbar_wait_clocks(x_empty + s, (n / p.stages - 1) & 1))) {
+        *dead = 1;
+        break;
+      }
+      if (elect_one()) {
+        mbar_arrive_expect_tx(x_full + s, p.k_blocks * kNarrowTile);
+        const int row = (blockIdx.x + n * gridDim.x) * 128;
+        for (int k = 0; k < p.k_blocks; ++k)
+          tma_load<1>(xs + (s * p.k_blocks + k) * kNarrowTile, &p.x, k * 64, row, 0, x_full + s);
+      }
+      __syncwarp();
+    }
+    // every copy has landed before the block may end
+    if (!mbar_wait_clocks(w_full, 0)) *dead = 1;
+    for (int i = n > p.stages ? n - p.stages : 0; i < n; ++i)
+      if (!mbar_wait_clocks(x_full + i % p.stages, (i / p.stages) & 1)) *dead = 1;
+  } else if (warp == 1) {
+    const uint32_t idesc1 = tc_idesc(p.f16, false, false, 128, 128), idesc2 = tc_idesc(p.f16, false, false, 128, p.out_pad);
+    const uint64_t dx = tc_desc(xs, false, 0, 64), dw = tc_desc(w_in, false, 0, 64), dh = tc_desc(hs, false, 0, 64),
+                   dout = tc_desc(w_out, false, 0, 64);
+    bool lost = !__all_sync(0xffffffffu, mbar_wait_clocks(w_full, 0));
+    // the second product of chunk j (of all of the block's)
+    auto second = [&](int j) {
+      const int tile = j / p.chunks, c = j - tile * p.chunks, b = j & 1;
+      if (c == 0 && tile >= 2 && !__all_sync(0xffffffffu, mbar_wait_clocks(y_empty + (tile & 1), (tile / 2 - 1) & 1)))
+        return false;
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_full + b, (j >> 1) & 1))) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma<1>(tmem + 256 + (tile & 1) * 128, dh + b * (kNarrowTile >> 4) + k * 2,
+                    dout + c * (p.out_pad * 128 >> 4) + k * 2, idesc2, c > 0 || k > 0);
+        tc_commit<1>(h_empty + b);
+        if (c == p.chunks - 1) tc_commit<1>(y_full + (tile & 1));
+      }
+      __syncwarp();
+      return true;
+    };
+    int j = 0;
+    for (int n = 0; n < mine && !lost; ++n) {
+      const int s = n % p.stages;
+      lost = !__all_sync(0xffffffffu, mbar_wait_clocks(x_full + s, (n / p.stages) & 1));
+      for (int c = 0; c < p.chunks && !lost; ++c, ++j) {
+        const int b = j & 1;
+        if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_clocks(s_empty + b, ((j >> 1) - 1) & 1))) {
+          lost = true;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          for (int k = 0; k < p.k_blocks; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              tc_mma<1>(tmem + b * 128, dx + (s * p.k_blocks + k) * (kNarrowTile >> 4) + q * 2,
+                        dw + (c * p.k_blocks + k) * (kNarrowTile >> 4) + q * 2, idesc1, k > 0 || q > 0);
+          tc_commit<1>(s_full + b);
+          if (c == p.chunks - 1) tc_commit<1>(x_empty + s);
+        }
+        __syncwarp();
+        if (j > 0) lost = !second(j - 1);
+      }
+    }
+    if (!lost && j > 0) lost = !second(j - 1);
+    if (lost) {
+      *dead = 1;
+      if (elect_one()) tc_commit<1>(drained);  // the mma in flight still read shared memory
+      __syncwarp();
+      mbar_wait_clocks(drained, 0);
+    }
+  } else {
+    const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
+    const int row = quarter * 32 + lane;  // of the tile
+    const uint32_t lanes = (uint32_t)quarter << 21;
+    // y of one tile: 16 columns at a time, the team's halves in turn
+    auto finish = [&](int tile) {
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(y_full + (tile & 1), (tile >> 1) & 1))) return false;
+      tc_fence_after();
+      const int64_t token = (blockIdx.x + (int64_t)tile * gridDim.x) * 128 + row;
+      for (int c = side * 16; c < p.out_pad; c += 32) {
+        float v[16];
+        tmem_load16(tmem + lanes + 256 + (tile & 1) * 128 + c, v);
+        tmem_wait(v);
+        const int count = p.out - c;
+        if (token < p.tokens && count > 0) {
+          if (p.b_out) add_bias<T, 16>(v, (const T *)p.b_out + c, count, p.b_out_vec);
+          store_row<T, 16>((T *)p.y + token * p.out + c, v, count, p.y_vec);
+        }
+      }
+      release_accumulator<1>(y_empty + (tile & 1), lane);
+      return true;
+    };
+    int pending = -1;  // a tile whose y this team has to store, once the next tile's chunks are under way
+    bool lost = false;
+    const int total = mine * p.chunks;
+    for (int j = team; j < total && !lost; j += 2) {
+      const int tile = j / p.chunks, f0 = (j - tile * p.chunks) * kNarrowChunk + side * 32;
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(s_full + team, (j >> 1) & 1))) {
+        lost = true;
+        break;
+      }
+      tc_fence_after();
+      uint32_t ph[2][8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float g[16], u[16], h[16];
+        tmem_load16(tmem + lanes + team * 128 + side * 32 + q * 16, g);
+        tmem_load16(tmem + lanes + team * 128 + 64 + side * 32 + q * 16, u);
+        if (p.b_in) {
+          float bg[16], bu[16];
+          const int count = p.hidden - f0 - q * 16;
+          load_row<T, 16>((const T *)p.b_in + f0 + q * 16, bg, count, p.b_in_vec);
+          load_row<T, 16>((const T *)p.b_in + p.hidden + f0 + q * 16, bu, count, p.b_in_vec);
+          tmem_wait(g);
+          tmem_wait(u);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 a = add2(f2(g[i], g[i + 1]), f2(bg[i], bg[i + 1]));
+            const float2 b = add2(f2(u[i], u[i + 1]), f2(bu[i], bu[i + 1]));
+            g[i] = a.x, g[i + 1] = a.y, u[i] = b.x, u[i + 1] = b.y;
+          }
+        } else {
+          tmem_wait(g);
+          tmem_wait(u);
+        }
+        if (q == 1) release_accumulator<1>(s_empty + team, lane);
+        with_activation(p.act, [&](auto act) { gate<act.value, false, 16>(g, u, h); });
+        pack16<T>(h, ph[q]);
+      }
+      if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_clocks(h_empty + team, ((j >> 1) - 1) & 1))) {
+        lost = true;
+        break;
+      }
+      const StoreBox<128> box{hs + team * kNarrowTile + quarter * 4096, lane};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) box.put(2 * side + q, ph[q]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(h_full + team);
+      if (pending >= 0 && tile > pending) {
+        lost = !finish(pending);
+        pending = -1;
+      }
+      if ((tile & 1) == team && pending < 0) pending = tile;
+    }
+    // tiles whose y is left: those of this team's parity that no later chunk of the team made it store
+    if (!lost && pending >= 0) lost = !finish(pending);
+    if (lost) *dead = 1;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  tc_fence_after();
+  if (warp == 1) tmem_free<1>(tmem, 512);
+  if (threadIdx.x == 0 && *dead) atomicAdd(p.timeouts, 1u);
+}
+
+template <typename T>
+cudaError_t launch_narrow_as(const NarrowArgs &p, int blocks, bool early, cudaStream_t st) {
+  const int smem = (int)narrow_bytes(p.k_blocks, p.chunks, p.out_pad, p.stages);
+  auto kernel = narrow_kernel<T>;
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !(allowed.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess) allowed.fetch_or(1ull << (dev & 63));
+  }
+  if (e != cudaSuccess) return e;
+  LaunchConfig cfg(dim3(blocks), 576, smem, st, early);
+  return cudaLaunchKernelEx(&cfg.c, kernel, p);
+}
+
+}  // namespace sla

@@ -1,5 +1,6 @@
-// The tensor-core products of sla_product.cuh and sla_few.cuh for f16 data.
+// The kernels of sla_product.cuh, sla_few.cuh and sla_narrow.cuh for f16 data.
 #include "sla_few.cuh"
+#include "sla_narrow.cuh"
 #include "sla_product.cuh"
 
 namespace sla {
@@ -16,6 +17,11 @@ cudaError_t launch_product<f16>(int epi, int shape, int blocks, const ProductLau
 template <>
 cudaError_t launch_few<f16>(Epilogue epi, const FewArgs &p, cudaStream_t st) {
   return epi == kGate ? launch_few_gate<f16, true>(p, st) : launch_few_gate<f16, false>(p, st);
+}
+
+template <>
+cudaError_t launch_narrow<f16>(const NarrowArgs &p, int blocks, bool early, cudaStream_t st) {
+  return launch_narrow_as<f16>(p, blocks, early, st);
 }
 
 }  // namespace sla

@@ -1,4 +1,4 @@
-// The tensor-core products of sla_product.cuh and sla_few.cuh for float data.
+// The kernels of sla_product.cuh and sla_few.cuh for float data.
 #include "sla_few.cuh"
 #include "sla_product.cuh"
 

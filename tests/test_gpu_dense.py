@@ -236,6 +236,20 @@ def test_ffn_forward_and_backward(shape, dtype):
     assert all(p is None or torch.equal(p, q) for p, q in zip(got, again))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens", [33, 20000, 60001])
+@pytest.mark.parametrize("width,hidden,out", [(64, 256, 64), (40, 50, 24), (128, 130, 128), (17, 192, 5), (72, 448, 16)])
+def test_ffn_narrow_forward(width, hidden, out, tokens, dtype):
+    """Narrow blocks run in one kernel, which takes several tiles of tokens in turn (one to seven chunks of h a tile)."""
+    bias = tokens != 20000
+    args = ffn_inputs(tokens, width, hidden, out, dtype, bias, seed=hidden)
+    y = sla.sla_gated_ffn(*args, activation="gelu_tanh")
+    ref = ffn64(*[None if t is None else t.double() for t in args], "gelu_tanh")
+    assert rel(y, ref) <= FFN_TOL[dtype]
+    assert float((y.double() - ref).abs().max()) <= 8 * FFN_TOL[dtype] * float(ref.abs().max())
+    assert torch.equal(y, sla.sla_gated_ffn(*args, activation="gelu_tanh"))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("tokens", [1, 40, 260])
