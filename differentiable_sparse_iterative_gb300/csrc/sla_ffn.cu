@@ -697,7 +697,7 @@ void run_narrow(Call &c, const sla_ffn *f, int stages, const Operand &x, const O
     p.k_blocks = (int)((f->width + 63) / 64), p.chunks = (int)((f->hidden + kNarrowChunk - 1) / kNarrowChunk);
     p.out_pad = (int)round_up(f->out, 16), p.stages = stages;
     p.f16 = f->dtype == SLA_F16, p.act = f->activation;
-    p.b_in = b_in, p.b_in_vec = aligned(b_in, 32) && f->hidden % 16 == 0;
+    p.b_in = b_in;
     p.b_out = b_out, p.b_out_vec = aligned(b_out, 32);
     p.y = y, p.y_vec = vec_out(y, f->out), p.timeouts = c.timeouts;
     cudaError_t e = encode(&p.x, x, 64, 128, f->dtype);

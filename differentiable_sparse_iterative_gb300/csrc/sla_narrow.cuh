@@ -28,27 +28,29 @@ struct NarrowArgs {
   int k_blocks, chunks, out_pad, stages;
   int f16, act;
   const void *b_in, *b_out;    // T or NULL
-  int b_in_vec, b_out_vec, y_vec;
+  int b_out_vec, y_vec;
   void *y;                     // T [tokens][out]
   uint32_t *timeouts;
 };
 
-// Bytes of shared memory with `stages` tiles of x: weights, x, H and the barriers.
+// Bytes of shared memory with `stages` tiles of x: weights, x, H, the biases of g and u in float32 and the barriers.
 inline int64_t narrow_bytes(int64_t k_blocks, int64_t chunks, int64_t out_pad, int stages) {
-  return chunks * (k_blocks * kNarrowTile + out_pad * 128) + stages * k_blocks * kNarrowTile + 2 * kNarrowTile + 1024 + 256;
+  return chunks * (k_blocks * kNarrowTile + out_pad * 128 + 2 * kNarrowChunk * 4) + stages * k_blocks * kNarrowTile +
+         2 * kNarrowTile + 1024 + 256;
 }
 
 template <typename T>
 cudaError_t launch_narrow(const NarrowArgs &p, int blocks, bool early, cudaStream_t st);
 
-template <typename T>
+template <typename T, int Act>
 __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ NarrowArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t *w_in = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   uint8_t *w_out = w_in + p.chunks * p.k_blocks * kNarrowTile;
   uint8_t *xs = w_out + p.chunks * p.out_pad * 128;
   uint8_t *hs = xs + p.stages * p.k_blocks * kNarrowTile;
-  uint64_t *w_full = (uint64_t *)(hs + 2 * kNarrowTile);
+  float *bias = (float *)(hs + 2 * kNarrowTile);  // of a chunk: 64 of g, then 64 of u
+  uint64_t *w_full = (uint64_t *)(bias + p.chunks * 2 * kNarrowChunk);
   uint64_t *s_full = w_full + 1, *s_empty = s_full + 2, *h_full = s_empty + 2, *h_empty = h_full + 2,
            *y_full = h_empty + 2, *y_empty = y_full + 2, *drained = y_empty + 2, *x_full = drained + 1,
            *x_empty = x_full + 4;
@@ -177,6 +179,14 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
     const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
     const int row = quarter * 32 + lane;  // of the tile
     const uint32_t lanes = (uint32_t)quarter << 21;
+    if (p.b_in) {
+      for (int i = threadIdx.x - 64; i < p.chunks * 2 * kNarrowChunk; i += 512) {
+        const int f = i / (2 * kNarrowChunk) * kNarrowChunk + i % kNarrowChunk;
+        const bool up = i / kNarrowChunk & 1;
+        bias[i] = f < p.hidden ? to_f32(((const T *)p.b_in)[f + (up ? p.hidden : 0)]) : 0.f;
+      }
+      asm volatile("bar.sync 1, 512;" ::: "memory");  // the epilogue warps
+    }
     // y of one tile: 16 columns at a time, the team's halves in turn
     auto finish = [&](int tile) {
       if (!__all_sync(0xffffffffu, mbar_wait_clocks(y_full + (tile & 1), (tile >> 1) & 1))) return false;
@@ -199,7 +209,7 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
     bool lost = false;
     const int total = mine * p.chunks;
     for (int j = team; j < total && !lost; j += 2) {
-      const int tile = j / p.chunks, f0 = (j - tile * p.chunks) * kNarrowChunk + side * 32;
+      const int tile = j / p.chunks;
       if (!__all_sync(0xffffffffu, mbar_wait_clocks(s_full + team, (j >> 1) & 1))) {
         lost = true;
         break;
@@ -211,25 +221,22 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
         float g[16], u[16], h[16];
         tmem_load16(tmem + lanes + team * 128 + side * 32 + q * 16, g);
         tmem_load16(tmem + lanes + team * 128 + 64 + side * 32 + q * 16, u);
+        tmem_wait(g);
+        tmem_wait(u);
         if (p.b_in) {
-          float bg[16], bu[16];
-          const int count = p.hidden - f0 - q * 16;
-          load_row<T, 16>((const T *)p.b_in + f0 + q * 16, bg, count, p.b_in_vec);
-          load_row<T, 16>((const T *)p.b_in + p.hidden + f0 + q * 16, bu, count, p.b_in_vec);
-          tmem_wait(g);
-          tmem_wait(u);
+          const float4 *bg = (const float4 *)(bias + (j - tile * p.chunks) * 2 * kNarrowChunk + side * 32 + q * 16);
+          const float4 *bu = bg + kNarrowChunk / 4;
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float2 a = add2(f2(g[i], g[i + 1]), f2(bg[i], bg[i + 1]));
-            const float2 b = add2(f2(u[i], u[i + 1]), f2(bu[i], bu[i + 1]));
-            g[i] = a.x, g[i + 1] = a.y, u[i] = b.x, u[i + 1] = b.y;
+          for (int i = 0; i < 4; ++i) {
+            const float4 a = bg[i], b = bu[i];
+            const float2 g0 = add2(f2(g[4 * i], g[4 * i + 1]), f2(a.x, a.y)), g1 = add2(f2(g[4 * i + 2], g[4 * i + 3]), f2(a.z, a.w));
+            const float2 u0 = add2(f2(u[4 * i], u[4 * i + 1]), f2(b.x, b.y)), u1 = add2(f2(u[4 * i + 2], u[4 * i + 3]), f2(b.z, b.w));
+            g[4 * i] = g0.x, g[4 * i + 1] = g0.y, g[4 * i + 2] = g1.x, g[4 * i + 3] = g1.y;
+            u[4 * i] = u0.x, u[4 * i + 1] = u0.y, u[4 * i + 2] = u1.x, u[4 * i + 3] = u1.y;
           }
-        } else {
-          tmem_wait(g);
-          tmem_wait(u);
         }
         if (q == 1) release_accumulator<1>(s_empty + team, lane);
-        with_activation(p.act, [&](auto act) { gate<act.value, false, 16>(g, u, h); });
+        gate<Act, false, 16>(g, u, h);
         pack16<T>(h, ph[q]);
       }
       if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_clocks(h_empty + team, ((j >> 1) - 1) & 1))) {
@@ -261,10 +268,10 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
   if (threadIdx.x == 0 && *dead) atomicAdd(p.timeouts, 1u);
 }
 
-template <typename T>
-cudaError_t launch_narrow_as(const NarrowArgs &p, int blocks, bool early, cudaStream_t st) {
+template <typename T, int Act>
+cudaError_t launch_narrow_act(const NarrowArgs &p, int blocks, bool early, cudaStream_t st) {
   const int smem = (int)narrow_bytes(p.k_blocks, p.chunks, p.out_pad, p.stages);
-  auto kernel = narrow_kernel<T>;
+  auto kernel = narrow_kernel<T, Act>;
   static std::atomic<uint64_t> allowed{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -275,6 +282,16 @@ cudaError_t launch_narrow_as(const NarrowArgs &p, int blocks, bool early, cudaSt
   if (e != cudaSuccess) return e;
   LaunchConfig cfg(dim3(blocks), 576, smem, st, early);
   return cudaLaunchKernelEx(&cfg.c, kernel, p);
+}
+
+template <typename T>
+cudaError_t launch_narrow_as(const NarrowArgs &p, int blocks, bool early, cudaStream_t st) {
+  switch (p.act) {
+    case SLA_ACT_SILU: return launch_narrow_act<T, SLA_ACT_SILU>(p, blocks, early, st);
+    case SLA_ACT_GELU: return launch_narrow_act<T, SLA_ACT_GELU>(p, blocks, early, st);
+    case SLA_ACT_GELU_TANH: return launch_narrow_act<T, SLA_ACT_GELU_TANH>(p, blocks, early, st);
+    default: return launch_narrow_act<T, SLA_ACT_RELU>(p, blocks, early, st);
+  }
 }
 
 }  // namespace sla
