@@ -5,12 +5,13 @@
 // the multiprocessor.  A block keeps both weight matrices in shared memory for its lifetime and takes
 // tiles of 128 tokens; of the hidden units it takes 64 at a time:
 //
-//   S = X [Wg; Wu]^T   128 x 128 in tensor memory, twice     (mma)
+//   S = X [Wg; Wu]^T   128 x 128 in tensor memory, three times (two with more than 64 outputs)   (mma)
 //   H = act(g) u       128 x 64 in shared memory, twice      (sixteen warps, in two teams)
 //   Y += H Wo^T        128 x out in tensor memory, twice     (mma)
 //
-// The mma warp issues the first product of a chunk, then the second of the chunk before, so that one team
-// computes H while the tensor core works for the other.  H is written as TMA would have put it there: 128-byte
+// The mma warp issues the first product as many chunks ahead of the second as there is room for, so that a
+// team that has left its H finds its next S (with two S, and the second product waited for in between,
+// 217 us for a million tokens).  H is written as TMA would have put it there: 128-byte
 // rows of 64 hidden units, 16-byte units swizzled by the row.
 #pragma once
 
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
   uint8_t *hs = xs + p.stages * p.k_blocks * kNarrowTile;
   float *bias = (float *)(hs + 2 * kNarrowTile);  // of a chunk: 64 of g, then 64 of u
   uint64_t *w_full = (uint64_t *)(bias + p.chunks * 2 * kNarrowChunk);
-  uint64_t *s_full = w_full + 1, *s_empty = s_full + 2, *h_full = s_empty + 2, *h_empty = h_full + 2,
+  uint64_t *s_full = w_full + 1, *s_empty = s_full + 3, *h_full = s_empty + 3, *h_empty = h_full + 2,
            *y_full = h_empty + 2, *y_empty = y_full + 2, *drained = y_empty + 2, *x_full = drained + 1,
            *x_empty = x_full + 4;
   uint32_t *tmem_slot = (uint32_t *)(x_empty + 4);
@@ -61,9 +62,11 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
 
   if (threadIdx.x == 0) {
     mbar_init(w_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(s_empty + i, 8);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(h_full + i, 8);
       mbar_init(h_empty + i, 1);
       mbar_init(y_full + i, 1);
@@ -86,6 +89,8 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int y_columns = p.out_pad <= 64 ? 64 : 128, sums = (512 - 2 * y_columns) / 128;
+  const uint32_t tmem_y = tmem + 512 - 2 * y_columns;
   grid_dependency_wait();
   grid_dependency_launch();
 
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma<1>(tmem + 256 + (tile & 1) * 128, dh + b * (kNarrowTile >> 4) + k * 2,
+          tc_mma<1>(tmem_y + (tile & 1) * y_columns, dh + b * (kNarrowTile >> 4) + k * 2,
                     dout + c * (p.out_pad * 128 >> 4) + k * 2, idesc2, c > 0 || k > 0);
         tc_commit<1>(h_empty + b);
         if (c == p.chunks - 1) tc_commit<1>(y_full + (tile & 1));
@@ -144,16 +149,13 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
       __syncwarp();
       return true;
     };
-    int j = 0;
-    for (int n = 0; n < mine && !lost; ++n) {
-      const int s = n % p.stages;
-      lost = !__all_sync(0xffffffffu, mbar_wait_clocks(x_full + s, (n / p.stages) & 1));
-      for (int c = 0; c < p.chunks && !lost; ++c, ++j) {
-        const int b = j & 1;
-        if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_clocks(s_empty + b, ((j >> 1) - 1) & 1))) {
-          lost = true;
-          break;
-        }
+    const int total = mine * p.chunks;
+    for (int j = 0, n = 0, c = 0; j < total + sums - 1 && !lost; ++j) {
+      if (j < total) {  // the first product of chunk j: chunk c of tile n
+        const int s = n % p.stages, b = j % sums;
+        lost = (c == 0 && !__all_sync(0xffffffffu, mbar_wait_clocks(x_full + s, (n / p.stages) & 1))) ||
+               (j >= sums && !__all_sync(0xffffffffu, mbar_wait_clocks(s_empty + b, (j / sums - 1) & 1)));
+        if (lost) break;
         tc_fence_after();
         if (elect_one()) {
           for (int k = 0; k < p.k_blocks; ++k)
@@ -165,10 +167,10 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
           if (c == p.chunks - 1) tc_commit<1>(x_empty + s);
         }
         __syncwarp();
-        if (j > 0) lost = !second(j - 1);
+        if (++c == p.chunks) c = 0, ++n;
       }
+      if (j >= sums - 1) lost = !second(j - (sums - 1));
     }
-    if (!lost && j > 0) lost = !second(j - 1);
     if (lost) {
       *dead = 1;
       if (elect_one()) tc_commit<1>(drained);  // the mma in flight still read shared memory
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
       const int64_t token = (blockIdx.x + (int64_t)tile * gridDim.x) * 128 + row;
       for (int c = side * 16; c < p.out_pad; c += 32) {
         float v[16];
-        tmem_load16(tmem + lanes + 256 + (tile & 1) * 128 + c, v);
+        tmem_load16(tmem_y + lanes + (tile & 1) * y_columns + c, v);
         tmem_wait(v);
         const int count = p.out - c;
         if (token < p.tokens && count > 0) {
@@ -210,7 +212,8 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
     const int total = mine * p.chunks;
     for (int j = team; j < total && !lost; j += 2) {
       const int tile = j / p.chunks;
-      if (!__all_sync(0xffffffffu, mbar_wait_clocks(s_full + team, (j >> 1) & 1))) {
+      const int b = j % sums;
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(s_full + b, (j / sums) & 1))) {
         lost = true;
         break;
       }
@@ -219,8 +222,8 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float g[16], u[16], h[16];
-        tmem_load16(tmem + lanes + team * 128 + side * 32 + q * 16, g);
-        tmem_load16(tmem + lanes + team * 128 + 64 + side * 32 + q * 16, u);
+        tmem_load16(tmem + lanes + b * 128 + side * 32 + q * 16, g);
+        tmem_load16(tmem + lanes + b * 128 + 64 + side * 32 + q * 16, u);
         tmem_wait(g);
         tmem_wait(u);
         if (p.b_in) {
@@ -228,14 +231,14 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
           const float4 *bu = bg + kNarrowChunk / 4;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 a = bg[i], b = bu[i];
+            const float4 a = bg[i], d = bu[i];
             const float2 g0 = add2(f2(g[4 * i], g[4 * i + 1]), f2(a.x, a.y)), g1 = add2(f2(g[4 * i + 2], g[4 * i + 3]), f2(a.z, a.w));
-            const float2 u0 = add2(f2(u[4 * i], u[4 * i + 1]), f2(b.x, b.y)), u1 = add2(f2(u[4 * i + 2], u[4 * i + 3]), f2(b.z, b.w));
+            const float2 u0 = add2(f2(u[4 * i], u[4 * i + 1]), f2(d.x, d.y)), u1 = add2(f2(u[4 * i + 2], u[4 * i + 3]), f2(d.z, d.w));
             g[4 * i] = g0.x, g[4 * i + 1] = g0.y, g[4 * i + 2] = g1.x, g[4 * i + 3] = g1.y;
             u[4 * i] = u0.x, u[4 * i + 1] = u0.y, u[4 * i + 2] = u1.x, u[4 * i + 3] = u1.y;
           }
         }
-        if (q == 1) release_accumulator<1>(s_empty + team, lane);
+        if (q == 1) release_accumulator<1>(s_empty + b, lane);
         gate<Act, false, 16>(g, u, h);
         pack16<T>(h, ph[q]);
       }
