@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
           }
         }
         if (q == 1) release_accumulator<1>(s_empty + b, lane);
-        gate<Act, false, 16>(g, u, h);
+        gate<Act, kCoarse<T>, false, 16>(g, u, h);
         pack16<T>(h, ph[q]);
       }
       if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_clocks(h_empty + team, ((j >> 1) - 1) & 1))) {
