@@ -131,45 +131,57 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
     const uint64_t dx = tc_desc(xs, false, 0, 64), dw = tc_desc(w_in, false, 0, 64), dh = tc_desc(hs, false, 0, 64),
                    dout = tc_desc(w_out, false, 0, 64);
     bool lost = !__all_sync(0xffffffffu, mbar_wait_clocks(w_full, 0));
-    // the second product of chunk j (of all of the block's)
-    auto second = [&](int j) {
-      const int tile = j / p.chunks, c = j - tile * p.chunks, b = j & 1;
-      if (c == 0 && tile >= 2 && !__all_sync(0xffffffffu, mbar_wait_clocks(y_empty + (tile & 1), (tile / 2 - 1) & 1)))
-        return false;
-      if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_full + b, (j >> 1) & 1))) return false;
+    // Buffers and phases are counted along: with the divisions that find them from a chunk's number this warp, which
+    // has a chunk's time for two products, was what the others waited for (2,000 clocks a chunk).  A wait for a
+    // fresh barrier's phase before its first is over at once.
+    int s = 0, b = 0, c = 0, c2 = 0;
+    uint32_t x_phase = 0, s_phase = 1, h_phase = 0, y_phase = 3;  // y_phase: bit for each of the two
+    uint32_t hb = 0, yb = 0;
+    const int total = mine * p.chunks;
+    auto second = [&] {  // the second product of the next chunk
+      if (c2 == 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait_clocks(y_empty + yb, (y_phase >> yb) & 1))) return false;
+        y_phase ^= 1u << yb;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_full + hb, h_phase))) return false;
       tc_fence_after();
+      const bool last = c2 == p.chunks - 1;
       if (elect_one()) {
+        const uint64_t da = dh + hb * (kNarrowTile >> 4), db = dout + c2 * (p.out_pad * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma<1>(tmem_y + (tile & 1) * y_columns, dh + b * (kNarrowTile >> 4) + k * 2,
-                    dout + c * (p.out_pad * 128 >> 4) + k * 2, idesc2, c > 0 || k > 0);
-        tc_commit<1>(h_empty + b);
-        if (c == p.chunks - 1) tc_commit<1>(y_full + (tile & 1));
+          tc_mma<1>(tmem_y + yb * y_columns, da + k * 2, db + k * 2, idesc2, c2 > 0 || k > 0);
+        tc_commit<1>(h_empty + hb);
+        if (last) tc_commit<1>(y_full + yb);
       }
       __syncwarp();
+      h_phase ^= hb;
+      hb ^= 1;
+      c2 = last ? 0 : c2 + 1;
+      yb ^= last;
       return true;
     };
-    const int total = mine * p.chunks;
-    for (int j = 0, n = 0, c = 0; j < total + sums - 1 && !lost; ++j) {
-      if (j < total) {  // the first product of chunk j: chunk c of tile n
-        const int s = n % p.stages, b = j % sums;
-        lost = (c == 0 && !__all_sync(0xffffffffu, mbar_wait_clocks(x_full + s, (n / p.stages) & 1))) ||
-               (j >= sums && !__all_sync(0xffffffffu, mbar_wait_clocks(s_empty + b, (j / sums - 1) & 1)));
+    for (int j = 0; j < total + sums - 1 && !lost; ++j) {
+      if (j < total) {  // the first product of the chunk
+        lost = (c == 0 && !__all_sync(0xffffffffu, mbar_wait_clocks(x_full + s, x_phase))) ||
+               !__all_sync(0xffffffffu, mbar_wait_clocks(s_empty + b, s_phase));
         if (lost) break;
         tc_fence_after();
+        const bool last = c == p.chunks - 1;
         if (elect_one()) {
-          for (int k = 0; k < p.k_blocks; ++k)
+          uint64_t da = dx + s * p.k_blocks * (kNarrowTile >> 4), db = dw + c * p.k_blocks * (kNarrowTile >> 4);
+          for (int k = 0; k < p.k_blocks; ++k, da += kNarrowTile >> 4, db += kNarrowTile >> 4)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              tc_mma<1>(tmem + b * 128, dx + (s * p.k_blocks + k) * (kNarrowTile >> 4) + q * 2,
-                        dw + (c * p.k_blocks + k) * (kNarrowTile >> 4) + q * 2, idesc1, k > 0 || q > 0);
+            for (int q = 0; q < 4; ++q) tc_mma<1>(tmem + b * 128, da + q * 2, db + q * 2, idesc1, k > 0 || q > 0);
           tc_commit<1>(s_full + b);
-          if (c == p.chunks - 1) tc_commit<1>(x_empty + s);
+          if (last) tc_commit<1>(x_empty + s);
         }
         __syncwarp();
-        if (++c == p.chunks) c = 0, ++n;
+        if (++b == sums) b = 0, s_phase ^= 1;
+        c = last ? 0 : c + 1;
+        if (last && ++s == p.stages) s = 0, x_phase ^= 1;
       }
-      if (j >= sums - 1) lost = !second(j - (sums - 1));
+      if (j >= sums - 1) lost = !second();
     }
     if (lost) {
       *dead = 1;
@@ -210,10 +222,11 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
     int pending = -1;  // a tile whose y this team has to store, once the next tile's chunks are under way
     bool lost = false;
     const int total = mine * p.chunks;
+    int tile = 0, c = team, b = team;  // chunk j is chunk c of its tile, its sums are in b
+    uint32_t s_phase = 0, h_phase = 1;
+    while (c >= p.chunks) c -= p.chunks, ++tile;
     for (int j = team; j < total && !lost; j += 2) {
-      const int tile = j / p.chunks;
-      const int b = j % sums;
-      if (!__all_sync(0xffffffffu, mbar_wait_clocks(s_full + b, (j / sums) & 1))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(s_full + b, s_phase))) {
         lost = true;
         break;
       }
@@ -227,7 +240,7 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
         tmem_wait(g);
         tmem_wait(u);
         if (p.b_in) {
-          const float4 *bg = (const float4 *)(bias + (j - tile * p.chunks) * 2 * kNarrowChunk + side * 32 + q * 16);
+          const float4 *bg = (const float4 *)(bias + c * 2 * kNarrowChunk + side * 32 + q * 16);
           const float4 *bu = bg + kNarrowChunk / 4;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -242,10 +255,11 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
         gate<Act, kCoarse<T>, false, 16>(g, u, h);
         pack16<T>(h, ph[q]);
       }
-      if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_clocks(h_empty + team, ((j >> 1) - 1) & 1))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_empty + team, h_phase))) {
         lost = true;
         break;
       }
+      h_phase ^= 1;
       const StoreBox<128> box{hs + team * kNarrowTile + quarter * 4096, lane};
 #pragma unroll
       for (int q = 0; q < 2; ++q) box.put(2 * side + q, ph[q]);
@@ -257,6 +271,10 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
         pending = -1;
       }
       if ((tile & 1) == team && pending < 0) pending = tile;
+      b += 2;
+      if (b >= sums) b -= sums, s_phase ^= 1;
+      c += 2;
+      while (c >= p.chunks) c -= p.chunks, ++tile;
     }
     // tiles whose y is left: those of this team's parity that no later chunk of the team made it store
     if (!lost && pending >= 0) lost = !finish(pending);
