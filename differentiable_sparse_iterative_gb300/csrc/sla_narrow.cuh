@@ -9,9 +9,7 @@
 //   H = act(g) u       128 x 64 in shared memory, twice      (sixteen warps, in two teams)
 //   Y += H Wo^T        128 x out in tensor memory, twice     (mma)
 //
-// The mma warp issues the first product as many chunks ahead of the second as there is room for, so that a
-// team that has left its H finds its next S (with two S, and the second product waited for in between,
-// 217 us for a million tokens).  H is written as TMA would have put it there: 128-byte
+// One warp issues the first products, as far ahead as there is room for, and another the second ones.  H is written as TMA would have put it there: 128-byte
 // rows of 64 hidden units, 16-byte units swizzled by the row.
 #pragma once
 
@@ -22,6 +20,7 @@ namespace sla {
 constexpr int kNarrowMost = 128;    // columns of x and of y at most
 constexpr int kNarrowChunk = 64;    // hidden units at a time
 constexpr int kNarrowTile = 16384;  // bytes of 128 rows of 64 values
+constexpr int kNarrowThreads = 19 * 32;
 
 struct NarrowArgs {
   CUtensorMap x, w_in, w_out;  // boxes of 64 columns by 128, 64 and out_pad rows
@@ -44,7 +43,7 @@ template <typename T>
 cudaError_t launch_narrow(const NarrowArgs &p, int blocks, bool early, cudaStream_t st);
 
 template <typename T, int Act>
-__global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ NarrowArgs p) {
+__global__ void __launch_bounds__(kNarrowThreads, 1) narrow_kernel(const __grid_constant__ NarrowArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t *w_in = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   uint8_t *w_out = w_in + p.chunks * p.k_blocks * kNarrowTile;
@@ -53,7 +52,7 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
   float *bias = (float *)(hs + 2 * kNarrowTile);  // of a chunk: 64 of g, then 64 of u
   uint64_t *w_full = (uint64_t *)(bias + p.chunks * 2 * kNarrowChunk);
   uint64_t *s_full = w_full + 1, *s_empty = s_full + 3, *h_full = s_empty + 3, *h_empty = h_full + 2,
-           *y_full = h_empty + 2, *y_empty = y_full + 2, *drained = y_empty + 2, *x_full = drained + 1,
+           *y_full = h_empty + 2, *y_empty = y_full + 2, *drained = y_empty + 2, *x_full = drained + 2,
            *x_empty = x_full + 4;
   uint32_t *tmem_slot = (uint32_t *)(x_empty + 4);
   volatile uint32_t *dead = tmem_slot + 1;
@@ -77,6 +76,7 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
       mbar_init(x_empty + i, 1);
     }
     mbar_init(drained, 1);
+    mbar_init(drained + 1, 1);
     *dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -127,67 +127,73 @@ __global__ void __launch_bounds__(576, 1) narrow_kernel(const __grid_constant__ 
     for (int i = n > p.stages ? n - p.stages : 0; i < n; ++i)
       if (!mbar_wait_clocks(x_full + i % p.stages, (i / p.stages) & 1)) *dead = 1;
   } else if (warp == 1) {
-    const uint32_t idesc1 = tc_idesc(p.f16, false, false, 128, 128), idesc2 = tc_idesc(p.f16, false, false, 128, p.out_pad);
-    const uint64_t dx = tc_desc(xs, false, 0, 64), dw = tc_desc(w_in, false, 0, 64), dh = tc_desc(hs, false, 0, 64),
-                   dout = tc_desc(w_out, false, 0, 64);
+    // Buffers and phases are counted along: with the divisions that find them from a chunk's number, and both
+    // products in one warp, issuing them took 2,000 clocks a chunk and was what the others waited for.  A wait
+    // for a fresh barrier's phase before its first is over at once.
+    const uint32_t idesc = tc_idesc(p.f16, false, false, 128, 128);
+    const uint64_t dx = tc_desc(xs, false, 0, 64), dw = tc_desc(w_in, false, 0, 64);
     bool lost = !__all_sync(0xffffffffu, mbar_wait_clocks(w_full, 0));
-    // Buffers and phases are counted along: with the divisions that find them from a chunk's number this warp, which
-    // has a chunk's time for two products, was what the others waited for (2,000 clocks a chunk).  A wait for a
-    // fresh barrier's phase before its first is over at once.
-    int s = 0, b = 0, c = 0, c2 = 0;
-    uint32_t x_phase = 0, s_phase = 1, h_phase = 0, y_phase = 3;  // y_phase: bit for each of the two
-    uint32_t hb = 0, yb = 0;
-    const int total = mine * p.chunks;
-    auto second = [&] {  // the second product of the next chunk
-      if (c2 == 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_clocks(y_empty + yb, (y_phase >> yb) & 1))) return false;
-        y_phase ^= 1u << yb;
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_full + hb, h_phase))) return false;
-      tc_fence_after();
-      const bool last = c2 == p.chunks - 1;
-      if (elect_one()) {
-        const uint64_t da = dh + hb * (kNarrowTile >> 4), db = dout + c2 * (p.out_pad * 128 >> 4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma<1>(tmem_y + yb * y_columns, da + k * 2, db + k * 2, idesc2, c2 > 0 || k > 0);
-        tc_commit<1>(h_empty + hb);
-        if (last) tc_commit<1>(y_full + yb);
-      }
-      __syncwarp();
-      h_phase ^= hb;
-      hb ^= 1;
-      c2 = last ? 0 : c2 + 1;
-      yb ^= last;
-      return true;
-    };
-    for (int j = 0; j < total + sums - 1 && !lost; ++j) {
-      if (j < total) {  // the first product of the chunk
-        lost = (c == 0 && !__all_sync(0xffffffffu, mbar_wait_clocks(x_full + s, x_phase))) ||
-               !__all_sync(0xffffffffu, mbar_wait_clocks(s_empty + b, s_phase));
-        if (lost) break;
+    int s = 0, b = 0;
+    uint32_t x_phase = 0, s_phase = 1;
+    for (int n = 0; n < mine && !lost; ++n) {
+      lost = !__all_sync(0xffffffffu, mbar_wait_clocks(x_full + s, x_phase));
+      for (int c = 0; c < p.chunks && !lost; ++c) {
+        if (!__all_sync(0xffffffffu, mbar_wait_clocks(s_empty + b, s_phase))) {
+          lost = true;
+          break;
+        }
         tc_fence_after();
-        const bool last = c == p.chunks - 1;
         if (elect_one()) {
           uint64_t da = dx + s * p.k_blocks * (kNarrowTile >> 4), db = dw + c * p.k_blocks * (kNarrowTile >> 4);
           for (int k = 0; k < p.k_blocks; ++k, da += kNarrowTile >> 4, db += kNarrowTile >> 4)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tc_mma<1>(tmem + b * 128, da + q * 2, db + q * 2, idesc1, k > 0 || q > 0);
+            for (int q = 0; q < 4; ++q) tc_mma<1>(tmem + b * 128, da + q * 2, db + q * 2, idesc, k > 0 || q > 0);
           tc_commit<1>(s_full + b);
-          if (last) tc_commit<1>(x_empty + s);
+          if (c == p.chunks - 1) tc_commit<1>(x_empty + s);
         }
         __syncwarp();
         if (++b == sums) b = 0, s_phase ^= 1;
-        c = last ? 0 : c + 1;
-        if (last && ++s == p.stages) s = 0, x_phase ^= 1;
       }
-      if (j >= sums - 1) lost = !second();
+      if (++s == p.stages) s = 0, x_phase ^= 1;
     }
     if (lost) {
       *dead = 1;
       if (elect_one()) tc_commit<1>(drained);  // the mma in flight still read shared memory
       __syncwarp();
       mbar_wait_clocks(drained, 0);
+    }
+  } else if (warp == 18) {
+    const uint32_t idesc = tc_idesc(p.f16, false, false, 128, p.out_pad);
+    const uint64_t dh = tc_desc(hs, false, 0, 64), dw = tc_desc(w_out, false, 0, 64);
+    bool lost = !__all_sync(0xffffffffu, mbar_wait_clocks(w_full, 0));
+    uint32_t b = 0, y = 0, h_phase = 0, y_phase = 3;  // y_phase: a bit for each of the two
+    for (int n = 0; n < mine && !lost; ++n) {
+      lost = !__all_sync(0xffffffffu, mbar_wait_clocks(y_empty + y, (y_phase >> y) & 1));
+      y_phase ^= 1u << y;
+      for (int c = 0; c < p.chunks && !lost; ++c) {
+        if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_full + b, h_phase))) {
+          lost = true;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t da = dh + b * (kNarrowTile >> 4), db = dw + c * (p.out_pad * 128 >> 4);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tc_mma<1>(tmem_y + y * y_columns, da + q * 2, db + q * 2, idesc, c > 0 || q > 0);
+          tc_commit<1>(h_empty + b);
+          if (c == p.chunks - 1) tc_commit<1>(y_full + y);
+        }
+        __syncwarp();
+        h_phase ^= b;
+        b ^= 1;
+      }
+      y ^= 1;
+    }
+    if (lost) {
+      *dead = 1;
+      if (elect_one()) tc_commit<1>(drained + 1);
+      __syncwarp();
+      mbar_wait_clocks(drained + 1, 0);
     }
   } else {
     const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
@@ -301,7 +307,7 @@ cudaError_t launch_narrow_act(const NarrowArgs &p, int blocks, bool early, cudaS
     if (e == cudaSuccess) allowed.fetch_or(1ull << (dev & 63));
   }
   if (e != cudaSuccess) return e;
-  LaunchConfig cfg(dim3(blocks), 576, smem, st, early);
+  LaunchConfig cfg(dim3(blocks), kNarrowThreads, smem, st, early);
   return cudaLaunchKernelEx(&cfg.c, kernel, p);
 }
 
