@@ -8,8 +8,8 @@
 // They are taken for pairs of values: packed float32 arithmetic, the approximate exponential and
 // reciprocal, and for gelu the normal distribution by Abramowitz and Stegun 7.1.26 (1.5e-7), whose
 // exponential is the density's too.  Errors are a few 2^-22, for float32 data below what its sums
-// lose, for 16-bit data far below the rounding to 2^-9 or 2^-12.  (expf, erff and division cost the
-// float32 epilogue three times the instructions.)
+// lose, for float16 far below its rounding to 2^-12.  (expf, erff and division cost the float32
+// epilogue three times the instructions.)
 #pragma once
 
 #include <cuda_runtime.h>
@@ -20,7 +20,7 @@
 
 namespace sla {
 
-// bfloat16 data, rounded to 2^-9, takes the coarse sigmoid.
+// bfloat16 data, rounded to 2^-9, takes the coarse sigmoid, whose error is an eighth of that.
 template <typename T>
 inline constexpr bool kCoarse = false;
 template <>

@@ -2,7 +2,7 @@
 //
 // With a token or a few the weights are read once and little else happens: the floor is their bytes
 // over the memory's rate (25 MB at 1024 -> 4096 -> 1024: 3.8 us).  tcgen05 tiles would be 128 rows high
-// for one to thirty-two tokens, and a GPU's worth of them needs sums across blocks; here the weights are
+// for one to sixteen tokens, and a GPU's worth of them needs sums across blocks; here the weights are
 // the 16 rows of mma.sync m16n8k16 and the tokens its 8 columns, and what matters is that every thread
 // has many 16-byte loads on their way.
 //
@@ -15,13 +15,17 @@
 //
 // The second product is launched while the first runs (programmatic dependent launch): it loads its
 // first weights, which do not depend on h, and then waits for h.
+//
+// Measured (both products): one token 9.9 us at 1024 -> 4096 -> 1024 in bfloat16, where the tiled products take
+// 21.1; 16 tokens 11.9 against 19.3, and 17.5 against 18.1 at 256 -> 1024 -> 256 in float32.  A third eight of
+// tokens does not pay any more: 18.0 against 19.4 and 27.8 against 18.1 at 24 tokens.
 #pragma once
 
 #include "sla_product.cuh"
 
 namespace sla {
 
-constexpr int kFewTokens = 32;
+constexpr int kFewTokens = 16;
 constexpr int kFewWarps = 8;
 constexpr int kFewTurns = 4;  // turns of weights a thread has on their way
 
@@ -252,9 +256,7 @@ cudaError_t launch_few_gate(const FewArgs &p, cudaStream_t st) {
   int ranks = 1;
   const int rows = (p.n + 15) / 16;
   while (ranks < 8 && rows * ranks * 2 <= 192 && p.k >= 32 * kFewWarps * ranks * 2) ranks *= 2;
-  if (p.tokens <= 8) return launch_few_as<T, Gate, 1>(p, ranks, st);
-  if (p.tokens <= 16) return launch_few_as<T, Gate, 2>(p, ranks, st);
-  return launch_few_as<T, Gate, 4>(p, ranks, st);
+  return p.tokens <= 8 ? launch_few_as<T, Gate, 1>(p, ranks, st) : launch_few_as<T, Gate, 2>(p, ranks, st);
 }
 
 }  // namespace sla

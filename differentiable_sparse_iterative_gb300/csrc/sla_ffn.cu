@@ -371,13 +371,10 @@ struct ProductJob {
 
 // Runs the wanted ones of up to kGroup products with the plan made for all of them (whose split sums `parts` holds).
 template <typename T>
-void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, float *parts) {
+void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, const ProductPlan &plan, float *parts) {
   if (c.err != cudaSuccess) return;
   constexpr int S = sheets_of<T>(), D = kDepth<T>;
   constexpr int32_t part = S == 3 ? SLA_BF16 : NetType<T>::dtype;  // type of the operands
-  ProductSize sizes[kGroup];
-  for (int j = 0; j < count; ++j) sizes[j] = jobs[j].s;
-  const ProductPlan plan = plan_products(epi, sizes, count, S);
   const ProductTile tile = kProductTiles[plan.shape];
   const int bm = 128 * tile.cg, bn = tile.bn;
   // items with the most k blocks first, so that the last round is one of short ones
@@ -626,19 +623,23 @@ struct ForwardScratch {
   void *x, *w_in, *w_out, *h;
   float *parts;
   size_t total;
+  ProductPlan gate, y;
 };
 
 ForwardScratch forward_scratch(const sla_ffn *f, char *base) {
   const int S = f->dtype == SLA_F32 ? 3 : 1;
   Arena a{base};
-  ForwardScratch w;
+  ForwardScratch w{};
+  w.h = a.take(saved_layout(f).x - saved_layout(f).h);
+  w.total = a.used;
+  if (f->tokens <= kFewTokens) return w;
   w.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
   w.w_in = a.take(packed_bytes(2 * f->hidden, f->width, f->dtype));
   w.w_out = a.take(packed_bytes(f->out, f->hidden, f->dtype));
-  w.h = a.take(saved_layout(f).x - saved_layout(f).h);
   const ProductSize gate = gate_size(f), out = out_size(f);
-  w.parts = (float *)a.take(
-      std::max(plan_products(kGate, &gate, 1, S).partial[1], plan_products(kStore, &out, 1, S).partial[1]));
+  w.gate = plan_products(kGate, &gate, 1, S);
+  w.y = plan_products(kStore, &out, 1, S);
+  w.parts = (float *)a.take(std::max(w.gate.partial[1], w.y.partial[1]));
   w.total = a.used;
   return w;
 }
@@ -647,6 +648,7 @@ struct BackwardScratch {
   void *dy, *x, *w_in, *w_out, *dgu;
   float *sums, *columns, *parts;
   size_t total;
+  ProductPlan dh, rest;
 };
 
 BackwardScratch backward_scratch(const sla_ffn *f, char *base) {
@@ -660,11 +662,10 @@ BackwardScratch backward_scratch(const sla_ffn *f, char *base) {
   w.dgu = a.take((size_t)f->tokens * (size_t)hidden_pitch(f) * 2 * 2 * S);
   w.sums = (float *)a.take((size_t)((f->tokens + 31) / 32) * 2 * (size_t)hidden_pitch(f) * sizeof(float));
   w.columns = (float *)a.take(kSumParts * sizeof(float) * (size_t)(2 * hidden_pitch(f) + f->out));
-  size_t parts = 0;
   const ProductSize dh = dh_size(f), rest[kGroup] = {dx_size(f), dw_in_size(f), dw_out_size(f)};
-  parts = std::max(parts, plan_products(kGateBack, &dh, 1, S).partial[1]);
-  parts = std::max(parts, plan_products(kStore, rest, kGroup, S).partial[kGroup]);
-  w.parts = (float *)a.take(parts);
+  w.dh = plan_products(kGateBack, &dh, 1, S);
+  w.rest = plan_products(kStore, rest, kGroup, S);
+  w.parts = (float *)a.take(std::max(w.dh.partial[1], w.rest.partial[kGroup]));
   w.total = a.used;
   return w;
 }
@@ -721,12 +722,11 @@ sla_status finish(const Call &c) {
 
 template <typename T>
 sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, const T *b_in, const T *w_out,
-                   const T *b_out, T *y, char *saved, char *ws, cudaStream_t st) {
+                   const T *b_out, T *y, char *saved, const ForwardScratch &w, cudaStream_t st) {
   Call c{st};
   c.timeouts = timeouts_address();
   if (!c.timeouts) return fail(cudaGetLastError());
   const SavedLayout L = saved_layout(f);
-  const ForwardScratch w = forward_scratch(f, ws);
   const int64_t ldg = hidden_pitch(f);
   void *h = saved ? saved + L.h : w.h;
   if (f->tokens <= kFewTokens) {
@@ -759,25 +759,24 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
   gate.p.bias = b_in, gate.p.bias_vec = b_in && aligned(b_in, 32) && f->hidden % 16 == 0;
   gate.p.g = saved, gate.p.u = saved ? saved + L.u : nullptr;
   gate.p.h = (uint16_t *)h, gate.p.ldg = ldg, gate.p.sheet = f->tokens * ldg;
-  run_products<T>(c, kGate, &gate, 1, w.parts);
+  run_products<T>(c, kGate, &gate, 1, w.gate, w.parts);
   ProductJob out{out_size(f), oh, false, oo, false, {}, true};
   out.p.bias = b_out, out.p.bias_vec = aligned(b_out, 32);
   out.p.c = y, out.p.ldc = f->out, out.p.vec = vec_out(y, f->out);
-  run_products<T>(c, kStore, &out, 1, w.parts);
+  run_products<T>(c, kStore, &out, 1, w.y, w.parts);
   return finish(c);
 }
 
 template <typename T>
 sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int64_t ldx, const T *w_in,
-                    const T *w_out, const char *saved, T *dx, T *dw_in, T *dw_out, T *db_in, T *db_out, char *ws,
-                    cudaStream_t st) {
+                    const T *w_out, const char *saved, T *dx, T *dw_in, T *dw_out, T *db_in, T *db_out,
+                    const BackwardScratch &w, cudaStream_t st) {
   using E = typename std::conditional<sizeof(T) == 4, bf16, T>::type;  // type of the operand sheets
   constexpr int S = sheets_of<T>();
   Call c{st};
   c.timeouts = timeouts_address();
   if (!c.timeouts) return fail(cudaGetLastError());
   const SavedLayout L = saved_layout(f);
-  const BackwardScratch w = backward_scratch(f, ws);
   const int64_t ldg = hidden_pitch(f), sheet = f->tokens * ldg;
   const bool inner = dx || dw_in || db_in;
   const bool kept_x = keeps_packed(f, f->width), kept_o = keeps_packed(f, f->hidden);
@@ -798,8 +797,8 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
     dh.p.g = sv, dh.p.u = sv + L.u;
     dh.p.h = (uint16_t *)w.dgu, dh.p.ldg = ldg, dh.p.sheet = sheet;
     // the epilogue sums dg and du over 32 rows on its way, unless the product is split
-    if (db_in && plan_products(kGateBack, &dh.s, 1, S).splits[0] == 1) dh.p.sums = w.sums;
-    run_products<T>(c, kGateBack, &dh, 1, w.parts);
+    if (db_in && w.dh.splits[0] == 1) dh.p.sums = w.sums;
+    run_products<T>(c, kGateBack, &dh, 1, w.dh, w.parts);
     if (dh.p.sums)
       columns.of<float, 1>((f->tokens + 31) / 32, 2 * ldg, w.sums, 2 * ldg, 0, ldg, f->hidden, db_in);
     else if (db_in)
@@ -816,7 +815,7 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
   };
   const ProductJob rest[kGroup] = {job(dx_size(f), odgu, false, oi, dx), job(dw_in_size(f), odgu, true, ox, dw_in),
                                    job(dw_out_size(f), ody, true, oh, dw_out)};
-  run_products<T>(c, kStore, rest, kGroup, w.parts);
+  run_products<T>(c, kStore, rest, kGroup, w.rest, w.parts);
   return finish(c);
 }
 
@@ -873,12 +872,13 @@ SLA_API sla_status sla_gated_ffn(const sla_ffn *f, const void *x, int64_t ldx, c
   SLA_CHECK(check_matrix(w_out, f->out, f->hidden, f->hidden, f->dtype));
   const size_t e = net_size(f->dtype);
   if (!aligned(b_in, e) || !aligned(b_out, e)) return SLA_INVALID_ARG;
-  if (saved) SLA_CHECK(check_scratch(saved, saved_bytes, sla_gated_ffn_saved_bytes(f)));
-  SLA_CHECK(check_scratch(workspace, ws_bytes, sla_gated_ffn_workspace_bytes(f)));
+  if (saved) SLA_CHECK(check_scratch(saved, saved_bytes, saved_layout(f).total));
+  const ForwardScratch w = forward_scratch(f, (char *)workspace);
+  SLA_CHECK(check_scratch(workspace, ws_bytes, w.total));
   if (f->tokens == 0) return SLA_OK;
 #define SLA_FFN_FWD(T)                                                                                             \
   forward<T>(f, (const T *)x, ldx, (const T *)w_in, (const T *)b_in, (const T *)w_out, (const T *)b_out, (T *)y, \
-             (char *)saved, (char *)workspace, (cudaStream_t)stream)
+             (char *)saved, w, (cudaStream_t)stream)
   return f->dtype == SLA_F32 ? SLA_FFN_FWD(float) : f->dtype == SLA_F16 ? SLA_FFN_FWD(f16) : SLA_FFN_FWD(bf16);
 #undef SLA_FFN_FWD
 }
@@ -896,8 +896,9 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
   for (const void *p : {(const void *)dx, (const void *)dw_in, (const void *)dw_out, (const void *)db_in,
                         (const void *)db_out})
     if (!aligned(p, e)) return SLA_INVALID_ARG;
-  SLA_CHECK(check_scratch(saved, saved_bytes, sla_gated_ffn_saved_bytes(f)));
-  SLA_CHECK(check_scratch(workspace, ws_bytes, sla_gated_ffn_backward_workspace_bytes(f)));
+  SLA_CHECK(check_scratch(saved, saved_bytes, saved_layout(f).total));
+  const BackwardScratch w = backward_scratch(f, (char *)workspace);
+  SLA_CHECK(check_scratch(workspace, ws_bytes, w.total));
   cudaStream_t st = (cudaStream_t)stream;
   if (f->tokens == 0) {  // sums over no tokens
     const struct {
@@ -913,7 +914,7 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
   }
 #define SLA_FFN_BWD(T)                                                                                               \
   backward<T>(f, (const T *)dy, lddy, (const T *)x, ldx, (const T *)w_in, (const T *)w_out, (const char *)saved,    \
-              (T *)dx, (T *)dw_in, (T *)dw_out, (T *)db_in, (T *)db_out, (char *)workspace, st)
+              (T *)dx, (T *)dw_in, (T *)dw_out, (T *)db_in, (T *)db_out, w, st)
   return f->dtype == SLA_F32 ? SLA_FFN_BWD(float) : f->dtype == SLA_F16 ? SLA_FFN_BWD(f16) : SLA_FFN_BWD(bf16);
 #undef SLA_FFN_BWD
 }

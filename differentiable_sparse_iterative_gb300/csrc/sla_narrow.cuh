@@ -9,8 +9,8 @@
 //   H = act(g) u       128 x 64 in shared memory, twice      (sixteen warps, in two teams)
 //   Y += H Wo^T        128 x out in tensor memory, twice     (mma)
 //
-// One warp issues the first products, as far ahead as there is room for, and another the second ones.  H is written as TMA would have put it there: 128-byte
-// rows of 64 hidden units, 16-byte units swizzled by the row.
+// One warp issues the first products, as far ahead as there is room for, and another the second ones.  H is
+// written as TMA would have put it there: 128-byte rows of 64 hidden units, 16-byte units swizzled by the row.
 #pragma once
 
 #include "sla_product.cuh"

@@ -11,6 +11,7 @@ autograd graph, leading dimensions allowed); layer_norm and gated_ffn are differ
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -61,6 +62,29 @@ def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> Tu
     if dim == 2 and (width == 1 or t.stride(1) == 1) and (t.stride(0) >= width or rows <= 1):
         return t.data_ptr(), rows, t.stride(0)
     raise ValueError(f"{name} must be contiguous, or a matrix with contiguous rows that do not overlap")
+
+
+# What a call needs that depends on its sizes alone is asked for once: two or three calls less of a
+# microsecond each, where one token's kernels take ten.
+@functools.lru_cache(maxsize=512)
+def _ln_backward_bytes(rows: int, width: int, dt: int, device: int) -> int:
+    return _lib().sla_layernorm_backward_workspace_bytes(rows, width, dt)
+
+
+class _FFNSizes:
+    def __init__(self, tokens, width, hidden, out, dt, act):
+        self.descriptor = _abi.sla_ffn(tokens, width, hidden, out, dt, act)
+        self.ref = ctypes.byref(self.descriptor)
+        self.hidden, self.out = hidden, out
+        lib = _lib()
+        self.saved = lib.sla_gated_ffn_saved_bytes(self.ref)
+        self.forward = lib.sla_gated_ffn_workspace_bytes(self.ref)
+        self.backward = lib.sla_gated_ffn_backward_workspace_bytes(self.ref)
+
+
+@functools.lru_cache(maxsize=512)
+def _ffn_sizes(tokens, width, hidden, out, dt, act, device) -> _FFNSizes:
+    return _FFNSizes(tokens, width, hidden, out, dt, act)
 
 
 def _param(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> Optional[int]:
@@ -163,7 +187,7 @@ def sla_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[t
         dbp = db.data_ptr()
     lib = _lib()
     if want_grad_weight or want_grad_bias:
-        ws, nbytes = _scratch(lib.sla_layernorm_backward_workspace_bytes(rows, width, dt), dev, workspace)
+        ws, nbytes = _scratch(_ln_backward_bytes(rows, width, dt, index), dev, workspace)
         wsp = ws.data_ptr()
     _check(lib.sla_layernorm_backward(rows, width, dt, _DT[pt], gptr, lddy, ptr, ldx, wp, mp, rp, dxp, dwp, dbp, wsp,
                                       nbytes, _stream(index)), "sla_layernorm_backward")
@@ -213,7 +237,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
 # --------------------------------------------------------------------------- gated feed-forward block
 
 def _ffn(x, w_in, w_out, activation):
-    """(descriptor, address of x, its leading dimension, addresses of w_in and w_out)"""
+    """(sizes, address of x, its leading dimension, addresses of w_in and w_out)"""
     ptr, rows, ldx = _rows(x, "x")
     act = ACTIVATIONS.get(activation)
     if act is None:
@@ -223,7 +247,7 @@ def _ffn(x, w_in, w_out, activation):
                          f"{tuple(w_in.shape)} and {tuple(w_out.shape)}")
     out, hidden = w_out.shape
     width, index = x.size(-1), x.get_device()
-    f = _abi.sla_ffn(rows, width, hidden, out, _type(x, "x"), act)
+    f = _ffn_sizes(rows, width, hidden, out, _type(x, "x"), act, index)
     return (f, ptr, ldx, _param(w_in, "w_in", (2 * hidden, width), x.dtype, index),
             _param(w_out, "w_out", (out, hidden), x.dtype, index))
 
@@ -237,7 +261,7 @@ def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in
     "silu", "gelu", "gelu_tanh" or "relu".  Returns y, or with save=True (y, saved): the byte buffer
     of intermediates that sla_gated_ffn_backward takes."""
     f, ptr, ldx, wip, wop = _ffn(x, w_in, w_out, activation)
-    lib, dt, dev, index, fp = _lib(), x.dtype, x.device, x.get_device(), ctypes.byref(f)
+    lib, dt, dev, index = _lib(), x.dtype, x.device, x.get_device()
     bip = _param(b_in, "b_in", (2 * f.hidden,), dt, index)
     bop = _param(b_out, "b_out", (f.out,), dt, index)
     shape = x.shape[:-1] + (f.out,)
@@ -248,10 +272,10 @@ def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in
         yp = _param(y, "y", shape, dt, index)
     saved, sp, sn = None, None, 0
     if save:
-        saved, sn = _scratch(lib.sla_gated_ffn_saved_bytes(fp), dev, None)
+        saved, sn = _scratch(f.saved, dev, None)
         sp = saved.data_ptr()
-    ws, nbytes = _scratch(lib.sla_gated_ffn_workspace_bytes(fp), dev, workspace)
-    _check(lib.sla_gated_ffn(fp, ptr, ldx, wip, bip, wop, bop, yp, sp, sn, ws.data_ptr(), nbytes, _stream(index)),
+    ws, nbytes = _scratch(f.forward, dev, workspace)
+    _check(lib.sla_gated_ffn(f.ref, ptr, ldx, wip, bip, wop, bop, yp, sp, sn, ws.data_ptr(), nbytes, _stream(index)),
            "sla_gated_ffn")
     return (y, saved) if save else y
 
@@ -268,7 +292,7 @@ def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor
         raise ValueError(f"dy must have shape {tuple(x.shape[:-1]) + (f.out,)}, got {tuple(dy.shape)}")
     if saved.dtype != torch.uint8 or saved.get_device() != x.get_device() or not saved.is_contiguous():
         raise ValueError("saved must be the buffer that sla_gated_ffn(..., save=True) returned")
-    lib, dt, dev, fp = _lib(), x.dtype, x.device, ctypes.byref(f)
+    lib, dt, dev = _lib(), x.dtype, x.device
     dx = dw_in = dw_out = db_in = db_out = None
     if want_grad_x:
         dx = _empty(x.shape, dtype=dt, device=dev)
@@ -277,8 +301,8 @@ def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor
     if want_grad_bias:
         db_in, db_out = _empty(2 * f.hidden, dtype=dt, device=dev), _empty(f.out, dtype=dt, device=dev)
     grads = (dx, dw_in, dw_out, db_in, db_out)
-    ws, nbytes = _scratch(lib.sla_gated_ffn_backward_workspace_bytes(fp), dev, workspace)
-    _check(lib.sla_gated_ffn_backward(fp, gptr, lddy, ptr, ldx, wip, wop, saved.data_ptr(), saved.numel(),
+    ws, nbytes = _scratch(f.backward, dev, workspace)
+    _check(lib.sla_gated_ffn_backward(f.ref, gptr, lddy, ptr, ldx, wip, wop, saved.data_ptr(), saved.numel(),
                                       *[None if t is None else t.data_ptr() for t in grads], ws.data_ptr(), nbytes,
                                       _stream(x.get_device())), "sla_gated_ffn_backward")
     return grads
@@ -293,7 +317,8 @@ def sla_gated_ffn_check(device: Optional[int] = None) -> None:
 
 class GatedFFN(torch.autograd.Function):
     """y = (act(x Wg^T + bg) * (x Wu^T + bu)) w_out^T + b_out.  Saved for backward: x, the weights and
-    g, u and h (3 hidden values a token)."""
+    u act'(g), act(g) and h (3 hidden values a token), and the copies that were laid out anew for the
+    tensor core (float32, or a width or hidden size that 8 does not divide)."""
 
     @staticmethod
     def forward(ctx, x, w_in, w_out, b_in, b_out, activation):

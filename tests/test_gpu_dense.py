@@ -185,6 +185,42 @@ def test_layernorm_on_another_stream():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", [(20, 8191), (9, 8191), (3, 4095), (1, 8193)])
+def test_layernorm_backward_of_fewer_rows_than_blocks(rows, width, dtype):
+    # odd widths, so that the rows' starts fall into several classes of alignment and some blocks have no row
+    x, dy = (randn(rows, width, dtype=dtype, seed=s, shift=0.4) for s in (21, 22))
+    w, b = (randn(width, dtype=torch.float32, seed=s) for s in (23, 24))
+    ref = ln_grads64(x, w, b, dy)
+    _, mean, rstd = sla.sla_layernorm(x, w, b, stats=True)
+    got = sla.sla_layernorm_backward(dy, x, w, mean, rstd)
+    # relative L2: the output's rounding (dw, db are float32) and float32 sums of `width` or `rows` terms
+    for g, r, u in zip(got, ref, (U[dtype], U[torch.float32], U[torch.float32])):
+        assert rel(g, r) <= u + FP32_LN * 4
+
+
+@pytest.mark.parametrize("width", [1024, 1001])
+def test_layernorm_past_32_bit_offsets(width):
+    rows, part, dtype = 2_200_003, 100_000, torch.bfloat16
+    assert rows * width > 1 << 31
+    x, dy = (randn(rows, width, dtype=dtype, seed=s, shift=0.4) for s in (25, 26))
+    w, b = (randn(width, dtype=torch.float32, seed=s) for s in (27, 28))
+    y, mean, rstd = sla.sla_layernorm(x, w, b, stats=True)
+    dx, dw, db = sla.sla_layernorm_backward(dy, x, w, mean, rstd)
+    sums, terms = [0.0, 0.0], 0.0
+    for r in range(0, rows, part):
+        c = slice(r, r + part)
+        check_ln(x[c], w, b, y[c])
+        _, xh, r64, _ = ln64(x[c], w, b, 1e-5)
+        ref = ln_grads64(x[c], w, b, dy[c])
+        assert rel(dx[c], ref[0]) <= U[dtype] + FP32_LN * 4
+        amp = 1 + x[c].double().abs().amax(-1, keepdim=True) * r64
+        terms = terms + (dy[c].double().abs() * (1 + xh.abs()) * amp).sum(0)
+        sums = [sums[0] + ref[1], sums[1] + ref[2]]
+    for g, r in zip((dw, db), sums):  # as in test_layernorm_backward
+        assert float(((g.double() - r).abs() - U[torch.float32] * r.abs() - 2 * FP32_LN * terms).max()) <= 0
+
+
 # ------------------------------------------------------------------ gated feed-forward block
 
 ACTS = {"silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu, "relu": torch.relu,
@@ -337,6 +373,33 @@ def test_ffn_leading_dimensions_autograd_and_no_tokens():
     out = sla.gated_ffn(none, *w2)
     out.sum().backward()
     assert out.shape == (0, 32) and all(float(t.grad.abs().sum()) == 0.0 for t in w2)
+
+
+def test_ffn_past_32_bit_offsets():
+    # tokens * hidden passes 2^31 in the saved factors and in their gradients
+    tokens, width, hidden, part, dtype = 550_001, 32, 4096, 50_000, torch.bfloat16
+    assert tokens * hidden > 1 << 31
+    args = ffn_inputs(tokens, width, hidden, width, dtype, True, seed=110)
+    dy = randn(tokens, width, dtype=dtype, seed=111)
+    y, saved = sla.sla_gated_ffn(*args, save=True)
+    got = sla.sla_gated_ffn_backward(dy, *args[:3], saved, want_grad_bias=True)
+    sums = [0.0] * 4
+    for r in range(0, tokens, part):
+        c = slice(r, r + part)
+        leaves = [t.double().requires_grad_() for t in (args[0][c], *args[1:])]
+        ref = ffn64(*leaves, "silu")
+        assert rel(y[c], ref.detach()) <= FFN_TOL[dtype]
+        grads = torch.autograd.grad(ref, leaves, dy[c].double())
+        assert rel(got[0][c], grads[0]) <= FFN_TOL[dtype]
+        sums = [s + g for s, g in zip(sums, grads[1:])]
+    for name, g, r in zip(("dw_in", "dw_out", "db_in", "db_out"), got[1:], (sums[0], sums[1], sums[2], sums[3])):
+        assert rel(g, r) <= FFN_TOL[dtype], (name, rel(g, r))
+
+
+def test_ffn_check_reports_nothing_after_good_calls():
+    args = ffn_inputs(300, 128, 320, 128, torch.bfloat16, True, seed=115)
+    sla.sla_gated_ffn(*args)
+    assert sla.sla_gated_ffn_check() is None and sla.sla_gated_ffn_check(torch.cuda.current_device()) is None
 
 
 def test_ffn_on_another_stream_and_in_a_graph():
