@@ -131,8 +131,8 @@ struct Share {
   int t, first;        // thread of the group; column of its first vector
   int end;             // the column that no vector reaches
   int edge;            // column of its single element, or -1
-  int64_t row, step;   // its first row; rows from turn to turn
-  int64_t next;        // rows between the rows of a bundle
+  uint32_t row, step;  // its first row; rows from turn to turn (there are less than 2^31 rows)
+  uint32_t next;       // rows between the rows of a bundle
 };
 
 template <int VEC, int R>
@@ -145,9 +145,9 @@ __device__ __forceinline__ Share share_of(int width, int tpr, int classes, int s
   s.end = head + body;
   const int e = s.t < head ? s.t : s.t + body;
   s.edge = e < width ? e : -1;
-  s.next = (int64_t)groups * classes;
-  s.row = ((int64_t)(blockIdx.x / classes) * R * groups + threadIdx.x / tpr) * classes + cls;
-  s.step = (int64_t)(gridDim.x / classes) * R * groups * classes;
+  s.next = groups * classes;
+  s.row = ((blockIdx.x / classes) * R * groups + threadIdx.x / tpr) * classes + cls;
+  s.step = (gridDim.x / classes) * R * groups * classes;
   return s;
 }
 
@@ -158,7 +158,7 @@ inline constexpr bool kKeepParams = NI * Vec<T>::n <= 16;
 // shift: elements between a 16-byte boundary and row 0, shift_step: added by each row (mod VEC).
 template <typename T, typename P, int NI, int R, bool Edge>
 __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 : 1)
-    ln_forward(int64_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec,
+    ln_forward(uint32_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec,
                const T *__restrict__ x, int64_t ldx, const P *__restrict__ w, const P *__restrict__ b, float eps,
                T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
   using V = Vec<T>;
@@ -180,17 +180,19 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 
   float we = 1.f, be = 0.f;
   if (edge && w) we = to_f32(w[s.edge]);
   if (edge && b) be = to_f32(b[s.edge]);
+  // As loaded: a conversion here would wait for the load.
   V raw[R][NI];
-  float raw_e[R];
+  T raw_e[R];
   const T *px = x + s.row * ldx;  // the row that is asked for next
   T *py = y + s.row * (int64_t)width;
-  const int64_t x_next = s.next * ldx, x_step = s.step * ldx, y_next = s.next * width, y_step = s.step * width;
-  auto ask = [&](int64_t row) {
+  const int64_t x_next = s.next * ldx, x_step = s.step * ldx;
+  const int64_t y_next = s.next * (int64_t)width, y_step = s.step * (int64_t)width;
+  auto ask = [&](uint32_t row) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const bool live = row + r * s.next < rows;
-      raw_e[r] = 0.f;
-      if (edge && live) raw_e[r] = to_f32(px[r * x_next + s.edge]);
+      raw_e[r] = from_f32<T>(0.f);
+      if (edge && live) raw_e[r] = px[r * x_next + s.edge];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int c = s.first + i * apart;
@@ -203,8 +205,8 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 
   ask(s.row);
   int turn = 0;  // the slots alternate, so a turn's sums never meet the previous one's reads
   // every thread of a block makes the same number of turns (the sums need whole warps and blocks)
-  const int64_t lead = s.row - (int64_t)(threadIdx.x / tpr) * classes;
-  for (int64_t ahead = lead, row = s.row; ahead < rows; ahead += s.step, row += s.step, py += y_step, turn ^= 1) {
+  const uint32_t lead = s.row - threadIdx.x / tpr * classes;
+  for (uint32_t ahead = lead, row = s.row; ahead < rows; ahead += s.step, row += s.step, py += y_step, turn ^= 1) {
     float2 v[R][NI][H];
     float sum[R], sq[R], ve[R];
 #pragma unroll
@@ -216,8 +218,8 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 
 #pragma unroll
         for (int k = 0; k < H; ++k) a = add2(a, v[r][i][k]);
       }
-      ve[r] = raw_e[r];
-      sum[r] = a.x + a.y + (Edge ? ve[r] : 0.f);
+      ve[r] = Edge ? to_f32(raw_e[r]) : 0.f;
+      sum[r] = a.x + a.y + ve[r];
     }
     if (ahead + s.step < rows) ask(row + s.step);
     group_sums<R>(sum, tpr, slots[turn][0]);
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 4 
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t at = row + r * s.next;
+      const uint32_t at = row + r * s.next;
       if (at >= rows) continue;
       if (edge) py[r * y_next + s.edge] = from_f32<T>(ve[r] * sq[r] * we + be);
       if (s.t == 0 && mean) {
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_forward_any(int64_t rows, int6
 // parts: [gridDim.x][2][width] partial sums of dw and db (NULL: dx only).
 template <typename T, typename P, int NI, int R, bool Edge>
 __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 : 1)
-    ln_backward(int64_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec,
+    ln_backward(uint32_t rows, int width, int tpr, int classes, int shift, int64_t shift_step, int pvec,
                 const T *__restrict__ dy, int64_t lddy, const T *__restrict__ x, int64_t ldx, const P *__restrict__ w,
                 const float *__restrict__ mean, const float *__restrict__ rstd, T *__restrict__ dx,
                 float *__restrict__ parts) {
@@ -333,20 +335,21 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
   float we = 1.f, awe = 0.f, abe = 0.f;
   if (edge && w) we = to_f32(w[s.edge]);
   V rx[R][NI], rg[R][NI];
-  float rm[R], rr[R], ex[R], eg[R];
+  float rm[R], rr[R];
+  T ex[R], eg[R];
   const T *px = x + s.row * ldx, *pg = dy + s.row * lddy;  // the rows that are asked for next
   T *pd = dx + s.row * (int64_t)width;
-  const int64_t x_next = s.next * ldx, g_next = s.next * lddy, d_next = s.next * width;
-  auto ask = [&](int64_t row) {
+  const int64_t x_next = s.next * ldx, g_next = s.next * lddy, d_next = s.next * (int64_t)width;
+  auto ask = [&](uint32_t row) {
 #pragma unroll
     for (int r = 0; r < R; ++r, row += s.next) {
       const bool live = row < rows;
       rm[r] = live ? mean[row] : 0.f;
       rr[r] = live ? rstd[row] : 0.f;
-      ex[r] = eg[r] = 0.f;
+      ex[r] = eg[r] = from_f32<T>(0.f);
       if (edge && live) {
-        ex[r] = to_f32(px[r * x_next + s.edge]);
-        eg[r] = to_f32(pg[r * g_next + s.edge]);
+        ex[r] = px[r * x_next + s.edge];
+        eg[r] = pg[r * g_next + s.edge];
       }
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
@@ -363,8 +366,8 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
   };
   ask(s.row);
   int turn = 0;
-  const int64_t lead = s.row - (int64_t)(threadIdx.x / tpr) * classes;
-  for (int64_t ahead = lead, row = s.row; ahead < rows; ahead += s.step, row += s.step, turn ^= 1) {
+  const uint32_t lead = s.row - threadIdx.x / tpr * classes;
+  for (uint32_t ahead = lead, row = s.row; ahead < rows; ahead += s.step, row += s.step, turn ^= 1) {
     float2 xh[R][NI][H], g[R][NI][H];
     float sums[2 * R], rs[R], xe[R], ge[R];
 #pragma unroll
@@ -399,10 +402,11 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
       sums[2 * r + 1] = a2.x + a2.y;
       xe[r] = ge[r] = 0.f;
       if (edge) {
-        xe[r] = (ex[r] - rm[r]) * rs[r];
-        awe += eg[r] * xe[r];
-        abe += eg[r];
-        ge[r] = eg[r] * we;
+        const float g1 = to_f32(eg[r]);
+        xe[r] = (to_f32(ex[r]) - rm[r]) * rs[r];
+        awe += g1 * xe[r];
+        abe += g1;
+        ge[r] = g1 * we;
         sums[2 * r] += ge[r];
         sums[2 * r + 1] += ge[r] * xe[r];
       }
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
     if (ahead + s.step < rows) ask(row + s.step);
     group_sums<2 * R>(sums, tpr, slots[turn]);
     T *out = pd;
-    pd += s.step * width;
+    pd += s.step * (int64_t)width;
     if (!dx) continue;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -612,7 +616,7 @@ void launch_forward(const LnPlan &pl, int64_t rows, int64_t width, const void *x
                     const void *b, float eps, void *y, float *mean, float *rstd, cudaStream_t st) {
   // as many as run at once (beyond one vector a thread registers admit half as many: 11.9 -> 9.7 us at 5003 x 1001)
   const int grid = ln_grid(pl, rows, pl.block / pl.tpr * R, NI == 1 ? 1024 : 512);
-  ln_forward<T, P, NI, R, Edge><<<grid, pl.block, 0, st>>>(rows, (int)width, pl.tpr, pl.classes, pl.shift,
+  ln_forward<T, P, NI, R, Edge><<<grid, pl.block, 0, st>>>((uint32_t)rows, (int)width, pl.tpr, pl.classes, pl.shift,
                                                            pl.shift_step, pl.pvec({w, b}), (const T *)x, ldx,
                                                            (const P *)w, (const P *)b, eps, (T *)y, mean, rstd);
 }
@@ -638,7 +642,7 @@ int launch_backward(const LnPlan &pl, int64_t rows, int64_t width, const void *d
                     cudaStream_t st) {
   const int groups = pl.block / pl.tpr, grid = ln_grid(pl, rows, groups * R, NI == 1 ? 768 : 512);
   const size_t smem = groups > 1 && parts ? 2 * sizeof(float) * (size_t)width : 0;
-  ln_backward<T, P, NI, R, Edge><<<grid, pl.block, smem, st>>>(rows, (int)width, pl.tpr, pl.classes, pl.shift,
+  ln_backward<T, P, NI, R, Edge><<<grid, pl.block, smem, st>>>((uint32_t)rows, (int)width, pl.tpr, pl.classes, pl.shift,
                                                                pl.shift_step, pl.pvec({w}), (const T *)dy, lddy,
                                                                (const T *)x, ldx, (const P *)w, mean, rstd, (T *)dx,
                                                                parts);
