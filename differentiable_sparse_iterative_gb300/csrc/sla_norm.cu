@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
   constexpr bool keep = kKeepParams<T, NI>;
   extern __shared__ float cols[];  // more than one group: [2][width]
   __shared__ float slots[2][2 * R * 16];
+  grid_dependency_launch();  // ln_reduce_parts starts as multiprocessors become free, and waits there
   const Share s = share_of<N, R>(width, tpr, classes, shift, shift_step);
   const int apart = tpr * N, groups = blockDim.x / tpr;
   const float inv = 1.f / (float)width;
@@ -548,6 +549,7 @@ __global__ void __launch_bounds__(1024) ln_reduce_parts(int nparts, int64_t widt
   const int64_t c = blockIdx.x * (int64_t)kColTile + lane;
   const int which = blockIdx.y;
   P *out = which ? db : dw;
+  grid_dependency_wait();
   if (!out) return;
   float s = 0.f;
   if (c < width)
@@ -671,8 +673,10 @@ cudaError_t backward(int64_t rows, int64_t width, const LnPlan &pl, const void *
     nparts = pl.items == 1 ? SLA_LN_BWD(1, 1) : pl.items == 2 ? SLA_LN_BWD(2, 1) : SLA_LN_BWD(4, 1);
   }
 #undef SLA_LN_BWD
-  if (parts) ln_reduce_parts<P><<<dim3(ctiles, 2), 1024, 0, st>>>(nparts, width, parts, (P *)dw, (P *)db);
-  return cudaGetLastError();
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || !parts) return err;
+  LaunchConfig cfg(dim3(ctiles, 2), 1024, 0, st, true);
+  return cudaLaunchKernelEx(&cfg.c, ln_reduce_parts<P>, nparts, width, (const float *)parts, (P *)dw, (P *)db);
 }
 
 sla_status check_ln(int64_t rows, int64_t width, int32_t dtype, int32_t param_dtype) {
