@@ -75,7 +75,7 @@ class _FFNSizes:
     def __init__(self, tokens, width, hidden, out, dt, act):
         self.descriptor = _abi.sla_ffn(tokens, width, hidden, out, dt, act)
         self.ref = ctypes.byref(self.descriptor)
-        self.hidden, self.out = hidden, out
+        self.tokens, self.hidden, self.out = tokens, hidden, out
         lib = _lib()
         self.saved = lib.sla_gated_ffn_saved_bytes(self.ref)
         self.forward = lib.sla_gated_ffn_workspace_bytes(self.ref)
@@ -264,7 +264,7 @@ def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in
     lib, dt, dev, index = _lib(), x.dtype, x.device, x.get_device()
     bip = _param(b_in, "b_in", (2 * f.hidden,), dt, index)
     bop = _param(b_out, "b_out", (f.out,), dt, index)
-    shape = x.shape[:-1] + (f.out,)
+    shape = (f.tokens, f.out) if x.dim() == 2 else x.shape[:-1] + (f.out,)
     if y is None:
         y = _empty(shape, dtype=dt, device=dev)
         yp = y.data_ptr()

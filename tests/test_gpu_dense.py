@@ -420,6 +420,65 @@ def test_ffn_on_another_stream_and_in_a_graph():
     assert torch.equal(out, want)
 
 
+def dense_step(z, w, b, args, dy):
+    h, mean, rstd = sla.sla_layernorm(z, w, b, stats=True)
+    y, saved = sla.sla_gated_ffn(h, *args[1:], save=True)
+    dh = sla.sla_gated_ffn_backward(dy, h, *args[1:3], saved, want_grad_bias=True)
+    return (y, *dh, *sla.sla_layernorm_backward(dh[0], z, w, mean, rstd))
+
+
+def dense_case(tokens, seed):
+    # width and out that 8 does not divide and a split k: the calls' workspaces are in use
+    args = ffn_inputs(tokens, 100, 320, 100, torch.bfloat16, True, seed=seed)
+    w, b = randn(100, dtype=torch.float32, seed=seed + 5, shift=1.0), randn(100, dtype=torch.float32, seed=seed + 6)
+    return args[0], w, b, args, randn(tokens, 100, dtype=torch.bfloat16, seed=seed + 7)
+
+
+def test_dense_workspaces_on_several_streams():
+    cases = [dense_case(t, 120 + t) for t in (300, 9, 700, 2000)]
+    want = [dense_step(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in cases]
+    for _ in range(20):
+        for k, (c, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                got[k].append(dense_step(*c))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert all(torch.equal(a, b) for run in runs for a, b in zip(run, w))
+
+
+def test_dense_workspaces_in_several_threads():
+    from concurrent.futures import ThreadPoolExecutor
+    cases = [dense_case(t, 140 + t) for t in (300, 9, 700, 2000)]
+    want = [dense_step(*c) for c in cases]
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(len(cases)) as pool:  # all on the default stream
+        got = list(pool.map(lambda c: [dense_step(*c) for _ in range(20)], cases))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert all(torch.equal(a, b) for run in runs for a, b in zip(run, w))
+
+
+def test_dense_workspace_of_a_graph_is_its_own():
+    case, other = dense_case(300, 160), dense_case(700, 170)
+    want, expect = dense_step(*case), dense_step(*other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = dense_step(*case)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):  # replays and calls side by side
+        with torch.cuda.stream(s):
+            graph.replay()
+        got = dense_step(*other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert all(torch.equal(a, b) for a, b in zip(got, expect))
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals():
