@@ -21,6 +21,10 @@
 // most VEC - 1 before and after them (Edge).  Arrays whose rows do not start at the same boundary (strided
 // or odd views) and rows wider than the registers of a 512-thread block hold take the *_any
 // kernels, which read element by element and re-read from L2.
+//
+// Measured, forward and backward together, against the copy rate of 6.69 TB/s: 1,000,000 x 64 bfloat16 122 us
+// (0.78), 65536 x 1024 bfloat16 140 us (0.72), x 1001 150 us (0.65), 65536 x 512 float32 125 us (0.80).  16-bit rows
+// are held up by instructions as much as by memory.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -19,6 +19,11 @@
 // rows) keeps a tile of 128 CG x BN in tensor memory, twice: while eight warps empty one through the
 // epilogue, one thread feeds the next tile's mma and another its TMA loads.  Blocks are persistent and
 // take tiles in bands of kBand tile rows, so that what the running blocks read stays in L2.
+//
+// Measured at 16,384 tokens, 1024 -> 4096 -> 1024 in bfloat16, where cuBLAS reaches 1,725 to 1,902 TFLOP/s: dx,
+// dw_in and dw_out in one launch 1,836 TFLOP/s (tensor cores 96 % busy), out 1,531, gate 1,487 (its three arrays
+// are 403 MB), gate backward 769: bound by its loads and stores of 1.07 GB a 32,768 tokens, not by its product.
+// With few tiles a block (4,096 tokens) filling, draining and the last epilogue are most of a launch.
 #pragma once
 
 #include <atomic>
