@@ -195,8 +195,10 @@ void run_packs(Call &c, const PackJobs &jobs) {
 constexpr int kPlanDepth = 64;  // k of the blocks that plans are made in
 
 // Deepest sum of products that float32 data adds up in one accumulator, in such blocks: the tensor core
-// drops up to one unit of the running sum for every 16 products (2048 / 16 * 2^-24 * 2/3 = 5e-6 in all).
-constexpr int kFloatBlocks = 2048 / kPlanDepth;
+// drops up to one unit of the running sum for every 16 products (512 / 16 * 2^-24 * 2/3 = 1.3e-6 in all, a
+// plain float32 product's error; measured 1.0e-6 to 1.5e-6, and 2.8e-6 to 4.1e-6 at 2048).  A training step of 4,096
+// tokens, 256 -> 1024 -> 256, takes 149 us (157 at 2048), one of 16,384 tokens, 512 -> 2048 -> 512, 1,344 (1,238).
+constexpr int kFloatBlocks = 512 / kPlanDepth;
 
 struct ProductSize {
   int64_t m, n, k;           // of one half, of one segment

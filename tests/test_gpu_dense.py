@@ -9,7 +9,7 @@ Tolerances (u = the type's unit roundoff: 2^-24, 2^-11, 2^-8 for float32, float1
       (8 u in float16, where small values have fewer bits) covers them all.
       float32 data: a sum of K products in the tensor cores loses at most one unit 2^-23 of the running
       sum for every 16 products, half of it on average, 2/3 of it over a sum that grows as sqrt(k):
-      K / 16 * 2^-24 * 2/3 = 5e-6 at K = 2048, the longest run taken; with the splits' 2^-22: 1e-5.
+      K / 16 * 2^-24 * 2/3 = 5e-6 at K = 2048 (no longer run is taken in one); with the splits' 2^-22: 1e-5.
 """
 import math
 
