@@ -194,12 +194,6 @@ void run_packs(Call &c, const PackJobs &jobs) {
 
 constexpr int kPlanDepth = 64;  // k of the blocks that plans are made in
 
-// Deepest sum of products that float32 data adds up in one accumulator, in such blocks: the tensor core
-// drops up to one unit of the running sum for every 16 products (512 / 16 * 2^-24 * 2/3 = 1.3e-6 in all, a
-// plain float32 product's error; measured 1.0e-6 to 1.5e-6, and 2.8e-6 to 4.1e-6 at 2048).  A training step of 4,096
-// tokens, 256 -> 1024 -> 256, takes 149 us (157 at 2048), one of 16,384 tokens, 512 -> 2048 -> 512, 1,344 (1,238).
-constexpr int kFloatBlocks = 512 / kPlanDepth;
-
 struct ProductSize {
   int64_t m, n, k;           // of one half, of one segment
   int m_halves, n_halves, k_halves;
@@ -230,26 +224,24 @@ ProductPlan plan_products(Epilogue epi, const ProductSize *s, int count, int she
   double best_us = 1e30;
   for (int i = sheets == 3 ? 1 : 0; i < kProductTileCount; ++i) {
     const int64_t bm = 128 * kProductTiles[i].cg, bn = kProductTiles[i].bn, workers = sms / kProductTiles[i].cg;
-    int64_t tiles[kGroup], kb[kGroup], least[kGroup];
+    int64_t tiles[kGroup], kb[kGroup];
     double per[kGroup], blocks = 0;
     for (int j = 0; j < count; ++j) {
       kb[j] = (s[j].k + kPlanDepth - 1) / kPlanDepth;
       per[j] = s[j].k_halves;
-      const int64_t deepest = sheets == 3 ? std::max(1, kFloatBlocks / s[j].k_halves) : kb[j];
-      least[j] = (kb[j] + deepest - 1) / deepest;
       // columns of g and of u make separate tiles when their product is split
       tiles[j] = s[j].m_halves * ((s[j].m + bm - 1) / bm) * (epi == kGate ? 2 : s[j].n_halves) * ((s[j].n + bn - 1) / bn);
       blocks += tiles[j] * kb[j] * per[j];
     }
-    for (int fill = 0; fill < 3; ++fill) {  // whole; as many items as workers; twice as many
+    for (int fill = 0; fill < 6; ++fill) {  // whole; as many items as workers, up to five times
       ProductPlan plan{i, {}, {}};
       double busy = 0, us = start_us[i], longest = 0;
       bool split = false;
       int64_t items = 0;
       size_t partial = 0;
       for (int j = 0; j < count; ++j) {
-        int64_t n = least[j], t = tiles[j];
-        if (fill) n = std::max(n, (int64_t)(kb[j] * per[j] * fill * workers / std::max(1.0, blocks)));
+        int64_t t = tiles[j];
+        int64_t n = std::max<int64_t>(1, (int64_t)(kb[j] * per[j] * fill * workers / std::max(1.0, blocks)));
         n = std::min(n, kb[j]);
         if (epi == kGate && n == 1)
           t = s[j].m_halves * ((s[j].m + bm - 1) / bm) * ((s[j].n + bn / 2 - 1) / (bn / 2));
@@ -270,7 +262,7 @@ ProductPlan plan_products(Epilogue epi, const ProductSize *s, int count, int she
       }
       plan.partial[count] = partial;
       us += count > 1 ? std::max(longest, busy + (items > workers ? 0.5 * longest : 0)) : busy;
-      if (split) us += 4.0 + 2.0 * partial / 5e6;
+      if (split) us += 4.0 + 1.0 * partial / 5e6;
       if (us < best_us) {
         best_us = us;
         best = plan;
@@ -373,7 +365,8 @@ struct ProductJob {
 
 // Runs the wanted ones of up to kGroup products with the plan made for all of them (whose split sums `parts` holds).
 template <typename T>
-void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, const ProductPlan &plan, float *parts) {
+void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, const ProductPlan &plan, float *parts,
+                  float *runs) {
   if (c.err != cudaSuccess) return;
   constexpr int S = sheets_of<T>(), D = kDepth<T>;
   constexpr int32_t part = S == 3 ? SLA_BF16 : NetType<T>::dtype;  // type of the operands
@@ -389,6 +382,7 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, cons
   l.count = 0;
   l.first[0] = 0;
   l.timeouts = c.timeouts;
+  l.runs = runs;
   SplitSums f;
   int nsplit = 0;
   int64_t items = 0, finish = 0;
@@ -621,9 +615,12 @@ ProductSize dx_size(const sla_ffn *f) { return {f->tokens, f->width, f->hidden, 
 ProductSize dw_in_size(const sla_ffn *f) { return {f->hidden, f->width, f->tokens, 2, 1, 1}; }
 ProductSize dw_out_size(const sla_ffn *f) { return {f->out, f->hidden, f->tokens, 1, 1, 1}; }
 
+// Sums of the runs so far of every block's tile (float32's tiles have 128 columns at most).
+size_t run_bytes(const sla_ffn *f) { return f->dtype == SLA_F32 ? (size_t)sm_count() * 128 * 128 * sizeof(float) : 0; }
+
 struct ForwardScratch {
   void *x, *w_in, *w_out, *h;
-  float *parts;
+  float *parts, *runs;
   size_t total;
   ProductPlan gate, y;
 };
@@ -642,13 +639,14 @@ ForwardScratch forward_scratch(const sla_ffn *f, char *base) {
   w.gate = plan_products(kGate, &gate, 1, S);
   w.y = plan_products(kStore, &out, 1, S);
   w.parts = (float *)a.take(std::max(w.gate.partial[1], w.y.partial[1]));
+  w.runs = (float *)a.take(run_bytes(f));
   w.total = a.used;
   return w;
 }
 
 struct BackwardScratch {
   void *dy, *x, *w_in, *w_out, *dgu;
-  float *sums, *columns, *parts;
+  float *sums, *columns, *parts, *runs;
   size_t total;
   ProductPlan dh, rest;
 };
@@ -668,6 +666,7 @@ BackwardScratch backward_scratch(const sla_ffn *f, char *base) {
   w.dh = plan_products(kGateBack, &dh, 1, S);
   w.rest = plan_products(kStore, rest, kGroup, S);
   w.parts = (float *)a.take(std::max(w.dh.partial[1], w.rest.partial[kGroup]));
+  w.runs = (float *)a.take(run_bytes(f));
   w.total = a.used;
   return w;
 }
@@ -761,11 +760,11 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
   gate.p.bias = b_in, gate.p.bias_vec = b_in && aligned(b_in, 32) && f->hidden % 16 == 0;
   gate.p.g = saved, gate.p.u = saved ? saved + L.u : nullptr;
   gate.p.h = (uint16_t *)h, gate.p.ldg = ldg, gate.p.sheet = f->tokens * ldg;
-  run_products<T>(c, kGate, &gate, 1, w.gate, w.parts);
+  run_products<T>(c, kGate, &gate, 1, w.gate, w.parts, w.runs);
   ProductJob out{out_size(f), oh, false, oo, false, {}, true};
   out.p.bias = b_out, out.p.bias_vec = aligned(b_out, 32);
   out.p.c = y, out.p.ldc = f->out, out.p.vec = vec_out(y, f->out);
-  run_products<T>(c, kStore, &out, 1, w.y, w.parts);
+  run_products<T>(c, kStore, &out, 1, w.y, w.parts, w.runs);
   return finish(c);
 }
 
@@ -800,7 +799,7 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
     dh.p.h = (uint16_t *)w.dgu, dh.p.ldg = ldg, dh.p.sheet = sheet;
     // the epilogue sums dg and du over 32 rows on its way, unless the product is split
     if (db_in && w.dh.splits[0] == 1) dh.p.sums = w.sums;
-    run_products<T>(c, kGateBack, &dh, 1, w.dh, w.parts);
+    run_products<T>(c, kGateBack, &dh, 1, w.dh, w.parts, w.runs);
     if (dh.p.sums)
       columns.of<float, 1>((f->tokens + 31) / 32, 2 * ldg, w.sums, 2 * ldg, 0, ldg, f->hidden, db_in);
     else if (db_in)
@@ -817,7 +816,7 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
   };
   const ProductJob rest[kGroup] = {job(dx_size(f), odgu, false, oi, dx), job(dw_in_size(f), odgu, true, ox, dw_in),
                                    job(dw_out_size(f), ody, true, oh, dw_out)};
-  run_products<T>(c, kStore, rest, kGroup, w.rest, w.parts);
+  run_products<T>(c, kStore, rest, kGroup, w.rest, w.parts, w.runs);
   return finish(c);
 }
 

@@ -11,7 +11,10 @@
 // six products share six tiles (two tiles a product left the smaller tile shapes waiting for L2: 1.53 us
 // a block of 64 k instead of 1.0), and the five small products have an accumulator of their own: the
 // tensor core drops up to a unit of the running sum for every 16 k, which the small products
-// would feel five times as often in the large one's.
+// would feel five times as often in the large one's.  The large one takes 512 of k at a time (kRun: 512 / 16 *
+// 2^-24 * 2/3 = 1.3e-6, a plain float32 product's error; measured 1.0e-6 to 1.5e-6, and 2.8e-6 to 4.1e-6 in runs of
+// 2048); the epilogue warps add the runs up in float32, in a scratch of their own that stays in L2, while the next
+// run is under way (4,096 tokens, 1024 -> 4096, forward: 395 us, 384 in runs of 2048, 486 with splits in their place).
 // Either operand may be k-major (k contiguous) or mn-major (rows or columns contiguous): the tensor
 // core reads both from the 128-byte swizzled tiles that TMA writes, so no operand is transposed.
 //
@@ -49,6 +52,8 @@ template <typename T>
 inline constexpr int kDepth = sizeof(T) == 4 ? 32 : 64;  // k of a stage
 template <typename T>
 inline constexpr int kSums = sizeof(T) == 4 ? 2 : 1;  // accumulators of a tile
+template <typename T>
+inline constexpr int kRun = sizeof(T) == 4 ? 512 / kDepth<T> : 1 << 30;  // stages that one accumulator adds up at most
 constexpr int kGroup = 3;       // products of one launch
 
 struct ProductArgs {
@@ -81,6 +86,7 @@ struct ProductLaunch {
   int first[kGroup + 1];     // work items before each product's
   int count;
   int lead, extra;           // see item_of
+  float *runs;               // float32 with more than kRun stages: [blocks][128][BN] sums of the runs so far
   uint32_t *timeouts;
 };
 
@@ -395,6 +401,28 @@ struct Sums {
   }
 };
 
+// Stages of a work item.
+__device__ __forceinline__ int steps_of(const ProductArgs &p, int split) {
+  int k0, k1;
+  split_range(p, split, k0, k1);
+  return p.segments * (k1 - k0);
+}
+
+// 16 columns of a thread's row among its block's sums of the runs so far, four at a time beside its warp's
+// other rows; only this thread reads what it wrote.
+__device__ __forceinline__ void add_run(const float *run, int column, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 a = *reinterpret_cast<const float4 *>(run + (column / 4 + i) * 128);
+    v[4 * i] += a.x, v[4 * i + 1] += a.y, v[4 * i + 2] += a.z, v[4 * i + 3] += a.w;
+  }
+}
+__device__ __forceinline__ void put_run(float *run, int column, const float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4 *>(run + (column / 4 + i) * 128) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
 // A warp has read its part of an accumulator.
 template <int CG>
 __device__ __forceinline__ void release_accumulator(uint64_t *acc_empty, int lane) {
@@ -406,6 +434,29 @@ __device__ __forceinline__ void release_accumulator(uint64_t *acc_empty, int lan
     else
       mbar_arrive(acc_empty);
   }
+}
+
+// All runs of a work item but the last, whose sums are added up in float32: `seq` counts the runs of the block.
+// The columns of the warp are [first, first + width) and, for Two, those again BN / 2 further on.  False: a wait expired.
+template <typename T, int CG, int BN, bool Two>
+__device__ __forceinline__ bool drain_runs(int runs, uint32_t &seq, float *run, uint32_t tmem, int first, int width,
+                                           uint64_t *acc_full, uint64_t *acc_empty, int lane) {
+  for (int r = 0; r + 1 < runs; ++r, ++seq) {
+    const uint32_t acc = seq & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (seq >> 1) & 1))) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int i = 0; i < (Two ? 2 : 1) * width; i += 16) {
+      const int c = i < width ? first + i : BN / 2 + first + i - width;
+      Sums<T, BN, 16> sum;
+      sum.load(tmem + acc * kSums<T> * BN + c);
+      sum.wait();
+      if (r) add_run(run, c, sum.v);
+      put_run(run, c, sum.v);
+    }
+    release_accumulator<CG>(acc_empty + acc, lane);
+  }
+  return true;
 }
 
 // A box of 32 rows in shared memory, thread = row, in TMA's swizzle for rows of `Bytes` bytes: units of 16
@@ -476,14 +527,25 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
       tma_store_commit();
     }
   };
-  for (int tile = team;; tile += kTeams<T, BN>) {
+  float *run = f32 ? l.runs + ((int64_t)blockIdx.x * 4 + quarter) * 32 * BN + lane * 4 : nullptr;
+  uint32_t seq = team;  // accumulators before this tile's (16-bit data: one a tile)
+  for (int tile = team;; tile += kTeams<T, BN>, seq += kTeams<T, BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
     const Tile t = tile_of<EPI, CG, BN>(p, item);
-    const uint32_t acc = tile & 1;
+    const int first = side * width;
+    int runs = 1;
+    if constexpr (f32) {
+      runs = (steps_of(p, t.split) + kRun<T> - 1) / kRun<T>;
+      if (!drain_runs<T, CG, BN, EPI == kGate>(runs, seq, run, tmem + ((uint32_t)quarter << 21), first, width, acc_full,
+                                               acc_empty, lane)) {
+        *dead = 1;
+        break;
+      }
+    }
+    const uint32_t acc = seq & 1;
     const int row0 = t.m0 + (int)rank * 128 + quarter * 32, row = row0 + lane;
     const bool live = row < p.m;
-    const int first = side * width;
     // What the next columns need from memory is on its way while these are worked on, and the first
     // columns' while the product runs.  kGateBack: the factors (rows are padded to whole sectors of 16
     // columns); kGate: the biases.
@@ -504,7 +566,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
       }
     };
     ask(first);
-    if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
+    if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (seq >> 1) & 1))) {
       *dead = 1;
       break;
     }
@@ -530,6 +592,11 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
           if (c + j + 16 < first + width) ask(c + j + 16);
           sum.wait();
           sum_u.wait();
+          if constexpr (f32)
+            if (runs > 1) {
+              add_run(run, c + j, v);
+              add_run(run, BN / 2 + c + j, u);
+            }
           if (p.bias_vec && count >= 16) {
             float bg[16], bu[16];
             bias_g.values(bg);
@@ -570,6 +637,8 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
           raw_u.values(u);
           if (c + j + 16 < first + width) ask(c + j + 16);
           sum.wait();
+          if constexpr (f32)
+            if (runs > 1) add_run(run, c + j, v);
           gate_gradients(v, g, u);
           if constexpr (f32) {
             put_sheets(sheets, box, lane, g);
@@ -639,15 +708,27 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
   const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
   constexpr int width = kWarpColumns<T, kStore, BN>, N = kTurnColumns<T, BN>, pitch = kRowBytes<T, BN>;
   uint8_t *mine = boxes + (warp - 2) * 32 * pitch;
-  for (int tile = team;; tile += kTeams<T, BN>) {
+  constexpr bool f32 = sizeof(T) == 4;
+  float *run = f32 ? l.runs + ((int64_t)blockIdx.x * 4 + quarter) * 32 * BN + lane * 4 : nullptr;
+  uint32_t seq = team;  // accumulators before this tile's (16-bit data: one a tile)
+  for (int tile = team;; tile += kTeams<T, BN>, seq += kTeams<T, BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
     const ProductArgs &p = l.p[product_of(l, item)];
     const Tile t = tile_of<kStore, CG, BN>(p, item);
-    const uint32_t acc = tile & 1;
+    int runs = 1;
+    if constexpr (f32) {
+      runs = (steps_of(p, t.split) + kRun<T> - 1) / kRun<T>;
+      if (!drain_runs<T, CG, BN, false>(runs, seq, run, tmem + ((uint32_t)quarter << 21), side * width, width, acc_full,
+                                        acc_empty, lane)) {
+        *dead = 1;
+        break;
+      }
+    }
+    const uint32_t acc = seq & 1;
     const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane;
     const bool live = row < p.m;
-    if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (tile >> 1) & 1))) {
+    if (!__all_sync(0xffffffffu, mbar_wait_clocks(acc_full + acc, (seq >> 1) & 1))) {
       *dead = 1;
       break;
     }
@@ -660,6 +741,11 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
       float(&v)[N] = sum.v;
       sum.load(base + c);
       sum.wait();
+      if constexpr (f32)
+        if (runs > 1) {
+#pragma unroll
+          for (int i = 0; i < N; i += 16) add_run(run, c + i, *reinterpret_cast<float(*)[16]>(v + i));
+        }
       if (c + N >= (side + 1) * width) release_accumulator<CG>(acc_empty + acc, lane);
       if (live && count > 0) {
         const int64_t o = t.m_half * p.c_m_half + t.n_half * p.c_n_half + row * p.ldc + col;
@@ -804,8 +890,8 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
       for (uint32_t i = n > S ? n - S : 0; i < n; ++i)
         if (!mbar_wait_clocks(full + i % S, (i / S) & 1)) *dead = 1;
   } else if (warp == 1 && rank == 0) {
-    uint32_t n = 0, tile = 0;
-    for (; !*dead; ++tile) {
+    uint32_t n = 0, seq = 0;  // stages and accumulators so far
+    for (int tile = 0; !*dead; ++tile) {
       int item = item_of(l, worker, workers, tile);
       if (item < 0) break;
       const int which = EPI == kStore ? product_of(l, item) : 0;
@@ -815,43 +901,46 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
       const uint64_t a0 = tc_desc(tiles, p.a_mn, Shape::a_bytes / 2, kDepth<T>);
       const uint64_t b0 = tc_desc(tiles + kParts<T> * Shape::a_bytes, p.b_mn, kDepth<T> * 128, kDepth<T>);
       const Tile t = tile_of<EPI, CG, BN>(p, item);
-      int k0, k1;
-      split_range(p, t.split, k0, k1);
-      const uint32_t acc = tile & 1, use = tile >> 1;
-      if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_clocks(acc_empty + acc, (use - 1) & 1))) {
-        *dead = 1;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d = tmem + acc * kSums<T> * BN;
-      const int steps = p.segments * (k1 - k0);
+      int left = steps_of(p, t.split);
       bool lost = false;
-      for (int i = 0; i < steps; ++i, ++n) {
-        const int s = n % S;
-        if (!__all_sync(0xffffffffu, mbar_wait_clocks(full + s, (n / S) & 1))) {
+      while (left && !lost) {
+        const uint32_t acc = seq & 1, use = seq >> 1;
+        if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_clocks(acc_empty + acc, (use - 1) & 1))) {
           lost = true;
           break;
         }
         tc_fence_after();
-        const uint64_t a = a0 + s * (Shape::stage_bytes >> 4), b = b0 + s * (Shape::stage_bytes >> 4);
-        if (elect_one()) {
-          if constexpr (kParts<T> == 3) {
-            constexpr int pairs[6][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {2, 0}};
+        const uint32_t d = tmem + acc * kSums<T> * BN;
+        const int steps = min(left, kRun<T>);
+        for (int i = 0; i < steps; ++i, ++n) {
+          const int s = n % S;
+          if (!__all_sync(0xffffffffu, mbar_wait_clocks(full + s, (n / S) & 1))) {
+            lost = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a = a0 + s * (Shape::stage_bytes >> 4), b = b0 + s * (Shape::stage_bytes >> 4);
+          if (elect_one()) {
+            if constexpr (kParts<T> == 3) {
+              constexpr int pairs[6][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {2, 0}};
 #pragma unroll
-            for (int q = 0; q < 6; ++q)
+              for (int q = 0; q < 6; ++q)
+#pragma unroll
+                for (int j = 0; j < kDepth<T> / 16; ++j)
+                  tc_mma<CG>(q ? d + BN : d, a + pairs[q][0] * (Shape::a_bytes >> 4) + j * a_step,
+                             b + pairs[q][1] * (Shape::b_bytes >> 4) + j * b_step, idesc, i > 0 || j > 0 || q > 1);
+            } else {
 #pragma unroll
               for (int j = 0; j < kDepth<T> / 16; ++j)
-                tc_mma<CG>(q ? d + BN : d, a + pairs[q][0] * (Shape::a_bytes >> 4) + j * a_step,
-                           b + pairs[q][1] * (Shape::b_bytes >> 4) + j * b_step, idesc, i > 0 || j > 0 || q > 1);
-          } else {
-#pragma unroll
-            for (int j = 0; j < kDepth<T> / 16; ++j)
-              tc_mma<CG>(d, a + j * a_step, b + j * b_step, idesc, i > 0 || j > 0);
+                tc_mma<CG>(d, a + j * a_step, b + j * b_step, idesc, i > 0 || j > 0);
+            }
+            tc_commit<CG>(empty + s);
+            if (i == steps - 1) tc_commit<CG>(acc_full + acc);
           }
-          tc_commit<CG>(empty + s);
-          if (i == steps - 1) tc_commit<CG>(acc_full + acc);
+          __syncwarp();
         }
-        __syncwarp();
+        left -= steps;
+        ++seq;
       }
       if (lost) {
         *dead = 1;
