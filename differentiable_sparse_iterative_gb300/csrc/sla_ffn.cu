@@ -164,17 +164,23 @@ struct Call {
   }
 };
 
-// The matrix as an operand: in place where TMA can read it, else a job to pack it into `to` (or, where an
-// earlier call did that, from there).
+// Where a call finds an operand laid out for TMA.
+enum Copy {
+  kOwn,   // in place where TMA can read it, else packed by and for this call alone
+  kLeft,  // packed whatever its layout: a later call reads the copy
+  kKept,  // an earlier call's copy
+};
+
+// The matrix as an operand: in place, or from `to` with, unless it is there already, a job to pack it.
 template <typename T>
 Operand as_operand(PackJobs &jobs, const T *src, int64_t rows, int64_t cols, int64_t ld, int halves, void *to,
-                   bool packed = false) {
+                   Copy copy = kOwn) {
   const int64_t half = rows * ld;                        // between the halves of src
   if (rows == 1 && halves == 1) ld = round_up(cols, 8);  // a single row has no distance to the next
-  if (!packed && sizeof(T) == 2 && tma_ready(src, ld) && (halves == 1 || half % 8 == 0))
+  if (copy == kOwn && sizeof(T) == 2 && tma_ready(src, ld) && (halves == 1 || half % 8 == 0))
     return {src, cols, rows, halves, ld, rows * ld};
   const int64_t pitch = round_up(cols, 8);
-  if (!packed) {
+  if (copy != kKept) {
     PackJob &j = jobs.job[jobs.count++];
     j.src = src, j.dst = (uint16_t *)to, j.rows = rows, j.cols = cols, j.src_ld = ld, j.src_half = half, j.ld = pitch;
     j.halves = halves, j.vec = aligned(src, 16) && ld * sizeof(T) % 16 == 0;
@@ -585,8 +591,10 @@ struct ColumnSums {
 
 int64_t hidden_pitch(const sla_ffn *f) { return round_up(f->hidden, 16); }
 
-// Whether a forward call leaves its packed copy of a matrix with this many columns to the backward call:
-// where TMA can never read the original.  (One that is only misaligned is packed by each call.)
+// Whether a forward call leaves a packed copy of a matrix with this many columns to the backward call: where
+// TMA cannot read a dense original.  The sizes alone decide, so that both calls and the layout of what is saved
+// agree: a view with wider rows, or a single row, is packed too, though TMA could read it where it is.  (A
+// matrix that is only misaligned is packed by each call.)
 bool keeps_packed(const sla_ffn *f, int64_t cols) {
   return f->tokens > kFewTokens && (f->dtype == SLA_F32 || cols % 8 != 0);
 }
@@ -745,10 +753,11 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
     return finish(c);
   }
   PackJobs packs;
-  const bool keep_x = saved && keeps_packed(f, f->width), keep_o = saved && keeps_packed(f, f->hidden);
-  const Operand ox = as_operand(packs, x, f->tokens, f->width, ldx, 1, keep_x ? saved + L.x : w.x);
-  const Operand oi = as_operand(packs, w_in, f->hidden, f->width, f->width, 2, keep_x ? saved + L.w_in : w.w_in);
-  const Operand oo = as_operand(packs, w_out, f->out, f->hidden, f->hidden, 1, keep_o ? saved + L.w_out : w.w_out);
+  const Copy copy_x = saved && keeps_packed(f, f->width) ? kLeft : kOwn;
+  const Copy copy_o = saved && keeps_packed(f, f->hidden) ? kLeft : kOwn;
+  const Operand ox = as_operand(packs, x, f->tokens, f->width, ldx, 1, copy_x ? saved + L.x : w.x, copy_x);
+  const Operand oi = as_operand(packs, w_in, f->hidden, f->width, f->width, 2, copy_x ? saved + L.w_in : w.w_in, copy_x);
+  const Operand oo = as_operand(packs, w_out, f->out, f->hidden, f->hidden, 1, copy_o ? saved + L.w_out : w.w_out, copy_o);
   run_packs<T>(c, packs);
   if (const int stages = saved ? 0 : narrow_stages(f)) {
     run_narrow<T>(c, f, stages, ox, oi, b_in, oo, b_out, y);
@@ -780,14 +789,14 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
   const SavedLayout L = saved_layout(f);
   const int64_t ldg = hidden_pitch(f), sheet = f->tokens * ldg;
   const bool inner = dx || dw_in || db_in;
-  const bool kept_x = keeps_packed(f, f->width), kept_o = keeps_packed(f, f->hidden);
+  const Copy copy_x = keeps_packed(f, f->width) ? kKept : kOwn, copy_o = keeps_packed(f, f->hidden) ? kKept : kOwn;
   char *sv = const_cast<char *>(saved);
   PackJobs packs;
   Operand ody{}, ox{}, oi{}, oo{};
   if (inner || dw_out) ody = as_operand(packs, dy, f->tokens, f->out, lddy, 1, w.dy);
-  if (dw_in) ox = as_operand(packs, x, f->tokens, f->width, ldx, 1, kept_x ? sv + L.x : w.x, kept_x);
-  if (dx) oi = as_operand(packs, w_in, f->hidden, f->width, f->width, 2, kept_x ? sv + L.w_in : w.w_in, kept_x);
-  if (inner) oo = as_operand(packs, w_out, f->out, f->hidden, f->hidden, 1, kept_o ? sv + L.w_out : w.w_out, kept_o);
+  if (dw_in) ox = as_operand(packs, x, f->tokens, f->width, ldx, 1, copy_x ? sv + L.x : w.x, copy_x);
+  if (dx) oi = as_operand(packs, w_in, f->hidden, f->width, f->width, 2, copy_x ? sv + L.w_in : w.w_in, copy_x);
+  if (inner) oo = as_operand(packs, w_out, f->out, f->hidden, f->hidden, 1, copy_o ? sv + L.w_out : w.w_out, copy_o);
   run_packs<T>(c, packs);
   const Operand odgu{w.dgu, f->hidden, f->tokens, 2 * S, ldg, sheet};
   const Operand oh{saved + L.h, f->hidden, f->tokens, S, ldg, sheet};
