@@ -15,6 +15,7 @@ import functools
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.function import once_differentiable
 
 from . import _abi
@@ -223,7 +224,10 @@ class LayerNorm(torch.autograd.Function):
 
 
 def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    """Whether the call belongs in the autograd graph.  A tensor with a forward-mode tangent takes the node as
+    well, which refuses it (NotImplementedError): past the node the tangent would be lost without a word."""
+    grad = torch.is_grad_enabled()
+    return any(t is not None and ((grad and t.requires_grad) or unpack_dual(t).tangent is not None) for t in tensors)
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,

@@ -1,0 +1,61 @@
+"""The dense operators' Python entries, with the calls behind them replaced (no GPU needed)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import torch.autograd.forward_ad as fwad  # noqa: E402
+
+import differentiable_sparse_iterative_gb300 as sla  # noqa: E402
+from differentiable_sparse_iterative_gb300 import dense  # noqa: E402
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    """The two forward calls as a few torch operations on CPU tensors."""
+    def layernorm(x, weight=None, bias=None, eps=1e-5, y=None, stats=False):
+        y = torch.nn.functional.layer_norm(x, x.shape[-1:], weight, bias, eps)
+        return (y, x[..., 0].clone(), x[..., 0].clone()) if stats else y
+
+    def gated_ffn(x, w_in, w_out, b_in=None, b_out=None, activation="silu", y=None, save=False, workspace=None):
+        g, u = torch.nn.functional.linear(x, w_in, b_in).chunk(2, -1)
+        y = torch.nn.functional.linear(torch.nn.functional.silu(g) * u, w_out, b_out)
+        return (y, torch.zeros(1, dtype=torch.uint8)) if save else y
+
+    monkeypatch.setattr(dense, "sla_layernorm", layernorm)
+    monkeypatch.setattr(dense, "sla_gated_ffn", gated_ffn)
+
+
+def _calls():
+    """(call, its arguments)"""
+    gen = torch.Generator().manual_seed(1)
+    x, w, b = torch.randn(3, 8, generator=gen), torch.randn(8, generator=gen), torch.randn(8, generator=gen)
+    w_in, w_out = torch.randn(12, 8, generator=gen), torch.randn(5, 6, generator=gen)
+    b_in, b_out = torch.randn(12, generator=gen), torch.randn(5, generator=gen)
+    return [(sla.layer_norm, [x, w, b]), (sla.gated_ffn, [x, w_in, w_out, b_in, b_out])]
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_a_forward_mode_tangent_is_refused_not_dropped(plain, grad):
+    for call, args in _calls():
+        call(*args)
+        for i, t in enumerate(args):
+            with fwad.dual_level(), torch.set_grad_enabled(grad):
+                moved = list(args)
+                moved[i] = fwad.make_dual(t, torch.ones_like(t))
+                with pytest.raises(NotImplementedError):
+                    call(*moved)
+            with pytest.raises(RuntimeError):  # as any node without a rule for torch.func
+                torch.func.jvp(lambda v: call(*args[:i], v, *args[i + 1:]), (t,), (torch.ones_like(t),))
+
+
+def test_the_node_is_taken_for_gradients_alone(plain):
+    for call, args in _calls():
+        assert call(*args).grad_fn is None
+        for i, t in enumerate(args):
+            moved = list(args)
+            moved[i] = t.clone().requires_grad_()
+            assert call(*moved).grad_fn is not None
+            with torch.no_grad():
+                assert call(*moved).grad_fn is None
+            with fwad.dual_level():
+                assert call(*args).grad_fn is None
