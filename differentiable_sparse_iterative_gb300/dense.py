@@ -19,6 +19,7 @@ from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.function import once_differentiable
 
 from . import _abi
+from ._buffers import usable
 
 ACTIVATIONS = {"silu": _abi.SLA_ACT_SILU, "gelu": _abi.SLA_ACT_GELU, "gelu_tanh": _abi.SLA_ACT_GELU_TANH,
                "relu": _abi.SLA_ACT_RELU}
@@ -111,10 +112,8 @@ def _type(t: torch.Tensor, name: str) -> int:
 
 def _scratch(need: int, device, ws: Optional[torch.Tensor]) -> Tuple[torch.Tensor, int]:
     """(buffer, bytes): the caller's workspace where it is large enough, else a new one."""
-    if ws is not None:
-        have = ws.numel() * ws.element_size()
-        if have >= need:
-            return ws, have
+    if usable(ws, need, device):
+        return ws, ws.numel() * ws.element_size()
     need = max(need, 256)
     return _empty(need, dtype=torch.uint8, device=device), need
 

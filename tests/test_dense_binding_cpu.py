@@ -59,3 +59,33 @@ def test_the_node_is_taken_for_gradients_alone(plain):
                 assert call(*moved).grad_fn is None
             with fwad.dual_level():
                 assert call(*args).grad_fn is None
+
+
+class _Cuda:
+    """What the check of a workspace looks at, of a CUDA tensor."""
+    is_cuda = True
+
+    def __init__(self, index, numel, contiguous=True):
+        self.index, self.size, self.contiguous, self.device = index, numel, contiguous, torch.device("cuda", index)
+
+    def get_device(self):
+        return self.index
+
+    def numel(self):
+        return self.size
+
+    def element_size(self):
+        return 4
+
+    def is_contiguous(self):
+        return self.contiguous
+
+
+def test_a_workspace_that_is_not_dense_memory_of_the_device_is_refused():
+    dev = torch.device("cuda", 0)
+    for ws, message in ((torch.empty(1 << 12, dtype=torch.uint8), "CUDA tensor"), (torch.empty(8), "CUDA tensor"),
+                        (_Cuda(1, 1 << 12), "on cuda:0"), (_Cuda(0, 1 << 12, contiguous=False), "contiguous")):
+        with pytest.raises(ValueError, match=message):
+            dense._scratch(1024, dev, ws)
+    good = _Cuda(0, 256)
+    assert dense._scratch(1024, dev, good) == (good, 1024)
