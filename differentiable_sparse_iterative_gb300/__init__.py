@@ -30,6 +30,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _abi
+from ._buffers import usable
 from ._abi import (SLA_OK, SLA_NOT_CONVERGED, SLA_BREAKDOWN, SLA_INVALID_ARG, SLA_BAD_CSR, SLA_NONFINITE,
                    SLA_WORKSPACE_TOO_SMALL, SLA_TIMEOUT, SLA_CUDA_ERROR, SLA_PRECOND_NONE, SLA_PRECOND_JACOBI, SLA_LOOP_AUTO,
                    SLA_LOOP_HOST, SLA_LOOP_GRAPH, SLA_LOOP_RESIDENT, SLA_LOOP_CLUSTER)
@@ -213,11 +214,13 @@ def sla_cg_workspace_bytes(n: int, batch: int, dtype: torch.dtype, precond: int)
     return lib().sla_cg_workspace_bytes(int(n), int(batch), _DT[dtype], int(precond))
 
 
+def _scratch(need: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
+    """The caller's workspace where it is large enough, else a new one."""
+    return ws if usable(ws, need, device) else torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+
+
 def _workspace(n, batch, dtype, precond, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
-    need = sla_cg_workspace_bytes(n, batch, dtype, precond)
-    if ws is not None and ws.numel() * ws.element_size() >= need:
-        return ws
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    return _scratch(sla_cg_workspace_bytes(n, batch, dtype, precond), device, ws)
 
 
 def sla_validate_csr(A: CSRMatrix, check_symmetric: bool = False) -> int:
@@ -272,7 +275,7 @@ def sla_cg_solve(A: CSRMatrix, b: torch.Tensor, x0: Optional[torch.Tensor] = Non
     st = lib().sla_cg_solve(ctypes.byref(_csr_struct(A)), _dev_ptr(b, dt, "b"), _dev_ptr(x0, dt, "x0"),
                             ctypes.byref(_opts(rtol, maxit, precond, unroll, loop)), _dev_ptr(x, dt, "x"),
                             ctypes.byref(info) if sync else None, _dev_ptr(hist, torch.float64, "history"),
-                            ws.data_ptr(), ws.numel(), _stream(dev))
+                            ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev))
     _check(st, "sla_cg_solve")
     return x, (_info(info) if sync else None), hist
 
@@ -293,7 +296,7 @@ def sla_cg_adjoint(A: CSRMatrix, x: torch.Tensor, g: torch.Tensor, rtol: float =
     st = lib().sla_cg_adjoint(ctypes.byref(_csr_struct(A)), _dev_ptr(x, dt, "x"), _dev_ptr(g, dt, "g"),
                               ctypes.byref(_opts(rtol, maxit, precond, unroll, loop)), _dev_ptr(grad_b, dt, "grad_b"),
                               _dev_ptr(grad_values, dt, "grad_values"), ctypes.byref(info) if sync else None,
-                              ws.data_ptr(), ws.numel(), _stream(dev))
+                              ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev))
     _check(st, "sla_cg_adjoint")
     return grad_b, grad_values, (_info(info) if sync else None)
 
@@ -315,7 +318,7 @@ def sla_cg_solve_batched(pattern: CSRMatrix, values: torch.Tensor, b: torch.Tens
                                     _dev_ptr(b, dt, "b"), _dev_ptr(x0, dt, "x0"),
                                     ctypes.byref(_opts(rtol, maxit, precond, unroll, loop)), _dev_ptr(x, dt, "x"),
                                     infos if sync else None, _dev_ptr(hist, torch.float64, "history"),
-                                    ws.data_ptr(), ws.numel(), _stream(dev))
+                                    ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev))
     _check(st, "sla_cg_solve_batched")
     return x, ([_info(infos[s]) for s in range(B)] if sync else None), hist
 
@@ -338,7 +341,8 @@ def sla_cg_adjoint_batched(pattern: CSRMatrix, values: torch.Tensor, x: torch.Te
                                       _dev_ptr(x, dt, "x"), _dev_ptr(g, dt, "g"),
                                       ctypes.byref(_opts(rtol, maxit, precond, unroll, loop)),
                                       _dev_ptr(grad_b, dt, "grad_b"), _dev_ptr(grad_values, dt, "grad_values"),
-                                      infos if sync else None, ws.data_ptr(), ws.numel(), _stream(dev))
+                                      infos if sync else None, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                      _stream(dev))
     _check(st, "sla_cg_adjoint_batched")
     return grad_b, grad_values, ([_info(infos[s]) for s in range(B)] if sync else None)
 
@@ -386,10 +390,7 @@ def sla_bicgstab_workspace_bytes(n: int, nnz: int, dtype: torch.dtype) -> int:
 
 
 def _bi_workspace(A: CSRMatrix, ws: Optional[torch.Tensor]) -> torch.Tensor:
-    need = sla_bicgstab_workspace_bytes(A.n, A.nnz, A.values.dtype)
-    if ws is not None and ws.numel() * ws.element_size() >= need:
-        return ws
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=A.values.device)
+    return _scratch(sla_bicgstab_workspace_bytes(A.n, A.nnz, A.values.dtype), A.values.device, ws)
 
 
 def sla_bicgstab_solve(A: CSRMatrix, b: torch.Tensor, x0: Optional[torch.Tensor] = None, rtol: float = 1e-8,
@@ -589,9 +590,7 @@ def sla_eig_smallest(A: CSRMatrix, v0: Optional[torch.Tensor] = None, tol: Optio
     if tol is None:
         tol = 1e-10 if dt == torch.float64 else 1e-5
     v = torch.ones(A.n, dtype=dt, device=dev) if v0 is None else v0.detach().clone()
-    need = sla_eig_workspace_bytes(A.n, dt, precond)
-    ws = workspace if workspace is not None and workspace.numel() * workspace.element_size() >= need else \
-        torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    ws = _scratch(sla_eig_workspace_bytes(A.n, dt, precond), dev, workspace)
     o = _abi.sla_eig_opts()
     o.tol, o.maxit, o.inner_factor, o.inner_maxit = float(tol), int(maxit), float(inner_factor), int(inner_maxit)
     o.precond, o.loop = int(precond), int(loop)
@@ -682,9 +681,7 @@ def sla_eigsh(A: CSRMatrix, k: int, V0: Optional[torch.Tensor] = None, tol: Opti
         V = V0.detach().to(dtype=dt).contiguous().clone()
     if V.dim() != 2 or V.shape[0] != int(k) or V.shape[1] != A.n:
         raise ValueError("V0 must have shape [k, n]")
-    need = sla_eigsh_workspace_bytes(A.n, k, dt, precond)
-    ws = workspace if workspace is not None and workspace.numel() * workspace.element_size() >= need else \
-        torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    ws = _scratch(sla_eigsh_workspace_bytes(A.n, k, dt, precond), dev, workspace)
     o = _abi.sla_eig_opts()
     o.tol, o.maxit, o.inner_factor, o.inner_maxit = float(tol), int(maxit), float(inner_factor), int(inner_maxit)
     o.precond, o.loop = int(precond), int(loop)

@@ -89,3 +89,14 @@ def test_a_workspace_that_is_not_dense_memory_of_the_device_is_refused():
             dense._scratch(1024, dev, ws)
     good = _Cuda(0, 256)
     assert dense._scratch(1024, dev, good) == (good, 1024)
+
+
+def test_a_solver_workspace_that_is_not_dense_memory_of_the_device_is_refused():
+    dev = torch.device("cuda", 0)
+    for ws, message in ((torch.empty(1 << 12, dtype=torch.uint8), "CUDA tensor"), (_Cuda(1, 1 << 12), "on cuda:0"),
+                        (_Cuda(0, 1 << 12, contiguous=False), "contiguous")):
+        with pytest.raises(ValueError, match=message):
+            sla._scratch(1024, dev, ws)
+    good = _Cuda(0, 256)
+    assert sla._scratch(1024, dev, good) is good
+    assert sla._scratch(100, torch.device("cpu"), None).numel() == 256
