@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 from typing import Optional, Tuple
 
 import torch
@@ -45,7 +46,24 @@ def _check(status: int, where: str) -> None:
 
 # a call is a few microseconds of GPU time for one token: the stream's handle without a Stream object
 _stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _empty = torch.empty
+
+
+def _on_device_of_first(call):
+    """call, with the device of its first argument as the current one: libsla launches on the current device and
+    asks it for its size, and the handle of a default stream names no device."""
+    first = next(iter(inspect.signature(call).parameters))
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        t = args[0] if args else kw.get(first)
+        if t is not None and t.is_cuda and t.get_device() != _current_device():
+            with torch.cuda.device(t.get_device()):
+                return call(*args, **kw)
+        return call(*args, **kw)
+
+    return run
 
 
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> Tuple[int, int, int]:
@@ -127,6 +145,7 @@ def _ln_params(x, weight, bias):
     return pt
 
 
+@_on_device_of_first
 def sla_layernorm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                   eps: float = 1e-5, y: Optional[torch.Tensor] = None, stats: bool = False):
     """Layer norm over the last dimension (asynchronous).  weight and bias ([width], of x's type or
@@ -156,6 +175,7 @@ def sla_layernorm_backward_workspace_bytes(rows: int, width: int, dtype: torch.d
     return _lib().sla_layernorm_backward_workspace_bytes(int(rows), int(width), _DT[dtype])
 
 
+@_on_device_of_first
 def sla_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
                            rstd: torch.Tensor, want_grad_x: bool = True, want_grad_weight: bool = True,
                            want_grad_bias: bool = True, param_dtype: Optional[torch.dtype] = None,
@@ -255,6 +275,7 @@ def _ffn(x, w_in, w_out, activation):
             _param(w_out, "w_out", (out, hidden), x.dtype, index))
 
 
+@_on_device_of_first
 def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in: Optional[torch.Tensor] = None,
                   b_out: Optional[torch.Tensor] = None, activation: str = "silu", y: Optional[torch.Tensor] = None,
                   save: bool = False, workspace: Optional[torch.Tensor] = None):
@@ -283,6 +304,7 @@ def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in
     return (y, saved) if save else y
 
 
+@_on_device_of_first
 def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor,
                            saved: torch.Tensor, activation: str = "silu", want_grad_x: bool = True,
                            want_grad_weights: bool = True, want_grad_bias: bool = False,
@@ -312,10 +334,11 @@ def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor
 
 
 def sla_gated_ffn_check(device: Optional[int] = None) -> None:
-    """Synchronises the current stream and raises SlaError(SLA_TIMEOUT) if a bounded wait inside a
-    gated_ffn kernel expired since the last check (never expected)."""
-    _check(_lib().sla_gated_ffn_check(_stream(torch.cuda.current_device() if device is None else device)),
-           "sla_gated_ffn_check")
+    """Synchronises the device's current stream and raises SlaError(SLA_TIMEOUT) if a bounded wait inside a
+    gated_ffn kernel on it expired since the last check (never expected)."""
+    device = torch.cuda.current_device() if device is None else device
+    with torch.cuda.device(device):
+        _check(_lib().sla_gated_ffn_check(_stream(device)), "sla_gated_ffn_check")
 
 
 class GatedFFN(torch.autograd.Function):

@@ -1,4 +1,6 @@
 """The dense operators' Python entries, with the calls behind them replaced (no GPU needed)."""
+import inspect
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -100,3 +102,56 @@ def test_a_solver_workspace_that_is_not_dense_memory_of_the_device_is_refused():
     good = _Cuda(0, 256)
     assert sla._scratch(1024, dev, good) is good
     assert sla._scratch(100, torch.device("cpu"), None).numel() == 256
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """Two devices of which 0 is current; the list gets what is done under which."""
+    state = {"current": 0, "seen": []}
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, state["current"] = state["current"], self.index
+
+        def __exit__(self, *_):
+            state["current"] = self.before
+
+    monkeypatch.setattr(dense, "_current_device", lambda: state["current"])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state["current"])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(dense, "_stream", lambda index: 1000 + index)
+    return state
+
+
+def test_a_call_runs_on_its_tensors_device(two_devices):
+    # each entry's first look at its tensors is recorded in place of the call
+    for call, name in ((sla.sla_layernorm, "x"), (sla.sla_layernorm_backward, "dy"), (sla.sla_gated_ffn, "x"),
+                       (sla.sla_gated_ffn_backward, "dy")):
+        body = call.__wrapped__
+
+        def record(*args, **kw):
+            two_devices["seen"].append(two_devices["current"])
+
+        record.__signature__ = inspect.signature(body)
+        wrapped = dense._on_device_of_first(record)
+        two_devices["seen"].clear()
+        wrapped(_Cuda(0, 1))
+        wrapped(_Cuda(1, 1))
+        wrapped(**{name: _Cuda(1, 1)})
+        wrapped(torch.ones(2))  # refused by the call itself
+        assert two_devices["seen"] == [0, 1, 1, 0] and two_devices["current"] == 0
+
+
+def test_the_check_reads_the_device_that_it_is_asked_about(two_devices, monkeypatch):
+    class Lib:
+        def sla_gated_ffn_check(self, stream):
+            two_devices["seen"].append((two_devices["current"], stream))
+            return 0
+
+    monkeypatch.setattr(dense, "_library", Lib())
+    sla.sla_gated_ffn_check()
+    sla.sla_gated_ffn_check(1)
+    assert two_devices["seen"] == [(0, 1000), (1, 1001)] and two_devices["current"] == 0
