@@ -264,6 +264,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_kernel(const __grid_
         if (q == 1) release_accumulator<1>(s_empty + b, lane);
         gate<Act, kCoarse<T>, false, 16>(g, u, h);
         pack16<T>(h, ph[q]);
+        // Units past the last: their products are zero only where x is finite, so h is set to it.
+        const int units = p.hidden - c * kNarrowChunk - side * 32 - q * 16;
+        if (units < 16) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ph[q][i] &= 2 * i + 1 < units ? 0xFFFFFFFFu : 2 * i < units ? 0xFFFFu : 0u;
+        }
       }
       if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_empty + team, h_phase))) {
         lost = true;
