@@ -378,10 +378,12 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       rs[r] = rr[r];
-      const float2 scale = f2(rs[r], rs[r]);
       float2 a1 = f2(0.f, 0.f), a2 = a1;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
+        // Outside of the row dy is 0 and so has to be xh: (0 - mean) rstd may pass the largest float32.
+        const float inside = s.first + i * apart < s.end ? rs[r] : 0.f;
+        const float2 scale = f2(inside, inside);
         float2 wv[H];
         if constexpr (keep) {
 #pragma unroll
@@ -394,7 +396,6 @@ __global__ void __launch_bounds__(NI == 1 ? kLnBlock : kMaxThreads, NI == 1 ? 3 
         rg[r][i].values(g[r][i]);
 #pragma unroll
         for (int k = 0; k < H; ++k) {
-          // dy is 0 outside of the row: what xh is there does not count
           xh[r][i][k] = mul2(add2(xh[r][i][k], f2(-rm[r], -rm[r])), scale);
           aw[i][k] = fma2(g[r][i][k], xh[r][i][k], aw[i][k]);
           ab[i][k] = add2(ab[i][k], g[r][i][k]);
