@@ -46,7 +46,9 @@ inline int64_t narrow_bytes(int64_t k_blocks, int64_t chunks, int64_t out_pad, i
 template <typename T>
 cudaError_t launch_narrow(const NarrowArgs &p, int blocks, bool early, cudaStream_t st);
 
-template <typename T, int Act>
+// Ragged: the last chunk has hidden units past the last one.  Their products are zero only where x is finite, so h is
+// set to it.  (A kernel of its own: a branch on it costs the others 2 to 7 us of 160 to 212 at a million tokens.)
+template <typename T, int Act, bool Ragged>
 __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_kernel(const __grid_constant__ NarrowArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t *w_in = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -264,18 +266,22 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_kernel(const __grid_
         if (q == 1) release_accumulator<1>(s_empty + b, lane);
         gate<Act, kCoarse<T>, false, 16>(g, u, h);
         pack16<T>(h, ph[q]);
-        // Units past the last: their products are zero only where x is finite, so h is set to it.
-        const int units = p.hidden - c * kNarrowChunk - side * 32 - q * 16;
-        if (units < 16) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ph[q][i] &= 2 * i + 1 < units ? 0xFFFFFFFFu : 2 * i < units ? 0xFFFFu : 0u;
-        }
       }
       if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_empty + team, h_phase))) {
         lost = true;
         break;
       }
       h_phase ^= 1;
+      if constexpr (Ragged)
+        if (c == p.chunks - 1) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int unit = c * kNarrowChunk + side * 32 + q * 16 + 2 * i;
+              ph[q][i] &= unit + 1 < p.hidden ? 0xFFFFFFFFu : unit < p.hidden ? 0xFFFFu : 0u;
+            }
+        }
       const StoreBox<128> box{hs + team * kNarrowTile + quarter * 4096, lane};
 #pragma unroll
       for (int q = 0; q < 2; ++q) box.put(2 * side + q, ph[q]);
@@ -305,10 +311,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_kernel(const __grid_
   if (threadIdx.x == 0 && *dead) atomicAdd(p.timeouts, 1u);
 }
 
-template <typename T, int Act>
+template <typename T, int Act, bool Ragged>
 cudaError_t launch_narrow_act(const NarrowArgs &p, int blocks, bool early, cudaStream_t st) {
   const int smem = (int)narrow_bytes(p.k_blocks, p.chunks, p.out_pad, p.stages);
-  auto kernel = narrow_kernel<T, Act>;
+  auto kernel = narrow_kernel<T, Act, Ragged>;
   static std::atomic<uint64_t> allowed{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -321,14 +327,20 @@ cudaError_t launch_narrow_act(const NarrowArgs &p, int blocks, bool early, cudaS
   return cudaLaunchKernelEx(&cfg.c, kernel, p);
 }
 
+template <typename T, bool Ragged>
+cudaError_t launch_narrow_ragged(const NarrowArgs &p, int blocks, bool early, cudaStream_t st) {
+  switch (p.act) {
+    case SLA_ACT_SILU: return launch_narrow_act<T, SLA_ACT_SILU, Ragged>(p, blocks, early, st);
+    case SLA_ACT_GELU: return launch_narrow_act<T, SLA_ACT_GELU, Ragged>(p, blocks, early, st);
+    case SLA_ACT_GELU_TANH: return launch_narrow_act<T, SLA_ACT_GELU_TANH, Ragged>(p, blocks, early, st);
+    default: return launch_narrow_act<T, SLA_ACT_RELU, Ragged>(p, blocks, early, st);
+  }
+}
+
 template <typename T>
 cudaError_t launch_narrow_as(const NarrowArgs &p, int blocks, bool early, cudaStream_t st) {
-  switch (p.act) {
-    case SLA_ACT_SILU: return launch_narrow_act<T, SLA_ACT_SILU>(p, blocks, early, st);
-    case SLA_ACT_GELU: return launch_narrow_act<T, SLA_ACT_GELU>(p, blocks, early, st);
-    case SLA_ACT_GELU_TANH: return launch_narrow_act<T, SLA_ACT_GELU_TANH>(p, blocks, early, st);
-    default: return launch_narrow_act<T, SLA_ACT_RELU>(p, blocks, early, st);
-  }
+  return p.hidden % kNarrowChunk ? launch_narrow_ragged<T, true>(p, blocks, early, st)
+                                 : launch_narrow_ragged<T, false>(p, blocks, early, st);
 }
 
 }  // namespace sla
