@@ -10,6 +10,10 @@
 // exponential is the density's too.  Errors are a few 2^-22, for float32 data below what its sums
 // lose, for float16 far below its rounding to 2^-12.  (expf, erff and division cost the float32
 // epilogue three times the instructions.)
+//
+// The sigmoid is taken as 1 / (1 + e^-x) for every type, so that its error is relative to its own value.  As
+// 1/2 + tanh(x/2) / 2 with the approximate tanh it would cost one special function in place of two, but is off by
+// 2^-12 of one: a tenth of the value at x = -6.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -19,12 +23,6 @@
 #include "sla_net.cuh"
 
 namespace sla {
-
-// bfloat16 data, rounded to 2^-9, takes the coarse sigmoid, whose error is an eighth of that.
-template <typename T>
-inline constexpr bool kCoarse = false;
-template <>
-inline constexpr bool kCoarse<bf16> = true;
 
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -37,32 +35,19 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-__device__ __forceinline__ float tanh_approx(float x) {
-  float y;
-  asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 1 / (1 + e^-x) of both.  Coarse: by the approximate tanh, one special function in place of two, with an error
-// of 2^-12.
-template <bool Coarse>
+// 1 / (1 + e^-x) of both.
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
-  if constexpr (Coarse) {
-    const float2 t = mul2(x, f2(0.5f, 0.5f));
-    return fma2(f2(tanh_approx(t.x), tanh_approx(t.y)), f2(0.5f, 0.5f), f2(0.5f, 0.5f));
-  } else {
-    const float2 m = mul2(x, f2(-1.4426950408889634f, -1.4426950408889634f));
-    const float2 d = add2(f2(ex2_approx(m.x), ex2_approx(m.y)), f2(1.f, 1.f));
-    return f2(rcp_approx(d.x), rcp_approx(d.y));
-  }
+  const float2 m = mul2(x, f2(-1.4426950408889634f, -1.4426950408889634f));
+  const float2 d = add2(f2(ex2_approx(m.x), ex2_approx(m.y)), f2(1.f, 1.f));
+  return f2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
 // The activation of a pair; da: also its derivative.
-template <int Act, bool Coarse, bool Derivative>
+template <int Act, bool Derivative>
 __device__ __forceinline__ void activate2(float2 g, float2 &a, float2 &da) {
   const float2 one = f2(1.f, 1.f);
   if constexpr (Act == SLA_ACT_SILU) {
-    const float2 s = sigmoid2<Coarse>(g);
+    const float2 s = sigmoid2(g);
     a = mul2(g, s);
     if (Derivative) da = fma2(a, fma2(s, f2(-1.f, -1.f), one), s);  // s + a (1 - s)
   } else if constexpr (Act == SLA_ACT_GELU) {
@@ -83,7 +68,7 @@ __device__ __forceinline__ void activate2(float2 g, float2 &a, float2 &da) {
     // (1 + tanh z) / 2 = 1 / (1 + e^-2z);  with s that: 1 - t^2 = 4 s (1 - s)
     constexpr float c = 0.7978845608028654f, k = 2.f * c;
     const float2 gg = mul2(g, g);
-    const float2 s = sigmoid2<Coarse>(mul2(g, fma2(gg, f2(k * 0.044715f, k * 0.044715f), f2(k, k))));
+    const float2 s = sigmoid2(mul2(g, fma2(gg, f2(k * 0.044715f, k * 0.044715f), f2(k, k))));
     a = mul2(g, s);
     if (Derivative) {
       const float2 dz = fma2(gg, f2(2.f * c * 3.f * 0.044715f, 2.f * c * 3.f * 0.044715f), f2(2.f * c, 2.f * c));
@@ -98,14 +83,14 @@ __device__ __forceinline__ void activate2(float2 g, float2 &a, float2 &da) {
 // h = act(g) u from g and u.  Keep: g and u become the factors of the backward pass, dg = dh (u act'(g)) and
 // du = dh act(g).  They are what a forward call leaves behind, in the place of g and u: as many bytes, one
 // rounding each, and the backward epilogue is two products.
-template <int Act, bool Coarse, bool Keep, int N>
+template <int Act, bool Keep, int N>
 __device__ __forceinline__ void gate(float (&g)[N], float (&u)[N], float (&h)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     constexpr int next = N > 1;
     float2 a, da;
     const float2 up = f2(u[i], u[i + next]);
-    activate2<Act, Coarse, Keep>(f2(g[i], g[i + next]), a, da);
+    activate2<Act, Keep>(f2(g[i], g[i + next]), a, da);
     const float2 v = mul2(a, up);
     h[i + next] = v.y, h[i] = v.x;
     if (Keep) {

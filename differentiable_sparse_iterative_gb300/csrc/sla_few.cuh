@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
     if (Gate) {
       const int64_t o = token * p.ldg + r;
       float a[1] = {v}, b[1] = {u}, h[1];
-      with_activation(p.act, [&](auto act) { gate<act.value, kCoarse<T>, true, 1>(a, b, h); });
+      with_activation(p.act, [&](auto act) { gate<act.value, true, 1>(a, b, h); });
       if (p.g) {
         ((T *)p.g)[o] = from_f32<T>(a[0]);
         ((T *)p.u)[o] = from_f32<T>(b[0]);

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
         }
       }
       float h[4];
-      with_activation(p.act, [&](auto act) { gate<act.value, kCoarse<T>, true, 4>(v, u, h); });
+      with_activation(p.act, [&](auto act) { gate<act.value, true, 4>(v, u, h); });
       if (p.g)
 #pragma unroll
         for (int k = 0; k < 4; ++k)

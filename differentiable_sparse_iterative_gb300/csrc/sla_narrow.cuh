@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_kernel(const __grid_
           }
         }
         if (q == 1) release_accumulator<1>(s_empty + b, lane);
-        gate<Act, kCoarse<T>, false, 16>(g, u, h);
+        gate<Act, false, 16>(g, u, h);
         pack16<T>(h, ph[q]);
       }
       if (!__all_sync(0xffffffffu, mbar_wait_clocks(h_empty + team, h_phase))) {

@@ -613,7 +613,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
           }
           float h[16];
           if (p.g) {
-            with_activation(p.act, [&](auto act) { gate<act.value, kCoarse<T>, true, 16>(v, u, h); });
+            with_activation(p.act, [&](auto act) { gate<act.value, true, 16>(v, u, h); });
             if constexpr (f32) {
               box0.put(v);
               box1.put(u);
@@ -625,7 +625,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
               box1.put(j / 16, w);
             }
           } else {
-            with_activation(p.act, [&](auto act) { gate<act.value, kCoarse<T>, false, 16>(v, u, h); });
+            with_activation(p.act, [&](auto act) { gate<act.value, false, 16>(v, u, h); });
           }
           if constexpr (f32)
             put_sheets(sheets, box, lane, h);
