@@ -6,14 +6,15 @@
 //   relu       a = max(g, 0),      a' = [g > 0]
 //
 // They are taken for pairs of values: packed float32 arithmetic, the approximate exponential and
-// reciprocal, and for gelu the normal distribution by Abramowitz and Stegun 7.1.26 (1.5e-7), whose
-// exponential is the density's too.  Errors are a few 2^-22, for float32 data below what its sums
-// lose, for float16 far below its rounding to 2^-12.  (expf, erff and division cost the float32
-// epilogue three times the instructions.)
-//
-// The sigmoid is taken as 1 / (1 + e^-x) for every type, so that its error is relative to its own value.  As
-// 1/2 + tanh(x/2) / 2 with the approximate tanh it would cost one special function in place of two, but is off by
-// 2^-12 of one: a tenth of the value at x = -6.
+// reciprocal.  (expf, erff and division cost the float32 epilogue three times the instructions.)  Every activation is
+// right relative to its own value, at negative gates too, where it is small: to 2^-19, and 2^-22 of the exponential's
+// argument, whose rounding the exponential multiplies; below the rounding of 16-bit data, and for float32 data below
+// what its sums lose.
+//   sigmoid: 1 / (1 + e^-x).  As 1/2 + tanh(x/2) / 2 with the approximate tanh it would cost one special function in
+//     place of two (narrow blocks: 158 us in place of 168), but be off by 2^-12 of one: a tenth of the value at x = -6.
+//   gelu: 1 - Phi(x) = e^(-x^2/2) t P(t), t = 1 / (1 + 0.3 x), for x >= 0.  P is the polynomial of degree 7 with the
+//     least relative error on 0 <= x <= 13.5 (found by linear programming; 9.3e-8, 4.4e-7 evaluated in float32); beyond, the
+//     exponential is zero.  It is the density's exponential too.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -52,15 +53,18 @@ __device__ __forceinline__ void activate2(float2 g, float2 &a, float2 &da) {
     if (Derivative) da = fma2(a, fma2(s, f2(-1.f, -1.f), one), s);  // s + a (1 - s)
   } else if constexpr (Act == SLA_ACT_GELU) {
     const float2 x = f2(fabsf(g.x), fabsf(g.y));
-    const float2 den = fma2(x, f2(0.3275911f * 0.7071067811865476f, 0.3275911f * 0.7071067811865476f), one);
+    const float2 den = fma2(x, f2(0.3f, 0.3f), one);
     const float2 t = f2(rcp_approx(den.x), rcp_approx(den.y));
-    float2 q = fma2(t, f2(1.061405429f, 1.061405429f), f2(-1.453152027f, -1.453152027f));
-    q = fma2(q, t, f2(1.421413741f, 1.421413741f));
-    q = fma2(q, t, f2(-0.284496736f, -0.284496736f));
-    q = fma2(q, t, f2(0.254829592f, 0.254829592f));
+    float2 q = fma2(t, f2(0.03592418f, 0.03592418f), f2(-0.15823323f, -0.15823323f));
+    q = fma2(q, t, f2(0.20810671f, 0.20810671f));
+    q = fma2(q, t, f2(-0.055270962f, -0.055270962f));
+    q = fma2(q, t, f2(0.12938385f, 0.12938385f));
+    q = fma2(q, t, f2(0.09967073f, 0.09967073f));
+    q = fma2(q, t, f2(0.12079171f, 0.12079171f));
+    q = fma2(q, t, f2(0.11962691f, 0.11962691f));
     const float2 m = mul2(mul2(g, g), f2(-0.7213475204444817f, -0.7213475204444817f));
     const float2 e = f2(ex2_approx(m.x), ex2_approx(m.y));
-    q = mul2(mul2(q, t), mul2(e, f2(0.5f, 0.5f)));  // 1 - Phi(|g|)
+    q = mul2(mul2(q, t), e);  // 1 - Phi(|g|)
     const float2 phi = f2(g.x < 0.f ? q.x : 1.f - q.x, g.y < 0.f ? q.y : 1.f - q.y);
     a = mul2(g, phi);
     if (Derivative) da = fma2(mul2(g, e), f2(0.3989422804014327f, 0.3989422804014327f), phi);

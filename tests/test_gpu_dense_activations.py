@@ -12,7 +12,7 @@ import math
 import pytest
 
 from gpu_helpers import sla, torch, DEV
-from test_gpu_dense import TYPES, U
+from test_gpu_dense import ACTS, TYPES, U
 
 pytestmark = pytest.mark.gpu
 
@@ -41,7 +41,7 @@ def within(got, ref, size, e, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("tokens", [16, 20001])  # few tokens; many: the narrow kernel (16 bits), tiles
 def test_activation_and_derivative_of_every_gate(act, tokens, dtype):
     g = torch.linspace(-9.0, 9.0, tokens, device=DEV).to(dtype)
