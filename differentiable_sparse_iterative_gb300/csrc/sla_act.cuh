@@ -76,7 +76,8 @@ __device__ __forceinline__ void activate2(float2 g, float2 &a, float2 &da) {
     a = mul2(g, s);
     if (Derivative) {
       const float2 dz = fma2(gg, f2(2.f * c * 3.f * 0.044715f, 2.f * c * 3.f * 0.044715f), f2(2.f * c, 2.f * c));
-      da = fma2(mul2(a, dz), fma2(s, f2(-1.f, -1.f), one), s);
+      // a (1 - s) first: far from zero one of the two is zero, while a z' may pass the largest float32
+      da = fma2(mul2(a, fma2(s, f2(-1.f, -1.f), one)), dz, s);
     }
   } else {
     a = f2(g.x < 0.f ? 0.f : g.x, g.y < 0.f ? 0.f : g.y);

@@ -60,3 +60,17 @@ def test_activation_and_derivative_of_every_gate(act, tokens, dtype):
                               ("du", dx[:, 1], a, a.abs()), ("dg", dx[:, 0], da, size)):
         bad = ~within(got, ref, s, e, dtype)
         assert not bad.any(), (name, int(bad.sum()), g[bad][:4].tolist(), got[bad][:4].tolist(), ref[bad][:4].tolist())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_gates_far_from_zero(act, tokens, dtype):
+    # act(g) is g or 0, act'(g) 1 or 0, as long as g^2 is finite
+    g = torch.tensor([1e14, -1e14], device=DEV).to(dtype).repeat(tokens // 2)
+    x = torch.stack((g, torch.ones_like(g)), 1)
+    w_in, w_out = torch.eye(2, dtype=dtype, device=DEV), torch.ones(1, 1, dtype=dtype, device=DEV)
+    y, saved = sla.sla_gated_ffn(x, w_in, w_out, activation=act, save=True)
+    assert torch.equal(y[:, 0], g.clamp(min=0)) and torch.equal(sla.sla_gated_ffn(x, w_in, w_out, activation=act), y)
+    dx = sla.sla_gated_ffn_backward(torch.ones_like(y), x, w_in, w_out, saved, activation=act)[0]
+    assert torch.equal(dx[:, 0], (g > 0).to(dtype)) and torch.equal(dx[:, 1], g.clamp(min=0))
