@@ -27,7 +27,7 @@ EXPORTS = [
     "sla_bicgstab_solve", "sla_bicgstab_adjoint", "sla_layernorm", "sla_layernorm_backward_workspace_bytes",
     "sla_layernorm_backward", "sla_gated_ffn_saved_bytes", "sla_gated_ffn_workspace_bytes",
     "sla_gated_ffn_backward_workspace_bytes", "sla_gated_ffn", "sla_gated_ffn_backward",
-    "sla_gated_ffn_check",
+    "sla_gated_ffn_check", "sla_test_expire_wait",
 ]
 SLA_SPMV_PLAIN, SLA_SPMV_TMA = 0, 1
 
@@ -117,6 +117,7 @@ def bind(lib):
         getattr(lib, name).restype = sz
     lib.sla_layernorm_backward_workspace_bytes.restype = sz
     lib.sla_gated_ffn_check.argtypes = [P]
+    lib.sla_test_expire_wait.argtypes = [P]
     lib.sla_gated_ffn.argtypes = [F, P, i64, P, P, P, P, P, P, sz, P, sz, P]
     lib.sla_gated_ffn_backward.argtypes = [F, P, i64, P, i64, P, P, P, sz, P, P, P, P, P, P, sz, P]
     lib.sla_set_spmv_variant.argtypes = [i32]
@@ -128,7 +129,7 @@ def bind(lib):
                  "sla_cg_solve_batched", "sla_cg_adjoint_batched", "sla_cg_solve_static", "sla_eig_smallest",
                  "sla_eig_grad_values", "sla_eigsh", "sla_bicgstab_solve", "sla_bicgstab_adjoint",
                  "sla_layernorm", "sla_layernorm_backward", "sla_gated_ffn", "sla_gated_ffn_backward",
-                 "sla_gated_ffn_check"]:
+                 "sla_gated_ffn_check", "sla_test_expire_wait"]:
         getattr(lib, name).restype = i32
     return lib
 

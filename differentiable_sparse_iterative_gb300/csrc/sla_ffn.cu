@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "sla_common.cuh"
 #include "sla_few.cuh"
@@ -21,20 +23,67 @@
 namespace sla {
 namespace {
 
-__device__ uint32_t d_timeouts;  // blocks of products that gave up a wait, since the last sla_gated_ffn_check
+// ------------------------------------------------------------------ expired waits
 
-uint32_t *timeouts_address() {
-  static thread_local int cached_dev = -1;
-  static thread_local uint32_t *cached = nullptr;
+constexpr int kDevices = 64;
+
+// A device's count of blocks of products that gave up a wait, since the process started.  It lies in host memory that the
+// kernels add to, so that a call sees without waiting for the GPU whether an earlier one was cut short.  It only
+// grows: what a thread has been told of is its own number, so that no thread takes another's report.
+struct Expired {
+  uint32_t *count = nullptr;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-  if (dev != cached_dev) {
-    void *p = nullptr;
-    if (cudaGetSymbolAddress(&p, d_timeouts) != cudaSuccess) return nullptr;
-    cached = (uint32_t *)p;
-    cached_dev = dev;
+  cudaError_t err = cudaSuccess;
+};
+
+std::mutex expired_mutex;
+std::atomic<uint32_t *> expired_count[kDevices];
+thread_local bool expired_met[kDevices];  // this thread has been here
+thread_local uint32_t expired_told[kDevices];
+
+uint32_t read_count(const Expired &x) { return *(const volatile uint32_t *)x.count; }
+
+// The current device's.  A thread is told of what expires after its first time here.
+Expired expired() {
+  Expired x;
+  x.err = cudaGetDevice(&x.dev);
+  if (x.err == cudaSuccess && x.dev >= kDevices) x.err = cudaErrorInvalidDevice;
+  if (x.err != cudaSuccess) return x;
+  x.count = expired_count[x.dev].load();
+  if (!x.count) {
+    std::lock_guard<std::mutex> lock(expired_mutex);
+    x.count = expired_count[x.dev].load();
+    if (!x.count) {
+      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // another thread's capture has nothing to do with this
+      cudaThreadExchangeStreamCaptureMode(&mode);
+      x.err = cudaHostAlloc((void **)&x.count, sizeof(uint32_t), cudaHostAllocPortable | cudaHostAllocMapped);
+      cudaThreadExchangeStreamCaptureMode(&mode);
+      if (x.err != cudaSuccess) return x;
+      *x.count = 0;
+      expired_count[x.dev].store(x.count);
+    }
   }
-  return cached;
+  if (!expired_met[x.dev]) {
+    expired_met[x.dev] = true;
+    expired_told[x.dev] = read_count(x);
+  }
+  return x;
+}
+
+// SLA_TIMEOUT if waits have expired that this thread has not been told of.
+sla_status report_expired(const Expired &x) {
+  const uint32_t n = read_count(x);
+  if (n == expired_told[x.dev]) return SLA_OK;
+  expired_told[x.dev] = n;
+  return SLA_TIMEOUT;
+}
+
+// A wait that nothing ends, of a quarter of a millisecond, counted as the products' kernels count theirs.
+__global__ void __launch_bounds__(32) expire_wait(uint32_t *timeouts) {
+  __shared__ uint64_t bar;
+  if (threadIdx.x == 0) mbar_init(&bar, 1);
+  __syncwarp();
+  if (!mbar_wait_clocks(&bar, 0, 500000) && threadIdx.x == 0) atomicAdd_system(timeouts, 1u);
 }
 
 // ------------------------------------------------------------------ operands
@@ -733,8 +782,10 @@ template <typename T>
 sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, const T *b_in, const T *w_out,
                    const T *b_out, T *y, char *saved, const ForwardScratch &w, cudaStream_t st) {
   Call c{st};
-  c.timeouts = timeouts_address();
-  if (!c.timeouts) return fail(cudaGetLastError());
+  const Expired earlier = expired();
+  if (earlier.err != cudaSuccess) return fail(earlier.err);
+  SLA_CHECK(report_expired(earlier));
+  c.timeouts = earlier.count;
   const SavedLayout L = saved_layout(f);
   const int64_t ldg = hidden_pitch(f);
   void *h = saved ? saved + L.h : w.h;
@@ -784,8 +835,10 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
   using E = typename std::conditional<sizeof(T) == 4, bf16, T>::type;  // type of the operand sheets
   constexpr int S = sheets_of<T>();
   Call c{st};
-  c.timeouts = timeouts_address();
-  if (!c.timeouts) return fail(cudaGetLastError());
+  const Expired earlier = expired();
+  if (earlier.err != cudaSuccess) return fail(earlier.err);
+  SLA_CHECK(report_expired(earlier));
+  c.timeouts = earlier.count;
   const SavedLayout L = saved_layout(f);
   const int64_t ldg = hidden_pitch(f), sheet = f->tokens * ldg;
   const bool inner = dx || dw_in || db_in;
@@ -930,14 +983,20 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
 }
 
 SLA_API sla_status sla_gated_ffn_check(void *stream) {
-  uint32_t *p = timeouts_address();
-  if (!p) return fail(cudaGetLastError());
-  uint32_t n = 0;
-  cudaError_t e = cudaMemcpyAsync(&n, p, sizeof(n), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
-  if (e == cudaSuccess && n) e = cudaMemsetAsync(p, 0, sizeof(n), (cudaStream_t)stream);
+  const Expired x = expired();
+  if (x.err != cudaSuccess) return fail(x.err);
+  const cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+  return e == cudaSuccess ? report_expired(x) : fail(e);
+}
+
+SLA_API sla_status sla_test_expire_wait(void *stream) {
+  const Expired x = expired();
+  if (x.err != cudaSuccess) return fail(x.err);
+  expire_wait<<<1, 32, 0, (cudaStream_t)stream>>>(x.count);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(e);
-  return n ? SLA_TIMEOUT : SLA_OK;
+  count_launches(1);
+  return SLA_OK;
 }
 
 }  // extern "C"

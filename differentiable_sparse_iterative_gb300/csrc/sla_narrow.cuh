@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) narrow_kernel(const __grid_
   __syncwarp();
   tc_fence_after();
   if (warp == 1) tmem_free<1>(tmem, 512);
-  if (threadIdx.x == 0 && *dead) atomicAdd(p.timeouts, 1u);
+  if (threadIdx.x == 0 && *dead) atomicAdd_system(p.timeouts, 1u);
 }
 
 template <typename T, int Act, bool Ragged>

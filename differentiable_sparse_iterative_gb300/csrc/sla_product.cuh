@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_free<CG>(tmem, Shape::columns);
-  if (threadIdx.x == 0 && *dead) atomicAdd(l.timeouts, 1u);
+  if (threadIdx.x == 0 && *dead) atomicAdd_system(l.timeouts, 1u);
 }
 
 // Tile shapes by index, widest first.  float32's two accumulators, twice, leave no room for the widest.

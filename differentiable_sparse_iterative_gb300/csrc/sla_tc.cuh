@@ -27,11 +27,11 @@ __device__ __forceinline__ bool mbar_try_wait_long(uint64_t *bar, uint32_t parit
   return ok != 0;
 }
 
-__device__ __forceinline__ bool mbar_wait_clocks(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_clocks(uint64_t *bar, uint32_t parity, long long limit = kWaitClocks) {
   if (mbar_try_wait_long(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait_long(bar, parity))
-    if (clock64() - t0 > kWaitClocks) return false;
+    if (clock64() - t0 > limit) return false;
   return true;
 }
 

@@ -335,10 +335,16 @@ def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor
 
 def sla_gated_ffn_check(device: Optional[int] = None) -> None:
     """Synchronises the device's current stream and raises SlaError(SLA_TIMEOUT) if a bounded wait inside a
-    gated_ffn kernel on it expired since the last check (never expected)."""
+    gated_ffn kernel on it has expired (never expected) that this thread has not been told of.  The other calls
+    raise it as well, for an earlier call's wait, without synchronising."""
     device = torch.cuda.current_device() if device is None else device
     with torch.cuda.device(device):
         _check(_lib().sla_gated_ffn_check(_stream(device)), "sla_gated_ffn_check")
+
+
+def sla_test_expire_wait() -> None:
+    """Test hook: a bounded wait on the current stream that expires (see sla.h)."""
+    _check(_lib().sla_test_expire_wait(_stream(torch.cuda.current_device())), "sla_test_expire_wait")
 
 
 class GatedFFN(torch.autograd.Function):

@@ -591,8 +591,11 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
 
 /*
  * Every wait inside the products' kernels is bounded (about two seconds); one that expires, which no
- * input can cause, leaves its tile unwritten.  Synchronises the stream and returns SLA_TIMEOUT if
- * that happened on this device since the last check, else SLA_OK.
+ * input can cause, leaves its tile unwritten and is counted.  Each host thread is told once of what has
+ * expired on a device since its own first call there: sla_gated_ffn and sla_gated_ffn_backward return
+ * SLA_TIMEOUT, and do nothing else, when they find that a wait of an earlier call has expired (its results
+ * are not valid); this call synchronises the stream first, so that the calls before it count, and
+ * returns SLA_TIMEOUT or SLA_OK.
  */
 SLA_API sla_status sla_gated_ffn_check(void *stream);
 
@@ -633,6 +636,13 @@ SLA_API sla_status sla_graph_cache_stats(int64_t *entries, int64_t *builds, int6
  * sla_test_set_barrier_wait(0, 0) restores normal operation.  SLA_INVALID_ARG otherwise.
  */
 SLA_API sla_status sla_test_set_barrier_wait(uint32_t extra, int64_t spin_limit);
+
+/*
+ * Test hook for failure detection (not an operation of the method): launches a kernel whose bounded wait
+ * (a quarter of a millisecond) nothing ends, and which counts its expiry as the kernels of sla_gated_ffn do.
+ * The CUDA context stays intact.
+ */
+SLA_API sla_status sla_test_expire_wait(void *stream);
 
 #ifdef __cplusplus
 }
