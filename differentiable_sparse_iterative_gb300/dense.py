@@ -96,6 +96,7 @@ class _FFNSizes:
         self.descriptor = _abi.sla_ffn(tokens, width, hidden, out, dt, act)
         self.ref = ctypes.byref(self.descriptor)
         self.tokens, self.hidden, self.out = tokens, hidden, out
+        self.key = (tokens, width, hidden, out, dt, act)
         lib = _lib()
         self.saved = lib.sla_gated_ffn_saved_bytes(self.ref)
         self.forward = lib.sla_gated_ffn_workspace_bytes(self.ref)
@@ -297,6 +298,7 @@ def sla_gated_ffn(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, b_in
     saved, sp, sn = None, None, 0
     if save:
         saved, sn = _scratch(f.saved, dev, None)
+        saved.made_for = f.key
         sp = saved.data_ptr()
     ws, nbytes = _scratch(f.forward, dev, workspace)
     _check(lib.sla_gated_ffn(f.ref, ptr, ldx, wip, bip, wop, bop, yp, sp, sn, ws.data_ptr(), nbytes, _stream(index)),
@@ -317,6 +319,9 @@ def sla_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_in: torch.Tensor
         raise ValueError(f"dy must have shape {tuple(x.shape[:-1]) + (f.out,)}, got {tuple(dy.shape)}")
     if saved.dtype != torch.uint8 or saved.get_device() != x.get_device() or not saved.is_contiguous():
         raise ValueError("saved must be the buffer that sla_gated_ffn(..., save=True) returned")
+    # a copy of the buffer has lost the note of what it was made for, but not its size
+    if getattr(saved, "made_for", f.key) != f.key or saved.numel() > max(f.saved, 256):
+        raise ValueError("saved is from a forward call of other sizes, another type or another activation")
     lib, dt, dev = _lib(), x.dtype, x.device
     dx = dw_in = dw_out = db_in = db_out = None
     if want_grad_x:

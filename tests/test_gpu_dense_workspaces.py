@@ -33,3 +33,21 @@ def test_workspaces_of_the_dense_operators():
         assert torch.equal(call(torch.empty(256, dtype=torch.uint8, device=DEV)), call(None))  # too small: not used
     assert torch.equal(want, calls[0](None))
     assert dense._scratch(100, torch.device(DEV), None)[1] == 256
+
+
+def test_saved_of_another_call_is_refused():
+    args = ffn_inputs(40, 96, 64, 32, torch.bfloat16, False, seed=245)
+    dy = randn(40, 32, dtype=torch.bfloat16, seed=246)
+    _, saved = sla.sla_gated_ffn(*args, save=True)
+    want = sla.sla_gated_ffn_backward(dy, *args[:3], saved)
+    other = ffn_inputs(40, 64, 64, 32, torch.bfloat16, False, seed=247)
+    _, theirs = sla.sla_gated_ffn(*other, save=True)
+    assert theirs.numel() == saved.numel()  # nothing is kept of x and the weights: the width does not count
+    half = ffn_inputs(40, 96, 64, 32, torch.float16, False, seed=248)
+    for bad, what in ((theirs, {}), (saved, {"activation": "gelu"}),
+                      (sla.sla_gated_ffn(*half, save=True)[1], {}), (torch.cat((saved, saved)), {})):
+        with pytest.raises(ValueError, match="another activation"):
+            sla.sla_gated_ffn_backward(dy, *args[:3], bad, **what)
+    for kept in (saved, saved.clone()):
+        got = sla.sla_gated_ffn_backward(dy, *args[:3], kept)
+        assert all(p is None or torch.equal(p, q) for p, q in zip(got, want))
