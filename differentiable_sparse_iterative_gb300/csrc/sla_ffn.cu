@@ -234,7 +234,7 @@ Operand as_operand(PackJobs &jobs, const T *src, int64_t rows, int64_t cols, int
     j.src = src, j.dst = (uint16_t *)to, j.rows = rows, j.cols = cols, j.src_ld = ld, j.src_half = half, j.ld = pitch;
     j.halves = halves, j.vec = aligned(src, 16) && ld * sizeof(T) % 16 == 0;
     j.first = jobs.blocks;
-    j.blocks = (int)std::min<int64_t>((halves * rows * (pitch / 8) + 255) / 256, 152 * 16);
+    j.blocks = (int)std::min<int64_t>((halves * rows * (pitch / 8) + 255) / 256, sm_count() * 16);
     jobs.blocks += j.blocks;
   }
   return {to, cols, rows, (int64_t)sheets_of<T>() * halves, pitch, rows * pitch};
@@ -513,7 +513,7 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, cons
   const int blocks = (int)workers * tile.cg;
   c.launched(launch_product<T>(as, plan.shape, blocks, l, c.early(), c.st));
   if (!nsplit) return;
-  const dim3 grid((unsigned)std::min<int64_t>((finish + 255) / 256, 152 * 16), nsplit);
+  const dim3 grid((unsigned)std::min<int64_t>((finish + 255) / 256, sm_count() * 16), nsplit);
   if (epi == kStore)
     c.launch(finish_splits<T, kStore>, grid, 256, f);
   else if (epi == kGate)
@@ -622,7 +622,7 @@ struct ColumnSums {
     while (tpr < 32 && tpr < chunks) tpr <<= 1;
     const int64_t tiles = (chunks + tpr - 1) / tpr;
     // enough blocks to fill the GPU, each with at least eight turns of its threads
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kSumParts, 152 * 8 / tiles));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kSumParts, sm_count() * 8 / tiles));
     const int64_t per = std::max<int64_t>(8 * (256 / tpr), (rows + most - 1) / most);
     const int nparts = (int)((rows + per - 1) / per);
     c.launch(vec ? column_parts<E, S, V> : column_parts<E, S, 1>, dim3((unsigned)tiles, nparts), 256, rows, cols, a, lda,
@@ -816,7 +816,7 @@ sla_status forward(const sla_ffn *f, const T *x, int64_t ldx, const T *w_in, con
   }
   const Operand oh{h, f->hidden, f->tokens, sheets_of<T>(), ldg, f->tokens * ldg};
   ProductJob gate{gate_size(f), ox, false, oi, false, {}, true};
-  gate.p.act = f->activation, gate.p.vec = 1;
+  gate.p.act = f->activation;
   gate.p.bias = b_in, gate.p.bias_vec = b_in && aligned(b_in, 32) && f->hidden % 16 == 0;
   gate.p.g = saved, gate.p.u = saved ? saved + L.u : nullptr;
   gate.p.h = (uint16_t *)h, gate.p.ldg = ldg, gate.p.sheet = f->tokens * ldg;
@@ -856,7 +856,6 @@ sla_status backward(const sla_ffn *f, const T *dy, int64_t lddy, const T *x, int
   ColumnSums columns{c, w.columns, {}};
   if (inner) {
     ProductJob dh{dh_size(f), ody, false, oo, true, {}, true};
-    dh.p.act = f->activation, dh.p.vec = 1;
     dh.p.g = sv, dh.p.u = sv + L.u;
     dh.p.h = (uint16_t *)w.dgu, dh.p.ldg = ldg, dh.p.sheet = sheet;
     // the epilogue sums dg and du over 32 rows on its way, unless the product is split

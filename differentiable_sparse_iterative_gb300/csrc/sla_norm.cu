@@ -635,7 +635,7 @@ cudaError_t forward(int64_t rows, int64_t width, const LnPlan &pl, const void *x
   (pl.edge ? launch_forward<T, P, NI, R, true>(pl, rows, width, x, ldx, w, b, eps, y, mean, rstd, st)           \
            : launch_forward<T, P, NI, R, false>(pl, rows, width, x, ldx, w, b, eps, y, mean, rstd, st))
   if (pl.items == 0)
-    ln_forward_any<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
+    ln_forward_any<T, P><<<(unsigned)std::min<int64_t>(rows, sm_count() * 64), kMaxThreads, 0, st>>>(
         rows, width, (const T *)x, ldx, (const P *)w, (const P *)b, eps, (T *)y, mean, rstd);
   else
     pl.items == 1 ? SLA_LN_FWD(1, 2) : pl.items == 2 ? SLA_LN_FWD(2, 1) : SLA_LN_FWD(4, 1);
@@ -667,7 +667,7 @@ cudaError_t backward(int64_t rows, int64_t width, const LnPlan &pl, const void *
            : launch_backward<T, P, NI, R, false>(pl, rows, width, dy, lddy, x, ldx, w, mean, rstd, dx, parts, st))
   if (pl.items == 0) {
     if (dx)
-      ln_backward_any<T, P><<<(unsigned)std::min<int64_t>(rows, 152 * 64), kMaxThreads, 0, st>>>(
+      ln_backward_any<T, P><<<(unsigned)std::min<int64_t>(rows, sm_count() * 64), kMaxThreads, 0, st>>>(
           rows, width, (const T *)dy, lddy, (const T *)x, ldx, (const P *)w, mean, rstd, (T *)dx);
     if (parts) {
       nparts = (int)std::max<int64_t>(1, std::min<int64_t>(16, (rows + 127) / 128));

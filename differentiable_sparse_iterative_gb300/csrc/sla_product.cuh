@@ -19,9 +19,9 @@
 // core reads both from the 128-byte swizzled tiles that TMA writes, so no operand is transposed.
 //
 // One block (or a pair of blocks on two multiprocessors, CG = 2, each with half of B and its own 128
-// rows) keeps a tile of 128 CG x BN in tensor memory, twice: while eight warps empty one through the
-// epilogue, one thread feeds the next tile's mma and another its TMA loads.  Blocks are persistent and
-// take tiles in bands of kBand tile rows, so that what the running blocks read stays in L2.
+// rows) keeps a tile of 128 CG x BN in tensor memory, twice: while eight warps (sixteen with the widest 16-bit tiles)
+// empty one through the epilogue, one warp feeds the next tile's mma and another its TMA loads.  Blocks are
+// persistent and take tiles in bands of kBand tile rows, so that what the running blocks read stays in L2.
 //
 // Measured at 16,384 tokens, 1024 -> 4096 -> 1024 in bfloat16, where cuBLAS reaches 1,725 to 1,902 TFLOP/s: dx,
 // dw_in and dw_out in one launch 1,836 TFLOP/s (tensor cores 96 % busy), out 1,531, gate 1,487 (its three arrays
@@ -67,7 +67,7 @@ struct ProductArgs {
   int a_mn, b_mn;
   int f16;                   // operands are float16 (else bfloat16)
   int act;
-  int vec;                   // rows of c are aligned to 32 bytes
+  int vec;                   // kStore: rows of c are aligned to 32 bytes
   void *c;                   // kStore: T, or with splits float [splits][..]
   int64_t ldc, c_m_half, c_n_half, c_split;
   const void *bias;          // T, [n] (kStore) or [2 n] (kGate), or NULL
@@ -200,19 +200,9 @@ __device__ __forceinline__ void store_operand(uint16_t *p, int64_t sheet, const 
   for (int q = 0; q < S; ++q) {
     uint16_t *d = p + q * sheet;
     if (vec && count >= N) {
-      if constexpr (N % 16 == 0) {
 #pragma unroll
-        for (int i = 0; i < N; i += 16) {
-          Sector t;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) t.w[k] = w[q][i + 2 * k] | ((uint32_t)w[q][i + 2 * k + 1] << 16);
-          store_sector(d + i, t);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 8)
-          *reinterpret_cast<Pack<uint16_t, 8> *>(d + i) = *reinterpret_cast<Pack<uint16_t, 8> *>(&w[q][i]);
-      }
+      for (int i = 0; i < N; i += 8)
+        *reinterpret_cast<Pack<uint16_t, 8> *>(d + i) = *reinterpret_cast<Pack<uint16_t, 8> *>(&w[q][i]);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
