@@ -17,7 +17,9 @@
 // first weights, which do not depend on h, and then waits for h.
 //
 // Measured (both products): one token 9.9 us at 1024 -> 4096 -> 1024 in bfloat16, where the tiled products take
-// 21.1; 16 tokens 11.9 against 19.3, and 17.5 against 18.1 at 256 -> 1024 -> 256 in float32.  A third eight of
+// 21.1; 16 tokens 11.9 against 19.3, and 17.5 against 18.1 at 256 -> 1024 -> 256 in float32.  In float32 one to eight
+// tokens take 27 us at 1024 -> 4096 -> 1024 (floor 7.5): every weight is split into three parts in registers and each 32
+// of k takes 12 mma.  A third eight of
 // tokens does not pay any more: 18.0 against 19.4 and 27.8 against 18.1 at 24 tokens.
 #pragma once
 

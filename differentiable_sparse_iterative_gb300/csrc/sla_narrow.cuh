@@ -12,9 +12,10 @@
 // One warp issues the first products, as far ahead as there is room for, and another the second ones.  H is
 // written as TMA would have put it there: 128-byte rows of 64 hidden units, 16-byte units swizzled by the row.
 //
-// Measured at 1,000,000 tokens: 157 us at 64 -> 256 -> 64 in bfloat16 where the two tiled products take 305, 79 against
-// 191 at 32 -> 128 -> 32 and 123 against 236 at 128 -> 96 -> 128; 64 tokens 7.6 us against 8.3.  Bound by the
-// load-store pipe (70 % busy: sums out of tensor memory, H into shared memory, biases); tensor cores 27 %, DRAM 17 %.
+// Measured at 1,000,000 tokens: 168 us at 64 -> 256 -> 64 in bfloat16 where the two tiled products take 323, 82 against
+// 189 at 32 -> 128 -> 32 and 137 against 242 at 128 -> 96 -> 128; 64 tokens 8.4 us against 8.6.  Bound by the
+// load-store pipe (66 % busy: sums out of tensor memory, H into shared memory, biases); special functions 34 %, tensor
+// cores 25 %, DRAM 16 %.
 #pragma once
 
 #include "sla_product.cuh"

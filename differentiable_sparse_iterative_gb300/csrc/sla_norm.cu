@@ -23,8 +23,10 @@
 // kernels, which read element by element and re-read from L2.
 //
 // Measured, forward and backward together, against the copy rate of 6.69 TB/s: 1,000,000 x 64 bfloat16 122 us
-// (0.78), 65536 x 1024 bfloat16 140 us (0.72), x 1001 150 us (0.65), 65536 x 512 float32 125 us (0.80).  16-bit rows
-// are held up by instructions as much as by memory.
+// (0.78), 65536 x 1024 bfloat16 140 us (0.72), x 1001 152 us (0.64), 300,000 x 100 bfloat16 86 us (0.52), 65536 x 512
+// float32 125 us (0.80).  Beyond 256 columns 16-bit rows wait for the two sums of a row, one after the other, across warps
+// (stalls on shared memory and barriers; issue 46 to 49 %, DRAM 46 to 51 %).  The *_any kernels: 4096 x 40000 bfloat16 997 us
+// (0.25), 65536 x 1024 as a view one element off 729 us (0.14).
 #include <cuda_runtime.h>
 
 #include <algorithm>

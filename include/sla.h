@@ -571,9 +571,11 @@ SLA_API size_t sla_gated_ffn_backward_workspace_bytes(const sla_ffn *f);
  *   workspace  device, sla_gated_ffn_workspace_bytes, 256-byte aligned
  * Sums run in float32.  With 16-bit data, h and what is saved (act(g) and u act'(g)) are rounded to
  * dtype; with float32 data they stay float32, and the products are float32's (each factor split into
- * three bfloat16 parts, 24 bits in all; an infinity among the factors gives NaN).  A float16 block
- * whose |h| passes 65504 gives infinities, as float16 data does everywhere.  The first call on a
- * device looks up addresses and sets kernel attributes: make it before any stream capture.
+ * three bfloat16 parts, 24 bits in all; an infinity among the factors, or a value beyond bfloat16's
+ * largest, 3.39e38, gives NaN).  A float16 block whose |h| passes 65504 gives infinities, as float16 data
+ * does everywhere; one whose |act(g)| or |u act'(g)| does, with a finite h, gives them in its gradients.
+ * The first call on a device allocates four bytes of host memory and sets kernel attributes: make it
+ * before any stream capture.
  */
 SLA_API sla_status sla_gated_ffn(const sla_ffn *f, const void *x, int64_t ldx, const void *w_in, const void *b_in,
                                  const void *w_out, const void *b_out, void *y, void *saved, size_t saved_bytes,
@@ -582,7 +584,9 @@ SLA_API sla_status sla_gated_ffn(const sla_ffn *f, const void *x, int64_t ldx, c
 /*
  * Gradients for an upstream gradient dy [tokens][out] (lddy): dx [tokens][width], dw_in, dw_out,
  * db_in [2 hidden] and db_out [out], each NULL when not wanted.  x, the weights and `saved` are the
- * forward call's.  tokens = 0 sets the weights' and biases' gradients to zero.
+ * forward call's: saved may hold packed copies of x and the weights, which are read in their place.  With
+ * 16-bit data the gradients of g and u are rounded to dtype between the products.  tokens = 0 sets the
+ * weights' and biases' gradients to zero.
  */
 SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                           const void *w_in, const void *w_out, const void *saved, size_t saved_bytes,
