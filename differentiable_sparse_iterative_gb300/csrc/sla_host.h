@@ -44,6 +44,21 @@ sla_status check_csr(const sla_csr *A, bool need_values);
 sla_status check_vec(const void *p, const sla_csr *A, bool allow_null);
 sla_status check_opts(const sla_cg_opts *o);
 
+// A device's count of blocks that gave up a bounded wait, since the process started.  It lies in host memory that the
+// kernels add to, so that a call sees without waiting for the GPU whether an earlier one was cut short.  It only
+// grows: what a thread has been told of is its own number, so that no thread takes another's report.
+struct Expired {
+  uint32_t *count = nullptr;
+  int dev = 0;
+  cudaError_t err = cudaSuccess;
+};
+
+// The current device's.  A thread is told of what expires after its first time here.
+Expired expired();
+
+// SLA_TIMEOUT if waits have expired that this thread has not been told of.
+sla_status report_expired(const Expired &x);
+
 #define SLA_CHECK(expr)            \
   do {                             \
     sla_status st_ = (expr);       \
