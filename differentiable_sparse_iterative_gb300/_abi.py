@@ -27,7 +27,8 @@ EXPORTS = [
     "sla_bicgstab_solve", "sla_bicgstab_adjoint", "sla_layernorm", "sla_layernorm_backward_workspace_bytes",
     "sla_layernorm_backward", "sla_gated_ffn_saved_bytes", "sla_gated_ffn_workspace_bytes",
     "sla_gated_ffn_backward_workspace_bytes", "sla_gated_ffn", "sla_gated_ffn_backward",
-    "sla_gated_ffn_check", "sla_test_expire_wait",
+    "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan_saved_bytes", "sla_gated_scan_workspace_bytes",
+    "sla_gated_scan", "sla_gated_scan_backward",
 ]
 SLA_SPMV_PLAIN, SLA_SPMV_TMA = 0, 1
 
@@ -61,6 +62,12 @@ class sla_eig_info(ctypes.Structure):
 class sla_ffn(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("width", ctypes.c_int64), ("hidden", ctypes.c_int64),
                 ("out", ctypes.c_int64), ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class sla_scan(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("sequences", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("offsets_type", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reverse", ctypes.c_int32), ("outside", ctypes.c_int32)]
 
 
 def bind(lib):
@@ -120,6 +127,12 @@ def bind(lib):
     lib.sla_test_expire_wait.argtypes = [P]
     lib.sla_gated_ffn.argtypes = [F, P, i64, P, P, P, P, P, P, sz, P, sz, P]
     lib.sla_gated_ffn_backward.argtypes = [F, P, i64, P, i64, P, P, P, sz, P, P, P, P, P, P, sz, P]
+    S = ctypes.POINTER(sla_scan)
+    for name in ["sla_gated_scan_saved_bytes", "sla_gated_scan_workspace_bytes"]:
+        getattr(lib, name).argtypes = [S]
+        getattr(lib, name).restype = sz
+    lib.sla_gated_scan.argtypes = [S, P, i64, P, i64, P, P, P, P, sz, P, sz, P]
+    lib.sla_gated_scan_backward.argtypes = [S, P, i64, P, P, i64, P, i64, P, P, sz, P, P, P, P, sz, P]
     lib.sla_set_spmv_variant.argtypes = [i32]
     lib.sla_graph_cache_stats.argtypes = [ctypes.POINTER(i64)] * 3
     lib.sla_test_set_barrier_wait.argtypes = [ctypes.c_uint32, i64]
@@ -129,7 +142,7 @@ def bind(lib):
                  "sla_cg_solve_batched", "sla_cg_adjoint_batched", "sla_cg_solve_static", "sla_eig_smallest",
                  "sla_eig_grad_values", "sla_eigsh", "sla_bicgstab_solve", "sla_bicgstab_adjoint",
                  "sla_layernorm", "sla_layernorm_backward", "sla_gated_ffn", "sla_gated_ffn_backward",
-                 "sla_gated_ffn_check", "sla_test_expire_wait"]:
+                 "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan", "sla_gated_scan_backward"]:
         getattr(lib, name).restype = i32
     return lib
 

@@ -594,6 +594,58 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
                                           void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * A gated scan: a linear recurrence along the rows of sequences, channel by channel, with a gate that says how much
+ * of the state is kept.
+ *   h_t = a_t h_{t-1} + (1 - a_t) x_t,   a_t = 1 / (1 + exp(-gate_t)),   h_0 = the sequence's state
+ * In each channel that is the solve of a unit lower bidiagonal system, and its backward call the solve with the
+ * transpose.  The rows of all sequences lie one behind another.  Without offsets they have rows / sequences rows each; with
+ * offsets, sequence i has the rows from offsets[i] to offsets[i + 1] (not less than offsets[i]; none if they are
+ * equal), offsets[sequences] <= rows, and rows before offsets[0] or behind offsets[sequences] belong to none.  (Offsets that
+ * break this give results without meaning, but nothing outside of the arrays is touched.)
+ */
+typedef struct sla_scan {
+  int64_t rows;           /* of all sequences, 0 <= rows < 2^31 */
+  int64_t channels;       /* 1 .. 2^24; rows / 128 times channels / 64 (both rounded up) below 2^31 */
+  int64_t sequences;      /* 0 .. 2^31 - 1; without offsets a divisor of rows */
+  const void *offsets;    /* device, [sequences + 1], or NULL */
+  int32_t offsets_type;   /* SLA_I32 or SLA_I64 */
+  int32_t dtype;          /* SLA_F32, SLA_F16 or SLA_BF16, of x, gate, h and their gradients */
+  int32_t reverse;        /* 0, or 1: each sequence from its last row to its first */
+  int32_t outside;        /* rows of h that belong to no sequence: 0 stay as they are, 1 become zero */
+} sla_scan;
+
+/* Bytes of what a forward call keeps for its backward call (float32 states of every 16th row), and of the scratch of
+   either call, which is 0 where no sequence needs more than one block (both 0 for invalid arguments). */
+SLA_API size_t sla_gated_scan_saved_bytes(const sla_scan *s);
+SLA_API size_t sla_gated_scan_workspace_bytes(const sla_scan *s);
+
+/*
+ *   x, gate      device, [rows][channels] with leading dimensions ldx and ldg
+ *   state        device, [sequences][channels] float32: the states before the sequences, or NULL: zero
+ *   h            device, [rows][channels]
+ *   final_state  device, [sequences][channels] float32: the states behind the sequences, or NULL.  It may be `state`.
+ *   saved        device, sla_gated_scan_saved_bytes, 256-byte aligned, or NULL
+ *   workspace    device, sla_gated_scan_workspace_bytes, 256-byte aligned
+ * States are float32 from row to row; h is what they round to.  A sequence with no rows ends in the state that it
+ * starts with.  An infinity or NaN makes NaN of the rest of its channel's sequence, and of nothing else.
+ * Blocks wait for one another's results within the launch, each wait for two seconds at most (see sla_gated_ffn_check).
+ */
+SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx, const void *gate, int64_t ldg,
+                                  const float *state, void *h, float *final_state, void *saved, size_t saved_size,
+                                  void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients for the upstream gradients dh (of h; lddh; NULL: zero) and dfinal (of final_state, float32; NULL: zero): dx and
+ * dgate, [rows][channels], zero in rows that belong to no sequence, and dstate, [sequences][channels] float32, each NULL when
+ * not wanted.  x, gate, state and saved are the forward call's.
+ */
+SLA_API sla_status sla_gated_scan_backward(const sla_scan *s, const void *dh, int64_t lddh, const float *dfinal,
+                                           const void *x, int64_t ldx, const void *gate, int64_t ldg,
+                                           const float *state, const void *saved, size_t saved_size, void *dx,
+                                           void *dgate, float *dstate, void *workspace, size_t ws_bytes,
+                                           void *stream);
+
+/*
  * Every wait inside the products' kernels is bounded (about two seconds); one that expires, which no
  * input can cause, leaves its tile unwritten and is counted.  Each host thread is told once of what has
  * expired on a device since its own first call there: sla_gated_ffn and sla_gated_ffn_backward return
