@@ -11,6 +11,8 @@ SLA_OK, SLA_NOT_CONVERGED, SLA_BREAKDOWN, SLA_INVALID_ARG, SLA_BAD_CSR, SLA_NONF
 SLA_WORKSPACE_TOO_SMALL, SLA_TIMEOUT, SLA_CUDA_ERROR = 6, 7, 8
 SLA_F32, SLA_F64, SLA_F16, SLA_BF16 = 0, 1, 2, 3
 SLA_ACT_SILU, SLA_ACT_GELU, SLA_ACT_GELU_TANH, SLA_ACT_RELU = 0, 1, 2, 3
+SLA_NORM_LAYER, SLA_NORM_RMS = 0, 1
+SLA_GATE_NONE, SLA_GATE_SIGMOID, SLA_GATE_SILU = 0, 1, 2
 SLA_I32, SLA_I64 = 0, 1
 SLA_PRECOND_NONE, SLA_PRECOND_JACOBI = 0, 1
 SLA_LOOP_AUTO, SLA_LOOP_HOST, SLA_LOOP_GRAPH, SLA_LOOP_RESIDENT, SLA_LOOP_CLUSTER = 0, 1, 2, 3, 4
@@ -28,7 +30,8 @@ EXPORTS = [
     "sla_layernorm_backward", "sla_gated_ffn_saved_bytes", "sla_gated_ffn_workspace_bytes",
     "sla_gated_ffn_backward_workspace_bytes", "sla_gated_ffn", "sla_gated_ffn_backward",
     "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan_saved_bytes", "sla_gated_scan_workspace_bytes",
-    "sla_gated_scan", "sla_gated_scan_backward",
+    "sla_gated_scan", "sla_gated_scan_backward", "sla_residual_norm", "sla_residual_norm_backward_workspace_bytes",
+    "sla_residual_norm_backward",
 ]
 SLA_SPMV_PLAIN, SLA_SPMV_TMA = 0, 1
 
@@ -68,6 +71,12 @@ class sla_scan(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("sequences", ctypes.c_int64),
                 ("offsets", ctypes.c_void_p), ("offsets_type", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("reverse", ctypes.c_int32), ("outside", ctypes.c_int32)]
+
+
+class sla_resnorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("norm", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("gate_act", ctypes.c_int32), ("reserved", ctypes.c_int32), ("eps", ctypes.c_double)]
 
 
 def bind(lib):
@@ -133,6 +142,11 @@ def bind(lib):
         getattr(lib, name).restype = sz
     lib.sla_gated_scan.argtypes = [S, P, i64, P, i64, P, P, P, P, sz, P, sz, P]
     lib.sla_gated_scan_backward.argtypes = [S, P, i64, P, P, i64, P, i64, P, P, sz, P, P, P, P, sz, P]
+    R = ctypes.POINTER(sla_resnorm)
+    lib.sla_residual_norm_backward_workspace_bytes.argtypes = [R]
+    lib.sla_residual_norm_backward_workspace_bytes.restype = sz
+    lib.sla_residual_norm.argtypes = [R, P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P, P]
+    lib.sla_residual_norm_backward.argtypes = [R] + [P, i64] * 5 + [P] * 14 + [sz, P]
     lib.sla_set_spmv_variant.argtypes = [i32]
     lib.sla_graph_cache_stats.argtypes = [ctypes.POINTER(i64)] * 3
     lib.sla_test_set_barrier_wait.argtypes = [ctypes.c_uint32, i64]
@@ -142,7 +156,8 @@ def bind(lib):
                  "sla_cg_solve_batched", "sla_cg_adjoint_batched", "sla_cg_solve_static", "sla_eig_smallest",
                  "sla_eig_grad_values", "sla_eigsh", "sla_bicgstab_solve", "sla_bicgstab_adjoint",
                  "sla_layernorm", "sla_layernorm_backward", "sla_gated_ffn", "sla_gated_ffn_backward",
-                 "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan", "sla_gated_scan_backward"]:
+                 "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan", "sla_gated_scan_backward",
+                 "sla_residual_norm", "sla_residual_norm_backward"]:
         getattr(lib, name).restype = i32
     return lib
 

@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import inspect
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 from torch.autograd.forward_ad import unpack_dual
@@ -256,6 +256,178 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     if _wants_grad(x, weight, bias):
         return LayerNorm.apply(x, weight, bias, eps)
     return sla_layernorm(_matrix_ready(x), weight, bias, eps=eps)
+
+
+# --------------------------------------------------------------------------- residual norm
+
+NORMS = {"layer": _abi.SLA_NORM_LAYER, "rms": _abi.SLA_NORM_RMS}
+GATE_ACTIVATIONS = {"none": _abi.SLA_GATE_NONE, "sigmoid": _abi.SLA_GATE_SIGMOID, "silu": _abi.SLA_GATE_SILU}
+
+
+class ResidualNormGrads(NamedTuple):
+    """Gradients of a residual norm, None where not wanted."""
+    block: Optional[torch.Tensor]
+    z: Optional[torch.Tensor]
+    gate: Optional[torch.Tensor]
+    scale: Optional[torch.Tensor]
+    post_weight: Optional[torch.Tensor]
+    post_bias: Optional[torch.Tensor]
+    weight: Optional[torch.Tensor]
+    bias: Optional[torch.Tensor]
+
+
+def _param_type(x, params):
+    """The parameters' common type: x's or float32."""
+    pt = next((p.dtype for p in params if p is not None), x.dtype)
+    if pt != x.dtype and pt != torch.float32:
+        raise ValueError(f"parameters must have dtype {x.dtype} or torch.float32, got {pt}")
+    return pt
+
+
+def _choice(value, choices, name):
+    found = choices.get(value)
+    if found is None:
+        raise ValueError(f"unknown {name} {value!r} (one of {', '.join(choices)})")
+    return found
+
+
+def _same_rows(t, x, name):
+    """(address, elements between rows) of a tensor of x's shape, or None."""
+    if t is None:
+        return None, 0
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must have the block's shape {tuple(x.shape)}, got {tuple(t.shape)}")
+    ptr, _, ld = _rows(t, name, x)
+    return ptr, ld
+
+
+class _ResNorm:
+    """A call's descriptor, the addresses of its inputs and their parameters."""
+
+    def __init__(self, block, z, gate, params, norm, post_norm, gate_activation, eps):
+        ptr, rows, ld = _rows(block, "block")
+        self.rows, self.width, self.index = rows, block.shape[-1], block.get_device()
+        self.pt = _param_type(block, params.values())
+        self.arrays = [ptr, ld, *_same_rows(z, block, "z"), *_same_rows(gate, block, "gate")]
+        self.params = [_param(t, name, (self.width,), self.pt, self.index) for name, t in params.items()]
+        d = _abi.sla_resnorm(rows, self.width, _type(block, "block"), _DT[self.pt], _choice(norm, NORMS, "norm"),
+                             1 if post_norm else 0, _choice(gate_activation, GATE_ACTIVATIONS, "gate activation"), 0, eps)
+        self.descriptor, self.ref = d, ctypes.byref(d)
+
+
+@_on_device_of_first
+def sla_residual_norm(block: torch.Tensor, z: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                      scale: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                      post_bias: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                      bias: Optional[torch.Tensor] = None, norm: str = "layer", post_norm: bool = True,
+                      next_norm: bool = True, gate_activation: str = "none", eps: float = 1e-5, stats: bool = False):
+    """A block's result joins the residual stream z (asynchronous): z' = z + scale * act(gate) * N(block) and
+    y = N(z'), the next block's input.
+
+    N(block) has post_weight and post_bias (post_norm=False: the block itself), N(z') weight and bias
+    (next_norm=False: y is None); norm is "layer" or "rms", gate_activation "none", "sigmoid" or "silu".  block, z and
+    gate have one shape; the parameters are [width], of its type or float32.  Returns (z', y), or with stats=True
+    (z', y, stats): the rows' float32 statistics that sla_residual_norm_backward takes."""
+    n = _ResNorm(block, z, gate, {"scale": scale, "post_weight": post_weight, "post_bias": post_bias, "weight": weight,
+                                  "bias": bias}, norm, post_norm, gate_activation, eps)
+    z_out = _empty(block.shape, dtype=block.dtype, device=block.device)
+    y = _empty(block.shape, dtype=block.dtype, device=block.device) if next_norm else None
+    kept = _empty((4, n.rows), dtype=torch.float32, device=block.device) if stats else None
+    _check(_lib().sla_residual_norm(n.ref, *n.arrays, *n.params, z_out.data_ptr(), y.data_ptr() if next_norm else None,
+                                    kept.data_ptr() if stats else None, _stream(n.index)), "sla_residual_norm")
+    return (z_out, y, kept) if stats else (z_out, y)
+
+
+@functools.lru_cache(maxsize=512)
+def _resnorm_backward_bytes(rows, width, dt, pt, device) -> int:
+    return _lib().sla_residual_norm_backward_workspace_bytes(ctypes.byref(_abi.sla_resnorm(rows, width, dt, pt, 0, 1, 0, 0, 0.0)))
+
+
+@_on_device_of_first
+def sla_residual_norm_backward(dz: Optional[torch.Tensor], dy: Optional[torch.Tensor], block: torch.Tensor,
+                               z: torch.Tensor, stats: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                               scale: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                               post_bias: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                               norm: str = "layer", post_norm: bool = True, gate_activation: str = "none",
+                               eps: float = 1e-5, want_grad_block: bool = True, want_grad_z: bool = True,
+                               want_grad_gate: bool = True, want_grad_params: bool = True,
+                               param_dtype: Optional[torch.dtype] = None,
+                               workspace: Optional[torch.Tensor] = None) -> ResidualNormGrads:
+    """Gradients of sla_residual_norm (asynchronous).  dz and dy belong to its two results; one of them may be None (zero).
+    The other arguments are the forward call's.  The parameters' gradients have the parameters' type (param_dtype, default the
+    block's, when there is none), also where the parameter itself was left out."""
+    n = _ResNorm(block, z, gate, {"scale": scale, "post_weight": post_weight, "post_bias": post_bias, "weight": weight},
+                 norm, post_norm, gate_activation, eps)
+    if all(p is None for p in (scale, post_weight, post_bias, weight)) and param_dtype is not None:
+        if param_dtype != block.dtype and param_dtype != torch.float32:
+            raise ValueError(f"param_dtype must be {block.dtype} or torch.float32, got {param_dtype}")
+        n.pt, n.descriptor.param_dtype = param_dtype, _DT[param_dtype]
+    up = [*_same_rows(dz, block, "dz"), *_same_rows(dy, block, "dy")]
+    sp = _param(stats, "stats", (4, n.rows), torch.float32, n.index)
+    dev = block.device
+
+    def rows_like(wanted):
+        return _empty(block.shape, dtype=block.dtype, device=dev) if wanted else None
+
+    def params_like(wanted):
+        return _empty(n.width, dtype=n.pt, device=dev) if wanted else None
+
+    post = want_grad_params and post_norm
+    after = want_grad_params and dy is not None
+    grads = ResidualNormGrads(rows_like(want_grad_block), rows_like(want_grad_z),
+                              rows_like(want_grad_gate and gate is not None), params_like(want_grad_params),
+                              params_like(post), params_like(post), params_like(after), params_like(after))
+    wsp, nbytes = None, 0
+    if want_grad_params:
+        ws, nbytes = _scratch(_resnorm_backward_bytes(n.rows, n.width, n.descriptor.dtype, n.descriptor.param_dtype,
+                                                      n.index), dev, workspace)
+        wsp = ws.data_ptr()
+    _check(_lib().sla_residual_norm_backward(n.ref, *up, *n.arrays, *n.params, sp,
+                                             *[None if t is None else t.data_ptr() for t in grads], wsp, nbytes,
+                                             _stream(n.index)), "sla_residual_norm_backward")
+    return grads
+
+
+class ResidualNorm(torch.autograd.Function):
+    """(z', y).  Saved for backward: block, z, the gate, the parameters and four floats a row (z' is formed again)."""
+
+    @staticmethod
+    def forward(ctx, block, z, gate, scale, post_weight, post_bias, weight, bias, how):
+        block, z = _matrix_ready(block), _matrix_ready(z)
+        gate = None if gate is None else _matrix_ready(gate)
+        z_out, y, stats = sla_residual_norm(block, z, gate, scale, post_weight, post_bias, weight, bias, stats=True, **how)
+        ctx.save_for_backward(block, z, gate, scale, post_weight, post_bias, weight, stats)
+        ctx.how = {k: v for k, v in how.items() if k != "next_norm"}
+        ctx.param_dtype = _param_type(block, (scale, post_weight, post_bias, weight, bias))
+        ctx.set_materialize_grads(False)
+        return z_out, y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dz, dy):
+        block, z, gate, scale, post_weight, post_bias, weight, stats = ctx.saved_tensors
+        if dz is None and dy is None:
+            return (None,) * 9
+        need = ctx.needs_input_grad
+        dz, dy = (None if t is None else _matrix_ready(t) for t in (dz, dy))
+        with torch.cuda.device(block.device):
+            g = sla_residual_norm_backward(dz, dy, block, z, stats, gate, scale, post_weight, post_bias, weight,
+                                           want_grad_block=need[0], want_grad_z=need[1], want_grad_gate=need[2],
+                                           want_grad_params=any(need[3:8]), param_dtype=ctx.param_dtype, **ctx.how)
+        return (*[t if n else None for t, n in zip(g, need)], None)
+
+
+def residual_norm(block: torch.Tensor, z: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                  post_bias: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                  bias: Optional[torch.Tensor] = None, norm: str = "layer", post_norm: bool = True,
+                  next_norm: bool = True, gate_activation: str = "none", eps: float = 1e-5):
+    """Differentiable residual norm (gradients flow to block, z, the gate and the parameters): (z', y)."""
+    how = {"norm": norm, "post_norm": post_norm, "next_norm": next_norm, "gate_activation": gate_activation, "eps": eps}
+    if _wants_grad(block, z, gate, scale, post_weight, post_bias, weight, bias):
+        return ResidualNorm.apply(block, z, gate, scale, post_weight, post_bias, weight, bias, how)
+    return sla_residual_norm(_matrix_ready(block), _matrix_ready(z), None if gate is None else _matrix_ready(gate), scale,
+                             post_weight, post_bias, weight, bias, **how)
 
 
 # --------------------------------------------------------------------------- gated feed-forward block

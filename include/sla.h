@@ -593,6 +593,66 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
                                           void *dx, void *dw_in, void *dw_out, void *db_in, void *db_out,
                                           void *workspace, size_t ws_bytes, void *stream);
 
+/* Norms of a residual norm, and what becomes of its gate. */
+typedef enum sla_norm {
+  SLA_NORM_LAYER = 0,     /* (x - mean) / sqrt(variance + eps) */
+  SLA_NORM_RMS = 1        /* x / sqrt(mean of x^2 + eps) */
+} sla_norm;
+typedef enum sla_gate {
+  SLA_GATE_NONE = 0,      /* taken as it is */
+  SLA_GATE_SIGMOID = 1,   /* 1 / (1 + exp(-g)) */
+  SLA_GATE_SILU = 2       /* g / (1 + exp(-g)) */
+} sla_gate;
+
+/*
+ * Where a block's result joins the residual stream: normed, gated, scaled and added, and the sum normed for the next
+ * block (z_out and y of one call are the next block's residual stream and input).
+ *   u = N(block) * post_weight + post_bias    (post_norm = 0: u = block)
+ *   z_out = z + scale * act(gate) * u,  y = N(z_out) * weight + bias
+ */
+typedef struct sla_resnorm {
+  int64_t rows;           /* 0 <= rows < 2^31 */
+  int64_t width;          /* 1 .. 2^24 */
+  int32_t dtype;          /* SLA_F32, SLA_F16 or SLA_BF16: of the rows' arrays */
+  int32_t param_dtype;    /* dtype or SLA_F32: of scale, the weights and biases, and their gradients */
+  int32_t norm;           /* sla_norm, of both */
+  int32_t post_norm;      /* 1: the block's result is normed; 0: it is not */
+  int32_t gate_act;       /* sla_gate; without a gate it is not looked at */
+  int32_t reserved;       /* 0 */
+  double eps;
+} sla_resnorm;
+
+/*
+ *   block, z, gate    device, [rows][width] with leading dimensions; gate may be NULL: one
+ *   scale, post_weight, weight    device, [width] or NULL: one;  post_bias, bias: NULL: zero
+ *   z_out, y          device, [rows][width]; y may be NULL: no second norm
+ *   stats             device, [4][rows] float32 or NULL: the rows' statistics, for the backward call
+ * Everything is computed in float32; y is the norm of the sum before its rounding to z_out.  The results may not overlap what
+ * is read.  A NaN or an infinity in a row makes NaN of that row's results alone.
+ */
+SLA_API sla_status sla_residual_norm(const sla_resnorm *n, const void *block, int64_t ldblock, const void *z, int64_t ldz,
+                                     const void *gate, int64_t ldgate, const void *scale, const void *post_weight,
+                                     const void *post_bias, const void *weight, const void *bias, void *z_out, void *y,
+                                     float *stats, void *stream);
+
+/* Scratch of sla_residual_norm_backward (0 for invalid arguments). */
+SLA_API size_t sla_residual_norm_backward_workspace_bytes(const sla_resnorm *n);
+
+/*
+ * Gradients for the upstream gradients dz_out and dy (each may be NULL: zero) of rows (dblock, dz, dgate, in dtype) and of
+ * parameters (dscale, dpost_weight, dpost_bias, dweight, dbias, [width] in param_dtype, summed in float32), each NULL
+ * when not wanted.  block, z, gate, the parameters and stats are the forward call's (all four rows of it: y was
+ * asked for there if dy is given here).  The workspace is needed for the parameters' gradients only.  rows = 0
+ * sets those to zero.
+ */
+SLA_API sla_status sla_residual_norm_backward(const sla_resnorm *n, const void *dz_out, int64_t lddz, const void *dy,
+                                              int64_t lddy, const void *block, int64_t ldblock, const void *z, int64_t ldz,
+                                              const void *gate, int64_t ldgate, const void *scale,
+                                              const void *post_weight, const void *post_bias, const void *weight,
+                                              const float *stats, void *dblock, void *dz, void *dgate, void *dscale,
+                                              void *dpost_weight, void *dpost_bias, void *dweight, void *dbias,
+                                              void *workspace, size_t ws_bytes, void *stream);
+
 /*
  * A gated scan: a linear recurrence along the rows of sequences, channel by channel, with a gate that says how much
  * of the state is kept.
