@@ -50,6 +50,7 @@ __all__ = [
     "sla_gated_ffn", "sla_gated_ffn_backward", "sla_gated_ffn_check", "GatedFFN", "gated_ffn",
     "sla_test_expire_wait", "sla_gated_scan", "sla_gated_scan_backward", "GatedScan", "gated_scan",
     "sla_residual_norm", "sla_residual_norm_backward", "ResidualNorm", "ResidualNormGrads", "residual_norm",
+    "sla_linear", "sla_linear_backward", "Linear", "linear",
 ]
 from ._abi import SLA_SPMV_PLAIN, SLA_SPMV_TMA  # noqa: E402
 
@@ -734,8 +735,8 @@ def eigsh(A: CSRMatrix, k: int = 1, tol: Optional[float] = None, maxit: int = 20
 
 # --------------------------------------------------------------------------- dense operators
 
-from .dense import (GatedFFN, LayerNorm, ResidualNorm, ResidualNormGrads, gated_ffn, layer_norm,  # noqa: E402
-                    residual_norm, sla_residual_norm, sla_residual_norm_backward, sla_gated_ffn, sla_gated_ffn_backward,
+from .dense import (GatedFFN, LayerNorm, Linear, ResidualNorm, ResidualNormGrads, gated_ffn, layer_norm,  # noqa: E402
+                    linear, residual_norm, sla_linear, sla_linear_backward, sla_residual_norm, sla_residual_norm_backward, sla_gated_ffn, sla_gated_ffn_backward,
                     sla_gated_ffn_check, sla_layernorm, sla_layernorm_backward, sla_layernorm_backward_workspace_bytes,
                     sla_test_expire_wait)
 from .scan import GatedScan, gated_scan, sla_gated_scan, sla_gated_scan_backward  # noqa: E402

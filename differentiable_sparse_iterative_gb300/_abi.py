@@ -10,7 +10,7 @@ LIB_PATH = os.path.join(HERE, "libsla.so")
 SLA_OK, SLA_NOT_CONVERGED, SLA_BREAKDOWN, SLA_INVALID_ARG, SLA_BAD_CSR, SLA_NONFINITE = 0, 1, 2, 3, 4, 5
 SLA_WORKSPACE_TOO_SMALL, SLA_TIMEOUT, SLA_CUDA_ERROR = 6, 7, 8
 SLA_F32, SLA_F64, SLA_F16, SLA_BF16 = 0, 1, 2, 3
-SLA_ACT_SILU, SLA_ACT_GELU, SLA_ACT_GELU_TANH, SLA_ACT_RELU = 0, 1, 2, 3
+SLA_ACT_SILU, SLA_ACT_GELU, SLA_ACT_GELU_TANH, SLA_ACT_RELU, SLA_ACT_NONE = 0, 1, 2, 3, 4
 SLA_NORM_LAYER, SLA_NORM_RMS = 0, 1
 SLA_GATE_NONE, SLA_GATE_SIGMOID, SLA_GATE_SILU = 0, 1, 2
 SLA_I32, SLA_I64 = 0, 1
@@ -31,7 +31,8 @@ EXPORTS = [
     "sla_gated_ffn_backward_workspace_bytes", "sla_gated_ffn", "sla_gated_ffn_backward",
     "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan_saved_bytes", "sla_gated_scan_workspace_bytes",
     "sla_gated_scan", "sla_gated_scan_backward", "sla_residual_norm", "sla_residual_norm_backward_workspace_bytes",
-    "sla_residual_norm_backward",
+    "sla_residual_norm_backward", "sla_linear_saved_bytes", "sla_linear_workspace_bytes",
+    "sla_linear_backward_workspace_bytes", "sla_linear", "sla_linear_backward",
 ]
 SLA_SPMV_PLAIN, SLA_SPMV_TMA = 0, 1
 
@@ -71,6 +72,11 @@ class sla_scan(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("sequences", ctypes.c_int64),
                 ("offsets", ctypes.c_void_p), ("offsets_type", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("reverse", ctypes.c_int32), ("outside", ctypes.c_int32)]
+
+
+class sla_layer(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("width", ctypes.c_int64), ("out", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
 
 
 class sla_resnorm(ctypes.Structure):
@@ -142,6 +148,12 @@ def bind(lib):
         getattr(lib, name).restype = sz
     lib.sla_gated_scan.argtypes = [S, P, i64, P, i64, P, P, P, P, sz, P, sz, P]
     lib.sla_gated_scan_backward.argtypes = [S, P, i64, P, P, i64, P, i64, P, P, sz, P, P, P, P, sz, P]
+    L = ctypes.POINTER(sla_layer)
+    for name in ["sla_linear_saved_bytes", "sla_linear_workspace_bytes", "sla_linear_backward_workspace_bytes"]:
+        getattr(lib, name).argtypes = [L]
+        getattr(lib, name).restype = sz
+    lib.sla_linear.argtypes = [L, P, i64, P, P, P, i64, P, P, sz, P, sz, P]
+    lib.sla_linear_backward.argtypes = [L, P, i64, P, i64, P, P, sz, P, P, P, P, sz, P]
     R = ctypes.POINTER(sla_resnorm)
     lib.sla_residual_norm_backward_workspace_bytes.argtypes = [R]
     lib.sla_residual_norm_backward_workspace_bytes.restype = sz
@@ -157,7 +169,7 @@ def bind(lib):
                  "sla_eig_grad_values", "sla_eigsh", "sla_bicgstab_solve", "sla_bicgstab_adjoint",
                  "sla_layernorm", "sla_layernorm_backward", "sla_gated_ffn", "sla_gated_ffn_backward",
                  "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan", "sla_gated_scan_backward",
-                 "sla_residual_norm", "sla_residual_norm_backward"]:
+                 "sla_residual_norm", "sla_residual_norm_backward", "sla_linear", "sla_linear_backward"]:
         getattr(lib, name).restype = i32
     return lib
 

@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsla.so")
 SOURCES = ["sla_cg.cu", "sla_api.cu", "sla_static.cu", "sla_resident.cu", "sla_cluster.cu", "sla_eig.cu", "sla_dist.cu",
            "sla_bicgstab.cu", "sla_norm.cu", "sla_waits.cu", "sla_scan.cu", "sla_resnorm.cu", "sla_resnorm_f32.cu", "sla_resnorm_f16.cu",
-           "sla_resnorm_bf16.cu", "sla_ffn.cu", "sla_product_f32.cu", "sla_product_f16.cu",
+           "sla_resnorm_bf16.cu", "sla_ffn.cu", "sla_linear.cu", "sla_product_f32.cu", "sla_product_f16.cu",
            "sla_product_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -1,4 +1,4 @@
-// Activations of the gated feed-forward block and their derivatives, in float32.
+// Activations of the gated feed-forward block and the linear layer and their derivatives, in float32.
 //
 //   silu       a = g s,            a' = s (1 + g (1 - s)),                 s = 1 / (1 + e^-g)
 //   gelu       a = g Phi(g),       a' = Phi(g) + g phi(g),                 Phi, phi of the normal distribution
@@ -105,6 +105,19 @@ __device__ __forceinline__ void gate(float (&g)[N], float (&u)[N], float (&h)[N]
       da = mul2(da, up);
       g[i + next] = da.y, g[i] = da.x, u[i + next] = a.y, u[i] = a.x;
     }
+  }
+}
+
+// v = act(v), and act'(v) if asked for.
+template <int Act, bool Derivative, int N>
+__device__ __forceinline__ void activate(float (&v)[N], float (&d)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    constexpr int next = N > 1;
+    float2 a, da;
+    activate2<Act, Derivative>(f2(v[i], v[i + next]), a, da);
+    v[i + next] = a.y, v[i] = a.x;
+    if (Derivative) d[i + next] = da.y, d[i] = da.x;
   }
 }
 

@@ -43,9 +43,11 @@ struct FewArgs {
   void *g, *u;             // T [tokens][ldg]: u act'(g) and act(g), or NULL (gate)
   uint16_t *h;             // operand sheets (gate)
   int64_t ldg, sheet;
+  const void *residual;    // T [tokens][ldr] or NULL (linear; act'(..) goes to g)
+  int64_t ldr;
 };
 
-// Gate product (kGate) or output product (kStore) of few tokens.
+// Gate product (kGate), output product (kStore) or linear layer (kLinear) of few tokens.
 template <typename T>
 cudaError_t launch_few(Epilogue epi, const FewArgs &p, cudaStream_t st);
 
@@ -130,8 +132,9 @@ __device__ __forceinline__ float cluster_read(const float *local, uint32_t rank)
 }
 
 // NT: tokens in eights.
-template <typename T, bool Gate, int NT>
+template <typename T, Epilogue EPI, int NT>
 __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, int ranks) {
+  constexpr bool Gate = EPI == kGate;
   constexpr int M = Gate ? 2 : 1, S = Eight<T>::S;
   extern __shared__ float sums[];  // [warps][M][16][8 NT], then [M][16][8 NT] of the block
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
   ask(turn);
   if (Gate)
     grid_dependency_launch();
-  else
+  else if (EPI == kStore)
     grid_dependency_wait();
 
   float acc[M][NT][4] = {};
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int token = min(j * 8 + g, p.tokens - 1);
-        if (Gate) {
+        if constexpr (EPI != kStore) {
           RawEight<T> r;
           r.load((const T *)p.x + token * p.ldx + k, left, p.x_vec);
           r.parts(x[j]);
@@ -239,26 +242,36 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
       }
       store_operand<T, 1>(p.h + o, p.sheet, h, 1, false);
     } else {
+      if constexpr (EPI == kLinear) {
+        if (p.act != SLA_ACT_NONE) {
+          float a[1] = {v}, da[1];
+          with_activation(p.act, [&](auto act) { activate<act.value, true, 1>(a, da); });
+          v = a[0];
+          if (p.g) ((T *)p.g)[token * p.ldg + r] = from_f32<T>(da[0]);
+        }
+        if (p.residual) v += to_f32(((const T *)p.residual)[token * p.ldr + r]);
+      }
       ((T *)p.c)[token * (int64_t)p.n + r] = from_f32<T>(v);
     }
   }
   if (ranks > 1) cluster_sync_all();  // the others may still read this block's sums
 }
 
-template <typename T, bool Gate, int NT>
-cudaError_t launch_few_as(const FewArgs &p, int ranks, cudaStream_t st) {
-  constexpr int per = (Gate ? 2 : 1) * 16 * 8 * NT;
-  LaunchConfig cfg(dim3((p.n + 15) / 16 * ranks), 32 * kFewWarps, (kFewWarps + 1) * per * sizeof(float), st, !Gate, ranks);
-  return cudaLaunchKernelEx(&cfg.c, few_kernel<T, Gate, NT>, p, ranks);
+template <typename T, Epilogue EPI, int NT>
+cudaError_t launch_few_ranks(const FewArgs &p, int ranks, cudaStream_t st) {
+  constexpr int per = (EPI == kGate ? 2 : 1) * 16 * 8 * NT;
+  LaunchConfig cfg(dim3((p.n + 15) / 16 * ranks), 32 * kFewWarps, (kFewWarps + 1) * per * sizeof(float), st, EPI == kStore,
+                   ranks);
+  return cudaLaunchKernelEx(&cfg.c, few_kernel<T, EPI, NT>, p, ranks);
 }
 
-template <typename T, bool Gate>
-cudaError_t launch_few_gate(const FewArgs &p, cudaStream_t st) {
+template <typename T, Epilogue EPI>
+cudaError_t launch_few_as(const FewArgs &p, cudaStream_t st) {
   // blocks of a cluster share k until there are about as many as multiprocessors
   int ranks = 1;
   const int rows = (p.n + 15) / 16;
   while (ranks < 8 && rows * ranks * 2 <= 192 && p.k >= 32 * kFewWarps * ranks * 2) ranks *= 2;
-  return p.tokens <= 8 ? launch_few_as<T, Gate, 1>(p, ranks, st) : launch_few_as<T, Gate, 2>(p, ranks, st);
+  return p.tokens <= 8 ? launch_few_ranks<T, EPI, 1>(p, ranks, st) : launch_few_ranks<T, EPI, 2>(p, ranks, st);
 }
 
 }  // namespace sla

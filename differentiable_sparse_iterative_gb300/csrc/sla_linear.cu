@@ -1,0 +1,294 @@
+// The linear layer, forward and backward.
+//
+//   p = x W^T + b,  y = act(p) + r
+//   dp = dy act'(p),  dx = dp W,  dW = dp^T x,  db = sum dp
+//
+// Three tensor-core products (sla_product.cuh): the forward one with activation, derivative and residual as its
+// epilogue, the two of the backward pass in one launch.  Between them stands dp, which both read as an operand: without an
+// activation it is dy itself, in place where TMA can read it; else a kernel forms it from dy and the kept act'(p), lays
+// it out, and sums its columns on the way.  Up to kFewTokens tokens the forward product is sla_few.cuh's.
+//
+// act'(p) is kept in the data's type, and dp rounded to it, as 16-bit tensor-core operands have to be: with the result that
+// makes three roundings on the way to dx and dW (0.0029 in relative L2 in bfloat16, where one is 0.0017), two bytes a
+// value.  db is summed from dp before its rounding.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "sla_dense.cuh"
+#include "sla_few.cuh"
+
+namespace sla {
+namespace {
+
+int64_t out_pitch(const sla_layer *f) { return round_up(f->out, 16); }
+bool activates(const sla_layer *f) { return f->activation != SLA_ACT_NONE; }
+
+// Whether a forward call leaves packed copies of x and the weight: where TMA cannot read dense originals (the sizes alone
+// decide, so that both calls and the layout of what is saved agree).
+bool keeps_packed(const sla_layer *f) {
+  return f->tokens > kFewTokens && (f->dtype == SLA_F32 || f->width % 8 != 0);
+}
+
+// act'(p), rows out_pitch apart, then packed copies of x and the weight.
+struct SavedLayout {
+  size_t x, w, total;
+};
+
+SavedLayout saved_layout(const sla_layer *f) {
+  SavedLayout L;
+  L.x = activates(f) ? align256((size_t)f->tokens * (size_t)out_pitch(f) * net_size(f->dtype)) : 0;
+  L.w = L.x + (keeps_packed(f) ? packed_bytes(f->tokens, f->width, f->dtype) : 0);
+  L.total = L.w + (keeps_packed(f) ? packed_bytes(f->out, f->width, f->dtype) : 0);
+  return L;
+}
+
+int sheets(const sla_layer *f) { return f->dtype == SLA_F32 ? 3 : 1; }
+ProductSize y_size(const sla_layer *f) { return {f->tokens, f->out, f->width, 1, 1, 1}; }
+ProductSize dx_size(const sla_layer *f) { return {f->tokens, f->width, f->out, 1, 1, 1}; }
+ProductSize dw_size(const sla_layer *f) { return {f->out, f->width, f->tokens, 1, 1, 1}; }
+
+struct ForwardScratch {
+  void *x, *w;
+  float *parts, *runs;
+  size_t total;
+  ProductPlan plan;
+};
+
+// (the plan is the epilogue's with everything: what is kept or added may differ from call to call, the scratch may not)
+ForwardScratch forward_scratch(const sla_layer *f, char *base) {
+  Arena a{base};
+  ForwardScratch s{};
+  if (f->tokens <= kFewTokens) return s;
+  s.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
+  s.w = a.take(packed_bytes(f->out, f->width, f->dtype));
+  const ProductSize y = y_size(f);
+  s.plan = plan_products(activates(f) ? kLinear : kStore, &y, 1, sheets(f));
+  s.parts = (float *)a.take(s.plan.partial[1]);
+  s.runs = (float *)a.take(run_bytes(f->dtype));
+  s.total = a.used;
+  return s;
+}
+
+struct BackwardScratch {
+  void *dp, *x, *w;
+  float *columns, *parts, *runs;
+  size_t total;
+  ProductPlan plan;
+};
+
+BackwardScratch backward_scratch(const sla_layer *f, char *base) {
+  Arena a{base};
+  BackwardScratch s{};
+  s.dp = a.take(packed_bytes(f->tokens, f->out, f->dtype));
+  s.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
+  s.w = a.take(packed_bytes(f->out, f->width, f->dtype));
+  s.columns = (float *)a.take(kSumParts * sizeof(float) * (size_t)f->out);
+  const ProductSize two[2] = {dx_size(f), dw_size(f)};
+  s.plan = plan_products(kStore, two, 2, sheets(f));
+  s.parts = (float *)a.take(s.plan.partial[2]);
+  s.runs = (float *)a.take(run_bytes(f->dtype));
+  s.total = a.used;
+  return s;
+}
+
+// dp = dy act'(p) as an operand (rows `pitch` apart, float32 in three sheets), eight columns a thread; a block covers 256 / tpr
+// rows at a time, from row blockIdx.y * per, and leaves the column sums of its rows (parts: [gridDim.y][cols], or NULL).
+template <typename T>
+__global__ void __launch_bounds__(256) form_dp(int64_t rows, int64_t cols, const T *__restrict__ dy, int64_t lddy, int vec,
+                                               const T *__restrict__ da, int64_t ldda, uint16_t *__restrict__ dp,
+                                               int64_t pitch, int tpr, int64_t per, float *__restrict__ parts) {
+  __shared__ float sm[256 * 8];
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = 256 / tpr;
+  const int64_t c = (blockIdx.x * (int64_t)tpr + t) * 8;
+  const int64_t r0 = blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
+  const int count = (int)(cols - c < 8 ? cols - c : 8);
+  float s[8] = {};
+  if (c < cols)
+#pragma unroll 2
+    for (int64_t r = r0 + group; r < r1; r += groups) {
+      float v[8], d[8];
+      load_f32<T, 8>(da + r * ldda + c, d);
+      if (vec && count == 8) {
+        load_f32<T, 8>(dy + r * lddy + c, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < count ? to_f32(dy[r * lddy + c + k]) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = k < count ? v[k] * d[k] : 0.f;
+        s[k] += v[k];
+      }
+      store_operand<T, 8>(dp + r * pitch + c, rows * pitch, v, 8, true);
+    }
+  if (!parts) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sm[threadIdx.x * 8 + k] = s[k];
+  __syncthreads();
+  for (int i = threadIdx.x; i < tpr * 8; i += 256) {
+    const int64_t col = blockIdx.x * (int64_t)tpr * 8 + i;
+    float sum = 0.f;
+    for (int g = 0; g < groups; ++g) sum += sm[g * tpr * 8 + i];
+    if (col < cols) parts[blockIdx.y * cols + col] = sum;
+  }
+}
+
+template <typename T>
+sla_status forward(const sla_layer *f, const T *x, int64_t ldx, const T *w, const T *bias, const T *residual, int64_t ldr,
+                   T *y, char *saved, const ForwardScratch &s, cudaStream_t st) {
+  Call c{st};
+  const Expired earlier = expired();
+  if (earlier.err != cudaSuccess) return fail(earlier.err);
+  SLA_CHECK(report_expired(earlier));
+  c.timeouts = earlier.count;
+  const SavedLayout L = saved_layout(f);
+  T *da = saved && activates(f) ? (T *)saved : nullptr;
+  if (f->tokens <= kFewTokens) {
+    FewArgs p{};
+    p.tokens = (int)f->tokens, p.n = (int)f->out, p.k = (int)f->width, p.act = f->activation;
+    p.x = x, p.ldx = ldx, p.w = w, p.bias = bias;
+    p.x_vec = aligned(x, 16) && (f->tokens == 1 || ldx % 8 == 0), p.w_vec = aligned(w, 16) && f->width % 8 == 0;
+    p.c = y, p.g = da, p.ldg = out_pitch(f), p.residual = residual, p.ldr = ldr;
+    c.launched(launch_few<T>(kLinear, p, st));
+    return finish(c);
+  }
+  PackJobs packs;
+  const Copy copy = saved && keeps_packed(f) ? kLeft : kOwn;
+  const Operand ox = as_operand(packs, x, f->tokens, f->width, ldx, 1, copy ? saved + L.x : s.x, copy);
+  const Operand ow = as_operand(packs, w, f->out, f->width, f->width, 1, copy ? saved + L.w : s.w, copy);
+  run_packs<T>(c, packs);
+  ProductJob job{y_size(f), ox, false, ow, false, {}, true};
+  job.p.bias = bias, job.p.bias_vec = aligned(bias, 32);
+  job.p.c = y, job.p.ldc = f->out, job.p.vec = vec_out(y, f->out);
+  job.p.act = f->activation, job.p.g = da, job.p.ldg = out_pitch(f);
+  job.p.residual = residual, job.p.ldr = ldr, job.p.residual_vec = vec_out(residual, ldr);
+  run_products<T>(c, activates(f) || residual ? kLinear : kStore, &job, 1, s.plan, s.parts, s.runs);
+  return finish(c);
+}
+
+template <typename T>
+sla_status backward(const sla_layer *f, const T *dy, int64_t lddy, const T *x, int64_t ldx, const T *w, const char *saved,
+                    T *dx, T *dw, T *db, const BackwardScratch &s, cudaStream_t st) {
+  Call c{st};
+  const Expired earlier = expired();
+  if (earlier.err != cudaSuccess) return fail(earlier.err);
+  SLA_CHECK(report_expired(earlier));
+  c.timeouts = earlier.count;
+  const SavedLayout L = saved_layout(f);
+  const Copy copy = keeps_packed(f) ? kKept : kOwn;
+  char *sv = const_cast<char *>(saved);
+  const bool products = dx || dw;
+  PackJobs packs;
+  Operand odp{}, ox{}, ow{};
+  ColumnSums columns{c, s.columns, {}};
+  if (products && !activates(f)) odp = as_operand(packs, dy, f->tokens, f->out, lddy, 1, s.dp);
+  if (dw) ox = as_operand(packs, x, f->tokens, f->width, ldx, 1, copy ? sv + L.x : s.x, copy);
+  if (dx) ow = as_operand(packs, w, f->out, f->width, f->width, 1, copy ? sv + L.w : s.w, copy);
+  run_packs<T>(c, packs);
+  if (activates(f)) {
+    const int64_t pitch = round_up(f->out, 8), chunks = pitch / 8;
+    int tpr = 1;
+    while (tpr < 32 && tpr < chunks) tpr <<= 1;
+    const int64_t tiles = (chunks + tpr - 1) / tpr;
+    // enough blocks to fill the GPU, each with at least four turns of its threads
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kSumParts, sm_count() * 8 / tiles));
+    const int64_t per = std::max<int64_t>(4 * (256 / tpr), (f->tokens + most - 1) / most);
+    const int nparts = (int)((f->tokens + per - 1) / per);
+    const int vec = aligned(dy, 16) && (f->tokens == 1 || lddy * sizeof(T) % 16 == 0);
+    c.launch(form_dp<T>, dim3((unsigned)tiles, nparts), 256, f->tokens, f->out, dy, lddy, vec, (const T *)saved,
+             out_pitch(f), (uint16_t *)s.dp, pitch, tpr, per, db ? s.columns : nullptr);
+    if (db) columns.add(s.columns, nparts, f->out, f->out, f->out, db);
+    odp = {s.dp, f->out, f->tokens, sheets_of<T>(), pitch, f->tokens * pitch};
+  } else if (db) {
+    columns.of<T, 1>(f->tokens, f->out, dy, lddy, 0, f->out, f->out, db);
+  }
+  columns.finish<T>();
+  if (products) {
+    auto job = [&](const ProductSize &size, bool a_mn, const Operand &b, T *out) {
+      ProductJob j{size, odp, a_mn, b, true, {}, out != nullptr};
+      j.p.c = out, j.p.ldc = size.n, j.p.vec = vec_out(out, size.n);
+      return j;
+    };
+    const ProductJob two[2] = {job(dx_size(f), false, ow, dx), job(dw_size(f), true, ox, dw)};
+    run_products<T>(c, kStore, two, 2, s.plan, s.parts, s.runs);
+  }
+  return finish(c);
+}
+
+sla_status check_layer(const sla_layer *f) {
+  if (!f) return SLA_INVALID_ARG;
+  const int64_t most = (int64_t)1 << 24;
+  if (f->tokens < 0 || f->tokens > (int64_t)1 << 30) return SLA_INVALID_ARG;
+  if (f->width < 1 || f->width > most || f->out < 1 || f->out > most) return SLA_INVALID_ARG;
+  if (!net_dtype(f->dtype) || f->activation < SLA_ACT_SILU || f->activation > SLA_ACT_NONE) return SLA_INVALID_ARG;
+  return SLA_OK;
+}
+
+}  // namespace
+}  // namespace sla
+
+using namespace sla;
+
+extern "C" {
+
+SLA_API size_t sla_linear_saved_bytes(const sla_layer *f) { return check_layer(f) == SLA_OK ? saved_layout(f).total : 0; }
+
+SLA_API size_t sla_linear_workspace_bytes(const sla_layer *f) {
+  return check_layer(f) == SLA_OK ? forward_scratch(f, nullptr).total : 0;
+}
+
+SLA_API size_t sla_linear_backward_workspace_bytes(const sla_layer *f) {
+  return check_layer(f) == SLA_OK ? backward_scratch(f, nullptr).total : 0;
+}
+
+SLA_API sla_status sla_linear(const sla_layer *f, const void *x, int64_t ldx, const void *weight, const void *bias,
+                              const void *residual, int64_t ldr, void *y, void *saved, size_t saved_bytes,
+                              void *workspace, size_t ws_bytes, void *stream) {
+  SLA_CHECK(check_layer(f));
+  SLA_CHECK(check_matrix(x, f->tokens, f->width, ldx, f->dtype));
+  SLA_CHECK(check_matrix(y, f->tokens, f->out, f->out, f->dtype));
+  SLA_CHECK(check_matrix(weight, f->out, f->width, f->width, f->dtype));
+  if (residual) SLA_CHECK(check_matrix(residual, f->tokens, f->out, ldr, f->dtype));
+  if (!aligned(bias, net_size(f->dtype))) return SLA_INVALID_ARG;
+  if (saved) SLA_CHECK(check_scratch(saved, saved_bytes, saved_layout(f).total));
+  const ForwardScratch s = forward_scratch(f, (char *)workspace);
+  SLA_CHECK(check_scratch(workspace, ws_bytes, s.total));
+  if (f->tokens == 0) return SLA_OK;
+#define SLA_LINEAR_FWD(T)                                                                                       \
+  forward<T>(f, (const T *)x, ldx, (const T *)weight, (const T *)bias, (const T *)residual, ldr, (T *)y, \
+             (char *)saved, s, (cudaStream_t)stream)
+  return f->dtype == SLA_F32 ? SLA_LINEAR_FWD(float) : f->dtype == SLA_F16 ? SLA_LINEAR_FWD(f16) : SLA_LINEAR_FWD(bf16);
+#undef SLA_LINEAR_FWD
+}
+
+SLA_API sla_status sla_linear_backward(const sla_layer *f, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                       const void *weight, const void *saved, size_t saved_bytes, void *dx,
+                                       void *dweight, void *dbias, void *workspace, size_t ws_bytes, void *stream) {
+  SLA_CHECK(check_layer(f));
+  SLA_CHECK(check_matrix(dy, f->tokens, f->out, lddy, f->dtype));
+  SLA_CHECK(check_matrix(x, f->tokens, f->width, ldx, f->dtype));
+  SLA_CHECK(check_matrix(weight, f->out, f->width, f->width, f->dtype));
+  const size_t e = net_size(f->dtype);
+  for (const void *p : {(const void *)dx, (const void *)dweight, (const void *)dbias})
+    if (!aligned(p, e)) return SLA_INVALID_ARG;
+  SLA_CHECK(check_scratch(saved, saved_bytes, saved_layout(f).total));
+  const BackwardScratch s = backward_scratch(f, (char *)workspace);
+  SLA_CHECK(check_scratch(workspace, ws_bytes, s.total));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (f->tokens == 0) {  // sums over no tokens
+    cudaError_t err = dweight ? cudaMemsetAsync(dweight, 0, e * (size_t)(f->out * f->width), st) : cudaSuccess;
+    if (err == cudaSuccess && dbias) err = cudaMemsetAsync(dbias, 0, e * (size_t)f->out, st);
+    return err == cudaSuccess ? SLA_OK : fail(err);
+  }
+  if (!dx && !dweight && !dbias) return SLA_OK;
+#define SLA_LINEAR_BWD(T)                                                                                             \
+  backward<T>(f, (const T *)dy, lddy, (const T *)x, ldx, (const T *)weight, (const char *)saved, (T *)dx, (T *)dweight, \
+              (T *)dbias, s, st)
+  return f->dtype == SLA_F32 ? SLA_LINEAR_BWD(float) : f->dtype == SLA_F16 ? SLA_LINEAR_BWD(f16) : SLA_LINEAR_BWD(bf16);
+#undef SLA_LINEAR_BWD
+}
+
+}  // extern "C"

@@ -41,7 +41,11 @@ enum Epilogue {
   kStore,     // c = sum (+ bias), or the float32 sums of one split of k
   kGate,      // columns of g and u side by side: h = act(g) u; u act'(g) and act(g) kept for kGateBack
   kGateBack,  // sum = dh: dg = dh (u act'(g)), du = dh act(g)
+  kLinear,    // c = act(sum + bias) + residual; act'(sum + bias) kept
 };
+// Whether an epilogue writes the caller's array straight from the registers.
+template <int EPI>
+inline constexpr bool kPlainStore = EPI == kStore || EPI == kLinear;
 
 constexpr int kBand = 8;
 constexpr int kMaxSegments = 2;
@@ -76,6 +80,9 @@ struct ProductArgs {
   uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
   int64_t ldg, sheet;        // elements between rows and between sheets of h
   float *sums;               // kGateBack: [m / 32][2][ldg] sums of dg and du over 32 rows, or NULL
+  const void *residual;      // kLinear: T [m][ldr], or NULL; act'(sum + bias) goes to g, T [m][ldg], unless that is NULL
+  int64_t ldr;
+  int residual_vec;          // rows of the residual are aligned to 32 bytes
 };
 
 // Up to three products that do not depend on one another, with one tile shape (kStore; one product else).
@@ -131,7 +138,7 @@ struct ProductShape {
   // a warp's boxes: 16-bit data two, which it uses again and again; float32 two of factors and three of h, or
   // three each of dg and du
   static constexpr int box = 32 * kStoreColumns<T, EPI, BN> * 2;
-  static constexpr int warp_boxes = EPI == kStore      ? 32 * kRowBytes<T, BN>
+  static constexpr int warp_boxes = kPlainStore<EPI>   ? 32 * kRowBytes<T, BN>
                                     : sizeof(T) == 2   ? 2 * box
                                     : EPI == kGate     ? 7 * box
                                                        : 6 * box;
@@ -265,6 +272,41 @@ __device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count
   load_row<T, N>(bias, b, count, vec);
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] += b[i];
+}
+
+// v = act(v) + the residual's N values of a row (asked for first); act'(v) is kept in g, whose rows are whole sectors.
+template <typename T, int N>
+__device__ __forceinline__ void finish_linear(const ProductArgs &p, int64_t row, int col, float (&v)[N], int count) {
+  constexpr bool sectors = N * sizeof(T) % 32 == 0;
+  float r[N];
+  if (p.residual) {
+    const T *from = (const T *)p.residual + row * p.ldr + col;
+    if constexpr (sectors) {
+      load_row<T, N>(from, r, count, p.residual_vec);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = i < count ? to_f32(from[i]) : 0.f;
+    }
+  }
+  if (p.act != SLA_ACT_NONE) {
+    float da[N];
+    if (p.g) {
+      with_activation(p.act, [&](auto act) { activate<act.value, true, N>(v, da); });
+      T *to = (T *)p.g + row * p.ldg + col;
+      if constexpr (sectors) {
+        store_row<T, N>(to, da, count, true);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (i < count) to[i] = from_f32<T>(da[i]);
+      }
+    } else {
+      with_activation(p.act, [&](auto act) { activate<act.value, false, N>(v, da); });
+    }
+  }
+  if (p.residual)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += r[i];
 }
 
 // Column sums of a tile of 32 rows (thread = row) and N = 16 or 32 columns: lane c gets column c's (N =
@@ -690,13 +732,13 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
 // kStore: straight from the registers, since TMA may not be able to write the caller's arrays.  Rows that are
 // not aligned to whole sectors would take a store an element, each to 32 lines: they go through shared
 // memory, so that a warp's stores run along the rows (2049 x 131 outputs: 16 -> 10 us).
-template <typename T, int CG, int BN>
+template <typename T, int EPI, int CG, int BN>
 __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t tmem, uint8_t *boxes,
                                                uint64_t *acc_full, uint64_t *acc_empty, volatile uint32_t *dead, int worker, int workers,
                                                uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
-  constexpr int width = kWarpColumns<T, kStore, BN>, N = kTurnColumns<T, BN>, pitch = kRowBytes<T, BN>;
+  constexpr int width = kWarpColumns<T, EPI, BN>, N = kTurnColumns<T, BN>, pitch = kRowBytes<T, BN>;
   uint8_t *mine = boxes + (warp - 2) * 32 * pitch;
   constexpr bool f32 = sizeof(T) == 4;
   float *run = f32 ? l.runs + ((int64_t)blockIdx.x * 4 + quarter) * 32 * BN + lane * 4 : nullptr;
@@ -704,8 +746,8 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
   for (int tile = team;; tile += kTeams<T, BN>, seq += kTeams<T, BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
-    const ProductArgs &p = l.p[product_of(l, item)];
-    const Tile t = tile_of<kStore, CG, BN>(p, item);
+    const ProductArgs &p = l.p[EPI == kStore ? product_of(l, item) : 0];
+    const Tile t = tile_of<EPI, CG, BN>(p, item);
     int runs = 1;
     if constexpr (f32) {
       runs = (steps_of(p, t.split) + kRun<T> - 1) / kRun<T>;
@@ -743,6 +785,7 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
           store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
         } else {
           if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
+          if constexpr (EPI == kLinear) finish_linear<T, N>(p, row, col, v, count);
           if (p.vec && count >= N) store_row<T, N>((T *)p.c + o, v, count, true);
         }
       }
@@ -943,10 +986,10 @@ __global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
       mbar_wait_clocks(drained, 0);
     }
   } else if (warp >= 2) {
-    if constexpr (EPI != kStore)
+    if constexpr (!kPlainStore<EPI>)
       tma_epilogue<T, EPI, CG, BN>(l, tmem, boxes, acc_full, acc_empty, dead, worker, workers, rank);
     else
-      store_epilogue<T, CG, BN>(l, tmem, boxes, acc_full, acc_empty, dead, worker, workers, rank);
+      store_epilogue<T, EPI, CG, BN>(l, tmem, boxes, acc_full, acc_empty, dead, worker, workers, rank);
   }
   __syncwarp();
   tc_fence_before();

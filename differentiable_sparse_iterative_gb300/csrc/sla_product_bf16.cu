@@ -10,13 +10,16 @@ cudaError_t launch_product<bf16>(int epi, int shape, int blocks, const ProductLa
   switch (epi) {
     case kStore: return launch_product_shape<bf16, kStore>(shape, blocks, l, early, st);
     case kGate: return launch_product_shape<bf16, kGate>(shape, blocks, l, early, st);
+    case kLinear: return launch_product_shape<bf16, kLinear>(shape, blocks, l, early, st);
     default: return launch_product_shape<bf16, kGateBack>(shape, blocks, l, early, st);
   }
 }
 
 template <>
 cudaError_t launch_few<bf16>(Epilogue epi, const FewArgs &p, cudaStream_t st) {
-  return epi == kGate ? launch_few_gate<bf16, true>(p, st) : launch_few_gate<bf16, false>(p, st);
+  return epi == kGate     ? launch_few_as<bf16, kGate>(p, st)
+         : epi == kLinear ? launch_few_as<bf16, kLinear>(p, st)
+                          : launch_few_as<bf16, kStore>(p, st);
 }
 
 template <>

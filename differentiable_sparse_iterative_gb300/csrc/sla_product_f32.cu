@@ -9,13 +9,16 @@ cudaError_t launch_product<float>(int epi, int shape, int blocks, const ProductL
   switch (epi) {
     case kStore: return launch_product_shape<float, kStore>(shape, blocks, l, early, st);
     case kGate: return launch_product_shape<float, kGate>(shape, blocks, l, early, st);
+    case kLinear: return launch_product_shape<float, kLinear>(shape, blocks, l, early, st);
     default: return launch_product_shape<float, kGateBack>(shape, blocks, l, early, st);
   }
 }
 
 template <>
 cudaError_t launch_few<float>(Epilogue epi, const FewArgs &p, cudaStream_t st) {
-  return epi == kGate ? launch_few_gate<float, true>(p, st) : launch_few_gate<float, false>(p, st);
+  return epi == kGate     ? launch_few_as<float, kGate>(p, st)
+         : epi == kLinear ? launch_few_as<float, kLinear>(p, st)
+                          : launch_few_as<float, kStore>(p, st);
 }
 
 }  // namespace sla

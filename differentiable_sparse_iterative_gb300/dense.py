@@ -430,6 +430,134 @@ def residual_norm(block: torch.Tensor, z: torch.Tensor, gate: Optional[torch.Ten
                              post_weight, post_bias, weight, bias, **how)
 
 
+# --------------------------------------------------------------------------- linear layer
+
+LINEAR_ACTIVATIONS = {"none": _abi.SLA_ACT_NONE, **ACTIVATIONS}
+
+
+class _LinearSizes:
+    def __init__(self, tokens, width, out, dt, act):
+        self.descriptor = _abi.sla_layer(tokens, width, out, dt, act)
+        self.ref = ctypes.byref(self.descriptor)
+        self.out = out
+        self.key = (tokens, width, out, dt, act)
+        lib = _lib()
+        self.saved = lib.sla_linear_saved_bytes(self.ref)
+        self.forward = lib.sla_linear_workspace_bytes(self.ref)
+        self.backward = lib.sla_linear_backward_workspace_bytes(self.ref)
+
+
+@functools.lru_cache(maxsize=512)
+def _linear_sizes(tokens, width, out, dt, act, device) -> _LinearSizes:
+    return _LinearSizes(tokens, width, out, dt, act)
+
+
+def _linear(x, weight, activation):
+    """(sizes, address of x, its leading dimension, address of the weight)"""
+    ptr, rows, ldx = _rows(x, "x")
+    act = _choice(activation, LINEAR_ACTIVATIONS, "activation")
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [out, width], got {tuple(weight.shape)}")
+    out, width, index = weight.size(0), x.size(-1), x.get_device()
+    f = _linear_sizes(rows, width, out, _type(x, "x"), act, index)
+    return f, ptr, ldx, _param(weight, "weight", (out, width), x.dtype, index)
+
+
+@_on_device_of_first
+def sla_linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, activation: str = "none", y: Optional[torch.Tensor] = None,
+               save: bool = False, workspace: Optional[torch.Tensor] = None):
+    """y = act(x weight^T + bias) + residual (asynchronous).
+
+    weight is [out, width], bias [out], residual of y's shape; activation: "none", "silu", "gelu", "gelu_tanh" or
+    "relu".  Returns y, or with save=True (y, saved): the byte buffer of intermediates that sla_linear_backward takes."""
+    f, ptr, ldx, wp = _linear(x, weight, activation)
+    dt, dev, index = x.dtype, x.device, x.get_device()
+    bp = _param(bias, "bias", (f.out,), dt, index)
+    shape = x.shape[:-1] + (f.out,)
+    rp, ldr = None, 0
+    if residual is not None:
+        if residual.shape != shape:
+            raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
+        rp, _, ldr = _rows(residual, "residual", x)
+    if y is None:
+        y = _empty(shape, dtype=dt, device=dev)
+        yp = y.data_ptr()
+    else:
+        yp = _param(y, "y", shape, dt, index)
+    saved, sp, sn = None, None, 0
+    if save:
+        saved, sn = _scratch(f.saved, dev, None)
+        saved.made_for = f.key
+        sp = saved.data_ptr()
+    wsp, nbytes = None, 0
+    if f.forward:
+        ws, nbytes = _scratch(f.forward, dev, workspace)
+        wsp = ws.data_ptr()
+    _check(_lib().sla_linear(f.ref, ptr, ldx, wp, bp, rp, ldr, yp, sp, sn, wsp, nbytes, _stream(index)), "sla_linear")
+    return (y, saved) if save else y
+
+
+@_on_device_of_first
+def sla_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, saved: torch.Tensor,
+                        activation: str = "none", want_grad_x: bool = True, want_grad_weight: bool = True,
+                        want_grad_bias: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Gradients of sla_linear (asynchronous): (dx, dweight, dbias), None where not wanted; the residual's is dy.  x, the
+    weight, the activation and `saved` are the forward call's."""
+    f, ptr, ldx, wp = _linear(x, weight, activation)
+    gptr, _, lddy = _rows(dy, "dy", x)
+    if dy.shape != x.shape[:-1] + (f.out,):
+        raise ValueError(f"dy must have shape {tuple(x.shape[:-1]) + (f.out,)}, got {tuple(dy.shape)}")
+    if saved.dtype != torch.uint8 or saved.get_device() != x.get_device() or not saved.is_contiguous():
+        raise ValueError("saved must be the buffer that sla_linear(..., save=True) returned")
+    # a copy of the buffer has lost the note of what it was made for, but not its size
+    if getattr(saved, "made_for", f.key) != f.key or saved.numel() > max(f.saved, 256):
+        raise ValueError("saved is from a forward call of other sizes, another type or another activation")
+    dt, dev = x.dtype, x.device
+    dx = _empty(x.shape, dtype=dt, device=dev) if want_grad_x else None
+    dw = _empty(weight.shape, dtype=dt, device=dev) if want_grad_weight else None
+    db = _empty(f.out, dtype=dt, device=dev) if want_grad_bias else None
+    ws, nbytes = _scratch(f.backward, dev, workspace)
+    _check(_lib().sla_linear_backward(f.ref, gptr, lddy, ptr, ldx, wp, saved.data_ptr(), saved.numel(),
+                                      *[None if t is None else t.data_ptr() for t in (dx, dw, db)], ws.data_ptr(), nbytes,
+                                      _stream(x.get_device())), "sla_linear_backward")
+    return dx, dw, db
+
+
+class Linear(torch.autograd.Function):
+    """y = act(x weight^T + bias) + residual.  Saved for backward: x, the weight, act'(x weight^T + bias) where there is an
+    activation, and the copies that were laid out anew for the tensor core (float32, or a width that 8 does not divide)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation):
+        x, weight = _matrix_ready(x), weight.contiguous()
+        residual = None if residual is None else _matrix_ready(residual)
+        y, saved = sla_linear(x, weight, bias, residual, activation=activation, save=True)
+        ctx.save_for_backward(x, weight, saved)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, saved = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if any(need[:3]):
+            dx, dw, db = sla_linear_backward(_matrix_ready(dy), x, weight, saved, activation=ctx.activation,
+                                             want_grad_x=need[0], want_grad_weight=need[1], want_grad_bias=need[2])
+        return dx, dw, db, dy if need[3] else None, None
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           residual: Optional[torch.Tensor] = None, activation: str = "none") -> torch.Tensor:
+    """Differentiable linear layer (gradients flow to x, the weight, the bias and the residual)."""
+    if _wants_grad(x, weight, bias, residual):
+        return Linear.apply(x, weight, bias, residual, activation)
+    return sla_linear(_matrix_ready(x), weight.contiguous(), bias, None if residual is None else _matrix_ready(residual),
+                      activation=activation)
+
+
 # --------------------------------------------------------------------------- gated feed-forward block
 
 def _ffn(x, w_in, w_out, activation):

@@ -543,7 +543,8 @@ typedef enum sla_act {
   SLA_ACT_SILU = 0,       /* g / (1 + exp(-g)) */
   SLA_ACT_GELU = 1,       /* g Phi(g), Phi the normal distribution function */
   SLA_ACT_GELU_TANH = 2,  /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
-  SLA_ACT_RELU = 3        /* max(g, 0), derivative 0 at 0 */
+  SLA_ACT_RELU = 3,       /* max(g, 0), derivative 0 at 0 */
+  SLA_ACT_NONE = 4        /* g: for a linear layer only */
 } sla_act;
 
 /* A gated feed-forward block: width -> 2 x hidden -> out, over `tokens` rows. */
@@ -592,6 +593,46 @@ SLA_API sla_status sla_gated_ffn_backward(const sla_ffn *f, const void *dy, int6
                                           const void *w_in, const void *w_out, const void *saved, size_t saved_bytes,
                                           void *dx, void *dw_in, void *dw_out, void *db_in, void *db_out,
                                           void *workspace, size_t ws_bytes, void *stream);
+
+/* A linear layer: width -> out, over `tokens` rows. */
+typedef struct sla_layer {
+  int64_t tokens;         /* rows of x, 0 <= tokens <= 2^30 */
+  int64_t width;          /* columns of x, 1 .. 2^24, as out */
+  int64_t out;            /* columns of y */
+  int32_t dtype;          /* SLA_F32, SLA_F16 or SLA_BF16, of every array */
+  int32_t activation;     /* sla_act, or SLA_ACT_NONE */
+} sla_layer;
+
+/* Bytes of the buffer that carries a forward call's intermediates to its backward call (0 where there are none: 16-bit data, no
+   activation and a width that 8 divides), and of the scratch of the two calls (0 for invalid arguments). */
+SLA_API size_t sla_linear_saved_bytes(const sla_layer *f);
+SLA_API size_t sla_linear_workspace_bytes(const sla_layer *f);
+SLA_API size_t sla_linear_backward_workspace_bytes(const sla_layer *f);
+
+/*
+ *   p = x weight^T + bias,  y = act(p) + residual
+ *   weight    device, [out][width];  bias [out] or NULL
+ *   residual  device, [tokens][out] with leading dimension ldr, or NULL
+ *   y         device, [tokens][out]
+ *   saved     device, sla_linear_saved_bytes, 256-byte aligned, or NULL: kept for the backward call (act'(p), in dtype,
+ *             and packed copies)
+ *   workspace device, sla_linear_workspace_bytes, 256-byte aligned
+ * Sums run in float32, the products of float32 data are float32's (as in sla_gated_ffn, whose bounded waits these
+ * calls share), and y is rounded once.  y may not overlap what is read.
+ */
+SLA_API sla_status sla_linear(const sla_layer *f, const void *x, int64_t ldx, const void *weight, const void *bias,
+                              const void *residual, int64_t ldr, void *y, void *saved, size_t saved_bytes,
+                              void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients for an upstream gradient dy [tokens][out] (lddy): with dp = dy act'(p), dx = dp weight [tokens][width],
+ * dweight = dp^T x [out][width], dbias = sum dp [out], each NULL when not wanted (the residual's is dy).  x, the weight and `saved`
+ * are the forward call's.  With 16-bit data act'(p) and dp are rounded to dtype before the products, dbias sums dp
+ * unrounded.  tokens = 0 sets dweight and dbias to zero.
+ */
+SLA_API sla_status sla_linear_backward(const sla_layer *f, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                       const void *weight, const void *saved, size_t saved_bytes, void *dx,
+                                       void *dweight, void *dbias, void *workspace, size_t ws_bytes, void *stream);
 
 /* Norms of a residual norm, and what becomes of its gate. */
 typedef enum sla_norm {
