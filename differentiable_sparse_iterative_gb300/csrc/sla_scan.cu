@@ -8,8 +8,8 @@
 // again from x and g, from float32 states that the forward call leaves every kRows rows: an eighth of what reading h
 // in 16 bits would cost, and exact).  To read everything once with the rows in parallel, a block
 // takes a tile of rows by kCols channels into registers, kRows rows a warp, two channels a lane, and goes
-// over them twice: once for the map (B, H) from the state before the rows to the state behind them,
-// s -> (1 - B) s + H, and, when that state is known, once for the results.  In between the maps of the block's warps
+// over them twice: once for the map (A, H) from the state before the rows to the state behind them,
+// s -> A s + H, and, when that state is known, once for the results.  In between the maps of the block's warps
 // are joined in shared memory, the block's is published, and the state before the tile is put together from
 // the maps of the tiles before it, back to the tile in which the sequence starts or the last of the states that
 // every kSpan-th tile publishes.  Tiles are handed out in order of time by a counter, so those waited for are
@@ -18,11 +18,13 @@
 // A map's two float32 are published as one 64-bit word, so that the word itself says whether it is there (the
 // workspace is set to ones, a NaN that no map has): no flag, no fence.
 //
-// Rounding.  Of a and 1 - a the smaller is kept (with the gate's sign), and a step is written as h + (1 - a)(x - h) or
-// x + a (h - x): with a rounded to float32 a constant gate close to 1 would lose 2^-25 / (1 - a) of the result, the same way
-// in every step.  For the same reason maps carry B = 1 - (product of a).  A sequence's start is a map with B = kCut, whose
-// H replaces what came before, whatever that is: an infinity or a NaN stays within its sequence (and makes NaN of what follows
-// it there).
+// A step is h' = x + a (h - x), so that a's rounding never makes a and 1 - a sum up to something else than one; where
+// 1 - a itself is a factor of a result it is e a with e = exp(-g), right relative to itself.  A sequence's start is a map
+// with A = kCut, whose H replaces what came before, whatever that is: an infinity or a NaN stays within its sequence.
+//
+// What costs is instructions as much as bytes (two special functions an element and some twenty other
+// instructions), so rows are walked with running pointers, and warps whose rows hold no sequence's start or end, nearly
+// all where sequences are long, take a copy of the loops without those checks.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,7 +42,7 @@ constexpr int kRows = 16;     // of a warp; the distance of the saved states
 constexpr int kCols = 64;     // channels of a tile, two a lane
 constexpr int kSpan = 64;     // tiles between published states
 constexpr int kForwardWarps = 16, kBackwardWarps = 8;
-constexpr float kCut = 2.f;
+constexpr float kCut = -1.f;
 constexpr long long kScanClocks = 4000000000ll;  // about two seconds
 constexpr uint64_t kAbsent = ~0ull;
 
@@ -56,7 +58,6 @@ struct ScanArgs {
   Sequences q;
   int channels, groups;  // groups of kCols channels
   int outside;           // rows outside of all sequences become zero
-  int vec;               // two channels may be moved at once
   const void *x, *g, *dh;
   int64_t ldx, ldg, lddh;
   void *out0, *out1;     // h; or dx and dg
@@ -130,24 +131,34 @@ __device__ __forceinline__ RowInfo rows_info(const Sequences &q, int64_t i0, int
   return f;
 }
 
-// Two channels of a row.
-template <typename T>
-struct Two {
+// A lane's two channels: neighbours where every row's pairs are aligned (Pair), else 32 apart, so that a warp's
+// accesses stay whole.
+template <typename T, bool Pair>
+struct Lane {
   using Raw = typename std::conditional<sizeof(T) == 4, float2, uint32_t>::type;
-  static __device__ __forceinline__ Raw zero() {
+  static constexpr int apart = Pair ? 1 : 32;
+  int c;          // the first channel
+  bool on0, on1;  // whether there are such channels
+  __device__ __forceinline__ Lane(int group, int lane, int channels)
+      : c(group * kCols + (Pair ? 2 * lane : lane)), on0(c < channels), on1(c + apart < channels) {}
+  static __device__ __forceinline__ Raw none() {
     if constexpr (sizeof(T) == 4)
       return f2(0.f, 0.f);
     else
       return 0u;
   }
-  static __device__ __forceinline__ Raw load(const T *p, int count, bool vec) {
-    if (vec) return count > 0 ? *reinterpret_cast<const Raw *>(p) : zero();
-    const T none = from_f32<T>(0.f);
-    const T a = count > 0 ? p[0] : none, b = count > 1 ? p[1] : none;
-    if constexpr (sizeof(T) == 4)
-      return f2(a, b);
-    else
-      return *reinterpret_cast<const uint16_t *>(&a) | ((uint32_t) * reinterpret_cast<const uint16_t *>(&b) << 16);
+  // p: the first channel's place
+  __device__ __forceinline__ Raw load(const T *p) const {
+    if constexpr (Pair) {
+      return on0 ? *reinterpret_cast<const Raw *>(p) : none();
+    } else {
+      const T zero = from_f32<T>(0.f);
+      const T a = on0 ? p[0] : zero, b = on1 ? p[apart] : zero;
+      if constexpr (sizeof(T) == 4)
+        return f2(a, b);
+      else
+        return *reinterpret_cast<const uint16_t *>(&a) | ((uint32_t) * reinterpret_cast<const uint16_t *>(&b) << 16);
+    }
   }
   static __device__ __forceinline__ float2 values(Raw r) {
     if constexpr (sizeof(T) == 4)
@@ -155,85 +166,86 @@ struct Two {
     else
       return unpair16(r, T{});
   }
-  static __device__ __forceinline__ void store(T *p, float2 v, int count, bool vec) {
-    if (vec) {
-      if (count <= 0) return;
+  __device__ __forceinline__ void store(T *p, float2 v) const {
+    if constexpr (Pair) {
+      if (!on0) return;
       if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float2 *>(p) = v;
       else
         *reinterpret_cast<uint32_t *>(p) = pair16(v.x, v.y, T{});
     } else {
-      if (count > 0) p[0] = from_f32<T>(v.x);
-      if (count > 1) p[1] = from_f32<T>(v.y);
+      if (on0) p[0] = from_f32<T>(v.x);
+      if (on1) p[apart] = from_f32<T>(v.y);
     }
   }
-};
-
-__device__ __forceinline__ bool below(float s) { return __float_as_int(s) < 0; }
-
-// The smaller of a and 1 - a, with the gate's sign: positive where it is 1 - a.
-template <bool Exact>
-__device__ __forceinline__ float small_side(float g) {
-  const float m = fabsf(g) * -1.4426950408889634f;
-  float e = ex2_approx(m);
-  // the rounding of the exponent, which the exponential multiplies (log2 e = 1.44269502... + 1.92596303e-8)
-  if constexpr (Exact) {
-    const float rest = fmaf(fabsf(g), -1.4426950408889634f, -m) + fabsf(g) * -1.92596303e-8f;
-    e = fmaf(e * 0.6931471805599453f, rest, e);
-    e = fabsf(g) > 88.f ? 0.f : e;  // an infinity's rest is no number
+  // float32 states, [rows][channels]
+  __device__ __forceinline__ float2 state(const float *p, int64_t row, int channels) const {
+    p += row * channels + c;
+    return f2(on0 ? p[0] : 0.f, on1 ? p[apart] : 0.f);
   }
-  return copysignf(e * rcp_approx(1.f + e), g);
-}
-
-// One step of h, and of B (which is h for x = 1 from 0).
-__device__ __forceinline__ float step(float h, float x, float s) { return fmaf(s, x - h, below(s) ? x : h); }
-__device__ __forceinline__ float2 step(float2 h, float2 x, float2 s) {
-  const float2 d = add2(x, f2(-h.x, -h.y));
-  return fma2(s, d, f2(below(s.x) ? x.x : h.x, below(s.y) ? x.y : h.y));
-}
-// One step of the gradient's message a l.
-__device__ __forceinline__ float2 message(float2 l, float2 s) {
-  return fma2(f2(-s.x, -s.y), l, f2(below(s.x) ? 0.f : l.x, below(s.y) ? 0.f : l.y));
-}
-
-// s -> (1 - b) s + h of two channels; b = kCut: s -> h.
-struct Map {
-  float2 b, h;
+  __device__ __forceinline__ void put_state(float *p, int64_t row, int channels, float2 v) const {
+    p += row * channels + c;
+    if (on0) p[0] = v.x;
+    if (on1) p[apart] = v.y;
+  }
 };
 
-__device__ __forceinline__ float apply(float b, float h, float s) { return b == kCut ? h : fmaf(-b, s, s) + h; }
-__device__ __forceinline__ float2 apply(const Map &m, float2 s) {
-  return f2(apply(m.b.x, m.h.x, s.x), apply(m.b.y, m.h.y, s.y));
-}
-__device__ __forceinline__ void join(float &b, float &h, float b2, float h2) {  // (b, h) first
-  h = apply(b2, h2, h);
-  b = b2 == kCut || b == kCut ? kCut : fmaf(b2, 1.f - b, b);
-}
-__device__ __forceinline__ void join(Map &m, const Map &n) {
-  join(m.b.x, m.h.x, n.b.x, n.h.x);
-  join(m.b.y, m.h.y, n.b.y, n.h.y);
+// The smaller of two, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-__device__ __forceinline__ uint64_t word_of(float b, float h) {
-  const uint64_t w = (uint64_t)__float_as_uint(h) << 32 | __float_as_uint(b);
+// e = exp(-g) (at most 2^126, so that nothing below is infinite) and a = 1 / (1 + e).
+__device__ __forceinline__ float2 exp_minus(float2 g) {
+  const float2 m = mul2(g, f2(-1.4426950408889634f, -1.4426950408889634f));
+  return f2(ex2_approx(min_nan(m.x, 126.f)), ex2_approx(min_nan(m.y, 126.f)));
+}
+__device__ __forceinline__ float2 keep_of(float2 e) {
+  const float2 d = add2(e, f2(1.f, 1.f));
+  return f2(rcp_approx(d.x), rcp_approx(d.y));
+}
+
+// One step of h.
+__device__ __forceinline__ float2 step(float2 h, float2 x, float2 a) { return fma2(a, add2(h, f2(-x.x, -x.y)), x); }
+
+// s -> a s + h of two channels; a = kCut: s -> h.
+struct Map {
+  float2 a, h;
+};
+
+__device__ __forceinline__ float2 apply(const Map &m, float2 s) {
+  const float2 r = fma2(m.a, s, m.h);
+  return m.a.x == kCut ? m.h : r;
+}
+__device__ __forceinline__ void join(Map &m, const Map &n) {  // m first
+  m.h = apply(n, m.h);
+  const float2 a = mul2(m.a, n.a);
+  const bool cut = m.a.x == kCut || n.a.x == kCut;
+  m.a = cut ? f2(kCut, kCut) : a;
+}
+
+__device__ __forceinline__ uint64_t word_of(float a, float h) {
+  const uint64_t w = (uint64_t)__float_as_uint(h) << 32 | __float_as_uint(a);
   return w == kAbsent ? 0x7fffffff7fffffffull : w;  // both are NaN: another one
 }
 __device__ __forceinline__ void publish(uint64_t *p, const Map &m) {
-  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(word_of(m.b.x, m.h.x)),
-               "l"(word_of(m.b.y, m.h.y))
+  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(word_of(m.a.x, m.h.x)),
+               "l"(word_of(m.a.y, m.h.y))
                : "memory");
 }
 __device__ __forceinline__ bool look(const uint64_t *p, Map &m) {
   uint64_t a, b;
   asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p) : "memory");
-  m.b = f2(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)b));
+  m.a = f2(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)b));
   m.h = f2(__uint_as_float((uint32_t)(a >> 32)), __uint_as_float((uint32_t)(b >> 32)));
   return a != kAbsent && b != kAbsent;
 }
 
-// Waits until all lanes' words are there.  False: they never came.
-__device__ __forceinline__ bool wait_for(const uint64_t *p, Map &m) {
-  if (__all_sync(0xffffffffu, look(p, m))) return true;
+// Looks until all lanes' words are there (`there`: what a first look found).  False: they never came.
+__device__ __forceinline__ bool wait_for(const uint64_t *p, Map &m, bool there) {
+  if (__all_sync(0xffffffffu, there)) return true;
   const long long t0 = clock64();
   for (;;) {
     if (__all_sync(0xffffffffu, look(p, m))) return true;
@@ -241,38 +253,25 @@ __device__ __forceinline__ bool wait_for(const uint64_t *p, Map &m) {
   }
 }
 
-__device__ __forceinline__ void copy_async(void *dst, const void *src, bool eight) {
-  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-  if (eight)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async(float *dst, const float *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
 }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Asks for the rows of `from` ([count][channels] float32) that belong to the sequences of the marked rows: to lane's
-// two places of row r of `to` ([kRows][kCols]), from where the lane itself reads them.
-__device__ __forceinline__ void ask_states(float *to, const float *from, uint32_t marks, int seq, int channels, int c,
+// Asks for the rows of `from` ([count][channels] float32) that belong to the sequences of the marked rows: to the lane's
+// two places of row r of `to` ([kRows][32] pairs), which the lane itself reads.
+template <typename L>
+__device__ __forceinline__ void ask_states(float2 *to, const float *from, uint32_t marks, int seq, int channels, const L &l,
                                            int lane) {
-  const bool both = channels % 2 == 0 && ((uintptr_t)from & 7) == 0;
   for (uint32_t m = marks; m; m &= m - 1) {
     const int r = __ffs(m) - 1;
     const int64_t s = __shfl_sync(0xffffffffu, seq, r);
-    const float *p = from + s * channels + c;
-    float *d = to + r * kCols + 2 * lane;
-    if (both) {
-      if (c < channels) copy_async(d, p, true);
-    } else {
-      if (c < channels) copy_async(d, p, false);
-      if (c + 1 < channels) copy_async(d + 1, p + 1, false);
-    }
+    const float *p = from + s * channels + l.c;
+    float *d = &to[r * 32 + lane].x;
+    if (l.on0) copy_async(d, p);
+    if (l.on1) copy_async(d + 1, p + L::apart);
   }
-}
-
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-__device__ __forceinline__ void put_state(float *to, int64_t s, int channels, int c, float2 v) {
-  if (c < channels) to[s * channels + c] = v.x;
-  if (c + 1 < channels) to[s * channels + c + 1] = v.y;
 }
 
 // The tile a block works on, and the maps of its warps.
@@ -284,66 +283,69 @@ struct TileMemory {
   uint32_t next;
 };
 
-// The state before the tile: what comes from the tiles before it, in the order of time.  `first` is the
-// tile where the present sequence starts.  All warps take part; afterwards (and a barrier) carry holds maps of which the
-// first `parts` are joined in order.
-template <int Warps>
-__device__ __forceinline__ int look_back(const ScanArgs &p, TileMemory<Warps> &sm, int tile, int group, int first,
-                                         int warp, int lane) {
-  const int base = tile / kSpan * kSpan, lo = max(first, base);
-  const bool known = first < base;  // the state before `base` is needed
-  const int count = tile - lo, per = (count + Warps - 1) / Warps;
-  const int from = lo + warp * per, to = min(tile, from + per);
-  bool ok = true;
-  Map m{f2(0.f, 0.f), f2(0.f, 0.f)};
-  if (warp == 0 && known)
-    ok = wait_for(p.states + ((int64_t)(base / kSpan - 1) * p.groups + group) * kCols + 2 * lane, m);
-  for (int i = from; i < to; ++i) {
-    Map n;
-    ok = wait_for(p.maps + ((int64_t)i * p.groups + group) * kCols + 2 * lane, n) && ok;
-    join(m, n);
-  }
-  sm.carry[warp][lane] = m;
-  if (!ok && lane == 0) atomicAdd_system(p.timeouts, 1u);
-  return per ? (count + per - 1) / per : 1;
-}
-
-// Joins the maps of the block's warps up to `warps`.
-template <int Warps>
-__device__ __forceinline__ Map joined(const TileMemory<Warps> &sm, int warps, int lane) {
-  Map m = sm.maps[0][lane];
-  for (int w = 1; w < warps; ++w) join(m, sm.maps[w][lane]);
-  return m;
-}
-
-// Publishes the tile's map, finds the state before it, publishes the state behind it where others look for it, and
-// returns the state before this warp's rows.  maps are in place (and a barrier behind them).
+// The state before this warp's rows.  maps are in place (and a barrier behind them); `own` is this warp's; i0: the scan's
+// index of the tile's first row.  On the way the tile's map is published, the state before the tile found, back from the
+// tile where the present sequence starts or the last published state, in the order of time, and the state
+// behind the tile published where others look for it.
 template <int Warps, bool Chain>
 __device__ __forceinline__ float2 state_before(const ScanArgs &p, TileMemory<Warps> &sm, int tile, int group, int64_t i0,
-                                               int warp, int lane) {
+                                               Map own, int warp, int lane) {
   float2 s = f2(0.f, 0.f);
-  if constexpr (Chain) {
+  Map before{f2(1.f, 1.f), f2(0.f, 0.f)};  // of the warps before this one
+  if constexpr (!Chain) {
+#pragma unroll 4
+    for (int w = 0; w < warp; ++w) join(before, sm.maps[w][lane]);
+    return apply(before, s);
+  } else {
     const int64_t origin = sm.origin;  // i0: nothing before the tile matters
     const bool needed = origin < i0;
-    Map own;
+    const int first = (int)(origin / (Warps * kRows)), base = tile / kSpan * kSpan, lo = max(first, base);
+    const bool known = first < base;  // the state before `base` is needed
+    const int count = needed ? tile - lo : 0, per = (count + Warps - 1) / Warps;
+    const int from = lo + warp * per, to = min(lo + count, from + per);
+    const int64_t apart = (int64_t)p.groups * kCols;
+    const uint64_t *at = p.maps + from * apart + group * kCols + 2 * lane;
+    Map n;
+    bool there = true;  // the first look is under way while the maps of the block are joined
+    if (from < to) there = look(at, n);
+#pragma unroll 4
+    for (int w = 0; w < warp; ++w) join(before, sm.maps[w][lane]);
     if (warp == Warps - 1) {
-      own = joined<Warps>(sm, Warps, lane);
-      publish(p.maps + ((int64_t)tile * p.groups + group) * kCols + 2 * lane, own);
+      Map all = before;
+      join(all, own);
+      publish(p.maps + tile * apart + group * kCols + 2 * lane, all);
+      own = all;
     }
-    int parts = 0;
-    if (needed) parts = look_back<Warps>(p, sm, tile, group, (int)(origin / (Warps * kRows)), warp, lane);
-    __syncthreads();
-    for (int w = 0; w < parts; ++w) s = apply(sm.carry[w][lane], s);
+    if (needed) {
+      Map m{f2(1.f, 1.f), f2(0.f, 0.f)};
+      bool ok = true;
+      if (warp == 0 && known) {
+        Map k;
+        const uint64_t *q = p.states + (base / kSpan - 1) * apart + group * kCols + 2 * lane;
+        ok = wait_for(q, k, look(q, k));
+        m = k;
+      }
+      for (int i = from; i < to; ++i, at += apart) {
+        if (i > from) there = look(at, n);
+        ok = wait_for(at, n, there) && ok;
+        join(m, n);
+      }
+      sm.carry[warp][lane] = m;
+      if (!ok && lane == 0) atomicAdd_system(p.timeouts, 1u);
+      __syncthreads();
+      const int parts = per ? (count + per - 1) / per : 1;
+#pragma unroll 4
+      for (int w = 0; w < parts; ++w) s = apply(sm.carry[w][lane], s);
+    }
     if (warp == Warps - 1 && (tile + 1) % kSpan == 0) {
       const Map behind{f2(kCut, kCut), apply(own, s)};
-      publish(p.states + ((int64_t)(tile / kSpan) * p.groups + group) * kCols + 2 * lane, behind);
+      publish(p.states + (tile / kSpan) * apart + group * kCols + 2 * lane, behind);
     }
+    return apply(before, s);
   }
-  for (int w = 0; w < warp; ++w) s = apply(sm.maps[w][lane], s);
-  return s;
 }
 
-// The next tile of the launch (of all groups), for all threads of the block.
+// The block's first tile of the launch (of all groups), for all its threads.
 template <int Warps, bool Chain>
 __device__ __forceinline__ uint32_t first_tile(const ScanArgs &p, TileMemory<Warps> &sm) {
   if constexpr (!Chain) return blockIdx.x;
@@ -352,66 +354,84 @@ __device__ __forceinline__ uint32_t first_tile(const ScanArgs &p, TileMemory<War
   return sm.next;
 }
 
-template <typename T, bool Chain>
+template <typename T, bool Chain, bool Pair>
 __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) == 2 ? 2 : 1) scan_forward(const __grid_constant__ ScanArgs p) {
   constexpr int W = kForwardWarps;
-  using Raw = typename Two<T>::Raw;
-  extern __shared__ float dynamic[];  // [W][kRows][kCols] states of the sequences that start in the tile
+  using L = Lane<T, Pair>;
+  extern __shared__ float2 dynamic[];  // [W][kRows][32] states of the sequences that start in the tile
   __shared__ TileMemory<W> sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float *starts = dynamic + warp * kRows * kCols;
+  float2 *starts = dynamic + warp * kRows * 32;
   const uint32_t all = (uint32_t)p.tiles * (uint32_t)p.groups;
+  const int64_t dir = p.q.reverse ? -1 : 1;
   uint32_t id = first_tile<W, Chain>(p, sm);
   while (id < all) {
     const int tile = id / (uint32_t)p.groups, group = id - tile * p.groups;
     const int64_t t0 = (int64_t)tile * W * kRows, i0 = t0 + warp * kRows;
-    const int c = group * kCols + 2 * lane, count = p.channels - c;
-    const int64_t row0 = row_of(p.q, i0), dir = p.q.reverse ? -1 : 1;
+    const L l(group, lane, p.channels);
+    const int64_t row0 = row_of(p.q, i0);
+    const int left = (int)min((int64_t)kRows, p.q.rows - i0);
     uint32_t ahead = 0;
     if (Chain && threadIdx.x == 0) ahead = atomicAdd(p.counter, 1u) + 1u;
-    Raw xr[kRows], gr[kRows];
+    typename L::Raw xr[kRows], gr[kRows];
+    {
+      const T *px = (const T *)p.x + row0 * p.ldx + l.c, *pg = (const T *)p.g + row0 * p.ldg + l.c;
+      const int64_t sx = dir * p.ldx, sg = dir * p.ldg;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      xr[r] = gr[r] = Two<T>::zero();
-      if (i0 + r < p.q.rows) {
-        const int64_t row = row0 + r * dir;
-        gr[r] = Two<T>::load((const T *)p.g + row * p.ldg + c, count, p.vec);
-        xr[r] = Two<T>::load((const T *)p.x + row * p.ldx + c, count, p.vec);
+      for (int r = 0; r < kRows; ++r, px += sx, pg += sg) {
+        xr[r] = gr[r] = L::none();
+        if (r < left) {
+          gr[r] = l.load(pg);
+          xr[r] = l.load(px);
+        }
       }
     }
     const RowInfo f = rows_info(p.q, i0, lane);
+    const bool inner = f.live == (1u << kRows) - 1 && !f.first && !f.last;
     if (Chain && threadIdx.x == 0) sm.origin = f.live & 1 ? f.origin : t0;
-    if (p.state) {
-      ask_states(starts, p.state, f.first, f.seq, p.channels, c, lane);
-    }
-    float2 s[kRows];
+    if (p.state && f.first) ask_states(starts, p.state, f.first, f.seq, p.channels, l, lane);
+    float2 a[kRows];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const float2 g = Two<T>::values(gr[r]);
-      s[r] = f2(small_side<sizeof(T) == 4>(g.x), small_side<sizeof(T) == 4>(g.y));
-    }
-    copies_done();
-    Map m{f2(0.f, 0.f), f2(0.f, 0.f)};
+    for (int r = 0; r < kRows; ++r) a[r] = keep_of(exp_minus(L::values(gr[r])));
+    Map m{f2(1.f, 1.f), f2(0.f, 0.f)};
+    auto start = [&](int r) { return p.state ? starts[r * 32 + lane] : f2(0.f, 0.f); };
+    if (inner) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (f.first >> r & 1) m.h = p.state ? *reinterpret_cast<float2 *>(starts + r * kCols + 2 * lane) : f2(0.f, 0.f);
-      m.h = step(m.h, Two<T>::values(xr[r]), s[r]);
-      m.b = step(m.b, f2(1.f, 1.f), s[r]);
+      for (int r = 0; r < kRows; ++r) {
+        m.h = step(m.h, L::values(xr[r]), a[r]);
+        m.a = mul2(m.a, a[r]);
+      }
+    } else {
+      copies_done();
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (f.first >> r & 1) m.h = start(r);
+        m.h = step(m.h, L::values(xr[r]), a[r]);
+        m.a = mul2(m.a, a[r]);
+      }
+      if (f.first) m.a = f2(kCut, kCut);
     }
-    if (f.first) m.b = f2(kCut, kCut);
     sm.maps[warp][lane] = m;
     __syncthreads();
-    float2 h = state_before<W, Chain>(p, sm, tile, group, t0, warp, lane);
-    if (p.saved && i0 < p.q.rows) put_state(p.saved, i0 / kRows, p.channels, c, h);
+    float2 h = state_before<W, Chain>(p, sm, tile, group, t0, m, warp, lane);
+    if (p.saved && left > 0) l.put_state(p.saved, i0 / kRows, p.channels, h);
+    T *po = (T *)p.out0 + row0 * p.channels + l.c;
+    const int64_t so = dir * p.channels;
+    if (inner) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (f.first >> r & 1) h = p.state ? *reinterpret_cast<float2 *>(starts + r * kCols + 2 * lane) : f2(0.f, 0.f);
-      h = step(h, Two<T>::values(xr[r]), s[r]);
-      const bool live = f.live >> r & 1;
-      if (live || (p.outside && i0 + r < p.q.rows))
-        Two<T>::store((T *)p.out0 + (row0 + r * dir) * p.channels + c, live ? h : f2(0.f, 0.f), count,
-                      p.vec);
-      if (p.end && (f.last >> r & 1)) put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, c, h);
+      for (int r = 0; r < kRows; ++r, po += so) {
+        h = step(h, L::values(xr[r]), a[r]);
+        l.store(po, h);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r, po += so) {
+        if (f.first >> r & 1) h = start(r);
+        h = step(h, L::values(xr[r]), a[r]);
+        const bool live = f.live >> r & 1;
+        if (live || (p.outside && r < left)) l.store(po, live ? h : f2(0.f, 0.f));
+        if (p.end && (f.last >> r & 1)) l.put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, h);
+      }
     }
     if (Chain && threadIdx.x == 0) sm.next = ahead;
     __syncthreads();  // everything in shared memory has been read
@@ -419,91 +439,115 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) == 2 ? 2 : 1) sc
   }
 }
 
-template <typename T, bool Chain>
+template <typename T, bool Chain, bool Pair>
 __global__ void __launch_bounds__(32 * kBackwardWarps, 2) scan_backward(const __grid_constant__ ScanArgs p) {
   constexpr int W = kBackwardWarps;
-  using Raw = typename Two<T>::Raw;
-  extern __shared__ float dynamic[];  // [W][2][kRows][kCols]: states where sequences start, dfinal where they end
+  using L = Lane<T, Pair>;
+  extern __shared__ float2 dynamic[];  // [W][2][kRows][32]: states where sequences start, dfinal where they end
   __shared__ TileMemory<W> sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float *starts = dynamic + warp * 2 * kRows * kCols, *ends = starts + kRows * kCols;
+  float2 *starts = dynamic + warp * 2 * kRows * 32, *ends = starts + kRows * 32;
   const uint32_t all = (uint32_t)p.tiles * (uint32_t)p.groups;
+  const int64_t dir = p.q.reverse ? -1 : 1;
   uint32_t id = first_tile<W, Chain>(p, sm);
   while (id < all) {
     // time runs backwards: tile 0 holds the last rows and warp 0 the last of a tile
     const int tile = id / (uint32_t)p.groups, group = id - tile * p.groups;
+    const int64_t t0 = (int64_t)tile * W * kRows;
     const int64_t i0 = ((int64_t)(p.tiles - 1 - tile) * W + (W - 1 - warp)) * kRows;
-    const int c = group * kCols + 2 * lane, count = p.channels - c;
-    const int64_t row0 = row_of(p.q, i0), dir = p.q.reverse ? -1 : 1;
+    const L l(group, lane, p.channels);
+    const int64_t row0 = row_of(p.q, i0);
+    const int left = (int)max(min((int64_t)kRows, p.q.rows - i0), (int64_t)0);
     uint32_t ahead = 0;
     if (Chain && threadIdx.x == 0) ahead = atomicAdd(p.counter, 1u) + 1u;
-    Raw xr[kRows], gr[kRows], dr[kRows];
+    typename L::Raw xr[kRows], gr[kRows], dr[kRows];
+    {
+      const T *px = (const T *)p.x + row0 * p.ldx + l.c, *pg = (const T *)p.g + row0 * p.ldg + l.c;
+      const T *pd = (const T *)p.dh + row0 * p.lddh + l.c;
+      const int64_t sx = dir * p.ldx, sg = dir * p.ldg, sd = dir * p.lddh;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      xr[r] = gr[r] = dr[r] = Two<T>::zero();
-      if (i0 + r < p.q.rows) {
-        const int64_t row = row0 + r * dir;
-        gr[r] = Two<T>::load((const T *)p.g + row * p.ldg + c, count, p.vec);
-        xr[r] = Two<T>::load((const T *)p.x + row * p.ldx + c, count, p.vec);
-        if (p.dh) dr[r] = Two<T>::load((const T *)p.dh + row * p.lddh + c, count, p.vec);
+      for (int r = 0; r < kRows; ++r, px += sx, pg += sg, pd += sd) {
+        xr[r] = gr[r] = dr[r] = L::none();
+        if (r < left) {
+          gr[r] = l.load(pg);
+          xr[r] = l.load(px);
+          if (p.dh) dr[r] = l.load(pd);
+        }
       }
     }
-    float2 h = f2(0.f, 0.f);
-    if (i0 < p.q.rows) {
-      const float *from = p.saved + i0 / kRows * p.channels + c;
-      if (count > 0) h.x = from[0];
-      if (count > 1) h.y = from[1];
-    }
+    float2 h = left > 0 ? l.state(p.saved, i0 / kRows, p.channels) : f2(0.f, 0.f);
     const RowInfo f = rows_info(p.q, i0, lane);
-    if (p.state) ask_states(starts, p.state, f.first, f.seq, p.channels, c, lane);
-    if (p.dfinal) ask_states(ends, p.dfinal, f.last, f.seq, p.channels, c, lane);
+    const bool inner = f.live == (1u << kRows) - 1 && !f.first && !f.last;
+    if (p.state && f.first) ask_states(starts, p.state, f.first, f.seq, p.channels, l, lane);
+    if (p.dfinal && f.last) ask_states(ends, p.dfinal, f.last, f.seq, p.channels, l, lane);
     if (Chain) {
       // the row behind which the present sequence ends, counted backwards from the end of the last tile
       const int64_t span = (int64_t)p.tiles * W * kRows;
       const int64_t until = __shfl_sync(0xffffffffu, f.until, kRows - 1);
-      if (threadIdx.x == 0) sm.origin = f.live >> (kRows - 1) & 1 ? span - until : (int64_t)tile * W * kRows;
+      if (threadIdx.x == 0) sm.origin = f.live >> (kRows - 1) & 1 ? span - until : t0;
     }
-    float2 s[kRows];
+    float2 a[kRows], e[kRows];  // e: h_{t-1} - x_t
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const float2 g = Two<T>::values(gr[r]);
-      s[r] = f2(small_side<sizeof(T) == 4>(g.x), small_side<sizeof(T) == 4>(g.y));
-    }
-    copies_done();
-    float2 e[kRows];  // h_{t-1} - x_t
+    for (int r = 0; r < kRows; ++r) a[r] = keep_of(exp_minus(L::values(gr[r])));
+    auto start = [&](int r) { return p.state ? starts[r * 32 + lane] : f2(0.f, 0.f); };
+    auto end = [&](int r) { return p.dfinal ? ends[r * 32 + lane] : f2(0.f, 0.f); };
+    Map m{f2(1.f, 1.f), f2(0.f, 0.f)};
+    if (inner) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (f.first >> r & 1) h = p.state ? *reinterpret_cast<float2 *>(starts + r * kCols + 2 * lane) : f2(0.f, 0.f);
-      const float2 x = Two<T>::values(xr[r]);
-      e[r] = add2(h, f2(-x.x, -x.y));
-      h = fma2(f2(-s[r].x, -s[r].y), e[r], f2(below(s[r].x) ? x.x : h.x, below(s[r].y) ? x.y : h.y));
-    }
-    Map m{f2(0.f, 0.f), f2(0.f, 0.f)};
+      for (int r = 0; r < kRows; ++r) {
+        const float2 x = L::values(xr[r]);
+        e[r] = add2(h, f2(-x.x, -x.y));
+        h = fma2(a[r], e[r], x);
+      }
 #pragma unroll
-    for (int r = kRows - 1; r >= 0; --r) {
-      if (f.last >> r & 1) m.h = p.dfinal ? *reinterpret_cast<float2 *>(ends + r * kCols + 2 * lane) : f2(0.f, 0.f);
-      m.h = message(add2(Two<T>::values(dr[r]), m.h), s[r]);
-      m.b = step(m.b, f2(1.f, 1.f), s[r]);
+      for (int r = kRows - 1; r >= 0; --r) {
+        m.h = mul2(a[r], add2(L::values(dr[r]), m.h));
+        m.a = mul2(m.a, a[r]);
+      }
+    } else {
+      copies_done();
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (f.first >> r & 1) h = start(r);
+        const float2 x = L::values(xr[r]);
+        e[r] = add2(h, f2(-x.x, -x.y));
+        h = fma2(a[r], e[r], x);
+      }
+#pragma unroll
+      for (int r = kRows - 1; r >= 0; --r) {
+        if (f.last >> r & 1) m.h = end(r);
+        m.h = mul2(a[r], add2(L::values(dr[r]), m.h));
+        m.a = mul2(m.a, a[r]);
+      }
+      if (f.last) m.a = f2(kCut, kCut);
     }
-    if (f.last) m.b = f2(kCut, kCut);
     sm.maps[warp][lane] = m;
     __syncthreads();
-    float2 carry = state_before<W, Chain>(p, sm, tile, group, (int64_t)tile * W * kRows, warp, lane);
+    float2 carry = state_before<W, Chain>(p, sm, tile, group, t0, m, warp, lane);
+    const int64_t so = dir * p.channels, o = (row0 + (kRows - 1) * dir) * p.channels + l.c;
+    T *px = (T *)p.out0 + o, *pg = (T *)p.out1 + o;
+    auto results = [&](int r, float2 lam, bool live) {
+      const float2 b = mul2(exp_minus(L::values(gr[r])), a[r]);  // 1 - a
+      const float2 none = f2(0.f, 0.f);
+      if (p.out0) l.store(px, live ? mul2(b, lam) : none);
+      if (p.out1) l.store(pg, live ? mul2(mul2(lam, e[r]), mul2(a[r], b)) : none);
+    };
+    if (inner) {
 #pragma unroll
-    for (int r = kRows - 1; r >= 0; --r) {
-      if (f.last >> r & 1) carry = p.dfinal ? *reinterpret_cast<float2 *>(ends + r * kCols + 2 * lane) : f2(0.f, 0.f);
-      const float2 l = add2(Two<T>::values(dr[r]), carry);
-      carry = message(l, s[r]);
-      const bool live = f.live >> r & 1;
-      if (i0 + r < p.q.rows) {
-        const float2 a = f2(fabsf(s[r].x), fabsf(s[r].y)), b = add2(f2(1.f, 1.f), f2(-a.x, -a.y));
-        const float2 in = f2(below(s[r].x) ? b.x : a.x, below(s[r].y) ? b.y : a.y);  // 1 - a
-        const int64_t at = (row0 + r * dir) * p.channels + c;
-        const float2 none = f2(0.f, 0.f);
-        if (p.out0) Two<T>::store((T *)p.out0 + at, live ? mul2(in, l) : none, count, p.vec);
-        if (p.out1) Two<T>::store((T *)p.out1 + at, live ? mul2(mul2(l, e[r]), mul2(a, b)) : none, count, p.vec);
+      for (int r = kRows - 1; r >= 0; --r, px -= so, pg -= so) {
+        const float2 lam = add2(L::values(dr[r]), carry);
+        carry = mul2(a[r], lam);
+        results(r, lam, true);
       }
-      if (p.end && (f.first >> r & 1)) put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, c, carry);
+    } else {
+#pragma unroll
+      for (int r = kRows - 1; r >= 0; --r, px -= so, pg -= so) {
+        if (f.last >> r & 1) carry = end(r);
+        const float2 lam = add2(L::values(dr[r]), carry);
+        carry = mul2(a[r], lam);
+        if (r < left) results(r, lam, f.live >> r & 1);
+        if (p.end && (f.first >> r & 1)) l.put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, carry);
+      }
     }
     if (Chain && threadIdx.x == 0) sm.next = ahead;
     __syncthreads();
@@ -512,21 +556,19 @@ __global__ void __launch_bounds__(32 * kBackwardWarps, 2) scan_backward(const __
 }
 
 // Sequences of one row: nothing to scan.  Two channels a thread.
-template <typename T>
+template <typename T, bool Pair>
 __global__ void __launch_bounds__(256) scan_single(const __grid_constant__ ScanArgs p) {
-  const int64_t pairs = (p.channels + 1) / 2, total = p.q.rows * pairs;
-  const bool both = p.channels % 2 == 0 && ((uintptr_t)p.state & 7) == 0 && ((uintptr_t)p.end & 7) == 0;
+  using L = Lane<T, Pair>;
+  const int64_t total = p.q.rows * p.groups * 32;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t row = i / pairs;
-    const int c = (int)(i - row * pairs) * 2, count = p.channels - c;
-    const float2 g = Two<T>::values(Two<T>::load((const T *)p.g + row * p.ldg + c, count, p.vec));
-    const float2 x = Two<T>::values(Two<T>::load((const T *)p.x + row * p.ldx + c, count, p.vec));
-    const int64_t at = row * p.channels + c;
-    float2 h = f2(0.f, 0.f);
-    if (p.state) h = Two<float>::load(p.state + at, count, both);
-    h = step(h, x, f2(small_side<sizeof(T) == 4>(g.x), small_side<sizeof(T) == 4>(g.y)));
-    Two<T>::store((T *)p.out0 + at, h, count, p.vec);
-    if (p.end) Two<float>::store(p.end + at, h, count, both);
+    const int64_t rg = i >> 5, row = rg / p.groups;
+    const L l((int)(rg - row * p.groups), (int)(i & 31), p.channels);
+    const float2 g = L::values(l.load((const T *)p.g + row * p.ldg + l.c));
+    const float2 x = L::values(l.load((const T *)p.x + row * p.ldx + l.c));
+    float2 h = p.state ? l.state(p.state, row, p.channels) : f2(0.f, 0.f);
+    h = step(h, x, keep_of(exp_minus(g)));
+    l.store((T *)p.out0 + row * p.channels + l.c, h);
+    if (p.end) l.put_state(p.end, row, p.channels, h);
   }
 }
 
@@ -595,7 +637,7 @@ ScanArgs scan_args(const sla_scan *s, int warps, void *ws) {
   return p;
 }
 
-// Whether two neighbouring channels of every row may be moved at once.
+// Whether every row's pairs of channels may be moved at once.
 bool pairs_aligned(const sla_scan *s, const void *p, int64_t ld) {
   return aligned(p, 2 * net_size(s->dtype)) && (s->rows == 1 || ld % 2 == 0);
 }
@@ -609,19 +651,34 @@ cudaError_t launch(K kernel, const ScanArgs &p, int block, size_t smem, int resi
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool Pair>
 cudaError_t run_forward(const ScanArgs &p, bool chain, cudaStream_t st) {
+  if (p.q.length == 1 && !p.saved) {
+    const int64_t threads = p.q.rows * p.groups * 32;
+    scan_single<T, Pair><<<(unsigned)std::min<int64_t>((threads + 255) / 256, sm_count() * 8), 256, 0, st>>>(p);
+    return cudaGetLastError();
+  }
   const size_t smem = p.state ? kForwardWarps * kRows * kCols * sizeof(float) : 0;
   constexpr int resident = sizeof(T) == 2 ? 2 : 1;
-  return chain ? launch(scan_forward<T, true>, p, 32 * kForwardWarps, smem, resident, st)
-               : launch(scan_forward<T, false>, p, 32 * kForwardWarps, smem, resident, st);
+  return chain ? launch(scan_forward<T, true, Pair>, p, 32 * kForwardWarps, smem, resident, st)
+               : launch(scan_forward<T, false, Pair>, p, 32 * kForwardWarps, smem, resident, st);
 }
 
-template <typename T>
+template <typename T, bool Pair>
 cudaError_t run_backward(const ScanArgs &p, bool chain, cudaStream_t st) {
   const size_t smem = p.state || p.dfinal ? kBackwardWarps * 2 * kRows * kCols * sizeof(float) : 0;
-  return chain ? launch(scan_backward<T, true>, p, 32 * kBackwardWarps, smem, 2, st)
-               : launch(scan_backward<T, false>, p, 32 * kBackwardWarps, smem, 2, st);
+  return chain ? launch(scan_backward<T, true, Pair>, p, 32 * kBackwardWarps, smem, 2, st)
+               : launch(scan_backward<T, false, Pair>, p, 32 * kBackwardWarps, smem, 2, st);
+}
+
+// Calls f with the element type and whether channels go in pairs.
+template <typename F>
+cudaError_t by_type(int32_t dtype, bool pairs, F &&f) {
+  using std::false_type;
+  using std::true_type;
+  if (dtype == SLA_F32) return pairs ? f(float{}, true_type{}) : f(float{}, false_type{});
+  if (dtype == SLA_F16) return pairs ? f(f16{}, true_type{}) : f(f16{}, false_type{});
+  return pairs ? f(bf16{}, true_type{}) : f(bf16{}, false_type{});
 }
 
 // `to` = `from`, or zero: what sequences without rows have.
@@ -667,26 +724,12 @@ SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx,
   ScanArgs p = scan_args(s, kForwardWarps, workspace);
   p.x = x, p.ldx = ldx, p.g = gate, p.ldg = ldg, p.state = state, p.out0 = h, p.end = final_state;
   p.saved = (float *)saved, p.timeouts = earlier.count;
-  p.vec = s->channels % 2 == 0 && pairs_aligned(s, x, ldx) && pairs_aligned(s, gate, ldg) &&
-          pairs_aligned(s, h, s->channels);
+  const bool pairs = s->channels % 2 == 0 && pairs_aligned(s, x, ldx) && pairs_aligned(s, gate, ldg) &&
+                     pairs_aligned(s, h, s->channels);
   const bool chain = need > 0;
   cudaError_t e = chain ? cudaMemsetAsync(workspace, 0xff, need, st) : cudaSuccess;
   if (e != cudaSuccess) return fail(e);
-  if (p.q.length == 1 && !saved) {
-    const int64_t pairs = p.q.rows * ((p.channels + 1) / 2);
-    const unsigned grid = (unsigned)std::min<int64_t>((pairs + 255) / 256, sm_count() * 8);
-    if (s->dtype == SLA_F32)
-      scan_single<float><<<grid, 256, 0, st>>>(p);
-    else if (s->dtype == SLA_F16)
-      scan_single<f16><<<grid, 256, 0, st>>>(p);
-    else
-      scan_single<bf16><<<grid, 256, 0, st>>>(p);
-    e = cudaGetLastError();
-  } else {
-    e = s->dtype == SLA_F32   ? run_forward<float>(p, chain, st)
-        : s->dtype == SLA_F16 ? run_forward<f16>(p, chain, st)
-                              : run_forward<bf16>(p, chain, st);
-  }
+  e = by_type(s->dtype, pairs, [&](auto t, auto pair) { return run_forward<decltype(t), decltype(pair)::value>(p, chain, st); });
   if (e != cudaSuccess) return fail(e);
   count_launches(1);
   return SLA_OK;
@@ -720,15 +763,13 @@ SLA_API sla_status sla_gated_scan_backward(const sla_scan *s, const void *dh, in
   p.dh = dh, p.lddh = lddh, p.x = x, p.ldx = ldx, p.g = gate, p.ldg = ldg, p.state = state, p.dfinal = dfinal;
   p.out0 = dx, p.out1 = dgate, p.end = dstate, p.saved = (float *)const_cast<void *>(saved);
   p.timeouts = earlier.count;
-  p.vec = s->channels % 2 == 0 && pairs_aligned(s, x, ldx) && pairs_aligned(s, gate, ldg) &&
-          (!dh || pairs_aligned(s, dh, lddh)) && pairs_aligned(s, dx, s->channels) &&
-          pairs_aligned(s, dgate, s->channels);
+  const bool pairs = s->channels % 2 == 0 && pairs_aligned(s, x, ldx) && pairs_aligned(s, gate, ldg) &&
+                     (!dh || pairs_aligned(s, dh, lddh)) && pairs_aligned(s, dx, s->channels) &&
+                     pairs_aligned(s, dgate, s->channels);
   const bool chain = need > 0;
   cudaError_t e = chain ? cudaMemsetAsync(workspace, 0xff, need, st) : cudaSuccess;
   if (e != cudaSuccess) return fail(e);
-  e = s->dtype == SLA_F32   ? run_backward<float>(p, chain, st)
-      : s->dtype == SLA_F16 ? run_backward<f16>(p, chain, st)
-                            : run_backward<bf16>(p, chain, st);
+  e = by_type(s->dtype, pairs, [&](auto t, auto pair) { return run_backward<decltype(t), decltype(pair)::value>(p, chain, st); });
   if (e != cudaSuccess) return fail(e);
   count_launches(1);
   return SLA_OK;
