@@ -371,8 +371,6 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) == 2 ? 2 : 1) sc
     const L l(group, lane, p.channels);
     const int64_t row0 = row_of(p.q, i0);
     const int left = (int)min((int64_t)kRows, p.q.rows - i0);
-    uint32_t ahead = 0;
-    if (Chain && threadIdx.x == 0) ahead = atomicAdd(p.counter, 1u) + 1u;
     typename L::Raw xr[kRows], gr[kRows];
     {
       const T *px = (const T *)p.x + row0 * p.ldx + l.c, *pg = (const T *)p.g + row0 * p.ldg + l.c;
@@ -414,6 +412,9 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) == 2 ? 2 : 1) sc
     sm.maps[warp][lane] = m;
     __syncthreads();
     float2 h = state_before<W, Chain>(p, sm, tile, group, t0, m, warp, lane);
+    // (taken no sooner: a tile that waits for its block's present one keeps all later ones waiting)
+    uint32_t ahead = 0;
+    if (Chain && threadIdx.x == 0) ahead = atomicAdd(p.counter, 1u) + 1u;
     if (p.saved && left > 0) l.put_state(p.saved, i0 / kRows, p.channels, h);
     T *po = (T *)p.out0 + row0 * p.channels + l.c;
     const int64_t so = dir * p.channels;
@@ -458,8 +459,6 @@ __global__ void __launch_bounds__(32 * kBackwardWarps, 2) scan_backward(const __
     const L l(group, lane, p.channels);
     const int64_t row0 = row_of(p.q, i0);
     const int left = (int)max(min((int64_t)kRows, p.q.rows - i0), (int64_t)0);
-    uint32_t ahead = 0;
-    if (Chain && threadIdx.x == 0) ahead = atomicAdd(p.counter, 1u) + 1u;
     typename L::Raw xr[kRows], gr[kRows], dr[kRows];
     {
       const T *px = (const T *)p.x + row0 * p.ldx + l.c, *pg = (const T *)p.g + row0 * p.ldg + l.c;
@@ -524,6 +523,8 @@ __global__ void __launch_bounds__(32 * kBackwardWarps, 2) scan_backward(const __
     sm.maps[warp][lane] = m;
     __syncthreads();
     float2 carry = state_before<W, Chain>(p, sm, tile, group, t0, m, warp, lane);
+    uint32_t ahead = 0;
+    if (Chain && threadIdx.x == 0) ahead = atomicAdd(p.counter, 1u) + 1u;
     const int64_t so = dir * p.channels, o = (row0 + (kRows - 1) * dir) * p.channels + l.c;
     T *px = (T *)p.out0 + o, *pg = (T *)p.out1 + o;
     auto results = [&](int r, float2 lam, bool live) {
