@@ -6,20 +6,26 @@
 //
 // Both are bound by memory: two reads and a write forward, three reads and two writes backward (h is formed
 // again from x and g, from float32 states that the forward call leaves every kRows rows: an eighth of what reading h
-// in 16 bits would cost, and exact).  To read everything once with the rows in parallel, a block
-// takes a tile of rows by kCols channels into registers, kRows rows a warp, two channels a lane, and goes
-// over them twice: once for the map (A, H) from the state before the rows to the state behind them,
-// s -> A s + H, and, when that state is known, once for the results.  In between the maps of the block's warps
-// are joined in shared memory, the block's is published, and the state before the tile is put together from
-// the maps of the tiles before it, back to the tile in which the sequence starts or the last of the states that
-// every kSpan-th tile publishes.  Tiles are handed out in order of time by a counter, so those waited for are
+// in 16 bits would cost, and exact).  To have the rows in parallel, they are taken in tiles of kTile rows by kCols channels,
+// kRows rows a warp, two channels a lane, and every tile twice: once for the map (A, H) from the state before it to the state
+// behind it, s -> A s + H, which is published, and once for the results, from the state before it, which is put together from the
+// maps of the tiles before it, back to the tile in which the sequence starts or the last of the states that
+// every kSpan-th tile publishes; every kFold-th tile publishes the map of its kFold tiles, so that at most 15 tiles, 15 folds
+// and a state are looked at.
+//
+// A block makes the map of its next tile before it looks back for the present one.  So nothing that waits keeps a map from being
+// published, all maps that are looked for are a tile's time old, and the second reading of a tile hits L2 (456 tiles of
+// 32 KB and as many ahead): memory sees one.  Made one after the other, from registers, with the next tile taken early or
+// late, the same tiles took 193 to 1000 us where they now take a third of that: one path of 1,000,000 rows waits from
+// state to state, and a tile that waits for its block keeps all later ones waiting.
+// Tiles are handed out in order of time by a counter, so those waited for are
 // always at work; which block takes which tile changes no result, and the maps are joined in a fixed order.
 //
 // A map's two float32 are published as one 64-bit word, so that the word itself says whether it is there (the
 // workspace is set to ones, a NaN that no map has): no flag, no fence.
 //
-// A step is h' = x + a (h - x), so that a's rounding never makes a and 1 - a sum up to something else than one; where
-// 1 - a itself is a factor of a result it is e a with e = exp(-g), right relative to itself.  A sequence's start is a map
+// A step is h' = a h + (x - a x), so that a's rounding never makes a and 1 - a sum up to something else than one; where
+// 1 - a itself is a factor of a result it is exp(-g) a, right relative to itself.  A sequence's start is a map
 // with A = kCut, whose H replaces what came before, whatever that is: an infinity or a NaN stays within its sequence.
 //
 // What costs is instructions as much as bytes (two special functions an element and some twenty other
@@ -40,8 +46,10 @@ namespace {
 
 constexpr int kRows = 16;     // of a warp; the distance of the saved states
 constexpr int kCols = 64;     // channels of a tile, two a lane
-constexpr int kSpan = 64;     // tiles between published states
-constexpr int kForwardWarps = 16, kBackwardWarps = 8;
+constexpr int kWarps = 8;     // of a block: a tile is kWarps kRows rows
+constexpr int kTile = kWarps * kRows;
+constexpr int kFold = 16;     // tiles whose maps the last of them joins to one
+constexpr int kSpan = 512;    // tiles between published states
 constexpr float kCut = -1.f;
 constexpr long long kScanClocks = 4000000000ll;  // about two seconds
 constexpr uint64_t kAbsent = ~0ull;
@@ -60,6 +68,7 @@ struct ScanArgs {
   int outside;           // rows outside of all sequences become zero
   const void *x, *g, *dh;
   int64_t ldx, ldg, lddh;
+  int bx, bg, bdh, bo;   // bytes from a row to the next in the scan's order; bo: of the results
   void *out0, *out1;     // h; or dx and dg
   const float *state;    // [count][channels] or NULL
   const float *dfinal;   // the same, backward
@@ -67,7 +76,8 @@ struct ScanArgs {
   float *saved;          // [rows / kRows][channels]: states before those rows
   int tiles;             // of a group
   uint32_t *counter;     // tiles taken so far, less one
-  uint64_t *maps, *states;  // [tiles][groups][kCols], [tiles / kSpan][groups][kCols]
+  // [tiles][groups][kCols], and of every kFold-th and every kSpan-th tile
+  uint64_t *maps, *folds, *states;
   uint32_t *timeouts;
 };
 
@@ -81,27 +91,52 @@ __device__ __forceinline__ int64_t offset_at(const Sequences &q, int64_t s) {
   return q.wide ? ((const int64_t *)q.offsets)[s] : ((const int32_t *)q.offsets)[s];
 }
 
-__device__ __forceinline__ Place place_of(const Sequences &q, int64_t row) {
+// The sequence of every lane's row; all lanes take part, and rows differ by less than 32.  With offsets: the last s with
+// offsets[s] <= the smallest row, by 33 parts at a time, and from there on through the next 31 offsets, and by halves where
+// they do not reach (many sequences without rows).
+__device__ __forceinline__ Place place_of(const Sequences &q, int64_t row, int lane) {
   Place p{-1, 0, 0};
-  if (row < 0 || row >= q.rows) return p;
+  const bool there = row >= 0 && row < q.rows;
   if (q.length) {
+    if (!there) return p;
     p.seq = (uint32_t)row / (uint32_t)q.length;
     p.begin = p.seq * q.length;
     p.end = p.begin + q.length;
     return p;
   }
-  int64_t lo = 0, hi = q.count;  // the last s in [0, count) with offsets[s] <= row
+  int64_t least = there ? row : q.rows;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) least = min(least, (int64_t)__shfl_xor_sync(0xffffffffu, least, o));
+  int64_t lo = 0, hi = q.count;  // how many s in [0, count) have offsets[s] <= least: in [lo, hi]
   while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (offset_at(q, mid) <= row)
-      lo = mid + 1;
-    else
-      hi = mid;
+    const int64_t step = (hi - lo + 32) / 33, at = lo + (lane + 1) * step - 1;
+    const int n = __popc(__ballot_sync(0xffffffffu, at < hi && offset_at(q, at) <= least));
+    hi = min(hi, lo + (n + 1) * step - 1);
+    lo = lo + n * step;
   }
-  if (lo == 0) return p;
+  // offsets[lo - 1] is the last; lane k has offsets[lo + k]
+  const int64_t next = lo + lane <= q.count ? offset_at(q, lo + lane) : INT64_MAX;
+  int n = 0;
+  for (int k = 0; k < 32; ++k) {
+    const int64_t v = __shfl_sync(0xffffffffu, next, k);
+    if (__all_sync(0xffffffffu, v > row || !there)) break;
+    n += v <= row && lo + k < q.count;
+  }
+  int64_t s = lo + n;
+  if (n == 32) {
+    int64_t top = q.count;
+    while (s < top) {
+      const int64_t mid = (s + top) >> 1;
+      if (offset_at(q, mid) <= row)
+        s = mid + 1;
+      else
+        top = mid;
+    }
+  }
+  if (s == 0 || !there) return p;
   // (offsets that are none may lie outside of the rows, or fall: no row is then taken to be in two places)
-  p.begin = max(offset_at(q, lo - 1), (int64_t)0), p.end = min(offset_at(q, lo), q.rows);
-  if (row >= p.begin && row < p.end) p.seq = (int)(lo - 1);
+  p.begin = max(offset_at(q, s - 1), (int64_t)0), p.end = min(offset_at(q, s), q.rows);
+  if (row >= p.begin && row < p.end) p.seq = (int)(s - 1);
   return p;
 }
 
@@ -119,8 +154,7 @@ struct RowInfo {
 __device__ __forceinline__ RowInfo rows_info(const Sequences &q, int64_t i0, int lane) {
   RowInfo f;
   const int64_t i = i0 + lane, row = row_of(q, i);
-  Place p{-1, 0, 0};
-  if (lane < kRows && i < q.rows) p = place_of(q, row);
+  const Place p = place_of(q, lane < kRows && i < q.rows ? row : -1, lane);
   const bool in = p.seq >= 0, at_begin = in && row == p.begin, at_end = in && row == p.end - 1;
   f.seq = p.seq;
   f.origin = q.reverse ? q.rows - p.end : p.begin;
@@ -137,10 +171,15 @@ template <typename T, bool Pair>
 struct Lane {
   using Raw = typename std::conditional<sizeof(T) == 4, float2, uint32_t>::type;
   static constexpr int apart = Pair ? 1 : 32;
-  int c;          // the first channel
+  int c;          // the first channel; a lane without one reads the row's first
+  int more;       // to the second, or to the first again
   bool on0, on1;  // whether there are such channels
-  __device__ __forceinline__ Lane(int group, int lane, int channels)
-      : c(group * kCols + (Pair ? 2 * lane : lane)), on0(c < channels), on1(c + apart < channels) {}
+  __device__ __forceinline__ Lane(int group, int lane, int channels) {
+    c = group * kCols + (Pair ? 2 * lane : lane);
+    on0 = c < channels, on1 = c + apart < channels;
+    if (!on0) c = 0;
+    more = on1 ? apart : 0;
+  }
   static __device__ __forceinline__ Raw none() {
     if constexpr (sizeof(T) == 4)
       return f2(0.f, 0.f);
@@ -150,10 +189,9 @@ struct Lane {
   // p: the first channel's place
   __device__ __forceinline__ Raw load(const T *p) const {
     if constexpr (Pair) {
-      return on0 ? *reinterpret_cast<const Raw *>(p) : none();
+      return *reinterpret_cast<const Raw *>(p);
     } else {
-      const T zero = from_f32<T>(0.f);
-      const T a = on0 ? p[0] : zero, b = on1 ? p[apart] : zero;
+      const T a = p[0], b = p[more];
       if constexpr (sizeof(T) == 4)
         return f2(a, b);
       else
@@ -190,25 +228,21 @@ struct Lane {
   }
 };
 
-// The smaller of two, NaN if either is.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
+// a = 1 / (1 + exp(-g)).
+__device__ __forceinline__ float keep(float g) { return rcp_approx(1.f + ex2_approx(g * -1.4426950408889634f)); }
+__device__ __forceinline__ float2 keep(float2 g) { return f2(keep(g.x), keep(g.y)); }
 
-// e = exp(-g) (at most 2^126, so that nothing below is infinite) and a = 1 / (1 + e).
-__device__ __forceinline__ float2 exp_minus(float2 g) {
-  const float2 m = mul2(g, f2(-1.4426950408889634f, -1.4426950408889634f));
-  return f2(ex2_approx(min_nan(m.x, 126.f)), ex2_approx(min_nan(m.y, 126.f)));
+// 1 - a, right relative to itself.
+__device__ __forceinline__ float drop(float g, float a) {
+  // exp(-g) a, but 1 where the exponential is infinite (a NaN remains one)
+  const float e = ex2_approx(g * -1.4426950408889634f);
+  return a == 0.f ? 1.f : e * a;
 }
-__device__ __forceinline__ float2 keep_of(float2 e) {
-  const float2 d = add2(e, f2(1.f, 1.f));
-  return f2(rcp_approx(d.x), rcp_approx(d.y));
-}
+__device__ __forceinline__ float2 drop(float2 g, float2 a) { return f2(drop(g.x, a.x), drop(g.y, a.y)); }
 
-// One step of h.
-__device__ __forceinline__ float2 step(float2 h, float2 x, float2 a) { return fma2(a, add2(h, f2(-x.x, -x.y)), x); }
+// One step of h: a h + (x - a x).
+__device__ __forceinline__ float step(float h, float x, float a) { return fmaf(a, h, fmaf(-a, x, x)); }
+__device__ __forceinline__ float2 step(float2 h, float2 x, float2 a) { return f2(step(h.x, x.x, a.x), step(h.y, x.y, a.y)); }
 
 // s -> a s + h of two channels; a = kCut: s -> h.
 struct Map {
@@ -248,6 +282,7 @@ __device__ __forceinline__ bool wait_for(const uint64_t *p, Map &m, bool there) 
   if (__all_sync(0xffffffffu, there)) return true;
   const long long t0 = clock64();
   for (;;) {
+    __nanosleep(100);  // many wait for the same words
     if (__all_sync(0xffffffffu, look(p, m))) return true;
     if (__any_sync(0xffffffffu, clock64() - t0 > kScanClocks)) return false;
   }
@@ -274,285 +309,320 @@ __device__ __forceinline__ void ask_states(float2 *to, const float *from, uint32
   }
 }
 
-// The tile a block works on, and the maps of its warps.
-template <int Warps>
+// What a block keeps of its tiles: of the present one, and of the next one or two.
 struct TileMemory {
-  Map maps[Warps][32];      // of the warps
-  Map carry[Warps][32];     // parts of the way from the known state to the tile
-  int64_t origin;           // the scan's index of the first row that the tile's first row depends on
+  Map maps[3][kWarps][32];  // of the warps
+  int64_t origin[3];        // the scan's index of the first row that the tile's first row depends on
+  Map carry[kWarps][32];    // parts of the way from the known state to the present tile: folds, then tiles
   uint32_t next;
 };
 
-// The state before this warp's rows.  maps are in place (and a barrier behind them); `own` is this warp's; i0: the scan's
-// index of the tile's first row.  On the way the tile's map is published, the state before the tile found, back from the
-// tile where the present sequence starts or the last published state, in the order of time, and the state
-// behind the tile published where others look for it.
-template <int Warps, bool Chain>
-__device__ __forceinline__ float2 state_before(const ScanArgs &p, TileMemory<Warps> &sm, int tile, int group, int64_t i0,
-                                               Map own, int warp, int lane) {
-  float2 s = f2(0.f, 0.f);
-  Map before{f2(1.f, 1.f), f2(0.f, 0.f)};  // of the warps before this one
-  if constexpr (!Chain) {
+__device__ __forceinline__ Map no_rows() { return {f2(1.f, 1.f), f2(0.f, 0.f)}; }
+
+__device__ __forceinline__ Map joined(const Map (*maps)[32], int from, int to, int lane) {
+  Map m = no_rows();
 #pragma unroll 4
-    for (int w = 0; w < warp; ++w) join(before, sm.maps[w][lane]);
-    return apply(before, s);
+  for (int w = from; w < to; ++w) join(m, maps[w][lane]);
+  return m;
+}
+
+// This warp's part of the way from the state before the tile's sequence, or span, to the tile.
+__device__ __forceinline__ Map look_back(const ScanArgs &p, int tile, int64_t origin, int64_t mine, int64_t apart, int warp,
+                                         int lane) {
+  Map m = no_rows();
+  const int first = (int)(origin / kTile), base = tile / kSpan * kSpan, fold = tile / kFold * kFold;
+  // half of the warps take the folds before the present one, half the tiles of the present one
+  constexpr int H = kWarps / 2;
+  const bool tiles = warp >= H;
+  const int lo = tiles ? max(first, fold) : max(first, base) / kFold, hi = tiles ? tile : fold / kFold;
+  const int per = (max(hi - lo, 0) + H - 1) / H, from = lo + (tiles ? warp - H : warp) * per, to = min(hi, from + per);
+  const uint64_t *at = (tiles ? p.maps : p.folds) + from * apart + mine;
+  bool ok = true;
+  if (warp == 0 && first < base) {
+    const uint64_t *q = p.states + (int64_t)(base / kSpan - 1) * apart + mine;
+    ok = wait_for(q, m, look(q, m));
+  }
+  for (int i = from; i < to; i += 2, at += 2 * apart) {
+    Map n, n2;
+    const bool two = i + 1 < to;
+    const bool there = look(at, n), there2 = !two || look(at + apart, n2);
+    ok = wait_for(at, n, there) && ok;
+    join(m, n);
+    if (two) {
+      ok = wait_for(at + apart, n2, there2) && ok;
+      join(m, n2);
+    }
+  }
+  if (!ok && lane == 0) atomicAdd_system(p.timeouts, 1u);
+  return m;
+}
+
+// Where a warp's rows of a tile lie, and what it knows of them.  Backward, tile 0 holds the last rows and warp 0 the last of
+// a tile.
+template <typename T, bool Pair, bool Backward>
+struct Rows {
+  Lane<T, Pair> l;
+  int tile, group, left;  // rows that there are
+  int64_t i0, row0;       // the scan's index of the first row, and its row
+  RowInfo f;
+  bool inner;             // all rows are in one sequence, and none is its first or last
+  __device__ __forceinline__ Rows(const ScanArgs &p, uint32_t id, int warp, int lane)
+      : l(id % (uint32_t)p.groups, lane, p.channels), tile(id / (uint32_t)p.groups), group(id % (uint32_t)p.groups) {
+    i0 = Backward ? ((int64_t)(p.tiles - 1 - tile) * kWarps + (kWarps - 1 - warp)) * kRows
+                  : (int64_t)tile * kTile + warp * kRows;
+    left = (int)max(min((int64_t)kRows, p.q.rows - i0), (int64_t)0);
+    row0 = row_of(p.q, i0);
+  }
+  // (apart from the constructor: the rows are asked for first)
+  __device__ __forceinline__ void inform(const Sequences &q, int lane) {
+    f = rows_info(q, i0, lane);
+    inner = f.live == (1u << kRows) - 1 && !f.first && !f.last;
+  }
+  // The first channel of the first row.
+  __device__ __forceinline__ const T *at(const void *base, int64_t ld) const { return (const T *)base + row0 * ld + l.c; }
+};
+
+// Loads a warp's rows, `step` bytes apart (one wide multiply-add an address).
+template <typename T, typename R, typename Raw>
+__device__ __forceinline__ void ask_rows(const R &t, const T *p, int step, Raw (&raw)[kRows]) {
+  const char *at = (const char *)p;
+  if (t.left == kRows) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) raw[r] = t.l.load((const T *)(at + (int64_t)step * r));
   } else {
-    const int64_t origin = sm.origin;  // i0: nothing before the tile matters
-    const bool needed = origin < i0;
-    const int first = (int)(origin / (Warps * kRows)), base = tile / kSpan * kSpan, lo = max(first, base);
-    const bool known = first < base;  // the state before `base` is needed
-    const int count = needed ? tile - lo : 0, per = (count + Warps - 1) / Warps;
-    const int from = lo + warp * per, to = min(lo + count, from + per);
-    const int64_t apart = (int64_t)p.groups * kCols;
-    const uint64_t *at = p.maps + from * apart + group * kCols + 2 * lane;
-    Map n;
-    bool there = true;  // the first look is under way while the maps of the block are joined
-    if (from < to) there = look(at, n);
-#pragma unroll 4
-    for (int w = 0; w < warp; ++w) join(before, sm.maps[w][lane]);
-    if (warp == Warps - 1) {
-      Map all = before;
-      join(all, own);
-      publish(p.maps + tile * apart + group * kCols + 2 * lane, all);
-      own = all;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      raw[r] = decltype(t.l)::none();
+      if (r < t.left) raw[r] = t.l.load((const T *)(at + (int64_t)step * r));
     }
-    if (needed) {
-      Map m{f2(1.f, 1.f), f2(0.f, 0.f)};
-      bool ok = true;
-      if (warp == 0 && known) {
-        Map k;
-        const uint64_t *q = p.states + (base / kSpan - 1) * apart + group * kCols + 2 * lane;
-        ok = wait_for(q, k, look(q, k));
-        m = k;
-      }
-      for (int i = from; i < to; ++i, at += apart) {
-        if (i > from) there = look(at, n);
-        ok = wait_for(at, n, there) && ok;
-        join(m, n);
-      }
-      sm.carry[warp][lane] = m;
-      if (!ok && lane == 0) atomicAdd_system(p.timeouts, 1u);
-      __syncthreads();
-      const int parts = per ? (count + per - 1) / per : 1;
-#pragma unroll 4
-      for (int w = 0; w < parts; ++w) s = apply(sm.carry[w][lane], s);
-    }
-    if (warp == Warps - 1 && (tile + 1) % kSpan == 0) {
-      const Map behind{f2(kCut, kCut), apply(own, s)};
-      publish(p.states + (tile / kSpan) * apart + group * kCols + 2 * lane, behind);
-    }
-    return apply(before, s);
   }
 }
 
-// The block's first tile of the launch (of all groups), for all its threads.
-template <int Warps, bool Chain>
-__device__ __forceinline__ uint32_t first_tile(const ScanArgs &p, TileMemory<Warps> &sm) {
-  if constexpr (!Chain) return blockIdx.x;
-  if (threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
+// The map of a warp's rows.  starts: [kRows][32], the lane's places for states (forward) or dfinal (backward).
+template <typename T, bool Pair, bool Backward>
+__device__ __forceinline__ Map map_rows(const ScanArgs &p, Rows<T, Pair, Backward> &t, float2 *starts, int lane) {
+  using L = Lane<T, Pair>;
+  typename L::Raw vr[kRows], gr[kRows];  // v: x, or dh
+  ask_rows<T>(t, t.at(p.g, p.ldg), p.bg, gr);
+  if (!Backward || p.dh) {
+    ask_rows<T>(t, t.at(Backward ? p.dh : p.x, Backward ? p.lddh : p.ldx), Backward ? p.bdh : p.bx, vr);
+  } else {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) vr[r] = L::none();
+  }
+  t.inform(p.q, lane);
+  const uint32_t cuts = Backward ? t.f.last : t.f.first;
+  const float *states = Backward ? p.dfinal : p.state;
+  Map m = no_rows();
+  auto go = [&](int r) {
+    const float2 a = keep(L::values(gr[r])), v = L::values(vr[r]);
+    m.h = Backward ? mul2(a, add2(v, m.h)) : step(m.h, v, a);
+    m.a = mul2(m.a, a);
+  };
+  if (!cuts) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) go(Backward ? kRows - 1 - r : r);
+    return m;
+  }
+  if (states) {
+    ask_states(starts, states, cuts, t.f.seq, p.channels, t.l, lane);
+    copies_done();
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = Backward ? kRows - 1 - k : k;
+    if (cuts >> r & 1) m.h = states ? starts[r * 32 + lane] : f2(0.f, 0.f);
+    go(r);
+  }
+  m.a = f2(kCut, kCut);
+  return m;
+}
+
+// Makes and publishes the map of a tile.  All threads take part; a barrier follows before anything is read from slot.
+template <typename T, bool Chain, bool Pair, bool Backward>
+__device__ __forceinline__ void map_tile(const ScanArgs &p, TileMemory &sm, uint32_t id, int slot, float2 *starts, int warp,
+                                         int lane) {
+  Rows<T, Pair, Backward> t(p, id, warp, lane);
+  sm.maps[slot][warp][lane] = map_rows<T, Pair, Backward>(p, t, starts, lane);
+  if (Chain && warp == 0) {
+    // Backward: the row behind which the present sequence ends, counted backwards from the end of the last tile.
+    const int64_t t0 = (int64_t)t.tile * kTile;
+    const int64_t until = (int64_t)p.tiles * kTile - __shfl_sync(0xffffffffu, t.f.until, kRows - 1);
+    if (lane == 0)
+      sm.origin[slot] = !(t.f.live >> (Backward ? kRows - 1 : 0) & 1) ? t0 : Backward ? until : t.f.origin;
+  }
   __syncthreads();
-  return sm.next;
+  if (Chain && warp == kWarps - 1)
+    publish(p.maps + ((int64_t)t.tile * p.groups + t.group) * kCols + 2 * lane, joined(sm.maps[slot], 0, kWarps, lane));
+}
+
+// The state before this warp's rows of the tile in slot; on the way, what others look for is published, and the block's
+// next tile taken.
+template <bool Chain>
+__device__ __forceinline__ float2 state_before(const ScanArgs &p, TileMemory &sm, int tile, int group, int slot, int warp,
+                                               int lane) {
+  float2 s = f2(0.f, 0.f);
+  const Map before = joined(sm.maps[slot], 0, warp, lane);
+  if constexpr (Chain) {
+    const int64_t apart = (int64_t)p.groups * kCols, mine = group * kCols + 2 * lane, origin = sm.origin[slot];
+    sm.carry[warp][lane] = origin < (int64_t)tile * kTile ? look_back(p, tile, origin, mine, apart, warp, lane) : no_rows();
+    Map own;
+    if ((tile + 1) % kFold == 0 && warp >= kWarps / 2) {
+      // as soon as the tiles' half is through, not waiting for the states that the others may wait for
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * (kWarps - kWarps / 2)) : "memory");
+      if (warp == kWarps - 1) {
+        own = before;
+        join(own, sm.maps[slot][kWarps - 1][lane]);
+        Map f = joined(sm.carry, kWarps / 2, kWarps, lane);
+        join(f, own);
+        publish(p.folds + (int64_t)(tile / kFold) * apart + mine, f);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s = apply(sm.carry[w][lane], s);
+    if (warp == kWarps - 1 && (tile + 1) % kSpan == 0)
+      publish(p.states + (int64_t)(tile / kSpan) * apart + mine, Map{f2(kCut, kCut), apply(own, s)});
+  }
+  return apply(before, s);
 }
 
 template <typename T, bool Chain, bool Pair>
-__global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) == 2 ? 2 : 1) scan_forward(const __grid_constant__ ScanArgs p) {
-  constexpr int W = kForwardWarps;
+__device__ __forceinline__ void results_forward(const ScanArgs &p, TileMemory &sm, uint32_t id, int slot, float2 *starts,
+                                                int warp, int lane) {
   using L = Lane<T, Pair>;
-  extern __shared__ float2 dynamic[];  // [W][kRows][32] states of the sequences that start in the tile
-  __shared__ TileMemory<W> sm;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float2 *starts = dynamic + warp * kRows * 32;
-  const uint32_t all = (uint32_t)p.tiles * (uint32_t)p.groups;
-  const int64_t dir = p.q.reverse ? -1 : 1;
-  uint32_t id = first_tile<W, Chain>(p, sm);
-  while (id < all) {
-    const int tile = id / (uint32_t)p.groups, group = id - tile * p.groups;
-    const int64_t t0 = (int64_t)tile * W * kRows, i0 = t0 + warp * kRows;
-    const L l(group, lane, p.channels);
-    const int64_t row0 = row_of(p.q, i0);
-    const int left = (int)min((int64_t)kRows, p.q.rows - i0);
-    typename L::Raw xr[kRows], gr[kRows];
-    {
-      const T *px = (const T *)p.x + row0 * p.ldx + l.c, *pg = (const T *)p.g + row0 * p.ldg + l.c;
-      const int64_t sx = dir * p.ldx, sg = dir * p.ldg;
+  Rows<T, Pair, false> t(p, id, warp, lane);
+  typename L::Raw xr[kRows], gr[kRows];
+  ask_rows<T>(t, t.at(p.g, p.ldg), p.bg, gr);
+  ask_rows<T>(t, t.at(p.x, p.ldx), p.bx, xr);
+  t.inform(p.q, lane);
+  if (p.state && t.f.first) ask_states(starts, p.state, t.f.first, t.f.seq, p.channels, t.l, lane);
+  float2 h = state_before<Chain>(p, sm, t.tile, t.group, slot, warp, lane);
+  if (p.saved && t.left > 0) t.l.put_state(p.saved, t.i0 / kRows, p.channels, h);
+  char *po = (char *)((T *)p.out0 + t.row0 * p.channels + t.l.c);
+  if (t.inner) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r, px += sx, pg += sg) {
-        xr[r] = gr[r] = L::none();
-        if (r < left) {
-          gr[r] = l.load(pg);
-          xr[r] = l.load(px);
-        }
-      }
+    for (int r = 0; r < kRows; ++r) {
+      h = step(h, L::values(xr[r]), keep(L::values(gr[r])));
+      t.l.store((T *)(po + (int64_t)p.bo * r), h);
     }
-    const RowInfo f = rows_info(p.q, i0, lane);
-    const bool inner = f.live == (1u << kRows) - 1 && !f.first && !f.last;
-    if (Chain && threadIdx.x == 0) sm.origin = f.live & 1 ? f.origin : t0;
-    if (p.state && f.first) ask_states(starts, p.state, f.first, f.seq, p.channels, l, lane);
-    float2 a[kRows];
+    return;
+  }
+  copies_done();
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) a[r] = keep_of(exp_minus(L::values(gr[r])));
-    Map m{f2(1.f, 1.f), f2(0.f, 0.f)};
-    auto start = [&](int r) { return p.state ? starts[r * 32 + lane] : f2(0.f, 0.f); };
-    if (inner) {
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        m.h = step(m.h, L::values(xr[r]), a[r]);
-        m.a = mul2(m.a, a[r]);
-      }
-    } else {
-      copies_done();
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (f.first >> r & 1) m.h = start(r);
-        m.h = step(m.h, L::values(xr[r]), a[r]);
-        m.a = mul2(m.a, a[r]);
-      }
-      if (f.first) m.a = f2(kCut, kCut);
-    }
-    sm.maps[warp][lane] = m;
-    __syncthreads();
-    float2 h = state_before<W, Chain>(p, sm, tile, group, t0, m, warp, lane);
-    // (taken no sooner: a tile that waits for its block's present one keeps all later ones waiting)
-    uint32_t ahead = 0;
-    if (Chain && threadIdx.x == 0) ahead = atomicAdd(p.counter, 1u) + 1u;
-    if (p.saved && left > 0) l.put_state(p.saved, i0 / kRows, p.channels, h);
-    T *po = (T *)p.out0 + row0 * p.channels + l.c;
-    const int64_t so = dir * p.channels;
-    if (inner) {
-#pragma unroll
-      for (int r = 0; r < kRows; ++r, po += so) {
-        h = step(h, L::values(xr[r]), a[r]);
-        l.store(po, h);
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < kRows; ++r, po += so) {
-        if (f.first >> r & 1) h = start(r);
-        h = step(h, L::values(xr[r]), a[r]);
-        const bool live = f.live >> r & 1;
-        if (live || (p.outside && r < left)) l.store(po, live ? h : f2(0.f, 0.f));
-        if (p.end && (f.last >> r & 1)) l.put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, h);
-      }
-    }
-    if (Chain && threadIdx.x == 0) sm.next = ahead;
-    __syncthreads();  // everything in shared memory has been read
-    id = Chain ? sm.next : id + gridDim.x;
+  for (int r = 0; r < kRows; ++r) {
+    if (t.f.first >> r & 1) h = p.state ? starts[r * 32 + lane] : f2(0.f, 0.f);
+    h = step(h, L::values(xr[r]), keep(L::values(gr[r])));
+    const bool live = t.f.live >> r & 1;
+    if (live || (p.outside && r < t.left)) t.l.store((T *)(po + (int64_t)p.bo * r), live ? h : f2(0.f, 0.f));
+    if (p.end && (t.f.last >> r & 1)) t.l.put_state(p.end, __shfl_sync(0xffffffffu, t.f.seq, r), p.channels, h);
   }
 }
 
 template <typename T, bool Chain, bool Pair>
-__global__ void __launch_bounds__(32 * kBackwardWarps, 2) scan_backward(const __grid_constant__ ScanArgs p) {
-  constexpr int W = kBackwardWarps;
+__device__ __forceinline__ void results_backward(const ScanArgs &p, TileMemory &sm, uint32_t id, int slot, float2 *starts,
+                                                 int warp, int lane) {
   using L = Lane<T, Pair>;
-  extern __shared__ float2 dynamic[];  // [W][2][kRows][32]: states where sequences start, dfinal where they end
-  __shared__ TileMemory<W> sm;
+  Rows<T, Pair, true> t(p, id, warp, lane);
+  float2 *ends = starts + kRows * 32;
+  typename L::Raw xr[kRows], gr[kRows], dr[kRows];
+  ask_rows<T>(t, t.at(p.g, p.ldg), p.bg, gr);
+  ask_rows<T>(t, t.at(p.x, p.ldx), p.bx, xr);
+  if (p.dh) {
+    ask_rows<T>(t, t.at(p.dh, p.lddh), p.bdh, dr);
+  } else {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) dr[r] = L::none();
+  }
+  float2 h = t.left > 0 ? t.l.state(p.saved, t.i0 / kRows, p.channels) : f2(0.f, 0.f);
+  t.inform(p.q, lane);
+  if (p.state && t.f.first) ask_states(starts, p.state, t.f.first, t.f.seq, p.channels, t.l, lane);
+  if (p.dfinal && t.f.last) ask_states(ends, p.dfinal, t.f.last, t.f.seq, p.channels, t.l, lane);
+  if (!t.inner) copies_done();
+  float2 a[kRows], e[kRows];  // e: h_{t-1} - x_t
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (!t.inner && (t.f.first >> r & 1)) h = p.state ? starts[r * 32 + lane] : f2(0.f, 0.f);
+    const float2 x = L::values(xr[r]);
+    a[r] = keep(L::values(gr[r]));
+    e[r] = f2(h.x - x.x, h.y - x.y);
+    h = f2(fmaf(a[r].x, e[r].x, x.x), fmaf(a[r].y, e[r].y, x.y));
+  }
+  float2 carry = state_before<Chain>(p, sm, t.tile, t.group, slot, warp, lane);
+  const int64_t o = t.row0 * p.channels + t.l.c;
+  char *px = (char *)((T *)p.out0 + o), *pg = (char *)((T *)p.out1 + o);
+  auto results = [&](int r, float2 lam, bool live) {
+    const float2 b = drop(L::values(gr[r]), a[r]);
+    const float2 none = f2(0.f, 0.f);
+    if (p.out0) t.l.store((T *)(px + (int64_t)p.bo * r), live ? mul2(b, lam) : none);
+    if (p.out1) t.l.store((T *)(pg + (int64_t)p.bo * r), live ? mul2(mul2(lam, e[r]), mul2(a[r], b)) : none);
+  };
+  if (t.inner) {
+#pragma unroll
+    for (int r = kRows - 1; r >= 0; --r) {
+      const float2 lam = add2(L::values(dr[r]), carry);
+      carry = mul2(a[r], lam);
+      results(r, lam, true);
+    }
+    return;
+  }
+#pragma unroll
+  for (int r = kRows - 1; r >= 0; --r) {
+    if (t.f.last >> r & 1) carry = p.dfinal ? ends[r * 32 + lane] : f2(0.f, 0.f);
+    const float2 lam = add2(L::values(dr[r]), carry);
+    carry = mul2(a[r], lam);
+    if (r < t.left) results(r, lam, t.f.live >> r & 1);
+    if (p.end && (t.f.first >> r & 1)) t.l.put_state(p.end, __shfl_sync(0xffffffffu, t.f.seq, r), p.channels, carry);
+  }
+}
+
+// Blocks of a multiprocessor: as many as the registers of a tile's rows admit.
+template <typename T, bool Backward>
+inline constexpr int kResident = Backward ? 2 : sizeof(T) == 2 ? 4 : 3;
+
+template <typename T, bool Chain, bool Pair, bool Backward>
+__global__ void __launch_bounds__(32 * kWarps, kResident<T, Backward>) scan_kernel(const __grid_constant__ ScanArgs p) {
+  // [kWarps][kRows][32], backward twice: states of the sequences that start (and end) in a tile
+  extern __shared__ float2 dynamic[];
+  __shared__ TileMemory sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float2 *starts = dynamic + warp * 2 * kRows * 32, *ends = starts + kRows * 32;
+  float2 *starts = dynamic + warp * (Backward ? 2 : 1) * kRows * 32;
   const uint32_t all = (uint32_t)p.tiles * (uint32_t)p.groups;
-  const int64_t dir = p.q.reverse ? -1 : 1;
-  uint32_t id = first_tile<W, Chain>(p, sm);
-  while (id < all) {
-    // time runs backwards: tile 0 holds the last rows and warp 0 the last of a tile
-    const int tile = id / (uint32_t)p.groups, group = id - tile * p.groups;
-    const int64_t t0 = (int64_t)tile * W * kRows;
-    const int64_t i0 = ((int64_t)(p.tiles - 1 - tile) * W + (W - 1 - warp)) * kRows;
-    const L l(group, lane, p.channels);
-    const int64_t row0 = row_of(p.q, i0);
-    const int left = (int)max(min((int64_t)kRows, p.q.rows - i0), (int64_t)0);
-    typename L::Raw xr[kRows], gr[kRows], dr[kRows];
-    {
-      const T *px = (const T *)p.x + row0 * p.ldx + l.c, *pg = (const T *)p.g + row0 * p.ldg + l.c;
-      const T *pd = (const T *)p.dh + row0 * p.lddh + l.c;
-      const int64_t sx = dir * p.ldx, sg = dir * p.ldg, sd = dir * p.lddh;
-#pragma unroll
-      for (int r = 0; r < kRows; ++r, px += sx, pg += sg, pd += sd) {
-        xr[r] = gr[r] = dr[r] = L::none();
-        if (r < left) {
-          gr[r] = l.load(pg);
-          xr[r] = l.load(px);
-          if (p.dh) dr[r] = l.load(pd);
-        }
-      }
+  auto results = [&](uint32_t id, int slot) {
+    if constexpr (Backward)
+      results_backward<T, Chain, Pair>(p, sm, id, slot, starts, warp, lane);
+    else
+      results_forward<T, Chain, Pair>(p, sm, id, slot, starts, warp, lane);
+  };
+  int slot = 0;
+  if constexpr (!Chain) {
+    for (uint32_t id = blockIdx.x; id < all; id += gridDim.x) {
+      map_tile<T, Chain, Pair, Backward>(p, sm, id, slot, starts, warp, lane);
+      results(id, slot);
+      slot = slot == 2 ? 0 : slot + 1;
     }
-    float2 h = left > 0 ? l.state(p.saved, i0 / kRows, p.channels) : f2(0.f, 0.f);
-    const RowInfo f = rows_info(p.q, i0, lane);
-    const bool inner = f.live == (1u << kRows) - 1 && !f.first && !f.last;
-    if (p.state && f.first) ask_states(starts, p.state, f.first, f.seq, p.channels, l, lane);
-    if (p.dfinal && f.last) ask_states(ends, p.dfinal, f.last, f.seq, p.channels, l, lane);
-    if (Chain) {
-      // the row behind which the present sequence ends, counted backwards from the end of the last tile
-      const int64_t span = (int64_t)p.tiles * W * kRows;
-      const int64_t until = __shfl_sync(0xffffffffu, f.until, kRows - 1);
-      if (threadIdx.x == 0) sm.origin = f.live >> (kRows - 1) & 1 ? span - until : t0;
-    }
-    float2 a[kRows], e[kRows];  // e: h_{t-1} - x_t
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) a[r] = keep_of(exp_minus(L::values(gr[r])));
-    auto start = [&](int r) { return p.state ? starts[r * 32 + lane] : f2(0.f, 0.f); };
-    auto end = [&](int r) { return p.dfinal ? ends[r * 32 + lane] : f2(0.f, 0.f); };
-    Map m{f2(1.f, 1.f), f2(0.f, 0.f)};
-    if (inner) {
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const float2 x = L::values(xr[r]);
-        e[r] = add2(h, f2(-x.x, -x.y));
-        h = fma2(a[r], e[r], x);
-      }
-#pragma unroll
-      for (int r = kRows - 1; r >= 0; --r) {
-        m.h = mul2(a[r], add2(L::values(dr[r]), m.h));
-        m.a = mul2(m.a, a[r]);
-      }
-    } else {
-      copies_done();
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (f.first >> r & 1) h = start(r);
-        const float2 x = L::values(xr[r]);
-        e[r] = add2(h, f2(-x.x, -x.y));
-        h = fma2(a[r], e[r], x);
-      }
-#pragma unroll
-      for (int r = kRows - 1; r >= 0; --r) {
-        if (f.last >> r & 1) m.h = end(r);
-        m.h = mul2(a[r], add2(L::values(dr[r]), m.h));
-        m.a = mul2(m.a, a[r]);
-      }
-      if (f.last) m.a = f2(kCut, kCut);
-    }
-    sm.maps[warp][lane] = m;
-    __syncthreads();
-    float2 carry = state_before<W, Chain>(p, sm, tile, group, t0, m, warp, lane);
-    uint32_t ahead = 0;
-    if (Chain && threadIdx.x == 0) ahead = atomicAdd(p.counter, 1u) + 1u;
-    const int64_t so = dir * p.channels, o = (row0 + (kRows - 1) * dir) * p.channels + l.c;
-    T *px = (T *)p.out0 + o, *pg = (T *)p.out1 + o;
-    auto results = [&](int r, float2 lam, bool live) {
-      const float2 b = mul2(exp_minus(L::values(gr[r])), a[r]);  // 1 - a
-      const float2 none = f2(0.f, 0.f);
-      if (p.out0) l.store(px, live ? mul2(b, lam) : none);
-      if (p.out1) l.store(pg, live ? mul2(mul2(lam, e[r]), mul2(a[r], b)) : none);
+  } else {
+    auto take = [&] {
+      if (threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
+      __syncthreads();
+      const uint32_t id = sm.next;
+      __syncthreads();
+      return id;
     };
-    if (inner) {
-#pragma unroll
-      for (int r = kRows - 1; r >= 0; --r, px -= so, pg -= so) {
-        const float2 lam = add2(L::values(dr[r]), carry);
-        carry = mul2(a[r], lam);
-        results(r, lam, true);
-      }
-    } else {
-#pragma unroll
-      for (int r = kRows - 1; r >= 0; --r, px -= so, pg -= so) {
-        if (f.last >> r & 1) carry = end(r);
-        const float2 lam = add2(L::values(dr[r]), carry);
-        carry = mul2(a[r], lam);
-        if (r < left) results(r, lam, f.live >> r & 1);
-        if (p.end && (f.first >> r & 1)) l.put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, carry);
-      }
+    uint32_t id = take();
+    if (id >= all) return;
+    map_tile<T, Chain, Pair, Backward>(p, sm, id, slot, starts, warp, lane);
+    uint32_t ahead = take();
+    while (id < all) {
+      const int then = slot == 2 ? 0 : slot + 1;
+      if (ahead < all) map_tile<T, Chain, Pair, Backward>(p, sm, ahead, then, starts, warp, lane);
+      results(id, slot);  // takes the tile after that
+      __syncthreads();
+      id = ahead;
+      ahead = sm.next;
+      slot = then;
     }
-    if (Chain && threadIdx.x == 0) sm.next = ahead;
-    __syncthreads();
-    id = Chain ? sm.next : id + gridDim.x;
   }
 }
 
@@ -567,7 +637,7 @@ __global__ void __launch_bounds__(256) scan_single(const __grid_constant__ ScanA
     const float2 g = L::values(l.load((const T *)p.g + row * p.ldg + l.c));
     const float2 x = L::values(l.load((const T *)p.x + row * p.ldx + l.c));
     float2 h = p.state ? l.state(p.state, row, p.channels) : f2(0.f, 0.f);
-    h = step(h, x, keep_of(exp_minus(g)));
+    h = step(h, x, keep(g));
     l.store((T *)p.out0 + row * p.channels + l.c, h);
     if (p.end) l.put_state(p.end, row, p.channels, h);
   }
@@ -575,20 +645,19 @@ __global__ void __launch_bounds__(256) scan_single(const __grid_constant__ ScanA
 
 // ------------------------------------------------------------------ the calls
 
-int64_t tiles_of(int64_t rows, int warps) { return (rows + warps * kRows - 1) / (warps * kRows); }
+int64_t tiles_of(int64_t rows) { return (rows + kTile - 1) / kTile; }
 
 // Whether no sequence leaves a tile: whole sequences in every one, or a single tile.
-bool closed_tiles(const sla_scan *s, int warps) {
-  const int64_t tile = warps * kRows;
-  if (s->rows <= tile) return true;
+bool closed_tiles(const sla_scan *s) {
+  if (s->rows <= kTile) return true;
   if (s->offsets || s->sequences < 1) return false;
-  return tile % (s->rows / s->sequences) == 0;
+  return kTile % (s->rows / s->sequences) == 0;
 }
 
-size_t chain_bytes(const sla_scan *s, int warps) {
-  if (closed_tiles(s, warps)) return 0;
-  const size_t groups = (size_t)((s->channels + kCols - 1) / kCols), tiles = (size_t)tiles_of(s->rows, warps);
-  return align256(256 + (tiles + tiles / kSpan) * groups * kCols * sizeof(uint64_t));
+size_t chain_bytes(const sla_scan *s) {
+  if (closed_tiles(s)) return 0;
+  const size_t groups = (size_t)((s->channels + kCols - 1) / kCols), tiles = (size_t)tiles_of(s->rows);
+  return align256(256 + (tiles + tiles / kFold + tiles / kSpan) * groups * kCols * sizeof(uint64_t));
 }
 
 size_t saved_bytes(const sla_scan *s) {
@@ -610,13 +679,14 @@ sla_status check_scan(const sla_scan *s) {
   }
   // tiles of all groups are counted in 32 bits
   const int64_t groups = (s->channels + kCols - 1) / kCols;
-  return tiles_of(s->rows, kBackwardWarps) * groups < most ? SLA_OK : SLA_INVALID_ARG;
+  return tiles_of(s->rows) * groups < most ? SLA_OK : SLA_INVALID_ARG;
 }
 
 sla_status check_rows(const void *p, const sla_scan *s, int64_t ld) {
   if (s->rows == 0) return SLA_OK;
   if (!p || !aligned(p, net_size(s->dtype))) return SLA_INVALID_ARG;
-  return ld >= s->channels || s->rows == 1 ? SLA_OK : SLA_INVALID_ARG;
+  // (the kernels count a row's bytes in 32 bits)
+  return s->rows == 1 || (ld >= s->channels && ld < (int64_t)1 << 28) ? SLA_OK : SLA_INVALID_ARG;
 }
 
 sla_status check_buffer(const void *p, size_t bytes, size_t need) {
@@ -625,16 +695,23 @@ sla_status check_buffer(const void *p, size_t bytes, size_t need) {
   return bytes < need ? SLA_WORKSPACE_TOO_SMALL : SLA_OK;
 }
 
-ScanArgs scan_args(const sla_scan *s, int warps, void *ws) {
+// Bytes from a row to the next in the scan's order.
+int row_bytes(const sla_scan *s, int64_t ld) {
+  return (int)((s->reverse ? -ld : ld) * (int64_t)net_size(s->dtype));
+}
+
+ScanArgs scan_args(const sla_scan *s, void *ws) {
   ScanArgs p{};
   p.q = {s->rows, s->sequences, s->offsets || !s->sequences ? 0 : s->rows / s->sequences, s->offsets,
          s->offsets_type == SLA_I64, s->reverse};
   p.channels = (int)s->channels, p.groups = (int)((s->channels + kCols - 1) / kCols);
   p.outside = s->outside;
-  p.tiles = (int)tiles_of(s->rows, warps);
+  p.tiles = (int)tiles_of(s->rows);
+  p.bo = row_bytes(s, s->channels);
   p.counter = (uint32_t *)ws;
   p.maps = (uint64_t *)((char *)ws + 256);
-  p.states = p.maps + (int64_t)p.tiles * p.groups * kCols;
+  p.folds = p.maps + (int64_t)p.tiles * p.groups * kCols;
+  p.states = p.folds + (int64_t)(p.tiles / kFold) * p.groups * kCols;
   return p;
 }
 
@@ -643,12 +720,12 @@ bool pairs_aligned(const sla_scan *s, const void *p, int64_t ld) {
   return aligned(p, 2 * net_size(s->dtype)) && (s->rows == 1 || ld % 2 == 0);
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const ScanArgs &p, int block, size_t smem, int resident, cudaStream_t st) {
+template <typename T, bool Backward, typename K>
+cudaError_t launch(K kernel, const ScanArgs &p, size_t smem, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.tiles * p.groups;
-  kernel<<<(unsigned)std::min<int64_t>(tiles, (int64_t)sm_count() * resident), block, smem, st>>>(p);
+  kernel<<<(unsigned)std::min<int64_t>(tiles, (int64_t)sm_count() * kResident<T, Backward>), 32 * kWarps, smem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -659,17 +736,16 @@ cudaError_t run_forward(const ScanArgs &p, bool chain, cudaStream_t st) {
     scan_single<T, Pair><<<(unsigned)std::min<int64_t>((threads + 255) / 256, sm_count() * 8), 256, 0, st>>>(p);
     return cudaGetLastError();
   }
-  const size_t smem = p.state ? kForwardWarps * kRows * kCols * sizeof(float) : 0;
-  constexpr int resident = sizeof(T) == 2 ? 2 : 1;
-  return chain ? launch(scan_forward<T, true, Pair>, p, 32 * kForwardWarps, smem, resident, st)
-               : launch(scan_forward<T, false, Pair>, p, 32 * kForwardWarps, smem, resident, st);
+  const size_t smem = p.state ? kWarps * kRows * kCols * sizeof(float) : 0;
+  return chain ? launch<T, false>(scan_kernel<T, true, Pair, false>, p, smem, st)
+               : launch<T, false>(scan_kernel<T, false, Pair, false>, p, smem, st);
 }
 
 template <typename T, bool Pair>
 cudaError_t run_backward(const ScanArgs &p, bool chain, cudaStream_t st) {
-  const size_t smem = p.state || p.dfinal ? kBackwardWarps * 2 * kRows * kCols * sizeof(float) : 0;
-  return chain ? launch(scan_backward<T, true, Pair>, p, 32 * kBackwardWarps, smem, 2, st)
-               : launch(scan_backward<T, false, Pair>, p, 32 * kBackwardWarps, smem, 2, st);
+  const size_t smem = p.state || p.dfinal ? kWarps * 2 * kRows * kCols * sizeof(float) : 0;
+  return chain ? launch<T, true>(scan_kernel<T, true, Pair, true>, p, smem, st)
+               : launch<T, true>(scan_kernel<T, false, Pair, true>, p, smem, st);
 }
 
 // Calls f with the element type and whether channels go in pairs.
@@ -699,7 +775,7 @@ extern "C" {
 SLA_API size_t sla_gated_scan_saved_bytes(const sla_scan *s) { return check_scan(s) == SLA_OK ? saved_bytes(s) : 0; }
 
 SLA_API size_t sla_gated_scan_workspace_bytes(const sla_scan *s) {
-  return check_scan(s) == SLA_OK ? std::max(chain_bytes(s, kForwardWarps), chain_bytes(s, kBackwardWarps)) : 0;
+  return check_scan(s) == SLA_OK ? chain_bytes(s) : 0;
 }
 
 SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx, const void *gate, int64_t ldg,
@@ -711,7 +787,7 @@ SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx,
   SLA_CHECK(check_rows(h, s, s->channels));
   if (!aligned(state, 4) || !aligned(final_state, 4)) return SLA_INVALID_ARG;
   if (saved) SLA_CHECK(check_buffer(saved, saved_size, saved_bytes(s)));
-  const size_t need = chain_bytes(s, kForwardWarps);
+  const size_t need = chain_bytes(s);
   SLA_CHECK(check_buffer(workspace, ws_bytes, need));
   cudaStream_t st = (cudaStream_t)stream;
   if (s->offsets || s->rows == 0) {
@@ -722,8 +798,9 @@ SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx,
   const Expired earlier = expired();
   if (earlier.err != cudaSuccess) return fail(earlier.err);
   SLA_CHECK(report_expired(earlier));
-  ScanArgs p = scan_args(s, kForwardWarps, workspace);
+  ScanArgs p = scan_args(s, workspace);
   p.x = x, p.ldx = ldx, p.g = gate, p.ldg = ldg, p.state = state, p.out0 = h, p.end = final_state;
+  p.bx = row_bytes(s, ldx), p.bg = row_bytes(s, ldg);
   p.saved = (float *)saved, p.timeouts = earlier.count;
   const bool pairs = s->channels % 2 == 0 && pairs_aligned(s, x, ldx) && pairs_aligned(s, gate, ldg) &&
                      pairs_aligned(s, h, s->channels);
@@ -749,7 +826,7 @@ SLA_API sla_status sla_gated_scan_backward(const sla_scan *s, const void *dh, in
   if (!aligned(state, 4) || !aligned(dfinal, 4) || !aligned(dstate, 4) || !aligned(dx, e0) || !aligned(dgate, e0))
     return SLA_INVALID_ARG;
   SLA_CHECK(check_buffer(saved, saved_size, saved_bytes(s)));
-  const size_t need = chain_bytes(s, kBackwardWarps);
+  const size_t need = chain_bytes(s);
   SLA_CHECK(check_buffer(workspace, ws_bytes, need));
   cudaStream_t st = (cudaStream_t)stream;
   if (s->offsets || s->rows == 0) {
@@ -760,8 +837,9 @@ SLA_API sla_status sla_gated_scan_backward(const sla_scan *s, const void *dh, in
   const Expired earlier = expired();
   if (earlier.err != cudaSuccess) return fail(earlier.err);
   SLA_CHECK(report_expired(earlier));
-  ScanArgs p = scan_args(s, kBackwardWarps, workspace);
+  ScanArgs p = scan_args(s, workspace);
   p.dh = dh, p.lddh = lddh, p.x = x, p.ldx = ldx, p.g = gate, p.ldg = ldg, p.state = state, p.dfinal = dfinal;
+  p.bx = row_bytes(s, ldx), p.bg = row_bytes(s, ldg), p.bdh = row_bytes(s, lddh);
   p.out0 = dx, p.out1 = dgate, p.end = dstate, p.saved = (float *)const_cast<void *>(saved);
   p.timeouts = earlier.count;
   const bool pairs = s->channels % 2 == 0 && pairs_aligned(s, x, ldx) && pairs_aligned(s, gate, ldg) &&

@@ -721,7 +721,7 @@ SLA_API size_t sla_gated_scan_saved_bytes(const sla_scan *s);
 SLA_API size_t sla_gated_scan_workspace_bytes(const sla_scan *s);
 
 /*
- *   x, gate      device, [rows][channels] with leading dimensions ldx and ldg
+ *   x, gate      device, [rows][channels] with leading dimensions ldx and ldg (below 2^28, as lddh)
  *   state        device, [sequences][channels] float32: the states before the sequences, or NULL: zero
  *   h            device, [rows][channels]
  *   final_state  device, [sequences][channels] float32: the states behind the sequences, or NULL.  It may be `state`.
