@@ -5,21 +5,20 @@
 //   dx = (1 - a) l,  dg = l (h_{t-1} - x) a (1 - a),  dstate = a_1 l_1                             with its transpose)
 //
 // Both are bound by memory: two reads and a write forward, three reads and two writes backward (h is formed
-// again from x and g, from float32 states that the forward call leaves every kRows rows: an eighth of what reading h
-// in 16 bits would cost, and exact).  To have the rows in parallel, they are taken in tiles of kTile rows by kCols channels,
-// kRows rows a warp, two channels a lane, and every tile twice: once for the map (A, H) from the state before it to the state
-// behind it, s -> A s + H, which is published, and once for the results, from the state before it, which is put together from the
-// maps of the tiles before it, back to the tile in which the sequence starts or the last of the states that
-// every kSpan-th tile publishes; every kFold-th tile publishes the map of its kFold tiles, so that at most 15 tiles, 15 folds
-// and a state are looked at.
+// again from x and g, from float32 states that the forward call leaves every kSaved rows: an eighth of what reading h
+// would cost, and exact).  To read everything once with the rows in parallel, a block
+// takes a tile of rows by kCols channels into registers, kRows rows a warp, two channels a lane, and goes
+// over them twice: once for the map (A, H) from the state before the rows to the state behind them,
+// s -> A s + H, and, when that state is known, once for the results.  In between the maps of the block's warps
+// are joined in shared memory, the block's is published, and the state before the tile is put together from
+// the maps of the tiles before it, back to the tile in which the sequence starts or the last of the states that
+// every kSpan-th tile publishes; every kFold-th tile publishes the map of its kFold tiles, so that at most 15 tiles, 31 folds
+// and a state are looked at.  (One path of 1,000,000 rows waits from state to state, 3 us each, so they are far apart.)
 //
-// A block makes the map of its next tile before it looks back for the present one.  So nothing that waits keeps a map from being
-// published, all maps that are looked for are a tile's time old, and the second reading of a tile hits L2 (456 tiles of
-// 32 KB and as many ahead): memory sees one.  Made one after the other, from registers, with the next tile taken early or
-// late, the same tiles took 193 to 1000 us where they now take a third of that: one path of 1,000,000 rows waits from
-// state to state, and a tile that waits for its block keeps all later ones waiting.
 // Tiles are handed out in order of time by a counter, so those waited for are
-// always at work; which block takes which tile changes no result, and the maps are joined in a fixed order.
+// always at work; which block takes which tile changes no result, and the maps are joined in a fixed order.  A block takes its
+// next tile only when the present one's state is known: a tile that waits for its block keeps all later ones waiting (taken
+// while the present one still waited, one path of 1,000,000 rows took 454 us, 1000 lines of 1000 a training step of 1023).
 //
 // A map's two float32 are published as one 64-bit word, so that the word itself says whether it is there (the
 // workspace is set to ones, a NaN that no map has): no flag, no fence.
@@ -44,10 +43,13 @@
 namespace sla {
 namespace {
 
-constexpr int kRows = 16;     // of a warp; the distance of the saved states
+// Rows of a warp: as many as the registers hold, backward with h_{t-1} - x_t beside the rest.
+template <typename T, bool Backward>
+inline constexpr int kRows = Backward && sizeof(T) == 4 ? 8 : 16;
+template <typename T>
+inline constexpr int kSaved = kRows<T, true>;  // rows between the saved states
 constexpr int kCols = 64;     // channels of a tile, two a lane
-constexpr int kWarps = 8;     // of a block: a tile is kWarps kRows rows
-constexpr int kTile = kWarps * kRows;
+constexpr int kWarps = 8;     // of a block
 constexpr int kFold = 16;     // tiles whose maps the last of them joins to one
 constexpr int kSpan = 512;    // tiles between published states
 constexpr float kCut = -1.f;
@@ -73,7 +75,7 @@ struct ScanArgs {
   const float *state;    // [count][channels] or NULL
   const float *dfinal;   // the same, backward
   float *end;            // [count][channels] or NULL: states behind the sequences; or dstate
-  float *saved;          // [rows / kRows][channels]: states before those rows
+  float *saved;          // [rows / kSaved][channels]: states before those rows
   int tiles;             // of a group
   uint32_t *counter;     // tiles taken so far, less one
   // [tiles][groups][kCols], and of every kFold-th and every kSpan-th tile
@@ -91,7 +93,7 @@ __device__ __forceinline__ int64_t offset_at(const Sequences &q, int64_t s) {
   return q.wide ? ((const int64_t *)q.offsets)[s] : ((const int32_t *)q.offsets)[s];
 }
 
-// The sequence of every lane's row; all lanes take part, and rows differ by less than 32.  With offsets: the last s with
+// The sequence of every lane's row; all lanes take part.  With offsets: the last s with
 // offsets[s] <= the smallest row, by 33 parts at a time, and from there on through the next 31 offsets, and by halves where
 // they do not reach (many sequences without rows).
 __device__ __forceinline__ Place place_of(const Sequences &q, int64_t row, int lane) {
@@ -151,10 +153,11 @@ struct RowInfo {
   int64_t until;               // ... and of the row behind its last
 };
 
+template <int N>
 __device__ __forceinline__ RowInfo rows_info(const Sequences &q, int64_t i0, int lane) {
   RowInfo f;
   const int64_t i = i0 + lane, row = row_of(q, i);
-  const Place p = place_of(q, lane < kRows && i < q.rows ? row : -1, lane);
+  const Place p = place_of(q, lane < N && i < q.rows ? row : -1, lane);
   const bool in = p.seq >= 0, at_begin = in && row == p.begin, at_end = in && row == p.end - 1;
   f.seq = p.seq;
   f.origin = q.reverse ? q.rows - p.end : p.begin;
@@ -229,8 +232,11 @@ struct Lane {
 };
 
 // a = 1 / (1 + exp(-g)).
-__device__ __forceinline__ float keep(float g) { return rcp_approx(1.f + ex2_approx(g * -1.4426950408889634f)); }
-__device__ __forceinline__ float2 keep(float2 g) { return f2(keep(g.x), keep(g.y)); }
+__device__ __forceinline__ float2 keep(float2 g) {
+  const float2 m = mul2(g, f2(-1.4426950408889634f, -1.4426950408889634f));
+  const float2 d = add2(f2(ex2_approx(m.x), ex2_approx(m.y)), f2(1.f, 1.f));
+  return f2(rcp_approx(d.x), rcp_approx(d.y));
+}
 
 // 1 - a, right relative to itself.
 __device__ __forceinline__ float drop(float g, float a) {
@@ -241,8 +247,9 @@ __device__ __forceinline__ float drop(float g, float a) {
 __device__ __forceinline__ float2 drop(float2 g, float2 a) { return f2(drop(g.x, a.x), drop(g.y, a.y)); }
 
 // One step of h: a h + (x - a x).
-__device__ __forceinline__ float step(float h, float x, float a) { return fmaf(a, h, fmaf(-a, x, x)); }
-__device__ __forceinline__ float2 step(float2 h, float2 x, float2 a) { return f2(step(h.x, x.x, a.x), step(h.y, x.y, a.y)); }
+__device__ __forceinline__ float2 step(float2 h, float2 x, float2 a) {
+  return fma2(a, h, f2(fmaf(-a.x, x.x, x.x), fmaf(-a.y, x.y, x.y)));
+}
 
 // s -> a s + h of two channels; a = kCut: s -> h.
 struct Map {
@@ -295,7 +302,7 @@ __device__ __forceinline__ void copy_async(float *dst, const float *src) {
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Asks for the rows of `from` ([count][channels] float32) that belong to the sequences of the marked rows: to the lane's
-// two places of row r of `to` ([kRows][32] pairs), which the lane itself reads.
+// two places of row r of `to` ([..][32] pairs), which the lane itself reads.
 template <typename L>
 __device__ __forceinline__ void ask_states(float2 *to, const float *from, uint32_t marks, int seq, int channels, const L &l,
                                            int lane) {
@@ -309,11 +316,10 @@ __device__ __forceinline__ void ask_states(float2 *to, const float *from, uint32
   }
 }
 
-// What a block keeps of its tiles: of the present one, and of the next one or two.
 struct TileMemory {
-  Map maps[3][kWarps][32];  // of the warps
-  int64_t origin[3];        // the scan's index of the first row that the tile's first row depends on
-  Map carry[kWarps][32];    // parts of the way from the known state to the present tile: folds, then tiles
+  Map maps[kWarps][32];   // of the block's warps
+  Map carry[kWarps][32];  // parts of the way from the known state to the tile: folds, then tiles
+  int64_t origin;         // the scan's index of the first row that the tile's first row depends on
   uint32_t next;
 };
 
@@ -326,11 +332,10 @@ __device__ __forceinline__ Map joined(const Map (*maps)[32], int from, int to, i
   return m;
 }
 
-// This warp's part of the way from the state before the tile's sequence, or span, to the tile.
-__device__ __forceinline__ Map look_back(const ScanArgs &p, int tile, int64_t origin, int64_t mine, int64_t apart, int warp,
-                                         int lane) {
+// This warp's part of the way from the start of the tile's sequence, in tile `first`, or the state before its span, to the tile.
+__device__ __forceinline__ Map look_back(const ScanArgs &p, int tile, int first, int64_t mine, int64_t apart, int warp, int lane) {
   Map m = no_rows();
-  const int first = (int)(origin / kTile), base = tile / kSpan * kSpan, fold = tile / kFold * kFold;
+  const int base = tile / kSpan * kSpan, fold = tile / kFold * kFold;
   // half of the warps take the folds before the present one, half the tiles of the present one
   constexpr int H = kWarps / 2;
   const bool tiles = warp >= H;
@@ -357,210 +362,209 @@ __device__ __forceinline__ Map look_back(const ScanArgs &p, int tile, int64_t or
   return m;
 }
 
-// Where a warp's rows of a tile lie, and what it knows of them.  Backward, tile 0 holds the last rows and warp 0 the last of
-// a tile.
+// Where a warp's rows of a tile lie.  Backward, tile 0 holds the last rows and warp 0 the last of a tile.
 template <typename T, bool Pair, bool Backward>
 struct Rows {
+  static constexpr int n = kRows<T, Backward>, tile_rows = kWarps * n;
   Lane<T, Pair> l;
   int tile, group, left;  // rows that there are
-  int64_t i0, row0;       // the scan's index of the first row, and its row
-  RowInfo f;
-  bool inner;             // all rows are in one sequence, and none is its first or last
+  int64_t t0, i0, row0;   // the tile's first row in the order of the tiles; the scan's index of the warp's first row, and its row
   __device__ __forceinline__ Rows(const ScanArgs &p, uint32_t id, int warp, int lane)
       : l(id % (uint32_t)p.groups, lane, p.channels), tile(id / (uint32_t)p.groups), group(id % (uint32_t)p.groups) {
-    i0 = Backward ? ((int64_t)(p.tiles - 1 - tile) * kWarps + (kWarps - 1 - warp)) * kRows
-                  : (int64_t)tile * kTile + warp * kRows;
-    left = (int)max(min((int64_t)kRows, p.q.rows - i0), (int64_t)0);
+    t0 = (int64_t)tile * tile_rows;
+    i0 = Backward ? ((int64_t)(p.tiles - 1 - tile) * kWarps + (kWarps - 1 - warp)) * n : t0 + warp * n;
+    left = (int)max(min((int64_t)n, p.q.rows - i0), (int64_t)0);
     row0 = row_of(p.q, i0);
   }
-  // (apart from the constructor: the rows are asked for first)
-  __device__ __forceinline__ void inform(const Sequences &q, int lane) {
-    f = rows_info(q, i0, lane);
-    inner = f.live == (1u << kRows) - 1 && !f.first && !f.last;
-  }
   // The first channel of the first row.
-  __device__ __forceinline__ const T *at(const void *base, int64_t ld) const { return (const T *)base + row0 * ld + l.c; }
-};
-
-// Loads a warp's rows, `step` bytes apart (one wide multiply-add an address).
-template <typename T, typename R, typename Raw>
-__device__ __forceinline__ void ask_rows(const R &t, const T *p, int step, Raw (&raw)[kRows]) {
-  const char *at = (const char *)p;
-  if (t.left == kRows) {
+  __device__ __forceinline__ char *at(const void *base, int64_t ld) const {
+    return (char *)const_cast<void *>(base) + (row0 * ld + l.c) * (int64_t)sizeof(T);
+  }
+  // Loads the rows, `step` bytes apart (one wide multiply-add an address).
+  __device__ __forceinline__ void ask(const void *base, int64_t ld, int step, typename Lane<T, Pair>::Raw (&raw)[n]) const {
+    const char *p = at(base, ld);
+    if (left == n) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) raw[r] = t.l.load((const T *)(at + (int64_t)step * r));
-  } else {
+      for (int r = 0; r < n; ++r) raw[r] = l.load((const T *)(p + (int64_t)step * r));
+    } else {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      raw[r] = decltype(t.l)::none();
-      if (r < t.left) raw[r] = t.l.load((const T *)(at + (int64_t)step * r));
-    }
-  }
-}
-
-// The map of a warp's rows.  starts: [kRows][32], the lane's places for states (forward) or dfinal (backward).
-template <typename T, bool Pair, bool Backward>
-__device__ __forceinline__ Map map_rows(const ScanArgs &p, Rows<T, Pair, Backward> &t, float2 *starts, int lane) {
-  using L = Lane<T, Pair>;
-  typename L::Raw vr[kRows], gr[kRows];  // v: x, or dh
-  ask_rows<T>(t, t.at(p.g, p.ldg), p.bg, gr);
-  if (!Backward || p.dh) {
-    ask_rows<T>(t, t.at(Backward ? p.dh : p.x, Backward ? p.lddh : p.ldx), Backward ? p.bdh : p.bx, vr);
-  } else {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) vr[r] = L::none();
-  }
-  t.inform(p.q, lane);
-  const uint32_t cuts = Backward ? t.f.last : t.f.first;
-  const float *states = Backward ? p.dfinal : p.state;
-  Map m = no_rows();
-  auto go = [&](int r) {
-    const float2 a = keep(L::values(gr[r])), v = L::values(vr[r]);
-    m.h = Backward ? mul2(a, add2(v, m.h)) : step(m.h, v, a);
-    m.a = mul2(m.a, a);
-  };
-  if (!cuts) {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) go(Backward ? kRows - 1 - r : r);
-    return m;
-  }
-  if (states) {
-    ask_states(starts, states, cuts, t.f.seq, p.channels, t.l, lane);
-    copies_done();
-  }
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int r = Backward ? kRows - 1 - k : k;
-    if (cuts >> r & 1) m.h = states ? starts[r * 32 + lane] : f2(0.f, 0.f);
-    go(r);
-  }
-  m.a = f2(kCut, kCut);
-  return m;
-}
-
-// Makes and publishes the map of a tile.  All threads take part; a barrier follows before anything is read from slot.
-template <typename T, bool Chain, bool Pair, bool Backward>
-__device__ __forceinline__ void map_tile(const ScanArgs &p, TileMemory &sm, uint32_t id, int slot, float2 *starts, int warp,
-                                         int lane) {
-  Rows<T, Pair, Backward> t(p, id, warp, lane);
-  sm.maps[slot][warp][lane] = map_rows<T, Pair, Backward>(p, t, starts, lane);
-  if (Chain && warp == 0) {
-    // Backward: the row behind which the present sequence ends, counted backwards from the end of the last tile.
-    const int64_t t0 = (int64_t)t.tile * kTile;
-    const int64_t until = (int64_t)p.tiles * kTile - __shfl_sync(0xffffffffu, t.f.until, kRows - 1);
-    if (lane == 0)
-      sm.origin[slot] = !(t.f.live >> (Backward ? kRows - 1 : 0) & 1) ? t0 : Backward ? until : t.f.origin;
-  }
-  __syncthreads();
-  if (Chain && warp == kWarps - 1)
-    publish(p.maps + ((int64_t)t.tile * p.groups + t.group) * kCols + 2 * lane, joined(sm.maps[slot], 0, kWarps, lane));
-}
-
-// The state before this warp's rows of the tile in slot; on the way, what others look for is published, and the block's
-// next tile taken.
-template <bool Chain>
-__device__ __forceinline__ float2 state_before(const ScanArgs &p, TileMemory &sm, int tile, int group, int slot, int warp,
-                                               int lane) {
-  float2 s = f2(0.f, 0.f);
-  const Map before = joined(sm.maps[slot], 0, warp, lane);
-  if constexpr (Chain) {
-    const int64_t apart = (int64_t)p.groups * kCols, mine = group * kCols + 2 * lane, origin = sm.origin[slot];
-    sm.carry[warp][lane] = origin < (int64_t)tile * kTile ? look_back(p, tile, origin, mine, apart, warp, lane) : no_rows();
-    Map own;
-    if ((tile + 1) % kFold == 0 && warp >= kWarps / 2) {
-      // as soon as the tiles' half is through, not waiting for the states that the others may wait for
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * (kWarps - kWarps / 2)) : "memory");
-      if (warp == kWarps - 1) {
-        own = before;
-        join(own, sm.maps[slot][kWarps - 1][lane]);
-        Map f = joined(sm.carry, kWarps / 2, kWarps, lane);
-        join(f, own);
-        publish(p.folds + (int64_t)(tile / kFold) * apart + mine, f);
+      for (int r = 0; r < n; ++r) {
+        raw[r] = Lane<T, Pair>::none();
+        if (r < left) raw[r] = l.load((const T *)(p + (int64_t)step * r));
       }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
+  }
+};
+
+// The state before this warp's rows.  All maps are in place (and a barrier behind them).  On the way the tile's map is
+// published, the state before the tile found, and what others look for published.
+template <bool Chain, typename R>
+__device__ __forceinline__ float2 state_before(const ScanArgs &p, TileMemory &sm, const R &t, int warp, int lane) {
+  float2 s = f2(0.f, 0.f);
+  if constexpr (!Chain) return apply(joined(sm.maps, 0, warp, lane), s);
+  const int64_t apart = (int64_t)p.groups * kCols, mine = t.group * kCols + 2 * lane, origin = sm.origin;
+  const bool needed = origin < t.t0;
+  const Map before = joined(sm.maps, 0, warp, lane);
+  Map own;
+  if (warp == kWarps - 1) {
+    own = before;
+    join(own, sm.maps[warp][lane]);
+    publish(p.maps + t.tile * apart + mine, own);
+  }
+  sm.carry[warp][lane] = needed ? look_back(p, t.tile, (int)(origin / R::tile_rows), mine, apart, warp, lane) : no_rows();
+  if ((t.tile + 1) % kFold == 0 && warp >= kWarps / 2) {
+    // as soon as the tiles' half is through, not waiting for the states that the others may wait for
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * (kWarps - kWarps / 2)) : "memory");
+    if (warp == kWarps - 1) {
+      Map f = joined(sm.carry, kWarps / 2, kWarps, lane);
+      join(f, own);
+      publish(p.folds + (int64_t)(t.tile / kFold) * apart + mine, f);
+    }
+  }
+  __syncthreads();
+  if (needed)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) s = apply(sm.carry[w][lane], s);
-    if (warp == kWarps - 1 && (tile + 1) % kSpan == 0)
-      publish(p.states + (int64_t)(tile / kSpan) * apart + mine, Map{f2(kCut, kCut), apply(own, s)});
-  }
+  if (warp == kWarps - 1 && (t.tile + 1) % kSpan == 0)
+    publish(p.states + (int64_t)(t.tile / kSpan) * apart + mine, Map{f2(kCut, kCut), apply(own, s)});
   return apply(before, s);
 }
 
 template <typename T, bool Chain, bool Pair>
-__device__ __forceinline__ void results_forward(const ScanArgs &p, TileMemory &sm, uint32_t id, int slot, float2 *starts,
-                                                int warp, int lane) {
+__device__ __forceinline__ void tile_forward(const ScanArgs &p, TileMemory &sm, uint32_t id, float2 *starts, int warp, int lane) {
   using L = Lane<T, Pair>;
-  Rows<T, Pair, false> t(p, id, warp, lane);
-  typename L::Raw xr[kRows], gr[kRows];
-  ask_rows<T>(t, t.at(p.g, p.ldg), p.bg, gr);
-  ask_rows<T>(t, t.at(p.x, p.ldx), p.bx, xr);
-  t.inform(p.q, lane);
-  if (p.state && t.f.first) ask_states(starts, p.state, t.f.first, t.f.seq, p.channels, t.l, lane);
-  float2 h = state_before<Chain>(p, sm, t.tile, t.group, slot, warp, lane);
-  if (p.saved && t.left > 0) t.l.put_state(p.saved, t.i0 / kRows, p.channels, h);
-  char *po = (char *)((T *)p.out0 + t.row0 * p.channels + t.l.c);
-  if (t.inner) {
+  constexpr int N = kRows<T, false>;
+  const Rows<T, Pair, false> t(p, id, warp, lane);
+  typename L::Raw xr[N], gr[N];
+  t.ask(p.g, p.ldg, p.bg, gr);
+  t.ask(p.x, p.ldx, p.bx, xr);
+  const RowInfo f = rows_info<N>(p.q, t.i0, lane);
+  const bool inner = f.live == (1u << N) - 1 && !f.first && !f.last;  // no row is the first or last of a sequence, or in none
+  if (Chain && threadIdx.x == 0) sm.origin = f.live & 1 ? f.origin : t.t0;
+  if (p.state && f.first) ask_states(starts, p.state, f.first, f.seq, p.channels, t.l, lane);
+  auto start = [&](int r) { return p.state ? starts[r * 32 + lane] : f2(0.f, 0.f); };
+  float2 a[N];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      h = step(h, L::values(xr[r]), keep(L::values(gr[r])));
-      t.l.store((T *)(po + (int64_t)p.bo * r), h);
+  for (int r = 0; r < N; ++r) a[r] = keep(L::values(gr[r]));
+  Map m = no_rows();
+  if (inner) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      m.h = step(m.h, L::values(xr[r]), a[r]);
+      m.a = mul2(m.a, a[r]);
+    }
+  } else {
+    copies_done();
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      if (f.first >> r & 1) m.h = start(r);
+      m.h = step(m.h, L::values(xr[r]), a[r]);
+      m.a = mul2(m.a, a[r]);
+    }
+    if (f.first) m.a = f2(kCut, kCut);
+  }
+  sm.maps[warp][lane] = m;
+  __syncthreads();
+  float2 h = state_before<Chain>(p, sm, t, warp, lane);
+  // (taken no sooner, see above)
+  if (Chain && threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
+  char *to = t.at(p.out0, p.channels);
+  auto save = [&](int r) {
+    if (r % kSaved<T> == 0 && p.saved && r < t.left) t.l.put_state(p.saved, (t.i0 + r) / kSaved<T>, p.channels, h);
+  };
+  if (inner) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      save(r);
+      h = step(h, L::values(xr[r]), a[r]);
+      t.l.store((T *)(to + (int64_t)p.bo * r), h);
     }
     return;
   }
-  copies_done();
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (t.f.first >> r & 1) h = p.state ? starts[r * 32 + lane] : f2(0.f, 0.f);
-    h = step(h, L::values(xr[r]), keep(L::values(gr[r])));
-    const bool live = t.f.live >> r & 1;
-    if (live || (p.outside && r < t.left)) t.l.store((T *)(po + (int64_t)p.bo * r), live ? h : f2(0.f, 0.f));
-    if (p.end && (t.f.last >> r & 1)) t.l.put_state(p.end, __shfl_sync(0xffffffffu, t.f.seq, r), p.channels, h);
+  for (int r = 0; r < N; ++r) {
+    save(r);
+    if (f.first >> r & 1) h = start(r);
+    h = step(h, L::values(xr[r]), a[r]);
+    const bool live = f.live >> r & 1;
+    if (live || (p.outside && r < t.left)) t.l.store((T *)(to + (int64_t)p.bo * r), live ? h : f2(0.f, 0.f));
+    if (p.end && (f.last >> r & 1)) t.l.put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, h);
   }
 }
 
 template <typename T, bool Chain, bool Pair>
-__device__ __forceinline__ void results_backward(const ScanArgs &p, TileMemory &sm, uint32_t id, int slot, float2 *starts,
-                                                 int warp, int lane) {
+__device__ __forceinline__ void tile_backward(const ScanArgs &p, TileMemory &sm, uint32_t id, float2 *starts, int warp, int lane) {
   using L = Lane<T, Pair>;
-  Rows<T, Pair, true> t(p, id, warp, lane);
-  float2 *ends = starts + kRows * 32;
-  typename L::Raw xr[kRows], gr[kRows], dr[kRows];
-  ask_rows<T>(t, t.at(p.g, p.ldg), p.bg, gr);
-  ask_rows<T>(t, t.at(p.x, p.ldx), p.bx, xr);
+  constexpr int N = kRows<T, true>;
+  const Rows<T, Pair, true> t(p, id, warp, lane);
+  float2 *ends = starts + N * 32;
+  typename L::Raw xr[N], gr[N], dr[N];
+  t.ask(p.g, p.ldg, p.bg, gr);
+  t.ask(p.x, p.ldx, p.bx, xr);
   if (p.dh) {
-    ask_rows<T>(t, t.at(p.dh, p.lddh), p.bdh, dr);
+    t.ask(p.dh, p.lddh, p.bdh, dr);
   } else {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) dr[r] = L::none();
+    for (int r = 0; r < N; ++r) dr[r] = L::none();
   }
-  float2 h = t.left > 0 ? t.l.state(p.saved, t.i0 / kRows, p.channels) : f2(0.f, 0.f);
-  t.inform(p.q, lane);
-  if (p.state && t.f.first) ask_states(starts, p.state, t.f.first, t.f.seq, p.channels, t.l, lane);
-  if (p.dfinal && t.f.last) ask_states(ends, p.dfinal, t.f.last, t.f.seq, p.channels, t.l, lane);
-  if (!t.inner) copies_done();
-  float2 a[kRows], e[kRows];  // e: h_{t-1} - x_t
+  float2 h = t.left > 0 ? t.l.state(p.saved, t.i0 / N, p.channels) : f2(0.f, 0.f);
+  const RowInfo f = rows_info<N>(p.q, t.i0, lane);
+  const bool inner = f.live == (1u << N) - 1 && !f.first && !f.last;
+  if (p.state && f.first) ask_states(starts, p.state, f.first, f.seq, p.channels, t.l, lane);
+  if (p.dfinal && f.last) ask_states(ends, p.dfinal, f.last, f.seq, p.channels, t.l, lane);
+  if (Chain) {
+    // the row behind which the present sequence ends, counted backwards from the end of the last tile
+    const int64_t span = (int64_t)p.tiles * t.tile_rows, until = __shfl_sync(0xffffffffu, f.until, N - 1);
+    if (threadIdx.x == 0) sm.origin = f.live >> (N - 1) & 1 ? span - until : t.t0;
+  }
+  auto start = [&](int r) { return p.state ? starts[r * 32 + lane] : f2(0.f, 0.f); };
+  auto end = [&](int r) { return p.dfinal ? ends[r * 32 + lane] : f2(0.f, 0.f); };
+  float2 a[N], e[N];  // e: h_{t-1} - x_t
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (!t.inner && (t.f.first >> r & 1)) h = p.state ? starts[r * 32 + lane] : f2(0.f, 0.f);
+  for (int r = 0; r < N; ++r) a[r] = keep(L::values(gr[r]));
+  Map m = no_rows();
+  auto form = [&](int r) {
     const float2 x = L::values(xr[r]);
-    a[r] = keep(L::values(gr[r]));
     e[r] = f2(h.x - x.x, h.y - x.y);
-    h = f2(fmaf(a[r].x, e[r].x, x.x), fmaf(a[r].y, e[r].y, x.y));
+    h = fma2(a[r], e[r], x);
+  };
+  auto pass = [&](int r) {
+    m.h = mul2(a[r], add2(L::values(dr[r]), m.h));
+    m.a = mul2(m.a, a[r]);
+  };
+  if (inner) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) form(r);
+#pragma unroll
+    for (int r = N - 1; r >= 0; --r) pass(r);
+  } else {
+    copies_done();
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      if (f.first >> r & 1) h = start(r);
+      form(r);
+    }
+#pragma unroll
+    for (int r = N - 1; r >= 0; --r) {
+      if (f.last >> r & 1) m.h = end(r);
+      pass(r);
+    }
+    if (f.last) m.a = f2(kCut, kCut);
   }
-  float2 carry = state_before<Chain>(p, sm, t.tile, t.group, slot, warp, lane);
-  const int64_t o = t.row0 * p.channels + t.l.c;
-  char *px = (char *)((T *)p.out0 + o), *pg = (char *)((T *)p.out1 + o);
+  sm.maps[warp][lane] = m;
+  __syncthreads();
+  float2 carry = state_before<Chain>(p, sm, t, warp, lane);
+  if (Chain && threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
+  char *tx = t.at(p.out0, p.channels), *tg = t.at(p.out1, p.channels);
   auto results = [&](int r, float2 lam, bool live) {
     const float2 b = drop(L::values(gr[r]), a[r]);
     const float2 none = f2(0.f, 0.f);
-    if (p.out0) t.l.store((T *)(px + (int64_t)p.bo * r), live ? mul2(b, lam) : none);
-    if (p.out1) t.l.store((T *)(pg + (int64_t)p.bo * r), live ? mul2(mul2(lam, e[r]), mul2(a[r], b)) : none);
+    if (p.out0) t.l.store((T *)(tx + (int64_t)p.bo * r), live ? mul2(b, lam) : none);
+    if (p.out1) t.l.store((T *)(tg + (int64_t)p.bo * r), live ? mul2(mul2(lam, e[r]), mul2(a[r], b)) : none);
   };
-  if (t.inner) {
+  if (inner) {
 #pragma unroll
-    for (int r = kRows - 1; r >= 0; --r) {
+    for (int r = N - 1; r >= 0; --r) {
       const float2 lam = add2(L::values(dr[r]), carry);
       carry = mul2(a[r], lam);
       results(r, lam, true);
@@ -568,61 +572,40 @@ __device__ __forceinline__ void results_backward(const ScanArgs &p, TileMemory &
     return;
   }
 #pragma unroll
-  for (int r = kRows - 1; r >= 0; --r) {
-    if (t.f.last >> r & 1) carry = p.dfinal ? ends[r * 32 + lane] : f2(0.f, 0.f);
+  for (int r = N - 1; r >= 0; --r) {
+    if (f.last >> r & 1) carry = end(r);
     const float2 lam = add2(L::values(dr[r]), carry);
     carry = mul2(a[r], lam);
-    if (r < t.left) results(r, lam, t.f.live >> r & 1);
-    if (p.end && (t.f.first >> r & 1)) t.l.put_state(p.end, __shfl_sync(0xffffffffu, t.f.seq, r), p.channels, carry);
+    if (r < t.left) results(r, lam, f.live >> r & 1);
+    if (p.end && (f.first >> r & 1)) t.l.put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, carry);
   }
 }
 
 // Blocks of a multiprocessor: as many as the registers of a tile's rows admit.
 template <typename T, bool Backward>
-inline constexpr int kResident = Backward ? 2 : sizeof(T) == 2 ? 4 : 3;
+inline constexpr int kResident = !Backward && sizeof(T) == 2 ? 3 : 2;
 
 template <typename T, bool Chain, bool Pair, bool Backward>
 __global__ void __launch_bounds__(32 * kWarps, kResident<T, Backward>) scan_kernel(const __grid_constant__ ScanArgs p) {
-  // [kWarps][kRows][32], backward twice: states of the sequences that start (and end) in a tile
+  // [kWarps][kRows][32], backward twice: states of the sequences that start (and end) in the tile
   extern __shared__ float2 dynamic[];
   __shared__ TileMemory sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float2 *starts = dynamic + warp * (Backward ? 2 : 1) * kRows * 32;
+  float2 *starts = dynamic + warp * (Backward ? 2 : 1) * kRows<T, Backward> * 32;
   const uint32_t all = (uint32_t)p.tiles * (uint32_t)p.groups;
-  auto results = [&](uint32_t id, int slot) {
+  uint32_t id = blockIdx.x;
+  if (Chain) {
+    if (threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
+    __syncthreads();
+    id = sm.next;
+  }
+  while (id < all) {
     if constexpr (Backward)
-      results_backward<T, Chain, Pair>(p, sm, id, slot, starts, warp, lane);
+      tile_backward<T, Chain, Pair>(p, sm, id, starts, warp, lane);
     else
-      results_forward<T, Chain, Pair>(p, sm, id, slot, starts, warp, lane);
-  };
-  int slot = 0;
-  if constexpr (!Chain) {
-    for (uint32_t id = blockIdx.x; id < all; id += gridDim.x) {
-      map_tile<T, Chain, Pair, Backward>(p, sm, id, slot, starts, warp, lane);
-      results(id, slot);
-      slot = slot == 2 ? 0 : slot + 1;
-    }
-  } else {
-    auto take = [&] {
-      if (threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
-      __syncthreads();
-      const uint32_t id = sm.next;
-      __syncthreads();
-      return id;
-    };
-    uint32_t id = take();
-    if (id >= all) return;
-    map_tile<T, Chain, Pair, Backward>(p, sm, id, slot, starts, warp, lane);
-    uint32_t ahead = take();
-    while (id < all) {
-      const int then = slot == 2 ? 0 : slot + 1;
-      if (ahead < all) map_tile<T, Chain, Pair, Backward>(p, sm, ahead, then, starts, warp, lane);
-      results(id, slot);  // takes the tile after that
-      __syncthreads();
-      id = ahead;
-      ahead = sm.next;
-      slot = then;
-    }
+      tile_forward<T, Chain, Pair>(p, sm, id, starts, warp, lane);
+    __syncthreads();  // everything in shared memory has been read
+    id = Chain ? sm.next : id + gridDim.x;
   }
 }
 
@@ -645,23 +628,32 @@ __global__ void __launch_bounds__(256) scan_single(const __grid_constant__ ScanA
 
 // ------------------------------------------------------------------ the calls
 
-int64_t tiles_of(int64_t rows) { return (rows + kTile - 1) / kTile; }
-
-// Whether no sequence leaves a tile: whole sequences in every one, or a single tile.
-bool closed_tiles(const sla_scan *s) {
-  if (s->rows <= kTile) return true;
-  if (s->offsets || s->sequences < 1) return false;
-  return kTile % (s->rows / s->sequences) == 0;
+int tile_rows(const sla_scan *s, bool backward) {
+  return kWarps * (s->dtype != SLA_F32 ? kRows<f16, true> : backward ? kRows<float, true> : kRows<float, false>);
 }
 
-size_t chain_bytes(const sla_scan *s) {
-  if (closed_tiles(s)) return 0;
-  const size_t groups = (size_t)((s->channels + kCols - 1) / kCols), tiles = (size_t)tiles_of(s->rows);
+int64_t tiles_of(const sla_scan *s, bool backward) {
+  const int n = tile_rows(s, backward);
+  return (s->rows + n - 1) / n;
+}
+
+// Whether no sequence leaves a tile: whole sequences in every one, or a single tile.
+bool closed_tiles(const sla_scan *s, bool backward) {
+  const int n = tile_rows(s, backward);
+  if (s->rows <= n) return true;
+  if (s->offsets || s->sequences < 1) return false;
+  return n % (s->rows / s->sequences) == 0;
+}
+
+size_t chain_bytes(const sla_scan *s, bool backward) {
+  if (closed_tiles(s, backward)) return 0;
+  const size_t groups = (size_t)((s->channels + kCols - 1) / kCols), tiles = (size_t)tiles_of(s, backward);
   return align256(256 + (tiles + tiles / kFold + tiles / kSpan) * groups * kCols * sizeof(uint64_t));
 }
 
 size_t saved_bytes(const sla_scan *s) {
-  return align256((size_t)((s->rows + kRows - 1) / kRows) * (size_t)s->channels * sizeof(float));
+  const int64_t apart = s->dtype == SLA_F32 ? kSaved<float> : kSaved<f16>;
+  return align256((size_t)((s->rows + apart - 1) / apart) * (size_t)s->channels * sizeof(float));
 }
 
 sla_status check_scan(const sla_scan *s) {
@@ -679,7 +671,7 @@ sla_status check_scan(const sla_scan *s) {
   }
   // tiles of all groups are counted in 32 bits
   const int64_t groups = (s->channels + kCols - 1) / kCols;
-  return tiles_of(s->rows) * groups < most ? SLA_OK : SLA_INVALID_ARG;
+  return tiles_of(s, true) * groups < most ? SLA_OK : SLA_INVALID_ARG;
 }
 
 sla_status check_rows(const void *p, const sla_scan *s, int64_t ld) {
@@ -700,13 +692,13 @@ int row_bytes(const sla_scan *s, int64_t ld) {
   return (int)((s->reverse ? -ld : ld) * (int64_t)net_size(s->dtype));
 }
 
-ScanArgs scan_args(const sla_scan *s, void *ws) {
+ScanArgs scan_args(const sla_scan *s, bool backward, void *ws) {
   ScanArgs p{};
   p.q = {s->rows, s->sequences, s->offsets || !s->sequences ? 0 : s->rows / s->sequences, s->offsets,
          s->offsets_type == SLA_I64, s->reverse};
   p.channels = (int)s->channels, p.groups = (int)((s->channels + kCols - 1) / kCols);
   p.outside = s->outside;
-  p.tiles = (int)tiles_of(s->rows);
+  p.tiles = (int)tiles_of(s, backward);
   p.bo = row_bytes(s, s->channels);
   p.counter = (uint32_t *)ws;
   p.maps = (uint64_t *)((char *)ws + 256);
@@ -736,14 +728,14 @@ cudaError_t run_forward(const ScanArgs &p, bool chain, cudaStream_t st) {
     scan_single<T, Pair><<<(unsigned)std::min<int64_t>((threads + 255) / 256, sm_count() * 8), 256, 0, st>>>(p);
     return cudaGetLastError();
   }
-  const size_t smem = p.state ? kWarps * kRows * kCols * sizeof(float) : 0;
+  const size_t smem = p.state ? kWarps * kRows<T, false> * kCols * sizeof(float) : 0;
   return chain ? launch<T, false>(scan_kernel<T, true, Pair, false>, p, smem, st)
                : launch<T, false>(scan_kernel<T, false, Pair, false>, p, smem, st);
 }
 
 template <typename T, bool Pair>
 cudaError_t run_backward(const ScanArgs &p, bool chain, cudaStream_t st) {
-  const size_t smem = p.state || p.dfinal ? kWarps * 2 * kRows * kCols * sizeof(float) : 0;
+  const size_t smem = p.state || p.dfinal ? kWarps * 2 * kRows<T, true> * kCols * sizeof(float) : 0;
   return chain ? launch<T, true>(scan_kernel<T, true, Pair, true>, p, smem, st)
                : launch<T, true>(scan_kernel<T, false, Pair, true>, p, smem, st);
 }
@@ -775,7 +767,7 @@ extern "C" {
 SLA_API size_t sla_gated_scan_saved_bytes(const sla_scan *s) { return check_scan(s) == SLA_OK ? saved_bytes(s) : 0; }
 
 SLA_API size_t sla_gated_scan_workspace_bytes(const sla_scan *s) {
-  return check_scan(s) == SLA_OK ? chain_bytes(s) : 0;
+  return check_scan(s) == SLA_OK ? std::max(chain_bytes(s, false), chain_bytes(s, true)) : 0;
 }
 
 SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx, const void *gate, int64_t ldg,
@@ -787,7 +779,7 @@ SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx,
   SLA_CHECK(check_rows(h, s, s->channels));
   if (!aligned(state, 4) || !aligned(final_state, 4)) return SLA_INVALID_ARG;
   if (saved) SLA_CHECK(check_buffer(saved, saved_size, saved_bytes(s)));
-  const size_t need = chain_bytes(s);
+  const size_t need = chain_bytes(s, false);
   SLA_CHECK(check_buffer(workspace, ws_bytes, need));
   cudaStream_t st = (cudaStream_t)stream;
   if (s->offsets || s->rows == 0) {
@@ -798,7 +790,7 @@ SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx,
   const Expired earlier = expired();
   if (earlier.err != cudaSuccess) return fail(earlier.err);
   SLA_CHECK(report_expired(earlier));
-  ScanArgs p = scan_args(s, workspace);
+  ScanArgs p = scan_args(s, false, workspace);
   p.x = x, p.ldx = ldx, p.g = gate, p.ldg = ldg, p.state = state, p.out0 = h, p.end = final_state;
   p.bx = row_bytes(s, ldx), p.bg = row_bytes(s, ldg);
   p.saved = (float *)saved, p.timeouts = earlier.count;
@@ -826,7 +818,7 @@ SLA_API sla_status sla_gated_scan_backward(const sla_scan *s, const void *dh, in
   if (!aligned(state, 4) || !aligned(dfinal, 4) || !aligned(dstate, 4) || !aligned(dx, e0) || !aligned(dgate, e0))
     return SLA_INVALID_ARG;
   SLA_CHECK(check_buffer(saved, saved_size, saved_bytes(s)));
-  const size_t need = chain_bytes(s);
+  const size_t need = chain_bytes(s, true);
   SLA_CHECK(check_buffer(workspace, ws_bytes, need));
   cudaStream_t st = (cudaStream_t)stream;
   if (s->offsets || s->rows == 0) {
@@ -837,7 +829,7 @@ SLA_API sla_status sla_gated_scan_backward(const sla_scan *s, const void *dh, in
   const Expired earlier = expired();
   if (earlier.err != cudaSuccess) return fail(earlier.err);
   SLA_CHECK(report_expired(earlier));
-  ScanArgs p = scan_args(s, workspace);
+  ScanArgs p = scan_args(s, true, workspace);
   p.dh = dh, p.lddh = lddh, p.x = x, p.ldx = ldx, p.g = gate, p.ldg = ldg, p.state = state, p.dfinal = dfinal;
   p.bx = row_bytes(s, ldx), p.bg = row_bytes(s, ldg), p.bdh = row_bytes(s, lddh);
   p.out0 = dx, p.out1 = dgate, p.end = dstate, p.saved = (float *)const_cast<void *>(saved);

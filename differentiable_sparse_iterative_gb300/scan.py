@@ -165,7 +165,7 @@ def sla_gated_scan_backward(dh: Optional[torch.Tensor], x: torch.Tensor, gate: t
 
 
 class GatedScan(torch.autograd.Function):
-    """(h, states behind the sequences).  Saved for backward: x, the gate, and a float32 state every 16th row."""
+    """(h, states behind the sequences).  Saved for backward: x, the gate, and a float32 state every 16th row (8th of float32)."""
 
     @staticmethod
     def forward(ctx, x, gate, state, offsets, reverse):

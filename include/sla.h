@@ -715,7 +715,7 @@ typedef struct sla_scan {
   int32_t outside;        /* rows of h that belong to no sequence: 0 stay as they are, 1 become zero */
 } sla_scan;
 
-/* Bytes of what a forward call keeps for its backward call (float32 states of every 16th row), and of the scratch of
+/* Bytes of what a forward call keeps for its backward call (float32 states of every 16th row, every 8th of float32 data), and of the scratch of
    either call, which is 0 where no sequence needs more than one block (both 0 for invalid arguments). */
 SLA_API size_t sla_gated_scan_saved_bytes(const sla_scan *s);
 SLA_API size_t sla_gated_scan_workspace_bytes(const sla_scan *s);
