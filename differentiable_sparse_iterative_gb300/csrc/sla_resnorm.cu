@@ -34,12 +34,13 @@ __global__ void __launch_bounds__(1024) resnorm_reduce(int nparts, int64_t width
   }
 }
 
+constexpr int kMostClasses = 8;
+
 // Blocks of the backward kernel, each of which leaves partial sums.
-int backward_grid(int64_t rows, int64_t width) {
+int backward_grid(int64_t rows, int64_t width, int classes) {
   const ResNormPlan pl = resnorm_plan(width);
   if (!pl.columns) return (int)std::max<int64_t>(1, std::min<int64_t>(kAnyParts, (rows + 127) / 128));
-  const int64_t groups = pl.block / pl.tpr;
-  return (int)std::max<int64_t>(1, std::min<int64_t>((rows + groups - 1) / groups, sm_count() * (512 / pl.block)));
+  return resnorm_grid(pl, rows, pl.block / pl.tpr, classes, 512);
 }
 
 size_t row_sum_bytes(int64_t rows, int64_t width) {
@@ -48,7 +49,8 @@ size_t row_sum_bytes(int64_t rows, int64_t width) {
 
 size_t backward_bytes(int64_t rows, int64_t width) {
   return row_sum_bytes(rows, width) +
-         align256((size_t)backward_grid(rows, width) * kNormSums * (size_t)width * sizeof(float));
+         align256((size_t)std::max(backward_grid(rows, width, 1), backward_grid(rows, width, kMostClasses)) * kNormSums *
+                  (size_t)width * sizeof(float));
 }
 
 sla_status check_resnorm(const sla_resnorm *n) {
@@ -67,7 +69,8 @@ sla_status check_resnorm(const sla_resnorm *n) {
 sla_status check_rows(const void *p, const sla_resnorm *n, int64_t ld, bool needed) {
   if (n->rows == 0 || (!p && !needed)) return SLA_OK;
   if (!p || !aligned(p, net_size(n->dtype))) return SLA_INVALID_ARG;
-  return ld >= n->width || n->rows == 1 ? SLA_OK : SLA_INVALID_ARG;
+  // (the kernels count a row's bytes in 32 bits)
+  return n->rows == 1 || (ld >= n->width && ld < (int64_t)1 << 29) ? SLA_OK : SLA_INVALID_ARG;
 }
 
 ResNormArgs resnorm_args(const sla_resnorm *n, const void *gate) {
@@ -78,22 +81,29 @@ ResNormArgs resnorm_args(const sla_resnorm *n, const void *gate) {
   return p;
 }
 
-// Whether every row of an array starts at a 16-byte boundary and holds whole vectors.
-struct Vectors {
+uint32_t row_bytes(const sla_resnorm *n, int64_t ld) { return n->rows == 1 ? 0 : (uint32_t)((size_t)ld * net_size(n->dtype)); }
+
+// How the rows of a call's arrays lie behind 16-byte boundaries, and whether they all lie alike.
+struct RowLayout {
   const sla_resnorm *n;
-  bool all;
-  explicit Vectors(const sla_resnorm *n_) : n(n_), all(n_->width % (16 / net_size(n_->dtype)) == 0) {}
-  Vectors &with(const void *p, int64_t ld) {
-    all = all && aligned(p, 16) && (!p || n->rows == 1 || ld % (16 / net_size(n->dtype)) == 0);
+  int vec, shift = 0, step = 0;
+  bool met = false, alike = true;
+  explicit RowLayout(const sla_resnorm *n_) : n(n_), vec((int)(16 / net_size(n_->dtype))) {}
+  RowLayout &with(const void *p, int64_t ld) {
+    if (!p) return *this;
+    const int s = (int)((uintptr_t)p % 16 / net_size(n->dtype)), d = n->rows == 1 ? 0 : (int)(ld % vec);
+    if (!met) shift = s, step = d, met = true;
+    alike = alike && s == shift && d == step;
     return *this;
   }
+  // Rows r, r + classes, ... start at the same place behind a boundary.  (The plan leaves room for a row that starts behind one
+  // only where the width says that rows may.)
+  bool put(ResNormArgs &p) const {
+    p.shift = shift, p.step = step, p.classes = 1;
+    while (p.classes * step % vec) p.classes *= 2;
+    return alike && (n->width % 8 != 0 || (shift == 0 && step == 0));
+  }
 };
-
-bool whole_params(std::initializer_list<const void *> params) {
-  for (const void *p : params)
-    if (!aligned(p, 16)) return false;
-  return true;
-}
 
 template <typename F>
 cudaError_t by_type(const sla_resnorm *n, F &&f) {
@@ -122,14 +132,14 @@ SLA_API sla_status sla_residual_norm(const sla_resnorm *n, const void *block, in
   const size_t ps = net_size(n->param_dtype);
   for (const void *p : {scale, post_weight, post_bias, weight, bias})
     if (!aligned(p, ps)) return SLA_INVALID_ARG;
-  if (!aligned(stats, 4)) return SLA_INVALID_ARG;
+  if (!aligned(stats, 16)) return SLA_INVALID_ARG;
   if (n->rows == 0) return SLA_OK;
   ResNormArgs p = resnorm_args(n, gate);
   p.f = block, p.ldf = ldblock, p.z = z, p.ldz = ldz, p.gate = gate, p.ldg = ldgate;
   p.scale = scale, p.w1 = post_weight, p.b1 = post_bias, p.w2 = weight, p.b2 = bias;
-  p.znew = z_out, p.y = y, p.stats = stats;
-  p.pvec = whole_params({scale, post_weight, post_bias, weight, bias});
-  const bool vec = Vectors(n).with(block, ldblock).with(z, ldz).with(gate, ldgate).with(z_out, n->width).with(y, n->width).all;
+  p.znew = z_out, p.y = y, p.stats = (float4 *)stats;
+  p.bf = row_bytes(n, ldblock), p.bz = row_bytes(n, ldz), p.bg = row_bytes(n, ldgate), p.bw = row_bytes(n, n->width);
+  const bool vec = RowLayout(n).with(block, ldblock).with(z, ldz).with(gate, ldgate).with(z_out, n->width).with(y, n->width).put(p);
   const cudaError_t e = by_type(n, [&](auto t, auto q) {
     return resnorm_forward<decltype(t), decltype(q)>(p, vec, (cudaStream_t)stream);
   });
@@ -161,7 +171,7 @@ SLA_API sla_status sla_residual_norm_backward(const sla_resnorm *n, const void *
   for (const void *p : {scale, post_weight, post_bias, weight, (const void *)dscale, (const void *)dpost_weight,
                         (const void *)dpost_bias, (const void *)dweight, (const void *)dbias})
     if (!aligned(p, ps)) return SLA_INVALID_ARG;
-  if (!aligned(stats, 4) || (n->rows > 0 && !stats) || (dgate && !gate && n->rows > 0)) return SLA_INVALID_ARG;
+  if (!aligned(stats, 16) || (n->rows > 0 && !stats) || (dgate && !gate && n->rows > 0)) return SLA_INVALID_ARG;
   const SumTargets to{{dscale, dpost_weight, dpost_bias, dweight, dbias}};
   const bool sums = dscale || dpost_weight || dpost_bias || dweight || dbias;
   // (a workspace is only needed for sums)
@@ -182,17 +192,18 @@ SLA_API sla_status sla_residual_norm_backward(const sla_resnorm *n, const void *
   ResNormArgs p = resnorm_args(n, gate);
   p.f = block, p.ldf = ldblock, p.z = z, p.ldz = ldz, p.gate = gate, p.ldg = ldgate;
   p.scale = scale, p.w1 = post_weight, p.b1 = post_bias, p.w2 = weight;
-  p.stats = const_cast<float *>(stats), p.dz = dz_out, p.lddz = lddz, p.dy = dy, p.lddy = lddy;
+  p.stats = (float4 *)const_cast<float *>(stats), p.dz = dz_out, p.lddz = lddz, p.dy = dy, p.lddy = lddy;
   p.df = dblock, p.dz_in = dz, p.dgate = dgate;
+  p.bf = row_bytes(n, ldblock), p.bz = row_bytes(n, ldz), p.bg = row_bytes(n, ldgate), p.bw = row_bytes(n, n->width);
+  p.bdz = row_bytes(n, lddz), p.bdy = row_bytes(n, lddy);
   if (sums) {
     const size_t first = row_sum_bytes(n->rows, n->width);
     p.row_sums = first ? (float *)workspace : nullptr;
     p.parts = (float *)((char *)workspace + first);
   }
-  p.pvec = whole_params({scale, post_weight, post_bias, weight});
-  const bool vec = Vectors(n).with(dz_out, lddz).with(dy, lddy).with(block, ldblock).with(z, ldz).with(gate, ldgate)
-                       .with(dblock, n->width).with(dz, n->width).with(dgate, n->width).all;
-  const int grid = backward_grid(n->rows, n->width);
+  const bool vec = RowLayout(n).with(dz_out, lddz).with(dy, lddy).with(block, ldblock).with(z, ldz).with(gate, ldgate)
+                       .with(dblock, n->width).with(dz, n->width).with(dgate, n->width).put(p);
+  const int grid = backward_grid(n->rows, n->width, vec ? p.classes : 1);
   cudaError_t e = by_type(n, [&](auto t, auto q) {
     return resnorm_backward<decltype(t), decltype(q)>(p, vec, grid, st);
   });

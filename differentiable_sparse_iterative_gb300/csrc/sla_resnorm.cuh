@@ -8,19 +8,27 @@
 //   N'(d; xh) = rstd (d - mean d - xh mean(d xh))                                             (rms: without mean d)
 //   dscale = sum D t,  dw1 = sum du fh,  db1 = sum du,  dw2 = sum dy zh,  db2 = sum dy         over the rows
 //
-// Bound by memory: five arrays of rows forward, eight backward, each once.  The backward call forms z' again from f, z and
+// Bound by memory, and by instructions where rows are narrow: five arrays of rows forward, eight backward, each once.  The
+// backward call forms z' again from f, z and
 // the gate (as many bytes as reading z' would cost, and not rounded).  A row lies in the registers of `tpr` threads (a power
-// of two: part of a warp, a warp, or the block), C columns each, in vectors of V; rows that no vector divides, or
-// that start at no 16-byte boundary, are moved element by element in the same kernel (V = 1: neighbouring threads have
-// neighbouring columns, so a warp's accesses stay whole).  A mean of squares is taken of differences from the mean, in a
-// second sweep over the registers.  The next row is asked for while the present one is worked on.  The five sums over the rows
-// stay in registers, then go through the block in a fixed order, then over the blocks in a second kernel: no
-// atomics.  Rows of more than kWidest columns take the *_any kernels, which read a row several times.
+// of two: part of a warp, a warp, or the block), C columns each, in vectors of V.  The parameters stand in shared memory in
+// float32, in the order in which the threads read them (read from L1 in their own type and converted again for every row they
+// made up a third of the instructions).  A mean of squares is taken of differences from the mean, in a
+// second sweep over the registers.  The next rows are asked for while the present ones are worked on.  The five sums over the
+// rows stay in registers, then go through the block in a fixed order, then over the blocks in a second kernel: no
+// atomics.
+//
+// Widths that no vector divides: row r starts (r ld) mod V elements behind a 16-byte boundary, which repeats every `classes`
+// rows.  A block takes the rows of one class, so that its threads keep their columns: vector i of a row starts `shift`
+// columns before column i V, and the first and last, which reach beyond the row, are moved element by element.  Arrays whose
+// rows do not all start at the same place behind a boundary are moved element by element throughout (V = 1: neighbouring threads
+// have neighbouring columns), and rows of more than kWidest columns take the *_any kernels, which read a row several times.
 #pragma once
 
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sla_act.cuh"
 #include "sla_common.cuh"
@@ -31,7 +39,7 @@ namespace sla {
 
 constexpr int kNormBlock = 256;    // threads of a block while a row takes no more
 constexpr int kNormThreads = 512;  // of a block that shares one row
-constexpr int kWidest = kNormThreads * 16;
+constexpr int kWidest = kNormThreads * 16 - 8;  // (a row may reach into one vector more)
 constexpr int kNormSums = 5;       // dscale, dw1, db1, dw2, db2
 constexpr int kAnyParts = 16;      // parts of the rows of the *_any column sums
 
@@ -42,13 +50,14 @@ struct ResNormArgs {
   int64_t width;
   int tpr;
   int rms, post, act;
-  int pvec;                    // parameters may be read in whole vectors
+  int classes, shift, step;    // rows of one class start (shift + class * step) mod V behind a vector's boundary
   float eps;
   const void *f, *z, *gate;    // T [rows][ld]
   int64_t ldf, ldz, ldg;
   const void *scale, *w1, *b1, *w2, *b2;  // P [width] or NULL: 1, 1, 0, 1, 0
   void *znew, *y;              // T [rows][width]; y NULL: no second norm
-  float *stats;                // [4][rows]: mean and rstd of f's norm and of z's, or NULL (forward)
+  uint32_t bf, bz, bg, bdz, bdy, bw;  // bytes between the rows of f, z, gate, dz, dy and of the results
+  float4 *stats;               // [rows]: mean and rstd of f's norm and of z's, or NULL (forward)
   const void *dz, *dy;         // T [rows][ld] or NULL: zero
   int64_t lddz, lddy;
   void *df, *dz_in, *dgate;    // T [rows][width] or NULL
@@ -56,9 +65,10 @@ struct ResNormArgs {
   float *row_sums;             // *_any: [2][rows] means of dy w2 and of dy w2 zh
 };
 
+// vec: p.classes, p.shift and p.step say how the rows of all arrays lie; else they are moved element by element.
 template <typename T, typename P>
 cudaError_t resnorm_forward(ResNormArgs p, bool vec, cudaStream_t st);
-// Blocks whose partial sums there are, and the launch.
+// grid: blocks, each of which leaves partial sums (a multiple of the classes).
 template <typename T, typename P>
 cudaError_t resnorm_backward(ResNormArgs p, bool vec, int grid, cudaStream_t st);
 
@@ -69,16 +79,24 @@ struct ResNormPlan {
 
 inline ResNormPlan resnorm_plan(int64_t width) {
   if (width > kWidest) return {0, kNormThreads, kNormThreads};
-  const int columns = width > kNormThreads * 8 ? 16 : 8;
+  const int64_t reach = width % 8 ? width + 7 : width;  // a row that starts behind a boundary reaches into one vector more
+  const int columns = reach > kNormThreads * 8 ? 16 : 8;
   int tpr = 1;
-  while (tpr * columns < width) tpr <<= 1;
+  while (tpr * columns < reach) tpr <<= 1;
   return {columns, tpr, std::max(tpr, kNormBlock)};
+}
+
+// Blocks that fill the GPU with `threads` a multiprocessor, in whole sets of classes, no more than there are rows for.
+inline int resnorm_grid(const ResNormPlan &pl, int64_t rows, int64_t rows_a_turn, int classes, int threads) {
+  const int64_t most = (int64_t)sm_count() * std::max(1, threads / pl.block);
+  const int64_t need = ((rows + classes - 1) / classes + rows_a_turn - 1) / rows_a_turn;
+  return (int)(std::max<int64_t>(1, std::min(most / classes, need)) * classes);
 }
 
 // ------------------------------------------------------------------ pieces
 
 // Sums over the tpr threads of a group, the same values in each of them.  `slot` (16 K floats) must not be in
-// use by an earlier sum that a thread still reads; for tpr > 32 every thread of the block takes part.
+// use by an earlier sum that a thread still reads.  Groups of several warps wait for their own alone.
 template <int K>
 __device__ __forceinline__ void row_sums(float (&v)[K], int tpr, float *slot) {
 #pragma unroll
@@ -92,7 +110,7 @@ __device__ __forceinline__ void row_sums(float (&v)[K], int tpr, float *slot) {
   if (lane == 0)
 #pragma unroll
     for (int k = 0; k < K; ++k) slot[k * 16 + warp] = v[k];
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / tpr), "r"(tpr) : "memory");
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = lane < warps ? slot[k * 16 + first + lane] : 0.f;
 #pragma unroll
@@ -103,7 +121,34 @@ __device__ __forceinline__ void row_sums(float (&v)[K], int tpr, float *slot) {
   for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
 }
 
-// C columns of a row as loaded, in vectors of V: vector i holds columns (t + i tpr) V and those behind it.
+// A thread's columns: C / V vectors, vector i from column (t + i tpr) V - shift on.
+template <int V, int C>
+struct Columns {
+  static constexpr int n = C / V;
+  int t, tpr, width, shift;
+  uint32_t whole, some;  // vectors that lie in the row, or at least reach into it
+  __device__ __forceinline__ Columns(int t_, int tpr_, int width_, int shift_) : t(t_), tpr(tpr_), width(width_), shift(shift_) {
+    whole = some = 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int c = first(i);
+      whole |= (c >= 0 && c + V <= width ? 1u : 0u) << i;
+      some |= (c + V > 0 && c < width ? 1u : 0u) << i;
+    }
+  }
+  __device__ __forceinline__ int first(int i) const { return (t + i * tpr) * V - shift; }
+  __device__ __forceinline__ int column(int j) const { return first(j / V) + j % V; }
+  __device__ __forceinline__ bool inside(int j) const { return column(j) >= 0 && column(j) < width; }
+  __device__ __forceinline__ bool full() const { return whole == (1u << n) - 1; }
+  // What lies outside of the row becomes zero.
+  __device__ __forceinline__ void mask(float2 (&v)[C / 2]) const {
+    if (full()) return;
+#pragma unroll
+    for (int j = 0; j < C; j += 2) v[j / 2] = make_float2(inside(j) ? v[j / 2].x : 0.f, inside(j + 1) ? v[j / 2].y : 0.f);
+  }
+};
+
+// C columns of a row as loaded.
 template <typename T, int V, int C>
 struct RowPart {
   static constexpr int n = C / V;
@@ -114,15 +159,20 @@ struct RowPart {
 #pragma unroll
       for (int k = 0; k < V; ++k) v[i].v[k] = from_f32<T>(0.f);
   }
-  __device__ __forceinline__ void load(const T *row, int t, int tpr, int width, bool there) {
+  __device__ __forceinline__ void load(const T *row, const Columns<V, C> &q, bool there) {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-      const int c = (t + i * tpr) * V;
-      if (there && c < width) {
+      const int c = q.first(i);
+      if (there && (q.whole >> i & 1)) {
         v[i] = *reinterpret_cast<const Pack<T, V> *>(row + c);
       } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) v[i].v[k] = from_f32<T>(0.f);
+        if (V > 1 && there && (q.some >> i & 1)) {
+#pragma unroll
+          for (int k = 0; k < V; ++k)
+            if (c + k >= 0 && c + k < q.width) v[i].v[k] = row[c + k];
+        }
       }
     }
   }
@@ -141,58 +191,78 @@ struct RowPart {
 };
 
 template <typename T, int V, int C>
-__device__ __forceinline__ void store_part(T *row, const float2 (&o)[C / 2], int t, int tpr, int width) {
+__device__ __forceinline__ void store_part(T *row, const float2 (&o)[C / 2], const Columns<V, C> &q) {
 #pragma unroll
   for (int i = 0; i < C / V; ++i) {
-    const int c = (t + i * tpr) * V;
-    if (c >= width) continue;
-    Pack<T, V> q;
+    const int c = q.first(i);
+    if (!(q.some >> i & 1)) continue;
+    Pack<T, V> w;
     if constexpr (V == 1) {
-      q.v[0] = from_f32<T>(i % 2 ? o[i / 2].y : o[i / 2].x);
+      w.v[0] = from_f32<T>(i % 2 ? o[i / 2].y : o[i / 2].x);
     } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int k = 0; k < V; k += 2)
-        *reinterpret_cast<uint32_t *>(&q.v[k]) = pair16(o[(i * V + k) / 2].x, o[(i * V + k) / 2].y, T{});
+        *reinterpret_cast<uint32_t *>(&w.v[k]) = pair16(o[(i * V + k) / 2].x, o[(i * V + k) / 2].y, T{});
     } else {
 #pragma unroll
-      for (int k = 0; k < V; k += 2) q.v[k] = o[(i * V + k) / 2].x, q.v[k + 1] = o[(i * V + k) / 2].y;
+      for (int k = 0; k < V; k += 2) w.v[k] = o[(i * V + k) / 2].x, w.v[k + 1] = o[(i * V + k) / 2].y;
     }
-    *reinterpret_cast<Pack<T, V> *>(row + c) = q;
+    if (q.whole >> i & 1) {
+      *reinterpret_cast<Pack<T, V> *>(row + c) = w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (c + k >= 0 && c + k < q.width) row[c + k] = w.v[k];
+    }
   }
 }
 
-// A parameter's values at a thread's columns, `other` where there is none, zero outside of the row.
-template <typename P, int V, int C>
-__device__ __forceinline__ void param_part(const P *p, float other, int t, int tpr, int width, bool vec,
-                                           float2 (&o)[C / 2]) {
-  float e[C];
+// Parameters in shared memory ([K][C / 4][tpr]): four columns of a thread beside those of the next thread, zero outside of the
+// row.  Bit k of `ones`: what parameter k is where it is absent.  All K are asked for at once: a single row waits once.
+template <typename P, int V, int C, int K>
+__device__ __forceinline__ void stage_params(float4 *sm, const void *const (&p)[K], uint32_t ones, int tpr, int width,
+                                             int shift) {
+  const int each = C / 4 * tpr;
+  for (int i = threadIdx.x; i < each; i += blockDim.x) {
+    const int t = i & (tpr - 1), h = i / tpr;
+    float e[K][4];
 #pragma unroll
-  for (int i = 0; i < C / V; ++i) {
-    const int c = (t + i * tpr) * V;
-    if (V > 1 && vec && p && c < width) {
-      float q[V];
-      load_f32<P, V>(p + c, q);
+    for (int j = 0; j < 4; ++j) {
+      const int c = (t + (4 * h + j) / V * tpr) * V + (4 * h + j) % V - shift;
+      const bool in = c >= 0 && c < width;
 #pragma unroll
-      for (int k = 0; k < V; ++k) e[i * V + k] = q[k];
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) e[i * V + k] = c < width ? (p ? to_f32(p[c + k]) : other) : 0.f;
+      for (int k = 0; k < K; ++k) {
+        e[k][j] = in && (ones >> k & 1) ? 1.f : 0.f;
+        if (in && p[k]) e[k][j] = to_f32(((const P *)p[k])[c]);
+      }
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k) sm[k * each + i] = make_float4(e[k][0], e[k][1], e[k][2], e[k][3]);
   }
-#pragma unroll
-  for (int j = 0; j < C / 2; ++j) o[j] = f2(e[2 * j], e[2 * j + 1]);
 }
-
-// Which of a thread's columns there are: one or zero.
-template <int V, int C>
-__device__ __forceinline__ void inside_part(int t, int tpr, int width, float2 (&o)[C / 2]) {
+template <int C>
+__device__ __forceinline__ void param_part(const float4 *sm, int t, int tpr, float2 (&o)[C / 2]) {
 #pragma unroll
-  for (int j = 0; j < C; j += 2)
-    o[j / 2] = f2((t + j / V * tpr) * V < width ? 1.f : 0.f, (t + (j + 1) / V * tpr) * V < width ? 1.f : 0.f);
+  for (int h = 0; h < C / 4; ++h) {
+    const float4 q = sm[h * tpr + t];
+    o[2 * h] = f2(q.x, q.y), o[2 * h + 1] = f2(q.z, q.w);
+  }
 }
 
 __device__ __forceinline__ float2 both(float v) { return f2(v, v); }
-__device__ __forceinline__ float2 neg2(float2 v) { return f2(-v.x, -v.y); }
+
+// The smaller of two, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Row `row` of rows `bytes` apart: one wide multiply-add.
+template <typename T>
+__device__ __forceinline__ T *row_at(const void *base, uint32_t row, uint32_t bytes) {
+  return (T *)((char *)const_cast<void *>(base) + (uint64_t)row * bytes);
+}
 
 // act(g) and, if asked for, act'(g).
 template <bool Derivative>
@@ -202,226 +272,281 @@ __device__ __forceinline__ void gate_act(int act, float2 g, float2 &a, float2 &d
     if (Derivative) da = both(1.f);
     return;
   }
-  const float2 s = sigmoid2(g);
-  const float2 r = sigmoid2(neg2(g));  // 1 - s, right relative to itself
-  if (act == kGateSigmoid) {
-    a = s;
-    if (Derivative) da = mul2(s, r);
-  } else {
-    a = mul2(g, s);
-    if (Derivative) da = fma2(a, r, s);
+  // e = exp(-g), at most 2^126, so that e s is 1 - s, right relative to itself, and never infinity times zero
+  const float2 m = mul2(g, both(-1.4426950408889634f));
+  const float2 e = f2(ex2_approx(min_nan(m.x, 126.f)), ex2_approx(min_nan(m.y, 126.f)));
+  const float2 d = add2(e, both(1.f)), s = f2(rcp_approx(d.x), rcp_approx(d.y));
+  a = act == kGateSigmoid ? s : mul2(g, s);
+  if (Derivative) {
+    const float2 r = mul2(e, s);
+    da = act == kGateSigmoid ? mul2(s, r) : fma2(a, r, s);
   }
 }
 
-// v becomes (v - mu) rstd; returns mu and rstd.  inside: one where there is a column.
-template <int H>
-__device__ __forceinline__ void norm_row(float2 (&v)[H], const float2 (&inside)[H], bool rms, float inv, float eps,
-                                         int tpr, float *slot0, float *slot1, float &mu, float &rstd) {
-  mu = 0.f;
+// The rows of v become (v - mu) rstd.
+template <int V, int C, int R>
+__device__ __forceinline__ void norm_rows(float2 (&v)[R][C / 2], const Columns<V, C> &q, bool rms, float inv, float eps,
+                                          float *slot0, float *slot1, float (&mu)[R], float (&rstd)[R]) {
+  constexpr int H = C / 2;
+  float s[R];
   if (!rms) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 a = both(0.f);
+#pragma unroll
+      for (int j = 0; j < H; ++j) a = add2(a, v[r][j]);
+      s[r] = a.x + a.y;
+    }
+    row_sums(s, q.tpr, slot0);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    mu[r] = rms ? 0.f : s[r] * inv;
+    if (!rms) {
+#pragma unroll
+      for (int j = 0; j < H; ++j) v[r][j] = add2(v[r][j], both(-mu[r]));
+      q.mask(v[r]);
+    }
     float2 a = both(0.f);
 #pragma unroll
-    for (int j = 0; j < H; ++j) a = add2(a, v[j]);
-    float s[1] = {a.x + a.y};
-    row_sums(s, tpr, slot0);
-    mu = s[0] * inv;
-#pragma unroll
-    for (int j = 0; j < H; ++j) v[j] = mul2(add2(v[j], both(-mu)), inside[j]);
+    for (int j = 0; j < H; ++j) a = fma2(v[r][j], v[r][j], a);
+    s[r] = a.x + a.y;
   }
-  float2 q = both(0.f);
+  row_sums(s, q.tpr, slot1);
 #pragma unroll
-  for (int j = 0; j < H; ++j) q = fma2(v[j], v[j], q);
-  float s[1] = {q.x + q.y};
-  row_sums(s, tpr, slot1);
-  rstd = rsqrtf(s[0] * inv + eps);  // 2 units in the last place
+  for (int r = 0; r < R; ++r) {
+    rstd[r] = rsqrtf(s[r] * inv + eps);  // 2 units in the last place
 #pragma unroll
-  for (int j = 0; j < H; ++j) v[j] = mul2(v[j], both(rstd));
+    for (int j = 0; j < H; ++j) v[r][j] = mul2(v[r][j], both(rstd[r]));
+  }
 }
+
+// Which rows a block's groups take: group g of a block row `row`, `step` rows on in the next turn; `next` between the rows of
+// a bundle of R.
+struct Turns {
+  uint32_t lead, row, step, next;  // (there are less than 2^31 rows)
+  template <int R>
+  __device__ __forceinline__ static Turns of(const ResNormArgs &p, int groups, std::integral_constant<int, R>) {
+    Turns w;
+    const int cls = blockIdx.x % p.classes;
+    w.next = groups * p.classes;
+    w.lead = (blockIdx.x / p.classes) * R * w.next + cls;
+    w.row = w.lead + threadIdx.x / p.tpr * p.classes;
+    w.step = (gridDim.x / p.classes) * R * w.next;
+    return w;
+  }
+};
 
 // ------------------------------------------------------------------ kernels
 
-template <typename T, typename P, int V, int C>
+// R: rows of a group at a time, whose sums go together and which share what is read of the parameters.
+template <typename T, typename P, int V, int C, int R>
 __global__ void __launch_bounds__(kNormThreads, 1) resnorm_forward_rows(const __grid_constant__ ResNormArgs p) {
   constexpr int H = C / 2;
-  __shared__ float slots[2][4][16];
+  extern __shared__ float4 params[];  // [5][C / 4][tpr]: scale, w1, b1, w2, b2
+  __shared__ float slots[2][4][R * 16];
   const int tpr = p.tpr, width = (int)p.width, groups = blockDim.x / tpr;
-  const int t = threadIdx.x & (tpr - 1);
+  const int shift = V > 1 ? (p.shift + (blockIdx.x % p.classes) * p.step) % V : 0;
+  const Columns<V, C> q(threadIdx.x & (tpr - 1), tpr, width, shift);
   const float inv = 1.f / (float)width;
-  float2 inside[H];
-  inside_part<V, C>(t, tpr, width, inside);
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t lead = (int64_t)blockIdx.x * groups, row = lead + threadIdx.x / tpr;
-  RowPart<T, V, C> rf, rz, rg;
-  rg.clear();
-  auto ask = [&](int64_t r) {
-    const bool there = r < p.rows;
-    rf.load((const T *)p.f + r * p.ldf, t, tpr, width, there);
-    if (p.act != kNoGate) rg.load((const T *)p.gate + r * p.ldg, t, tpr, width, there);
-    rz.load((const T *)p.z + r * p.ldz, t, tpr, width, there);
+  const int each = C / 4 * tpr;
+  const Turns w = Turns::of(p, groups, std::integral_constant<int, R>{});
+  RowPart<T, V, C> rf[R], rz[R], rg[R];
+  const uint32_t rows = (uint32_t)p.rows;
+  auto ask = [&](uint32_t row) {
+#pragma unroll
+    for (int r = 0; r < R; ++r, row += w.next) {
+      const bool there = row < rows;
+      rf[r].load(row_at<T>(p.f, (uint32_t)row, p.bf), q, there);
+      if (p.act != kNoGate) rg[r].load(row_at<T>(p.gate, (uint32_t)row, p.bg), q, there);
+      rz[r].load(row_at<T>(p.z, (uint32_t)row, p.bz), q, there);
+    }
   };
-  ask(row);
+#pragma unroll
+  for (int r = 0; r < R; ++r) rg[r].clear();
+  ask(w.row);
+  const void *const from[5] = {p.scale, p.w1, p.b1, p.w2, p.b2};
+  stage_params<P, V, C, 5>(params, from, 0b01011, tpr, width, shift);
+  __syncthreads();
   int turn = 0;  // the slots alternate, so a turn's sums never meet the previous one's reads
   // every thread of a block makes the same number of turns (the sums need whole warps and blocks)
-  for (; lead < p.rows; lead += step, row += step, turn ^= 1) {
-    float2 v[H], z[H], w[H];
-    rf.values(v);
-    rz.values(z);
-    float2 a[H];
-    if (p.act != kNoGate) {
-      float2 g[H], none;
-      rg.values(g);
+  uint32_t row = w.row;
+  for (uint32_t lead = w.lead; lead < rows; lead += w.step, row += w.step, turn ^= 1) {
+    float2 v[R][H], z[R][H], a[R][H], k[H], k2[H];
 #pragma unroll
-      for (int j = 0; j < H; ++j) gate_act<false>(p.act, g[j], a[j], none);
+    for (int r = 0; r < R; ++r) {
+      rf[r].values(v[r]);
+      rz[r].values(z[r]);
+      if (p.act != kNoGate) rg[r].values(a[r]);
     }
-    if (lead + step < p.rows) ask(row + step);
-    float mu1 = 0.f, rs1 = 0.f, mu2 = 0.f, rs2 = 0.f;
+    if (lead + w.step < rows) ask(row + w.step);
+    if (p.act != kNoGate)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          float2 none;
+          gate_act<false>(p.act, a[r][j], a[r][j], none);
+        }
+    float mu1[R] = {}, rs1[R] = {}, mu2[R] = {}, rs2[R] = {};
     if (p.post) {
-      norm_row<H>(v, inside, p.rms, inv, p.eps, tpr, slots[turn][0], slots[turn][1], mu1, rs1);
-      param_part<P, V, C>((const P *)p.w1, 1.f, t, tpr, width, p.pvec, w);
+      norm_rows<V, C, R>(v, q, p.rms, inv, p.eps, slots[turn][0], slots[turn][1], mu1, rs1);
+      param_part<C>(params + each, q.t, tpr, k);
+      param_part<C>(params + 2 * each, q.t, tpr, k2);
 #pragma unroll
-      for (int j = 0; j < H; ++j) v[j] = mul2(v[j], w[j]);
-      if (p.b1) {
-        param_part<P, V, C>((const P *)p.b1, 0.f, t, tpr, width, p.pvec, w);
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int j = 0; j < H; ++j) v[j] = add2(v[j], w[j]);
-      }
+        for (int j = 0; j < H; ++j) v[r][j] = fma2(v[r][j], k[j], k2[j]);
     }
-    if (p.act != kNoGate) {
+    param_part<C>(params, q.t, tpr, k);
 #pragma unroll
-      for (int j = 0; j < H; ++j) v[j] = mul2(v[j], a[j]);
+    for (int r = 0; r < R; ++r) {
+      if (p.act != kNoGate)
+#pragma unroll
+        for (int j = 0; j < H; ++j) v[r][j] = mul2(v[r][j], a[r][j]);
+#pragma unroll
+      for (int j = 0; j < H; ++j) v[r][j] = fma2(v[r][j], k[j], z[r][j]);
+      const uint32_t at = row + r * w.next;
+      if (at < rows) store_part<T, V, C>(row_at<T>(p.znew, at, p.bw), v[r], q);
     }
-    param_part<P, V, C>((const P *)p.scale, 1.f, t, tpr, width, p.pvec, w);
-#pragma unroll
-    for (int j = 0; j < H; ++j) v[j] = fma2(v[j], w[j], z[j]);
-    if (row < p.rows) store_part<T, V, C>((T *)p.znew + row * width, v, t, tpr, width);
     if (p.y) {
-      norm_row<H>(v, inside, p.rms, inv, p.eps, tpr, slots[turn][2], slots[turn][3], mu2, rs2);
-      param_part<P, V, C>((const P *)p.w2, 1.f, t, tpr, width, p.pvec, w);
+      norm_rows<V, C, R>(v, q, p.rms, inv, p.eps, slots[turn][2], slots[turn][3], mu2, rs2);
+      param_part<C>(params + 3 * each, q.t, tpr, k);
+      param_part<C>(params + 4 * each, q.t, tpr, k2);
 #pragma unroll
-      for (int j = 0; j < H; ++j) v[j] = mul2(v[j], w[j]);
-      if (p.b2) {
-        param_part<P, V, C>((const P *)p.b2, 0.f, t, tpr, width, p.pvec, w);
+      for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int j = 0; j < H; ++j) v[j] = add2(v[j], w[j]);
+        for (int j = 0; j < H; ++j) v[r][j] = fma2(v[r][j], k[j], k2[j]);
+        const uint32_t at = row + r * w.next;
+        if (at < rows) store_part<T, V, C>(row_at<T>(p.y, at, p.bw), v[r], q);
       }
-      if (row < p.rows) store_part<T, V, C>((T *)p.y + row * width, v, t, tpr, width);
     }
-    if (p.stats && t == 0 && row < p.rows) {
-      p.stats[row] = mu1, p.stats[p.rows + row] = rs1;
-      p.stats[2 * p.rows + row] = mu2, p.stats[3 * p.rows + row] = rs2;
-    }
+    if (p.stats && q.t == 0)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t at = row + r * w.next;
+        if (at >= rows) continue;
+        p.stats[at] = make_float4(mu1[r], rs1[r], mu2[r], rs2[r]);
+      }
   }
 }
 
 template <typename T, typename P, int V, int C>
 __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const __grid_constant__ ResNormArgs p) {
   constexpr int H = C / 2;
-  extern __shared__ float cols[];  // more than one group: [kNormSums][width]
+  extern __shared__ float4 params[];  // [4][C / 4][tpr]: scale, w1, b1, w2; then, with more than one group, [kNormSums][width]
   __shared__ float slots[2][2][32];
   grid_dependency_launch();  // the sums over blocks start as multiprocessors become free, and wait there
   const int tpr = p.tpr, width = (int)p.width, groups = blockDim.x / tpr;
-  const int t = threadIdx.x & (tpr - 1);
+  const int shift = V > 1 ? (p.shift + (blockIdx.x % p.classes) * p.step) % V : 0;
+  const Columns<V, C> q(threadIdx.x & (tpr - 1), tpr, width, shift);
   const float inv = 1.f / (float)width;
-  float2 inside[H], sums[kNormSums][H];
-  inside_part<V, C>(t, tpr, width, inside);
+  const int each = C / 4 * tpr;
+  const Turns w = Turns::of(p, groups, std::integral_constant<int, 1>{});
+  float2 sums[kNormSums][H];
 #pragma unroll
   for (int k = 0; k < kNormSums; ++k)
 #pragma unroll
     for (int j = 0; j < H; ++j) sums[k][j] = both(0.f);
-  const int64_t step = (int64_t)gridDim.x * groups;
-  int64_t lead = (int64_t)blockIdx.x * groups, row = lead + threadIdx.x / tpr;
+  const uint32_t rows = (uint32_t)p.rows;  // (below 2^31)
   RowPart<T, V, C> rf, rz, rg, rdz, rdy;
-  float st[4];
+  float4 st;
   rg.clear();
   rdz.clear();
   rdy.clear();
-  auto ask = [&](int64_t r) {
-    const bool there = r < p.rows;
-    rf.load((const T *)p.f + r * p.ldf, t, tpr, width, there);
-    rz.load((const T *)p.z + r * p.ldz, t, tpr, width, there);
-    if (p.act != kNoGate) rg.load((const T *)p.gate + r * p.ldg, t, tpr, width, there);
-    if (p.dz) rdz.load((const T *)p.dz + r * p.lddz, t, tpr, width, there);
-    if (p.dy) rdy.load((const T *)p.dy + r * p.lddy, t, tpr, width, there);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) st[k] = there ? p.stats[k * p.rows + r] : 0.f;
+  auto ask = [&](uint32_t r) {
+    const bool there = r < rows;
+    rf.load(row_at<T>(p.f, r, p.bf), q, there);
+    if (p.act != kNoGate) rg.load(row_at<T>(p.gate, r, p.bg), q, there);
+    rz.load(row_at<T>(p.z, r, p.bz), q, there);
+    if (p.dy) rdy.load(row_at<T>(p.dy, r, p.bdy), q, there);
+    if (p.dz) rdz.load(row_at<T>(p.dz, r, p.bdz), q, there);
+    st = there ? p.stats[r] : make_float4(0.f, 0.f, 0.f, 0.f);
   };
-  ask(row);
+  ask(w.row);
+  const void *const from[4] = {p.scale, p.w1, p.b1, p.w2};
+  stage_params<P, V, C, 4>(params, from, 0b1011, tpr, width, shift);
+  __syncthreads();
   int turn = 0;
-  for (; lead < p.rows; lead += step, row += step, turn ^= 1) {
-    float2 fh[H], u[H], a[H], da[H], sc[H], d[H];
-    const float mu1 = st[0], rs1 = st[1], mu2 = st[2], rs2 = st[3];
+  uint32_t row = w.row;
+  for (uint32_t lead = w.lead; lead < rows; lead += w.step, row += w.step, turn ^= 1) {
+    // t = act(gate) u;  sa = scale act(gate), by which D becomes du;  sg = scale u act'(gate), by which it becomes dgate
+    float2 fh[H], t[H], sa[H], sg[H], d[H], k[H];
+    const float mu1 = st.x, rs1 = st.y, mu2 = st.z, rs2 = st.w;
     rf.values(fh);
     if (p.post) {
-      float2 w[H];
-      // outside of the row everything is zero, as (0 - mean) rstd would not be
 #pragma unroll
-      for (int j = 0; j < H; ++j) fh[j] = mul2(add2(fh[j], both(-mu1)), mul2(inside[j], both(rs1)));
-      param_part<P, V, C>((const P *)p.w1, 1.f, t, tpr, width, p.pvec, w);
+      for (int j = 0; j < H; ++j) fh[j] = mul2(add2(fh[j], both(-mu1)), both(rs1));
+      q.mask(fh);  // where there is no row, (0 - mean) rstd may pass the largest float32
+      param_part<C>(params + each, q.t, tpr, k);
+      param_part<C>(params + 2 * each, q.t, tpr, t);
 #pragma unroll
-      for (int j = 0; j < H; ++j) u[j] = mul2(fh[j], w[j]);
-      if (p.b1) {
-        param_part<P, V, C>((const P *)p.b1, 0.f, t, tpr, width, p.pvec, w);
-#pragma unroll
-        for (int j = 0; j < H; ++j) u[j] = add2(u[j], w[j]);
-      }
+      for (int j = 0; j < H; ++j) t[j] = fma2(fh[j], k[j], t[j]);
     } else {
 #pragma unroll
-      for (int j = 0; j < H; ++j) u[j] = fh[j];
+      for (int j = 0; j < H; ++j) t[j] = fh[j];
     }
-#pragma unroll
-    for (int j = 0; j < H; ++j) a[j] = both(1.f), da[j] = both(0.f);
+    param_part<C>(params, q.t, tpr, k);
     if (p.act != kNoGate) {
       float2 g[H];
       rg.values(g);
 #pragma unroll
-      for (int j = 0; j < H; ++j) gate_act<true>(p.act, g[j], a[j], da[j]);
+      for (int j = 0; j < H; ++j) {
+        float2 a, da;
+        gate_act<true>(p.act, g[j], a, da);
+        sg[j] = mul2(mul2(k[j], t[j]), da);
+        sa[j] = mul2(k[j], a);
+        t[j] = mul2(t[j], a);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < H; ++j) sg[j] = both(0.f), sa[j] = k[j];
     }
-    param_part<P, V, C>((const P *)p.scale, 1.f, t, tpr, width, p.pvec, sc);
     rdz.values(d);
     if (p.dy) {
-      float2 zh[H], dy[H], w[H];
+      float2 zh[H], dy[H];
       rz.values(zh);
       rdy.values(dy);
-      param_part<P, V, C>((const P *)p.w2, 1.f, t, tpr, width, p.pvec, w);
+#pragma unroll
+      for (int j = 0; j < H; ++j) zh[j] = mul2(add2(fma2(t[j], k[j], zh[j]), both(-mu2)), both(rs2));
+      q.mask(zh);
+      param_part<C>(params + 3 * each, q.t, tpr, k);
       float2 s1 = both(0.f), s2 = s1;
 #pragma unroll
       for (int j = 0; j < H; ++j) {
-        zh[j] = fma2(mul2(u[j], a[j]), sc[j], zh[j]);
-        zh[j] = mul2(add2(zh[j], both(-mu2)), mul2(inside[j], both(rs2)));
         sums[3][j] = fma2(dy[j], zh[j], sums[3][j]);
         sums[4][j] = add2(sums[4][j], dy[j]);
-        dy[j] = mul2(dy[j], w[j]);
+        dy[j] = mul2(dy[j], k[j]);
         s1 = add2(s1, dy[j]);
         s2 = fma2(dy[j], zh[j], s2);
       }
+      if (lead + w.step < rows) ask(row + w.step);
       float s[2] = {s1.x + s1.y, s2.x + s2.y};
       row_sums(s, tpr, slots[turn][0]);
       const float m1 = p.rms ? 0.f : -s[0] * inv, m2 = -s[1] * inv;
 #pragma unroll
       for (int j = 0; j < H; ++j)
         d[j] = fma2(fma2(zh[j], both(m2), add2(dy[j], both(m1))), both(rs2), d[j]);
+    } else if (lead + w.step < rows) {
+      ask(row + w.step);
     }
-    const int64_t at = row * width, present = row;
-    const bool live = row < p.rows;
-    if (live && p.dz_in) store_part<T, V, C>((T *)p.dz_in + at, d, t, tpr, width);
+    const bool live = row < rows;
+    if (live && p.dz_in) store_part<T, V, C>(row_at<T>(p.dz_in, row, p.bw), d, q);
 #pragma unroll
     for (int j = 0; j < H; ++j) {
-      sums[0][j] = fma2(d[j], mul2(a[j], u[j]), sums[0][j]);
-      d[j] = mul2(d[j], sc[j]);
-      u[j] = mul2(mul2(d[j], u[j]), da[j]);  // dgate
-      d[j] = mul2(d[j], a[j]);               // du
+      sums[0][j] = fma2(d[j], t[j], sums[0][j]);
+      sg[j] = mul2(sg[j], d[j]);
+      d[j] = mul2(d[j], sa[j]);
     }
-    if (live && p.dgate) store_part<T, V, C>((T *)p.dgate + at, u, t, tpr, width);
-    if (lead + step < p.rows) ask(present + step);
+    if (live && p.dgate) store_part<T, V, C>(row_at<T>(p.dgate, row, p.bw), sg, q);
     if (p.post) {
-      float2 w[H];
-      param_part<P, V, C>((const P *)p.w1, 1.f, t, tpr, width, p.pvec, w);
+      param_part<C>(params + each, q.t, tpr, k);
       float2 s1 = both(0.f), s2 = s1;
 #pragma unroll
       for (int j = 0; j < H; ++j) {
         sums[1][j] = fma2(d[j], fh[j], sums[1][j]);
         sums[2][j] = add2(sums[2][j], d[j]);
-        d[j] = mul2(d[j], w[j]);
+        d[j] = mul2(d[j], k[j]);
         s1 = add2(s1, d[j]);
         s2 = fma2(d[j], fh[j], s2);
       }
@@ -431,17 +556,16 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
 #pragma unroll
       for (int j = 0; j < H; ++j) d[j] = mul2(fma2(fh[j], both(m2), add2(d[j], both(m1))), both(rs1));
     }
-    if (live && p.df) store_part<T, V, C>((T *)p.df + at, d, t, tpr, width);
+    if (live && p.df) store_part<T, V, C>(row_at<T>(p.df, row, p.bw), d, q);
   }
   if (!p.parts) return;
-  float *to = p.parts + (int64_t)blockIdx.x * kNormSums * width;
-  auto column = [&](int j) { return (t + j / V * tpr) * V + j % V; };
+  float *to = p.parts + (int64_t)blockIdx.x * kNormSums * width, *cols = (float *)(params + 4 * each);
   if (groups == 1) {
 #pragma unroll
     for (int k = 0; k < kNormSums; ++k)
 #pragma unroll
       for (int j = 0; j < C; ++j)
-        if (column(j) < width) to[k * width + column(j)] = j % 2 ? sums[k][j / 2].y : sums[k][j / 2].x;
+        if (q.inside(j)) to[k * width + q.column(j)] = j % 2 ? sums[k][j / 2].y : sums[k][j / 2].x;
     return;
   }
   // the groups of a warp by shuffles, then the warps one after another
@@ -460,9 +584,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
       for (int k = 0; k < kNormSums; ++k)
 #pragma unroll
         for (int j = 0; j < C; ++j)
-          if (column(j) < width) {
+          if (q.inside(j)) {
             const float s = j % 2 ? sums[k][j / 2].y : sums[k][j / 2].x;
-            float *c = cols + k * width + column(j);
+            float *c = cols + k * width + q.column(j);
             *c = from ? *c + s : s;
           }
     __syncthreads();
@@ -536,10 +660,7 @@ __global__ void __launch_bounds__(kNormThreads) resnorm_forward_any(const __grid
                                                     (p.b2 ? to_f32(((const P *)p.b2)[c]) : 0.f));
       }
     }
-    if (p.stats && threadIdx.x == 0) {
-      p.stats[row] = mu1, p.stats[p.rows + row] = rs1;
-      p.stats[2 * p.rows + row] = mu2, p.stats[3 * p.rows + row] = rs2;
-    }
+    if (p.stats && threadIdx.x == 0) p.stats[row] = make_float4(mu1, rs1, mu2, rs2);
     __syncthreads();  // the slots are free again
   }
 }
@@ -563,8 +684,8 @@ __global__ void __launch_bounds__(kNormThreads) resnorm_backward_any(const __gri
   __shared__ float slots[4][16];
   const float inv = 1.f / (float)p.width;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const float mu1 = p.stats[row], rs1 = p.stats[p.rows + row];
-    const float mu2 = p.stats[2 * p.rows + row], rs2 = p.stats[3 * p.rows + row];
+    const float4 st = p.stats[row];
+    const float mu1 = st.x, rs1 = st.y, mu2 = st.z, rs2 = st.w;
     float m1 = 0.f, m2 = 0.f, n1 = 0.f, n2 = 0.f, zh, dy;
     auto weighted = [&](int64_t c) {
       return to_f32(((const T *)p.dy)[row * p.lddy + c]) * (p.w2 ? to_f32(((const P *)p.w2)[c]) : 1.f);
@@ -610,10 +731,10 @@ __global__ void __launch_bounds__(1024) resnorm_columns_any(const __grid_constan
   float s[kNormSums] = {};
   if (c < p.width)
     for (int64_t r = blockIdx.y * 32ll + wy; r < p.rows; r += gridDim.y * 32ll) {
-      const Element e = element<T, P>(p, r, c, p.stats[r], p.stats[p.rows + r]);
+      const float4 st = p.stats[r];
+      const Element e = element<T, P>(p, r, c, st.x, st.y);
       float zh, dy;
-      const float d = stream_gradient<T, P>(p, e, r, c, p.stats[2 * p.rows + r], p.stats[3 * p.rows + r], p.row_sums[r],
-                                            p.row_sums[p.rows + r], zh, dy);
+      const float d = stream_gradient<T, P>(p, e, r, c, st.z, st.w, p.row_sums[r], p.row_sums[p.rows + r], zh, dy);
       const float du = d * e.sc * e.a;
       s[0] += d * (e.a * e.u);
       s[1] += du * e.fh;
@@ -651,13 +772,15 @@ cudaError_t resnorm_forward_as(ResNormArgs p, bool vec, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   p.tpr = pl.tpr;
   if (!pl.columns) return launch_resnorm(resnorm_forward_any<T, P>, p, any_grid(p.rows), pl.block, 0, st);
-  const int64_t groups = pl.block / pl.tpr;
-  const int grid = (int)std::min<int64_t>((p.rows + groups - 1) / groups, sm_count() * (1024 / pl.block));
+  if (!vec) p.classes = 1, p.shift = p.step = 0;
+  const int R = pl.columns == 8 && vec ? 2 : 1;
+  const int grid = resnorm_grid(pl, p.rows, (int64_t)(pl.block / pl.tpr) * R, p.classes, 512);
+  const size_t smem = 5 * sizeof(float) * (size_t)pl.tpr * pl.columns;
   if (pl.columns == 8)
-    return vec ? launch_resnorm(resnorm_forward_rows<T, P, V, 8>, p, grid, pl.block, 0, st)
-               : launch_resnorm(resnorm_forward_rows<T, P, 1, 8>, p, grid, pl.block, 0, st);
-  return vec ? launch_resnorm(resnorm_forward_rows<T, P, V, 16>, p, grid, pl.block, 0, st)
-             : launch_resnorm(resnorm_forward_rows<T, P, 1, 16>, p, grid, pl.block, 0, st);
+    return vec ? launch_resnorm(resnorm_forward_rows<T, P, V, 8, 2>, p, grid, pl.block, smem, st)
+               : launch_resnorm(resnorm_forward_rows<T, P, 1, 8, 1>, p, grid, pl.block, smem, st);
+  return vec ? launch_resnorm(resnorm_forward_rows<T, P, V, 16, 1>, p, grid, pl.block, smem, st)
+             : launch_resnorm(resnorm_forward_rows<T, P, 1, 16, 1>, p, grid, pl.block, smem, st);
 }
 
 template <typename T, typename P>
@@ -671,7 +794,9 @@ cudaError_t resnorm_backward_as(ResNormArgs p, bool vec, int grid, cudaStream_t 
     resnorm_columns_any<T, P><<<dim3((unsigned)((p.width + 31) / 32), grid), 1024, 0, st>>>(p);
     return cudaGetLastError();
   }
-  const size_t smem = pl.block > pl.tpr && p.parts ? kNormSums * sizeof(float) * (size_t)p.width : 0;
+  if (!vec) p.classes = 1, p.shift = p.step = 0;
+  const size_t smem = 4 * sizeof(float) * (size_t)pl.tpr * pl.columns +
+                      (pl.block > pl.tpr && p.parts ? kNormSums * sizeof(float) * (size_t)p.width : 0);
   if (pl.columns == 8)
     return vec ? launch_resnorm(resnorm_backward_rows<T, P, V, 8>, p, grid, pl.block, smem, st)
                : launch_resnorm(resnorm_backward_rows<T, P, 1, 8>, p, grid, pl.block, smem, st);

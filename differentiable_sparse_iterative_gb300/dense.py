@@ -332,7 +332,7 @@ def sla_residual_norm(block: torch.Tensor, z: torch.Tensor, gate: Optional[torch
                                   "bias": bias}, norm, post_norm, gate_activation, eps)
     z_out = _empty(block.shape, dtype=block.dtype, device=block.device)
     y = _empty(block.shape, dtype=block.dtype, device=block.device) if next_norm else None
-    kept = _empty((4, n.rows), dtype=torch.float32, device=block.device) if stats else None
+    kept = _empty((n.rows, 4), dtype=torch.float32, device=block.device) if stats else None
     _check(_lib().sla_residual_norm(n.ref, *n.arrays, *n.params, z_out.data_ptr(), y.data_ptr() if next_norm else None,
                                     kept.data_ptr() if stats else None, _stream(n.index)), "sla_residual_norm")
     return (z_out, y, kept) if stats else (z_out, y)
@@ -363,7 +363,7 @@ def sla_residual_norm_backward(dz: Optional[torch.Tensor], dy: Optional[torch.Te
             raise ValueError(f"param_dtype must be {block.dtype} or torch.float32, got {param_dtype}")
         n.pt, n.descriptor.param_dtype = param_dtype, _DT[param_dtype]
     up = [*_same_rows(dz, block, "dz"), *_same_rows(dy, block, "dy")]
-    sp = _param(stats, "stats", (4, n.rows), torch.float32, n.index)
+    sp = _param(stats, "stats", (n.rows, 4), torch.float32, n.index)
     dev = block.device
 
     def rows_like(wanted):

@@ -664,10 +664,10 @@ typedef struct sla_resnorm {
 } sla_resnorm;
 
 /*
- *   block, z, gate    device, [rows][width] with leading dimensions; gate may be NULL: one
+ *   block, z, gate    device, [rows][width] with leading dimensions (below 2^29, as those below); gate may be NULL: one
  *   scale, post_weight, weight    device, [width] or NULL: one;  post_bias, bias: NULL: zero
  *   z_out, y          device, [rows][width]; y may be NULL: no second norm
- *   stats             device, [4][rows] float32 or NULL: the rows' statistics, for the backward call
+ *   stats             device, [rows][4] float32, 16-byte aligned, or NULL: the rows' statistics, for the backward call
  * Everything is computed in float32; y is the norm of the sum before its rounding to z_out.  The results may not overlap what
  * is read.  A NaN or an infinity in a row makes NaN of that row's results alone.
  */
@@ -682,8 +682,8 @@ SLA_API size_t sla_residual_norm_backward_workspace_bytes(const sla_resnorm *n);
 /*
  * Gradients for the upstream gradients dz_out and dy (each may be NULL: zero) of rows (dblock, dz, dgate, in dtype) and of
  * parameters (dscale, dpost_weight, dpost_bias, dweight, dbias, [width] in param_dtype, summed in float32), each NULL
- * when not wanted.  block, z, gate, the parameters and stats are the forward call's (all four rows of it: y was
- * asked for there if dy is given here).  The workspace is needed for the parameters' gradients only.  rows = 0
+ * when not wanted.  block, z, gate, the parameters and stats are the forward call's (which was asked for y
+ * if dy is given here).  The workspace is needed for the parameters' gradients only.  rows = 0
  * sets those to zero.
  */
 SLA_API sla_status sla_residual_norm_backward(const sla_resnorm *n, const void *dz_out, int64_t lddz, const void *dy,
