@@ -294,7 +294,13 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (p.bias && k < count) v[k] += to_f32(((const T *)p.bias)[col + k]);
-      if constexpr (EPI == kLinear) finish_linear<T, 4>(p, row, col, v, count);
+      if constexpr (EPI == kLinear) {
+        float r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          r[k] = p.residual && k < count ? to_f32(((const T *)p.residual)[row * p.ldr + col + k]) : 0.f;
+        finish_linear<T, 4>(p, row, col, v, r, count);
+      }
       if (p.vec && count >= 4) {
         store_f32<T, 4>(out, v);
       } else {

@@ -55,7 +55,6 @@ struct ForwardScratch {
   ProductPlan plan;
 };
 
-// (the plan is the epilogue's with everything: what is kept or added may differ from call to call, the scratch may not)
 ForwardScratch forward_scratch(const sla_layer *f, char *base) {
   Arena a{base};
   ForwardScratch s{};
@@ -63,7 +62,7 @@ ForwardScratch forward_scratch(const sla_layer *f, char *base) {
   s.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
   s.w = a.take(packed_bytes(f->out, f->width, f->dtype));
   const ProductSize y = y_size(f);
-  s.plan = plan_products(activates(f) ? kLinear : kStore, &y, 1, sheets(f));
+  s.plan = plan_products(kLinear, &y, 1, sheets(f));
   s.parts = (float *)a.take(s.plan.partial[1]);
   s.runs = (float *)a.take(run_bytes(f->dtype));
   s.total = a.used;
@@ -165,7 +164,10 @@ sla_status forward(const sla_layer *f, const T *x, int64_t ldx, const T *w, cons
   job.p.c = y, job.p.ldc = f->out, job.p.vec = vec_out(y, f->out);
   job.p.act = f->activation, job.p.g = da, job.p.ldg = out_pitch(f);
   job.p.residual = residual, job.p.ldr = ldr, job.p.residual_vec = vec_out(residual, ldr);
-  run_products<T>(c, activates(f) || residual ? kLinear : kStore, &job, 1, s.plan, s.parts, s.runs);
+  // with nothing to add, the wide tiles' plain epilogue (32,768 tokens, 1024 -> 2048: 97 -> 90 us); on the narrow ones the
+  // linear layer's has twice the warps
+  const bool plain = !activates(f) && !residual && kProductTiles[s.plan.shape].bn > 64;
+  run_products<T>(c, plain ? kStore : kLinear, &job, 1, s.plan, s.parts, s.runs);
   return finish(c);
 }
 

@@ -100,13 +100,14 @@ struct ProductLaunch {
 // Warps that empty the accumulators: each waits on tensor memory, on global memory and on the special
 // function unit in turn, so the widest 16-bit tiles, whose epilogue would else outlast their products, take
 // sixteen.  (float32's need the registers of eight, and their products take six times as long.)
-template <typename T, int BN>
-inline constexpr int kEpilogueWarps = BN == 256 && sizeof(T) == 2 ? 16 : 8;
+// A linear layer's narrow tiles too: with a width of 64 their product is over in a tenth of a microsecond.
+template <typename T, int EPI, int BN>
+inline constexpr int kEpilogueWarps = (BN == 256 || (EPI == kLinear && BN == 64)) && sizeof(T) == 2 ? 16 : 8;
 
 // Teams of epilogue warps, which take the tiles in turn: while one waits (for the accumulator, for its
 // stores) the other computes.  Elsewhere all warps share a tile: a block often has but one.
-template <typename T, int BN>
-inline constexpr int kTeams = kEpilogueWarps<T, BN> / 8;
+template <typename T, int EPI, int BN>
+inline constexpr int kTeams = kEpilogueWarps<T, EPI, BN> / 8;
 
 // Columns that one warp of the epilogue takes.
 template <typename T, int EPI, int BN>
@@ -123,10 +124,10 @@ inline constexpr int kStoreColumns = sizeof(T) == 4 || kWarpColumns<T, EPI, BN> 
 
 // kStore: columns of a turn (as many as the registers hold: 96 a thread with sixteen warps), and the bytes from
 // row to row of the transposing buffer: an odd number of words, so that neither rows nor columns meet bank conflicts.
-template <typename T, int BN>
-inline constexpr int kTurnColumns = kEpilogueWarps<T, BN> == 16 ? 16 : 32;
-template <typename T, int BN>
-inline constexpr int kRowBytes = kTurnColumns<T, BN> * sizeof(T) + 4;
+template <typename T, int EPI, int BN>
+inline constexpr int kTurnColumns = kEpilogueWarps<T, EPI, BN> == 16 ? 16 : 32;
+template <typename T, int EPI, int BN>
+inline constexpr int kRowBytes = kTurnColumns<T, EPI, BN> * sizeof(T) + 4;
 
 // Tile shapes: CG blocks of 128 rows, BN columns, stages that fill what the stores leave of a multiprocessor's
 // shared memory.
@@ -138,11 +139,11 @@ struct ProductShape {
   // a warp's boxes: 16-bit data two, which it uses again and again; float32 two of factors and three of h, or
   // three each of dg and du
   static constexpr int box = 32 * kStoreColumns<T, EPI, BN> * 2;
-  static constexpr int warp_boxes = kPlainStore<EPI>   ? 32 * kRowBytes<T, BN>
+  static constexpr int warp_boxes = kPlainStore<EPI>   ? 32 * kRowBytes<T, EPI, BN>
                                     : sizeof(T) == 2   ? 2 * box
                                     : EPI == kGate     ? 7 * box
                                                        : 6 * box;
-  static constexpr int boxes = (kEpilogueWarps<T, BN> * warp_boxes + 1023) / 1024 * 1024;
+  static constexpr int boxes = (kEpilogueWarps<T, EPI, BN> * warp_boxes + 1023) / 1024 * 1024;
   static constexpr int room = (225 * 1024 - boxes) / stage_bytes;
   static constexpr int stages = room > 8 ? 8 : room;
   static constexpr int smem = stages * stage_bytes + boxes + 1024 /* alignment */ + 256 /* barriers */;
@@ -274,20 +275,11 @@ __device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count
   for (int i = 0; i < N; ++i) v[i] += b[i];
 }
 
-// v = act(v) + the residual's N values of a row (asked for first); act'(v) is kept in g, whose rows are whole sectors.
+// v = act(v) + r, r the residual's N values of the row; act'(v) is kept in g, whose rows are whole sectors.
 template <typename T, int N>
-__device__ __forceinline__ void finish_linear(const ProductArgs &p, int64_t row, int col, float (&v)[N], int count) {
+__device__ __forceinline__ void finish_linear(const ProductArgs &p, int64_t row, int col, float (&v)[N], const float (&r)[N],
+                                              int count) {
   constexpr bool sectors = N * sizeof(T) % 32 == 0;
-  float r[N];
-  if (p.residual) {
-    const T *from = (const T *)p.residual + row * p.ldr + col;
-    if constexpr (sectors) {
-      load_row<T, N>(from, r, count, p.residual_vec);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = i < count ? to_f32(from[i]) : 0.f;
-    }
-  }
   if (p.act != SLA_ACT_NONE) {
     float da[N];
     if (p.g) {
@@ -406,6 +398,8 @@ __device__ __forceinline__ int product_of(const ProductLaunch &l, int &item) {
 }
 
 __device__ __forceinline__ void split_range(const ProductArgs &p, int split, int &k0, int &k1) {
+  k0 = 0, k1 = p.k_blocks;
+  if (p.splits == 1) return;  // (no division for a tile of one or two stages)
   k0 = (int)((int64_t)p.k_blocks * split / p.splits);
   k1 = (int)((int64_t)p.k_blocks * (split + 1) / p.splits);
 }
@@ -561,7 +555,7 @@ __device__ __forceinline__ void tma_epilogue(const ProductLaunch &l, uint32_t tm
   };
   float *run = f32 ? l.runs + ((int64_t)blockIdx.x * 4 + quarter) * 32 * BN + lane * 4 : nullptr;
   uint32_t seq = team;  // accumulators before this tile's (16-bit data: one a tile)
-  for (int tile = team;; tile += kTeams<T, BN>, seq += kTeams<T, BN>) {
+  for (int tile = team;; tile += kTeams<T, EPI, BN>, seq += kTeams<T, EPI, BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
     const Tile t = tile_of<EPI, CG, BN>(p, item);
@@ -738,12 +732,25 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
                                                uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, team = (warp - 2) >> 3, side = (warp - 2) >> 2 & 1;
-  constexpr int width = kWarpColumns<T, EPI, BN>, N = kTurnColumns<T, BN>, pitch = kRowBytes<T, BN>;
+  constexpr int width = kWarpColumns<T, EPI, BN>, N = kTurnColumns<T, EPI, BN>, pitch = kRowBytes<T, EPI, BN>;
   uint8_t *mine = boxes + (warp - 2) * 32 * pitch;
   constexpr bool f32 = sizeof(T) == 4;
   float *run = f32 ? l.runs + ((int64_t)blockIdx.x * 4 + quarter) * 32 * BN + lane * 4 : nullptr;
+  // kLinear: the residual's columns of the next turn are asked for while the present ones are worked on, those of a tile's
+  // first turn while the tile before it is (1,000,000 tokens, 64 -> 64: 107 -> 102 us; the bias's too cost registers: 112)
+  RawRow<T, N> raw;
+  auto ask = [&](const Tile &t, int c) {
+    const ProductArgs &p = l.p[0];
+    const int row = t.m0 + (int)rank * 128 + quarter * 32 + lane, col = t.n0 + c;
+    if (p.residual && p.residual_vec && row < p.m && p.n - col >= N) raw.load((const T *)p.residual + row * p.ldr + col);
+  };
+  auto ask_tile = [&](int tile) {
+    const int item = item_of(l, worker, workers, tile);
+    if (item >= 0) ask(tile_of<EPI, CG, BN>(l.p[0], item), side * width);
+  };
+  if (EPI == kLinear) ask_tile(team);
   uint32_t seq = team;  // accumulators before this tile's (16-bit data: one a tile)
-  for (int tile = team;; tile += kTeams<T, BN>, seq += kTeams<T, BN>) {
+  for (int tile = team;; tile += kTeams<T, EPI, BN>, seq += kTeams<T, EPI, BN>) {
     int item = item_of(l, worker, workers, tile);
     if (item < 0) break;
     const ProductArgs &p = l.p[EPI == kStore ? product_of(l, item) : 0];
@@ -772,6 +779,19 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
       Sums<T, BN, N> sum;
       float(&v)[N] = sum.v;
       sum.load(base + c);
+      float r[EPI == kLinear ? N : 1];
+      if constexpr (EPI == kLinear) {
+        if (p.residual && live && count > 0) {
+          if (p.residual_vec && count >= N)
+            raw.values(r);
+          else
+            load_row<T, N>((const T *)p.residual + row * p.ldr + col, r, count, p.residual_vec);
+        }
+        if (c + N < (side + 1) * width)
+          ask(t, c + N);
+        else
+          ask_tile(tile + kTeams<T, EPI, BN>);
+      }
       sum.wait();
       if constexpr (f32)
         if (runs > 1) {
@@ -785,7 +805,7 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
           store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
         } else {
           if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
-          if constexpr (EPI == kLinear) finish_linear<T, N>(p, row, col, v, count);
+          if constexpr (EPI == kLinear) finish_linear<T, N>(p, row, col, v, r, count);
           if (p.vec && count >= N) store_row<T, N>((T *)p.c + o, v, count, true);
         }
       }
@@ -814,7 +834,7 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
 }
 
 template <typename T, int EPI, int CG, int BN>
-__global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, BN>, 1)
+__global__ void __launch_bounds__(64 + 32 * kEpilogueWarps<T, EPI, BN>, 1)
     product_kernel(const __grid_constant__ ProductLaunch l) {
   using Shape = ProductShape<T, EPI, CG, BN>;
   constexpr int S = Shape::stages;
@@ -1026,7 +1046,7 @@ cudaError_t launch_product_as(int blocks, const ProductLaunch &l, bool early, cu
     if (e == cudaSuccess) allowed.fetch_or(1ull << (dev & 63));
   }
   if (e != cudaSuccess) return e;
-  LaunchConfig cfg(dim3(blocks), 64 + 32 * kEpilogueWarps<T, BN>, smem, st, early, CG);
+  LaunchConfig cfg(dim3(blocks), 64 + 32 * kEpilogueWarps<T, EPI, BN>, smem, st, early, CG);
   return cudaLaunchKernelEx(&cfg.c, kernel, l);
 }
 
