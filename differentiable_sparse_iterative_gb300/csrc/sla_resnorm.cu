@@ -48,9 +48,9 @@ size_t row_sum_bytes(int64_t rows, int64_t width) {
 }
 
 size_t backward_bytes(int64_t rows, int64_t width) {
-  return row_sum_bytes(rows, width) +
-         align256((size_t)std::max(backward_grid(rows, width, 1), backward_grid(rows, width, kMostClasses)) * kNormSums *
-                  (size_t)width * sizeof(float));
+  int blocks = 0;  // the most that any layout of these rows takes
+  for (int classes = 1; classes <= kMostClasses; classes *= 2) blocks = std::max(blocks, backward_grid(rows, width, classes));
+  return row_sum_bytes(rows, width) + align256((size_t)blocks * kNormSums * (size_t)width * sizeof(float));
 }
 
 sla_status check_resnorm(const sla_resnorm *n) {

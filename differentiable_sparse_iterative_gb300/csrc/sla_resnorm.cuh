@@ -39,7 +39,7 @@ namespace sla {
 
 constexpr int kNormBlock = 256;    // threads of a block while a row takes no more
 constexpr int kNormThreads = 512;  // of a block that shares one row
-constexpr int kWidest = kNormThreads * 16 - 8;  // (a row may reach into one vector more)
+constexpr int kWidest = kNormThreads * 16;
 constexpr int kNormSums = 5;       // dscale, dw1, db1, dw2, db2
 constexpr int kAnyParts = 16;      // parts of the rows of the *_any column sums
 
@@ -78,8 +78,8 @@ struct ResNormPlan {
 };
 
 inline ResNormPlan resnorm_plan(int64_t width) {
-  if (width > kWidest) return {0, kNormThreads, kNormThreads};
   const int64_t reach = width % 8 ? width + 7 : width;  // a row that starts behind a boundary reaches into one vector more
+  if (reach > kWidest) return {0, kNormThreads, kNormThreads};
   const int columns = reach > kNormThreads * 8 ? 16 : 8;
   int tpr = 1;
   while (tpr * columns < reach) tpr <<= 1;

@@ -5,7 +5,11 @@ cells' conductivities make the values of a five-point diffusion matrix; the matr
 sources; the loss compares the solutions with those of the true field.  Its gradient flows back through
 the adjoint solve (grad_values = -lambda_i x_j) into the network's layer norms and gated feed-forward blocks.
 
-    python examples/learned_conductivity.py
+With mixing, blocks that carry information from cell to cell stand between those: a linear layer makes inputs and gates of
+a scan along the grid's lines, there and back, along x and along y in turn, a second one leads back to the residual stream, and
+a residual norm joins the two.
+
+    python examples/learned_conductivity.py [--mixing]
 """
 import math
 import os
@@ -19,10 +23,42 @@ import differentiable_sparse_iterative_gb300 as sla  # noqa: E402
 from workloads import poisson_5pt  # noqa: E402
 
 
+class Mixing(torch.nn.Module):
+    """z, y -> the residual stream and the next block's input, after scans along the lines of an m x m grid, there and back."""
+
+    def __init__(self, width, param, device):
+        super().__init__()
+        # inputs and gates of the two directions; gates start open, so that a state lasts some twenty cells
+        self.w_scan = param(4 * width, width, scale=width ** -0.5)
+        self.b_scan = torch.nn.Parameter(torch.cat((torch.zeros(width), torch.full((width,), 3.0)) * 2).to(device,
+                                                                                                         self.w_scan.dtype))
+        self.w_gate = param(width, width, scale=width ** -0.5)
+        self.w_back = param(width, 2 * width, scale=(2 * width) ** -0.5)
+        self.scale = torch.nn.Parameter(torch.full((width,), 0.5, device=device))
+        self.norms = torch.nn.ParameterList([torch.nn.Parameter(f(width, device=device))
+                                             for f in (torch.ones, torch.zeros, torch.ones, torch.zeros)])
+
+    def forward(self, z, y, m, along_x):
+        width = z.shape[-1]
+
+        def lines(t):  # [m lines][m cells of a line][..]
+            t = t.view(m, m, -1)
+            return t if along_x else t.transpose(0, 1)
+
+        x0, g0, x1, g1 = lines(sla.linear(y, self.w_scan, self.b_scan)).split(width, -1)
+        there, _ = sla.gated_scan(x0, g0)
+        back, _ = sla.gated_scan(x1, g1, reverse=True)
+        h = lines(torch.cat((there, back), -1)).reshape(m * m, 2 * width)
+        w1, b1, w2, b2 = self.norms
+        return sla.residual_norm(sla.linear(h, self.w_back), z, sla.linear(y, self.w_gate), self.scale, w1, b1, w2, b2,
+                                 gate_activation="sigmoid")
+
+
 class ConductivityNet(torch.nn.Module):
     """Fourier features of a cell's position -> residual blocks z + ffn(norm(z)) -> log conductivity."""
 
-    def __init__(self, features=16, width=64, hidden=128, blocks=2, dtype=torch.float32, device="cuda", seed=0):
+    def __init__(self, features=16, width=64, hidden=128, blocks=2, dtype=torch.float32, device="cuda", seed=0,
+                 mixing=False):
         super().__init__()
         gen = torch.Generator().manual_seed(seed)
 
@@ -38,13 +74,24 @@ class ConductivityNet(torch.nn.Module):
         self.w_in = torch.nn.ParameterList([param(2 * hidden, width, scale=width ** -0.5) for _ in range(blocks)])
         self.w_out = torch.nn.ParameterList([param(width, hidden, scale=0.5 * hidden ** -0.5) for _ in range(blocks)])
         self.head = param(1, width, scale=0.1 * width ** -0.5)
+        self.mixing = torch.nn.ModuleList([Mixing(width, param, device) for _ in range(blocks if mixing else 0)])
 
     def forward(self, xy):
         phase = 2.0 * math.pi * (xy @ self.freq)
         z = torch.cat((phase.sin(), phase.cos()), -1).to(self.embed.dtype) @ self.embed.t()
+        if self.mixing:
+            return self.forward_mixing(z, math.isqrt(xy.shape[0]))
         for i, (w_in, w_out) in enumerate(zip(self.w_in, self.w_out)):
             z = z + sla.gated_ffn(sla.layer_norm(z, self.norm_w[i], self.norm_b[i]), w_in, w_out, activation="silu")
         return (sla.layer_norm(z, self.norm_w[-1], self.norm_b[-1]) @ self.head.t()).squeeze(-1)
+
+    def forward_mixing(self, z, m):
+        y = sla.layer_norm(z, self.norm_w[0], self.norm_b[0])
+        for i, (mix, w_in, w_out) in enumerate(zip(self.mixing, self.w_in, self.w_out)):
+            z, y = mix(z, y, m, i % 2 == 0)
+            z, y = sla.residual_norm(sla.gated_ffn(y, w_in, w_out), z, weight=self.norm_w[i + 1], bias=self.norm_b[i + 1],
+                                     post_norm=False)
+        return sla.linear(y, self.head).squeeze(-1)
 
 
 class Diffusion:
@@ -75,7 +122,7 @@ def true_field(cells):
     return torch.exp(0.8 * torch.sin(2 * math.pi * x) * torch.cos(math.pi * y) - 0.5 * y)
 
 
-def train(m=32, steps=80, sources=4, lr=3e-3, dtype=torch.float32, seed=0, report=None):
+def train(m=32, steps=80, sources=4, lr=3e-3, dtype=torch.float32, seed=0, report=None, mixing=False):
     """Returns the losses and the relative error of the learned field."""
     problem = Diffusion(m)
     gen = torch.Generator().manual_seed(seed)
@@ -84,7 +131,7 @@ def train(m=32, steps=80, sources=4, lr=3e-3, dtype=torch.float32, seed=0, repor
     with torch.no_grad():
         A = problem.matrix(target_k)
         targets = [A.solve(b, rtol=1e-10, maxit=20000) for b in rhs]
-    net = ConductivityNet(dtype=dtype, seed=seed)
+    net = ConductivityNet(dtype=dtype, seed=seed, mixing=mixing)
     opt = torch.optim.Adam(net.parameters(), lr=lr)
     losses = []
     for step in range(steps):
@@ -103,5 +150,5 @@ def train(m=32, steps=80, sources=4, lr=3e-3, dtype=torch.float32, seed=0, repor
 
 
 if __name__ == "__main__":
-    losses, err = train(steps=200, report=20)
+    losses, err = train(steps=200, report=20, mixing="--mixing" in sys.argv[1:])
     print(f"relative error of the field: {err:.3f}")
