@@ -353,6 +353,7 @@ struct ProductJob {
   bool b_mn;
   ProductArgs p;
   bool wanted;
+  bool same_b = false;  // all segments take the one sheet of B (those of A are parts of one value)
 };
 
 // Runs the wanted ones of up to kGroup products with the plan made for all of them (whose split sums `parts` holds).
@@ -394,7 +395,7 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, cons
     p.splits = plan.splits[j];
     p.a_mn = jobs[j].a_mn, p.b_mn = jobs[j].b_mn, p.f16 = sizeof(T) == 2 && NetType<T>::dtype == SLA_F16;
     p.segments = s.k_halves;
-    for (int h = 0; h < s.k_halves; ++h) p.a_sheet[h] = p.b_sheet[h] = (int8_t)h;
+    for (int h = 0; h < s.k_halves; ++h) p.a_sheet[h] = (int8_t)h, p.b_sheet[h] = (int8_t)(jobs[j].same_b ? 0 : h);
     cudaError_t e = encode(&l.a[l.count], a, p.a_mn ? 64 : D, p.a_mn ? D : 128, part);
     if (e == cudaSuccess) e = encode(&l.b[l.count], b, p.b_mn ? 64 : D, p.b_mn ? D : gate ? bn / 2 : bn / tile.cg, part);
     if (epi != kStore && epi != kLinear && !split) {

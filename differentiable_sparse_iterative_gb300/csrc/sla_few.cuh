@@ -43,7 +43,7 @@ struct FewArgs {
   void *g, *u;             // T [tokens][ldg]: u act'(g) and act(g), or NULL (gate)
   uint16_t *h;             // operand sheets (gate)
   int64_t ldg, sheet;
-  const void *residual;    // T [tokens][ldr] or NULL (linear; act'(..) goes to g)
+  const void *residual;    // T [tokens][ldr] or NULL (linear; act'(..) goes to g, float [tokens][ldg])
   int64_t ldr;
 };
 
@@ -109,15 +109,17 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// c += the 16 rows (lo: rows g, hi: rows g + 8) times 8 tokens over 32 values of k; float32's six products, smallest first.
+// c += the 16 rows (lo: rows g, hi: rows g + 8) times 8 tokens over 32 values of k; float32's six products, smallest first, the
+// five small ones into `small`.
 template <typename T>
-__device__ __forceinline__ void few_mma(float (&c)[4], const Eight<T> &lo, const Eight<T> &hi, const Eight<T> &x) {
+__device__ __forceinline__ void few_mma(float (&c)[4], float (&small)[4], const Eight<T> &lo, const Eight<T> &hi,
+                                        const Eight<T> &x) {
   constexpr int order[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
 #pragma unroll
   for (int q = sizeof(T) == 4 ? 0 : 5; q < 6; ++q)
 #pragma unroll
     for (int j = 0; j < 4; j += 2)
-      mma16(c, lo.w[order[q][0]][j], hi.w[order[q][0]][j], lo.w[order[q][0]][j + 1], hi.w[order[q][0]][j + 1],
+      mma16(q < 5 ? small : c, lo.w[order[q][0]][j], hi.w[order[q][0]][j], lo.w[order[q][0]][j + 1], hi.w[order[q][0]][j + 1],
             x.w[order[q][1]][j], x.w[order[q][1]][j + 1], operand_t<T>{});
 }
 
@@ -164,7 +166,11 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
   else if (EPI == kStore)
     grid_dependency_wait();
 
-  float acc[M][NT][4] = {};
+  // A linear layer in float32: the small products have a sum of their own, and both are added up in float32 every kFewTurns
+  // turns, since the tensor core drops up to a unit of a running sum with every product (16 tokens, 4096 -> 1000: relative error
+  // 1.6e-6 in one sum).
+  constexpr bool apart = EPI == kLinear && sizeof(T) == 4;
+  float acc[M][NT][4] = {}, small[apart ? NT : 1][4] = {}, total[apart ? NT : 1][4] = {};
   for (; turn < turns; turn += kFewTurns * stride) {
 #pragma unroll
     for (int i = 0; i < kFewTurns; ++i) {
@@ -192,11 +198,24 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
         raw[i][m][0].parts(lo);
         raw[i][m][1].parts(hi);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) few_mma<T>(acc[m][j], lo, hi, x[j]);
+        for (int j = 0; j < NT; ++j) few_mma<T>(acc[m][j], apart ? small[j] : acc[m][j], lo, hi, x[j]);
       }
     }
     if (turn + kFewTurns * stride < turns) ask(turn + kFewTurns * stride);
+    if constexpr (apart)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          total[j][e] += acc[0][j][e] + small[j][e];
+          acc[0][j][e] = small[j][e] = 0.f;
+        }
   }
+  if constexpr (apart)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][j][e] = total[j][e];
 
   constexpr int per = M * 16 * 8 * NT;
 #pragma unroll
@@ -247,7 +266,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const FewArgs p, in
           float a[1] = {v}, da[1];
           with_activation(p.act, [&](auto act) { activate<act.value, true, 1>(a, da); });
           v = a[0];
-          if (p.g) ((T *)p.g)[token * p.ldg + r] = from_f32<T>(da[0]);
+          if (p.g) ((float *)p.g)[token * p.ldg + r] = da[0];
         }
         if (p.residual) v += to_f32(((const T *)p.residual)[token * p.ldr + r]);
       }

@@ -8,9 +8,11 @@
 // activation it is dy itself, in place where TMA can read it; else a kernel forms it from dy and the kept act'(p), lays
 // it out, and sums its columns on the way.  Up to kFewTokens tokens the forward product is sla_few.cuh's.
 //
-// act'(p) is kept in the data's type, and dp rounded to it, as 16-bit tensor-core operands have to be: with the result that
-// makes three roundings on the way to dx and dW (0.0029 in relative L2 in bfloat16, where one is 0.0017), two bytes a
-// value.  db is summed from dp before its rounding.
+// act'(p) is kept in float32.  16-bit tensor-core operands have to be 16 bits: dp = dy act'(p) is rounded once, beside the
+// result's own rounding (0.0024 in relative L2 in bfloat16, 0.0003 in float16, where one rounding makes 0.0017 and 0.00021;
+// act'(p) kept in 16 bits made it 0.0004, for two bytes a value less), unless the products are small (kTwoParts): then dp
+// is two 16-bit parts, which the products take one after the other, and the result's rounding is the only one.  db is
+// summed from dp before its rounding.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -30,23 +32,34 @@ bool keeps_packed(const sla_layer *f) {
   return f->tokens > kFewTokens && (f->dtype == SLA_F32 || f->width % 8 != 0);
 }
 
-// act'(p), rows out_pitch apart, then packed copies of x and the weight.
+// act'(p) in float32, rows out_pitch apart, then packed copies of x and the weight.
 struct SavedLayout {
   size_t x, w, total;
 };
 
 SavedLayout saved_layout(const sla_layer *f) {
   SavedLayout L;
-  L.x = activates(f) ? align256((size_t)f->tokens * (size_t)out_pitch(f) * net_size(f->dtype)) : 0;
+  L.x = activates(f) ? align256((size_t)f->tokens * (size_t)out_pitch(f) * sizeof(float)) : 0;
   L.w = L.x + (keeps_packed(f) ? packed_bytes(f->tokens, f->width, f->dtype) : 0);
   L.total = L.w + (keeps_packed(f) ? packed_bytes(f->out, f->width, f->dtype) : 0);
   return L;
 }
 
+// Up to this many multiply-adds of each product of the backward pass dp has two parts: the second costs 4.3 GFLOP a product at
+// most, and a gradient of few rows or columns does not average its roundings out (its error may be several times the result's
+// rounding by chance).  Beyond, it would double the products' time.  relu's dp, dy or zero, is exact in one.
+constexpr int64_t kTwoParts = (int64_t)1 << 31;
+
+bool two_parts(const sla_layer *f) {
+  if (!activates(f) || f->activation == SLA_ACT_RELU || f->dtype == SLA_F32) return false;
+  const int64_t plane = f->width * f->out;  // at most 2^48
+  return plane <= kTwoParts && f->tokens <= kTwoParts / plane;
+}
+
 int sheets(const sla_layer *f) { return f->dtype == SLA_F32 ? 3 : 1; }
 ProductSize y_size(const sla_layer *f) { return {f->tokens, f->out, f->width, 1, 1, 1}; }
-ProductSize dx_size(const sla_layer *f) { return {f->tokens, f->width, f->out, 1, 1, 1}; }
-ProductSize dw_size(const sla_layer *f) { return {f->out, f->width, f->tokens, 1, 1, 1}; }
+ProductSize dx_size(const sla_layer *f) { return {f->tokens, f->width, f->out, 1, 1, two_parts(f) ? 2 : 1}; }
+ProductSize dw_size(const sla_layer *f) { return {f->out, f->width, f->tokens, 1, 1, two_parts(f) ? 2 : 1}; }
 
 struct ForwardScratch {
   void *x, *w;
@@ -79,7 +92,7 @@ struct BackwardScratch {
 BackwardScratch backward_scratch(const sla_layer *f, char *base) {
   Arena a{base};
   BackwardScratch s{};
-  s.dp = a.take(packed_bytes(f->tokens, f->out, f->dtype));
+  s.dp = a.take((two_parts(f) ? 2 : 1) * packed_bytes(f->tokens, f->out, f->dtype));
   s.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
   s.w = a.take(packed_bytes(f->out, f->width, f->dtype));
   s.columns = (float *)a.take(kSumParts * sizeof(float) * (size_t)f->out);
@@ -91,12 +104,12 @@ BackwardScratch backward_scratch(const sla_layer *f, char *base) {
   return s;
 }
 
-// dp = dy act'(p) as an operand (rows `pitch` apart, float32 in three sheets), eight columns a thread; a block covers 256 / tpr
+// dp = dy act'(p) as an operand (rows `pitch` apart, float32 in three sheets; two: 16 bits in two), eight columns a thread; a block covers 256 / tpr
 // rows at a time, from row blockIdx.y * per, and leaves the column sums of its rows (parts: [gridDim.y][cols], or NULL).
 template <typename T>
 __global__ void __launch_bounds__(256) form_dp(int64_t rows, int64_t cols, const T *__restrict__ dy, int64_t lddy, int vec,
-                                               const T *__restrict__ da, int64_t ldda, uint16_t *__restrict__ dp,
-                                               int64_t pitch, int tpr, int64_t per, float *__restrict__ parts) {
+                                               const float *__restrict__ da, int64_t ldda, uint16_t *__restrict__ dp,
+                                               int64_t pitch, int two, int tpr, int64_t per, float *__restrict__ parts) {
   __shared__ float sm[256 * 8];
   grid_dependency_wait();
   grid_dependency_launch();
@@ -109,7 +122,7 @@ __global__ void __launch_bounds__(256) form_dp(int64_t rows, int64_t cols, const
 #pragma unroll 2
     for (int64_t r = r0 + group; r < r1; r += groups) {
       float v[8], d[8];
-      load_f32<T, 8>(da + r * ldda + c, d);
+      load_f32<float, 8>(da + r * ldda + c, d);
       if (vec && count == 8) {
         load_f32<T, 8>(dy + r * lddy + c, v);
       } else {
@@ -122,6 +135,15 @@ __global__ void __launch_bounds__(256) form_dp(int64_t rows, int64_t cols, const
         s[k] += v[k];
       }
       store_operand<T, 8>(dp + r * pitch + c, rows * pitch, v, 8, true);
+      if constexpr (sizeof(T) == 2)
+        if (two) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float rest = v[k] - to_f32(from_f32<T>(v[k]));
+            v[k] = isfinite(rest) ? rest : 0.f;  // an infinity or NaN stays in the first part
+          }
+          store_operand<T, 8>(dp + (rows + r) * pitch + c, rows * pitch, v, 8, true);
+        }
     }
   if (!parts) return;
 #pragma unroll
@@ -144,7 +166,7 @@ sla_status forward(const sla_layer *f, const T *x, int64_t ldx, const T *w, cons
   SLA_CHECK(report_expired(earlier));
   c.timeouts = earlier.count;
   const SavedLayout L = saved_layout(f);
-  T *da = saved && activates(f) ? (T *)saved : nullptr;
+  float *da = saved && activates(f) ? (float *)saved : nullptr;
   if (f->tokens <= kFewTokens) {
     FewArgs p{};
     p.tokens = (int)f->tokens, p.n = (int)f->out, p.k = (int)f->width, p.act = f->activation;
@@ -200,10 +222,10 @@ sla_status backward(const sla_layer *f, const T *dy, int64_t lddy, const T *x, i
     const int64_t per = std::max<int64_t>(4 * (256 / tpr), (f->tokens + most - 1) / most);
     const int nparts = (int)((f->tokens + per - 1) / per);
     const int vec = aligned(dy, 16) && (f->tokens == 1 || lddy * sizeof(T) % 16 == 0);
-    c.launch(form_dp<T>, dim3((unsigned)tiles, nparts), 256, f->tokens, f->out, dy, lddy, vec, (const T *)saved,
-             out_pitch(f), (uint16_t *)s.dp, pitch, tpr, per, db ? s.columns : nullptr);
+    c.launch(form_dp<T>, dim3((unsigned)tiles, nparts), 256, f->tokens, f->out, dy, lddy, vec, (const float *)saved,
+             out_pitch(f), (uint16_t *)s.dp, pitch, (int)two_parts(f), tpr, per, db ? s.columns : nullptr);
     if (db) columns.add(s.columns, nparts, f->out, f->out, f->out, db);
-    odp = {s.dp, f->out, f->tokens, sheets_of<T>(), pitch, f->tokens * pitch};
+    odp = {s.dp, f->out, f->tokens, two_parts(f) ? 2 : sheets_of<T>(), pitch, f->tokens * pitch};
   } else if (db) {
     columns.of<T, 1>(f->tokens, f->out, dy, lddy, 0, f->out, f->out, db);
   }
@@ -212,6 +234,7 @@ sla_status backward(const sla_layer *f, const T *dy, int64_t lddy, const T *x, i
     auto job = [&](const ProductSize &size, bool a_mn, const Operand &b, T *out) {
       ProductJob j{size, odp, a_mn, b, true, {}, out != nullptr};
       j.p.c = out, j.p.ldc = size.n, j.p.vec = vec_out(out, size.n);
+      j.same_b = two_parts(f);
       return j;
     };
     const ProductJob two[2] = {job(dx_size(f), false, ow, dx), job(dw_size(f), true, ox, dw)};

@@ -80,7 +80,7 @@ struct ProductArgs {
   uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
   int64_t ldg, sheet;        // elements between rows and between sheets of h
   float *sums;               // kGateBack: [m / 32][2][ldg] sums of dg and du over 32 rows, or NULL
-  const void *residual;      // kLinear: T [m][ldr], or NULL; act'(sum + bias) goes to g, T [m][ldg], unless that is NULL
+  const void *residual;      // kLinear: T [m][ldr], or NULL; act'(sum + bias) goes to g, float [m][ldg], unless that is NULL
   int64_t ldr;
   int residual_vec;          // rows of the residual are aligned to 32 bytes
 };
@@ -279,18 +279,17 @@ __device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count
 template <typename T, int N>
 __device__ __forceinline__ void finish_linear(const ProductArgs &p, int64_t row, int col, float (&v)[N], const float (&r)[N],
                                               int count) {
-  constexpr bool sectors = N * sizeof(T) % 32 == 0;
   if (p.act != SLA_ACT_NONE) {
     float da[N];
     if (p.g) {
       with_activation(p.act, [&](auto act) { activate<act.value, true, N>(v, da); });
-      T *to = (T *)p.g + row * p.ldg + col;
-      if constexpr (sectors) {
-        store_row<T, N>(to, da, count, true);
+      float *to = (float *)p.g + row * p.ldg + col;
+      if constexpr (N % 8 == 0) {
+        store_row<float, N>(to, da, count, true);
       } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (i < count) to[i] = from_f32<T>(da[i]);
+          if (i < count) to[i] = da[i];
       }
     } else {
       with_activation(p.act, [&](auto act) { activate<act.value, false, N>(v, da); });

@@ -614,7 +614,7 @@ SLA_API size_t sla_linear_backward_workspace_bytes(const sla_layer *f);
  *   weight    device, [out][width];  bias [out] or NULL
  *   residual  device, [tokens][out] with leading dimension ldr, or NULL
  *   y         device, [tokens][out]
- *   saved     device, sla_linear_saved_bytes, 256-byte aligned, or NULL: kept for the backward call (act'(p), in dtype,
+ *   saved     device, sla_linear_saved_bytes, 256-byte aligned, or NULL: kept for the backward call (act'(p), in float32,
  *             and packed copies)
  *   workspace device, sla_linear_workspace_bytes, 256-byte aligned
  * Sums run in float32, the products of float32 data are float32's (as in sla_gated_ffn, whose bounded waits these
@@ -627,8 +627,8 @@ SLA_API sla_status sla_linear(const sla_layer *f, const void *x, int64_t ldx, co
 /*
  * Gradients for an upstream gradient dy [tokens][out] (lddy): with dp = dy act'(p), dx = dp weight [tokens][width],
  * dweight = dp^T x [out][width], dbias = sum dp [out], each NULL when not wanted (the residual's is dy).  x, the weight and `saved`
- * are the forward call's.  With 16-bit data act'(p) and dp are rounded to dtype before the products, dbias sums dp
- * unrounded.  tokens = 0 sets dweight and dbias to zero.
+ * are the forward call's.  With 16-bit data dp is rounded to dtype before large products and taken in two parts, as
+ * good as unrounded, by small ones; dbias sums dp unrounded.  tokens = 0 sets dweight and dbias to zero.
  */
 SLA_API sla_status sla_linear_backward(const sla_layer *f, const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                        const void *weight, const void *saved, size_t saved_bytes, void *dx,

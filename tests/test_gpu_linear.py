@@ -4,9 +4,9 @@ Tolerances, relative L2 (U: the type's unit roundoff, K: the products of a sum):
   16-bit y: the result's rounding, U at most, and the float32 sum's, K / 16 * 2^-24 * 2/3 (what a tensor core drops: a unit
       2^-23 of the running sum for every 16 products at most, half of it on average, 2/3 of that over a sum that grows as its
       root) below 4 * 2^-16 for K <= 2^14.
-  16-bit gradients: act'(p), dp and the result are rounded, each by U at most and, independent of one another, by U / 2
-      in L2 on average (a rounding to nearest is off by U / sqrt(3) of the spacing's upper end, less below it): 2 U covers three and the
-      activations' own 2^-19.  A sum over one or two rows or columns may have all of one sign: 3 U + U there.
+  16-bit gradients: dp and the result are rounded, each by U at most and, independent of one another, by U / 2
+      in L2 on average (a rounding to nearest is off by U / sqrt(3) of the spacing's upper end, less below it): 2 U covers both and the
+      activations' own 2^-19.  A sum over one or two rows or columns may have all of one sign: 4 U there.
   float32: runs of 512 products: 512 / 16 * 2^-24 * 2/3 = 1.3e-6, dropped third parts 2^-24, activations 2^-19 = 1.9e-6,
       the sums of splits and runs 2^-22: 5e-6.
 """
