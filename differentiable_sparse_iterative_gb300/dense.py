@@ -301,18 +301,36 @@ def _same_rows(t, x, name):
     return ptr, ld
 
 
+@functools.lru_cache(maxsize=512)
+def _resnorm_descriptor(rows, width, dt, pt, norm, post_norm, gate_activation, eps):
+    d = _abi.sla_resnorm(rows, width, dt, pt, norm, post_norm, gate_activation, 0, eps)
+    return d, ctypes.byref(d)
+
+
 class _ResNorm:
     """A call's descriptor, the addresses of its inputs and their parameters."""
 
-    def __init__(self, block, z, gate, params, norm, post_norm, gate_activation, eps):
+    def __init__(self, block, z, gate, names, params, norm, post_norm, gate_activation, eps, param_dtype=None):
         ptr, rows, ld = _rows(block, "block")
         self.rows, self.width, self.index = rows, block.shape[-1], block.get_device()
-        self.pt = _param_type(block, params.values())
-        self.arrays = [ptr, ld, *_same_rows(z, block, "z"), *_same_rows(gate, block, "gate")]
-        self.params = [_param(t, name, (self.width,), self.pt, self.index) for name, t in params.items()]
-        d = _abi.sla_resnorm(rows, self.width, _type(block, "block"), _DT[self.pt], _choice(norm, NORMS, "norm"),
-                             1 if post_norm else 0, _choice(gate_activation, GATE_ACTIVATIONS, "gate activation"), 0, eps)
-        self.descriptor, self.ref = d, ctypes.byref(d)
+        if param_dtype is not None and all(p is None for p in params):
+            if param_dtype != block.dtype and param_dtype != torch.float32:
+                raise ValueError(f"param_dtype must be {block.dtype} or torch.float32, got {param_dtype}")
+            self.pt = param_dtype
+        else:
+            self.pt = _param_type(block, params)
+        zp, ldz = _same_rows(z, block, "z")
+        gp, ldg = _same_rows(gate, block, "gate")
+        self.arrays = (ptr, ld, zp, ldz, gp, ldg)
+        shape, pt, index = (self.width,), self.pt, self.index
+        self.params = [None if t is None else _param(t, name, shape, pt, index) for t, name in zip(params, names)]
+        self.types = (_type(block, "block"), _DT[pt])
+        self.descriptor, self.ref = _resnorm_descriptor(
+            rows, self.width, *self.types, _choice(norm, NORMS, "norm"), 1 if post_norm else 0,
+            _choice(gate_activation, GATE_ACTIVATIONS, "gate activation"), eps)
+
+
+_RESNORM_PARAMS = ("scale", "post_weight", "post_bias", "weight", "bias")
 
 
 @_on_device_of_first
@@ -328,11 +346,12 @@ def sla_residual_norm(block: torch.Tensor, z: torch.Tensor, gate: Optional[torch
     (next_norm=False: y is None); norm is "layer" or "rms", gate_activation "none", "sigmoid" or "silu".  block, z and
     gate have one shape; the parameters are [width], of its type or float32.  Returns (z', y), or with stats=True
     (z', y, stats): the rows' float32 statistics that sla_residual_norm_backward takes."""
-    n = _ResNorm(block, z, gate, {"scale": scale, "post_weight": post_weight, "post_bias": post_bias, "weight": weight,
-                                  "bias": bias}, norm, post_norm, gate_activation, eps)
-    z_out = _empty(block.shape, dtype=block.dtype, device=block.device)
-    y = _empty(block.shape, dtype=block.dtype, device=block.device) if next_norm else None
-    kept = _empty((n.rows, 4), dtype=torch.float32, device=block.device) if stats else None
+    n = _ResNorm(block, z, gate, _RESNORM_PARAMS, (scale, post_weight, post_bias, weight, bias), norm, post_norm,
+                 gate_activation, eps)
+    shape, dt, dev = block.shape, block.dtype, block.device
+    z_out = _empty(shape, dtype=dt, device=dev)
+    y = _empty(shape, dtype=dt, device=dev) if next_norm else None
+    kept = _empty((n.rows, 4), dtype=torch.float32, device=dev) if stats else None
     _check(_lib().sla_residual_norm(n.ref, *n.arrays, *n.params, z_out.data_ptr(), y.data_ptr() if next_norm else None,
                                     kept.data_ptr() if stats else None, _stream(n.index)), "sla_residual_norm")
     return (z_out, y, kept) if stats else (z_out, y)
@@ -356,12 +375,8 @@ def sla_residual_norm_backward(dz: Optional[torch.Tensor], dy: Optional[torch.Te
     """Gradients of sla_residual_norm (asynchronous).  dz and dy belong to its two results; one of them may be None (zero).
     The other arguments are the forward call's.  The parameters' gradients have the parameters' type (param_dtype, default the
     block's, when there is none), also where the parameter itself was left out."""
-    n = _ResNorm(block, z, gate, {"scale": scale, "post_weight": post_weight, "post_bias": post_bias, "weight": weight},
-                 norm, post_norm, gate_activation, eps)
-    if all(p is None for p in (scale, post_weight, post_bias, weight)) and param_dtype is not None:
-        if param_dtype != block.dtype and param_dtype != torch.float32:
-            raise ValueError(f"param_dtype must be {block.dtype} or torch.float32, got {param_dtype}")
-        n.pt, n.descriptor.param_dtype = param_dtype, _DT[param_dtype]
+    n = _ResNorm(block, z, gate, _RESNORM_PARAMS, (scale, post_weight, post_bias, weight), norm, post_norm, gate_activation,
+                 eps, param_dtype)
     up = [*_same_rows(dz, block, "dz"), *_same_rows(dy, block, "dy")]
     sp = _param(stats, "stats", (n.rows, 4), torch.float32, n.index)
     dev = block.device
@@ -379,8 +394,7 @@ def sla_residual_norm_backward(dz: Optional[torch.Tensor], dy: Optional[torch.Te
                               params_like(post), params_like(post), params_like(after), params_like(after))
     wsp, nbytes = None, 0
     if want_grad_params:
-        ws, nbytes = _scratch(_resnorm_backward_bytes(n.rows, n.width, n.descriptor.dtype, n.descriptor.param_dtype,
-                                                      n.index), dev, workspace)
+        ws, nbytes = _scratch(_resnorm_backward_bytes(n.rows, n.width, *n.types, n.index), dev, workspace)
         wsp = ws.data_ptr()
     _check(_lib().sla_residual_norm_backward(n.ref, *up, *n.arrays, *n.params, sp,
                                              *[None if t is None else t.data_ptr() for t in grads], wsp, nbytes,

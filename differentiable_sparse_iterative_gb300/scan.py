@@ -26,6 +26,7 @@ from .dense import _check, _empty, _lib, _on_device_of_first, _param, _rows, _sc
 _OFFSETS = {torch.int32: _abi.SLA_I32, torch.int64: _abi.SLA_I64}
 
 
+# What a call needs that depends on its sizes alone is made once: a single step is a few microseconds of GPU time.
 @functools.lru_cache(maxsize=512)
 def _sizes(rows, channels, sequences, ragged, dt):
     """(bytes kept for the backward call, bytes of scratch)"""
@@ -33,56 +34,81 @@ def _sizes(rows, channels, sequences, ragged, dt):
     return _lib().sla_gated_scan_saved_bytes(ctypes.byref(s)), _lib().sla_gated_scan_workspace_bytes(ctypes.byref(s))
 
 
-def _matrix(t: torch.Tensor) -> torch.Tensor:
-    """t as the rows of one matrix where its strides allow that (the halves of a linear layer's rows, say)."""
-    if t.dim() == 2 or t.is_contiguous():
-        return t
-    try:
-        return t.view(-1, t.shape[-1])
-    except RuntimeError:
-        return t  # refused by name
+class _Uniform:
+    """What calls over sequences of one length share."""
+
+    def __init__(self, rows, channels, sequences, dt, reverse, outside):
+        self.descriptor = _abi.sla_scan(rows, channels, sequences, None, 0, dt, reverse, outside)
+        self.ref = ctypes.byref(self.descriptor)
+        self.saved, self.scratch = _sizes(rows, channels, sequences, False, dt)
+
+
+_uniform = functools.lru_cache(maxsize=512)(_Uniform)
+
+
+def _matrix_rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None):
+    """(address, rows, elements between rows) of a tensor whose strides let it be read as the rows of one matrix (the halves
+    of a linear layer's rows, say)."""
+    if t.dim() == 3 and not t.is_contiguous() and t.is_cuda:
+        q, n, c = t.shape
+        sq, sn, sc = t.stride()
+        if (sc == 1 or c == 1) and c and (n == 1 or q == 1 or sq == n * sn):
+            ld = sq if n == 1 else sn
+            if (ld >= c or q * n <= 1) and (like is None or (t.dtype == like.dtype and t.get_device() == like.get_device())):
+                return t.data_ptr(), q * n, max(ld, c)
+    elif t.dim() > 3 and not t.is_contiguous():
+        try:
+            t = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            pass  # refused by name
+    return _rows(t, name, like)
 
 
 def _matrix_ready(t: torch.Tensor) -> torch.Tensor:
     """t, or a contiguous copy where its rows cannot be read in place."""
-    m = _matrix(t)
-    if m.is_contiguous() or (m.dim() == 2 and m.stride(1) == 1 and m.stride(0) >= m.shape[1]):
-        return t
-    return t.contiguous()
+    if not t.is_contiguous() and t.is_cuda and t.dim() >= 2:
+        try:
+            _matrix_rows(t, "")
+        except ValueError:
+            return t.contiguous()
+    return t
 
 
 class _Scan:
     """A call's descriptor and what follows from it."""
 
     def __init__(self, x, gate, offsets, reverse, outside):
-        if x.dim() < 2:
-            raise ValueError(f"x must be [..., length, channels], got shape {tuple(x.shape)}")
-        if gate.shape != x.shape:
-            raise ValueError(f"gate must have x's shape {tuple(x.shape)}, got {tuple(gate.shape)}")
-        self.x, rows, self.ldx = _rows(_matrix(x), "x")
-        self.gate, _, self.ldg = _rows(_matrix(gate), "gate", x)
-        self.channels, self.dt, self.index = x.shape[-1], _type(x, "x"), x.get_device()
-        address = kind = None
-        if offsets is None:
-            self.sequences = math.prod(x.shape[:-2])
+        shape = x.shape
+        if len(shape) < 2:
+            raise ValueError(f"x must be [..., length, channels], got shape {tuple(shape)}")
+        if gate.shape != shape:
+            raise ValueError(f"gate must have x's shape {tuple(shape)}, got {tuple(gate.shape)}")
+        self.x, rows, self.ldx = _matrix_rows(x, "x")
+        self.gate, _, self.ldg = _matrix_rows(gate, "gate", x)
+        channels, dt, self.index = shape[-1], _type(x, "x"), x.get_device()
+        self.rows, ragged = rows, offsets is not None
+        if not ragged:
+            self.sequences = shape[0] if len(shape) == 3 else math.prod(shape[:-2])
+            u = _uniform(rows, channels, self.sequences, dt, 1 if reverse else 0, 1 if outside else 0)
+            self.ref, self.saved, self.scratch = u.ref, u.saved, u.scratch
         else:
-            if x.dim() != 2:
-                raise ValueError(f"with offsets x must be [rows, channels], got shape {tuple(x.shape)}")
+            if len(shape) != 2:
+                raise ValueError(f"with offsets x must be [rows, channels], got shape {tuple(shape)}")
             kind = _OFFSETS.get(offsets.dtype)
             if kind is None or offsets.dim() != 1 or offsets.numel() < 1:
                 raise ValueError("offsets must be an int32 or int64 vector of at least one element, got "
                                  f"{offsets.dtype} of shape {tuple(offsets.shape)}")
             address = _param(offsets, "offsets", offsets.shape, offsets.dtype, self.index)
             self.sequences = offsets.numel() - 1
-        self.descriptor = _abi.sla_scan(rows, self.channels, self.sequences, address, kind or 0, self.dt,
-                                        1 if reverse else 0, 1 if outside else 0)
-        self.ref = ctypes.byref(self.descriptor)
-        self.saved, self.scratch = _sizes(rows, self.channels, self.sequences, offsets is not None, self.dt)
-        self.key = (rows, self.channels, self.sequences, offsets is not None, self.dt, bool(reverse))
-        self.states = (self.sequences, self.channels)
+            self.descriptor = _abi.sla_scan(rows, channels, self.sequences, address, kind, dt, 1 if reverse else 0,
+                                            1 if outside else 0)
+            self.ref = ctypes.byref(self.descriptor)
+            self.saved, self.scratch = _sizes(rows, channels, self.sequences, True, dt)
+        self.key = (rows, channels, self.sequences, ragged, dt, bool(reverse))
+        self.states = (self.sequences, channels)
 
     def state(self, t, name):
-        return _param(t, name, self.states, torch.float32, self.index)
+        return None if t is None else _param(t, name, self.states, torch.float32, self.index)
 
 
 @_on_device_of_first
@@ -137,7 +163,7 @@ def sla_gated_scan_backward(dh: Optional[torch.Tensor], x: torch.Tensor, gate: t
     if dh is not None:
         if dh.shape != x.shape:
             raise ValueError(f"dh must have x's shape {tuple(x.shape)}, got {tuple(dh.shape)}")
-        dhp, _, lddh = _rows(_matrix(dh), "dh", x)
+        dhp, _, lddh = _matrix_rows(dh, "dh", x)
     dfp, sp = s.state(dfinal, "dfinal"), s.state(state, "state")
     if saved.dtype != torch.uint8 or saved.get_device() != s.index or not saved.is_contiguous():
         raise ValueError("saved must be the buffer that sla_gated_scan(..., save=True) returned")
