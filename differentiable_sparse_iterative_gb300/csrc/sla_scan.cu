@@ -52,6 +52,7 @@ constexpr int kCols = 64;     // channels of a tile, two a lane
 constexpr int kWarps = 8;     // of a block
 constexpr int kFold = 16;     // tiles whose maps the last of them joins to one
 constexpr int kSpan = 512;    // tiles between published states
+constexpr int kWalkRows = 64, kWalks = 5;  // see walks_pay
 constexpr float kCut = -1.f;
 constexpr long long kScanClocks = 4000000000ll;  // about two seconds
 constexpr uint64_t kAbsent = ~0ull;
@@ -609,6 +610,157 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<T, Backward>) scan_kern
   }
 }
 
+// ------------------------------------------------------------------ many sequences of one length: a warp walks along each
+
+// With a sequence and kCols channels for every warp that there is room for, nothing has to be joined: a warp walks from row to
+// row with the state in its registers, one pass, and what counts is that enough rows are on their way: kAhead forward,
+// a chunk of kSaved rows backward while the one behind it is worked on.  Rows in the middle are worked on without a branch, so
+// that their gates are formed side by side (with a test a row: 443 us in place of 81).
+template <typename T>
+inline constexpr int kAhead = sizeof(T) == 2 ? 32 : 16;
+
+template <typename T>
+__global__ void __launch_bounds__(32) walk_forward(const __grid_constant__ ScanArgs p) {
+  using L = Lane<T, true>;
+  constexpr int D = kAhead<T>;
+  const int lane = threadIdx.x, seq = blockIdx.x / (uint32_t)p.groups;
+  const L l(blockIdx.x % (uint32_t)p.groups, lane, p.channels);
+  const int n = (int)p.q.length;
+  const int64_t row0 = p.q.reverse ? (seq + 1) * p.q.length - 1 : seq * p.q.length;
+  const int64_t i0 = p.q.reverse ? p.q.rows - (seq + 1) * p.q.length : row0;  // the scan's index of the first row
+  const char *px = (const char *)((const T *)p.x + row0 * p.ldx + l.c), *pg = (const char *)((const T *)p.g + row0 * p.ldg + l.c);
+  char *po = (char *)((T *)p.out0 + row0 * p.channels + l.c);
+  typename L::Raw xr[D], gr[D];
+#pragma unroll
+  for (int r = 0; r < D; ++r) {
+    gr[r] = xr[r] = L::none();
+    if (r < n) {
+      gr[r] = l.load((const T *)(pg + (int64_t)p.bg * r));
+      xr[r] = l.load((const T *)(px + (int64_t)p.bx * r));
+    }
+  }
+  float2 h = p.state ? l.state(p.state, seq, p.channels) : f2(0.f, 0.f);
+  const int phase = (int)(i0 % kSaved<T>);
+  float *saved = p.saved ? p.saved + i0 / kSaved<T> * p.channels + l.c : nullptr;
+  auto row = [&](int t, int r) {
+    const float2 a = keep(L::values(gr[r]));
+    if (saved && (phase + t + r) % kSaved<T> == 0) {
+      float *to = saved + (int64_t)((phase + t + r) / kSaved<T>) * p.channels;
+      if (l.on0) to[0] = h.x;
+      if (l.on1) to[L::apart] = h.y;
+    }
+    h = step(h, L::values(xr[r]), a);
+    l.store((T *)(po + (int64_t)p.bo * r), h);
+  };
+  int t = 0;
+  for (; t + 2 * D <= n; t += D) {
+    px += (int64_t)p.bx * D, pg += (int64_t)p.bg * D;
+#pragma unroll
+    for (int r = 0; r < D; ++r) {
+      row(t, r);
+      gr[r] = l.load((const T *)(pg + (int64_t)p.bg * r));
+      xr[r] = l.load((const T *)(px + (int64_t)p.bx * r));
+    }
+    po += (int64_t)p.bo * D;
+  }
+  for (; t < n; t += D) {
+    px += (int64_t)p.bx * D, pg += (int64_t)p.bg * D;
+#pragma unroll
+    for (int r = 0; r < D; ++r)
+      if (t + r < n) {
+        row(t, r);
+        if (t + r + D < n) {
+          gr[r] = l.load((const T *)(pg + (int64_t)p.bg * r));
+          xr[r] = l.load((const T *)(px + (int64_t)p.bx * r));
+        }
+      }
+    po += (int64_t)p.bo * D;
+  }
+  if (p.end) l.put_state(p.end, seq, p.channels, h);
+}
+
+template <typename T>
+struct WalkRows {
+  typename Lane<T, true>::Raw x[kSaved<T>], g[kSaved<T>], d[kSaved<T>];
+  float2 h;  // the state before them
+};
+
+template <typename T>
+__global__ void __launch_bounds__(32) walk_backward(const __grid_constant__ ScanArgs p) {
+  using L = Lane<T, true>;
+  constexpr int N = kSaved<T>;
+  const int lane = threadIdx.x, seq = blockIdx.x / (uint32_t)p.groups;
+  const L l(blockIdx.x % (uint32_t)p.groups, lane, p.channels);
+  const int64_t n = p.q.length;
+  const int64_t row0 = p.q.reverse ? (seq + 1) * n - 1 : seq * n, i0 = p.q.reverse ? p.q.rows - (seq + 1) * n : row0;
+  const int dir = p.q.reverse ? -1 : 1;
+  // chunk k: the scan's rows from k N on, of which those of the sequence count
+  const int64_t first = i0 / N, last = (i0 + n - 1) / N;
+  auto at = [&](const void *base, int64_t ld, int64_t k) {
+    return (char *)const_cast<void *>(base) + ((row0 + dir * (k * N - i0)) * ld + l.c) * (int64_t)sizeof(T);
+  };
+  auto ask = [&](WalkRows<T> &w, int64_t k) {
+    if (k < first) return;
+    const char *px = at(p.x, p.ldx, k), *pg = at(p.g, p.ldg, k), *pd = at(p.dh, p.lddh, k);
+    const int lo = (int)max(i0 - k * N, (int64_t)0), hi = (int)min(i0 + n - k * N, (int64_t)N);
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      w.g[r] = w.x[r] = w.d[r] = L::none();
+      if (r >= lo && r < hi) {
+        w.g[r] = l.load((const T *)(pg + (int64_t)p.bg * r));
+        w.x[r] = l.load((const T *)(px + (int64_t)p.bx * r));
+        if (p.dh) w.d[r] = l.load((const T *)(pd + (int64_t)p.bdh * r));
+      }
+    }
+    if (k * N > i0)
+      w.h = l.state(p.saved, k, p.channels);
+    else
+      w.h = p.state ? l.state(p.state, seq, p.channels) : f2(0.f, 0.f);
+  };
+  float2 carry = p.dfinal ? l.state(p.dfinal, seq, p.channels) : f2(0.f, 0.f);
+  auto work = [&](const WalkRows<T> &w, int64_t k) {
+    const int lo = (int)max(i0 - k * N, (int64_t)0), hi = (int)min(i0 + n - k * N, (int64_t)N);
+    char *tx = at(p.out0, p.channels, k), *tg = at(p.out1, p.channels, k);
+    float2 a[N], e[N], h = w.h;
+    auto form = [&](int r) {
+      const float2 x = L::values(w.x[r]);
+      e[r] = f2(h.x - x.x, h.y - x.y);
+      h = fma2(a[r], e[r], x);
+    };
+    auto results = [&](int r) {
+      const float2 lam = add2(L::values(w.d[r]), carry), b = drop(L::values(w.g[r]), a[r]);
+      carry = mul2(a[r], lam);
+      if (p.out0) l.store((T *)(tx + (int64_t)p.bo * r), mul2(b, lam));
+      if (p.out1) l.store((T *)(tg + (int64_t)p.bo * r), mul2(mul2(lam, e[r]), mul2(a[r], b)));
+    };
+#pragma unroll
+    for (int r = 0; r < N; ++r) a[r] = keep(L::values(w.g[r]));
+    if (lo == 0 && hi == N) {
+#pragma unroll
+      for (int r = 0; r < N; ++r) form(r);
+#pragma unroll
+      for (int r = N - 1; r >= 0; --r) results(r);
+      return;
+    }
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+      if (r >= lo) form(r);  // (rows behind the last one change what nothing reads)
+#pragma unroll
+    for (int r = N - 1; r >= 0; --r)
+      if (r >= lo && r < hi) results(r);
+  };
+  WalkRows<T> even, odd;
+  ask(even, last);
+  for (int64_t k = last; k >= first; k -= 2) {
+    ask(odd, k - 1);
+    work(even, k);
+    if (k - 1 < first) break;
+    ask(even, k - 2);
+    work(odd, k - 1);
+  }
+  if (p.end) l.put_state(p.end, seq, p.channels, carry);
+}
+
 // Sequences of one row: nothing to scan.  Two channels a thread.
 template <typename T, bool Pair>
 __global__ void __launch_bounds__(256) scan_single(const __grid_constant__ ScanArgs p) {
@@ -643,6 +795,16 @@ bool closed_tiles(const sla_scan *s, bool backward) {
   if (s->rows <= n) return true;
   if (s->offsets || s->sequences < 1) return false;
   return n % (s->rows / s->sequences) == 0;
+}
+
+// Whether a warp for each sequence and kCols channels pays, where channels go in pairs: sequences long enough for rows on their
+// way, and enough of them to keep the memory busy.  A training step in bfloat16, walks against tiles: 1000 sequences of 1000 x 64
+// 264 us and 329 (float32 328 and 432), 16,000 of 64 x 64 242 and 288, 300 of 1000 x 130 256 and 298; but 500 of 1000 x 64 212
+// and 174, 16 of 2048 x 2048 429 and 319.  (Single channels 32 apart: 1,074 and 350.)
+bool walks_pay(const sla_scan *s, bool pairs) {
+  if (!pairs || s->offsets || s->sequences < 1 || s->rows / s->sequences < kWalkRows) return false;
+  const int64_t strands = s->sequences * ((s->channels + kCols - 1) / kCols);
+  return strands >= (int64_t)kWalks * sm_count() && strands < ((int64_t)1 << 31);
 }
 
 size_t chain_bytes(const sla_scan *s, bool backward) {
@@ -714,15 +876,21 @@ bool pairs_aligned(const sla_scan *s, const void *p, int64_t ld) {
 
 template <typename T, bool Backward, typename K>
 cudaError_t launch(K kernel, const ScanArgs &p, size_t smem, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   const int64_t tiles = (int64_t)p.tiles * p.groups;
   kernel<<<(unsigned)std::min<int64_t>(tiles, (int64_t)sm_count() * kResident<T, Backward>), 32 * kWarps, smem, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, bool Pair>
-cudaError_t run_forward(const ScanArgs &p, bool chain, cudaStream_t st) {
+cudaError_t run_forward(const ScanArgs &p, bool walk, bool chain, cudaStream_t st) {
+  if (Pair && walk) {
+    walk_forward<T><<<(unsigned)(p.q.count * p.groups), 32, 0, st>>>(p);
+    return cudaGetLastError();
+  }
   if (p.q.length == 1 && !p.saved) {
     const int64_t threads = p.q.rows * p.groups * 32;
     scan_single<T, Pair><<<(unsigned)std::min<int64_t>((threads + 255) / 256, sm_count() * 8), 256, 0, st>>>(p);
@@ -734,7 +902,11 @@ cudaError_t run_forward(const ScanArgs &p, bool chain, cudaStream_t st) {
 }
 
 template <typename T, bool Pair>
-cudaError_t run_backward(const ScanArgs &p, bool chain, cudaStream_t st) {
+cudaError_t run_backward(const ScanArgs &p, bool walk, bool chain, cudaStream_t st) {
+  if (Pair && walk) {
+    walk_backward<T><<<(unsigned)(p.q.count * p.groups), 32, 0, st>>>(p);
+    return cudaGetLastError();
+  }
   const size_t smem = p.state || p.dfinal ? kWarps * 2 * kRows<T, true> * kCols * sizeof(float) : 0;
   return chain ? launch<T, true>(scan_kernel<T, true, Pair, true>, p, smem, st)
                : launch<T, true>(scan_kernel<T, false, Pair, true>, p, smem, st);
@@ -796,10 +968,10 @@ SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx,
   p.saved = (float *)saved, p.timeouts = earlier.count;
   const bool pairs = s->channels % 2 == 0 && pairs_aligned(s, x, ldx) && pairs_aligned(s, gate, ldg) &&
                      pairs_aligned(s, h, s->channels);
-  const bool chain = need > 0;
+  const bool walk = walks_pay(s, pairs), chain = !walk && need > 0;
   cudaError_t e = chain ? cudaMemsetAsync(workspace, 0xff, need, st) : cudaSuccess;
   if (e != cudaSuccess) return fail(e);
-  e = by_type(s->dtype, pairs, [&](auto t, auto pair) { return run_forward<decltype(t), decltype(pair)::value>(p, chain, st); });
+  e = by_type(s->dtype, pairs, [&](auto t, auto pair) { return run_forward<decltype(t), decltype(pair)::value>(p, walk, chain, st); });
   if (e != cudaSuccess) return fail(e);
   count_launches(1);
   return SLA_OK;
@@ -837,10 +1009,10 @@ SLA_API sla_status sla_gated_scan_backward(const sla_scan *s, const void *dh, in
   const bool pairs = s->channels % 2 == 0 && pairs_aligned(s, x, ldx) && pairs_aligned(s, gate, ldg) &&
                      (!dh || pairs_aligned(s, dh, lddh)) && pairs_aligned(s, dx, s->channels) &&
                      pairs_aligned(s, dgate, s->channels);
-  const bool chain = need > 0;
+  const bool walk = walks_pay(s, pairs), chain = !walk && need > 0;
   cudaError_t e = chain ? cudaMemsetAsync(workspace, 0xff, need, st) : cudaSuccess;
   if (e != cudaSuccess) return fail(e);
-  e = by_type(s->dtype, pairs, [&](auto t, auto pair) { return run_backward<decltype(t), decltype(pair)::value>(p, chain, st); });
+  e = by_type(s->dtype, pairs, [&](auto t, auto pair) { return run_backward<decltype(t), decltype(pair)::value>(p, walk, chain, st); });
   if (e != cudaSuccess) return fail(e);
   count_launches(1);
   return SLA_OK;

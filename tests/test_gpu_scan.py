@@ -97,7 +97,9 @@ def inputs(shape, sequences, dtype, seed, scale=1.5):
 
 
 UNIFORM = [(1, 1, 1), (3, 1, 5), (64, 1, 64), (5, 1, 130), (1, 2, 3), (2, 15, 64), (5, 16, 2), (4, 17, 66),
-           (3, 255, 130), (2, 256, 64), (2, 257, 33), (7, 100, 64), (300, 3, 40), (1, 5000, 70), (1, 20001, 64)]
+           (3, 255, 130), (2, 256, 64), (2, 257, 33), (7, 100, 64), (300, 3, 40), (1, 5000, 70), (1, 20001, 64),
+           # many sequences of one length, each a warp's: from the shortest that are taken so, in all phases of the saved states
+           (760, 64, 2), (770, 65, 6), (380, 101, 66), (765, 131, 4), (256, 70, 180), (800, 71, 3)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
