@@ -199,10 +199,10 @@ ProductPlan plan_products(Epilogue epi, const ProductSize *s, int count, int she
   static const double blocks_us[2][kProductTileCount] = {{0.27, 0.225, 0.255, 0.245}, {0, 0.81, 1.0, 0.84}};
   const auto &block_us = blocks_us[sheets == 3];
   static const double start_us[kProductTileCount] = {5.0, 5.0, 3.0, 3.0};
-  static const double epilogues_us[2][4][kProductTileCount] = {
-      // kStore, kGate, kGateBack, kLinear
-      {{2.1, 1.25, 1.25, 0.8}, {3.0, 1.8, 1.8, 1.15}, {10.0, 5.5, 5.5, 3.0}, {3.0, 1.8, 1.8, 1.15}},
-      {{0, 1.6, 1.6, 0.9}, {0, 4.5, 4.5, 2.3}, {0, 6.0, 6.0, 3.0}, {0, 2.5, 2.5, 1.4}}};  // float32
+  static const double epilogues_us[2][5][kProductTileCount] = {
+      // kStore, kGate, kGateBack, kLinear, kAdd
+      {{2.1, 1.25, 1.25, 0.8}, {3.0, 1.8, 1.8, 1.15}, {10.0, 5.5, 5.5, 3.0}, {3.0, 1.8, 1.8, 1.15}, {3.0, 1.8, 1.8, 1.15}},
+      {{0, 1.6, 1.6, 0.9}, {0, 4.5, 4.5, 2.3}, {0, 6.0, 6.0, 3.0}, {0, 2.5, 2.5, 1.4}, {0, 2.5, 2.5, 1.4}}};  // float32
   const auto &epilogue_us = epilogues_us[sheets == 3];
   const int sms = sm_count();
   ProductPlan best{};
@@ -294,12 +294,12 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (p.bias && k < count) v[k] += to_f32(((const T *)p.bias)[col + k]);
-      if constexpr (EPI == kLinear) {
+      if constexpr (kLayer<EPI>) {
         float r[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           r[k] = p.residual && k < count ? to_f32(((const T *)p.residual)[row * p.ldr + col + k]) : 0.f;
-        finish_linear<T, 4>(p, row, col, v, r, count);
+        finish_linear<T, 4, EPI == kLinear>(p, row, col, v, r, count);
       }
       if (p.vec && count >= 4) {
         store_f32<T, 4>(out, v);
@@ -398,7 +398,7 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, cons
     for (int h = 0; h < s.k_halves; ++h) p.a_sheet[h] = (int8_t)h, p.b_sheet[h] = (int8_t)(jobs[j].same_b ? 0 : h);
     cudaError_t e = encode(&l.a[l.count], a, p.a_mn ? 64 : D, p.a_mn ? D : 128, part);
     if (e == cudaSuccess) e = encode(&l.b[l.count], b, p.b_mn ? 64 : D, p.b_mn ? D : gate ? bn / 2 : bn / tile.cg, part);
-    if (epi != kStore && epi != kLinear && !split) {
+    if (epi != kStore && epi != kLinear && epi != kAdd && !split) {
       // the epilogue's own arrays (see tma_epilogue); a warp's columns of the 64-wide gate tile are 16
       const int box = S == 3 || (gate && bn == 64) ? 16 : 32;
       const Operand h{p.h, s.n, s.m, S * (epi == kGate ? 1 : 2), p.ldg, p.sheet};
@@ -456,6 +456,8 @@ void run_products(Call &c, Epilogue epi, const ProductJob *jobs, int count, cons
     c.launch(finish_splits<T, kStore>, grid, 256, f);
   else if (epi == kLinear)
     c.launch(finish_splits<T, kLinear>, grid, 256, f);
+  else if (epi == kAdd)
+    c.launch(finish_splits<T, kAdd>, grid, 256, f);
   else if (epi == kGate)
     c.launch(finish_splits<T, kGate>, grid, 256, f);
   else

@@ -75,7 +75,7 @@ ForwardScratch forward_scratch(const sla_layer *f, char *base) {
   s.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
   s.w = a.take(packed_bytes(f->out, f->width, f->dtype));
   const ProductSize y = y_size(f);
-  s.plan = plan_products(kLinear, &y, 1, sheets(f));
+  s.plan = plan_products(activates(f) ? kLinear : kAdd, &y, 1, sheets(f));
   s.parts = (float *)a.take(s.plan.partial[1]);
   s.runs = (float *)a.take(run_bytes(f->dtype));
   s.total = a.used;
@@ -188,8 +188,8 @@ sla_status forward(const sla_layer *f, const T *x, int64_t ldx, const T *w, cons
   job.p.residual = residual, job.p.ldr = ldr, job.p.residual_vec = vec_out(residual, ldr);
   // with nothing to add, the wide tiles' plain epilogue (32,768 tokens, 1024 -> 2048: 97 -> 90 us); on the narrow ones the
   // linear layer's has twice the warps
-  const bool plain = !activates(f) && !residual && kProductTiles[s.plan.shape].bn > 64;
-  run_products<T>(c, plain ? kStore : kLinear, &job, 1, s.plan, s.parts, s.runs);
+  const bool plain = !residual && kProductTiles[s.plan.shape].bn > 64;
+  run_products<T>(c, activates(f) ? kLinear : plain ? kStore : kAdd, &job, 1, s.plan, s.parts, s.runs);
   return finish(c);
 }
 

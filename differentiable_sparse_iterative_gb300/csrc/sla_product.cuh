@@ -42,10 +42,13 @@ enum Epilogue {
   kGate,      // columns of g and u side by side: h = act(g) u; u act'(g) and act(g) kept for kGateBack
   kGateBack,  // sum = dh: dg = dh (u act'(g)), du = dh act(g)
   kLinear,    // c = act(sum + bias) + residual; act'(sum + bias) kept
+  kAdd,       // c = sum + bias + residual: kLinear without an activation, whose registers it does without
 };
 // Whether an epilogue writes the caller's array straight from the registers.
 template <int EPI>
-inline constexpr bool kPlainStore = EPI == kStore || EPI == kLinear;
+inline constexpr bool kPlainStore = EPI == kStore || EPI == kLinear || EPI == kAdd;
+template <int EPI>
+inline constexpr bool kLayer = EPI == kLinear || EPI == kAdd;
 
 constexpr int kBand = 8;
 constexpr int kMaxSegments = 2;
@@ -80,7 +83,7 @@ struct ProductArgs {
   uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
   int64_t ldg, sheet;        // elements between rows and between sheets of h
   float *sums;               // kGateBack: [m / 32][2][ldg] sums of dg and du over 32 rows, or NULL
-  const void *residual;      // kLinear: T [m][ldr], or NULL; act'(sum + bias) goes to g, float [m][ldg], unless that is NULL
+  const void *residual;      // kLinear, kAdd: T [m][ldr], or NULL; act'(sum + bias) goes to g, float [m][ldg], unless that is NULL
   int64_t ldr;
   int residual_vec;          // rows of the residual are aligned to 32 bytes
 };
@@ -102,7 +105,7 @@ struct ProductLaunch {
 // sixteen.  (float32's need the registers of eight, and their products take six times as long.)
 // A linear layer's narrow tiles too: with a width of 64 their product is over in a tenth of a microsecond.
 template <typename T, int EPI, int BN>
-inline constexpr int kEpilogueWarps = (BN == 256 || (EPI == kLinear && BN == 64)) && sizeof(T) == 2 ? 16 : 8;
+inline constexpr int kEpilogueWarps = (BN == 256 || (kLayer<EPI> && BN == 64)) && sizeof(T) == 2 ? 16 : 8;
 
 // Teams of epilogue warps, which take the tiles in turn: while one waits (for the accumulator, for its
 // stores) the other computes.  Elsewhere all warps share a tile: a block often has but one.
@@ -276,10 +279,10 @@ __device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count
 }
 
 // v = act(v) + r, r the residual's N values of the row; act'(v) is kept in g, whose rows are whole sectors.
-template <typename T, int N>
+template <typename T, int N, bool Activates>
 __device__ __forceinline__ void finish_linear(const ProductArgs &p, int64_t row, int col, float (&v)[N], const float (&r)[N],
                                               int count) {
-  if (p.act != SLA_ACT_NONE) {
+  if (Activates && p.act != SLA_ACT_NONE) {
     float da[N];
     if (p.g) {
       with_activation(p.act, [&](auto act) { activate<act.value, true, N>(v, da); });
@@ -735,7 +738,7 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
   uint8_t *mine = boxes + (warp - 2) * 32 * pitch;
   constexpr bool f32 = sizeof(T) == 4;
   float *run = f32 ? l.runs + ((int64_t)blockIdx.x * 4 + quarter) * 32 * BN + lane * 4 : nullptr;
-  // kLinear: the residual's columns of the next turn are asked for while the present ones are worked on, those of a tile's
+  // kLinear, kAdd: the residual's columns of the next turn are asked for while the present ones are worked on, those of a tile's
   // first turn while the tile before it is (1,000,000 tokens, 64 -> 64: 107 -> 102 us; the bias's too cost registers: 112)
   RawRow<T, N> raw;
   auto ask = [&](const Tile &t, int c) {
@@ -747,7 +750,7 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
     const int item = item_of(l, worker, workers, tile);
     if (item >= 0) ask(tile_of<EPI, CG, BN>(l.p[0], item), side * width);
   };
-  if (EPI == kLinear) ask_tile(team);
+  if (kLayer<EPI>) ask_tile(team);
   uint32_t seq = team;  // accumulators before this tile's (16-bit data: one a tile)
   for (int tile = team;; tile += kTeams<T, EPI, BN>, seq += kTeams<T, EPI, BN>) {
     int item = item_of(l, worker, workers, tile);
@@ -778,8 +781,8 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
       Sums<T, BN, N> sum;
       float(&v)[N] = sum.v;
       sum.load(base + c);
-      float r[EPI == kLinear ? N : 1];
-      if constexpr (EPI == kLinear) {
+      float r[kLayer<EPI> ? N : 1];
+      if constexpr (kLayer<EPI>) {
         if (p.residual && live && count > 0) {
           if (p.residual_vec && count >= N)
             raw.values(r);
@@ -804,7 +807,7 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
           store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
         } else {
           if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
-          if constexpr (EPI == kLinear) finish_linear<T, N>(p, row, col, v, r, count);
+          if constexpr (kLayer<EPI>) finish_linear<T, N, EPI == kLinear>(p, row, col, v, r, count);
           if (p.vec && count >= N) store_row<T, N>((T *)p.c + o, v, count, true);
         }
       }

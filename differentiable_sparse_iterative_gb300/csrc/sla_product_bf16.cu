@@ -11,6 +11,7 @@ cudaError_t launch_product<bf16>(int epi, int shape, int blocks, const ProductLa
     case kStore: return launch_product_shape<bf16, kStore>(shape, blocks, l, early, st);
     case kGate: return launch_product_shape<bf16, kGate>(shape, blocks, l, early, st);
     case kLinear: return launch_product_shape<bf16, kLinear>(shape, blocks, l, early, st);
+    case kAdd: return launch_product_shape<bf16, kAdd>(shape, blocks, l, early, st);
     default: return launch_product_shape<bf16, kGateBack>(shape, blocks, l, early, st);
   }
 }

@@ -11,6 +11,7 @@ cudaError_t launch_product<f16>(int epi, int shape, int blocks, const ProductLau
     case kStore: return launch_product_shape<f16, kStore>(shape, blocks, l, early, st);
     case kGate: return launch_product_shape<f16, kGate>(shape, blocks, l, early, st);
     case kLinear: return launch_product_shape<f16, kLinear>(shape, blocks, l, early, st);
+    case kAdd: return launch_product_shape<f16, kAdd>(shape, blocks, l, early, st);
     default: return launch_product_shape<f16, kGateBack>(shape, blocks, l, early, st);
   }
 }

@@ -10,6 +10,7 @@ cudaError_t launch_product<float>(int epi, int shape, int blocks, const ProductL
     case kStore: return launch_product_shape<float, kStore>(shape, blocks, l, early, st);
     case kGate: return launch_product_shape<float, kGate>(shape, blocks, l, early, st);
     case kLinear: return launch_product_shape<float, kLinear>(shape, blocks, l, early, st);
+    case kAdd: return launch_product_shape<float, kAdd>(shape, blocks, l, early, st);
     default: return launch_product_shape<float, kGateBack>(shape, blocks, l, early, st);
   }
 }
