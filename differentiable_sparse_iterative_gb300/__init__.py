@@ -19,6 +19,11 @@ A network that predicts the values is built from layer_norm and gated_ffn (``den
 gradients flow on from the solve's:
 
     z = z + gated_ffn(layer_norm(z, w, b), w_in, w_out, b_in, b_out, activation="silu")
+
+and from linear layers, scans from cell to cell (``scan.py``) and the norm that joins a block's result with the residual stream:
+
+    x, g = linear(y, w, b).chunk(2, -1)
+    z, y = residual_norm(linear(gated_scan(x, g)[0], w2), z, gate, scale, w1, b1, w3, b3)
 """
 from __future__ import annotations
 

@@ -1,12 +1,14 @@
-"""Dense operators of a coefficient network: layer norm and the gated feed-forward block.
+"""Dense operators of a coefficient network: layer norm, residual norm, linear layer and the gated feed-forward block.
 
 The values of a matrix often come from a network over the grid cells (one token a cell) that is
-trained through the solve; these are the two halves of its residual block z + gated_ffn(layer_norm(z)).
-As everywhere in this package the compute is libsla's (``csrc/sla_norm.cu``, ``csrc/sla_ffn.cu``, C ABI
-in ``include/sla.h``): this module marshals torch tensors, and a CPU tensor raises.
+trained through the solve; layer norm and feed-forward block are the two halves of its residual block
+z + gated_ffn(layer_norm(z)), linear layers stand around the scan of a mixing block (``scan.py``), and the residual norm
+joins a block's result with the residual stream z and norms the sum for the next block.
+As everywhere in this package the compute is libsla's (``csrc/sla_norm.cu``, ``sla_resnorm.cu``, ``sla_linear.cu``, ``sla_ffn.cu``,
+C ABI in ``include/sla.h``): this module marshals torch tensors, and a CPU tensor raises.
 
 Data is float32, float16 or bfloat16.  The sla_* functions are the C calls under their names (no
-autograd graph, leading dimensions allowed); layer_norm and gated_ffn are differentiable.
+autograd graph, leading dimensions allowed); layer_norm, residual_norm, linear and gated_ffn are differentiable.
 """
 from __future__ import annotations
 

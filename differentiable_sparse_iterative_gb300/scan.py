@@ -94,10 +94,10 @@ class _Scan:
         else:
             if len(shape) != 2:
                 raise ValueError(f"with offsets x must be [rows, channels], got shape {tuple(shape)}")
-            kind = _OFFSETS.get(offsets.dtype)
+            kind = _OFFSETS.get(offsets.dtype) if isinstance(offsets, torch.Tensor) else None
             if kind is None or offsets.dim() != 1 or offsets.numel() < 1:
-                raise ValueError("offsets must be an int32 or int64 vector of at least one element, got "
-                                 f"{offsets.dtype} of shape {tuple(offsets.shape)}")
+                got = f"{offsets.dtype} of shape {tuple(offsets.shape)}" if isinstance(offsets, torch.Tensor) else type(offsets)
+                raise ValueError(f"offsets must be an int32 or int64 vector of at least one element, got {got}")
             address = _param(offsets, "offsets", offsets.shape, offsets.dtype, self.index)
             self.sequences = offsets.numel() - 1
             self.descriptor = _abi.sla_scan(rows, channels, self.sequences, address, kind, dt, 1 if reverse else 0,

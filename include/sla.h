@@ -504,8 +504,9 @@ SLA_API sla_status sla_cg_solve_static(const sla_csr *A, const void *b, const vo
 
 /*
  * A matrix's values often come from a network over the grid cells (one row, or token, a cell),
- * trained through the solve.  These two operators are its residual block  z + ffn(layernorm(z)).
- * Both take SLA_F32, SLA_F16 or SLA_BF16 data and compute in float32.  Matrices are row-major with
+ * trained through the solve.  These operators are its residual blocks: z + ffn(layernorm(z)), and linear layers, a scan
+ * from cell to cell and the norm that joins a block's result with the residual stream.
+ * All take SLA_F32, SLA_F16 or SLA_BF16 data and compute in float32.  Matrices are row-major with
  * unit column stride; the leading dimensions ldx and lddy (elements between rows) may exceed the
  * row length, weights and outputs are dense.  Rows of no alignment beyond their element type are
  * taken.  All calls are asynchronous on the stream; results do not depend on the order in which
@@ -728,7 +729,7 @@ SLA_API size_t sla_gated_scan_workspace_bytes(const sla_scan *s);
  *   saved        device, sla_gated_scan_saved_bytes, 256-byte aligned, or NULL
  *   workspace    device, sla_gated_scan_workspace_bytes, 256-byte aligned
  * States are float32 from row to row; h is what they round to.  A sequence with no rows ends in the state that it
- * starts with.  An infinity or NaN makes NaN of the rest of its channel's sequence, and of nothing else.
+ * starts with.  An infinity or NaN makes NaN or infinities of the rest of its channel's sequence, and of nothing else.
  * Blocks wait for one another's results within the launch, each wait for two seconds at most (see sla_gated_ffn_check).
  */
 SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx, const void *gate, int64_t ldg,
@@ -747,10 +748,10 @@ SLA_API sla_status sla_gated_scan_backward(const sla_scan *s, const void *dh, in
                                            void *stream);
 
 /*
- * Every wait inside the products' kernels is bounded (about two seconds); one that expires, which no
+ * Every wait inside the products' and the scan's kernels is bounded (about two seconds); one that expires, which no
  * input can cause, leaves its tile unwritten and is counted.  Each host thread is told once of what has
- * expired on a device since its own first call there: sla_gated_ffn and sla_gated_ffn_backward return
- * SLA_TIMEOUT, and do nothing else, when they find that a wait of an earlier call has expired (its results
+ * expired on a device since its own first call there: sla_gated_ffn, sla_linear, sla_gated_scan and their
+ * backward calls return SLA_TIMEOUT, and do nothing else, when they find that a wait of an earlier call has expired (its results
  * are not valid); this call synchronises the stream first, so that the calls before it count, and
  * returns SLA_TIMEOUT or SLA_OK.
  */

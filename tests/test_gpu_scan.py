@@ -33,50 +33,52 @@ def f64(t):
 
 
 def scan64(x, g, state, marks, reverse, dh=None, dfinal=None):
-    """Results and their bounds (without the rounding to a type), from numpy arrays [rows, channels]."""
+    """Results and their bounds (without the rounding to a type), from numpy arrays [rows, channels]: step after step, all
+    sequences that are long enough at a time."""
     n, c = x.shape
     a, b = 1 / (1 + np.exp(-g)), 1 / (1 + np.exp(g))
     d = np.abs(g) * 2.0 ** -23 + 2.0 ** -21
     small = np.minimum(a, b)
-    h, eh = np.zeros((n, c)), np.zeros((n, c))
-    before, eb = np.zeros((n, c)), np.zeros((n, c))
-    final, ef = state.copy(), np.zeros_like(state)
-    back = dh is not None
-    dx, dg, edx, edg = (np.zeros((n, c)) for _ in range(4))
-    ds, eds = (dfinal.copy() if back else None), np.zeros_like(state)
+    h, eh, before, eb = (np.zeros((n, c)) for _ in range(4))
+    begin, length = np.array(marks[:-1], dtype=int), np.diff(marks)
+    most = np.abs(state)
     for q, (p0, p1) in enumerate(zip(marks[:-1], marks[1:])):
-        rows = list(range(p1 - 1, p0 - 1, -1) if reverse else range(p0, p1))
-        if not rows:
-            continue
-        most = np.maximum(np.abs(x[p0:p1]).max(0), np.abs(state[q]))
-        s, e = state[q].copy(), np.zeros(c)
-        for t in rows:
-            before[t], eb[t] = s, e
-            s = a[t] * s + b[t] * x[t]
-            e = a[t] * e + 2 * most * (4 * F + d[t] * b[t])
-            h[t], eh[t] = s, e
-        final[q], ef[q] = s, e
-        if not back:
-            continue
-        m, ls = dfinal[q].copy(), {}
-        for t in reversed(rows):
-            ls[t] = dh[t] + m
-            m = a[t] * ls[t]
-        ds[q] = m
-        most = np.abs(np.stack(list(ls.values()))).max(0)
-        most = np.maximum(most, np.abs(dfinal[q]))
-        e = np.zeros(c)
-        for t in reversed(rows):
-            l, el = ls[t], e + 2 * F * most
-            gap = before[t] - x[t]
-            dx[t], edx[t] = b[t] * l, b[t] * (el + (d[t] + 2 * F) * np.abs(l))
-            ab = a[t] * b[t]
-            dg[t] = l * gap * ab
-            edg[t] = ab * (el * np.abs(gap) + np.abs(l) * (eb[t] + F * (np.abs(before[t]) + np.abs(x[t])))
-                           + (3 * d[t] + 4 * F) * np.abs(l * gap))
-            e = a[t] * el + 2 * most * (4 * F + d[t] * small[t])
-        eds[q] = e
-    return dict(h=(h, eh), final=(final, ef), dx=(dx, edx), dg=(dg, edg), ds=(ds, eds))
+        if p1 > p0:
+            most[q] = np.maximum(most[q], np.abs(x[p0:p1]).max(0))
+
+    def rows(t):
+        on = np.flatnonzero(length > t)
+        return on, (begin + length - 1 - t if reverse else begin + t)[on]
+
+    s, e = state.copy(), np.zeros_like(state)
+    steps = int(length.max(initial=0))
+    for t in range(steps):
+        on, r = rows(t)
+        before[r], eb[r] = s[on], e[on]
+        s[on] = a[r] * s[on] + b[r] * x[r]
+        e[on] = a[r] * e[on] + 2 * most[on] * (4 * F + d[r] * b[r])
+        h[r], eh[r] = s[on], e[on]
+    out = dict(h=(h, eh), final=(s, e))
+    if dh is None:
+        return out
+    dx, dg, edx, edg, ls = (np.zeros((n, c)) for _ in range(5))
+    m, most = dfinal.copy(), np.abs(dfinal)
+    for t in reversed(range(steps)):
+        on, r = rows(t)
+        ls[r] = dh[r] + m[on]
+        m[on] = a[r] * ls[r]
+        most[on] = np.maximum(most[on], np.abs(ls[r]))
+    e = np.zeros_like(state)
+    for t in reversed(range(steps)):
+        on, r = rows(t)
+        l, el = ls[r], e[on] + 2 * F * most[on]
+        gap, ab = before[r] - x[r], a[r] * b[r]
+        dx[r], edx[r] = b[r] * l, b[r] * (el + (d[r] + 2 * F) * np.abs(l))
+        dg[r] = l * gap * ab
+        edg[r] = ab * (el * np.abs(gap) + np.abs(l) * (eb[r] + F * (np.abs(before[r]) + np.abs(x[r])))
+                       + (3 * d[r] + 4 * F) * np.abs(l * gap))
+        e[on] = a[r] * el + 2 * most[on] * (4 * F + d[r] * small[r])
+    return dict(out, dx=(dx, edx), dg=(dg, edg), ds=(m, e))
 
 
 def check(got, want, dtype, what):
@@ -364,6 +366,7 @@ def test_refusals():
             (lambda: sla.sla_gated_scan(x, x, state.half()), "state must have"),
             (lambda: sla.sla_gated_scan(x, x, offsets=off), "with offsets"),
             (lambda: sla.sla_gated_scan(x[0], x[0], offsets=off.float()), "offsets must be"),
+            (lambda: sla.sla_gated_scan(x[0], x[0], offsets=[0, 6]), "offsets must be"),
             (lambda: sla.sla_gated_scan(x[0], x[0], offsets=off[:0]), "offsets must be"),
             (lambda: sla.sla_gated_scan(x[0], x[0], offsets=off.cpu()), "offsets must be"),
             (lambda: sla.sla_gated_scan(x, x, h=x[:2].clone()), "h must have"),
