@@ -360,6 +360,11 @@ template <int EPI, int CG, int BN>
 __device__ __forceinline__ Tile tile_of(const ProductArgs &p, int item) {
   const int mt = p.m_halves * p.m_tiles, nt = p.n_halves * p.n_tiles, per = mt * nt;
   Tile t;
+  if (nt == 1 && p.m_halves == 1 && p.splits == 1) {  // a narrow layer's tiles are over before the divisions below
+    t.split = t.m_half = t.n_half = t.n0 = 0;
+    t.m0 = item * 128 * CG;
+    return t;
+  }
   t.split = item / per;
   int i = item - t.split * per;
   const int band = i / (kBand * nt);

@@ -20,7 +20,10 @@
 //
 // Widths that no vector divides: row r starts (r ld) mod V elements behind a 16-byte boundary, which repeats every `classes`
 // rows.  A block takes the rows of one class, so that its threads keep their columns: vector i of a row starts `shift`
-// columns before column i V, and the first and last, which reach beyond the row, are moved element by element.  Arrays whose
+// columns before column i V.  The first and last vector reach into the neighbouring rows: they are read whole (but for the first
+// and last rows of all) and what is not the row's is dropped when its values are needed, not at the load, which would
+// wait for memory there and then (backward, 5003 x 1001: 64 us a call with elements loaded one by one), and are written
+// element by element.  Arrays whose
 // rows do not all start at the same place behind a boundary are moved element by element throughout (V = 1: neighbouring threads
 // have neighbouring columns), and rows of more than kWidest columns take the *_any kernels, which read a row several times.
 #pragma once
@@ -121,8 +124,9 @@ __device__ __forceinline__ void row_sums(float (&v)[K], int tpr, float *slot) {
   for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
 }
 
-// A thread's columns: C / V vectors, vector i from column (t + i tpr) V - shift on.
-template <int V, int C>
+// A thread's columns: C / V vectors, vector i from column (t + i tpr) V - shift on.  Edge: there are vectors that lie in the row
+// in part (rows that start or end behind a boundary).
+template <int V, int C, bool Edge>
 struct Columns {
   static constexpr int n = C / V;
   int t, tpr, width, shift;
@@ -144,12 +148,15 @@ struct Columns {
   __device__ __forceinline__ void mask(float2 (&v)[C / 2]) const {
     if (full()) return;
 #pragma unroll
-    for (int j = 0; j < C; j += 2) v[j / 2] = make_float2(inside(j) ? v[j / 2].x : 0.f, inside(j + 1) ? v[j / 2].y : 0.f);
+    for (int j = 0; j < C; j += 2) {
+      const bool in0 = Edge ? inside(j) : whole >> (j / V) & 1, in1 = Edge ? inside(j + 1) : whole >> ((j + 1) / V) & 1;
+      v[j / 2] = make_float2(in0 ? v[j / 2].x : 0.f, in1 ? v[j / 2].y : 0.f);
+    }
   }
 };
 
 // C columns of a row as loaded.
-template <typename T, int V, int C>
+template <typename T, int V, int C, bool Edge>
 struct RowPart {
   static constexpr int n = C / V;
   Pack<T, V> v[n];
@@ -159,16 +166,18 @@ struct RowPart {
 #pragma unroll
       for (int k = 0; k < V; ++k) v[i].v[k] = from_f32<T>(0.f);
   }
-  __device__ __forceinline__ void load(const T *row, const Columns<V, C> &q, bool there) {
+  // beside: the rows around this one cover what its first and last vectors read of them
+  __device__ __forceinline__ void load(const T *row, const Columns<V, C, Edge> &q, bool there, bool beside) {
+    const uint32_t may = Edge && beside ? q.some : q.whole;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const int c = q.first(i);
-      if (there && (q.whole >> i & 1)) {
+      if (there && (may >> i & 1)) {
         v[i] = *reinterpret_cast<const Pack<T, V> *>(row + c);
       } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) v[i].v[k] = from_f32<T>(0.f);
-        if (V > 1 && there && (q.some >> i & 1)) {
+        if (Edge && there && (q.some >> i & 1)) {
 #pragma unroll
           for (int k = 0; k < V; ++k)
             if (c + k >= 0 && c + k < q.width) v[i].v[k] = row[c + k];
@@ -176,7 +185,11 @@ struct RowPart {
       }
     }
   }
-  __device__ __forceinline__ void values(float2 (&o)[C / 2]) const {
+  __device__ __forceinline__ void values(float2 (&o)[C / 2], const Columns<V, C, Edge> &q) const {
+    unpack(o);
+    if (Edge) q.mask(o);
+  }
+  __device__ __forceinline__ void unpack(float2 (&o)[C / 2]) const {
     if constexpr (sizeof(T) == 2 && V > 1) {
 #pragma unroll
       for (int i = 0; i < n; ++i)
@@ -190,12 +203,12 @@ struct RowPart {
   }
 };
 
-template <typename T, int V, int C>
-__device__ __forceinline__ void store_part(T *row, const float2 (&o)[C / 2], const Columns<V, C> &q) {
+template <typename T, int V, int C, bool Edge>
+__device__ __forceinline__ void store_part(T *row, const float2 (&o)[C / 2], const Columns<V, C, Edge> &q) {
 #pragma unroll
   for (int i = 0; i < C / V; ++i) {
     const int c = q.first(i);
-    if (!(q.some >> i & 1)) continue;
+    if (!((Edge ? q.some : q.whole) >> i & 1)) continue;
     Pack<T, V> w;
     if constexpr (V == 1) {
       w.v[0] = from_f32<T>(i % 2 ? o[i / 2].y : o[i / 2].x);
@@ -207,7 +220,7 @@ __device__ __forceinline__ void store_part(T *row, const float2 (&o)[C / 2], con
 #pragma unroll
       for (int k = 0; k < V; k += 2) w.v[k] = o[(i * V + k) / 2].x, w.v[k + 1] = o[(i * V + k) / 2].y;
     }
-    if (q.whole >> i & 1) {
+    if (!Edge || (q.whole >> i & 1)) {
       *reinterpret_cast<Pack<T, V> *>(row + c) = w;
     } else {
 #pragma unroll
@@ -284,8 +297,8 @@ __device__ __forceinline__ void gate_act(int act, float2 g, float2 &a, float2 &d
 }
 
 // The rows of v become (v - mu) rstd.
-template <int V, int C, int R>
-__device__ __forceinline__ void norm_rows(float2 (&v)[R][C / 2], const Columns<V, C> &q, bool rms, float inv, float eps,
+template <int V, int C, bool Edge, int R>
+__device__ __forceinline__ void norm_rows(float2 (&v)[R][C / 2], const Columns<V, C, Edge> &q, bool rms, float inv, float eps,
                                           float *slot0, float *slot1, float (&mu)[R], float (&rstd)[R]) {
   constexpr int H = C / 2;
   float s[R];
@@ -340,26 +353,26 @@ struct Turns {
 // ------------------------------------------------------------------ kernels
 
 // R: rows of a group at a time, whose sums go together and which share what is read of the parameters.
-template <typename T, typename P, int V, int C, int R>
+template <typename T, typename P, int V, int C, bool Edge, int R>
 __global__ void __launch_bounds__(kNormThreads, 1) resnorm_forward_rows(const __grid_constant__ ResNormArgs p) {
   constexpr int H = C / 2;
   extern __shared__ float4 params[];  // [5][C / 4][tpr]: scale, w1, b1, w2, b2
   __shared__ float slots[2][4][R * 16];
   const int tpr = p.tpr, width = (int)p.width, groups = blockDim.x / tpr;
   const int shift = V > 1 ? (p.shift + (blockIdx.x % p.classes) * p.step) % V : 0;
-  const Columns<V, C> q(threadIdx.x & (tpr - 1), tpr, width, shift);
+  const Columns<V, C, Edge> q(threadIdx.x & (tpr - 1), tpr, width, shift);
   const float inv = 1.f / (float)width;
   const int each = C / 4 * tpr;
   const Turns w = Turns::of(p, groups, std::integral_constant<int, R>{});
-  RowPart<T, V, C> rf[R], rz[R], rg[R];
-  const uint32_t rows = (uint32_t)p.rows;
+  RowPart<T, V, C, Edge> rf[R], rz[R], rg[R];
+  const uint32_t rows = (uint32_t)p.rows, margin = V / width + 1;
   auto ask = [&](uint32_t row) {
 #pragma unroll
     for (int r = 0; r < R; ++r, row += w.next) {
-      const bool there = row < rows;
-      rf[r].load(row_at<T>(p.f, (uint32_t)row, p.bf), q, there);
-      if (p.act != kNoGate) rg[r].load(row_at<T>(p.gate, (uint32_t)row, p.bg), q, there);
-      rz[r].load(row_at<T>(p.z, (uint32_t)row, p.bz), q, there);
+      const bool there = row < rows, beside = row >= margin && row + margin < rows;
+      rf[r].load(row_at<T>(p.f, row, p.bf), q, there, beside);
+      if (p.act != kNoGate) rg[r].load(row_at<T>(p.gate, row, p.bg), q, there, beside);
+      rz[r].load(row_at<T>(p.z, row, p.bz), q, there, beside);
     }
   };
 #pragma unroll
@@ -375,9 +388,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_forward_rows(const __
     float2 v[R][H], z[R][H], a[R][H], k[H], k2[H];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      rf[r].values(v[r]);
-      rz[r].values(z[r]);
-      if (p.act != kNoGate) rg[r].values(a[r]);
+      rf[r].values(v[r], q);
+      rz[r].values(z[r], q);
+      if (p.act != kNoGate) rg[r].values(a[r], q);
     }
     if (lead + w.step < rows) ask(row + w.step);
     if (p.act != kNoGate)
@@ -390,7 +403,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_forward_rows(const __
         }
     float mu1[R] = {}, rs1[R] = {}, mu2[R] = {}, rs2[R] = {};
     if (p.post) {
-      norm_rows<V, C, R>(v, q, p.rms, inv, p.eps, slots[turn][0], slots[turn][1], mu1, rs1);
+      norm_rows<V, C, Edge, R>(v, q, p.rms, inv, p.eps, slots[turn][0], slots[turn][1], mu1, rs1);
       param_part<C>(params + each, q.t, tpr, k);
       param_part<C>(params + 2 * each, q.t, tpr, k2);
 #pragma unroll
@@ -407,10 +420,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_forward_rows(const __
 #pragma unroll
       for (int j = 0; j < H; ++j) v[r][j] = fma2(v[r][j], k[j], z[r][j]);
       const uint32_t at = row + r * w.next;
-      if (at < rows) store_part<T, V, C>(row_at<T>(p.znew, at, p.bw), v[r], q);
+      if (at < rows) store_part<T, V, C, Edge>(row_at<T>(p.znew, at, p.bw), v[r], q);
     }
     if (p.y) {
-      norm_rows<V, C, R>(v, q, p.rms, inv, p.eps, slots[turn][2], slots[turn][3], mu2, rs2);
+      norm_rows<V, C, Edge, R>(v, q, p.rms, inv, p.eps, slots[turn][2], slots[turn][3], mu2, rs2);
       param_part<C>(params + 3 * each, q.t, tpr, k);
       param_part<C>(params + 4 * each, q.t, tpr, k2);
 #pragma unroll
@@ -418,7 +431,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_forward_rows(const __
 #pragma unroll
         for (int j = 0; j < H; ++j) v[r][j] = fma2(v[r][j], k[j], k2[j]);
         const uint32_t at = row + r * w.next;
-        if (at < rows) store_part<T, V, C>(row_at<T>(p.y, at, p.bw), v[r], q);
+        if (at < rows) store_part<T, V, C, Edge>(row_at<T>(p.y, at, p.bw), v[r], q);
       }
     }
     if (p.stats && q.t == 0)
@@ -431,7 +444,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_forward_rows(const __
   }
 }
 
-template <typename T, typename P, int V, int C>
+template <typename T, typename P, int V, int C, bool Edge>
 __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const __grid_constant__ ResNormArgs p) {
   constexpr int H = C / 2;
   extern __shared__ float4 params[];  // [4][C / 4][tpr]: scale, w1, b1, w2; then, with more than one group, [kNormSums][width]
@@ -439,7 +452,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
   grid_dependency_launch();  // the sums over blocks start as multiprocessors become free, and wait there
   const int tpr = p.tpr, width = (int)p.width, groups = blockDim.x / tpr;
   const int shift = V > 1 ? (p.shift + (blockIdx.x % p.classes) * p.step) % V : 0;
-  const Columns<V, C> q(threadIdx.x & (tpr - 1), tpr, width, shift);
+  const Columns<V, C, Edge> q(threadIdx.x & (tpr - 1), tpr, width, shift);
   const float inv = 1.f / (float)width;
   const int each = C / 4 * tpr;
   const Turns w = Turns::of(p, groups, std::integral_constant<int, 1>{});
@@ -448,19 +461,19 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
   for (int k = 0; k < kNormSums; ++k)
 #pragma unroll
     for (int j = 0; j < H; ++j) sums[k][j] = both(0.f);
-  const uint32_t rows = (uint32_t)p.rows;  // (below 2^31)
-  RowPart<T, V, C> rf, rz, rg, rdz, rdy;
+  const uint32_t rows = (uint32_t)p.rows, margin = V / width + 1;  // (below 2^31)
+  RowPart<T, V, C, Edge> rf, rz, rg, rdz, rdy;
   float4 st;
   rg.clear();
   rdz.clear();
   rdy.clear();
   auto ask = [&](uint32_t r) {
-    const bool there = r < rows;
-    rf.load(row_at<T>(p.f, r, p.bf), q, there);
-    if (p.act != kNoGate) rg.load(row_at<T>(p.gate, r, p.bg), q, there);
-    rz.load(row_at<T>(p.z, r, p.bz), q, there);
-    if (p.dy) rdy.load(row_at<T>(p.dy, r, p.bdy), q, there);
-    if (p.dz) rdz.load(row_at<T>(p.dz, r, p.bdz), q, there);
+    const bool there = r < rows, beside = r >= margin && r + margin < rows;
+    rf.load(row_at<T>(p.f, r, p.bf), q, there, beside);
+    if (p.act != kNoGate) rg.load(row_at<T>(p.gate, r, p.bg), q, there, beside);
+    rz.load(row_at<T>(p.z, r, p.bz), q, there, beside);
+    if (p.dy) rdy.load(row_at<T>(p.dy, r, p.bdy), q, there, beside);
+    if (p.dz) rdz.load(row_at<T>(p.dz, r, p.bdz), q, there, beside);
     st = there ? p.stats[r] : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   ask(w.row);
@@ -473,7 +486,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
     // t = act(gate) u;  sa = scale act(gate), by which D becomes du;  sg = scale u act'(gate), by which it becomes dgate
     float2 fh[H], t[H], sa[H], sg[H], d[H], k[H];
     const float mu1 = st.x, rs1 = st.y, mu2 = st.z, rs2 = st.w;
-    rf.values(fh);
+    rf.values(fh, q);
     if (p.post) {
 #pragma unroll
       for (int j = 0; j < H; ++j) fh[j] = mul2(add2(fh[j], both(-mu1)), both(rs1));
@@ -489,7 +502,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
     param_part<C>(params, q.t, tpr, k);
     if (p.act != kNoGate) {
       float2 g[H];
-      rg.values(g);
+      rg.values(g, q);
 #pragma unroll
       for (int j = 0; j < H; ++j) {
         float2 a, da;
@@ -502,11 +515,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
 #pragma unroll
       for (int j = 0; j < H; ++j) sg[j] = both(0.f), sa[j] = k[j];
     }
-    rdz.values(d);
+    rdz.values(d, q);
     if (p.dy) {
       float2 zh[H], dy[H];
-      rz.values(zh);
-      rdy.values(dy);
+      rz.values(zh, q);
+      rdy.values(dy, q);
 #pragma unroll
       for (int j = 0; j < H; ++j) zh[j] = mul2(add2(fma2(t[j], k[j], zh[j]), both(-mu2)), both(rs2));
       q.mask(zh);
@@ -531,14 +544,14 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
       ask(row + w.step);
     }
     const bool live = row < rows;
-    if (live && p.dz_in) store_part<T, V, C>(row_at<T>(p.dz_in, row, p.bw), d, q);
+    if (live && p.dz_in) store_part<T, V, C, Edge>(row_at<T>(p.dz_in, row, p.bw), d, q);
 #pragma unroll
     for (int j = 0; j < H; ++j) {
       sums[0][j] = fma2(d[j], t[j], sums[0][j]);
       sg[j] = mul2(sg[j], d[j]);
       d[j] = mul2(d[j], sa[j]);
     }
-    if (live && p.dgate) store_part<T, V, C>(row_at<T>(p.dgate, row, p.bw), sg, q);
+    if (live && p.dgate) store_part<T, V, C, Edge>(row_at<T>(p.dgate, row, p.bw), sg, q);
     if (p.post) {
       param_part<C>(params + each, q.t, tpr, k);
       float2 s1 = both(0.f), s2 = s1;
@@ -556,7 +569,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) resnorm_backward_rows(const _
 #pragma unroll
       for (int j = 0; j < H; ++j) d[j] = mul2(fma2(fh[j], both(m2), add2(d[j], both(m1))), both(rs1));
     }
-    if (live && p.df) store_part<T, V, C>(row_at<T>(p.df, row, p.bw), d, q);
+    if (live && p.df) store_part<T, V, C, Edge>(row_at<T>(p.df, row, p.bw), d, q);
   }
   if (!p.parts) return;
   float *to = p.parts + (int64_t)blockIdx.x * kNormSums * width, *cols = (float *)(params + 4 * each);
@@ -776,11 +789,13 @@ cudaError_t resnorm_forward_as(ResNormArgs p, bool vec, cudaStream_t st) {
   const int R = pl.columns == 8 && vec ? 2 : 1;
   const int grid = resnorm_grid(pl, p.rows, (int64_t)(pl.block / pl.tpr) * R, p.classes, 512);
   const size_t smem = 5 * sizeof(float) * (size_t)pl.tpr * pl.columns;
+  const bool edge = vec && (p.shift || p.step || p.width % V);
+#define SLA_RESNORM_FWD(V, C, EDGE, R) \
+  launch_resnorm(resnorm_forward_rows<T, P, V, C, EDGE, R>, p, grid, pl.block, smem, st)
   if (pl.columns == 8)
-    return vec ? launch_resnorm(resnorm_forward_rows<T, P, V, 8, 2>, p, grid, pl.block, smem, st)
-               : launch_resnorm(resnorm_forward_rows<T, P, 1, 8, 1>, p, grid, pl.block, smem, st);
-  return vec ? launch_resnorm(resnorm_forward_rows<T, P, V, 16, 1>, p, grid, pl.block, smem, st)
-             : launch_resnorm(resnorm_forward_rows<T, P, 1, 16, 1>, p, grid, pl.block, smem, st);
+    return !vec ? SLA_RESNORM_FWD(1, 8, false, 1) : edge ? SLA_RESNORM_FWD(V, 8, true, 2) : SLA_RESNORM_FWD(V, 8, false, 2);
+  return !vec ? SLA_RESNORM_FWD(1, 16, false, 1) : edge ? SLA_RESNORM_FWD(V, 16, true, 1) : SLA_RESNORM_FWD(V, 16, false, 1);
+#undef SLA_RESNORM_FWD
 }
 
 template <typename T, typename P>
@@ -797,11 +812,12 @@ cudaError_t resnorm_backward_as(ResNormArgs p, bool vec, int grid, cudaStream_t 
   if (!vec) p.classes = 1, p.shift = p.step = 0;
   const size_t smem = 4 * sizeof(float) * (size_t)pl.tpr * pl.columns +
                       (pl.block > pl.tpr && p.parts ? kNormSums * sizeof(float) * (size_t)p.width : 0);
+  const bool edge = vec && (p.shift || p.step || p.width % V);
+#define SLA_RESNORM_BWD(V, C, EDGE) launch_resnorm(resnorm_backward_rows<T, P, V, C, EDGE>, p, grid, pl.block, smem, st)
   if (pl.columns == 8)
-    return vec ? launch_resnorm(resnorm_backward_rows<T, P, V, 8>, p, grid, pl.block, smem, st)
-               : launch_resnorm(resnorm_backward_rows<T, P, 1, 8>, p, grid, pl.block, smem, st);
-  return vec ? launch_resnorm(resnorm_backward_rows<T, P, V, 16>, p, grid, pl.block, smem, st)
-             : launch_resnorm(resnorm_backward_rows<T, P, 1, 16>, p, grid, pl.block, smem, st);
+    return !vec ? SLA_RESNORM_BWD(1, 8, false) : edge ? SLA_RESNORM_BWD(V, 8, true) : SLA_RESNORM_BWD(V, 8, false);
+  return !vec ? SLA_RESNORM_BWD(1, 16, false) : edge ? SLA_RESNORM_BWD(V, 16, true) : SLA_RESNORM_BWD(V, 16, false);
+#undef SLA_RESNORM_BWD
 }
 
 }  // namespace sla

@@ -128,7 +128,7 @@ def check_grads(g, want):
 
 
 SHAPES = [(1, 1), (3, 2), (5, 7), (1, 64), (33, 64), (257, 96), (64, 250), (2, 1001), (19, 1024), (5003, 136), (300, 256),
-          (7, 4099), (9, 4096), (3, 4104), (5, 8192), (4, 8191), (3, 8200), (2, 20001), (70000, 8)]
+          (7, 4099), (9, 4096), (3, 4104), (5, 8192), (4, 8191), (3, 8183), (3, 8200), (2, 20001), (70000, 8), (50, 3), (90, 9)]
 HOWS = [dict(norm="layer", post_norm=True, gate_activation="sigmoid"), dict(norm="rms", post_norm=True, gate_activation="silu"),
         dict(norm="layer", post_norm=False, gate_activation="none"), dict(norm="rms", post_norm=True, gate_activation="")]
 
