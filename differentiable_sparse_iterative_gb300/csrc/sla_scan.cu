@@ -30,6 +30,10 @@
 // What costs is instructions as much as bytes (two special functions an element and some twenty other
 // instructions), so rows are walked with running pointers, and warps whose rows hold no sequence's start or end, nearly
 // all where sequences are long, take a copy of the loops without those checks.
+//
+// Measured by tiles, against the copy rate of 6.8 TB/s: one sequence of 1,000,000 x 64 float32 179 us (0.63), in bfloat16 159
+// (0.37) and 395 a training step (0.40); 57 packed sequences, 60,001 x 333 float16, backwards, a training step 173 us (0.27).
+// By walks (below): 1000 sequences of 1000 x 64 bfloat16, a training step 263 us (0.57), in float32 328 (0.92).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -197,3 +197,70 @@ def test_the_example_with_mixing():
         d, g = (f[0] - f[1]) / (2 * h), float((p.grad.double() * v.double()).sum())
         # h^2 of the third derivative, and float32 rounding of the network (1e-6 of the loss) over h
         assert abs(d - g) <= 2e-3 * float(p.grad.norm()) + 2e-4 * f[0], (d, g)
+
+
+def test_a_training_step_from_a_graph():
+    dtype, width, n = torch.bfloat16, 64, 600
+    p = weights(width, 96, dtype)
+    data = [randn(n, width, dtype=dtype, seed=70), randn(n, width, dtype=dtype, seed=71),
+            randn(2, width, dtype=torch.float32, seed=72)]
+    offsets = torch.tensor([0, 250, n], dtype=torch.int32, device=DEV)
+    up = randn(n, width, dtype=dtype, seed=73)
+
+    def step(leaves):
+        z, y, final = network(*leaves[:3], leaves[3:], offsets)
+        return [z, y, final, *torch.autograd.grad([z, y], leaves, [up, up])]
+
+    want = [t.detach().clone() for t in step([t.clone().requires_grad_() for t in (*data, *p)])]
+    leaves = [t.clone().requires_grad_() for t in (*data, *p)]  # of the graph alone
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(leaves)
+    for _ in range(3):
+        for t in out:
+            t.detach().zero_()
+        graph.replay()
+        assert all(torch.equal(a, r) for a, r in zip(out, want))
+    sla.sla_gated_ffn_check()
+
+
+def test_arrays_of_more_than_2_31_elements():
+    # the last rows of large arrays against a call on them alone
+    width, dtype, tail = 64, torch.bfloat16, 5000
+    n = (1 << 31) // width + 7 * tail
+    base = randn(1 << 16, width, dtype=dtype, seed=80)
+    x = base.repeat(n // (1 << 16) + 1, 1)[:n]
+    last = x[-tail:].clone()
+    w, b = randn(width, width, dtype=dtype, seed=81, scale=width ** -0.5), randn(width, dtype=dtype, seed=82)
+    y = sla.sla_linear(x, w, b, residual=x)
+    assert torch.equal(y[-tail:], sla.sla_linear(last, w, b, residual=last))
+    del y
+    z, y, stats = sla.sla_residual_norm(x, x, scale=b, weight=b, stats=True)
+    z1, y1, stats1 = sla.sla_residual_norm(last, last, scale=b, weight=b, stats=True)
+    assert torch.equal(z[-tail:], z1) and torch.equal(y[-tail:], y1) and torch.equal(stats[-tail:], stats1)
+    del z, y
+    g = sla.sla_residual_norm_backward(x, x, x, x, stats, scale=b, weight=b, want_grad_params=False)
+    g1 = sla.sla_residual_norm_backward(last, last, last, last, stats1, scale=b, weight=b, want_grad_params=False)
+    assert torch.equal(g.block[-tail:], g1.block) and torch.equal(g.z[-tail:], g1.z)
+    del g, stats
+    # tiles (one long sequence before the last) and walks (sequences of `tail` rows); the last sequence has the same rows, but
+    # tiles of others: float32 steps apart, a rounding of the result
+    for how in (dict(offsets=torch.tensor([0, n - tail, n], dtype=torch.int64, device=DEV)), dict()):
+        rows = x if how else x[n % tail:].view(-1, tail, width)
+        h, final, saved = sla.sla_gated_scan(rows, rows, save=True, **how)
+        h1, final1, saved1 = sla.sla_gated_scan(last, last, save=True)
+        flat = h.view(-1, width)
+        assert float((final[-1:] - final1).abs().max()) <= 2.0 ** -18
+        assert float((flat[-tail:].float() - h1.float()).abs().max()) <= 2.0 ** -7 * float(h1.abs().max())
+        dx, dg, _ = sla.sla_gated_scan_backward(rows, rows, rows, saved, **how)
+        dx1, dg1, _ = sla.sla_gated_scan_backward(last, last, last, saved1)
+        for a, r in ((dx, dx1), (dg, dg1)):
+            assert float((a.view(-1, width)[-tail:].float() - r.float()).abs().max()) <= 2.0 ** -7 * float(r.abs().max())
+        del h, saved, flat, dx, dg
+    sla.sla_gated_ffn_check()
