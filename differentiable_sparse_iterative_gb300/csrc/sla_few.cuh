@@ -1,4 +1,4 @@
-// The gated feed-forward block for few tokens (up to kFewTokens), forward.
+// The gated feed-forward block and the linear layer for few tokens (up to kFewTokens), forward.
 //
 // With a token or a few the weights are read once and little else happens: the floor is their bytes
 // over the memory's rate (25 MB at 1024 -> 4096 -> 1024: 3.8 us).  tcgen05 tiles would be 128 rows high

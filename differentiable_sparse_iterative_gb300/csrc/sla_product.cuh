@@ -1,4 +1,4 @@
-// Tensor-core matrix products of the gated feed-forward block, with the block's elementwise work as
+// Tensor-core matrix products of the gated feed-forward block and the linear layer, with the elementwise work of both as
 // their epilogues.
 //
 //   C[m][n] = sum over segments s, sum over k of A_s(m, k) B_s(n, k)

@@ -28,7 +28,7 @@
 // with A = kCut, whose H replaces what came before, whatever that is: an infinity or a NaN stays within its sequence.
 //
 // What costs is instructions as much as bytes (two special functions an element and some twenty other
-// instructions), so rows are walked with running pointers, and warps whose rows hold no sequence's start or end, nearly
+// instructions), so an address is one multiply-add, and warps whose rows hold no sequence's start or end, nearly
 // all where sequences are long, take a copy of the loops without those checks.
 //
 // Measured by tiles, against the copy rate of 6.8 TB/s: one sequence of 1,000,000 x 64 float32 179 us (0.63), in bfloat16 159
@@ -326,6 +326,7 @@ struct TileMemory {
   Map carry[kWarps][32];  // parts of the way from the known state to the tile: folds, then tiles
   int64_t origin;         // the scan's index of the first row that the tile's first row depends on
   uint32_t next;
+  volatile uint32_t dead; // a wait of this block has expired: it waits no more, so that the launch ends
 };
 
 __device__ __forceinline__ Map no_rows() { return {f2(1.f, 1.f), f2(0.f, 0.f)}; }
@@ -338,8 +339,10 @@ __device__ __forceinline__ Map joined(const Map (*maps)[32], int from, int to, i
 }
 
 // This warp's part of the way from the start of the tile's sequence, in tile `first`, or the state before its span, to the tile.
-__device__ __forceinline__ Map look_back(const ScanArgs &p, int tile, int first, int64_t mine, int64_t apart, int warp, int lane) {
+__device__ __forceinline__ Map look_back(const ScanArgs &p, TileMemory &sm, int tile, int first, int64_t mine, int64_t apart,
+                                         int warp, int lane) {
   Map m = no_rows();
+  if (__any_sync(0xffffffffu, sm.dead)) return m;
   const int base = tile / kSpan * kSpan, fold = tile / kFold * kFold;
   // half of the warps take the folds before the present one, half the tiles of the present one
   constexpr int H = kWarps / 2;
@@ -352,18 +355,21 @@ __device__ __forceinline__ Map look_back(const ScanArgs &p, int tile, int first,
     const uint64_t *q = p.states + (int64_t)(base / kSpan - 1) * apart + mine;
     ok = wait_for(q, m, look(q, m));
   }
-  for (int i = from; i < to; i += 2, at += 2 * apart) {
+  for (int i = from; i < to && ok; i += 2, at += 2 * apart) {
     Map n, n2;
     const bool two = i + 1 < to;
     const bool there = look(at, n), there2 = !two || look(at + apart, n2);
-    ok = wait_for(at, n, there) && ok;
+    ok = wait_for(at, n, there);
     join(m, n);
-    if (two) {
-      ok = wait_for(at + apart, n2, there2) && ok;
+    if (two && ok) {
+      ok = wait_for(at + apart, n2, there2);
       join(m, n2);
     }
   }
-  if (!ok && lane == 0) atomicAdd_system(p.timeouts, 1u);
+  if (!ok && lane == 0) {
+    sm.dead = 1;
+    atomicAdd_system(p.timeouts, 1u);
+  }
   return m;
 }
 
@@ -416,7 +422,7 @@ __device__ __forceinline__ float2 state_before(const ScanArgs &p, TileMemory &sm
     join(own, sm.maps[warp][lane]);
     publish(p.maps + t.tile * apart + mine, own);
   }
-  sm.carry[warp][lane] = needed ? look_back(p, t.tile, (int)(origin / R::tile_rows), mine, apart, warp, lane) : no_rows();
+  sm.carry[warp][lane] = needed ? look_back(p, sm, t.tile, (int)(origin / R::tile_rows), mine, apart, warp, lane) : no_rows();
   if ((t.tile + 1) % kFold == 0 && warp >= kWarps / 2) {
     // as soon as the tiles' half is through, not waiting for the states that the others may wait for
     asm volatile("bar.sync 1, %0;" ::"n"(32 * (kWarps - kWarps / 2)) : "memory");
@@ -600,7 +606,10 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<T, Backward>) scan_kern
   const uint32_t all = (uint32_t)p.tiles * (uint32_t)p.groups;
   uint32_t id = blockIdx.x;
   if (Chain) {
-    if (threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
+    if (threadIdx.x == 0) {
+      sm.dead = 0;
+      sm.next = atomicAdd(p.counter, 1u) + 1u;
+    }
     __syncthreads();
     id = sm.next;
   }
