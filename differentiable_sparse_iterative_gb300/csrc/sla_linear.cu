@@ -6,7 +6,8 @@
 // Three tensor-core products (sla_product.cuh): the forward one with activation, derivative and residual as its
 // epilogue, the two of the backward pass in one launch.  Between them stands dp, which both read as an operand: without an
 // activation it is dy itself, in place where TMA can read it; else a kernel forms it from dy and the kept act'(p), lays
-// it out, and sums its columns on the way.  Up to kFewTokens tokens the forward product is sla_few.cuh's.
+// it out, and sums its columns on the way.  Up to kFewTokens tokens the forward product is sla_few.cuh's; layers of a few
+// outputs are sla_skinny.cuh's (skinny).
 //
 // act'(p) is kept in float32.  16-bit tensor-core operands have to be 16 bits: dp = dy act'(p) is rounded once, beside the
 // result's own rounding (0.0024 in relative L2 in bfloat16, 0.0003 in float16, where one rounding makes 0.0017 and 0.00021;
@@ -23,6 +24,7 @@
 
 #include "sla_dense.cuh"
 #include "sla_few.cuh"
+#include "sla_skinny.cuh"
 
 namespace sla {
 namespace {
@@ -30,10 +32,24 @@ namespace {
 int64_t out_pitch(const sla_layer *f) { return round_up(f->out, 16); }
 bool activates(const sla_layer *f) { return f->activation != SLA_ACT_NONE; }
 
+// Few outputs take sla_skinny.cuh's kernels.  Training step, there against here: float32, 302,053 tokens, 384 -> 5 507 us
+// against 710, 1,000,000, 64 -> 1 136 against 645; 16 bits, 300,000 tokens, 384 -> 2 224 against 331, 384 -> 4 490 against 332
+// (the arithmetic outweighs the copies of float32 data in parts), 1,000,000, 128 -> 4 423 against 477, 128 -> 8 550 against 498.
+bool skinny(const sla_layer *f) {
+  if (f->out > kSkinny || f->width > kSkinnyWidth) return false;
+  return f->dtype == SLA_F32 || f->out <= 2 || f->out * f->width <= 512;
+}
+
+// Forward, 16-bit rows of some length, or of no alignment, are the tensor cores' all the same (384 -> 1: 55 us against 69; 63 -> 4:
+// 122 against 155; 128 -> 2: 85 against 66), and up to kFewTokens tokens sla_few.cuh's.
+bool skinny_y(const sla_layer *f) {
+  return skinny(f) && (f->dtype == SLA_F32 || (f->width <= 128 && f->width % 8 == 0));
+}
+
 // Whether a forward call leaves packed copies of x and the weight: where TMA cannot read dense originals (the sizes alone
 // decide, so that both calls and the layout of what is saved agree).
 bool keeps_packed(const sla_layer *f) {
-  return f->tokens > kFewTokens && (f->dtype == SLA_F32 || f->width % 8 != 0);
+  return !skinny(f) && f->tokens > kFewTokens && (f->dtype == SLA_F32 || f->width % 8 != 0);
 }
 
 // act'(p) in float32, rows out_pitch apart, then packed copies of x and the weight.
@@ -55,7 +71,7 @@ SavedLayout saved_layout(const sla_layer *f) {
 constexpr int64_t kTwoParts = (int64_t)1 << 31;
 
 bool two_parts(const sla_layer *f) {
-  if (!activates(f) || f->activation == SLA_ACT_RELU || f->dtype == SLA_F32) return false;
+  if (!activates(f) || f->activation == SLA_ACT_RELU || f->dtype == SLA_F32 || skinny(f)) return false;
   const int64_t plane = f->width * f->out;  // at most 2^48
   return plane <= kTwoParts && f->tokens <= kTwoParts / plane;
 }
@@ -75,7 +91,7 @@ struct ForwardScratch {
 ForwardScratch forward_scratch(const sla_layer *f, char *base) {
   Arena a{base};
   ForwardScratch s{};
-  if (f->tokens <= kFewTokens) return s;
+  if (f->tokens <= kFewTokens || skinny_y(f)) return s;
   s.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
   s.w = a.take(packed_bytes(f->out, f->width, f->dtype));
   const ProductSize y = y_size(f);
@@ -93,9 +109,24 @@ struct BackwardScratch {
   ProductPlan plan;
 };
 
+// Blocks of the backward kernel for few outputs, each of which leaves partial sums.
+int skinny_blocks(const sla_layer *f) {
+  int tpr = 1;
+  while (tpr * 8 < f->width) tpr <<= 1;
+  const int64_t rows = (int64_t)(256 / tpr) * kSkinnyBackRows;  // of a block's turn
+  return (int)std::min<int64_t>(sm_count() * 2, (f->tokens + rows - 1) / rows);
+}
+
 BackwardScratch backward_scratch(const sla_layer *f, char *base) {
   Arena a{base};
   BackwardScratch s{};
+  if (skinny(f)) {
+    const size_t blocks = (size_t)skinny_blocks(f);
+    s.parts = (float *)a.take(blocks * (size_t)(f->out * f->width) * sizeof(float));
+    s.columns = (float *)a.take(blocks * (size_t)f->out * sizeof(float));
+    s.total = a.used;
+    return s;
+  }
   s.dp = a.take((two_parts(f) ? 2 : 1) * packed_bytes(f->tokens, f->out, f->dtype));
   s.x = a.take(packed_bytes(f->tokens, f->width, f->dtype));
   s.w = a.take(packed_bytes(f->out, f->width, f->dtype));
@@ -161,6 +192,61 @@ __global__ void __launch_bounds__(256) form_dp(int64_t rows, int64_t cols, const
   }
 }
 
+// Calls run with O = 1, 2, 4 or 8, no fewer than the outputs.
+template <typename F>
+cudaError_t by_outputs(int64_t out, F &&run) {
+  if (out <= 1) return run(std::integral_constant<int, 1>{});
+  if (out <= 2) return run(std::integral_constant<int, 2>{});
+  return out <= 4 ? run(std::integral_constant<int, 4>{}) : run(std::integral_constant<int, 8>{});
+}
+
+template <typename K>
+cudaError_t launch_skinny(K kernel, const SkinnyArgs &p, int blocks, size_t smem, cudaStream_t st) {
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<blocks, 256, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+// Whether rows of x (and dx) may be read in vectors of 16 bytes.
+template <typename T>
+bool skinny_vec(const SkinnyArgs &p) {
+  constexpr int V = 16 / sizeof(T);
+  return p.width % V == 0 && aligned(p.x, 16) && (p.tokens == 1 || p.ldx % V == 0) && aligned(p.dx, 16);
+}
+
+template <typename T>
+cudaError_t run_skinny_forward(SkinnyArgs p, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = skinny_vec<T>(p);
+  p.tpr = 1;
+  while (p.tpr < 32 && p.tpr * (vec ? V : 1) < p.width) p.tpr <<= 1;
+  const int64_t rows = (int64_t)(256 / p.tpr) * kSkinnyRows;
+  const int blocks = (int)std::min<int64_t>((p.tokens + rows - 1) / rows, sm_count() * 6);
+  return by_outputs(p.out, [&](auto o) {
+    constexpr int O = decltype(o)::value;
+    const size_t smem = O * sizeof(float) * (size_t)skinny_padded(p.width, p.tpr, vec ? V : 1);
+    return vec ? launch_skinny(skinny_forward<T, O, V>, p, blocks, smem, st)
+               : launch_skinny(skinny_forward<T, O, 1>, p, blocks, smem, st);
+  });
+}
+
+template <typename T>
+cudaError_t run_skinny_backward(SkinnyArgs p, int blocks, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = skinny_vec<T>(p);
+  p.tpr = 1;
+  while (p.tpr * 8 < p.width) p.tpr <<= 1;
+  return by_outputs(p.out, [&](auto o) {
+    constexpr int O = decltype(o)::value;
+    const size_t smem = O * sizeof(float) * (size_t)p.tpr * 8;
+    return vec ? launch_skinny(skinny_backward<T, O, V>, p, blocks, smem, st)
+               : launch_skinny(skinny_backward<T, O, 1>, p, blocks, smem, st);
+  });
+}
+
 template <typename T>
 sla_status forward(const sla_layer *f, const T *x, int64_t ldx, const T *w, const T *bias, const T *residual, int64_t ldr,
                    T *y, char *saved, const ForwardScratch &s, cudaStream_t st) {
@@ -178,6 +264,14 @@ sla_status forward(const sla_layer *f, const T *x, int64_t ldx, const T *w, cons
     p.x_vec = aligned(x, 16) && (f->tokens == 1 || ldx % 8 == 0), p.w_vec = aligned(w, 16) && f->width % 8 == 0;
     p.c = y, p.g = da, p.ldg = out_pitch(f), p.residual = residual, p.ldr = ldr;
     c.launched(launch_few<T>(kLinear, p, st));
+    return finish(c);
+  }
+  if (skinny_y(f)) {
+    SkinnyArgs p{};
+    p.tokens = f->tokens, p.width = (int)f->width, p.out = (int)f->out, p.act = f->activation;
+    p.x = x, p.ldx = ldx, p.w = w, p.bias = bias, p.residual = residual, p.ldr = ldr, p.y = y;
+    p.da = da, p.ldda = out_pitch(f);
+    c.launched(run_skinny_forward<T>(p, st));
     return finish(c);
   }
   PackJobs packs;
@@ -205,6 +299,19 @@ sla_status backward(const sla_layer *f, const T *dy, int64_t lddy, const T *x, i
   if (earlier.err != cudaSuccess) return fail(earlier.err);
   SLA_CHECK(report_expired(earlier));
   c.timeouts = earlier.count;
+  if (skinny(f)) {
+    const int blocks = skinny_blocks(f);
+    SkinnyArgs p{};
+    p.tokens = f->tokens, p.width = (int)f->width, p.out = (int)f->out;
+    p.x = x, p.ldx = ldx, p.w = w, p.da = activates(f) ? (float *)const_cast<char *>(saved) : nullptr, p.ldda = out_pitch(f);
+    p.dy = dy, p.lddy = lddy, p.dx = dx, p.parts = dw ? s.parts : nullptr, p.bias_parts = db ? s.columns : nullptr;
+    c.launched(run_skinny_backward<T>(p, blocks, st));
+    ColumnSums sums{c, nullptr, {}};
+    if (dw) sums.add(s.parts, blocks, f->out * f->width, f->out * f->width, f->out * f->width, dw);
+    if (db) sums.add(s.columns, blocks, f->out, f->out, f->out, db);
+    sums.finish<T>();
+    return finish(c);
+  }
   const SavedLayout L = saved_layout(f);
   const Copy copy = keeps_packed(f) ? kKept : kOwn;
   char *sv = const_cast<char *>(saved);

@@ -224,3 +224,78 @@ def test_refusals():
             (lambda: sla.sla_linear_backward(y[:8], x[:8], w, saved, activation="gelu"), "saved is from")):
         with pytest.raises(ValueError, match=message):
             call()
+
+
+# Few outputs.  A thread adds up at most tokens / 304 + 2 products of dW in a row: a random walk of roundings, below 2^-24
+# sqrt(300) = 1.1e-6 here, within the tolerances above.
+FEW = [(17, 1, 1), (19, 3, 2), (33, 7, 3), (40, 64, 8), (301, 250, 5), (70001, 64, 1), (1003, 384, 4), (515, 2047, 8),
+       (260, 2048, 2), (100, 2049, 2), (2000, 129, 2), (70, 130, 1), (3, 64, 3), (1, 2048, 8), (5000, 48, 7), (300, 64, 9)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,width,out", FEW)
+def test_few_outputs(tokens, width, out, dtype):
+    x, w, b, r, dy = data(tokens, width, out, dtype, seed=300)
+    for act, bias, res in (("none", b, None), ("gelu", b, r), ("relu", None, r), ("silu", None, None)):
+        leaves = [t.double().requires_grad_() for t in (x, w, b)]
+        want = linear64(leaves[0], leaves[1], None if bias is None else leaves[2], None if res is None else res.double(), act)
+        y, saved = sla.sla_linear(x, w, bias, res, activation=act, save=True)
+        for t in (y, sla.sla_linear(x, w, bias, res, activation=act)):
+            assert float((t.double() - want.detach()).norm()) <= y_tol(dtype) * float(want.detach().norm() + b.double().norm()), act
+        want.backward(dy.double())
+        dx, dw, db = sla.sla_linear_backward(dy, x, w, saved, activation=act, want_grad_bias=True)
+        # of a single row or column the sums may nearly cancel: relative to the terms' sizes
+        p = linear64(leaves[0], leaves[1], None if bias is None else leaves[2], None, "none").detach().requires_grad_()
+        linear64(p, torch.eye(out, dtype=torch.float64, device=DEV), None, None, act).backward(dy.double())
+        dp, x64, w64 = p.grad.abs(), x.double().abs(), w.double().abs()
+        for got, ref, size in ((dx, leaves[0].grad, dp @ w64), (dw, leaves[1].grad, dp.T @ x64)):
+            scale = float(ref.norm()) + 2.0 ** -8 * float(size.norm())
+            assert float((got.double() - ref).norm()) <= grad_tol(dtype, min(tokens, out)) * scale, act
+        if bias is not None:
+            scale = float(leaves[2].grad.norm()) + 2.0 ** -8 * float(dp.sum(0).norm())
+            assert float((db.double() - leaves[2].grad).norm()) <= grad_tol(dtype, 1) * scale, act
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width,out", [(64, 3), (63, 2), (96, 1)])
+def test_few_outputs_layouts_and_rows_apart(width, out, dtype):
+    tokens = 203
+    x, w, b, r, dy = data(tokens, width, out, dtype, seed=320)
+    y, saved = sla.sla_linear(x, w, b, r, activation="silu", save=True)
+    dx, dw, db = sla.sla_linear_backward(dy, x, w, saved, activation="silu", want_grad_bias=True)
+    for pad in (1, 8):
+        wide, wide_dy = torch.full((tokens, width + pad), float("nan"), dtype=dtype, device=DEV), torch.zeros_like(dy.repeat(1, 3))
+        wide[:, :width], wide_dy[:, 1:1 + out] = x, dy
+        xs, dys = wide[:, :width], wide_dy[:, 1:1 + out]
+        y2, saved2 = sla.sla_linear(xs, w, b, r, activation="silu", save=True)
+        dx2, dw2, db2 = sla.sla_linear_backward(dys, xs, w, saved2, activation="silu", want_grad_bias=True)
+        assert rel(y2, y) <= 2 * y_tol(dtype)  # (columns of a thread differ: so does the order of the sums)
+        for a, c in ((dx2, dx), (dw2, dw), (db2, db)):
+            assert rel(a, c) <= 2 * grad_tol(dtype)
+    again = sla.sla_linear_backward(dy, x, w, saved, activation="silu", want_grad_bias=True)
+    assert all(torch.equal(a, c) for a, c in zip(again, (dx, dw, db)))
+    for value in (float("nan"), float("inf")):  # the last row too, which threads without a row read
+        x2 = x.clone()
+        x2[tokens - 1, width - 1], x2[3, 0] = value, value
+        y2 = sla.sla_linear(x2, w, b, r, activation="none")
+        kept = torch.ones(tokens, dtype=torch.bool, device=DEV)
+        kept[3] = kept[tokens - 1] = False
+        assert torch.equal(y2[kept], sla.sla_linear(x, w, b, r, activation="none")[kept]) and not bool(y2[~kept].isfinite().any())
+        if value == value:  # dW_oc = sum dp_o x_c: infinite in those columns, no NaN in any
+            _, dw2, _ = sla.sla_linear_backward(dy, x2, w, sla.sla_linear(x2, w, b, save=True)[1])
+            assert not bool(dw2[:, 1:width - 1].isinf().any()) and not bool(dw2.isnan().any())
+            assert bool(dw2[:, [0, width - 1]].isinf().all())
+
+
+def test_few_outputs_some_gradients_and_no_tokens():
+    x, w, b, r, dy = data(50, 64, 2, torch.float32, seed=340)
+    _, saved = sla.sla_linear(x, w, b, save=True)
+    full = sla.sla_linear_backward(dy, x, w, saved, want_grad_bias=True)
+    x, w, b = (t.clone().requires_grad_() for t in (x, w, b))
+    for leaves, want in (((x,), full[:1]), ((w,), full[1:2]), ((b,), full[2:]), ((x, b), (full[0], full[2]))):
+        args = [t if any(t is q for q in leaves) else t.detach() for t in (x, w, b)]
+        got = torch.autograd.grad(sla.linear(*args), leaves, dy)
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+    _, saved = sla.sla_linear(x[:0].detach(), w.detach(), b.detach(), save=True)
+    dx, dw, db = sla.sla_linear_backward(dy[:0], x[:0].detach(), w.detach(), saved, want_grad_bias=True)
+    assert dx.shape == (0, 64) and not bool(dw.any()) and not bool(db.any())
