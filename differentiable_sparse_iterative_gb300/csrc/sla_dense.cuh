@@ -181,6 +181,7 @@ constexpr int kPlanDepth = 64;  // k of the blocks that plans are made in
 struct ProductSize {
   int64_t m, n, k;           // of one half, of one segment
   int m_halves, n_halves, k_halves;
+  int64_t longest = 0;       // k that one accumulator may add up (a multiple of kPlanDepth); 0: any
 };
 
 // Tile shape and splits of the products of one launch.
@@ -227,6 +228,7 @@ ProductPlan plan_products(Epilogue epi, const ProductSize *s, int count, int she
       for (int j = 0; j < count; ++j) {
         int64_t t = tiles[j];
         int64_t n = std::max<int64_t>(1, (int64_t)(kb[j] * per[j] * fill * workers / std::max(1.0, blocks)));
+        if (s[j].longest) n = std::max(n, (s[j].k + s[j].longest - 1) / s[j].longest);
         n = std::min(n, kb[j]);
         if (epi == kGate && n == 1)
           t = s[j].m_halves * ((s[j].m + bm - 1) / bm) * ((s[j].n + bn / 2 - 1) / (bn / 2));

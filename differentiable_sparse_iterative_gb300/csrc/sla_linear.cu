@@ -77,9 +77,15 @@ bool two_parts(const sla_layer *f) {
 }
 
 int sheets(const sla_layer *f) { return f->dtype == SLA_F32 ? 3 : 1; }
-ProductSize y_size(const sla_layer *f) { return {f->tokens, f->out, f->width, 1, 1, 1}; }
-ProductSize dx_size(const sla_layer *f) { return {f->tokens, f->width, f->out, 1, 1, two_parts(f) ? 2 : 1}; }
-ProductSize dw_size(const sla_layer *f) { return {f->out, f->width, f->tokens, 1, 1, two_parts(f) ? 2 : 1}; }
+
+// What the tensor core drops of a running sum (2^-24 of it for every 16 products, on average over a sum that grows as its root
+// 2/3 of that) grows with the sum's length: dW over 250,000 tokens, 2048 -> 2048, was too small by 1.3e-4 of itself in one
+// sum, beside float16's rounding of 2.1e-4.  So 16-bit sums end after 2^14 products (4.1e-5 by that formula), and the parts are added
+// in float32; their bytes are out / 2^13 of x's (that case's backward call: 2,480 us as before).  float32's end after 512 (kRun).
+int64_t longest(const sla_layer *f) { return f->dtype == SLA_F32 ? 0 : 1 << 14; }
+ProductSize y_size(const sla_layer *f) { return {f->tokens, f->out, f->width, 1, 1, 1, longest(f)}; }
+ProductSize dx_size(const sla_layer *f) { return {f->tokens, f->width, f->out, 1, 1, two_parts(f) ? 2 : 1, longest(f)}; }
+ProductSize dw_size(const sla_layer *f) { return {f->out, f->width, f->tokens, 1, 1, two_parts(f) ? 2 : 1, longest(f)}; }
 
 struct ForwardScratch {
   void *x, *w;
