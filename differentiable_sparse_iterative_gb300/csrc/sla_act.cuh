@@ -36,6 +36,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// The smaller of two, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // 1 / (1 + e^-x) of both.
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
   const float2 m = mul2(x, f2(-1.4426950408889634f, -1.4426950408889634f));

@@ -268,13 +268,6 @@ __device__ __forceinline__ void param_part(const float4 *sm, int t, int tpr, flo
 
 __device__ __forceinline__ float2 both(float v) { return f2(v, v); }
 
-// The smaller of two, NaN if either is.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Row `row` of rows `bytes` apart: one wide multiply-add.
 template <typename T>
 __device__ __forceinline__ T *row_at(const void *base, uint32_t row, uint32_t bytes) {

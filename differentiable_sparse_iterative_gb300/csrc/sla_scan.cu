@@ -23,17 +23,23 @@
 // A map's two float32 are published as one 64-bit word, so that the word itself says whether it is there (the
 // workspace is set to ones, a NaN that no map has): no flag, no fence.
 //
-// A step is h' = a h + (x - a x), so that a's rounding never makes a and 1 - a sum up to something else than one; where
-// 1 - a itself is a factor of a result it is exp(-g) a, right relative to itself.  A sequence's start is a map
-// with A = kCut, whose H replaces what came before, whatever that is: an infinity or a NaN stays within its sequence.
+// A gate is held as the smaller of a and 1 - a, right relative to itself (next to one, float32's a has lost what 1 - a is: from a
+// gate of 17 on nothing of x would be left, at 10 one part in 1,700 of what x adds to a state of zero would be wrong), and a step is
+// h' = h + (1 - a) (x - h) where the gate is open, x + a (h - x) where it is closed: a and 1 - a sum up to one in both.  What a map
+// takes from the state is held in the same way: a gate of 14 keeps a state over a path of a million rows, each of which takes less
+// than two parts in a million (as a product of float32's a it was off by 0.5 % at the end).  A state is rounded once a row, so
+// that n rows may move it by n 2^-25 of itself; a walk's (below) by all of its rows, a tile's by its 128 and the maps before it.  A
+// sequence's start is a map with A = kCut, whose H replaces what came before, whatever that is: an infinity or a NaN stays
+// within its sequence.
 //
-// What costs is instructions as much as bytes (two special functions an element and some twenty other
+// What costs is instructions as much as bytes (two special functions an element and some thirty other
 // instructions), so an address is one multiply-add, and warps whose rows hold no sequence's start or end, nearly
 // all where sequences are long, take a copy of the loops without those checks.
 //
-// Measured by tiles, against the copy rate of 6.8 TB/s: one sequence of 1,000,000 x 64 float32 179 us (0.63), in bfloat16 159
-// (0.37) and 395 a training step (0.40); 57 packed sequences, 60,001 x 333 float16, backwards, a training step 173 us (0.27).
-// By walks (below): 1000 sequences of 1000 x 64 bfloat16, a training step 263 us (0.57), in float32 328 (0.92).
+// Measured by tiles, against the copy rate of 6.8 TB/s: one sequence of 1,000,000 x 64 float32 209 us (0.54), in bfloat16 181
+// (0.31) and 434 a training step (0.35); 57 packed sequences, 60,001 x 333 float16, backwards, a training step 185 us (0.25).
+// By walks (below): 1000 sequences of 1000 x 64 bfloat16, a training step 286 us (0.53), in float32 352 (0.86).  (With maps of
+// float32's a and 1 - a taken from that: 181, 153 and 384; 173; 263 and 328.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -236,41 +242,106 @@ struct Lane {
   }
 };
 
-// a = 1 / (1 + exp(-g)).
-__device__ __forceinline__ float2 keep(float2 g) {
-  const float2 m = mul2(g, f2(-1.4426950408889634f, -1.4426950408889634f));
-  const float2 d = add2(f2(ex2_approx(m.x), ex2_approx(m.y)), f2(1.f, 1.f));
-  return f2(rcp_approx(d.x), rcp_approx(d.y));
+// A gate is held as the smaller of its two factors, m = e^-|g| / (1 + e^-|g|), which is right relative to itself, with a sign that
+// says which it is: c = -m where the gate is open (m = 1 - a), c = m where it is closed (m = a).
+// An open gate's value, or a closed one's: by masks, so that no row takes a branch (a select may become one).
+__device__ __forceinline__ float choose(float c, float open, float closed) {
+  const int m = __float_as_int(c) >> 31;
+  return __int_as_float((__float_as_int(open) & m) | (__float_as_int(closed) & ~m));
+}
+__device__ __forceinline__ float2 choose(float2 c, float2 open, float2 closed) {
+  return f2(choose(c.x, open.x, closed.x), choose(c.y, open.y, closed.y));
 }
 
-// 1 - a, right relative to itself.
-__device__ __forceinline__ float drop(float g, float a) {
-  // exp(-g) a, but 1 where the exponential is infinite (a NaN remains one)
-  const float e = ex2_approx(g * -1.4426950408889634f);
-  return a == 0.f ? 1.f : e * a;
-}
-__device__ __forceinline__ float2 drop(float2 g, float2 a) { return f2(drop(g.x, a.x), drop(g.y, a.y)); }
-
-// One step of h: a h + (x - a x).
-__device__ __forceinline__ float2 step(float2 h, float2 x, float2 a) {
-  return fma2(a, h, f2(fmaf(-a.x, x.x, x.x), fmaf(-a.y, x.y, x.y)));
+// v's magnitude with the sign bit of `of`.  (A zero's sign is set by its bits, and not left to sums and products.)
+__device__ __forceinline__ float with_sign(float v, int of) {
+  return __int_as_float((__float_as_int(v) & INT32_MAX) | (of & INT32_MIN));
 }
 
-// s -> a s + h of two channels; a = kCut: s -> h.
+// e^-t for t >= 0.
+template <typename T>
+__device__ __forceinline__ float2 exp_of_minus(float2 t) {
+  if constexpr (sizeof(T) == 2) {
+    // the exponent's rounding is off by 2^-24 of t, beside the rounding of 16-bit data
+    return f2(ex2_approx(t.x * -1.4426950408889634f), ex2_approx(t.y * -1.4426950408889634f));
+  } else {
+    // what the product and log2(e) lose to rounding follows as a factor 1 + rest (beyond 128 the exponential is zero)
+    t = f2(min_nan(t.x, 128.f), min_nan(t.y, 128.f));
+    constexpr float L = 1.4426950408889634f, L2 = (float)(1.4426950408889634074 - (double)L), ln2 = 0.6931471805599453f;
+    const float2 n = mul2(t, f2(-L, -L));
+    const float2 rest = fma2(t, f2(-L2 * ln2, -L2 * ln2), mul2(fma2(t, f2(-L, -L), f2(-n.x, -n.y)), f2(ln2, ln2)));
+    const float2 e = f2(ex2_approx(n.x), ex2_approx(n.y));
+    return mul2(e, add2(rest, f2(1.f, 1.f)));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float2 gate_of(float2 g) {
+  const float2 e = exp_of_minus<T>(f2(fabsf(g.x), fabsf(g.y))), d = add2(e, f2(1.f, 1.f));
+  const float2 m = mul2(e, f2(rcp_approx(d.x), rcp_approx(d.y)));
+  auto sign = [](float v, float of) { return __int_as_float(__float_as_int(v) | (~__float_as_int(of) & INT32_MIN)); };
+  return f2(sign(m.x, g.x), sign(m.y, g.y));
+}
+
+// 1 - a, and a (1 - a).
+__device__ __forceinline__ float2 drop(float2 v, float2 c) {
+  return fma2(f2(-c.x, -c.y), v, choose(c, f2(0.f, 0.f), v));
+}
+__device__ __forceinline__ float2 keep_drop(float2 c) {
+  return f2(fmaf(-c.x, c.x, fabsf(c.x)), fmaf(-c.y, c.y, fabsf(c.y)));
+}
+
+// a v: v - m v where the gate is open, so that a is not rounded.
+__device__ __forceinline__ float2 keep(float2 v, float2 c) {
+  return fma2(c, v, choose(c, v, f2(0.f, 0.f)));
+}
+
+// d + a v: the gradient of a row's h from that of the next one's.  (An open gate's v + d first, then less m v: two steps in a
+// chain of rows, where keep makes three.)
+__device__ __forceinline__ float2 back(float2 d, float2 v, float2 c) {
+  return fma2(c, v, fma2(choose(c, f2(1.f, 1.f), f2(0.f, 0.f)), v, d));
+}
+
+// One step of h, a h + (1 - a) x: h + m (x - h) where the gate is open, x + m (h - x) where it is closed (c h and c x apart: the
+// difference of h and x may pass the largest float32).
+__device__ __forceinline__ float2 step(float2 h, float2 x, float2 c) {
+  const float2 t = mul2(c, x), u = fma2(c, h, f2(-t.x, -t.y));
+  return add2(choose(c, h, x), u);
+}
+
+// s -> A s + h of two channels.  A is held as a gate's factors are: a = A, or, next to one, a = A - 1 (with the sign bit, -0 is one),
+// so that what a state loses over many open rows is right relative to itself.  a = kCut: s -> h.
 struct Map {
   float2 a, h;
 };
 
 __device__ __forceinline__ float2 apply(const Map &m, float2 s) {
-  const float2 r = fma2(m.a, s, m.h);
+  const float2 r = add2(choose(m.a, s, f2(0.f, 0.f)), fma2(m.a, s, m.h));
   return m.a.x == kCut ? m.h : r;
 }
 __device__ __forceinline__ void join(Map &m, const Map &n) {  // m first
   m.h = apply(n, m.h);
-  const float2 a = mul2(m.a, n.a);
   const bool cut = m.a.x == kCut || n.a.x == kCut;
-  m.a = cut ? f2(kCut, kCut) : a;
+  const float2 A = add2(choose(m.a, f2(1.f, 1.f), f2(0.f, 0.f)), m.a), v = fma2(n.a, A, choose(n.a, m.a, f2(0.f, 0.f)));
+  // (two factors next to one make one that is not positive, whatever the sign of a zero)
+  auto factor = [](float v, float a, float b) {
+    return v < -0.5f ? 1.f + v : with_sign(v, __float_as_int(a) & __float_as_int(b));
+  };
+  m.a = cut ? f2(kCut, kCut) : f2(factor(v.x, m.a.x, n.a.x), factor(v.y, m.a.y, n.a.y));
 }
+
+// The factor of a map over rows, taken row after row, as A and as A - 1.
+struct Factor {
+  float2 all = f2(1.f, 1.f), less = f2(-0.f, -0.f);
+  __device__ __forceinline__ void row(float2 c) {
+    all = keep(all, c);
+    less = fma2(c, add2(less, f2(1.f, 1.f)), choose(c, less, f2(-1.f, -1.f)));
+  }
+  __device__ __forceinline__ float2 a() const {
+    auto one = [](float less, float all) { return less >= -0.5f ? __int_as_float(__float_as_int(less) | INT32_MIN) : all; };
+    return f2(one(less.x, all.x), one(less.y, all.y));
+  }
+};
 
 __device__ __forceinline__ uint64_t word_of(float a, float h) {
   const uint64_t w = (uint64_t)__float_as_uint(h) << 32 | __float_as_uint(a);
@@ -329,7 +400,7 @@ struct TileMemory {
   volatile uint32_t dead; // a wait of this block has expired: it waits no more, so that the launch ends
 };
 
-__device__ __forceinline__ Map no_rows() { return {f2(1.f, 1.f), f2(0.f, 0.f)}; }
+__device__ __forceinline__ Map no_rows() { return {f2(-0.f, -0.f), f2(0.f, 0.f)}; }
 
 __device__ __forceinline__ Map joined(const Map (*maps)[32], int from, int to, int lane) {
   Map m = no_rows();
@@ -454,25 +525,27 @@ __device__ __forceinline__ void tile_forward(const ScanArgs &p, TileMemory &sm, 
   if (Chain && threadIdx.x == 0) sm.origin = f.live & 1 ? f.origin : t.t0;
   if (p.state && f.first) ask_states(starts, p.state, f.first, f.seq, p.channels, t.l, lane);
   auto start = [&](int r) { return p.state ? starts[r * 32 + lane] : f2(0.f, 0.f); };
-  float2 a[N];
+  float2 c[N];
 #pragma unroll
-  for (int r = 0; r < N; ++r) a[r] = keep(L::values(gr[r]));
+  for (int r = 0; r < N; ++r) c[r] = gate_of<T>(L::values(gr[r]));
   Map m = no_rows();
+  Factor factor;
   if (inner) {
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-      m.h = step(m.h, L::values(xr[r]), a[r]);
-      m.a = mul2(m.a, a[r]);
+      m.h = step(m.h, L::values(xr[r]), c[r]);
+      factor.row(c[r]);
     }
+    m.a = factor.a();
   } else {
     copies_done();
 #pragma unroll
     for (int r = 0; r < N; ++r) {
       if (f.first >> r & 1) m.h = start(r);
-      m.h = step(m.h, L::values(xr[r]), a[r]);
-      m.a = mul2(m.a, a[r]);
+      m.h = step(m.h, L::values(xr[r]), c[r]);
+      factor.row(c[r]);
     }
-    if (f.first) m.a = f2(kCut, kCut);
+    m.a = f.first ? f2(kCut, kCut) : factor.a();
   }
   sm.maps[warp][lane] = m;
   __syncthreads();
@@ -487,7 +560,7 @@ __device__ __forceinline__ void tile_forward(const ScanArgs &p, TileMemory &sm, 
 #pragma unroll
     for (int r = 0; r < N; ++r) {
       save(r);
-      h = step(h, L::values(xr[r]), a[r]);
+      h = step(h, L::values(xr[r]), c[r]);
       t.l.store((T *)(to + (int64_t)p.bo * r), h);
     }
     return;
@@ -496,7 +569,7 @@ __device__ __forceinline__ void tile_forward(const ScanArgs &p, TileMemory &sm, 
   for (int r = 0; r < N; ++r) {
     save(r);
     if (f.first >> r & 1) h = start(r);
-    h = step(h, L::values(xr[r]), a[r]);
+    h = step(h, L::values(xr[r]), c[r]);
     const bool live = f.live >> r & 1;
     if (live || (p.outside && r < t.left)) t.l.store((T *)(to + (int64_t)p.bo * r), live ? h : f2(0.f, 0.f));
     if (p.end && (f.last >> r & 1)) t.l.put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, h);
@@ -530,24 +603,31 @@ __device__ __forceinline__ void tile_backward(const ScanArgs &p, TileMemory &sm,
   }
   auto start = [&](int r) { return p.state ? starts[r * 32 + lane] : f2(0.f, 0.f); };
   auto end = [&](int r) { return p.dfinal ? ends[r * 32 + lane] : f2(0.f, 0.f); };
-  float2 a[N], e[N];  // e: h_{t-1} - x_t
+  float2 c[N], e[N];  // e: h_{t-1} - x_t
 #pragma unroll
-  for (int r = 0; r < N; ++r) a[r] = keep(L::values(gr[r]));
+  for (int r = 0; r < N; ++r) c[r] = gate_of<T>(L::values(gr[r]));
   Map m = no_rows();
+  Factor factor;
   auto form = [&](int r) {
     const float2 x = L::values(xr[r]);
     e[r] = f2(h.x - x.x, h.y - x.y);
-    h = fma2(a[r], e[r], x);
+    h = step(h, x, c[r]);
   };
   auto pass = [&](int r) {
-    m.h = mul2(a[r], add2(L::values(dr[r]), m.h));
-    m.a = mul2(m.a, a[r]);
+    m.h = keep(add2(L::values(dr[r]), m.h), c[r]);
+    factor.row(c[r]);
   };
   if (inner) {
 #pragma unroll
     for (int r = 0; r < N; ++r) form(r);
 #pragma unroll
-    for (int r = N - 1; r >= 0; --r) pass(r);
+    for (int r = N - 1; r >= 0; --r) {
+      const float2 d = L::values(dr[r]);
+      m.h = r == N - 1 ? d : back(d, m.h, c[r + 1 < N ? r + 1 : r]);
+      factor.row(c[r]);
+    }
+    m.h = keep(m.h, c[0]);
+    m.a = factor.a();
   } else {
     copies_done();
 #pragma unroll
@@ -560,7 +640,7 @@ __device__ __forceinline__ void tile_backward(const ScanArgs &p, TileMemory &sm,
       if (f.last >> r & 1) m.h = end(r);
       pass(r);
     }
-    if (f.last) m.a = f2(kCut, kCut);
+    m.a = f.last ? f2(kCut, kCut) : factor.a();
   }
   sm.maps[warp][lane] = m;
   __syncthreads();
@@ -568,17 +648,16 @@ __device__ __forceinline__ void tile_backward(const ScanArgs &p, TileMemory &sm,
   if (Chain && threadIdx.x == 0) sm.next = atomicAdd(p.counter, 1u) + 1u;
   char *tx = t.at(p.out0, p.channels), *tg = t.at(p.out1, p.channels);
   auto results = [&](int r, float2 lam, bool live) {
-    const float2 b = drop(L::values(gr[r]), a[r]);
     const float2 none = f2(0.f, 0.f);
-    if (p.out0) t.l.store((T *)(tx + (int64_t)p.bo * r), live ? mul2(b, lam) : none);
-    if (p.out1) t.l.store((T *)(tg + (int64_t)p.bo * r), live ? mul2(mul2(lam, e[r]), mul2(a[r], b)) : none);
+    if (p.out0) t.l.store((T *)(tx + (int64_t)p.bo * r), live ? drop(lam, c[r]) : none);
+    if (p.out1) t.l.store((T *)(tg + (int64_t)p.bo * r), live ? mul2(mul2(lam, e[r]), keep_drop(c[r])) : none);
   };
   if (inner) {
 #pragma unroll
     for (int r = N - 1; r >= 0; --r) {
-      const float2 lam = add2(L::values(dr[r]), carry);
-      carry = mul2(a[r], lam);
-      results(r, lam, true);
+      const float2 d = L::values(dr[r]);
+      carry = r == N - 1 ? add2(d, carry) : back(d, carry, c[r + 1 < N ? r + 1 : r]);  // the row's l
+      results(r, carry, true);
     }
     return;
   }
@@ -586,7 +665,7 @@ __device__ __forceinline__ void tile_backward(const ScanArgs &p, TileMemory &sm,
   for (int r = N - 1; r >= 0; --r) {
     if (f.last >> r & 1) carry = end(r);
     const float2 lam = add2(L::values(dr[r]), carry);
-    carry = mul2(a[r], lam);
+    carry = keep(lam, c[r]);
     if (r < t.left) results(r, lam, f.live >> r & 1);
     if (p.end && (f.first >> r & 1)) t.l.put_state(p.end, __shfl_sync(0xffffffffu, f.seq, r), p.channels, carry);
   }
@@ -628,7 +707,8 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<T, Backward>) scan_kern
 // With a sequence and kCols channels for every warp that there is room for, nothing has to be joined: a warp walks from row to
 // row with the state in its registers, one pass, and what counts is that enough rows are on their way: kAhead forward,
 // a chunk of kSaved rows backward while the one behind it is worked on.  Rows in the middle are worked on without a branch, so
-// that their gates are formed side by side (with a test a row: 443 us in place of 81).
+// that their gates are formed side by side (with a test a row: 443 us in place of 81), four rows' at a time: a barrier of the warp
+// every four rows keeps the compiler from forming all rows' first, for which it spills (203 us in place of 88).
 template <typename T>
 inline constexpr int kAhead = sizeof(T) == 2 ? 32 : 16;
 
@@ -656,13 +736,13 @@ __global__ void __launch_bounds__(32) walk_forward(const __grid_constant__ ScanA
   const int phase = (int)(i0 % kSaved<T>);
   float *saved = p.saved ? p.saved + i0 / kSaved<T> * p.channels + l.c : nullptr;
   auto row = [&](int t, int r) {
-    const float2 a = keep(L::values(gr[r]));
+    const float2 c = gate_of<T>(L::values(gr[r]));
     if (saved && (phase + t + r) % kSaved<T> == 0) {
       float *to = saved + (int64_t)((phase + t + r) / kSaved<T>) * p.channels;
       if (l.on0) to[0] = h.x;
       if (l.on1) to[L::apart] = h.y;
     }
-    h = step(h, L::values(xr[r]), a);
+    h = step(h, L::values(xr[r]), c);
     l.store((T *)(po + (int64_t)p.bo * r), h);
   };
   int t = 0;
@@ -670,6 +750,7 @@ __global__ void __launch_bounds__(32) walk_forward(const __grid_constant__ ScanA
     px += (int64_t)p.bx * D, pg += (int64_t)p.bg * D;
 #pragma unroll
     for (int r = 0; r < D; ++r) {
+      if (r % 4 == 0) __syncwarp();
       row(t, r);
       gr[r] = l.load((const T *)(pg + (int64_t)p.bg * r));
       xr[r] = l.load((const T *)(px + (int64_t)p.bx * r));
@@ -734,25 +815,27 @@ __global__ void __launch_bounds__(32) walk_backward(const __grid_constant__ Scan
   auto work = [&](const WalkRows<T> &w, int64_t k) {
     const int lo = (int)max(i0 - k * N, (int64_t)0), hi = (int)min(i0 + n - k * N, (int64_t)N);
     char *tx = at(p.out0, p.channels, k), *tg = at(p.out1, p.channels, k);
-    float2 a[N], e[N], h = w.h;
+    float2 c[N], e[N], h = w.h;
     auto form = [&](int r) {
       const float2 x = L::values(w.x[r]);
       e[r] = f2(h.x - x.x, h.y - x.y);
-      h = fma2(a[r], e[r], x);
+      h = step(h, x, c[r]);
     };
-    auto results = [&](int r) {
-      const float2 lam = add2(L::values(w.d[r]), carry), b = drop(L::values(w.g[r]), a[r]);
-      carry = mul2(a[r], lam);
-      if (p.out0) l.store((T *)(tx + (int64_t)p.bo * r), mul2(b, lam));
-      if (p.out1) l.store((T *)(tg + (int64_t)p.bo * r), mul2(mul2(lam, e[r]), mul2(a[r], b)));
+    float2 lam;
+    auto results = [&](int r, bool first) {
+      const float2 d = L::values(w.d[r]);
+      lam = first ? add2(d, carry) : back(d, lam, c[r + 1 < N ? r + 1 : r]);
+      if (p.out0) l.store((T *)(tx + (int64_t)p.bo * r), drop(lam, c[r]));
+      if (p.out1) l.store((T *)(tg + (int64_t)p.bo * r), mul2(mul2(lam, e[r]), keep_drop(c[r])));
     };
 #pragma unroll
-    for (int r = 0; r < N; ++r) a[r] = keep(L::values(w.g[r]));
+    for (int r = 0; r < N; ++r) c[r] = gate_of<T>(L::values(w.g[r]));
     if (lo == 0 && hi == N) {
 #pragma unroll
       for (int r = 0; r < N; ++r) form(r);
 #pragma unroll
-      for (int r = N - 1; r >= 0; --r) results(r);
+      for (int r = N - 1; r >= 0; --r) results(r, r == N - 1);
+      carry = keep(lam, c[0]);
       return;
     }
 #pragma unroll
@@ -760,7 +843,10 @@ __global__ void __launch_bounds__(32) walk_backward(const __grid_constant__ Scan
       if (r >= lo) form(r);  // (rows behind the last one change what nothing reads)
 #pragma unroll
     for (int r = N - 1; r >= 0; --r)
-      if (r >= lo && r < hi) results(r);
+      if (r >= lo && r < hi) {
+        results(r, true);
+        carry = keep(lam, c[r]);
+      }
   };
   WalkRows<T> even, odd;
   ask(even, last);
@@ -785,7 +871,7 @@ __global__ void __launch_bounds__(256) scan_single(const __grid_constant__ ScanA
     const float2 g = L::values(l.load((const T *)p.g + row * p.ldg + l.c));
     const float2 x = L::values(l.load((const T *)p.x + row * p.ldx + l.c));
     float2 h = p.state ? l.state(p.state, row, p.channels) : f2(0.f, 0.f);
-    h = step(h, x, keep(g));
+    h = step(h, x, gate_of<T>(g));
     l.store((T *)p.out0 + row * p.channels + l.c, h);
     if (p.end) l.put_state(p.end, row, p.channels, h);
   }
@@ -812,8 +898,8 @@ bool closed_tiles(const sla_scan *s, bool backward) {
 
 // Whether a warp for each sequence and kCols channels pays, where channels go in pairs: sequences long enough for rows on their
 // way, and enough of them to keep the memory busy.  A training step in bfloat16, walks against tiles: 1000 sequences of 1000 x 64
-// 264 us and 329 (float32 328 and 432), 16,000 of 64 x 64 242 and 288, 300 of 1000 x 130 256 and 298; but 500 of 1000 x 64 212
-// and 174, 16 of 2048 x 2048 429 and 319.  (Single channels 32 apart: 1,074 and 350.)
+// 292 us and 373 (float32 353 and 495), 16,000 of 64 x 64 253 and 365, 300 of 1000 x 130 288 and 335, 760 of 1000 x 64 280 and 290;
+// but 500 of 1000 x 64 234 and 198, 16 of 2048 x 2048 467 and 368.  (Single channels 32 apart were three times the tiles' time.)
 bool walks_pay(const sla_scan *s, bool pairs) {
   if (!pairs || s->offsets || s->sequences < 1 || s->rows / s->sequences < kWalkRows) return false;
   const int64_t strands = s->sequences * ((s->channels + kCols - 1) / kCols);

@@ -728,8 +728,9 @@ SLA_API size_t sla_gated_scan_workspace_bytes(const sla_scan *s);
  *   final_state  device, [sequences][channels] float32: the states behind the sequences, or NULL.  It may be `state`.
  *   saved        device, sla_gated_scan_saved_bytes, 256-byte aligned, or NULL
  *   workspace    device, sla_gated_scan_workspace_bytes, 256-byte aligned
- * States are float32 from row to row; h is what they round to.  A sequence with no rows ends in the state that it
- * starts with.  An infinity or NaN makes NaN or infinities of the rest of its channel's sequence, and of nothing else.
+ * States are float32 from row to row (n rows may round one by n 2^-25 of itself); h is what they round to.  1 - a is right
+ * relative to itself, however open a gate is, to 2^-20 (16-bit data: and |gate| 2^-23); beyond gates of 87 it is zero, as a is below
+ * -87.  A sequence with no rows ends in the state that it starts with.  An infinity or NaN makes NaN or infinities of the rest of its channel's sequence, and of nothing else.
  * Blocks wait for one another's results within the launch, each wait for two seconds at most (see sla_gated_ffn_check).
  */
 SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx, const void *gate, int64_t ldg,
