@@ -229,7 +229,7 @@ ProductPlan plan_products(Epilogue epi, const ProductSize *s, int count, int she
         int64_t t = tiles[j];
         int64_t n = std::max<int64_t>(1, (int64_t)(kb[j] * per[j] * fill * workers / std::max(1.0, blocks)));
         if (s[j].longest) n = std::max(n, (s[j].k + s[j].longest - 1) / s[j].longest);
-        n = std::min(n, kb[j]);
+        n = std::max<int64_t>(1, std::min(n, kb[j]));  // (no tokens: a sum over nothing is one of one part)
         if (epi == kGate && n == 1)
           t = s[j].m_halves * ((s[j].m + bm - 1) / bm) * ((s[j].n + bn / 2 - 1) / (bn / 2));
         const double main = (kb[j] + n - 1) / n * per[j] * block_us[i], end = epilogue_us[n > 1 ? kStore : epi][i];
