@@ -53,13 +53,15 @@ _empty = torch.empty
 
 
 def _on_device_of_first(call):
-    """call, with the device of its first argument as the current one: libsla launches on the current device and
-    asks it for its size, and the handle of a default stream names no device."""
+    """call, with the device of its first argument (of the first tensor, where that is None) as the current one: libsla
+    launches on the current device and asks it for its size, and the handle of a default stream names no device."""
     first = next(iter(inspect.signature(call).parameters))
 
     @functools.wraps(call)
     def run(*args, **kw):
         t = args[0] if args else kw.get(first)
+        if t is None:
+            t = next((a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor)), None)
         if t is not None and t.is_cuda and t.get_device() != _current_device():
             with torch.cuda.device(t.get_device()):
                 return call(*args, **kw)
