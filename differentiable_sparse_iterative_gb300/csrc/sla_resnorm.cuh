@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "sla_act.cuh"
@@ -282,13 +283,13 @@ __device__ __forceinline__ void gate_act(int act, float2 g, float2 &a, float2 &d
     if (Derivative) da = both(1.f);
     return;
   }
-  // e = exp(-g), at most 2^126, so that e s is 1 - s, right relative to itself, and never infinity times zero
+  // e = exp(-g); e s is 1 - s, right relative to itself.  Where e is infinite s is zero, and so is what 1 - s multiplies.
   const float2 m = mul2(g, both(-1.4426950408889634f));
-  const float2 e = f2(ex2_approx(min_nan(m.x, 126.f)), ex2_approx(min_nan(m.y, 126.f)));
+  const float2 e = f2(ex2_approx(m.x), ex2_approx(m.y));
   const float2 d = add2(e, both(1.f)), s = f2(rcp_approx(d.x), rcp_approx(d.y));
   a = act == kGateSigmoid ? s : mul2(g, s);
   if (Derivative) {
-    const float2 r = mul2(e, s);
+    const float2 r = mul2(f2(min_nan(e.x, FLT_MAX), min_nan(e.y, FLT_MAX)), s);  // never infinity times zero
     da = act == kGateSigmoid ? mul2(s, r) : fma2(a, r, s);
   }
 }
