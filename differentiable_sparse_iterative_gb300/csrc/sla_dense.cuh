@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(256) finish_splits(const __grid_constant__ Spl
     }
     if constexpr (kPlainStore<EPI>) {
       T *out = (T *)p.c + row * (int64_t)p.n + col;
+      if constexpr (kScales<T, EPI>) scale_sums(p, v);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (p.bias && k < count) v[k] += to_f32(((const T *)p.bias)[col + k]);

@@ -83,6 +83,7 @@ struct ProductArgs {
   uint16_t *h;               // kGate: sheets of [m][ldg]; kGateBack: dg and du, sheets of [m][ldg]
   int64_t ldg, sheet;        // elements between rows and between sheets of h
   float *sums;               // kGateBack: [m / 32][2][ldg] sums of dg and du over 32 rows, or NULL
+  const float *factor;       // kStore, float16: what the sums are multiplied by, or NULL
   const void *residual;      // kLinear, kAdd: T [m][ldr], or NULL; act'(sum + bias) goes to g, float [m][ldg], unless that is NULL
   int64_t ldr;
   int residual_vec;          // rows of the residual are aligned to 32 bytes
@@ -276,6 +277,17 @@ __device__ __forceinline__ void add_bias(float (&v)[N], const T *bias, int count
   load_row<T, N>(bias, b, count, vec);
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] += b[i];
+}
+
+// Operands that were scaled to float16's range (by a power of two).
+template <typename T, int EPI>
+inline constexpr bool kScales = EPI == kStore && NetType<T>::dtype == SLA_F16;
+template <int N>
+__device__ __forceinline__ void scale_sums(const ProductArgs &p, float (&v)[N]) {
+  if (!p.factor) return;
+  const float f = *p.factor;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] *= f;
 }
 
 // v = act(v) + r, r the residual's N values of the row; act'(v) is kept in g, whose rows are whole sectors.
@@ -811,6 +823,7 @@ __device__ __forceinline__ void store_epilogue(const ProductLaunch &l, uint32_t 
         if (p.splits > 1) {
           store_row<float, N>((float *)p.c + t.split * p.c_split + o, v, count, true);
         } else {
+          if constexpr (kScales<T, EPI>) scale_sums(p, v);
           if (p.bias) add_bias<T, N>(v, (const T *)p.bias + col, count, p.bias_vec);
           if constexpr (kLayer<EPI>) finish_linear<T, N, EPI == kLinear>(p, row, col, v, r, count);
           if (p.vec && count >= N) store_row<T, N>((T *)p.c + o, v, count, true);

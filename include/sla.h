@@ -628,8 +628,8 @@ SLA_API sla_status sla_linear(const sla_layer *f, const void *x, int64_t ldx, co
 /*
  * Gradients for an upstream gradient dy [tokens][out] (lddy): with dp = dy act'(p), dx = dp weight [tokens][width],
  * dweight = dp^T x [out][width], dbias = sum dp [out], each NULL when not wanted (the residual's is dy).  x, the weight and `saved`
- * are the forward call's.  With 16-bit data dp is rounded to dtype before large products and taken in two parts, as
- * good as unrounded, by small ones; dbias sums dp unrounded.  tokens = 0 sets dweight and dbias to zero.
+ * are the forward call's.  With 16-bit data dp is rounded to dtype (float16: scaled to its range by a power of two) before
+ * large products and taken in two parts, as good as unrounded, by small ones; dbias sums dp unrounded.  tokens = 0 sets dweight and dbias to zero.
  */
 SLA_API sla_status sla_linear_backward(const sla_layer *f, const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                        const void *weight, const void *saved, size_t saved_bytes, void *dx,
