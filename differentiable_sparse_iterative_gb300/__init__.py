@@ -53,7 +53,7 @@ __all__ = [
     "eigsh_smallest", "sla_spmv_transpose", "sla_matvec_grad_values", "MatVec", "sla_set_spmv_variant", "sla_graph_cache_stats", "sla_test_set_barrier_wait", "SLA_SPMV_PLAIN", "SLA_SPMV_TMA",
     "sla_layernorm", "sla_layernorm_backward_workspace_bytes", "sla_layernorm_backward", "LayerNorm", "layer_norm",
     "sla_gated_ffn", "sla_gated_ffn_backward", "sla_gated_ffn_check", "GatedFFN", "gated_ffn",
-    "sla_test_expire_wait", "sla_gated_scan", "sla_gated_scan_backward", "GatedScan", "gated_scan",
+    "sla_test_expire_wait", "sla_test_set_scan_wait", "sla_gated_scan", "sla_gated_scan_backward", "GatedScan", "gated_scan",
     "sla_residual_norm", "sla_residual_norm_backward", "ResidualNorm", "ResidualNormGrads", "residual_norm",
     "sla_linear", "sla_linear_backward", "Linear", "linear",
 ]
@@ -744,4 +744,5 @@ from .dense import (GatedFFN, LayerNorm, Linear, ResidualNorm, ResidualNormGrads
                     linear, residual_norm, sla_linear, sla_linear_backward, sla_residual_norm, sla_residual_norm_backward, sla_gated_ffn, sla_gated_ffn_backward,
                     sla_gated_ffn_check, sla_layernorm, sla_layernorm_backward, sla_layernorm_backward_workspace_bytes,
                     sla_test_expire_wait)
-from .scan import GatedScan, gated_scan, sla_gated_scan, sla_gated_scan_backward  # noqa: E402
+from .scan import (GatedScan, gated_scan, sla_gated_scan, sla_gated_scan_backward,  # noqa: E402
+                   sla_test_set_scan_wait)

@@ -29,7 +29,7 @@ EXPORTS = [
     "sla_bicgstab_solve", "sla_bicgstab_adjoint", "sla_layernorm", "sla_layernorm_backward_workspace_bytes",
     "sla_layernorm_backward", "sla_gated_ffn_saved_bytes", "sla_gated_ffn_workspace_bytes",
     "sla_gated_ffn_backward_workspace_bytes", "sla_gated_ffn", "sla_gated_ffn_backward",
-    "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan_saved_bytes", "sla_gated_scan_workspace_bytes",
+    "sla_gated_ffn_check", "sla_test_expire_wait", "sla_test_set_scan_wait", "sla_gated_scan_saved_bytes", "sla_gated_scan_workspace_bytes",
     "sla_gated_scan", "sla_gated_scan_backward", "sla_residual_norm", "sla_residual_norm_backward_workspace_bytes",
     "sla_residual_norm_backward", "sla_linear_saved_bytes", "sla_linear_workspace_bytes",
     "sla_linear_backward_workspace_bytes", "sla_linear", "sla_linear_backward",
@@ -162,13 +162,14 @@ def bind(lib):
     lib.sla_set_spmv_variant.argtypes = [i32]
     lib.sla_graph_cache_stats.argtypes = [ctypes.POINTER(i64)] * 3
     lib.sla_test_set_barrier_wait.argtypes = [ctypes.c_uint32, i64]
+    lib.sla_test_set_scan_wait.argtypes = [i32, i64]
     for name in ["sla_spmv_transpose", "sla_matvec_grad_values", "sla_dist_scatter_add", "sla_dist_cg_begin", "sla_dist_cg_start", "sla_dist_cg_spmv", "sla_dist_cg_update",
                  "sla_dist_cg_direction", "sla_dist_pack", "sla_dist_cg_info",
                  "sla_set_spmv_variant", "sla_graph_cache_stats", "sla_test_set_barrier_wait", "sla_validate_csr", "sla_spmv", "sla_cg_solve", "sla_cg_adjoint", "sla_grad_values",
                  "sla_cg_solve_batched", "sla_cg_adjoint_batched", "sla_cg_solve_static", "sla_eig_smallest",
                  "sla_eig_grad_values", "sla_eigsh", "sla_bicgstab_solve", "sla_bicgstab_adjoint",
                  "sla_layernorm", "sla_layernorm_backward", "sla_gated_ffn", "sla_gated_ffn_backward",
-                 "sla_gated_ffn_check", "sla_test_expire_wait", "sla_gated_scan", "sla_gated_scan_backward",
+                 "sla_gated_ffn_check", "sla_test_expire_wait", "sla_test_set_scan_wait", "sla_gated_scan", "sla_gated_scan_backward",
                  "sla_residual_norm", "sla_residual_norm_backward", "sla_linear", "sla_linear_backward"]:
         getattr(lib, name).restype = i32
     return lib

@@ -43,6 +43,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "sla_act.cuh"
@@ -66,6 +67,10 @@ constexpr int kWalkRows = 64, kWalks = 5;  // see walks_pay
 constexpr float kCut = -1.f;
 constexpr long long kScanClocks = 4000000000ll;  // about two seconds
 constexpr uint64_t kAbsent = ~0ull;
+
+// Of the next launches (sla_test_set_scan_wait; normally 0 and kScanClocks).
+std::atomic<int> withheld{0};
+std::atomic<int64_t> wait_clocks{kScanClocks};
 
 struct Sequences {
   int64_t rows;          // of all
@@ -92,6 +97,8 @@ struct ScanArgs {
   // [tiles][groups][kCols], and of every kFold-th and every kSpan-th tile
   uint64_t *maps, *folds, *states;
   uint32_t *timeouts;
+  long long clocks;      // of a wait
+  int withheld;          // tiles before this one publish no map: 0
 };
 
 // The sequence of a row (in memory order): -1 outside of all.
@@ -361,13 +368,13 @@ __device__ __forceinline__ bool look(const uint64_t *p, Map &m) {
 }
 
 // Looks until all lanes' words are there (`there`: what a first look found).  False: they never came.
-__device__ __forceinline__ bool wait_for(const uint64_t *p, Map &m, bool there) {
+__device__ __forceinline__ bool wait_for(const uint64_t *p, Map &m, bool there, long long clocks) {
   if (__all_sync(0xffffffffu, there)) return true;
   const long long t0 = clock64();
   for (;;) {
     __nanosleep(100);  // many wait for the same words
     if (__all_sync(0xffffffffu, look(p, m))) return true;
-    if (__any_sync(0xffffffffu, clock64() - t0 > kScanClocks)) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > clocks)) return false;
   }
 }
 
@@ -424,16 +431,16 @@ __device__ __forceinline__ Map look_back(const ScanArgs &p, TileMemory &sm, int 
   bool ok = true;
   if (warp == 0 && first < base) {
     const uint64_t *q = p.states + (int64_t)(base / kSpan - 1) * apart + mine;
-    ok = wait_for(q, m, look(q, m));
+    ok = wait_for(q, m, look(q, m), p.clocks);
   }
   for (int i = from; i < to && ok; i += 2, at += 2 * apart) {
     Map n, n2;
     const bool two = i + 1 < to;
     const bool there = look(at, n), there2 = !two || look(at + apart, n2);
-    ok = wait_for(at, n, there);
+    ok = wait_for(at, n, there, p.clocks);
     join(m, n);
     if (two && ok) {
-      ok = wait_for(at + apart, n2, there2);
+      ok = wait_for(at + apart, n2, there2, p.clocks);
       join(m, n2);
     }
   }
@@ -491,7 +498,7 @@ __device__ __forceinline__ float2 state_before(const ScanArgs &p, TileMemory &sm
   if (warp == kWarps - 1) {
     own = before;
     join(own, sm.maps[warp][lane]);
-    publish(p.maps + t.tile * apart + mine, own);
+    if (t.tile >= p.withheld) publish(p.maps + t.tile * apart + mine, own);
   }
   sm.carry[warp][lane] = needed ? look_back(p, sm, t.tile, (int)(origin / R::tile_rows), mine, apart, warp, lane) : no_rows();
   if ((t.tile + 1) % kFold == 0 && warp >= kWarps / 2) {
@@ -965,6 +972,7 @@ ScanArgs scan_args(const sla_scan *s, bool backward, void *ws) {
   p.maps = (uint64_t *)((char *)ws + 256);
   p.folds = p.maps + (int64_t)p.tiles * p.groups * kCols;
   p.states = p.folds + (int64_t)(p.tiles / kFold) * p.groups * kCols;
+  p.clocks = wait_clocks.load(), p.withheld = withheld.load();
   return p;
 }
 
@@ -1073,6 +1081,13 @@ SLA_API sla_status sla_gated_scan(const sla_scan *s, const void *x, int64_t ldx,
   e = by_type(s->dtype, pairs, [&](auto t, auto pair) { return run_forward<decltype(t), decltype(pair)::value>(p, walk, chain, st); });
   if (e != cudaSuccess) return fail(e);
   count_launches(1);
+  return SLA_OK;
+}
+
+SLA_API sla_status sla_test_set_scan_wait(int32_t withhold, int64_t clocks) {
+  if (withhold < 0 || withhold > 1 || clocks < 0 || clocks > kScanClocks) return SLA_INVALID_ARG;
+  withheld.store(withhold);
+  wait_clocks.store(clocks ? clocks : kScanClocks);
   return SLA_OK;
 }
 

@@ -190,6 +190,11 @@ def sla_gated_scan_backward(dh: Optional[torch.Tensor], x: torch.Tensor, gate: t
     return dx, dgate, dstate
 
 
+def sla_test_set_scan_wait(withhold: int, clocks: int) -> None:
+    """Test hook: what the next scans' blocks wait for, and for how long (see sla.h); (0, 0) restores normal operation."""
+    _check(_lib().sla_test_set_scan_wait(int(withhold), int(clocks)), "sla_test_set_scan_wait")
+
+
 class GatedScan(torch.autograd.Function):
     """(h, states behind the sequences).  Saved for backward: x, the gate, and a float32 state every 16th row (8th of float32)."""
 

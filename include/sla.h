@@ -803,6 +803,15 @@ SLA_API sla_status sla_test_set_barrier_wait(uint32_t extra, int64_t spin_limit)
  */
 SLA_API sla_status sla_test_expire_wait(void *stream);
 
+/*
+ * Test hook for failure detection (not an operation of the method).  Process-wide, for the next launches of the gated scan: the first
+ * tile of rows withholds (withhold = 1) what others wait for, and a wait gives up after `clocks` of the multiprocessor (0 = the library
+ * default, about two seconds, which is the most).  With withhold = 1 a scan of sequences longer than a tile ends with
+ * meaningless results, nothing outside of its arrays touched and the CUDA context intact, and the next call reports
+ * SLA_TIMEOUT.  sla_test_set_scan_wait(0, 0) restores normal operation.  SLA_INVALID_ARG otherwise.
+ */
+SLA_API sla_status sla_test_set_scan_wait(int32_t withhold, int64_t clocks);
+
 #ifdef __cplusplus
 }
 #endif
