@@ -544,7 +544,8 @@ def sla_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
 
 class Linear(torch.autograd.Function):
     """y = act(x weight^T + bias) + residual.  Saved for backward: x, the weight, act'(x weight^T + bias) where there is an
-    activation, and the copies that were laid out anew for the tensor core (float32, or a width that 8 does not divide)."""
+    activation, and the copies that were laid out anew for the tensor core (float32, or a width that 8 does not divide; none up to
+    16 tokens and for layers of few outputs, which are not the tensor core's)."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, residual, activation):

@@ -604,8 +604,10 @@ typedef struct sla_layer {
   int32_t activation;     /* sla_act, or SLA_ACT_NONE */
 } sla_layer;
 
-/* Bytes of the buffer that carries a forward call's intermediates to its backward call (0 where there are none: 16-bit data, no
-   activation and a width that 8 divides), and of the scratch of the two calls (0 for invalid arguments). */
+/* Bytes of the buffer that carries a forward call's intermediates to its backward call, and of the scratch of the two calls
+   (0 for invalid arguments).  Intermediates are act'(p), where there is an activation, and copies of x and the weight, where the
+   tensor core cannot read them in place (float32, or a width that 8 does not divide) and the call is its: not up to 16 tokens, nor
+   for layers of few outputs.  There may be none: 0.  Ask, as which calls those are may change. */
 SLA_API size_t sla_linear_saved_bytes(const sla_layer *f);
 SLA_API size_t sla_linear_workspace_bytes(const sla_layer *f);
 SLA_API size_t sla_linear_backward_workspace_bytes(const sla_layer *f);
