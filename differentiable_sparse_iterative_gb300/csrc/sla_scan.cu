@@ -290,7 +290,7 @@ __device__ __forceinline__ float2 gate_of(float2 g) {
   return f2(sign(m.x, g.x), sign(m.y, g.y));
 }
 
-// 1 - a, and a (1 - a).
+// (1 - a) v, and a (1 - a).
 __device__ __forceinline__ float2 drop(float2 v, float2 c) {
   return fma2(f2(-c.x, -c.y), v, choose(c, f2(0.f, 0.f), v));
 }
